@@ -59,7 +59,8 @@ enum {
   PG_ERR_CUDA = -16,          /* a CUDA runtime call failed                                    */
   PG_ERR_DEVICE_BOUNDS = -17, /* a kernel saw out-of-range metadata and skipped the access     */
   PG_ERR_ALIGN = -18,         /* a device pointer or token stride breaks its stated alignment  */
-  PG_ERR_DEVICE_TIMEOUT = -19 /* a kernel's bounded wait ran out; its outputs are not valid    */
+  PG_ERR_DEVICE_TIMEOUT = -19,/* a kernel's bounded wait ran out; its outputs are not valid    */
+  PG_ERR_SHARED_PAGE = -20    /* a page is listed twice where each request needs its own       */
 };
 
 /* ---------------------------------------------------------------- pool descriptor */
@@ -321,6 +322,116 @@ int pg_attn_paged_prefill_hd512_lse(const pg_plan_t plan, const pg_pool_t* pool,
 int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf16_t* out_b,
                          const float* lse_b, pg_bf16_t* out, float* lse, int64_t rows,
                          int32_t head_dim, pg_stream_t stream);
+
+/* ---------------------------------------------------------------- bounded caches */
+/*
+ * A request's cache grows by one key per token. The entries below bound it: a local layer keeps
+ * a window and the first tokens (pg_attn_paged_sink); a global layer accumulates every key's
+ * attention weight (pg_attn_paged_mass) and gives up the keys that got least
+ * (pg_kv_evict_select, pg_kv_evict_apply). The pages leave both open ([P3] Description: the
+ * local family fails closed at its window, the global family grows with the request).
+ *
+ * They take plans of pg_plan_paged_prefill and pg_plan_paged_segment (PG_ERR_PLAN_MISMATCH for a
+ * ring plan: its slots forget the positions these keep), and the plan's own device must be
+ * current (PG_ERR_STREAM otherwise).
+ *
+ * After an eviction the cache's slots no longer count positions. The request's next plan is a
+ * segment plan with kv_start = the number of its keys evicted so far: position p of a new token
+ * then has slot p - kv_start, behind the kept keys, prep writes it there, and full causal
+ * attention (window_left -1) sees every kept key, whatever slot it sits in.
+ */
+
+/*
+ * pg_attn_paged_sink -- the attention of pg_attn_paged_prefill (plan head_dim 256) or
+ * pg_attn_paged_prefill_hd512 (512), prefill and decode, in which the first num_sink positions
+ * stay visible behind the window: from position p the keys j <= p with
+ *   window_left < 0  or  p - j <= window_left  or  j < num_sink.
+ * Positions are absolute: on a segment plan the sinks are the segment's keys below num_sink, so
+ * disjoint segments still merge with pg_merge_attn_states. num_sink 0 is the windowed attention;
+ * window_left -1 sees everything. Pages none of whose keys a query of its tile sees are not read
+ * (head_dim 256 decode: 16 keys a tile; other decode 32; prefill 64).
+ *   lse  [T][Hq] float32 or NULL: natural-log normaliser of the row's fp32 scores (-inf, with
+ *        out 0, for a row that sees no key)
+ * The row sum adds the fp32 weights (the entries above sum the bf16-rounded ones), so out and
+ * lse agree with those entries to bf16 rounding, not bit for bit.
+ *   q, out, workspace, ws_bytes: as for pg_attn_paged_prefill (pg_workspace_bytes).
+ * A key that some rows of its tile see and others do not takes part with weight 0 in the latter:
+ * a non-finite V row among the keys held makes every row of a prefill tile that spans it
+ * non-finite. K rows have no such effect, and in decode only visible keys take part.
+ * Errors: those of pg_attn_paged_prefill, and PG_ERR_WINDOW for num_sink < 0.
+ */
+int pg_attn_paged_sink(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
+                       const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
+                       int32_t num_sink, float sm_scale, void* workspace, size_t ws_bytes,
+                       pg_stream_t stream);
+
+/*
+ * Per-key statistics beside a pool: for every layer, page, KV head and slot the accumulated
+ * attention weight (mass, fp32) and the key's position (pos), each
+ *   [layer][page][kv_head][slot],  dense, 4-byte aligned,
+ * with the pool's geometry; capacity is the element count of each array.
+ */
+typedef struct {
+  float* mass;
+  int32_t* pos;
+  int32_t num_layers, num_pages, page_size, num_kv_heads;
+  int64_t capacity;
+} pg_kv_stats_t;
+
+/* Bytes of device workspace pg_attn_paged_mass needs for this plan (0 when none). */
+size_t pg_mass_workspace_bytes(const pg_plan_t plan);
+
+/*
+ * pg_attn_paged_mass -- pg_attn_paged_sink (same out and lse; lse must not be NULL), which also
+ * accumulates every key's attention weight: for KV head g and key j
+ *   c = sum over the step's rows t that see j and the query heads h of g of
+ *       exp( sm_scale * <q[t][h], K_j> - lse[t][h] )
+ * a key the step itself wrote (position >= start_pos) gets mass = c and pos = its position; an
+ * older key gets mass += c. Keys that no row sees and all other statistics stay as they were.
+ * Sums are fp32 in a fixed order: equal calls give equal bits.
+ *   workspace: ws_bytes >= pg_mass_workspace_bytes(plan), 16-byte aligned
+ * A page may be listed only once in the plan (PG_ERR_SHARED_PAGE): a shared page's slots belong
+ * to several requests. A plan updated under a captured graph must keep to that.
+ * Errors: those of pg_attn_paged_sink; PG_ERR_ARG (lse or stats NULL), PG_ERR_LAYOUT (statistics
+ * geometry or capacity), PG_ERR_ALIGN.
+ */
+int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
+                       const pg_bf16_t* q, pg_bf16_t* out, float* lse, const pg_kv_stats_t* stats,
+                       int32_t window_left, int32_t num_sink, float sm_scale, void* workspace,
+                       size_t ws_bytes, pg_stream_t stream);
+
+/*
+ * pg_kv_evict_select -- choose the keys each (layer, request, KV head) keeps, layers
+ * [layer, layer + num_layers). Of a request's n keys (slots [0, n) of its pages, as the plan of
+ * the step just run holds them) n' = min(n, budget) stay: the keys whose position (pos) is below
+ * num_sink or among the num_recent last ones (at or past the step's last position + 1 -
+ * num_recent), then the largest masses, equal masses by lower slot (NaN counts as -inf). The
+ * positions of a segment's keys must be distinct.
+ *   src [num_layers][num_req][num_kv_heads][budget] int32, written whole: src[s] is the slot
+ *       whose key will sit in slot s < n'. A kept key below n' stays (src[s] == s); the kept
+ *       keys at or past n' fill the slots of evicted keys below n', both in ascending order.
+ *       -1 for s >= n'.
+ * Nothing else is written; pg_kv_evict_apply makes the moves. 1 <= budget,
+ * num_sink + num_recent <= budget (PG_ERR_ARG). A page listed twice: PG_ERR_SHARED_PAGE. Other
+ * errors: PG_ERR_STREAM, PG_ERR_PLAN_MISMATCH, PG_ERR_LAYER, PG_ERR_LAYOUT, PG_ERR_PAGE_OOB,
+ * PG_ERR_ALIGN, PG_ERR_I32_OVERFLOW, PG_ERR_CUDA.
+ */
+int pg_kv_evict_select(const pg_plan_t plan, const pg_kv_stats_t* stats, int32_t layer,
+                       int32_t num_layers, int32_t budget, int32_t num_sink, int32_t num_recent,
+                       int32_t* src, pg_stream_t stream);
+
+/*
+ * pg_kv_evict_apply -- make the moves of pg_kv_evict_select (same plan, layers and budget): where
+ * src[s] is not s or -1, the K and V rows, mass and pos of slot src[s] are copied to slot s, in
+ * every layer of the range. Slots at or past n' keep what they held; the caller shortens the
+ * request to n' keys (a segment plan, see above) and may reuse the pages past them. Sources lie
+ * at or past n', destinations below it, so a repeated call changes nothing. An entry that select
+ * does not give (a source below n' or past the request's keys) is skipped and sets the device
+ * status word. Errors: as pg_kv_evict_select, and the pool checks of pg_attn_paged_prefill.
+ */
+int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_stats_t* stats,
+                      int32_t layer, int32_t num_layers, int32_t budget, const int32_t* src,
+                      pg_stream_t stream);
 
 /* ---------------------------------------------------------------- decode without allocation */
 /*

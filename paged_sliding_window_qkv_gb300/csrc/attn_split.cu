@@ -15,6 +15,14 @@
 //   decode (every request has one query token): one CTA per (request, KV head, key
 //   chunk); each chunk writes a partial (o, m, l) and a merge kernel combines them.
 //   A request whose visible keys fit one chunk is written directly.
+//
+// BC is the bounded-cache form: the first num_sink positions stay visible behind the window
+// (the key walk of bounded.cuh, tiles aligned from the first key held), the row sum adds the
+// unrounded fp32 weights, so lse is that of the fp32 scores, and a decode step's scores are kept
+// for the caller when it accumulates attention weights. The bf16 rounding of the weights that
+// multiply V (half a step, 2^-9 of each) then reaches the output instead of cancelling against
+// a rounded sum; it is as large as the rounding of the output itself.
+#include "bounded.cuh"
 #include "pg_internal.h"
 #include "../../include/pg.h"
 
@@ -28,6 +36,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
+constexpr int kDecTile = 32;  // keys per tile of the decode form
 constexpr float kLn2 = 0.69314718055994531f;  // log2 units to natural log
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -103,7 +112,7 @@ struct Cfg {
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-template <class C>
+template <class C, bool BC>
 __global__ void __launch_bounds__(kThreads, C::D == 256 ? 2 : 1)
 attn_split_kernel(AttnArgs a) {
   constexpr int D = C::D, BM = C::BM, BN = C::BN;
@@ -146,13 +155,35 @@ attn_split_kernel(AttnArgs a) {
   int32_t lo = W >= 0 ? max(ks0, p_first - W) : ks0;
   int32_t hi = min(p_last + 1, kv_len);
   int32_t nchunks = 1;
-  if (C::DECODE) {
+  KeyWalk walk{};
+  int32_t ntiles, vt0 = 0;  // BC: this CTA walks tiles vt0 .. vt0 + ntiles - 1 of the key walk
+  if constexpr (BC) {
+    walk = key_walk(W, a.num_sink, ks0, kv_len, p_first, p_last, BN);
+    lo = walk.lo;
+    ntiles = walk.total;
+    if (C::DECODE) {
+      const int32_t ct = a.kv_chunk / BN;
+      nchunks = (walk.total + ct - 1) / ct;
+      if (chunk >= max(nchunks, 1)) return;
+      vt0 = chunk * ct;
+      ntiles = min(ct, walk.total - vt0);
+    }
+  } else if (C::DECODE) {
     nchunks = (hi - lo + a.kv_chunk - 1) / a.kv_chunk;
     // a row that sees no key (possible in a key segment) is still written, by chunk 0
     if (chunk >= max(nchunks, 1)) return;
     lo = lo + chunk * a.kv_chunk;
     hi = min(hi, lo + a.kv_chunk);
   }
+  if constexpr (!BC) ntiles = (hi - lo + BN - 1) / BN;
+  // first key of the CTA's it-th tile
+  auto tile_key = [&](int32_t it) -> int32_t {
+    return BC ? ks0 + walk.tile(vt0 + it) * BN : lo + it * BN;
+  };
+  // a key that some row of the tile sees (others are not read: they act as zero rows)
+  auto key_live = [&](int32_t j) -> bool {
+    return j < hi && (!BC || (j >= ks0 && (W < 0 || j >= lo || j < a.num_sink)));
+  };
 
   // ---- Q tile (rows beyond the tile's tokens are zero) ----
   {
@@ -181,7 +212,7 @@ attn_split_kernel(AttnArgs a) {
   auto row_fetch = [&](int32_t kb) {
     RowAt r{-1, -1};
     const int32_t j = kb + jj;
-    if (j < hi) {
+    if (key_live(j)) {
       const int32_t rel = j - ks0;  // index among the keys held
       const int32_t lp = rel / ps;  // logical page; ring addressing wraps it over the pages held
       const int32_t pidx = kvp0 + (pl.ring ? lp % max(kvp1 - kvp0, 1) : lp);
@@ -210,19 +241,18 @@ attn_split_kernel(AttnArgs a) {
     }
   };
 
-  const int32_t ntiles = (hi - lo + BN - 1) / BN;
   // the first NS - 1 tiles (one commit group each; Q rides in the first), their lookups first
   {
     RowAt first[C::NS - 1];
 #pragma unroll
-    for (int st = 0; st < C::NS - 1; ++st) first[st] = row_fetch(lo + st * BN);
+    for (int st = 0; st < C::NS - 1; ++st) first[st] = row_fetch(tile_key(st));
 #pragma unroll
     for (int st = 0; st < C::NS - 1; ++st) {
       if (st < ntiles) row_issue(st, first[st]);
       cp_async_commit();
     }
   }
-  RowAt pend = row_fetch(lo + (C::NS - 1) * BN);  // the tile the first iteration loads
+  RowAt pend = row_fetch(tile_key(C::NS - 1));  // the tile the first iteration loads
 
   // S-warp coordinates
   const int s_mt = warp % C::WM;
@@ -248,14 +278,14 @@ attn_split_kernel(AttnArgs a) {
 
   for (int32_t it = 0; it < ntiles; ++it) {
     const int stage = it % C::NS;
-    const int32_t kb = lo + it * BN;
+    const int32_t kb = tile_key(it);
     // tile it has landed (at most NS - 2 newer groups pending); every warp is past tile it - 1,
     // whose stage the next load reuses
     cp_async_wait<C::NS - 2>();
     __syncthreads();
     if (it + C::NS - 1 < ntiles) row_issue((it + C::NS - 1) % C::NS, pend);
     cp_async_commit();
-    pend = row_fetch(kb + C::NS * BN);  // the next iteration's tile
+    pend = row_fetch(BC ? tile_key(it + C::NS) : kb + C::NS * BN);  // the next iteration's tile
 
     // ---- S = Q K^T (this warp: one m-tile, NT n-tiles, one k-split) ----
     {
@@ -317,8 +347,10 @@ attn_split_kernel(AttnArgs a) {
             const int32_t j = kb + col;
             // decode: every key in [lo, hi) is visible (the range already applies the window
             // and hi <= position + 1)
-            const bool vis = C::DECODE ? rv && j < hi
-                                       : rv && j < hi && j <= pos && (W < 0 || pos - j <= W);
+            const bool vis =
+                BC ? rv && key_live(j) && j <= pos && (W < 0 || pos - j <= W || j < a.num_sink)
+                : C::DECODE ? rv && j < hi
+                            : rv && j < hi && j <= pos && (W < 0 || pos - j <= W);
             S[m * C::SLD + col] = vis ? acc[nt][h2 * 2 + e] * a.sm_scale_log2 : -INFINITY;
           }
         }
@@ -340,6 +372,18 @@ attn_split_kernel(AttnArgs a) {
           s[v] += y.x; s[v + 1] += y.y;
         }
       }
+      if constexpr (BC && C::DECODE) {
+        // the scores of the keys the row sees, [slot of the batch's page list][query head]
+        if (a.logits && sm_valid) {
+#pragma unroll
+          for (int v = 0; v < C::VPT; ++v) {
+            const int32_t j = kb + sm_sub * C::VPT + v;
+            const int64_t slot = (int64_t)kvp0 * ps + (j - ks0);
+            if (key_live(j) && slot < a.logit_slots)
+              a.logits[slot * Hq + g * G + sm_row] = s[v];
+          }
+        }
+      }
       float mx = -INFINITY;
 #pragma unroll
       for (int v = 0; v < C::VPT; ++v) mx = fmaxf(mx, s[v]);
@@ -354,8 +398,9 @@ attn_split_kernel(AttnArgs a) {
       for (int v = 0; v < C::VPT; v += 2) {
         // sum the bf16-rounded weights that the PV product uses (O / l stays an exact
         // weighted average of V rows)
-        const __nv_bfloat162 pb = __floats2bfloat162_rn(exp2f(s[v] - m_use), exp2f(s[v + 1] - m_use));
-        sum += __bfloat162float(pb.x) + __bfloat162float(pb.y);
+        const float e0 = exp2f(s[v] - m_use), e1 = exp2f(s[v + 1] - m_use);
+        const __nv_bfloat162 pb = __floats2bfloat162_rn(e0, e1);
+        sum += BC ? e0 + e1 : __bfloat162float(pb.x) + __bfloat162float(pb.y);
         *reinterpret_cast<__nv_bfloat162*>(P + v) = pb;
       }
 #pragma unroll
@@ -440,7 +485,7 @@ attn_split_kernel(AttnArgs a) {
 // The chunks' (m, l) pairs are loaded once, spread over the threads, and kept in shared memory
 // (256 chunks at a time); then each thread issues its loads of four columns for eight chunks at
 // once, so a row waits for about two round trips to memory rather than one per chunk.
-template <int D>
+template <int D, bool BC>
 __global__ void __launch_bounds__(D / 4)
 attn_merge_kernel(AttnArgs a) {
   constexpr int NT = D / 4, NWARP = NT / 32, CB = 256;
@@ -455,7 +500,12 @@ attn_merge_kernel(AttnArgs a) {
   const int32_t W = a.window_left;
   const int32_t lo = W >= 0 ? max(ks0, p - W) : ks0;
   const int32_t hi = min(p + 1, kv_len);
-  const int32_t nch = (hi - lo + a.kv_chunk - 1) / a.kv_chunk;
+  int32_t nch = (hi - lo + a.kv_chunk - 1) / a.kv_chunk;
+  if constexpr (BC) {
+    // the key walk is counted in the partition kernel's tiles; a chunk is a whole number of them
+    const KeyWalk walk = key_walk(W, a.num_sink, ks0, kv_len, p, p, kDecTile);
+    nch = (walk.total + a.kv_chunk / kDecTile - 1) / (a.kv_chunk / kDecTile);
+  }
   if (nch <= 1) return;  // written directly by the partition kernel
   const int64_t row = ((int64_t)r * a.num_qo_heads + h) * a.max_chunks;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -523,19 +573,20 @@ using Pre512 = Cfg<512, 32, 32, 1, 1, false>;
 // 16): the CTA is alone on its SM, so the chains' latency is what it waits on.
 using Dec256 = Cfg<256, 16, 32, 1, 2, true, 3>;
 using Dec512 = Cfg<512, 16, 32, 2, 4, true, 3>;
+static_assert(Dec256::BN == kDecTile && Dec512::BN == kDecTile, "decode tile");
 
-template <class C>
+template <class C, bool BC>
 cudaError_t launch_split(const AttnArgs& a, dim3 grid, cudaStream_t stream) {
   static PerDeviceOnce setup;  // the shared-memory opt-in, once per device
   int dev = 0, unused = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = setup.get(dev, [](int*) {
-    return cudaFuncSetAttribute(attn_split_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(attn_split_kernel<C, BC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)C::SMEM);
   }, &unused);
   if (e != cudaSuccess) return e;
-  attn_split_kernel<C><<<grid, kThreads, C::SMEM, stream>>>(a);
+  attn_split_kernel<C, BC><<<grid, kThreads, C::SMEM, stream>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -557,8 +608,11 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t head_dim, cudaStream_
   if (attn_tc_supported(head_dim, a.group, a.pool.page_size))
     return launch_attn_prefill_tc(a, head_dim, stream);
   dim3 grid(a.plan.num_work, a.pool.num_kv_heads, 1);
-  return head_dim == 256 ? launch_split<Pre256>(a, grid, stream)
-                         : launch_split<Pre512>(a, grid, stream);
+  if (a.bounded)
+    return head_dim == 256 ? launch_split<Pre256, true>(a, grid, stream)
+                           : launch_split<Pre512, true>(a, grid, stream);
+  return head_dim == 256 ? launch_split<Pre256, false>(a, grid, stream)
+                         : launch_split<Pre512, false>(a, grid, stream);
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& args, int32_t head_dim, cudaStream_t stream) {
@@ -571,12 +625,20 @@ cudaError_t launch_attn_decode(const AttnArgs& args, int32_t head_dim, cudaStrea
   a.ws_o = reinterpret_cast<float*>(a.ws_raw);
   a.ws_ml = a.ws_o + rows * (size_t)head_dim;
   dim3 grid(a.plan.num_req, a.pool.num_kv_heads, a.max_chunks);
-  cudaError_t e = head_dim == 256 ? launch_split<Dec256>(a, grid, stream)
-                                  : launch_split<Dec512>(a, grid, stream);
+  const bool bc = a.bounded != 0;
+  cudaError_t e = head_dim == 256 ? (bc ? launch_split<Dec256, true>(a, grid, stream)
+                                        : launch_split<Dec256, false>(a, grid, stream))
+                                  : (bc ? launch_split<Dec512, true>(a, grid, stream)
+                                        : launch_split<Dec512, false>(a, grid, stream));
   if (e != cudaSuccess) return e;
   dim3 mgrid(a.plan.num_req, a.num_qo_heads, 1);
-  if (head_dim == 256) attn_merge_kernel<256><<<mgrid, 256 / 4, 0, stream>>>(a);
-  else attn_merge_kernel<512><<<mgrid, 512 / 4, 0, stream>>>(a);
+  if (head_dim == 256) {
+    if (bc) attn_merge_kernel<256, true><<<mgrid, 256 / 4, 0, stream>>>(a);
+    else attn_merge_kernel<256, false><<<mgrid, 256 / 4, 0, stream>>>(a);
+  } else {
+    if (bc) attn_merge_kernel<512, true><<<mgrid, 512 / 4, 0, stream>>>(a);
+    else attn_merge_kernel<512, false><<<mgrid, 512 / 4, 0, stream>>>(a);
+  }
   count_launch();
   return cudaGetLastError();
 }

@@ -44,9 +44,14 @@
 // O holds 256 output columns: for head_dim 512 each query tile is two units, each computing
 // the full 512-wide S and half of O. The TMEM map is described at TcCfg.
 //
+// BC is the bounded-cache form: the first num_sink positions stay visible behind the window, so
+// a unit walks its sink tiles and then its window tiles (bounded.cuh; one run where they meet),
+// and the row sum adds the unrounded weights (see attn_split.cu).
+//
 // Every wait is bounded (two seconds of %globaltimer unless the launch passes a shorter limit);
 // a wait that runs out sets the device status word, makes the CTA drain and free its tensor
 // memory, and return.
+#include "bounded.cuh"
 #include "pg_internal.h"
 
 #include <cuda.h>
@@ -124,7 +129,7 @@ struct TcArgs {
   __nv_bfloat16* out;
   const __nv_bfloat16* pool_layer;  // pool base of the called layer
   int64_t stride_page, stride_kv, stride_head;
-  int32_t num_qo_heads, group, cta_tile_q, window_left;
+  int32_t num_qo_heads, group, cta_tile_q, window_left, num_sink;
   int32_t page_size, num_pages, num_kv_heads, box_rows_k, box_rows_v;
   float scale_log2;
   float* lse;  // optional [T][Hq] natural-log normaliser of each row (null: not written)
@@ -366,7 +371,13 @@ struct TcUnit {
   int32_t q0, tok0, ntok;  // this CTA's query tile: request's first token, tile start, tokens (0: none)
   // keys held: positions [kv_start, kv_len); key tiles start kb0 + 64 t, 64-aligned from kv_start
   int32_t kvp0, kvp1, kv_len, kv_start, sp, kb0, ntiles, g, dh;
+  int32_t ns;  // BC: the first ns tiles are sink tiles, aligned from kv_start
+  template <bool BC>
+  __device__ __forceinline__ int32_t key(int32_t t) const {  // first key of the t-th tile
+    return BC && t < ns ? kv_start + t * kBN : kb0 + (BC ? t - ns : t) * kBN;
+  }
 };
+template <bool BC>
 __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t ndh, int32_t rank) {
   const PlanDev& pl = a.plan;
   TcUnit u;
@@ -389,6 +400,14 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
   // the pair's key range: the keys some row of either tile sees
   const int32_t W = a.window_left;
   const int32_t p_first = u.sp + t0, p_last = u.sp + min(t0 + 2 * TQ, len) - 1;
+  u.ns = 0;
+  if constexpr (BC) {
+    const KeyWalk k = key_walk(W, a.num_sink, u.kv_start, u.kv_len, p_first, p_last, kBN);
+    u.ns = k.ns;
+    u.kb0 = u.kv_start + k.ft * kBN;
+    u.ntiles = k.total;
+    return u;
+  }
   const int32_t lo = W >= 0 ? max(u.kv_start, p_first - W) : u.kv_start;
   const int32_t hi = min(p_last + 1, u.kv_len);
   // tiles are aligned from the first key held, so a box of page rows never straddles a page
@@ -402,7 +421,7 @@ __device__ __forceinline__ void tc_unit_prefetch(const TcArgs& a, int32_t w, int
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a.plan.pair_tab + 8 * pr));
 }
 
-template <int DQK>
+template <int DQK, bool BC>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                const __grid_constant__ CUtensorMap tm_v, TcArgs a) {
@@ -527,7 +546,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     auto stage_q = [&](int32_t k) -> bool {
       if (lane != 0) return true;
       if (k > 0 && !mbar_wait(QSFREE, (k - 1) & 1, wc)) return false;
-      const TcUnit v = tc_unit(a, unit_at(k), NDH, (int32_t)rank);
+      const TcUnit v = tc_unit<BC>(a, unit_at(k), NDH, (int32_t)rank);
       mbar_expect_tx(QSFULL, v.ntok > 0 ? (uint32_t)C::QS_BYTES : 0u);
       if (v.ntok > 0)
         for (int c = 0; c < 4; ++c)
@@ -538,7 +557,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     int32_t J = 0;  // tiles of this cluster's earlier units
     int32_t ui = 0;
     for (int32_t w = unit_at(0); ok && w < nunits; w = unit_at(++ui)) {
-      const TcUnit u = tc_unit(a, w, NDH, (int32_t)rank);
+      const TcUnit u = tc_unit<BC>(a, w, NDH, (int32_t)rank);
       // head_dim 256: the next unit's Q is staged after this unit's fourth K tile has been issued:
       // that tile's slot wait shows this unit's first QK complete, so its Q has left the staging
       // buffer and the wait for it does not hold up the ring (in units of up to four tiles it
@@ -550,7 +569,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // L2, so the softmax warps' move to that unit waits on L2 rather than DRAM
         if (unit_at(ui + 2) < nunits) tc_unit_prefetch(a, unit_at(ui + 2), NDH);
         if (DQK != 256 && unit_at(ui + 1) < nunits) {
-          const TcUnit un = tc_unit(a, unit_at(ui + 1), NDH, (int32_t)rank);
+          const TcUnit un = tc_unit<BC>(a, unit_at(ui + 1), NDH, (int32_t)rank);
           if (un.ntok > 0)
             for (int c = 0; c < DQK / 64; ++c) tma_prefetch_3d(&tm_q, c * 64, un.g * G, un.q0 + un.tok0);
         }
@@ -582,7 +601,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       auto lookup = [&](int32_t t0) -> int32_t {  // page id of this lane's box in the batch at t0
         const int32_t tt = t0 + my_t;
         if (tt >= u.ntiles) return -1;
-        const int32_t ks = u.kb0 + tt * kBN + key_off + my_b * BR;
+        const int32_t ks = u.key<BC>(tt) + key_off + my_b * BR;
         if (ks >= u.kv_len) return -1;
         const int32_t lp = (ks - u.kv_start) / ps;  // logical page; a ring wraps it over its pages
         const int32_t pidx = u.kvp0 + (pl.ring ? lp % max(u.kvp1 - u.kvp0, 1) : lp);
@@ -604,7 +623,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           my_page = pg_next;
           pg_next = lookup(t + TB);  // used TB tiles from now
           const int32_t tt = t + my_t;
-          const int32_t ks = u.kb0 + tt * kBN + key_off + my_b * BR;
+          const int32_t ks = u.key<BC>(tt) + key_off + my_b * BR;
           const bool live = tt < u.ntiles;
           const bool past = !live || ks >= u.kv_len;
           const bool bad = !past && (my_page < 0 || my_page >= a.num_pages);
@@ -682,7 +701,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               fix_phase ^= 1u;
             }
             // zero this warp's rows that must not be read: keys past kv_len, keys on bad pages
-            const int32_t kb = u.kb0 + t * kBN + key_off;  // first key of this CTA's half
+            const int32_t kb = u.key<BC>(t) + key_off;  // first key of this CTA's half
             for (int b = 0; b < nbox; ++b) {
               const int32_t pb = __shfl_sync(0xffffffffu, my_page, sh + b);
               for (int rr = 0; rr < BR; ++rr) {
@@ -729,7 +748,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     int32_t ui = 0;
     int32_t nof = 0;  // head_dim 256: units with tiles whose PVs this warp has issued
     for (int32_t w = unit_at(0); leader && ok && w < nunits; w = unit_at(++ui)) {
-      const int32_t ntiles = tc_unit(a, w, NDH, 0).ntiles;
+      const int32_t ntiles = tc_unit<BC>(a, w, NDH, 0).ntiles;
       if (warp == 1) {
         ok = wait1(QFULL, ui & 1);  // this unit's Q is in place in both CTAs
         for (int32_t j = 0; ok && j < ntiles; ++j) {
@@ -908,7 +927,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     TcUnit u;
     int32_t ui = 0;
     if (unit_at(0) < nunits) {
-      u = tc_unit(a, unit_at(0), NDH, (int32_t)rank);
+      u = tc_unit<BC>(a, unit_at(0), NDH, (int32_t)rank);
       if (DQK != 256 || h == 0) ok = store_q(u, 0);
     }
     for (int32_t w = unit_at(0); ok && w < nunits; w = unit_at(++ui)) {
@@ -917,6 +936,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const int32_t prow = u.sp + u.tok0 + (row >> gsh);
       const int32_t rlo = W >= 0 ? max(u.kv_start, prow - W) : u.kv_start;
       const int32_t rhi = min(prow + 1, u.kv_len);
+      const int32_t sink = a.num_sink;  // BC: keys below it are visible whatever the window
       float m_ref = -INFINITY, l = 0.f;
       if constexpr (DQK == 256) {
         // Tile-parity softmax: the two warps of a lane quarter take alternate key tiles (warp h
@@ -942,13 +962,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           __syncwarp();
           // this warp has read S(JJ): the S buffer is free for QK(JJ + 2) once all have
           if (lane == 0) mbar_arrive_cl(LEAD(SFREE + 8 * b));
-          const int32_t kb = u.kb0 + j * kBN;
-          const bool interior = __all_sync(0xffffffffu, rvalid && kb >= rlo && kb + kBN <= rhi);
+          const int32_t kb = u.key<BC>(j);
+          const bool interior =
+              __all_sync(0xffffffffu, rvalid && (kb >= rlo || (BC && kb + kBN <= sink)) && kb + kBN <= rhi);
           if (!interior) {
 #pragma unroll
             for (int k = 0; k < kBN; ++k) {
               const int32_t key = kb + k;
-              const bool vis = rvalid && key >= rlo && key < rhi;
+              const bool vis = rvalid && (key >= rlo || (BC && key < sink)) && key < rhi;
               sv[k] = vis ? sv[k] : 0xFF800000u;  // -inf
             }
           }
@@ -995,14 +1016,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           uint32_t pk[kBN / 2];
           {
             // exponents and row sums on fp32 pairs; the row sum adds the bf16-rounded weights the
-            // PV product uses, so O / l is an exact weighted average of V rows
+            // PV product uses, so O / l is an exact weighted average of V rows (BC: the unrounded)
             const float2 ts2 = make_float2(tscale, tscale), nmu2 = make_float2(-mu, -mu);
             float2 sa = make_float2(0.f, 0.f), sb2 = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kBN / 2; ++k) {
               const float2 e = __ffma2_rn(make_float2(t[2 * k], t[2 * k + 1]), ts2, nmu2);
-              pk[k] = pack_bf16(ex2(e.x), ex2(e.y));
-              const float2 wv = make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
+              const float2 x = make_float2(ex2(e.x), ex2(e.y));
+              pk[k] = pack_bf16(x.x, x.y);
+              const float2 wv =
+                  BC ? x : make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
               if (k & 1) sb2 = __fadd2_rn(sb2, wv);
               else sa = __fadd2_rn(sa, wv);
             }
@@ -1069,7 +1092,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // this thread's 32 keys (masked keys: -inf); log2 units are t * tscale
         float t[HC];
         const float tscale = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
-        const int32_t kb = u.kb0 + j * kBN;
+        const int32_t kb = u.key<BC>(j);
         {
         // both warps of the pair read the whole 64-key row: the row maximum needs no exchange
         uint32_t sv[kBN];
@@ -1080,12 +1103,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         __syncwarp();
         // this warp has read S(JJ): the S buffer is free for QK(JJ + 2) once all have
         if (lane == 0) mbar_arrive_cl(LEAD(SFREE + 8 * b));
-        const bool interior = __all_sync(0xffffffffu, rvalid && kb >= rlo && kb + kBN <= rhi);
+        const bool interior =
+            __all_sync(0xffffffffu, rvalid && (kb >= rlo || (BC && kb + kBN <= sink)) && kb + kBN <= rhi);
         if (!interior) {
 #pragma unroll
           for (int k = 0; k < kBN; ++k) {
             const int32_t key = kb + k;
-            const bool vis = rvalid && key >= rlo && key < rhi;
+            const bool vis = rvalid && (key >= rlo || (BC && key < sink)) && key < rhi;
             sv[k] = vis ? sv[k] : 0xFF800000u;  // -inf
           }
         }
@@ -1145,8 +1169,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
           for (int k = 0; k < HC / 2; ++k) {
             const float2 e = __ffma2_rn(make_float2(t[2 * k], t[2 * k + 1]), ts2, nmu2);
-            pk[k] = pack_bf16(ex2(e.x), ex2(e.y));
-            const float2 w = make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
+            const float2 x = make_float2(ex2(e.x), ex2(e.y));
+            pk[k] = pack_bf16(x.x, x.y);
+            const float2 w =
+                BC ? x : make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
             if (k & 1) sb2 = __fadd2_rn(sb2, w);
             else sa = __fadd2_rn(sa, w);
           }
@@ -1177,7 +1203,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (!ok) break;
       const int32_t wn = unit_at(ui + 1);
       TcUnit un;
-      if (wn < nunits) un = tc_unit(a, wn, NDH, (int32_t)rank);
+      if (wn < nunits) un = tc_unit<BC>(a, wn, NDH, (int32_t)rank);
       if constexpr (DQK == 256) {
         // The row sum is the sum of the two warps' partial sums, swapped through shared memory.
         // The warp that wrote the last tile's P waits for that tile's PV before publishing (its
@@ -1356,7 +1382,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-template <int DQK>
+template <int DQK, bool BC>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
@@ -1410,6 +1436,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   t.group = G;
   t.cta_tile_q = TQ;
   t.window_left = a.window_left;
+  t.num_sink = a.num_sink;
   t.page_size = ps;
   t.num_pages = a.pool.num_pages;
   t.num_kv_heads = a.pool.num_kv_heads;
@@ -1431,7 +1458,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = setup.get(dev, [dev](int* n) {
-    cudaError_t r = cudaFuncSetAttribute(attn_tc_kernel<DQK>,
+    cudaError_t r = cudaFuncSetAttribute(attn_tc_kernel<DQK, BC>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<DQK>::SMEM);
     if (r != cudaSuccess) return r;
     r = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
@@ -1457,7 +1484,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK>, tq, tkv, tv, t);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, BC>, tq, tkv, tv, t);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -1474,7 +1501,9 @@ bool attn_tc_supported(int32_t head_dim, int32_t group, int32_t page_size) {
 
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
   if (a.plan.num_work == 0) return cudaSuccess;
-  return head_dim == 256 ? launch_tc<256>(a, stream) : launch_tc<512>(a, stream);
+  if (a.bounded)
+    return head_dim == 256 ? launch_tc<256, true>(a, stream) : launch_tc<512, true>(a, stream);
+  return head_dim == 256 ? launch_tc<256, false>(a, stream) : launch_tc<512, false>(a, stream);
 }
 
 int32_t attn_tc_rows() { return kM; }

@@ -103,6 +103,9 @@ struct pg_plan {
   size_t o_qo = 0, o_kvp = 0, o_pages = 0, o_last = 0, o_start = 0, o_kvs = 0, o_tokreq = 0,
          o_wreq = 0, o_wtok = 0, o_pair = 0;
   PlanStage stage;  // carried over from build to build of the same plan
+  int32_t max_seen = 0;           // the most keys a request holds
+  std::vector<int32_t> host_ids;  // the page list, for the check below
+  mutable int8_t shared = -1;     // a page is listed twice (-1: not looked at yet)
 };
 
 namespace {
@@ -330,11 +333,13 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.stream = stream; q.device = dev;
   q.dev = d; q.dev_elems = host.size();
   q.dev_cap = fresh ? bytes : p->dev_cap;
+  q.max_seen = max_seen;
+  q.host_ids = std::move(pids);
 
   // Commit: only now does the caller's plan change.
   int32_t* old = p->dev;
   q.stage = p->stage;
-  *p = q;
+  *p = std::move(q);
   if (fresh && old) cudaFreeAsync(old, stream);
   return PG_OK;
 }
@@ -468,9 +473,19 @@ size_t workspace_bytes(const pg_plan* p) {
   return rows * (size_t)p->head_dim * sizeof(float) + rows * 2 * sizeof(float);
 }
 
+// Bounded-cache attention: the sinks, and the decode scores to keep (see AttnArgs).
+struct Bounded {
+  int32_t num_sink = 0;
+  float* logits = nullptr;
+  int64_t logit_slots = 0;
+};
+
+// `args` (optional) receives the launched call's arguments, with num_tokens 0 when nothing ran.
 int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32_t D,
                 const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
-                float sm_scale, void* ws, size_t ws_bytes, cudaStream_t stream) {
+                float sm_scale, void* ws, size_t ws_bytes, cudaStream_t stream,
+                const Bounded* bounded = nullptr, AttnArgs* args = nullptr) {
+  if (args) args->plan.num_tokens = 0;
   if (!plan) return PG_ERR_ARG;
   if (stream != plan->stream) return PG_ERR_STREAM;
   int rc = check_plan_pool(plan, pool, layer, D);
@@ -518,17 +533,128 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   a.kv_chunk = plan->kv_chunk;
   a.max_chunks = plan->max_chunks;
   a.status = st;
+  a.bounded = bounded ? 1 : 0;
+  a.num_sink = bounded ? bounded->num_sink : 0;
+  a.logits = bounded ? bounded->logits : nullptr;
+  a.logit_slots = bounded ? bounded->logit_slots : 0;
   wait_settings(&a.wait_ns, &a.test_withhold);
   cudaError_t e;
   a.ws_raw = ws;
   a.ws_o = nullptr;
   a.ws_ml = nullptr;
+  if (args) *args = a;
   if (plan->decode) {
     e = launch_attn_decode(a, D, stream);
   } else {
     e = launch_attn_prefill(a, D, stream);
   }
   return e == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+// ---- bounded-cache operators: checks shared by their entries
+// A page that two places of the page list name has no statistics of its own, and rows moved
+// within it for one request would move under the other.
+int shares_pages(const pg_plan* p, bool* out) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lk(mu);
+  if (p->shared < 0) {
+    try {
+      std::vector<int32_t> ids(p->host_ids);
+      std::sort(ids.begin(), ids.end());
+      p->shared = std::adjacent_find(ids.begin(), ids.end()) != ids.end() ? 1 : 0;
+    } catch (const std::bad_alloc&) {
+      return PG_ERR_ARG;
+    }
+  }
+  *out = p->shared == 1;
+  return PG_OK;
+}
+
+int check_stats(const pg_plan* p, const pg_kv_stats_t* st, int32_t layer, int32_t num_layers) {
+  if (!st || !st->mass || !st->pos) return PG_ERR_ARG;
+  if (st->num_layers <= 0 || st->num_pages <= 0 || st->page_size <= 0 || st->num_kv_heads <= 0)
+    return PG_ERR_LAYOUT;
+  if (((uintptr_t)st->mass & 3u) || ((uintptr_t)st->pos & 3u)) return PG_ERR_ALIGN;
+  int64_t n = 0;
+  if (!mul_i64(st->num_layers, st->num_pages, &n) || !mul_i64(n, st->num_kv_heads, &n) ||
+      !mul_i64(n, st->page_size, &n))
+    return PG_ERR_I32_OVERFLOW;
+  if (st->capacity != n) return PG_ERR_LAYOUT;
+  if (p->num_kv_heads != st->num_kv_heads || p->page_size != st->page_size)
+    return PG_ERR_PLAN_MISMATCH;
+  if (layer < 0 || num_layers < 1 || layer > st->num_layers - num_layers) return PG_ERR_LAYER;
+  if (p->max_page_id >= st->num_pages) return PG_ERR_PAGE_OOB;
+  return PG_OK;
+}
+
+StatsDev stats_dev(const pg_kv_stats_t* st, int32_t layer) {
+  StatsDev v;
+  v.stride_layer = (int64_t)st->num_pages * st->num_kv_heads * st->page_size;
+  v.mass = st->mass + layer * v.stride_layer;
+  v.pos = st->pos + layer * v.stride_layer;
+  return v;
+}
+
+// plan, stream and device of a bounded-cache call
+int check_bounded_plan(const pg_plan* plan, cudaStream_t stream) {
+  if (!plan) return PG_ERR_ARG;
+  if (stream != plan->stream) return PG_ERR_STREAM;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PG_ERR_CUDA;
+  if (dev != plan->device) return PG_ERR_STREAM;
+  if (plan->ring) return PG_ERR_PLAN_MISMATCH;  // a ring overwrites the positions these keep
+  return PG_OK;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Scores that a decode step of the plan keeps: [slots of the page list][num_qo_heads].
+int64_t logit_slots(const pg_plan* p) { return (int64_t)p->num_page_ids * p->page_size; }
+
+size_t mass_workspace_bytes(const pg_plan* p) {
+  if (!p || p->num_req == 0) return 0;
+  if (p->decode)
+    return align256(workspace_bytes(p)) + (size_t)logit_slots(p) * p->num_qo_heads * sizeof(float);
+  return 0;
+}
+
+// Checks of an eviction call, and its arguments.
+int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer, int32_t num_layers,
+                 int32_t budget, const int32_t* src, cudaStream_t stream, EvictArgs* a) {
+  int rc = check_bounded_plan(plan, stream);
+  if (rc) return rc;
+  if ((rc = check_stats(plan, stats, layer, num_layers))) return rc;
+  if (budget < 1) return PG_ERR_ARG;
+  bool shared = false;
+  if ((rc = shares_pages(plan, &shared))) return rc;
+  if (shared) return PG_ERR_SHARED_PAGE;
+  a->plan = plan_dev(plan);
+  if (plan->num_req == 0) return PG_OK;
+  if (!src) return PG_ERR_ARG;
+  if ((uintptr_t)src & 3u) return PG_ERR_ALIGN;
+  // every grid of the call fits: a block covers 8 groups of 32 kept slots, or one segment
+  int64_t segs = 0, groups = 0;
+  const int64_t keep = std::min(plan->max_seen, budget);
+  if (!mul_i64(num_layers, plan->num_req, &segs) || !mul_i64(segs, plan->num_kv_heads, &segs) ||
+      !mul_i64(segs, (keep + 31) / 32, &groups) || !fits_i32(segs) || !fits_i32(groups / 8 + 1))
+    return PG_ERR_I32_OVERFLOW;
+  int err = PG_OK;
+  int* st = status_word(&err);
+  if (!st) return err;
+  a->pool = PoolDev{};
+  a->pool.num_pages = stats->num_pages;
+  a->pool.page_size = stats->page_size;
+  a->pool.num_kv_heads = stats->num_kv_heads;
+  a->pool.head_dim = plan->head_dim;
+  a->pool_stride_layer = 0;
+  a->stats = stats_dev(stats, layer);
+  a->src = const_cast<int32_t*>(src);
+  a->num_layers = num_layers;
+  a->budget = budget;
+  a->num_sink = a->num_recent = 0;
+  a->max_keys = plan->max_seen;
+  a->status = st;
+  return PG_OK;
 }
 
 // The device's status word if it already exists; never allocates.
@@ -740,6 +866,98 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
   return e == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
+int pg_attn_paged_sink(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
+                       const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
+                       int32_t num_sink, float sm_scale, void* workspace, size_t ws_bytes,
+                       pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int rc = check_bounded_plan(plan, s);
+  if (rc) return rc;
+  if (num_sink < 0) return PG_ERR_WINDOW;
+  if (plan->head_dim != 256 && plan->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
+  Bounded b;
+  b.num_sink = num_sink;
+  return attn_common(plan, pool, layer, plan->head_dim, q, out, lse, window_left, sm_scale, workspace,
+                     ws_bytes, s, &b);
+}
+
+size_t pg_mass_workspace_bytes(const pg_plan_t plan) { return mass_workspace_bytes(plan); }
+
+int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
+                       const pg_bf16_t* q, pg_bf16_t* out, float* lse, const pg_kv_stats_t* stats,
+                       int32_t window_left, int32_t num_sink, float sm_scale, void* workspace,
+                       size_t ws_bytes, pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = check_bounded_plan(plan, s);
+  if (rc) return rc;
+  if (num_sink < 0) return PG_ERR_WINDOW;
+  if (plan->head_dim != 256 && plan->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
+  if ((rc = check_plan_pool(plan, pool, layer, plan->head_dim))) return rc;
+  if ((rc = check_stats(plan, stats, layer, 1))) return rc;
+  if (stats->num_layers != pool->num_layers || stats->num_pages != pool->num_pages)
+    return PG_ERR_LAYOUT;
+  bool shared = false;
+  if ((rc = shares_pages(plan, &shared))) return rc;
+  if (shared) return PG_ERR_SHARED_PAGE;
+  if (plan->num_tokens > 0 && !lse) return PG_ERR_ARG;
+  const size_t need = mass_workspace_bytes(plan);
+  if (need > 0) {
+    if (!workspace || ws_bytes < need) return PG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PG_ERR_ALIGN;
+  }
+  // one block per 64 keys of a head (prefill) or 256 keys of a request (decode)
+  int64_t blocks = 0;
+  if (!mul_i64((plan->max_seen + 63) / 64, plan->num_req, &blocks) ||
+      !mul_i64(blocks, plan->num_kv_heads, &blocks) || !fits_i32(blocks))
+    return PG_ERR_I32_OVERFLOW;
+  Bounded b;
+  b.num_sink = num_sink;
+  const size_t attn_ws = align256(workspace_bytes(plan));
+  if (plan->decode && plan->num_req > 0) {
+    b.logits = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn_ws);
+    b.logit_slots = logit_slots(plan);
+  }
+  MassArgs m{};
+  rc = attn_common(plan, pool, layer, plan->head_dim, q, out, lse, window_left, sm_scale, workspace,
+                   attn_ws, s, &b, &m.attn);
+  if (rc != PG_OK || plan->num_tokens == 0) return rc;
+  m.stats = stats_dev(stats, layer);
+  m.max_keys = plan->max_seen;
+  const cudaError_t e =
+      plan->decode ? launch_mass_decode(m, s) : launch_mass_prefill(m, plan->head_dim, s);
+  return e == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+int pg_kv_evict_select(const pg_plan_t plan, const pg_kv_stats_t* stats, int32_t layer,
+                       int32_t num_layers, int32_t budget, int32_t num_sink, int32_t num_recent,
+                       int32_t* src, pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  EvictArgs a;
+  if (num_sink < 0 || num_recent < 0 || (int64_t)num_sink + num_recent > budget) return PG_ERR_ARG;
+  const int rc = evict_common(plan, stats, layer, num_layers, budget, src, s, &a);
+  if (rc != PG_OK || plan->num_req == 0) return rc;
+  a.num_sink = num_sink;
+  a.num_recent = num_recent;
+  return launch_evict_select(a, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_stats_t* stats,
+                      int32_t layer, int32_t num_layers, int32_t budget, const int32_t* src,
+                      pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  EvictArgs a;
+  int rc = evict_common(plan, stats, layer, num_layers, budget, src, s, &a);
+  if (rc) return rc;
+  if ((rc = check_plan_pool(plan, pool, layer, plan->head_dim))) return rc;
+  if (stats->num_layers != pool->num_layers || stats->num_pages != pool->num_pages)
+    return PG_ERR_LAYOUT;
+  if (plan->head_dim % 8 != 0) return PG_ERR_ALIGN;
+  if (plan->num_req == 0) return PG_OK;
+  a.pool = pool_dev(pool, layer);
+  a.pool_stride_layer = pool->stride_layer;
+  return launch_evict_apply(a, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
 int pg_attn_paged_decode_noalloc(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
                                  const pg_bf16_t* q, pg_bf16_t* out, int32_t window_left,
                                  float sm_scale, pg_stream_t stream) {
@@ -773,7 +991,7 @@ int pg_attn_paged_decode_noalloc(const pg_plan_t plan, const pg_pool_t* pool, in
   int err = PG_OK;
   int* st = status_word_existing(&err);
   if (!st) return err;
-  AttnArgs a;
+  AttnArgs a{};
   a.plan = plan_dev(plan);
   a.pool = pool_dev(pool, layer);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
@@ -844,6 +1062,7 @@ const char* pg_status_string(int s) {
     case PG_ERR_CUDA: return "CUDA runtime error";
     case PG_ERR_DEVICE_BOUNDS: return "a kernel skipped an out-of-range access";
     case PG_ERR_ALIGN: return "pointer or stride not 16-byte aligned";
+    case PG_ERR_SHARED_PAGE: return "a page is listed twice where each needs its own";
     case PG_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait and returned early";
     default: return "unknown status";
   }

@@ -89,9 +89,46 @@ struct AttnArgs {
   int32_t cta_tile_q;   // query tokens per prefill CTA
   int32_t kv_chunk;     // keys per decode chunk
   int32_t max_chunks;
+  // bounded-cache form (0: off): the first num_sink positions stay visible behind the window, and
+  // row sums add unrounded weights; decode scores go to logits[slot][Hq] (log2 units; slot counts
+  // through the batch's page list, below logit_slots) when logits is not null
+  int32_t bounded;
+  int32_t num_sink;
+  float* logits;
+  int64_t logit_slots;
   int* status;
   uint64_t wait_ns;       // limit of the kernels' bounded waits (nanoseconds)
   int32_t test_withhold;  // test hook of pg_test_bounded_wait (0: off)
+};
+
+// Per-key statistics of one layer range: mass (accumulated attention weight) and pos (position)
+// of [layer][page][kv_head][slot], at the first layer of the call.
+struct StatsDev {
+  float* mass;
+  int32_t* pos;
+  int64_t stride_layer;  // elements
+};
+
+// Accumulation of attention weights into the statistics (see attn_mass.cu).
+struct MassArgs {
+  AttnArgs attn;      // the attention call whose weights are accumulated (lse written by it)
+  StatsDev stats;     // of the called layer
+  float* partial;     // tensor-core form: [splits][num_kv_heads][partial_slots] sums
+  int64_t partial_slots;
+  int32_t splits, chunk;  // tensor-core form: query-range splits, query tiles in each
+  int32_t max_keys;       // the most keys a request of the plan holds
+};
+
+// Choice and compaction of an eviction (see evict.cu).
+struct EvictArgs {
+  PlanDev plan;
+  PoolDev pool;           // apply: layer 0 of the range; select: geometry only
+  int64_t pool_stride_layer;
+  StatsDev stats;
+  int32_t* src;           // [num_layers][num_req][num_kv_heads][budget]
+  int32_t num_layers, budget, num_sink, num_recent;
+  int32_t max_keys;       // the plan's longest request
+  int* status;
 };
 
 // Bounded-wait settings for the next launches: the default limit, or the test hook's.
@@ -138,5 +175,12 @@ cudaError_t launch_merge_states(const __nv_bfloat16* out_a, const float* lse_a,
                                 const __nv_bfloat16* out_b, const float* lse_b,
                                 __nv_bfloat16* out, float* lse, int32_t rows, int32_t head_dim,
                                 cudaStream_t stream);
+
+// Adds the attention weights of a finished attention call to the per-key statistics.
+cudaError_t launch_mass_decode(const MassArgs& m, cudaStream_t stream);
+cudaError_t launch_mass_prefill(const MassArgs& m, int32_t head_dim, cudaStream_t stream);
+// Eviction: the source slot of every kept slot, and the moves it describes.
+cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace pg

@@ -45,6 +45,7 @@ PG_ERR_CUDA = -16
 PG_ERR_DEVICE_BOUNDS = -17
 PG_ERR_ALIGN = -18
 PG_ERR_DEVICE_TIMEOUT = -19
+PG_ERR_SHARED_PAGE = -20
 
 
 class PgError(RuntimeError):
@@ -60,6 +61,12 @@ class pg_pool_t(C.Structure):
                 ("stride_layer", C.c_int64), ("stride_page", C.c_int64), ("stride_kv", C.c_int64),
                 ("stride_head", C.c_int64), ("stride_slot", C.c_int64),
                 ("capacity", C.c_int64)]
+
+
+class pg_kv_stats_t(C.Structure):
+    _fields_ = [("mass", C.c_void_p), ("pos", C.c_void_p),
+                ("num_layers", C.c_int32), ("num_pages", C.c_int32), ("page_size", C.c_int32),
+                ("num_kv_heads", C.c_int32), ("capacity", C.c_int64)]
 
 
 class pg_plan_info_t(C.Structure):
@@ -323,7 +330,72 @@ def pg_attn_paged_decode_noalloc(plan, pool: pg_pool_t, layer, q, out, window_le
                          _ptr(q), _ptr(out), int(window_left), float(sm_scale), _stream(stream))
 
 
-EXPORTED = ["pg_plan_paged_prefill", "pg_plan_paged_prefill_ring", "pg_plan_paged_segment",
+# ---------------------------------------------------------------- bounded caches
+_attn_sink = _sig("pg_attn_paged_sink", C.c_int, _P, C.POINTER(pg_pool_t), _I32, _P, _P, _P, _I32,
+                  _I32, _F32, _P, _SZ, _P)
+_mass_wsb = _sig("pg_mass_workspace_bytes", _SZ, _P)
+_attn_mass = _sig("pg_attn_paged_mass", C.c_int, _P, C.POINTER(pg_pool_t), _I32, _P, _P, _P,
+                  C.POINTER(pg_kv_stats_t), _I32, _I32, _F32, _P, _SZ, _P)
+_evict_select = _sig("pg_kv_evict_select", C.c_int, _P, C.POINTER(pg_kv_stats_t), _I32, _I32, _I32,
+                     _I32, _I32, _P, _P)
+_evict_apply = _sig("pg_kv_evict_apply", C.c_int, _P, C.POINTER(pg_pool_t),
+                    C.POINTER(pg_kv_stats_t), _I32, _I32, _I32, _P, _P)
+
+
+def stats_descriptor(mass, pos, **override) -> pg_kv_stats_t:
+    """pg_kv_stats_t for a torch float32 (mass) and int32 (pos) tensor, each dense
+    [L, P, Hkv, ps]."""
+    if mass.shape != pos.shape or not (mass.is_contiguous() and pos.is_contiguous()):
+        raise ValueError("mass and pos must be contiguous and of one shape")
+    if str(mass.dtype) != "torch.float32" or str(pos.dtype) != "torch.int32":
+        raise ValueError("mass is float32 and pos int32")
+    L, P, Hkv, ps = mass.shape
+    d = pg_kv_stats_t(mass.data_ptr(), pos.data_ptr(), L, P, ps, Hkv, mass.numel())
+    for k, v in override.items():
+        setattr(d, k, v)
+    return d
+
+
+def pg_attn_paged_sink(plan, pool: pg_pool_t, layer, q, out, lse, window_left, num_sink, sm_scale,
+                       workspace=None, ws_bytes=0, stream=None) -> int:
+    """Windowed attention in which the first num_sink positions stay visible."""
+    return _attn_sink(plan.handle if plan is not None else None, C.byref(pool), int(layer), _ptr(q),
+                      _ptr(out), _ptr(lse), int(window_left), int(num_sink), float(sm_scale),
+                      _ptr(workspace), int(ws_bytes), _stream(stream))
+
+
+def pg_mass_workspace_bytes(plan) -> int:
+    return int(_mass_wsb(plan.handle if plan is not None else None))
+
+
+def pg_attn_paged_mass(plan, pool: pg_pool_t, layer, q, out, lse, stats: pg_kv_stats_t, window_left,
+                       num_sink, sm_scale, workspace=None, ws_bytes=0, stream=None) -> int:
+    """pg_attn_paged_sink that also accumulates every key's attention weight in stats."""
+    return _attn_mass(plan.handle if plan is not None else None, C.byref(pool), int(layer), _ptr(q),
+                      _ptr(out), _ptr(lse), C.byref(stats) if stats is not None else None,
+                      int(window_left), int(num_sink), float(sm_scale), _ptr(workspace),
+                      int(ws_bytes), _stream(stream))
+
+
+def pg_kv_evict_select(plan, stats: pg_kv_stats_t, layer, num_layers, budget, num_sink, num_recent,
+                       src, stream=None) -> int:
+    """Source slot of every kept slot into src [num_layers, num_req, num_kv_heads, budget]."""
+    return _evict_select(plan.handle if plan is not None else None,
+                         C.byref(stats) if stats is not None else None, int(layer),
+                         int(num_layers), int(budget), int(num_sink), int(num_recent), _ptr(src),
+                         _stream(stream))
+
+
+def pg_kv_evict_apply(plan, pool: pg_pool_t, stats: pg_kv_stats_t, layer, num_layers, budget, src,
+                      stream=None) -> int:
+    """Make the moves of src (pg_kv_evict_select) in the pool and the statistics."""
+    return _evict_apply(plan.handle if plan is not None else None, C.byref(pool),
+                        C.byref(stats) if stats is not None else None, int(layer), int(num_layers),
+                        int(budget), _ptr(src), _stream(stream))
+
+
+EXPORTED = ["pg_attn_paged_sink", "pg_mass_workspace_bytes", "pg_attn_paged_mass",
+            "pg_kv_evict_select", "pg_kv_evict_apply", "pg_plan_paged_prefill", "pg_plan_paged_prefill_ring", "pg_plan_paged_segment",
             "pg_attn_paged_prefill_lse", "pg_attn_paged_prefill_hd512_lse", "pg_merge_attn_states",
             "pg_plan_destroy", "pg_plan_info", "pg_rope_table",
             "pg_prep_paged_hd256", "pg_prep_paged_hd512", "pg_workspace_bytes",
