@@ -11,7 +11,7 @@
 //            2 Hkv D bf16 of its K and V rows), and one thread per key adds the group's weights;
 //   prefill  the scores are formed again with keys as MMA rows, S^T = K Q^T: a key's sum then
 //            runs along its own row, in registers, with no atomics and in one fixed order.
-#include "bounded.cuh"
+#include "mass.cuh"
 #include "pg_internal.h"
 
 #include <cuda_bf16.h>
@@ -50,69 +50,34 @@ __device__ __forceinline__ uint32_t swz(int m, int c) {
   return (uint32_t)(m * (D * 2) + ((c ^ (m & 7)) << 4));
 }
 
-// Request r's geometry, read from the plan.
-struct Req {
-  int32_t q0, len, sp, kvp0, kvp1, ks0, n;  // n: keys held, positions [ks0, ks0 + n)
-};
-__device__ __forceinline__ Req load_req(const PlanDev& pl, int32_t r, int32_t ps) {
-  Req q;
-  q.q0 = pl.qo_indptr[r];
-  q.len = pl.qo_indptr[r + 1] - q.q0;
-  q.sp = pl.start_pos[r];
-  q.kvp0 = pl.kv_page_indptr[r];
-  q.kvp1 = pl.kv_page_indptr[r + 1];
-  q.ks0 = pl.kv_start[r];
-  q.n = (q.kvp1 - q.kvp0 - 1) * ps + pl.last_page_len[r];
-  return q;
-}
-// Page holding key index rel of the request (num_pages when the metadata is out of range).
-__device__ __forceinline__ int32_t page_of(const PlanDev& pl, const Req& q, int32_t rel, int32_t ps,
-                                           int32_t num_pages) {
-  const int32_t pidx = q.kvp0 + rel / ps;
-  const int32_t p = (pidx < q.kvp1 && pidx < pl.num_page_ids) ? pl.page_ids[pidx] : num_pages;
-  return p < 0 || p >= num_pages ? num_pages : p;
-}
-// mass and position of one key: new keys are set, older ones add
-__device__ __forceinline__ void store_key(const MassArgs& m, const Req& q, int32_t page, int32_t g,
-                                          int32_t rel, float sum) {
-  const AttnArgs& a = m.attn;
-  const int32_t ps = a.pool.page_size, j = q.ks0 + rel;
-  const int64_t at = ((int64_t)page * a.pool.num_kv_heads + g) * ps + rel % ps;
-  if (j >= q.sp) {
-    m.stats.mass[at] = sum;
-    m.stats.pos[at] = j;
-  } else {
-    m.stats.mass[at] += sum;
-  }
-}
-
 // Decode: one thread per key adds the weights of its query heads from the kept scores.
 constexpr int kDecThreads = 256;
 __global__ void __launch_bounds__(kDecThreads) mass_decode_kernel(MassArgs m, int32_t blocks_per_req) {
   const AttnArgs& a = m.attn;
   extern __shared__ float s_lse[];  // the request's lse, log2 units
   const int32_t r = (int32_t)blockIdx.x / blocks_per_req;
-  const int32_t blk = (int32_t)blockIdx.x % blocks_per_req;
   const int32_t ps = a.pool.page_size, Hq = a.num_qo_heads, G = a.group;
-  const Req q = load_req(a.plan, r, ps);
-  if ((int64_t)blk * kDecThreads >= q.n) return;
+  const MassReq q = mass_req(a.plan, r, ps);
   for (int h = threadIdx.x; h < Hq; h += kDecThreads) s_lse[h] = a.lse[(int64_t)q.q0 * Hq + h] * kLog2e;
   __syncthreads();
-  const int32_t rel = blk * kDecThreads + (int32_t)threadIdx.x;
-  if (rel >= q.n) return;
-  const int32_t j = q.ks0 + rel, p = q.sp;
-  if (j > p || !(a.window_left < 0 || p - j <= a.window_left || j < a.num_sink)) return;
-  const int64_t slot = (int64_t)q.kvp0 * ps + rel;
-  const int32_t page = page_of(a.plan, q, rel, ps, a.pool.num_pages);
-  if (page == a.pool.num_pages || slot >= a.logit_slots) {
-    atomicOr(a.status, kStatusBounds);
-    return;
-  }
-  const float* s = a.logits + slot * Hq;
-  for (int32_t g = 0; g < a.pool.num_kv_heads; ++g) {
-    float sum = 0.f;
-    for (int32_t h = g * G; h < (g + 1) * G; ++h) sum += ex2(s[h] - s_lse[h]);
-    store_key(m, q, page, g, rel, sum);
+  const int32_t p = q.sp;
+  // (a graph's plan may have grown since the capture: the blocks stride over the keys)
+  for (int64_t i = (int32_t)blockIdx.x % blocks_per_req * kDecThreads + (int32_t)threadIdx.x; i < q.n;
+       i += (int64_t)blocks_per_req * kDecThreads) {
+    const int32_t rel = (int32_t)i, j = q.ks0 + rel;
+    if (j > p || !(a.window_left < 0 || p - j <= a.window_left || j < a.num_sink)) continue;
+    const int64_t slot = (int64_t)q.kvp0 * ps + rel;
+    const int32_t page = mass_page(a.plan, q, rel, ps, a.pool.num_pages);
+    if (page == a.pool.num_pages || slot >= a.logit_slots) {
+      atomicOr(a.status, kStatusBounds);
+      continue;
+    }
+    const float* s = a.logits + slot * Hq;
+    for (int32_t g = 0; g < a.pool.num_kv_heads; ++g) {
+      float sum = 0.f;
+      for (int32_t h = g * G; h < (g + 1) * G; ++h) sum += ex2(s[h] - s_lse[h]);
+      mass_store(m, q, page, g, rel, sum);
+    }
   }
 }
 
@@ -132,7 +97,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, 
   const int32_t g = (int32_t)blockIdx.x % Hkv;
   const int32_t kt = ((int32_t)blockIdx.x / Hkv) % tiles_per_req;
   const int32_t r = (int32_t)blockIdx.x / Hkv / tiles_per_req;
-  const Req q = load_req(a.plan, r, ps);
+  const MassReq q = mass_req(a.plan, r, ps);
   const int32_t rel0 = kt * kKeys;
   if (rel0 >= q.n) return;
   const int32_t k0 = q.ks0 + rel0, nk = min(kKeys, q.n - rel0);
@@ -141,7 +106,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, 
     const int k = idx / CH, c = idx % CH;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (k < nk) {
-      const int32_t page = page_of(a.plan, q, rel0 + k, ps, a.pool.num_pages);
+      const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
       if (page < a.pool.num_pages)
         v = *reinterpret_cast<const uint4*>(a.pool.layer_base + (int64_t)page * a.pool.stride_page +
                                             (int64_t)g * a.pool.stride_head +
@@ -208,8 +173,8 @@ __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, 
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     const int k = warp * 16 + gid + 8 * e;
     if (tig == 0 && k < nk) {
-      const int32_t page = page_of(a.plan, q, rel0 + k, ps, a.pool.num_pages);
-      if (page < a.pool.num_pages) store_key(m, q, page, g, rel0 + k, s);
+      const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
+      if (page < a.pool.num_pages) mass_store(m, q, page, g, rel0 + k, s);
       else atomicOr(a.status, kStatusBounds);
     }
   }
@@ -248,6 +213,8 @@ cudaError_t launch_mass_decode(const MassArgs& m, cudaStream_t stream) {
 
 cudaError_t launch_mass_prefill(const MassArgs& m, int32_t head_dim, cudaStream_t stream) {
   if (m.max_keys <= 0 || m.attn.plan.num_req == 0) return cudaSuccess;
+  if (attn_tc_supported(head_dim, m.attn.group, m.attn.pool.page_size))
+    return launch_mass_prefill_tc(m, head_dim, stream);
   return head_dim == 256 ? launch_mass_mma<256>(m, m.max_keys, stream)
                          : launch_mass_mma<512>(m, m.max_keys, stream);
 }

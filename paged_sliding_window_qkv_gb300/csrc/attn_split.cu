@@ -505,6 +505,10 @@ attn_merge_kernel(AttnArgs a) {
     // the key walk is counted in the partition kernel's tiles; a chunk is a whole number of them
     const KeyWalk walk = key_walk(W, a.num_sink, ks0, kv_len, p, p, kDecTile);
     nch = (walk.total + a.kv_chunk / kDecTile - 1) / (a.kv_chunk / kDecTile);
+    if (nch > a.max_chunks) {  // a plan that grew past the launch it was captured with
+      if (threadIdx.x == 0) atomicOr(a.status, kStatusBounds);
+      nch = a.max_chunks;
+    }
   }
   if (nch <= 1) return;  // written directly by the partition kernel
   const int64_t row = ((int64_t)r * a.num_qo_heads + h) * a.max_chunks;

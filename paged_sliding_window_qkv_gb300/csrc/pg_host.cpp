@@ -559,9 +559,22 @@ int shares_pages(const pg_plan* p, bool* out) {
   std::lock_guard<std::mutex> lk(mu);
   if (p->shared < 0) {
     try {
-      std::vector<int32_t> ids(p->host_ids);
-      std::sort(ids.begin(), ids.end());
-      p->shared = std::adjacent_find(ids.begin(), ids.end()) != ids.end() ? 1 : 0;
+      // one bit per page, or a sort where the page ids are far sparser than that
+      bool twice = false;
+      const size_t words = (size_t)(p->max_page_id + 1) / 64 + 1;
+      if (words <= p->host_ids.size() + 4096) {
+        std::vector<uint64_t> seen(words, 0);
+        for (const int32_t id : p->host_ids) {
+          const uint64_t bit = 1ull << (id & 63);
+          twice |= (seen[id >> 6] & bit) != 0;
+          seen[id >> 6] |= bit;
+        }
+      } else {
+        std::vector<int32_t> ids(p->host_ids);
+        std::sort(ids.begin(), ids.end());
+        twice = std::adjacent_find(ids.begin(), ids.end()) != ids.end();
+      }
+      p->shared = twice ? 1 : 0;
     } catch (const std::bad_alloc&) {
       return PG_ERR_ARG;
     }
@@ -611,10 +624,20 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Scores that a decode step of the plan keeps: [slots of the page list][num_qo_heads].
 int64_t logit_slots(const pg_plan* p) { return (int64_t)p->num_page_ids * p->page_size; }
 
+bool mass_on_tensor_cores(const pg_plan* p) {
+  return !p->decode && p->num_req > 0 &&
+         attn_tc_supported(p->head_dim, p->num_qo_heads / p->num_kv_heads, p->page_size);
+}
+MassSplit plan_mass_split(const pg_plan* p) {
+  return mass_split(p->num_req, p->num_kv_heads, p->num_qo_heads / p->num_kv_heads, p->num_tokens,
+                    p->max_qo_len, p->max_seen);
+}
 size_t mass_workspace_bytes(const pg_plan* p) {
   if (!p || p->num_req == 0) return 0;
   if (p->decode)
     return align256(workspace_bytes(p)) + (size_t)logit_slots(p) * p->num_qo_heads * sizeof(float);
+  if (mass_on_tensor_cores(p))  // the sums of each range of query tiles
+    return (size_t)plan_mass_split(p).splits * p->num_kv_heads * (size_t)logit_slots(p) * sizeof(float);
   return 0;
 }
 
@@ -910,12 +933,15 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
   if (!mul_i64((plan->max_seen + 63) / 64, plan->num_req, &blocks) ||
       !mul_i64(blocks, plan->num_kv_heads, &blocks) || !fits_i32(blocks))
     return PG_ERR_I32_OVERFLOW;
+  if (mass_on_tensor_cores(plan) && plan_mass_split(plan).units > INT32_MAX / 2)
+    return PG_ERR_I32_OVERFLOW;  // two blocks per unit
   Bounded b;
   b.num_sink = num_sink;
   const size_t attn_ws = align256(workspace_bytes(plan));
   if (plan->decode && plan->num_req > 0) {
     b.logits = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn_ws);
-    b.logit_slots = logit_slots(plan);
+    // as many as the workspace holds: a graph's plan may grow into a larger one
+    b.logit_slots = (int64_t)((ws_bytes - attn_ws) / ((size_t)plan->num_qo_heads * sizeof(float)));
   }
   MassArgs m{};
   rc = attn_common(plan, pool, layer, plan->head_dim, q, out, lse, window_left, sm_scale, workspace,
@@ -923,6 +949,13 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
   m.stats = stats_dev(stats, layer);
   m.max_keys = plan->max_seen;
+  if (mass_on_tensor_cores(plan)) {
+    const MassSplit sp = plan_mass_split(plan);
+    m.partial = static_cast<float*>(workspace);
+    m.partial_slots = logit_slots(plan);
+    m.splits = sp.splits;
+    m.chunk = sp.chunk;
+  }
   const cudaError_t e =
       plan->decode ? launch_mass_decode(m, s) : launch_mass_prefill(m, plan->head_dim, s);
   return e == cudaSuccess ? PG_OK : PG_ERR_CUDA;

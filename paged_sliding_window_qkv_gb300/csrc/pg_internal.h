@@ -179,6 +179,14 @@ cudaError_t launch_merge_states(const __nv_bfloat16* out_a, const float* lse_a,
 // Adds the attention weights of a finished attention call to the per-key statistics.
 cudaError_t launch_mass_decode(const MassArgs& m, cudaStream_t stream);
 cudaError_t launch_mass_prefill(const MassArgs& m, int32_t head_dim, cudaStream_t stream);
+// Tensor-core form (geometries of attn_tc_supported): query tiles per range, ranges, and units.
+struct MassSplit {
+  int32_t chunk, splits;
+  int64_t units;
+};
+MassSplit mass_split(int32_t num_req, int32_t num_kv_heads, int32_t group, int64_t num_tokens,
+                     int32_t max_qo_len, int32_t max_keys);
+cudaError_t launch_mass_prefill_tc(const MassArgs& m, int32_t head_dim, cudaStream_t stream);
 // Eviction: the source slot of every kept slot, and the moves it describes.
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream);
