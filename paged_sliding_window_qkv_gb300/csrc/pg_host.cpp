@@ -655,11 +655,12 @@ int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer,
   if (plan->num_req == 0) return PG_OK;
   if (!src) return PG_ERR_ARG;
   if ((uintptr_t)src & 3u) return PG_ERR_ALIGN;
-  // every grid of the call fits: a block covers 8 groups of 32 kept slots, or one segment
-  int64_t segs = 0, groups = 0;
-  const int64_t keep = std::min(plan->max_seen, budget);
+  // every grid of the call fits
+  int64_t segs = 0, blocks = 0;
+  const int32_t per_seg = std::max(evict_select_ranks(plan->max_seen),
+                                   evict_apply_blocks(std::min(plan->max_seen, budget)));
   if (!mul_i64(num_layers, plan->num_req, &segs) || !mul_i64(segs, plan->num_kv_heads, &segs) ||
-      !mul_i64(segs, (keep + 31) / 32, &groups) || !fits_i32(segs) || !fits_i32(groups / 8 + 1))
+      !mul_i64(segs, per_seg, &blocks) || !fits_i32(segs) || !fits_i32(blocks))
     return PG_ERR_I32_OVERFLOW;
   int err = PG_OK;
   int* st = status_word(&err);
@@ -676,6 +677,7 @@ int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer,
   a->budget = budget;
   a->num_sink = a->num_recent = 0;
   a->max_keys = plan->max_seen;
+  set_page_divisor(a);
   a->status = st;
   return PG_OK;
 }
@@ -984,7 +986,7 @@ int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_s
   if ((rc = check_plan_pool(plan, pool, layer, plan->head_dim))) return rc;
   if (stats->num_layers != pool->num_layers || stats->num_pages != pool->num_pages)
     return PG_ERR_LAYOUT;
-  if (plan->head_dim % 8 != 0) return PG_ERR_ALIGN;
+  if (plan->head_dim != 256 && plan->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
   if (plan->num_req == 0) return PG_OK;
   a.pool = pool_dev(pool, layer);
   a.pool_stride_layer = pool->stride_layer;

@@ -128,6 +128,7 @@ struct EvictArgs {
   int32_t* src;           // [num_layers][num_req][num_kv_heads][budget]
   int32_t num_layers, budget, num_sink, num_recent;
   int32_t max_keys;       // the plan's longest request
+  uint32_t page_mul, page_shift;  // division by the page size (page_mul 0: page size 1)
   int* status;
 };
 
@@ -188,6 +189,9 @@ MassSplit mass_split(int32_t num_req, int32_t num_kv_heads, int32_t group, int64
                      int32_t max_qo_len, int32_t max_keys);
 cudaError_t launch_mass_prefill_tc(const MassArgs& m, int32_t head_dim, cudaStream_t stream);
 // Eviction: the source slot of every kept slot, and the moves it describes.
+void set_page_divisor(EvictArgs* a);
+int32_t evict_select_ranks(int32_t max_keys);  // blocks of select per segment
+int32_t evict_apply_blocks(int32_t keep);      // blocks of apply per segment
 cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream);
 

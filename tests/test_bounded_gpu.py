@@ -272,7 +272,7 @@ def test_evict(D, hkv, ps, budget, sinks, recent):
     c.close()
 
 
-@pytest.mark.parametrize("n,budget", [(20000, 12345), (40000, 39999), (70000, 100), (9000, 8999)])
+@pytest.mark.parametrize("n,budget", [(20000, 12345), (40000, 39999), (70000, 100), (9000, 8999), (140000, 70000)])
 def test_evict_long(n, budget):
     c = Case(256, 1, 1, [1, 1], [n - 1, n - 700], seed=n)
     _scramble(c, n)
