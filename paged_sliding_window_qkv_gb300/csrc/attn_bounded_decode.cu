@@ -1,0 +1,1005 @@
+// Decode attention of bounded caches (sinks, window, optionally the weights of every key) on the
+// tensor cores (tcgen05 + TMEM + TMA). Page sizes 8, 16, 32, ..., groups up to 16.
+//
+// A decode step reads every visible K and V row once and computes little with it, so the kernel
+// is built to keep copies in flight and nothing else: the products are transposed so that keys and
+// output columns are the 128 MMA rows and the group's query rows the 16 columns,
+//   S^T = K Q^T   (M = 128 keys, N = 16, K = 16 d a step; A = K as it lands, K-major)
+//   O^T = V^T P^T (M = 128 output columns, N = 16, K = 16 keys a step; A = V as it lands, MN-major)
+// and a tile of 128 keys costs the tensor core about an eighth of the time its bytes take from
+// HBM; the CUDA cores see 16 scores per key. O^T stays in TMEM for the segment.
+//
+// Work: a (request, KV head) segment's visible keys lie in boxes of 16 keys (8 at page size 8),
+// sinks first, then the window (bounded.cuh); a tile is the next 128 rows of boxes, whatever
+// positions they hold, so a few sinks cost one box and not a tile of their own (with tiles of
+// consecutive keys 4 sinks beside a window of 1024 cost 10% of the call: a near-empty tile holds
+// its ring slots as long as a full one). CTA s of S takes tiles [s U / S, (s + 1) U / S). A segment
+// cut between CTAs leaves fp32 records (O / l, m, l) that the join kernel combines.
+//
+//   warp 0    producer: 32 KB slots (128 keys x 128 d of K or V, one 4-D box per page and slot, all
+//             landing as [8 keys][64-d chunk][8 rows][128 B]), in the order K0 K1 V0 K2 V1 ...; the
+//             group's query rows per segment; a header per tile (visible keys as bits, flags)
+//   warp 1    MMA issuer: QK of tile i + 1 before PV of tile i, so a tile's softmax has a tile's
+//             load time to finish
+//   warps 2-5 softmax: a thread is a key (TMEM lane); 16 scores, exponentials against a per-row
+//             reference with 2^64 headroom that moves only when a score outgrows it by 2^48 (so no
+//             maximum is taken across keys in the common tile), P to shared memory; V rows of keys
+//             that are not visible are zeroed (whatever they held); a segment's output leaves one
+//             tile late, when its last PV is done anyway.
+//
+// Weights: the scores of visible keys go to the workspace (64 contiguous bytes a key at 16 heads),
+// and the join kernel, which has the normalisers, adds each key's weights to its statistics in
+// the same launch that combines the records.
+//
+// Every wait is bounded (a wait that runs out sets the device status word and the CTA leaves); the
+// softmax warps agree on giving up before any barrier among themselves.
+#include "bounded.cuh"
+#include "mass.cuh"
+#include "pg_internal.h"
+#include "tc_ptx.cuh"
+
+#include <math.h>
+
+#include <algorithm>
+
+namespace pg {
+namespace {
+
+constexpr int kT = 128;               // keys per tile
+constexpr int kSlot = kT * 256;       // 128 keys x 128 d
+constexpr int kN = 16;                // MMA columns: query rows of the group, padded
+constexpr int kThreadsDec = 192;
+constexpr int kMaxCtas = 256;         // records are sized for at most this many CTAs
+constexpr int kHdrs = 4;
+constexpr float kRescale = 48.f, kHeadroom = 64.f;  // see attn_tc.cu
+constexpr float kLn2f = 0.69314718055994531f, kLog2ef = 1.4426950408889634f;
+
+constexpr int kFirst = 1, kLast = 2, kSplit = 4, kEnd = 8, kEmpty = 16, kRec1 = 32;
+
+struct alignas(16) TileHdr {
+  uint32_t vis[4];  // visible keys
+  int32_t rel[16];  // key index (from the request's first key) of each box's first row
+  int32_t flags, r, g, tok;
+  int64_t slot0;    // slot of the request's first key, counted through the batch's page list
+};
+
+template <int D>
+struct BdCfg {
+  static constexpr int PARTS = D / 128;            // slots per tile of K, and of V
+  static constexpr int NSLOT = D == 256 ? 6 : 5;
+  static constexpr int Q_BYTES = (D / 64) * kN * 128;  // [64-d chunk][16 rows][128 B]
+  static constexpr int P_BYTES = 2 * kN * 128;         // [64-key chunk][16 rows][128 B]
+  static constexpr int OFF_Q = NSLOT * kSlot;
+  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_HDR = OFF_P + 2 * P_BYTES;
+  static constexpr int OFF_RED = OFF_HDR + kHdrs * (int)sizeof(TileHdr);  // [4 warps][16]
+  static constexpr int OFF_FIN = OFF_RED + 4 * kN * 4;                    // [16] (l, reference)
+  static constexpr int OFF_BAR = OFF_FIN + kN * 8;
+  // FULL, EMPTY; QFULL[2], QEMPTY[2], HFULL[4], HEMPTY[4], SFULL[2], SFREE[2], PFULL[2], PVDONE[2],
+  // OFREE[2], DRAIN
+  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1;
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+  static constexpr uint32_t TM_O = 0, O_COLS = PARTS * kN, TM_S = 2 * O_COLS;
+  static constexpr uint32_t TM_COLS = TM_S + 2 * kN <= 128 ? 128 : 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct BdArgs {
+  AttnArgs a;
+  float* rec_o;     // [S][2][G][D]
+  float* rec_ml;    // [S][2][G][2]
+  int64_t* prefix;  // [R + 1] tiles before request r (all heads)
+  int32_t box_rows;
+  int32_t box_lg, page_lg;  // log2 of box_rows and of the page size (both powers of two)
+};
+
+// ------------------------------------------------------------------ PTX (one CTA)
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* tm, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tm), "r"(0), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+template <uint32_t IDESC>
+__device__ __forceinline__ void mma1(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, p;\n .reg .u32 ln;\n mov.u32 ln, %%laneid;\n setp.eq.u32 e, ln, 0;\n setp.ne.b32 p, %3, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(acc), "n"(IDESC)
+      : "memory");
+}
+__device__ __forceinline__ void commit1(uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .u32 ln;\n mov.u32 ln, %%laneid;\n setp.eq.u32 e, ln, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : PG_R8(0), PG_R8(8)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      PG_W8(0), PG_W8(8)
+      : "memory");
+}
+// barriers among the 128 softmax threads
+__device__ __forceinline__ bool any4(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync4() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+// maximum over the warp
+__device__ __forceinline__ float warp_max(float x) {
+  const int32_t b = __float_as_int(x);
+  const int32_t m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7FFFFFFF));
+  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+}
+
+// The boxes of request r that its query sees, and the tiles they fill (one KV head).
+struct ReqTiles {
+  KeyWalk w;      // in boxes
+  int32_t total;  // tiles
+  int32_t tok, kvp0, kvp1, kv_len, ks0, sink;
+  __device__ __forceinline__ bool sees(int32_t key) const {
+    return key < w.hi && (key >= w.lo || key < sink);
+  }
+};
+__device__ __forceinline__ ReqTiles req_tiles(const BdArgs& args, int32_t r) {
+  const AttnArgs& a = args.a;
+  const int4 e0 = __ldg(reinterpret_cast<const int4*>(a.plan.pair_tab) + 2 * r);
+  const int4 e1 = __ldg(reinterpret_cast<const int4*>(a.plan.pair_tab) + 2 * r + 1);
+  ReqTiles t;
+  t.tok = e0.y;
+  t.kvp0 = e1.x;
+  t.kvp1 = e1.y;
+  t.kv_len = e1.z;
+  t.ks0 = e1.w;
+  t.sink = a.window_left >= 0 ? a.num_sink : 0;
+  t.w = key_walk(a.window_left, a.num_sink, t.ks0, t.kv_len, e0.w, e0.w, args.box_rows);
+  const int32_t nbox = kT >> args.box_lg;
+  t.total = (t.w.total + nbox - 1) / nbox;
+  return t;
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreadsDec, 1)
+bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                      BdArgs args) {
+  using C = BdCfg<D>;
+  constexpr int NS = C::NSLOT, PARTS = C::PARTS;
+  const AttnArgs& a = args.a;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* gb = smem_raw + (base - raw);
+  const uint32_t bars = base + C::OFF_BAR;
+  auto FULL = [&](int s) { return bars + 8u * s; };
+  auto EMPTY = [&](int s) { return bars + 8u * (NS + s); };
+  const uint32_t QFULL = bars + 8u * (2 * NS), QEMPTY = QFULL + 16, HFULL = QFULL + 32, HEMPTY = HFULL + 32,
+                 SFULL = HEMPTY + 32, SFREE = SFULL + 16, PFULL = SFULL + 32, PVDONE = SFULL + 48,
+                 OFREE = SFULL + 64, DRAIN = SFULL + 80;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::OFF_BAR + C::NBAR * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const WaitCtx wc{abort_flag, a.status, a.wait_ns};
+  TileHdr* const hdrs = reinterpret_cast<TileHdr*>(gb + C::OFF_HDR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t G = a.group, Hq = a.num_qo_heads, Hkv = a.pool.num_kv_heads, ps = a.pool.page_size;
+
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(QFULL + 8 * b, 1);
+      mbar_init(QEMPTY + 8 * b, 1);
+      mbar_init(SFULL + 8 * b, 1);
+      mbar_init(SFREE + 8 * b, 4);
+      mbar_init(PFULL + 8 * b, 4);
+      mbar_init(PVDONE + 8 * b, 1);
+      mbar_init(OFREE + 8 * b, 4);
+    }
+    for (int h = 0; h < kHdrs; ++h) {
+      mbar_init(HFULL + 8 * h, 1);
+      mbar_init(HEMPTY + 8 * h, 5);  // the softmax warps and the MMA issuer
+    }
+    mbar_init(DRAIN, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // query and weight rows past the group stay zero
+  if (warp >= 2) {
+    for (int i = threadIdx.x - 64; i < (2 * C::Q_BYTES + 2 * C::P_BYTES) / 16; i += kThreadsDec - 64)
+      *reinterpret_cast<uint4*>(gb + C::OFF_Q + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
+  }
+  // (the producer finds its tiles while the others set up)
+  int32_t n = 0, r = 0;
+  int64_t in_req = 0;
+  if (warp == 0) {
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_kv) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_q) : "memory");
+    }
+    const int32_t R = a.plan.num_req;
+    const int64_t S = gridDim.x, s = blockIdx.x;
+    // Tiles of every request (all heads) in scans of 32 requests: the total, (CTA 0) the prefix for
+    // the join, and the request that holds the CTA's first tile. The first scans' counts are
+    // loaded together and kept.
+    constexpr int kHeld = 4;
+    auto tiles_of = [&](int32_t r) -> int64_t { return r < R ? (int64_t)req_tiles(args, r).total * Hkv : 0; };
+    auto scan = [&](int64_t v) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      return v;
+    };
+    int64_t held[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) held[j] = tiles_of(32 * j + lane);
+    int64_t U = 0;
+    for (int32_t c = 0; c < R; c += 32) {
+      const int j = c / 32;
+      const int64_t v = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : j == 3 ? held[3] : tiles_of(c + lane);
+      const int64_t incl = scan(v);
+      if (s == 0 && c + lane < R) args.prefix[c + lane] = U + incl - v;
+      U += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (s == 0 && lane == 0) args.prefix[R] = U;
+    const int64_t u0 = s * U / S, u1 = (s + 1) * U / S;
+    n = (int32_t)(u1 - u0);
+    if (n > 0) {
+      int64_t run = 0;
+      for (int32_t c = 0; c < R; c += 32) {
+        const int j = c / 32;
+        const int64_t v = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : j == 3 ? held[3] : tiles_of(c + lane);
+        const int64_t incl = scan(v);
+        const uint32_t past = __ballot_sync(0xffffffffu, run + incl > u0);
+        if (past) {
+          const int f = __ffs(past) - 1;
+          r = c + f;
+          in_req = u0 - run - __shfl_sync(0xffffffffu, incl - v, f);
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                 "r"(C::TM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    bool ok = true;
+    if (n == 0) {
+      if (lane == 0) {
+        hdrs[0].flags = kEmpty | kEnd;
+        mbar_arrive(HFULL);
+      }
+    } else {
+      const int br = args.box_rows, nbox = kT / br;
+      // the tile that the iterator stands on
+      ReqTiles q = req_tiles(args, r);
+      int32_t g = (int32_t)(in_req / q.total), j = (int32_t)(in_req % q.total);
+      int32_t nseg = 0;
+      struct Tile {
+        int32_t flags, r, g;
+        int32_t rel, page, off;  // this lane's box: key index of its first row, page, row in the page
+        bool live;               // the lane has a box
+        ReqTiles q;
+      };
+      // describes tile i and steps on; the lane's page id is loaded here and used a tile later
+      int32_t seg_split = 0;
+      auto next = [&](int32_t i) {
+        Tile t;
+        if (i == 0 || j == 0) {
+          const int32_t rest = q.total - j;
+          seg_split = (j != 0 || rest > n - i) ? kSplit : 0;
+          seg_split |= nseg > 0 ? kRec1 : 0;
+          ++nseg;
+          t.flags = kFirst;
+        } else {
+          t.flags = 0;
+        }
+        t.flags |= seg_split | (j == q.total - 1 || i == n - 1 ? kLast : 0) | (i == n - 1 ? kEnd : 0);
+        t.r = r;
+        t.g = g;
+        t.q = q;
+        const int32_t v = j * nbox + lane;
+        t.live = lane < nbox && v < q.w.total;
+        t.rel = t.live ? q.w.tile(v) << args.box_lg : 0;
+        t.page = -1;
+        t.off = t.rel & (ps - 1);
+        if (t.live) {
+          const int32_t pidx = q.kvp0 + (t.rel >> args.page_lg);
+          t.page = (pidx < q.kvp1 && pidx < a.plan.num_page_ids) ? a.plan.page_ids[pidx] : -1;
+        }
+        if (++j == q.total && i + 1 < n) {
+          j = 0;
+          if (++g == Hkv) {
+            g = 0;
+            do q = req_tiles(args, ++r);
+            while (q.total == 0);
+          }
+        }
+        return t;
+      };
+      int32_t slot = 0, round = 0;
+      auto load = [&](const Tile& t, bool good, int kv) {
+        // one K (kv 0) or V slot after the other
+        const uint32_t mask = __ballot_sync(0xffffffffu, good);
+        const int32_t row = (int32_t)((((int64_t)t.page * 2 + kv) * Hkv + t.g) * ps + t.off);
+        for (int p = 0; ok && p < PARTS; ++p) {
+          int go = 1;
+          if (lane == 0) {
+            go = mbar_wait_inline(EMPTY(slot), (round & 1) ^ 1, wc) ? 1 : 0;
+            if (go) mbar_expect_tx(FULL(slot), (uint32_t)__popc(mask) * br * 256u);
+          }
+          if (!__shfl_sync(0xffffffffu, go, 0)) {
+            ok = false;
+            break;
+          }
+          if (good) tma_4d(base + slot * kSlot + lane * br * 256, &tm_kv, 2 * p, row / 8, FULL(slot));
+          __syncwarp();
+          if (++slot == NS) { slot = 0; ++round; }
+        }
+      };
+      Tile cur = next(0), prev = cur;
+      bool prev_good = false;
+      int32_t segs = 0;
+      for (int32_t i = 0; ok && i <= n; ++i) {
+        bool good = false;
+        if (i < n) {
+          const bool first = cur.flags & kFirst;
+          int go = 1;
+          if (lane == 0) {
+            if (first) {
+              const int qb = segs & 1;
+              go = mbar_wait_inline(QEMPTY + 8 * qb, ((segs >> 1) & 1) ^ 1, wc) ? 1 : 0;
+              if (go) {
+                mbar_expect_tx(QFULL + 8 * qb, (uint32_t)(G * D * 2));
+                for (int c = 0; c < D / 64; ++c)
+                  tma_3d(base + C::OFF_Q + qb * C::Q_BYTES + c * (kN * 128), &tm_q, c * 64, cur.g * G,
+                         cur.q.tok, QFULL + 8 * qb);
+              }
+            }
+            if (go) go = mbar_wait_inline(HEMPTY + 8 * (i % kHdrs), ((i / kHdrs) & 1) ^ 1, wc) ? 1 : 0;
+          }
+          if (!__shfl_sync(0xffffffffu, go, 0)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();  // (lane 0's wait orders every lane's header writes)
+          if (first) ++segs;
+          good = cur.live && cur.page >= 0 && cur.page < a.pool.num_pages;
+          const uint32_t boxes = __ballot_sync(0xffffffffu, good);
+          if (__any_sync(0xffffffffu, cur.live && !good) && lane == 0) atomicOr(a.status, kStatusBounds);
+          uint32_t vis[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int k = 32 * w + lane, box = k >> args.box_lg;
+            const int32_t key = cur.q.ks0 + __shfl_sync(0xffffffffu, cur.rel, box) + (k & (br - 1));
+            vis[w] = __ballot_sync(0xffffffffu, ((boxes >> box) & 1u) && cur.q.sees(key));
+          }
+          TileHdr& h = hdrs[i % kHdrs];
+          if (lane < nbox) h.rel[lane] = cur.rel;
+          if (lane == 0) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) h.vis[w] = vis[w];
+            h.flags = cur.flags;
+            h.r = cur.r;
+            h.g = cur.g;
+            h.tok = cur.q.tok;
+            h.slot0 = (int64_t)cur.q.kvp0 * ps;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(HFULL + 8 * (i % kHdrs));
+          load(cur, good, 0);
+        }
+        // the next tile's page ids load behind this tile's K and the previous tile's V
+        Tile ahead = cur;
+        if (i + 1 < n) ahead = next(i + 1);
+        if (ok && i > 0) load(prev, prev_good, 1);
+        prev = cur;
+        prev_good = good;
+        cur = ahead;
+      }
+    }
+    if (!ok) {
+      const uint64_t t0 = globaltimer();  // the copies already issued land before the CTA leaves
+      while (globaltimer() - t0 < 100000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t IDESC_QK = idesc_bf16(kT, kN, false);
+    constexpr uint32_t IDESC_PV = idesc_bf16(kT, kN, false) | (1u << 15);  // A (V) is MN-major
+    auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
+      const bool w = lane == 0 ? mbar_wait_inline(bar, parity, wc) : false;
+      return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+    };
+    int slot = 0, round = 0;
+    auto step = [&]() {
+      if (++slot == NS) { slot = 0; ++round; }
+    };
+    int32_t segs = 0, flags = 0, pflags = 0, pseg = 0;
+    bool end = false;
+    for (int32_t i = 0;; ++i) {
+      bool ok = true;
+      pflags = flags;
+      pseg = segs - 1;  // the segment of tile i - 1
+      if (!end) {
+        ok = wait1(HFULL + 8 * (i % kHdrs), (i / kHdrs) & 1);
+        if (!ok) break;
+        flags = hdrs[i % kHdrs].flags;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(HEMPTY + 8 * (i % kHdrs));
+        if (flags & kEmpty) break;
+        if (flags & kFirst) {
+          ok = wait1(QFULL + 8 * (segs & 1), (segs >> 1) & 1);
+          ++segs;
+        }
+        const int sb = i & 1;
+        ok = ok && wait1(SFREE + 8 * sb, ((i >> 1) & 1) ^ 1);
+        const uint32_t qb = base + C::OFF_Q + ((segs - 1) & 1) * C::Q_BYTES;
+        for (int p = 0; ok && p < PARTS; ++p) {
+          ok = wait1(FULL(slot), round & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = sdesc(base + slot * kSlot, 16, 2048);
+          const uint64_t qd = sdesc(qb + p * 2 * (kN * 128), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma1<IDESC_QK>(tmem + C::TM_S + sb * kN, kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4),
+                           qd + (uint64_t)(((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4),
+                           (p > 0 || kk > 0) ? 1u : 0u);
+          commit1(EMPTY(slot));
+          step();
+        }
+        if (!ok) break;
+        commit1(SFULL + 8 * sb);
+        if (flags & kLast) commit1(QEMPTY + 8 * ((segs - 1) & 1));
+      }
+      if (i > 0) {
+        const int32_t jt = i - 1;
+        const int pb = jt & 1, ob = pseg & 1;
+        ok = wait1(PFULL + 8 * pb, (jt >> 1) & 1);
+        if (ok && (pflags & kFirst)) ok = wait1(OFREE + 8 * ob, ((pseg >> 1) & 1) ^ 1);
+        for (int p = 0; ok && p < PARTS; ++p) {
+          ok = wait1(FULL(slot), round & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = sdesc(base + slot * kSlot, 1024, 2048);
+          const uint64_t pd = sdesc(base + C::OFF_P + pb * C::P_BYTES, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < kT / 16; ++kk)
+            mma1<IDESC_PV>(tmem + C::TM_O + ob * C::O_COLS + p * kN, vd + (uint64_t)((kk * 4096) >> 4),
+                           pd + (uint64_t)(((kk >> 2) * (kN * 128) + (kk & 3) * 32) >> 4),
+                           ((pflags & kFirst) && kk == 0) ? 0u : 1u);
+          commit1(EMPTY(slot));
+          step();
+        }
+        if (!ok) break;
+        commit1(PVDONE + 8 * pb);
+            }
+      if (end) break;
+      end = flags & kEnd;
+    }
+    commit1(DRAIN);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;  // the thread's key of each tile, and output column of 128
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    float* const red = reinterpret_cast<float*>(gb + C::OFF_RED);
+    float2* const fin = reinterpret_cast<float2*>(gb + C::OFF_FIN);
+    float l[NQ], ref[NQ];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
+    bool ok = true;
+    int32_t segs = 0;
+    // the segment whose output is still to leave
+    bool pending = false;
+    int32_t p_tile = 0, p_flags = 0, p_g = 0, p_tok = 0, p_seg = 0;
+    auto epilogue = [&]() {
+      if (!__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (p_tile & 1), (p_tile >> 1) & 1, wc))) {
+        ok = false;
+        return;
+      }
+      tc_fence_after();
+      const int64_t row0 = (int64_t)p_tok * Hq + (int64_t)p_g * G;
+      const int64_t rec = ((int64_t)blockIdx.x * 2 + ((p_flags & kRec1) ? 1 : 0)) * G;
+      float inv[NQ];
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) inv[x] = fin[x].x == 0.f ? 0.f : 1.f / fin[x].x;
+#pragma unroll 1
+      for (int p = 0; p < PARTS; ++p) {
+        uint32_t o[kN];
+        tmem_ld16(tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * kN, o);
+        tmem_wait_ld();
+        const int d = p * 128 + row;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+          if (x >= G) break;
+          const float v = inv[x] == 0.f ? 0.f : __uint_as_float(o[x]) * inv[x];
+          if (p_flags & kSplit) args.rec_o[(rec + x) * D + d] = v;
+          else a.out[(row0 + x) * D + d] = __float2bfloat16_rn(v);
+        }
+      }
+      if (row < G) {
+        const float2 f = fin[row];
+        if (p_flags & kSplit) *reinterpret_cast<float2*>(args.rec_ml + (rec + row) * 2) = make_float2(f.y, f.x);
+        else if (a.lse) a.lse[row0 + row] = f.x != 0.f ? (f.y + log2f(f.x)) * kLn2f : -INFINITY;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(OFREE + 8 * (p_seg & 1));
+    };
+    for (int32_t i = 0;; ++i) {
+      const int b = i & 1, hb = i % kHdrs;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(HFULL + 8 * hb, (i / kHdrs) & 1, wc));
+      struct { int32_t flags, g, tok; int64_t slot; uint32_t mine, all; } h{};
+      if (ok) {
+        const TileHdr& x = hdrs[hb];
+        h.flags = x.flags;
+        h.g = x.g;
+        h.tok = x.tok;
+        h.slot = x.slot0 + x.rel[row >> args.box_lg] + (row & (args.box_rows - 1));
+        h.mine = x.vis[quarter];
+        h.all = x.vis[0] & x.vis[1] & x.vis[2] & x.vis[3];
+      }
+      if (any4(!ok)) break;  // all four warps leave together
+      if (h.flags & kEmpty) break;
+      ok = __all_sync(0xffffffffu, mbar_wait_inline(SFULL + 8 * b, (i >> 1) & 1, wc));
+      if (h.flags & kFirst) {
+        ++segs;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
+      }
+      const bool vis = (h.mine >> lane) & 1u;
+      uint32_t sv[kN];
+      tc_fence_after();
+      tmem_ld16(tl + C::TM_S + b * kN, sv);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(SFREE + 8 * b);
+        mbar_arrive(HEMPTY + 8 * hb);
+      }
+      float t[NQ];
+      bool over = false;
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+        t[x] = vis ? __uint_as_float(sv[x]) * a.sm_scale_log2 : -INFINITY;
+        over |= t[x] > ref[x] + kRescale;
+      }
+      if (a.logits && vis) {
+        if (h.slot < a.logit_slots) {
+          float* dst = a.logits + h.slot * Hq + h.g * G;
+          if (NQ % 4 == 0 && G == NQ) {
+#pragma unroll
+            for (int x = 0; x + 3 < NQ; x += 4)
+              *reinterpret_cast<float4*>(dst + x) = make_float4(t[x], t[x + 1], t[x + 2], t[x + 3]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+              if (x < G) dst[x] = t[x];
+          }
+        } else {
+          atomicOr(a.status, kStatusBounds);
+        }
+      }
+      if (any4(over)) {
+        // the rows' maximum over the tile, then references with headroom where it outgrew them
+        float mine = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+          const float m = warp_max(t[x]);
+          if (lane == x) mine = m;
+        }
+        if (lane < NQ) red[quarter * kN + lane] = mine;
+        sync4();
+        float al[NQ];
+        bool scaled = false;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+          const float m = fmaxf(fmaxf(red[x], red[kN + x]), fmaxf(red[2 * kN + x], red[3 * kN + x]));
+          al[x] = 1.f;
+          if (m > ref[x] + kRescale) {
+            const float r2 = m + kHeadroom;
+            if (ref[x] != -INFINITY) {
+              al[x] = ex2(ref[x] - r2);
+              l[x] *= al[x];
+              scaled = true;
+            }
+            ref[x] = r2;
+          }
+        }
+        // O holds the segment's earlier tiles at the old references (uniform over the threads)
+        if (scaled && !(h.flags & kFirst)) {
+          const int32_t jt = i - 1;
+          if (__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jt & 1), (jt >> 1) & 1, wc))) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int p = 0; p < PARTS; ++p) {
+              uint32_t o[kN];
+              const uint32_t at = tl + C::TM_O + ((segs - 1) & 1) * C::O_COLS + p * kN;
+              tmem_ld16(at, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < NQ; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * al[x]);
+              tmem_st16(at, o);
+            }
+            tmem_wait_st();
+          } else {
+            ok = false;
+          }
+        }
+        sync4();  // red has been read
+      }
+      // the P buffer is free once PV(i - 2) has read it
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(PVDONE + 8 * b, ((i >> 1) & 1) ^ 1, wc));
+      unsigned char* const pp = gb + C::OFF_P + b * C::P_BYTES + (row >> 6) * (kN * 128) + (row & 7) * 2;
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) {
+        const float e = ex2(t[x] - (ref[x] == -INFINITY ? 0.f : ref[x]));
+        l[x] += e;
+        *reinterpret_cast<__nv_bfloat16*>(pp + x * 128 + ((((row >> 3) & 7) ^ (x & 7)) << 4)) =
+            __float2bfloat16_rn(e);
+      }
+      if (h.all != 0xFFFFFFFFu) {
+        // V rows of keys that are not visible: zero once the copies have landed. The tile's V slots
+        // follow K(i + 1) in the ring (K(0), K(1), V(0), ...; the last tile's follow V(i - 1))
+        const int32_t before = PARTS * ((h.flags & kEnd) ? 2 * i + 1 : 2 * i + 2);
+#pragma unroll 1
+        for (int p = 0; p < PARTS; ++p) {
+          const int32_t at = before + p, sl = at % NS;
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(FULL(sl), (at / NS) & 1, wc));
+          if (ok && !vis) {
+            unsigned char* v = gb + sl * kSlot + (row >> 3) * 2048 + (row & 7) * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(v + 1024 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+      }
+      fence_proxy_async();  // the MMA reads P (and cleared V rows) through the async proxy
+      tc_fence_before();    // and O after any rescaling above
+      __syncwarp();
+      if (lane == 0) mbar_arrive(PFULL + 8 * b);
+      if (pending && ok) epilogue();
+      pending = false;
+      if (h.flags & kLast) {
+        // the row sums over the 128 keys of every tile, and the references, for the epilogue
+        float mine = 0.f;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+          float s = l[x];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane == x) mine = s;
+        }
+        if (lane < NQ) red[quarter * kN + lane] = mine;
+        sync4();
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+          if (row == x) fin[x] = make_float2((red[x] + red[kN + x]) + (red[2 * kN + x] + red[3 * kN + x]), ref[x]);
+        sync4();
+        pending = true;
+        p_tile = i;
+        p_flags = h.flags;
+        p_g = h.g;
+        p_tok = h.tok;
+        p_seg = segs - 1;
+      }
+      if (h.flags & kEnd) break;
+    }
+    if (pending && ok) epilogue();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(DRAIN, 0)) {
+        if (globaltimer() - t0 > a.wait_ns) {
+          atomicOr(a.status, kStatusTimeout);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TM_COLS) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ join
+// Where the records of a segment are: CTAs sa .. sb, the record slot of sa. (64-bit divisions only
+// where the products need them: S is at most 256.)
+struct SegRecs {
+  int32_t sa, sb, slot_a;
+  bool sparse;  // fewer tiles than CTAs: some of the CTAs hold none
+};
+__device__ __forceinline__ SegRecs seg_recs(int64_t first, int64_t tiles, int64_t U, int32_t S) {
+  SegRecs s;
+  if (U < (1 << 23)) {
+    const uint32_t u = (uint32_t)U, f = (uint32_t)first, t = (uint32_t)tiles;
+    s.sa = (int32_t)(((f + 1) * S - 1) / u);
+    s.sb = (int32_t)(((f + t) * S - 1) / u);
+    s.slot_a = (uint32_t)s.sa * u / (uint32_t)S < f ? 1 : 0;
+  } else {
+    s.sa = (int32_t)(((first + 1) * S - 1) / U);
+    s.sb = (int32_t)(((first + tiles) * S - 1) / U);
+    s.slot_a = (int64_t)s.sa * U / S < first ? 1 : 0;
+  }
+  s.sparse = U < S;
+  return s;
+}
+__device__ __forceinline__ bool holds_tiles(const SegRecs& s, int32_t c, int64_t U, int32_t S) {
+  if (!s.sparse) return true;
+  const uint32_t u = (uint32_t)U;
+  return (uint32_t)c * u / (uint32_t)S < (uint32_t)(c + 1) * u / (uint32_t)S;
+}
+
+// Blocks [0, R Hkv G D / 512): 512 columns of one segment's records into its output (segments
+// inside one CTA were written directly; a segment without keys gets zeros), four columns a thread
+// and eight records in flight, so a segment cut into many waits for memory once per eight.
+// Blocks from there on (weights): 128 keys of one request, a thread per key, all heads; the
+// normalisers come from the records, or from lse where the segment was written directly.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRecs = 8;
+__host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D) {
+  return (group * D + 511) / 512;
+}
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) bounded_join_kernel(BdArgs args, int32_t S,
+                                                                    int32_t key_blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const AttnArgs& a = args.a;
+  const int32_t Hkv = a.pool.num_kv_heads, G = a.group, Hq = a.num_qo_heads, R = a.plan.num_req;
+  const int64_t U = args.prefix[R];
+  const int tid = threadIdx.x;
+  const int32_t parts = join_parts(G, D), merges = R * Hkv * parts;
+  if ((int32_t)blockIdx.x < merges) {
+    const int32_t seg = (int32_t)blockIdx.x / parts, r = seg / Hkv, g = seg % Hkv;
+    const int32_t idx = ((int32_t)blockIdx.x % parts) * kJoinThreads + tid;  // four columns of a row
+    const int32_t row = idx / (D / 4), c4 = idx % (D / 4);
+    const int64_t pre = args.prefix[r];
+    const ReqTiles q = req_tiles(args, r);
+    const int64_t row0 = (int64_t)q.tok * Hq + (int64_t)g * G;
+    if (row >= G) return;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (row0 + row) * D + 4 * c4);
+    if (q.total == 0) {
+      dst[0] = dst[1] = 0u;
+      if (a.lse && c4 == 0) a.lse[row0 + row] = -INFINITY;
+      return;
+    }
+    const SegRecs s = seg_recs(pre + (int64_t)g * q.total, q.total, U, S);
+    if (s.sa == s.sb) return;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int32_t c0 = s.sa; c0 <= s.sb; c0 += kJoinRecs) {
+      float2 ml[kJoinRecs];
+      float4 v[kJoinRecs];
+#pragma unroll
+      for (int k = 0; k < kJoinRecs; ++k) {
+        const int32_t c = c0 + k;
+        const bool in = c <= s.sb && holds_tiles(s, c, U, S);
+        const int64_t rb = ((int64_t)c * 2 + (c == s.sa ? s.slot_a : 0)) * G + row;
+        ml[k] = in ? *reinterpret_cast<const float2*>(args.rec_ml + rb * 2) : make_float2(-INFINITY, 0.f);
+        v[k] = in ? *reinterpret_cast<const float4*>(args.rec_o + rb * D + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kJoinRecs; ++k) {
+        if (ml[k].y == 0.f) continue;  // saw no key (a NaN sum stays)
+        const float mn = fmaxf(M, ml[k].x);
+        const float so = exp2f(M - mn), w = ml[k].y * exp2f(ml[k].x - mn);
+        acc.x = acc.x * so + w * v[k].x; acc.y = acc.y * so + w * v[k].y;
+        acc.z = acc.z * so + w * v[k].z; acc.w = acc.w * so + w * v[k].w;
+        den = den * so + w;
+        M = mn;
+      }
+    }
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    dst[0] = pack_bf16(acc.x * inv, acc.y * inv);
+    dst[1] = pack_bf16(acc.z * inv, acc.w * inv);
+    if (a.lse && c4 == 0) a.lse[row0 + row] = den != 0.f ? (M + log2f(den)) * kLn2f : -INFINITY;
+    return;
+  }
+  // ---- weights
+  extern __shared__ float s_lse[];  // the request's normalisers, log2 units
+  const int32_t ps = a.pool.page_size;
+  const int32_t r = ((int32_t)blockIdx.x - merges) / key_blocks, kb = ((int32_t)blockIdx.x - merges) % key_blocks;
+  const MassReq q = mass_req(a.plan, r, ps);
+  if (kb * kJoinThreads >= q.n) return;
+  const ReqTiles t = req_tiles(args, r);
+  if (t.total == 0) return;
+  const int64_t pre = args.prefix[r];
+  // a warp per head, a lane per record
+  const int lane = tid & 31;
+#pragma unroll 4
+  for (int h = tid >> 5; h < Hq; h += kJoinThreads / 32) {
+    const SegRecs s = seg_recs(pre + (int64_t)(h / G) * t.total, t.total, U, S);
+    float v;
+    if (s.sa == s.sb) {
+      v = a.lse[(int64_t)q.q0 * Hq + h] * kLog2ef;
+    } else {
+      float M = -INFINITY, den = 0.f;
+      for (int32_t c = s.sa + lane; c <= s.sb; c += 32) {
+        const int64_t rb = ((int64_t)c * 2 + (c == s.sa ? s.slot_a : 0)) * G + h % G;
+        const float2 ml = holds_tiles(s, c, U, S) ? *reinterpret_cast<const float2*>(args.rec_ml + rb * 2)
+                                                  : make_float2(-INFINITY, 0.f);
+        if (ml.y != 0.f) {
+          const float mn = fmaxf(M, ml.x);
+          den = den * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
+          M = mn;
+        }
+      }
+      const float mx = warp_max(M);
+      float d = den != 0.f ? den * exp2f(M - mx) : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      v = mx + log2f(d);
+    }
+    if (lane == 0) s_lse[h] = v;
+  }
+  __syncthreads();
+  // (a graph's plan may have grown since the capture: the blocks stride over the keys)
+  for (int64_t i = (int64_t)kb * kJoinThreads + tid; i < q.n; i += (int64_t)key_blocks * kJoinThreads) {
+    const int32_t rel = (int32_t)i;
+    if (!t.sees(q.ks0 + rel)) continue;
+    const int64_t slot = (int64_t)q.kvp0 * ps + rel;
+    const int32_t page = mass_page(a.plan, q, rel, ps, a.pool.num_pages);
+    if (page == a.pool.num_pages || slot >= a.logit_slots) continue;  // reported by the decode kernel
+    const float* s = a.logits + slot * Hq;
+    for (int32_t g = 0; g < Hkv; ++g) {
+      float sum = 0.f;
+      if (G % 4 == 0) {
+        for (int32_t h = g * G; h < (g + 1) * G; h += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(s + h);
+          sum += (ex2(x.x - s_lse[h]) + ex2(x.y - s_lse[h + 1])) + (ex2(x.z - s_lse[h + 2]) + ex2(x.w - s_lse[h + 3]));
+        }
+      } else {
+        for (int32_t h = g * G; h < (g + 1) * G; ++h) sum += ex2(s[h] - s_lse[h]);
+      }
+      mass_store(a, q, page, g, rel, sum);
+    }
+  }
+}
+
+size_t al16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+template <int D, int NQ>
+cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
+  using C = BdCfg<D>;
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const int32_t ps = a.pool.page_size, Hkv = a.pool.num_kv_heads, G = a.group;
+  CUtensorMap tq, tkv;
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.num_qo_heads, (cuuint64_t)a.plan.num_tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.num_qo_heads * D * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, 1};
+    if (enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)a.q, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  const int32_t br = std::min(ps, 16);  // key rows per box
+  {
+    // (64 d, row within an 8-row group, 64-d chunk, 8-row group): a box is br rows x 128 d
+    const cuuint64_t rows = (cuuint64_t)a.pool.num_pages * 2 * Hkv * ps;
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)D / 64, rows / 8};
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 2 * 8};
+    cuuint32_t box[4] = {64, 8, 2, (cuuint32_t)br / 8};
+    if (enc(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)a.pool.layer_base, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  static PerDeviceOnce setup;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = setup.get(dev, [dev](int* n) {
+    cudaError_t r = cudaFuncSetAttribute(bounded_decode_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::SMEM);
+    if (r != cudaSuccess) return r;
+    return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  }, &sms);
+  if (e != cudaSuccess) return e;
+  const int32_t S = std::max(1, std::min(std::min(sms, kMaxCtas), a.max_tiles));
+  BdArgs b;
+  b.a = a;
+  b.box_rows = br;
+  b.box_lg = 31 - __builtin_clz((unsigned)br);
+  b.page_lg = 31 - __builtin_clz((unsigned)ps);
+  unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws_raw);
+  b.prefix = reinterpret_cast<int64_t*>(ws);
+  b.rec_ml = reinterpret_cast<float*>(ws + al16((size_t)(a.plan.num_req + 1) * 8));
+  b.rec_o = b.rec_ml + (size_t)S * 2 * G * 2;
+  bounded_decode_kernel<D, NQ><<<(unsigned)S, kThreadsDec, C::SMEM, stream>>>(tq, tkv, b);
+  count_launch();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join's launch overlaps the decode kernel's tail (programmatic stream serialisation)
+  const bool weigh = a.stats.mass != nullptr;
+  const int32_t key_blocks = weigh ? (a.max_keys + kJoinThreads - 1) / kJoinThreads : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.plan.num_req * (Hkv * join_parts(G, D) + key_blocks)), 1, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.dynamicSmemBytes = weigh ? a.num_qo_heads * sizeof(float) : 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, bounded_join_kernel<D>, b, S, std::max(key_blocks, 1));
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool bounded_decode_supported(int32_t head_dim, int32_t group, int32_t page_size) {
+  return (head_dim == 256 || head_dim == 512) && group >= 1 && group <= kN && page_size >= 8 &&
+         (page_size & (page_size - 1)) == 0;
+}
+
+size_t bounded_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles) {
+  const size_t S = (size_t)std::max(1, std::min(kMaxCtas, max_tiles));
+  return al16((size_t)(num_req + 1) * 8) + S * 2 * group * 2 * 4 + S * 2 * group * head_dim * 4;
+}
+
+cudaError_t launch_bounded_decode(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
+  if (a.plan.num_req == 0) return cudaSuccess;
+  // the fewest softmax rows that hold the group
+  if (head_dim == 256) {
+    if (a.group <= 2) return launch_bd<256, 2>(a, stream);
+    if (a.group <= 4) return launch_bd<256, 4>(a, stream);
+    if (a.group <= 8) return launch_bd<256, 8>(a, stream);
+    return launch_bd<256, 16>(a, stream);
+  }
+  if (a.group <= 4) return launch_bd<512, 4>(a, stream);
+  if (a.group <= 8) return launch_bd<512, 8>(a, stream);
+  return launch_bd<512, 16>(a, stream);
+}
+
+}  // namespace pg

@@ -39,16 +39,9 @@
 // rings are short (3 stages at head_dim 256, 2 at 512) so that 4 (transposed form), 3 or 2
 // CTAs share each SM, each with its own producer and consumers.
 //
-// BC is the bounded-cache form: the first num_sink positions stay visible behind the window. A
-// segment's units are its sink units and then its window units (bounded.cuh; one run where they
-// meet), each unit's visible keys are 16 bits of its header (every other key's V row acts as
-// zero), the row sum adds the unrounded weights, and the scores are kept when the caller
-// accumulates attention weights.
-//
 // Every wait is bounded (two seconds of %globaltimer unless the launch passes a shorter limit);
 // a wait that runs out sets the device status word and the CTA leaves its loop; a producer that
 // gives up waits 100 us for its issued copies to land before the CTA's shared memory is released.
-#include "bounded.cuh"
 #include "pg_internal.h"
 
 #include <cuda.h>
@@ -111,13 +104,6 @@ struct alignas(16) DecUnit {
   int32_t klo, khi;   // visible positions [klo, khi) of the unit
   int32_t vz;         // V rows [vz, 16) hold no key of the request: they must read as zero
   int32_t flags;
-  // BC: klo holds the visible keys' bits, and khi and vz the slot (through the batch's page
-  // list) of the unit's first key
-  __device__ __forceinline__ void set_slot(int64_t s) {
-    khi = (int32_t)(uint32_t)s;
-    vz = (int32_t)(s >> 32);
-  }
-  __device__ __forceinline__ int64_t slot() const { return ((int64_t)vz << 32) | (uint32_t)khi; }
   int32_t rec;        // record slot (0: the CTA's first segment, 1: its last) when split
 };
 
@@ -129,9 +115,7 @@ struct DecArgs {
   float* rec_o;              // [kMaxDecodeCtas][2][G][D] fp32 (O / l of a split segment)
   float* rec_ml;             // [kMaxDecodeCtas][2][G][2] (m in log2 units, l)
   int64_t* prefix;           // [R + 1] units before request r (all heads); [R] = U
-  int32_t num_qo_heads, num_kv_heads, group, page_size, num_pages, window_left, num_sink;
-  float* logits;             // BC, optional: the scores of visible keys, [slot][Hq], log2 units
-  int64_t logit_slots;
+  int32_t num_qo_heads, num_kv_heads, group, page_size, num_pages, window_left;
   int32_t box_rows;          // key rows per TMA box: min(page_size, 16)
   int32_t box_lg, page_lg;   // log2 of box_rows and of page_size (both powers of two)
   float scale_log2;
@@ -246,17 +230,7 @@ __device__ __forceinline__ uint32_t kv_off(int k, int c, int u, int br) {
 // is request r: {0, qo_indptr[r], 1, start_pos, kvp0, kvp1, kv_end, kv_start}).
 struct ReqUnits {
   int32_t n, j0, lo, hi, tok, kvp0, kvp1, kv_len, ks0;
-  int32_t ns, sink;  // BC: sink units, and the end of the sink keys
-  // unit number (from the first key held) of the segment's j-th unit
-  template <bool BC>
-  __device__ __forceinline__ int32_t unit(int32_t j) const {
-    return BC && j < ns ? j : j0 + (BC ? j - ns : j);
-  }
-  __device__ __forceinline__ bool sees(int32_t key) const {
-    return key < hi && (key >= lo || key < sink);
-  }
 };
-template <bool BC>
 __device__ __forceinline__ ReqUnits req_units(const DecArgs& a, int32_t r) {
   const int4 e0 = __ldg(reinterpret_cast<const int4*>(a.plan.pair_tab) + 2 * r);
   const int4 e1 = __ldg(reinterpret_cast<const int4*>(a.plan.pair_tab) + 2 * r + 1);
@@ -269,15 +243,6 @@ __device__ __forceinline__ ReqUnits req_units(const DecArgs& a, int32_t r) {
   u.ks0 = e1.w;
   u.lo = a.window_left >= 0 ? max(u.ks0, p - a.window_left) : u.ks0;
   u.hi = min(p + 1, u.kv_len);
-  u.ns = u.sink = 0;
-  if constexpr (BC) {
-    const KeyWalk k = key_walk(a.window_left, a.num_sink, u.ks0, u.kv_len, p, p, kUnit);
-    u.n = k.total;
-    u.j0 = k.ft;
-    u.ns = k.ns;
-    u.sink = a.num_sink;
-    return u;
-  }
   if (u.hi > u.lo) {
     u.j0 = (u.lo - u.ks0) / kUnit;
     u.n = (u.hi - 1 - u.ks0) / kUnit - u.j0 + 1;
@@ -288,7 +253,7 @@ __device__ __forceinline__ ReqUnits req_units(const DecArgs& a, int32_t r) {
   return u;
 }
 
-template <int D, bool TR, bool BC>
+template <int D, bool TR>
 __global__ void __launch_bounds__(DecCfg<D, TR>::THREADS, DecCfg<D, TR>::MIN_CTAS)
 attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
   using C = DecCfg<D, TR>;
@@ -340,7 +305,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
     // (CTA 0) the prefix for the merge kernel. The first kHeld chunks' counts are loaded at
     // once (one round trip to memory) and stay in registers for the second scan.
     constexpr int kHeld = 8;
-    auto units_of = [&](int32_t r) -> int64_t { return r < R ? (int64_t)req_units<BC>(a, r).n * Hkv : 0; };
+    auto units_of = [&](int32_t r) -> int64_t { return r < R ? (int64_t)req_units(a, r).n * Hkv : 0; };
     auto scan32 = [&](int64_t v) {  // inclusive prefix over the warp
       int64_t incl = v;
 #pragma unroll
@@ -412,7 +377,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
     int32_t nseg = 0;  // segments started by this CTA
     bool ok = true;
     while (ok && u < u1) {
-      const ReqUnits q = req_units<BC>(a, r);
+      const ReqUnits q = req_units(a, r);
       const int64_t in_req = u - rbase;
       if (q.n == 0 || in_req >= (int64_t)q.n * Hkv) {  // next request
         rbase += (int64_t)q.n * Hkv;
@@ -449,11 +414,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         // lane l resolves box l % NB of unit ub + l / NB: its page id (or -1 past the keys held,
         // or num_pages when the metadata is out of range)
         const int32_t jl = (int32_t)(ub - seg0) + (lane >> LNB);  // unit within the segment
-        const int32_t rel = q.unit<BC>(jl) * kUnit + (lane & (NB - 1)) * BR;  // key index among those held
+        const int32_t rel = (q.j0 + jl) * kUnit + (lane & (NB - 1)) * BR;  // key index among those held
         int32_t page = -1, row = 0;
-        const int32_t bk = q.ks0 + rel;  // the box's first key; BC: boxes without a visible key stay
-        const bool seen = !BC || (bk < q.hi && (bk + BR > q.lo || bk < q.sink));
-        if (ub + (lane >> LNB) < stop && bk < q.kv_len && seen) {
+        if (ub + (lane >> LNB) < stop && q.ks0 + rel < q.kv_len) {
           const int32_t lp = rel >> a.page_lg;
           const int32_t pidx = q.kvp0 + (a.plan.ring ? lp % max(npg, 1) : lp);
           page = (pidx < q.kvp1 && pidx < a.plan.num_page_ids) ? a.plan.page_ids[pidx] : a.num_pages;
@@ -464,9 +427,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         for (int32_t t = 0; t < nb_units; ++t, ++i) {
           const int st = i % NS;
           const int32_t jj = (int32_t)(ub - seg0) + t;
-          const int32_t k0 = q.ks0 + q.unit<BC>(jj) * kUnit;
-          const uint32_t vis =
-              BC ? __ballot_sync(0xffffffffu, lane < kUnit && q.sees(k0 + lane)) : 0u;
+          const int32_t k0 = q.ks0 + (q.j0 + jj) * kUnit;
           const bool lane_box = (lane >> LNB) == t;
           const bool bad = __any_sync(0xffffffffu, lane_box && page == a.num_pages);
           const uint32_t nload = __popc(__ballot_sync(0xffffffffu, lane_box && page >= 0 &&
@@ -483,10 +444,6 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
               h.klo = max(q.lo, k0);
               h.khi = min(q.hi, k0 + kUnit);
               h.vz = min(max(q.kv_len - k0, 0), kUnit);
-              if constexpr (BC) {
-                h.klo = (int32_t)vis;
-                h.set_slot((int64_t)q.kvp0 * ps + (k0 - q.ks0));
-              }
               const int64_t uu = ub + t;
               h.flags = (uu == u ? kFirst : 0) | (uu + 1 == stop ? kLast : 0) |
                         (split ? kSplit : 0) | (bad ? kBad : 0) | (uu + 1 == u1 ? kEnd : 0);
@@ -592,19 +549,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         for (int e = 0; e < 4; ++e) {
           const float sv = (sa[0][e] + sa[1][e]) + (sa[2][e] + sa[3][e]);
           const int32_t key = h.k0 + gid + 8 * (e >> 1);
-          t[e] = (BC ? (h.klo >> (key - h.k0)) & 1 : key >= h.klo && key < h.khi) ? sv * a.scale_log2
-                                                                                  : -INFINITY;
-        }
-        if constexpr (BC) {
-          if (a.logits) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = gid + 8 * (e >> 1), row = 2 * tig + (e & 1);
-              const int64_t slot = h.slot() + k;
-              if (row < G && ((h.klo >> k) & 1) && slot < a.logit_slots)
-                a.logits[slot * Hq + h.g * G + row] = t[e];
-            }
-          }
+          t[e] = (key >= h.klo && key < h.khi) ? sv * a.scale_log2 : -INFINITY;
         }
         float mx0 = fmaxf(t[0], t[2]), mx1 = fmaxf(t[1], t[3]);
 #pragma unroll
@@ -618,15 +563,14 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         const float al0 = ex2(m[0] - r0), al1 = ex2(m[1] - r1);
         m[0] = n0;
         m[1] = n1;
-        const float w0 = ex2(t[0] - r0), w1 = ex2(t[1] - r1), w2 = ex2(t[2] - r0), w3 = ex2(t[3] - r1);
-        const uint32_t plo = pack_bf16(w0, w1);  // key gid
-        const uint32_t phi = pack_bf16(w2, w3);  // key gid + 8
+        const uint32_t plo = pack_bf16(ex2(t[0] - r0), ex2(t[1] - r1));  // key gid
+        const uint32_t phi = pack_bf16(ex2(t[2] - r0), ex2(t[3] - r1));  // key gid + 8
         // the row sums add the bf16-rounded weights the PV product uses (this lane's two keys;
         // summed over the lanes at the segment's end)
         auto lo16 = [](uint32_t v) { return __uint_as_float(v << 16); };
         auto hi16 = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
-        l[0] = l[0] * al0 + (BC ? w0 + w2 : lo16(plo) + lo16(phi));
-        l[1] = l[1] * al1 + (BC ? w1 + w3 : hi16(plo) + hi16(phi));
+        l[0] = l[0] * al0 + (lo16(plo) + lo16(phi));
+        l[1] = l[1] * al1 + (hi16(plo) + hi16(phi));
         if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
@@ -639,12 +583,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         const uint32_t pb1 = __byte_perm(__shfl_sync(0xffffffffu, phi, src0),
                                          __shfl_sync(0xffffffffu, phi, src1), psel);
         // V rows past the keys the request holds may be anything: they read as zero
-        const bool clear = BC ? h.klo != 0xFFFF : h.vz < kUnit;
-        if (clear) {
-          const int v0 = BC ? 0 : h.vz;
-          for (int idx = lane; idx < (kUnit - v0) * NC * 8; idx += 32) {
-            const int k = v0 + idx / (NC * 8);
-            if (BC && ((h.klo >> k) & 1)) continue;
+        if (h.vz < kUnit) {
+          for (int idx = lane; idx < (kUnit - h.vz) * NC * 8; idx += 32) {
+            const int k = h.vz + idx / (NC * 8);
             *reinterpret_cast<uint4*>(gb + (vb - base) + kv_off<NC>(k, (idx >> 3) % NC, idx & 7, BR)) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
@@ -664,7 +605,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) mma_bf16(o[8 * hb + j], vf[j], pb0, pb1);
         }
-        if (clear) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (h.vz < kUnit) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       if (h.flags & kLast) {
         // ---- the segment's output (or this CTA's record of it): query rows 2 tig + j < G
@@ -785,19 +726,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int32_t key = h.k0 + 8 * (e >> 2) + 2 * tig + (e & 1);
-          t[e] = (BC ? (h.klo >> (key - h.k0)) & 1 : key >= h.klo && key < h.khi) ? sv[e] * a.scale_log2
-                                                                                  : -INFINITY;
-        }
-        if constexpr (BC) {
-          if (a.logits && w == 0) {  // every warp holds the same scores
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int k = 8 * (e >> 2) + 2 * tig + (e & 1), row = gid + 8 * ((e >> 1) & 1);
-              const int64_t slot = h.slot() + k;
-              if (row < G && ((h.klo >> k) & 1) && slot < a.logit_slots)
-                a.logits[slot * Hq + h.g * G + row] = t[e];
-            }
-          }
+          t[e] = (key >= h.klo && key < h.khi) ? sv[e] * a.scale_log2 : -INFINITY;
         }
         float mx0 = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[4], t[5]));
         float mx1 = fmaxf(fmaxf(t[2], t[3]), fmaxf(t[6], t[7]));
@@ -806,26 +735,19 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
         const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-        // BC: a unit may show a row nothing (reference 0, weight 0)
-        const float r0 = BC && n0 == -INFINITY ? 0.f : n0, r1 = BC && n1 == -INFINITY ? 0.f : n1;
-        const float al0 = ex2(m0 - r0), al1 = ex2(m1 - r1);  // -inf - finite: 0
+        const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);  // -inf - finite: 0
         m0 = n0;
         m1 = n1;
-        float wt8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wt8[e] = ex2(t[e] - ((e & 2) ? r1 : r0));
         uint32_t pa[4];
-        pa[0] = pack_bf16(wt8[0], wt8[1]);
-        pa[1] = pack_bf16(wt8[2], wt8[3]);
-        pa[2] = pack_bf16(wt8[4], wt8[5]);
-        pa[3] = pack_bf16(wt8[6], wt8[7]);
-        // the row sums add the bf16-rounded weights the PV product uses (BC: the unrounded)
+        pa[0] = pack_bf16(ex2(t[0] - n0), ex2(t[1] - n0));
+        pa[1] = pack_bf16(ex2(t[2] - n1), ex2(t[3] - n1));
+        pa[2] = pack_bf16(ex2(t[4] - n0), ex2(t[5] - n0));
+        pa[3] = pack_bf16(ex2(t[6] - n1), ex2(t[7] - n1));
+        // the row sums add the bf16-rounded weights the PV product uses
         auto lo16 = [](uint32_t v) { return __uint_as_float(v << 16); };
         auto hi16 = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
-        l0 = l0 * al0 + (BC ? (wt8[0] + wt8[1]) + (wt8[4] + wt8[5])
-                            : (lo16(pa[0]) + hi16(pa[0])) + (lo16(pa[2]) + hi16(pa[2])));
-        l1 = l1 * al1 + (BC ? (wt8[2] + wt8[3]) + (wt8[6] + wt8[7])
-                            : (lo16(pa[1]) + hi16(pa[1])) + (lo16(pa[3]) + hi16(pa[3])));
+        l0 = l0 * al0 + ((lo16(pa[0]) + hi16(pa[0])) + (lo16(pa[2]) + hi16(pa[2])));
+        l1 = l1 * al1 + ((lo16(pa[1]) + hi16(pa[1])) + (lo16(pa[3]) + hi16(pa[3])));
         if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
@@ -835,12 +757,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
         }
         // V rows past the keys the request holds may be anything: this warp's two chunks of
         // them read as zero
-        const bool clear = BC ? h.klo != 0xFFFF : h.vz < kUnit;
-        if (clear) {
-          const int v0 = BC ? 0 : h.vz;
-          for (int idx = lane; idx < (kUnit - v0) * 16; idx += 32) {
-            const int k = v0 + idx / 16;
-            if (BC && ((h.klo >> k) & 1)) continue;
+        if (h.vz < kUnit) {
+          for (int idx = lane; idx < (kUnit - h.vz) * 16; idx += 32) {
+            const int k = h.vz + idx / 16;
             *reinterpret_cast<uint4*>(gb + (vb - base) +
                                       kv_off<NC>(k, 2 * w + ((idx >> 3) & 1), idx & 7, BR)) =
                 make_uint4(0u, 0u, 0u, 0u);
@@ -856,7 +775,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
           mma_bf16(o[2 * np], pa, b[0], b[1]);
           mma_bf16(o[2 * np + 1], pa, b[2], b[3]);
         }
-        if (clear) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (h.vz < kUnit) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
       if (h.flags & kLast) {
         // ---- the segment's output (or this CTA's record of it)
@@ -917,14 +836,14 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, DecArgs a) {
 // One CTA per (request, KV head). The request's entry and the unit prefixes are loaded together,
 // then each thread loads the (m, l) and columns of up to four records at once and folds them
 // in with a running maximum: about two round trips to memory per segment.
-template <int D, bool BC>
+template <int D>
 __global__ void __launch_bounds__(128) attn_decode_merge_kernel(DecArgs a, int32_t S) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t Hkv = a.num_kv_heads, G = a.group, Hq = a.num_qo_heads;
   const int32_t r = (int32_t)blockIdx.x / Hkv, g = (int32_t)blockIdx.x % Hkv;
   const int64_t U = a.prefix[a.plan.num_req];
   const int64_t pre = a.prefix[r];
-  const ReqUnits q = req_units<BC>(a, r);
+  const ReqUnits q = req_units(a, r);
   const int64_t row0 = (int64_t)q.tok * Hq + (int64_t)g * G;
   if (q.n == 0) {
     for (int i = threadIdx.x; i < G * D / 2; i += blockDim.x)
@@ -996,7 +915,7 @@ EncodeTiledFn encode_fn_dec() {
 
 size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-template <int D, bool TR, bool BC>
+template <int D, bool TR>
 cudaError_t launch_dec(const AttnArgs& a, cudaStream_t stream) {
   using C = DecCfg<D, TR>;
   EncodeTiledFn enc = encode_fn_dec();
@@ -1032,9 +951,6 @@ cudaError_t launch_dec(const AttnArgs& a, cudaStream_t stream) {
   d.page_size = ps;
   d.num_pages = a.pool.num_pages;
   d.window_left = a.window_left;
-  d.num_sink = a.num_sink;
-  d.logits = a.logits;
-  d.logit_slots = a.logit_slots;
   d.box_rows = br;
   d.box_lg = 31 - __builtin_clz((unsigned)br);
   d.page_lg = 31 - __builtin_clz((unsigned)ps);
@@ -1047,13 +963,13 @@ cudaError_t launch_dec(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = setup.get(dev, [dev](int* n) {
-    cudaError_t rr = cudaFuncSetAttribute(attn_decode_kernel<D, TR, BC>,
+    cudaError_t rr = cudaFuncSetAttribute(attn_decode_kernel<D, TR>,
                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (rr != cudaSuccess) return rr;
     int sms = 0, per = 0;
     rr = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (rr != cudaSuccess) return rr;
-    rr = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_decode_kernel<D, TR, BC>, C::THREADS,
+    rr = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_decode_kernel<D, TR>, C::THREADS,
                                                        C::SMEM);
     if (rr != cudaSuccess) return rr;
     *n = std::max(1, sms * std::max(per, 1));
@@ -1062,7 +978,7 @@ cudaError_t launch_dec(const AttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // one persistent CTA per slot; CTAs beyond the step's units run an empty range
   const int32_t grid = std::min(slots, kMaxDecodeCtas);
-  attn_decode_kernel<D, TR, BC><<<(unsigned)grid, C::THREADS, C::SMEM, stream>>>(tm, d);
+  attn_decode_kernel<D, TR><<<(unsigned)grid, C::THREADS, C::SMEM, stream>>>(tm, d);
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1078,7 +994,7 @@ cudaError_t launch_dec(const AttnArgs& a, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_decode_merge_kernel<D, BC>, d, grid);
+  e = cudaLaunchKernelEx(&cfg, attn_decode_merge_kernel<D>, d, grid);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -1105,11 +1021,9 @@ size_t attn_decode_stream_ws_bytes(int32_t num_req, int32_t group, int32_t head_
 
 cudaError_t launch_attn_decode_stream(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
   if (a.plan.num_req == 0) return cudaSuccess;
-  if (head_dim == 256 && a.bounded)
-    return a.group <= 4 ? launch_dec<256, true, true>(a, stream) : launch_dec<256, false, true>(a, stream);
   if (head_dim == 256)
-    return a.group <= 4 ? launch_dec<256, true, false>(a, stream) : launch_dec<256, false, false>(a, stream);
-  return launch_dec<512, false, false>(a, stream);
+    return a.group <= 4 ? launch_dec<256, true>(a, stream) : launch_dec<256, false>(a, stream);
+  return launch_dec<512, false>(a, stream);
 }
 
 }  // namespace pg

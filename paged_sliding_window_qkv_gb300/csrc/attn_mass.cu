@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kDecThreads) mass_decode_kernel(MassArgs m, in
     for (int32_t g = 0; g < a.pool.num_kv_heads; ++g) {
       float sum = 0.f;
       for (int32_t h = g * G; h < (g + 1) * G; ++h) sum += ex2(s[h] - s_lse[h]);
-      mass_store(m, q, page, g, rel, sum);
+      mass_store(a, q, page, g, rel, sum);
     }
   }
 }
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, 
     const int k = warp * 16 + gid + 8 * e;
     if (tig == 0 && k < nk) {
       const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
-      if (page < a.pool.num_pages) mass_store(m, q, page, g, rel0 + k, s);
+      if (page < a.pool.num_pages) mass_store(a, q, page, g, rel0 + k, s);
       else atomicOr(a.status, kStatusBounds);
     }
   }
@@ -202,7 +202,7 @@ cudaError_t launch_mass_mma(const MassArgs& m, int32_t max_keys, cudaStream_t st
 }  // namespace
 
 cudaError_t launch_mass_decode(const MassArgs& m, cudaStream_t stream) {
-  const int32_t blocks = (m.max_keys + kDecThreads - 1) / kDecThreads;
+  const int32_t blocks = (m.attn.max_keys + kDecThreads - 1) / kDecThreads;
   const int64_t grid = (int64_t)blocks * m.attn.plan.num_req;
   if (grid == 0) return cudaSuccess;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
@@ -212,11 +212,11 @@ cudaError_t launch_mass_decode(const MassArgs& m, cudaStream_t stream) {
 }
 
 cudaError_t launch_mass_prefill(const MassArgs& m, int32_t head_dim, cudaStream_t stream) {
-  if (m.max_keys <= 0 || m.attn.plan.num_req == 0) return cudaSuccess;
+  if (m.attn.max_keys <= 0 || m.attn.plan.num_req == 0) return cudaSuccess;
   if (attn_tc_supported(head_dim, m.attn.group, m.attn.pool.page_size))
     return launch_mass_prefill_tc(m, head_dim, stream);
-  return head_dim == 256 ? launch_mass_mma<256>(m, m.max_keys, stream)
-                         : launch_mass_mma<512>(m, m.max_keys, stream);
+  return head_dim == 256 ? launch_mass_mma<256>(m, m.attn.max_keys, stream)
+                         : launch_mass_mma<512>(m, m.attn.max_keys, stream);
 }
 
 }  // namespace pg

@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256) mass_join_kernel(MassArgs m, int32_t bloc
     float sum = 0.f;
     for (int32_t c = t.first / m.chunk; c <= (t.end - 1) / m.chunk && c < m.splits; ++c)
       sum += m.partial[((int64_t)c * Hkv + g) * m.partial_slots + slot];
-    mass_store(m, q, page, g, rel, sum);
+    mass_store(a, q, page, g, rel, sum);
   }
 }
 
@@ -380,7 +380,7 @@ cudaError_t launch_mass(const MassArgs& m, cudaStream_t stream) {
                                 MassCfg<D>::SMEM);
   }, &unused);
   if (e != cudaSuccess) return e;
-  const int32_t key_tiles = (m.max_keys + 2 * kMK - 1) / (2 * kMK);
+  const int32_t key_tiles = (a.max_keys + 2 * kMK - 1) / (2 * kMK);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (int64_t)key_tiles * a.pool.num_kv_heads * a.plan.num_req * m.splits), 1, 1);
   cfg.blockDim = dim3(kThreadsMass, 1, 1);
@@ -396,7 +396,7 @@ cudaError_t launch_mass(const MassArgs& m, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, mass_tc_kernel<D>, tq, tk, m, key_tiles, br);
   if (e != cudaSuccess) return e;
   count_launch();
-  const int32_t blocks = (m.max_keys + 255) / 256;
+  const int32_t blocks = (a.max_keys + 255) / 256;
   mass_join_kernel<<<(unsigned)(blocks * (int64_t)a.plan.num_req), 256, 0, stream>>>(m, blocks);
   count_launch();
   return cudaGetLastError();

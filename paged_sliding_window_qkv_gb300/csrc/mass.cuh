@@ -51,16 +51,15 @@ __device__ __forceinline__ MassTiles mass_tiles(const AttnArgs& a, const MassReq
 }
 
 // mass and position of one key: keys that the step wrote are set, older ones add
-__device__ __forceinline__ void mass_store(const MassArgs& m, const MassReq& q, int32_t page,
+__device__ __forceinline__ void mass_store(const AttnArgs& a, const MassReq& q, int32_t page,
                                            int32_t g, int32_t rel, float sum) {
-  const AttnArgs& a = m.attn;
   const int32_t ps = a.pool.page_size, j = q.ks0 + rel;
   const int64_t at = ((int64_t)page * a.pool.num_kv_heads + g) * ps + rel % ps;
   if (j >= q.sp) {
-    m.stats.mass[at] = sum;
-    m.stats.pos[at] = j;
+    a.stats.mass[at] = sum;
+    a.stats.pos[at] = j;
   } else {
-    m.stats.mass[at] += sum;
+    a.stats.mass[at] += sum;
   }
 }
 

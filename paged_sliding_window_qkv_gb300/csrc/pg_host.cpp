@@ -104,6 +104,7 @@ struct pg_plan {
          o_wreq = 0, o_wtok = 0, o_pair = 0;
   PlanStage stage;  // carried over from build to build of the same plan
   int32_t max_seen = 0;           // the most keys a request holds
+  int64_t tiles128 = 0;           // tiles of 128 keys over all requests (one KV head)
   std::vector<int32_t> host_ids;  // the page list, for the check below
   mutable int8_t shared = -1;     // a page is listed twice (-1: not looked at yet)
 };
@@ -157,6 +158,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     if (qo_indptr[0] != 0 || kv_page_indptr[0] != 0) return PG_ERR_ARG;
   }
   int32_t max_page = -1, max_last = 0, max_qo = 0, max_kv = 0, max_end = 0, max_seen = 0;
+  int64_t tiles128 = 0;
   bool all_one = num_req > 0, prep_ok = true;
   for (int32_t r = 0; r < num_req; ++r) {
     const int64_t q0 = qo_indptr[r], q1 = qo_indptr[r + 1];
@@ -202,6 +204,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     start[r] = (int32_t)sp;
     kvs[r] = (int32_t)seg0;
     if (kv_len - seg0 > max_seen) max_seen = (int32_t)(kv_len - seg0);
+    tiles128 += (kv_len - seg0 + 127) / 128;
     if (lpl > max_last) max_last = lpl;
     if (qo_len > max_qo) max_qo = (int32_t)qo_len;
     if (kv_len > max_kv) max_kv = (int32_t)kv_len;
@@ -334,6 +337,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.dev = d; q.dev_elems = host.size();
   q.dev_cap = fresh ? bytes : p->dev_cap;
   q.max_seen = max_seen;
+  q.tiles128 = tiles128;
   q.host_ids = std::move(pids);
 
   // Commit: only now does the caller's plan change.
@@ -478,9 +482,26 @@ struct Bounded {
   int32_t num_sink = 0;
   float* logits = nullptr;
   int64_t logit_slots = 0;
+  StatsDev stats = {};
 };
 
-// `args` (optional) receives the launched call's arguments, with num_tokens 0 when nothing ran.
+// Workspace of the bounded-cache form: the tensor-core kernel's records, or the chunked kernel's
+// partials where that one runs.
+int32_t plan_max_tiles(const pg_plan* p) {
+  return (int32_t)std::min<int64_t>(p->tiles128 * p->num_kv_heads, INT32_MAX);
+}
+size_t bounded_ws_bytes(const pg_plan* p) {
+  if (!p || !p->decode || p->num_req == 0) return 0;
+  const int32_t group = p->num_qo_heads / p->num_kv_heads;
+  if (bounded_decode_supported(p->head_dim, group, p->page_size))
+    return bounded_decode_ws_bytes(p->num_req, group, p->head_dim, plan_max_tiles(p));
+  const size_t rows = (size_t)p->num_req * p->num_qo_heads * p->max_chunks;
+  return rows * (size_t)p->head_dim * sizeof(float) + rows * 2 * sizeof(float);
+}
+
+size_t plan_ws_bytes(const pg_plan* p) { return std::max(workspace_bytes(p), bounded_ws_bytes(p)); }
+
+// `args` (the accumulating entry, whose workspace holds more) receives the launched call's arguments, with num_tokens 0 when nothing ran.
 int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32_t D,
                 const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
                 float sm_scale, void* ws, size_t ws_bytes, cudaStream_t stream,
@@ -511,7 +532,8 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   // the tensor-core prefill kernel reads Q rows and writes output rows in 32-byte accesses
   if ((((uintptr_t)q | (uintptr_t)out) & 31u) != 0) return PG_ERR_ALIGN;
   if (lse && ((uintptr_t)lse & 3u) != 0) return PG_ERR_ALIGN;
-  const size_t need = workspace_bytes(plan);
+  // one size serves every entry that takes pg_workspace_bytes
+  const size_t need = args ? bounded_ws_bytes(plan) : plan_ws_bytes(plan);
   if (need > 0) {
     if (!ws || ws_bytes < need) return PG_ERR_WORKSPACE;
     if (!aligned16(ws)) return PG_ERR_ALIGN;
@@ -537,6 +559,9 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   a.num_sink = bounded ? bounded->num_sink : 0;
   a.logits = bounded ? bounded->logits : nullptr;
   a.logit_slots = bounded ? bounded->logit_slots : 0;
+  a.stats = bounded ? bounded->stats : StatsDev{};
+  a.max_keys = plan->max_seen;
+  a.max_tiles = plan_max_tiles(plan);
   wait_settings(&a.wait_ns, &a.test_withhold);
   cudaError_t e;
   a.ws_raw = ws;
@@ -635,7 +660,7 @@ MassSplit plan_mass_split(const pg_plan* p) {
 size_t mass_workspace_bytes(const pg_plan* p) {
   if (!p || p->num_req == 0) return 0;
   if (p->decode)
-    return align256(workspace_bytes(p)) + (size_t)logit_slots(p) * p->num_qo_heads * sizeof(float);
+    return align256(bounded_ws_bytes(p)) + (size_t)logit_slots(p) * p->num_qo_heads * sizeof(float);
   if (mass_on_tensor_cores(p))  // the sums of each range of query tiles
     return (size_t)plan_mass_split(p).splits * p->num_kv_heads * (size_t)logit_slots(p) * sizeof(float);
   return 0;
@@ -838,7 +863,9 @@ int pg_prep_paged_hd512(const pg_plan_t plan, const pg_pool_t* pool, int32_t lay
   return launch_prep_hd512(a, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
-size_t pg_workspace_bytes(const pg_plan_t plan) { return workspace_bytes(plan); }
+size_t pg_workspace_bytes(const pg_plan_t plan) {
+  return plan_ws_bytes(plan);
+}
 
 int pg_attn_paged_prefill(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
                           const pg_bf16_t* q, pg_bf16_t* out, int32_t window_left, float sm_scale,
@@ -930,16 +957,19 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
     if (!workspace || ws_bytes < need) return PG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PG_ERR_ALIGN;
   }
-  // one block per 64 keys of a head (prefill) or 256 keys of a request (decode)
-  int64_t blocks = 0;
+  // every grid fits: at most a block per 64 keys of a head, and (decode) one per 512 output columns
+  int64_t blocks = 0, joins = 0;
   if (!mul_i64((plan->max_seen + 63) / 64, plan->num_req, &blocks) ||
-      !mul_i64(blocks, plan->num_kv_heads, &blocks) || !fits_i32(blocks))
+      !mul_i64(blocks, plan->num_kv_heads, &blocks) ||
+      !mul_i64((int64_t)plan->num_req * plan->num_qo_heads, plan->head_dim / 256, &joins) ||
+      !fits_i32(blocks + joins))
     return PG_ERR_I32_OVERFLOW;
   if (mass_on_tensor_cores(plan) && plan_mass_split(plan).units > INT32_MAX / 2)
     return PG_ERR_I32_OVERFLOW;  // two blocks per unit
   Bounded b;
   b.num_sink = num_sink;
-  const size_t attn_ws = align256(workspace_bytes(plan));
+  b.stats = stats_dev(stats, layer);
+  const size_t attn_ws = align256(bounded_ws_bytes(plan));
   if (plan->decode && plan->num_req > 0) {
     b.logits = reinterpret_cast<float*>(static_cast<char*>(workspace) + attn_ws);
     // as many as the workspace holds: a graph's plan may grow into a larger one
@@ -949,8 +979,6 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
   rc = attn_common(plan, pool, layer, plan->head_dim, q, out, lse, window_left, sm_scale, workspace,
                    attn_ws, s, &b, &m.attn);
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
-  m.stats = stats_dev(stats, layer);
-  m.max_keys = plan->max_seen;
   if (mass_on_tensor_cores(plan)) {
     const MassSplit sp = plan_mass_split(plan);
     m.partial = static_cast<float*>(workspace);
@@ -958,8 +986,11 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
     m.splits = sp.splits;
     m.chunk = sp.chunk;
   }
-  const cudaError_t e =
-      plan->decode ? launch_mass_decode(m, s) : launch_mass_prefill(m, plan->head_dim, s);
+  // (the tensor-core decode adds the weights itself)
+  const bool done = plan->decode && bounded_decode_supported(plan->head_dim, m.attn.group, plan->page_size);
+  const cudaError_t e = done           ? cudaSuccess
+                        : plan->decode ? launch_mass_decode(m, s)
+                                       : launch_mass_prefill(m, plan->head_dim, s);
   return e == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 

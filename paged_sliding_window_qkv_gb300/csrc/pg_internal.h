@@ -73,6 +73,14 @@ struct PrepArgs {
   int* status;
 };
 
+// Per-key statistics of one layer range: mass (accumulated attention weight) and pos (position)
+// of [layer][page][kv_head][slot], at the first layer of the call.
+struct StatsDev {
+  float* mass;
+  int32_t* pos;
+  int64_t stride_layer;  // elements
+};
+
 struct AttnArgs {
   PlanDev plan;
   PoolDev pool;
@@ -96,27 +104,20 @@ struct AttnArgs {
   int32_t num_sink;
   float* logits;
   int64_t logit_slots;
+  StatsDev stats;       // decode: accumulate the weights here (mass null: do not)
+  int32_t max_keys;     // the most keys a request holds
+  int32_t max_tiles;    // decode: tiles of 128 keys over all requests and KV heads
   int* status;
   uint64_t wait_ns;       // limit of the kernels' bounded waits (nanoseconds)
   int32_t test_withhold;  // test hook of pg_test_bounded_wait (0: off)
 };
 
-// Per-key statistics of one layer range: mass (accumulated attention weight) and pos (position)
-// of [layer][page][kv_head][slot], at the first layer of the call.
-struct StatsDev {
-  float* mass;
-  int32_t* pos;
-  int64_t stride_layer;  // elements
-};
-
 // Accumulation of attention weights into the statistics (see attn_mass.cu).
 struct MassArgs {
   AttnArgs attn;      // the attention call whose weights are accumulated (lse written by it)
-  StatsDev stats;     // of the called layer
   float* partial;     // tensor-core form: [splits][num_kv_heads][partial_slots] sums
   int64_t partial_slots;
   int32_t splits, chunk;  // tensor-core form: query-range splits, query tiles in each
-  int32_t max_keys;       // the most keys a request of the plan holds
 };
 
 // Choice and compaction of an eviction (see evict.cu).
@@ -166,6 +167,12 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int32_t head_dim, cudaStream_t
 bool attn_decode_stream_supported(int32_t head_dim, int32_t group, int32_t page_size);
 size_t attn_decode_stream_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim);
 cudaError_t launch_attn_decode_stream(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
+
+// Bounded-cache decode on the tensor cores (and, with stats, the accumulated weights): the
+// geometry it handles, its workspace for a plan of max_tiles tiles, and its launch.
+bool bounded_decode_supported(int32_t head_dim, int32_t group, int32_t page_size);
+size_t bounded_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles);
+cudaError_t launch_bounded_decode(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
 
 // Decode attention with its partials in the library's static scratch (no allocation).
 // The caller has already checked the plan's workspace size against that scratch.
