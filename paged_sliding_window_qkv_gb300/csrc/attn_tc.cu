@@ -191,6 +191,14 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
   u.ntiles = hi > u.kb0 ? (hi - u.kb0 + kBN - 1) / kBN : 0;
   return u;
 }
+// BC: the keys of a tile that a row sees: below hi, and from lo on or below sink (all relative to
+// the tile's first key).
+__device__ __forceinline__ uint64_t bits_below(int32_t n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+__device__ __forceinline__ uint64_t tile_bits(int32_t hi, int32_t lo, int32_t sink) {
+  return bits_below(hi) & (~bits_below(lo) | bits_below(sink));
+}
 // L2 prefetch of unit w's pair-table entry, so tc_unit finds it there later
 __device__ __forceinline__ void tc_unit_prefetch(const TcArgs& a, int32_t w, int32_t ndh) {
   const int32_t pr = a.plan.num_pairs - 1 - w / (a.num_kv_heads * ndh);
@@ -742,11 +750,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const bool interior =
               __all_sync(0xffffffffu, rvalid && (kb >= rlo || (BC && kb + kBN <= sink)) && kb + kBN <= rhi);
           if (!interior) {
+            if constexpr (BC) {
+              // the row's visible keys as 64 bits: a test per key whatever the sinks
+              const uint64_t vis = tile_bits(rvalid ? rhi - kb : 0, rlo - kb, sink - kb);
+#pragma unroll
+              for (int k = 0; k < kBN; ++k) sv[k] = (vis >> k) & 1u ? sv[k] : 0xFF800000u;
+            } else {
 #pragma unroll
             for (int k = 0; k < kBN; ++k) {
               const int32_t key = kb + k;
-              const bool vis = rvalid && (key >= rlo || (BC && key < sink)) && key < rhi;
+              const bool vis = rvalid && key >= rlo && key < rhi;
               sv[k] = vis ? sv[k] : 0xFF800000u;  // -inf
+            }
             }
           }
           // this tile's row maximum in log2 units; t holds the values the exponent scales
@@ -882,11 +897,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const bool interior =
             __all_sync(0xffffffffu, rvalid && (kb >= rlo || (BC && kb + kBN <= sink)) && kb + kBN <= rhi);
         if (!interior) {
+          if constexpr (BC) {
+            const uint64_t vis = tile_bits(rvalid ? rhi - kb : 0, rlo - kb, sink - kb);
+#pragma unroll
+            for (int k = 0; k < kBN; ++k) sv[k] = (vis >> k) & 1u ? sv[k] : 0xFF800000u;
+          } else {
 #pragma unroll
           for (int k = 0; k < kBN; ++k) {
             const int32_t key = kb + k;
-            const bool vis = rvalid && (key >= rlo || (BC && key < sink)) && key < rhi;
+            const bool vis = rvalid && key >= rlo && key < rhi;
             sv[k] = vis ? sv[k] : 0xFF800000u;  // -inf
+          }
           }
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
