@@ -193,9 +193,6 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
 }
 // BC: the keys of a tile that a row sees: below hi, and from lo on or below sink (all relative to
 // the tile's first key).
-__device__ __forceinline__ uint64_t bits_below(int32_t n) {
-  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-}
 __device__ __forceinline__ uint64_t tile_bits(int32_t hi, int32_t lo, int32_t sink) {
   return bits_below(hi) & (~bits_below(lo) | bits_below(sink));
 }

@@ -11,6 +11,11 @@
 
 namespace pg {
 
+// The low n of 64 bits.
+__device__ __forceinline__ uint64_t bits_below(int32_t n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 struct KeyWalk {
   int32_t ns, ft, total;  // sink tiles, first window tile, tiles in all
   int32_t lo, hi;         // the window part's keys [lo, hi); sinks lie below min(num_sink, hi)

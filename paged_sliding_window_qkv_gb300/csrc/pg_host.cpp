@@ -653,17 +653,11 @@ bool mass_on_tensor_cores(const pg_plan* p) {
   return !p->decode && p->num_req > 0 &&
          attn_tc_supported(p->head_dim, p->num_qo_heads / p->num_kv_heads, p->page_size);
 }
-MassSplit plan_mass_split(const pg_plan* p) {
-  return mass_split(p->num_req, p->num_kv_heads, p->num_qo_heads / p->num_kv_heads, p->num_tokens,
-                    p->max_qo_len, p->max_seen);
-}
 size_t mass_workspace_bytes(const pg_plan* p) {
   if (!p || p->num_req == 0) return 0;
   if (p->decode)
     return align256(bounded_ws_bytes(p)) + (size_t)logit_slots(p) * p->num_qo_heads * sizeof(float);
-  if (mass_on_tensor_cores(p))  // the sums of each range of query tiles
-    return (size_t)plan_mass_split(p).splits * p->num_kv_heads * (size_t)logit_slots(p) * sizeof(float);
-  return 0;
+  return mass_on_tensor_cores(p) ? mass_tc_ws_bytes() : 0;
 }
 
 // Checks of an eviction call, and its arguments.
@@ -964,8 +958,6 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
       !mul_i64((int64_t)plan->num_req * plan->num_qo_heads, plan->head_dim / 256, &joins) ||
       !fits_i32(blocks + joins))
     return PG_ERR_I32_OVERFLOW;
-  if (mass_on_tensor_cores(plan) && plan_mass_split(plan).units > INT32_MAX / 2)
-    return PG_ERR_I32_OVERFLOW;  // two blocks per unit
   Bounded b;
   b.num_sink = num_sink;
   b.stats = stats_dev(stats, layer);
@@ -979,13 +971,7 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
   rc = attn_common(plan, pool, layer, plan->head_dim, q, out, lse, window_left, sm_scale, workspace,
                    attn_ws, s, &b, &m.attn);
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
-  if (mass_on_tensor_cores(plan)) {
-    const MassSplit sp = plan_mass_split(plan);
-    m.partial = static_cast<float*>(workspace);
-    m.partial_slots = logit_slots(plan);
-    m.splits = sp.splits;
-    m.chunk = sp.chunk;
-  }
+  m.ws = workspace;  // (prefill attention itself needs none)
   // (the tensor-core decode adds the weights itself)
   const bool done = plan->decode && bounded_decode_supported(plan->head_dim, m.attn.group, plan->page_size);
   const cudaError_t e = done           ? cudaSuccess

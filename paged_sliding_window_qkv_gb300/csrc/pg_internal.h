@@ -115,9 +115,7 @@ struct AttnArgs {
 // Accumulation of attention weights into the statistics (see attn_mass.cu).
 struct MassArgs {
   AttnArgs attn;      // the attention call whose weights are accumulated (lse written by it)
-  float* partial;     // tensor-core form: [splits][num_kv_heads][partial_slots] sums
-  int64_t partial_slots;
-  int32_t splits, chunk;  // tensor-core form: query-range splits, query tiles in each
+  void* ws;           // tensor-core prefill: mass_tc_ws_bytes() of the caller's workspace
 };
 
 // Choice and compaction of an eviction (see evict.cu).
@@ -187,13 +185,8 @@ cudaError_t launch_merge_states(const __nv_bfloat16* out_a, const float* lse_a,
 // Adds the attention weights of a finished attention call to the per-key statistics.
 cudaError_t launch_mass_decode(const MassArgs& m, cudaStream_t stream);
 cudaError_t launch_mass_prefill(const MassArgs& m, int32_t head_dim, cudaStream_t stream);
-// Tensor-core form (geometries of attn_tc_supported): query tiles per range, ranges, and units.
-struct MassSplit {
-  int32_t chunk, splits;
-  int64_t units;
-};
-MassSplit mass_split(int32_t num_req, int32_t num_kv_heads, int32_t group, int64_t num_tokens,
-                     int32_t max_qo_len, int32_t max_keys);
+// Tensor-core form (geometries of attn_tc_supported) and its workspace.
+size_t mass_tc_ws_bytes();
 cudaError_t launch_mass_prefill_tc(const MassArgs& m, int32_t head_dim, cudaStream_t stream);
 // Eviction: the source slot of every kept slot, and the moves it describes.
 void set_page_divisor(EvictArgs* a);
