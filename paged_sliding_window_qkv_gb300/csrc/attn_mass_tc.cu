@@ -163,7 +163,8 @@ struct alignas(16) MassCut {
   int32_t r, g, kt, slot;  // slot: its record in cluster s (0: the cluster's first segment, 1)
   int32_t last;            // the last cluster that has tiles of it (-1: no such segment)
   int32_t empty;           // the cluster has no tiles, and no record
-  int32_t pad[2];
+  int32_t sparse;          // the step has fewer tiles than clusters: some are empty
+  int32_t pad;
 };
 
 template <int D>
@@ -199,11 +200,15 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const bool leader = rank == 0;
   auto LEAD = [&](uint32_t bar) { return mapa(bar, 0); };
 
+  // the join's launch overlaps this kernel; this one's own start overlaps the attention's tail
+  // (programmatic launches): only the sums need what the attention wrote, its lse
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (w.left == 0) {  // (both CTAs of the cluster)
-    if (leader && threadIdx.x == 0) cuts[s] = MassCut{0, 0, 0, 0, -1, 1, {0, 0}};
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (leader && threadIdx.x == 0) cuts[s] = MassCut{0, 0, 0, 0, -1, 1, 1, 0};
     return;
   }
-  if (leader && warp == 2 && lane == 0) cuts[s] = MassCut{0, 0, 0, 0, -1, 0, {0, 0}};  // until its end
+  if (leader && warp == 2 && lane == 0) cuts[s] = MassCut{0, 0, 0, 0, -1, 0, 0, 0};  // until its end
   if (threadIdx.x == 0) {
     for (int x = 0; x < NS; ++x) {
       mbar_init(FULL(x), 2);  // one arrival (with its byte count) from each CTA's producer
@@ -357,6 +362,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (tk >= w.q.len) return -INFINITY;
       return a.lse[(int64_t)(w.q.q0 + tk) * Hq + w.g * G + (col & (G - 1))] * -1.4426950408889634f;
     };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     bool ok = true, more = true;
     const float2 sc = make_float2(a.sm_scale_log2, a.sm_scale_log2);
     int32_t i = 0;
@@ -462,7 +468,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const bool last = w.left == w.t_hi - w.t;
       if (last && leader && warp == 2 && lane == 0) {
         // a segment that starts here and goes on: its end among the clusters, for the join
-        MassCut cut{w.r, w.g, w.kt, w.first ? 0 : 1, -1, 0, {0, 0}};
+        MassCut cut{w.r, w.g, w.kt, w.first ? 0 : 1, -1, 0, total < S ? 1 : 0, 0};
         if (w.t == w.mt.first && w.t_hi < w.mt.end) {
           const int64_t end = (int64_t)(s + 1) * total / S + (w.mt.end - w.t_hi);  // its tiles end here
           cut.last = (int32_t)((end * S - 1) / total);
@@ -498,6 +504,7 @@ __global__ void __launch_bounds__(2 * kMK) mass_join_kernel(MassArgs m) {
   const MassCut* cuts = reinterpret_cast<const MassCut*>(m.ws);
   const float* recs = reinterpret_cast<const float*>(cuts + kMaxClusters);
   const int32_t s = (int32_t)blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const MassCut c = cuts[s];
   if (c.last <= s) return;
   const MassReq q = mass_req(a.plan, c.r, a.pool.page_size);
@@ -506,14 +513,16 @@ __global__ void __launch_bounds__(2 * kMK) mass_join_kernel(MassArgs m) {
   const int32_t page = mass_page(a.plan, q, rel, a.pool.page_size, a.pool.num_pages);
   if (page == a.pool.num_pages) return;  // reported by the producer
   float sum = recs[((int64_t)s * 2 + c.slot) * (2 * kMK) + threadIdx.x];
-  // (a cluster between them without tiles, when there are fewer tiles than clusters, has no record)
-  for (int32_t k0 = s + 1; k0 <= c.last; k0 += 8) {
-    float v[8];
+  // (a cluster between them without tiles has no record)
+  for (int32_t k0 = s + 1; k0 <= c.last; k0 += 16) {
+    float v[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = k0 + k <= c.last && !cuts[k0 + k].empty ? recs[((int64_t)(k0 + k) * 2) * (2 * kMK) + threadIdx.x] : 0.f;
+    for (int k = 0; k < 16; ++k)
+      v[k] = k0 + k <= c.last && !(c.sparse && cuts[k0 + k].empty)
+                 ? recs[((int64_t)(k0 + k) * 2) * (2 * kMK) + threadIdx.x]
+                 : 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum += v[k];
+    for (int k = 0; k < 16; ++k) sum += v[k];
   }
   mass_store(a, q, page, c.g, rel, sum);
 }
@@ -562,17 +571,24 @@ cudaError_t launch_mass(const MassArgs& m, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreadsMass, 1, 1);
   cfg.dynamicSmemBytes = MassCfg<D>::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, mass_tc_kernel<D>, tq, tk, m, br);
   if (e != cudaSuccess) return e;
   count_launch();
-  mass_join_kernel<<<(unsigned)clusters, 2 * kMK, 0, stream>>>(m);
+  cfg.gridDim = dim3((unsigned)clusters, 1, 1);
+  cfg.blockDim = dim3(2 * kMK, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, mass_join_kernel, m);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }

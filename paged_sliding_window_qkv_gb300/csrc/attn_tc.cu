@@ -298,6 +298,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   cluster_sync();  // both CTAs' barriers exist before either CTA signals the other
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // BC: the pass that accumulates weights may start on SMs that this one has left (it waits for
+  // this grid's completion before it reads lse)
+  if constexpr (BC) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------ producers
