@@ -66,11 +66,12 @@ struct alignas(16) TileHdr {
 template <int D>
 struct BdCfg {
   static constexpr int PARTS = D / 128;            // slots per tile of K, and of V
-  static constexpr int NSLOT = D == 256 ? 6 : 5;
+  static constexpr int NSLOT = 6;
+  static constexpr int NQB = D == 256 ? 2 : 1;     // query buffers (segments)
   static constexpr int Q_BYTES = (D / 64) * kN * 128;  // [64-d chunk][16 rows][128 B]
   static constexpr int P_BYTES = 2 * kN * 128;         // [64-key chunk][16 rows][128 B]
   static constexpr int OFF_Q = NSLOT * kSlot;
-  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_P = OFF_Q + NQB * Q_BYTES;
   static constexpr int OFF_HDR = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_RED = OFF_HDR + kHdrs * (int)sizeof(TileHdr);  // [4 warps][16]
   static constexpr int OFF_FIN = OFF_RED + 4 * kN * 4;                    // [16] (l, reference)
@@ -227,7 +228,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   }
   // query and weight rows past the group stay zero
   if (warp >= 2) {
-    for (int i = threadIdx.x - 64; i < (2 * C::Q_BYTES + 2 * C::P_BYTES) / 16; i += kThreadsDec - 64)
+    for (int i = threadIdx.x - 64; i < (C::NQB * C::Q_BYTES + 2 * C::P_BYTES) / 16; i += kThreadsDec - 64)
       *reinterpret_cast<uint4*>(gb + C::OFF_Q + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
   }
@@ -295,7 +296,6 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -383,8 +383,8 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           int go = 1;
           if (lane == 0) {
             if (first) {
-              const int qb = segs & 1;
-              go = mbar_wait_inline(QEMPTY + 8 * qb, ((segs >> 1) & 1) ^ 1, wc) ? 1 : 0;
+              const int qb = segs % C::NQB;
+              go = mbar_wait_inline(QEMPTY + 8 * qb, ((segs / C::NQB) & 1) ^ 1, wc) ? 1 : 0;
               if (go) {
                 mbar_expect_tx(QFULL + 8 * qb, (uint32_t)(G * D * 2));
                 for (int c = 0; c < D / 64; ++c)
@@ -465,12 +465,12 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         if (lane == 0) mbar_arrive(HEMPTY + 8 * (i % kHdrs));
         if (flags & kEmpty) break;
         if (flags & kFirst) {
-          ok = wait1(QFULL + 8 * (segs & 1), (segs >> 1) & 1);
+          ok = wait1(QFULL + 8 * (segs % C::NQB), (segs / C::NQB) & 1);
           ++segs;
         }
         const int sb = i & 1;
         ok = ok && wait1(SFREE + 8 * sb, ((i >> 1) & 1) ^ 1);
-        const uint32_t qb = base + C::OFF_Q + ((segs - 1) & 1) * C::Q_BYTES;
+        const uint32_t qb = base + C::OFF_Q + ((segs - 1) % C::NQB) * C::Q_BYTES;
         for (int p = 0; ok && p < PARTS; ++p) {
           ok = wait1(FULL(slot), round & 1);
           if (!ok) break;
@@ -487,7 +487,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         if (!ok) break;
         commit1(SFULL + 8 * sb);
-        if (flags & kLast) commit1(QEMPTY + 8 * ((segs - 1) & 1));
+        if (flags & kLast) commit1(QEMPTY + 8 * ((segs - 1) % C::NQB));
       }
       if (i > 0) {
         const int32_t jt = i - 1;
@@ -778,17 +778,21 @@ __device__ __forceinline__ bool holds_tiles(const SegRecs& s, int32_t c, int64_t
 // Blocks [0, R Hkv G D / 512): 512 columns of one segment's records into its output (segments
 // inside one CTA were written directly; a segment without keys gets zeros), four columns a thread
 // and eight records in flight, so a segment cut into many waits for memory once per eight.
-// Blocks from there on (weights): 128 keys of one request, a thread per key, all heads; the
-// normalisers come from the records, or from lse where the segment was written directly.
+// Blocks from there on (weights): 256 keys of one request, two a thread, all heads. The scores and
+// page ids load while the normalisers are taken from the records (eight lanes per head), or from
+// lse where the segment was written directly.
+// (Launched without programmatic serialisation: blocks that wait on the SMs while the decode
+// kernel streams cost it more than their earlier start saves, 236 against 222 us on 64 requests
+// of 8001 keys at head_dim 512.)
 constexpr int kJoinThreads = 128;
+constexpr int kPer = 2;                         // keys of a thread
+constexpr int kJoinKeys = kPer * kJoinThreads;  // keys of a weight block
 constexpr int kJoinRecs = 8;
 __host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D) {
   return (group * D + 511) / 512;
 }
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) bounded_join_kernel(BdArgs args, int32_t S,
-                                                                    int32_t key_blocks) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
   const AttnArgs& a = args.a;
   const int32_t Hkv = a.pool.num_kv_heads, G = a.group, Hq = a.num_qo_heads, R = a.plan.num_req;
   const int64_t U = args.prefix[R];
@@ -841,62 +845,112 @@ __global__ void __launch_bounds__(kJoinThreads) bounded_join_kernel(BdArgs args,
     return;
   }
   // ---- weights
-  extern __shared__ float s_lse[];  // the request's normalisers, log2 units
+  extern __shared__ __align__(16) float s_lse[];  // the request's normalisers, log2 units
   const int32_t ps = a.pool.page_size;
   const int32_t r = ((int32_t)blockIdx.x - merges) / key_blocks, kb = ((int32_t)blockIdx.x - merges) % key_blocks;
   const MassReq q = mass_req(a.plan, r, ps);
-  if (kb * kJoinThreads >= q.n) return;
+  if ((int64_t)kb * kJoinKeys >= q.n) return;
   const ReqTiles t = req_tiles(args, r);
   if (t.total == 0) return;
   const int64_t pre = args.prefix[r];
-  // a warp per head, a lane per record
-  const int lane = tid & 31;
-#pragma unroll 4
-  for (int h = tid >> 5; h < Hq; h += kJoinThreads / 32) {
-    const SegRecs s = seg_recs(pre + (int64_t)(h / G) * t.total, t.total, U, S);
-    float v;
-    if (s.sa == s.sb) {
-      v = a.lse[(int64_t)q.q0 * Hq + h] * kLog2ef;
-    } else {
-      float M = -INFINITY, den = 0.f;
-      for (int32_t c = s.sa + lane; c <= s.sb; c += 32) {
-        const int64_t rb = ((int64_t)c * 2 + (c == s.sa ? s.slot_a : 0)) * G + h % G;
-        const float2 ml = holds_tiles(s, c, U, S) ? *reinterpret_cast<const float2*>(args.rec_ml + rb * 2)
-                                                  : make_float2(-INFINITY, 0.f);
-        if (ml.y != 0.f) {
-          const float mn = fmaxf(M, ml.x);
-          den = den * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
-          M = mn;
+  const float* src[kPer];
+  int32_t page[kPer];
+  float4 x[kPer][4];
+  const bool vec = Hq == 16;  // a key's scores are four vectors
+  auto load = [&](int64_t k0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t k = k0 + i * kJoinThreads + tid;
+      const int32_t rel = (int32_t)min(k, (int64_t)q.n - 1);
+      const int64_t slot = (int64_t)q.kvp0 * ps + rel;
+      const bool seen = k < q.n && t.sees(q.ks0 + rel) && slot < a.logit_slots;
+      // (a page out of range was reported by the decode kernel)
+      page[i] = seen ? mass_page(a.plan, q, rel, ps, a.pool.num_pages) : a.pool.num_pages;
+      src[i] = a.logits + (seen ? slot * Hq : 0);
+      if (vec && seen) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[i][v] = reinterpret_cast<const float4*>(src[i])[v];
+      }
+    }
+  };
+  load((int64_t)kb * kJoinKeys);
+  // eight lanes per head, a record each at a time
+  const int sub = tid & 7;
+  for (int h0 = 0; h0 < Hq; h0 += kJoinThreads / 8) {
+    const int h = h0 + (tid >> 3);
+    float M = -INFINITY, den = 0.f, direct = 0.f;
+    SegRecs s{0, 0, 0, false};
+    if (h < Hq) {
+      s = seg_recs(pre + (int64_t)(h / G) * t.total, t.total, U, S);
+      if (s.sa == s.sb) {
+        direct = a.lse[(int64_t)q.q0 * Hq + h] * kLog2ef;
+      } else {
+        for (int32_t c = s.sa + sub; c <= s.sb; c += 8) {
+          const int64_t rb = ((int64_t)c * 2 + (c == s.sa ? s.slot_a : 0)) * G + h % G;
+          const float2 ml = holds_tiles(s, c, U, S) ? *reinterpret_cast<const float2*>(args.rec_ml + rb * 2)
+                                                    : make_float2(-INFINITY, 0.f);
+          if (ml.y != 0.f) {
+            const float mn = fmaxf(M, ml.x);
+            den = den * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
+            M = mn;
+          }
         }
       }
-      const float mx = warp_max(M);
-      float d = den != 0.f ? den * exp2f(M - mx) : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      v = mx + log2f(d);
     }
-    if (lane == 0) s_lse[h] = v;
+    float mx = M;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float d = den != 0.f ? den * exp2f(M - mx) : 0.f;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (h < Hq && sub == 0) s_lse[h] = s.sa == s.sb ? direct : mx + log2f(d);
   }
   __syncthreads();
   // (a graph's plan may have grown since the capture: the blocks stride over the keys)
-  for (int64_t i = (int64_t)kb * kJoinThreads + tid; i < q.n; i += (int64_t)key_blocks * kJoinThreads) {
-    const int32_t rel = (int32_t)i;
-    if (!t.sees(q.ks0 + rel)) continue;
-    const int64_t slot = (int64_t)q.kvp0 * ps + rel;
-    const int32_t page = mass_page(a.plan, q, rel, ps, a.pool.num_pages);
-    if (page == a.pool.num_pages || slot >= a.logit_slots) continue;  // reported by the decode kernel
-    const float* s = a.logits + slot * Hq;
-    for (int32_t g = 0; g < Hkv; ++g) {
-      float sum = 0.f;
-      if (G % 4 == 0) {
-        for (int32_t h = g * G; h < (g + 1) * G; h += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(s + h);
-          sum += (ex2(x.x - s_lse[h]) + ex2(x.y - s_lse[h + 1])) + (ex2(x.z - s_lse[h + 2]) + ex2(x.w - s_lse[h + 3]));
+  for (int64_t k0 = (int64_t)kb * kJoinKeys; k0 < q.n; k0 += (int64_t)key_blocks * kJoinKeys) {
+    if (k0 != (int64_t)kb * kJoinKeys) load(k0);
+    if (vec) {
+      // the group's sums of four heads at a time: a group is 1, 2 or a multiple of 4 of them
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (page[i] >= a.pool.num_pages) continue;
+        const int32_t rel = (int32_t)(k0 + i * kJoinThreads + tid);
+        float run = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float4 z = *reinterpret_cast<const float4*>(s_lse + 4 * v);
+          const float e[4] = {ex2(x[i][v].x - z.x), ex2(x[i][v].y - z.y), ex2(x[i][v].z - z.z), ex2(x[i][v].w - z.w)};
+          if (G >= 4) {
+            run += (e[0] + e[1]) + (e[2] + e[3]);
+            if ((4 * v + 4) % G == 0) {
+              mass_store(a, q, page[i], 4 * v / G, rel, run);
+              run = 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              run += e[k];
+              if ((k + 1) % G == 0) {
+                mass_store(a, q, page[i], (4 * v + k) / G, rel, run);
+                run = 0.f;
+              }
+            }
+          }
         }
-      } else {
-        for (int32_t h = g * G; h < (g + 1) * G; ++h) sum += ex2(s[h] - s_lse[h]);
       }
-      mass_store(a, q, page, g, rel, sum);
+    } else {
+      for (int32_t g = 0; g < Hkv; ++g) {
+        float sum[kPer] = {};
+        for (int32_t h = g * G; h < (g + 1) * G; ++h) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (page[i] < a.pool.num_pages) sum[i] += ex2(src[i][h] - s_lse[h]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (page[i] < a.pool.num_pages)
+            mass_store(a, q, page[i], g, (int32_t)(k0 + i * kJoinThreads + tid), sum[i]);
+      }
     }
   }
 }
@@ -957,21 +1011,11 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   count_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // the join's launch overlaps the decode kernel's tail (programmatic stream serialisation)
   const bool weigh = a.stats.mass != nullptr;
-  const int32_t key_blocks = weigh ? (a.max_keys + kJoinThreads - 1) / kJoinThreads : 0;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.plan.num_req * (Hkv * join_parts(G, D) + key_blocks)), 1, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.dynamicSmemBytes = weigh ? a.num_qo_heads * sizeof(float) : 0;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, bounded_join_kernel<D>, b, S, std::max(key_blocks, 1));
-  if (e != cudaSuccess) return e;
+  const int32_t key_blocks = weigh ? (a.max_keys + kJoinKeys - 1) / kJoinKeys : 0;
+  const unsigned grid = (unsigned)((int64_t)a.plan.num_req * (Hkv * join_parts(G, D) + key_blocks));
+  bounded_join_kernel<D><<<grid, kJoinThreads, weigh ? a.num_qo_heads * sizeof(float) : 0, stream>>>(
+      b, S, std::max(key_blocks, 1));
   count_launch();
   return cudaGetLastError();
 }
