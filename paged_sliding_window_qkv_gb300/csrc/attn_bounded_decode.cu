@@ -14,11 +14,14 @@
 // positions they hold, so a few sinks cost one box and not a tile of their own (with tiles of
 // consecutive keys 4 sinks beside a window of 1024 cost 10% of the call: a near-empty tile holds
 // its ring slots as long as a full one). CTA s of S takes tiles [s U / S, (s + 1) U / S). A segment
-// cut between CTAs leaves fp32 records (O / l, m, l) that the join kernel combines.
+// cut between CTAs leaves fp32 records (O / l, m, l) that the join kernel combines. (Smaller tiles
+// for steps that leave SMs idle were slower: one request of 8001 keys at head_dim 512 took 24.6 us
+// in tiles of 32 keys, whose unused rows have to be cleared, against 16.4.)
 //
-//   warp 0    producer: 32 KB slots (128 keys x 128 d of K or V, one 4-D box per page and slot, all
-//             landing as [8 keys][64-d chunk][8 rows][128 B]), in the order K0 K1 V0 K2 V1 ...; the
-//             group's query rows per segment; a header per tile (visible keys as bits, flags)
+//   warps 0, 6  producers of K and of V: 32 KB slots (128 keys x 128 d, one 4-D box per 16 keys and
+//             slot, all landing as [8 keys][64-d chunk][8 rows][128 B]) of one ring, in the order
+//             K0 K1 V0 K2 V1 ...; warp 0 also the group's query rows per segment and a header per
+//             tile (visible keys as bits, flags)
 //   warp 1    MMA issuer: QK of tile i + 1 before PV of tile i, so a tile's softmax has a tile's
 //             load time to finish
 //   warps 2-5 softmax: a thread is a key (TMEM lane); 16 scores, exponentials against a per-row
@@ -48,7 +51,7 @@ namespace {
 constexpr int kT = 128;               // keys per tile
 constexpr int kSlot = kT * 256;       // 128 keys x 128 d
 constexpr int kN = 16;                // MMA columns: query rows of the group, padded
-constexpr int kThreadsDec = 192;
+constexpr int kThreadsDec = 224;
 constexpr int kMaxCtas = 256;         // records are sized for at most this many CTAs
 constexpr int kHdrs = 4;
 constexpr float kRescale = 48.f, kHeadroom = 64.f;  // see attn_tc.cu
@@ -227,15 +230,17 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // query and weight rows past the group stay zero
-  if (warp >= 2) {
-    for (int i = threadIdx.x - 64; i < (C::NQB * C::Q_BYTES + 2 * C::P_BYTES) / 16; i += kThreadsDec - 64)
+  if (warp >= 2 && warp < 6) {
+    for (int i = threadIdx.x - 64; i < (C::NQB * C::Q_BYTES + 2 * C::P_BYTES) / 16; i += 128)
       *reinterpret_cast<uint4*>(gb + C::OFF_Q + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
   }
+  // everything below reads or writes memory that earlier work of the stream may still use
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // (the producer finds its tiles while the others set up)
   int32_t n = 0, r = 0;
   int64_t in_req = 0;
-  if (warp == 0) {
+  if (warp == 0 || warp == 6) {
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_kv) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_q) : "memory");
@@ -263,10 +268,10 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       const int j = c / 32;
       const int64_t v = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : j == 3 ? held[3] : tiles_of(c + lane);
       const int64_t incl = scan(v);
-      if (s == 0 && c + lane < R) args.prefix[c + lane] = U + incl - v;
+      if (s == 0 && warp == 0 && c + lane < R) args.prefix[c + lane] = U + incl - v;
       U += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (s == 0 && lane == 0) args.prefix[R] = U;
+    if (s == 0 && threadIdx.x == 0) args.prefix[R] = U;
     const int64_t u0 = s * U / S, u1 = (s + 1) * U / S;
     n = (int32_t)(u1 - u0);
     if (n > 0) {
@@ -297,11 +302,14 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------ producers
+    // Both walk the tiles; warp 0 issues K, the queries and the headers, warp 6 issues V. (One warp
+    // for both took some 5 us a tile at head_dim 512 without any copy in it: the copies' issue.)
+    const bool is_v = warp == 6;
     bool ok = true;
     if (n == 0) {
-      if (lane == 0) {
+      if (lane == 0 && !is_v) {
         hdrs[0].flags = kEmpty | kEnd;
         mbar_arrive(HFULL);
       }
@@ -353,85 +361,71 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         return t;
       };
-      int32_t slot = 0, round = 0;
-      auto load = [&](const Tile& t, bool good, int kv) {
-        // one K (kv 0) or V slot after the other
-        const uint32_t mask = __ballot_sync(0xffffffffu, good);
-        const int32_t row = (int32_t)((((int64_t)t.page * 2 + kv) * Hkv + t.g) * ps + t.off);
-        for (int p = 0; ok && p < PARTS; ++p) {
-          int go = 1;
-          if (lane == 0) {
-            go = mbar_wait_inline(EMPTY(slot), (round & 1) ^ 1, wc) ? 1 : 0;
-            if (go) mbar_expect_tx(FULL(slot), (uint32_t)__popc(mask) * br * 256u);
-          }
-          if (!__shfl_sync(0xffffffffu, go, 0)) {
-            ok = false;
-            break;
-          }
-          if (good) tma_4d(base + slot * kSlot + lane * br * 256, &tm_kv, 2 * p, row / 8, FULL(slot));
+      // PARTS slots of K or V, from the at-th of the CTA's stream of slots (K0 K1 V0 K2 V1 ...)
+      auto load = [&](const Tile& t, bool good, int32_t at) {
+        const uint32_t boxes = __ballot_sync(0xffffffffu, good);
+        const int32_t row = (int32_t)((((int64_t)t.page * 2 + (is_v ? 1 : 0)) * Hkv + t.g) * ps + t.off);
+        int slot = at % NS, round = at / NS;
+        for (int p = 0; p < PARTS; ++p) {
+          if (!__all_sync(0xffffffffu, mbar_wait_inline(EMPTY(slot), (round & 1) ^ 1, wc))) return false;
+          if (lane == 0) mbar_expect_tx(FULL(slot), (uint32_t)__popc(boxes) * br * 256u);
           __syncwarp();
+          if (good) tma_4d(base + slot * kSlot + lane * br * 256, &tm_kv, 2 * p, row / 8, FULL(slot));
           if (++slot == NS) { slot = 0; ++round; }
         }
+        return true;
       };
-      Tile cur = next(0), prev = cur;
-      bool prev_good = false;
+      Tile cur = next(0);
       int32_t segs = 0;
-      for (int32_t i = 0; ok && i <= n; ++i) {
-        bool good = false;
-        if (i < n) {
-          const bool first = cur.flags & kFirst;
-          int go = 1;
-          if (lane == 0) {
-            if (first) {
-              const int qb = segs % C::NQB;
-              go = mbar_wait_inline(QEMPTY + 8 * qb, ((segs / C::NQB) & 1) ^ 1, wc) ? 1 : 0;
-              if (go) {
-                mbar_expect_tx(QFULL + 8 * qb, (uint32_t)(G * D * 2));
-                for (int c = 0; c < D / 64; ++c)
-                  tma_3d(base + C::OFF_Q + qb * C::Q_BYTES + c * (kN * 128), &tm_q, c * 64, cur.g * G,
-                         cur.q.tok, QFULL + 8 * qb);
-              }
-            }
-            if (go) go = mbar_wait_inline(HEMPTY + 8 * (i % kHdrs), ((i / kHdrs) & 1) ^ 1, wc) ? 1 : 0;
-          }
-          if (!__shfl_sync(0xffffffffu, go, 0)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();  // (lane 0's wait orders every lane's header writes)
-          if (first) ++segs;
-          good = cur.live && cur.page >= 0 && cur.page < a.pool.num_pages;
-          const uint32_t boxes = __ballot_sync(0xffffffffu, good);
-          if (__any_sync(0xffffffffu, cur.live && !good) && lane == 0) atomicOr(a.status, kStatusBounds);
-          uint32_t vis[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int k = 32 * w + lane, box = k >> args.box_lg;
-            const int32_t key = cur.q.ks0 + __shfl_sync(0xffffffffu, cur.rel, box) + (k & (br - 1));
-            vis[w] = __ballot_sync(0xffffffffu, ((boxes >> box) & 1u) && cur.q.sees(key));
-          }
-          TileHdr& h = hdrs[i % kHdrs];
-          if (lane < nbox) h.rel[lane] = cur.rel;
-          if (lane == 0) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) h.vis[w] = vis[w];
-            h.flags = cur.flags;
-            h.r = cur.r;
-            h.g = cur.g;
-            h.tok = cur.q.tok;
-            h.slot0 = (int64_t)cur.q.kvp0 * ps;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(HFULL + 8 * (i % kHdrs));
-          load(cur, good, 0);
+      for (int32_t i = 0; ok && i < n; ++i) {
+        const bool good = cur.live && cur.page >= 0 && cur.page < a.pool.num_pages;
+        if (is_v) {
+          const int32_t at = PARTS * (i == n - 1 ? 2 * i + 1 : 2 * i + 2);
+          // the next tile's page ids load behind this tile's copies
+          const Tile t = cur;
+          if (i + 1 < n) cur = next(i + 1);
+          ok = load(t, good, at);
+          continue;
         }
-        // the next tile's page ids load behind this tile's K and the previous tile's V
-        Tile ahead = cur;
-        if (i + 1 < n) ahead = next(i + 1);
-        if (ok && i > 0) load(prev, prev_good, 1);
-        prev = cur;
-        prev_good = good;
-        cur = ahead;
+        const bool first = cur.flags & kFirst;
+        if (first) {
+          const int qb = segs % C::NQB;
+          ok = __all_sync(0xffffffffu, mbar_wait_inline(QEMPTY + 8 * qb, ((segs / C::NQB) & 1) ^ 1, wc));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(QFULL + 8 * qb, (uint32_t)(G * D * 2));
+          __syncwarp();
+          if (lane < D / 64)
+            tma_3d(base + C::OFF_Q + qb * C::Q_BYTES + lane * (kN * 128), &tm_q, lane * 64, cur.g * G, cur.q.tok,
+                   QFULL + 8 * qb);
+          ++segs;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_inline(HEMPTY + 8 * (i % kHdrs), ((i / kHdrs) & 1) ^ 1, wc));
+        if (!ok) break;
+        const uint32_t boxes = __ballot_sync(0xffffffffu, good);
+        if (__any_sync(0xffffffffu, cur.live && !good) && lane == 0) atomicOr(a.status, kStatusBounds);
+        uint32_t vis[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int k = 32 * w + lane, box = k >> args.box_lg;
+          const int32_t key = cur.q.ks0 + __shfl_sync(0xffffffffu, cur.rel, box) + (k & (br - 1));
+          vis[w] = __ballot_sync(0xffffffffu, ((boxes >> box) & 1u) && cur.q.sees(key));
+        }
+        TileHdr& h = hdrs[i % kHdrs];
+        if (lane < nbox) h.rel[lane] = cur.rel;
+        if (lane == 0) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) h.vis[w] = vis[w];
+          h.flags = cur.flags;
+          h.r = cur.r;
+          h.g = cur.g;
+          h.tok = cur.q.tok;
+          h.slot0 = (int64_t)cur.q.kvp0 * ps;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(HFULL + 8 * (i % kHdrs));
+        const Tile t = cur;
+        if (i + 1 < n) cur = next(i + 1);
+        ok = load(t, good, i == 0 ? 0 : PARTS * (2 * i - 1));
       }
     }
     if (!ok) {
@@ -775,9 +769,9 @@ __device__ __forceinline__ bool holds_tiles(const SegRecs& s, int32_t c, int64_t
   return (uint32_t)c * u / (uint32_t)S < (uint32_t)(c + 1) * u / (uint32_t)S;
 }
 
-// Blocks [0, R Hkv G D / 512): 512 columns of one segment's records into its output (segments
-// inside one CTA were written directly; a segment without keys gets zeros), four columns a thread
-// and eight records in flight, so a segment cut into many waits for memory once per eight.
+// Blocks [0, R Hkv G D RG / 512): 512 / RG columns of one segment's records into its output
+// (segments inside one CTA were written directly; a segment without keys gets zeros), four columns
+// a thread and eight records in flight.
 // Blocks from there on (weights): 256 keys of one request, two a thread, all heads. The scores and
 // page ids load while the normalisers are taken from the records (eight lanes per head), or from
 // lse where the segment was written directly.
@@ -788,54 +782,77 @@ constexpr int kJoinThreads = 128;
 constexpr int kPer = 2;                         // keys of a thread
 constexpr int kJoinKeys = kPer * kJoinThreads;  // keys of a weight block
 constexpr int kJoinRecs = 8;
-__host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D) {
-  return (group * D + 511) / 512;
+// RG: threads that share the records of four columns (4 where segments are cut into many, so that
+// 32 records are in flight, else 1)
+__host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D, int32_t RG) {
+  return (group * D * RG + 511) / 512;
 }
-template <int D>
+template <int D, int RG>
 __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
   const AttnArgs& a = args.a;
+  // (a following kernel launched programmatically may set up; it waits for this one)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int32_t Hkv = a.pool.num_kv_heads, G = a.group, Hq = a.num_qo_heads, R = a.plan.num_req;
   const int64_t U = args.prefix[R];
   const int tid = threadIdx.x;
-  const int32_t parts = join_parts(G, D), merges = R * Hkv * parts;
+  const int32_t parts = join_parts(G, D, RG), merges = R * Hkv * parts;
   if ((int32_t)blockIdx.x < merges) {
     const int32_t seg = (int32_t)blockIdx.x / parts, r = seg / Hkv, g = seg % Hkv;
-    const int32_t idx = ((int32_t)blockIdx.x % parts) * kJoinThreads + tid;  // four columns of a row
+    constexpr int kCols = kJoinThreads / RG;
+    __shared__ float4 s_acc[kJoinThreads];
+    __shared__ float2 s_md[kJoinThreads];
+    const int rg = tid / kCols;
+    const int32_t idx = ((int32_t)blockIdx.x % parts) * kCols + tid % kCols;  // four columns of a row
     const int32_t row = idx / (D / 4), c4 = idx % (D / 4);
     const int64_t pre = args.prefix[r];
     const ReqTiles q = req_tiles(args, r);
     const int64_t row0 = (int64_t)q.tok * Hq + (int64_t)g * G;
-    if (row >= G) return;
+    if (RG == 1 && row >= G) return;
+    const bool mine = row < G && rg == 0;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (row0 + row) * D + 4 * c4);
     if (q.total == 0) {
-      dst[0] = dst[1] = 0u;
-      if (a.lse && c4 == 0) a.lse[row0 + row] = -INFINITY;
+      if (mine) {
+        dst[0] = dst[1] = 0u;
+        if (a.lse && c4 == 0) a.lse[row0 + row] = -INFINITY;
+      }
       return;
     }
     const SegRecs s = seg_recs(pre + (int64_t)g * q.total, q.total, U, S);
     if (s.sa == s.sb) return;
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int32_t c0 = s.sa; c0 <= s.sb; c0 += kJoinRecs) {
+    auto add = [&](float m2, float w2, float4 x, bool mean) {
+      if (w2 == 0.f) return;  // saw no key (a NaN sum stays)
+      const float mn = fmaxf(M, m2), so = exp2f(M - mn), e = exp2f(m2 - mn);
+      const float w = mean ? w2 * e : e;  // records hold means, partial states sums
+      acc.x = acc.x * so + w * x.x; acc.y = acc.y * so + w * x.y;
+      acc.z = acc.z * so + w * x.z; acc.w = acc.w * so + w * x.w;
+      den = den * so + w2 * e;
+      M = mn;
+    };
+    for (int32_t c0 = s.sa + rg; row < G && c0 <= s.sb; c0 += RG * kJoinRecs) {
       float2 ml[kJoinRecs];
       float4 v[kJoinRecs];
 #pragma unroll
       for (int k = 0; k < kJoinRecs; ++k) {
-        const int32_t c = c0 + k;
+        const int32_t c = c0 + RG * k;
         const bool in = c <= s.sb && holds_tiles(s, c, U, S);
         const int64_t rb = ((int64_t)c * 2 + (c == s.sa ? s.slot_a : 0)) * G + row;
         ml[k] = in ? *reinterpret_cast<const float2*>(args.rec_ml + rb * 2) : make_float2(-INFINITY, 0.f);
         v[k] = in ? *reinterpret_cast<const float4*>(args.rec_o + rb * D + 4 * c4) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int k = 0; k < kJoinRecs; ++k) {
-        if (ml[k].y == 0.f) continue;  // saw no key (a NaN sum stays)
-        const float mn = fmaxf(M, ml[k].x);
-        const float so = exp2f(M - mn), w = ml[k].y * exp2f(ml[k].x - mn);
-        acc.x = acc.x * so + w * v[k].x; acc.y = acc.y * so + w * v[k].y;
-        acc.z = acc.z * so + w * v[k].z; acc.w = acc.w * so + w * v[k].w;
-        den = den * so + w;
-        M = mn;
+      for (int k = 0; k < kJoinRecs; ++k) add(ml[k].x, ml[k].y, v[k], true);
+    }
+    if constexpr (RG > 1) {
+      s_acc[tid] = acc;
+      s_md[tid] = make_float2(M, den);
+      __syncthreads();
+      if (!mine) return;
+#pragma unroll
+      for (int k = 1; k < RG; ++k) {
+        const float2 md = s_md[tid + k * kCols];
+        add(md.x, md.y, s_acc[tid + k * kCols], false);
       }
     }
     const float inv = den != 0.f ? 1.f / den : 0.f;
@@ -1007,15 +1024,30 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   b.prefix = reinterpret_cast<int64_t*>(ws);
   b.rec_ml = reinterpret_cast<float*>(ws + al16((size_t)(a.plan.num_req + 1) * 8));
   b.rec_o = b.rec_ml + (size_t)S * 2 * G * 2;
-  bounded_decode_kernel<D, NQ><<<(unsigned)S, kThreadsDec, C::SMEM, stream>>>(tq, tkv, b);
-  count_launch();
-  e = cudaGetLastError();
+  // programmatic serialisation: the CTAs' set-up overlaps the end of the stream's previous kernel
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)S, 1, 1);
+  cfg.blockDim = dim3(kThreadsDec, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, bounded_decode_kernel<D, NQ>, tq, tkv, b);
   if (e != cudaSuccess) return e;
+  count_launch();
   const bool weigh = a.stats.mass != nullptr;
   const int32_t key_blocks = weigh ? (a.max_keys + kJoinKeys - 1) / kJoinKeys : 0;
-  const unsigned grid = (unsigned)((int64_t)a.plan.num_req * (Hkv * join_parts(G, D) + key_blocks));
-  bounded_join_kernel<D><<<grid, kJoinThreads, weigh ? a.num_qo_heads * sizeof(float) : 0, stream>>>(
-      b, S, std::max(key_blocks, 1));
+  const int32_t segs = a.plan.num_req * Hkv;
+  auto join = [&](auto kernel, int32_t RG) {
+    const unsigned grid =
+        (unsigned)((int64_t)segs * join_parts(G, D, RG) + (int64_t)a.plan.num_req * key_blocks);
+    kernel<<<grid, kJoinThreads, weigh ? a.num_qo_heads * sizeof(float) : 0, stream>>>(b, S, std::max(key_blocks, 1));
+  };
+  if (segs * 4 < S) join(bounded_join_kernel<D, 4>, 4);
+  else join(bounded_join_kernel<D, 1>, 1);
   count_launch();
   return cudaGetLastError();
 }

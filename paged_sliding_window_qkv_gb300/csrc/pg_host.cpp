@@ -104,7 +104,7 @@ struct pg_plan {
          o_wreq = 0, o_wtok = 0, o_pair = 0;
   PlanStage stage;  // carried over from build to build of the same plan
   int32_t max_seen = 0;           // the most keys a request holds
-  int64_t tiles128 = 0;           // tiles of 128 keys over all requests (one KV head)
+  int64_t tiles = 0;              // tiles of 128 keys over all requests (one KV head)
   std::vector<int32_t> host_ids;  // the page list, for the check below
   mutable int8_t shared = -1;     // a page is listed twice (-1: not looked at yet)
 };
@@ -158,7 +158,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     if (qo_indptr[0] != 0 || kv_page_indptr[0] != 0) return PG_ERR_ARG;
   }
   int32_t max_page = -1, max_last = 0, max_qo = 0, max_kv = 0, max_end = 0, max_seen = 0;
-  int64_t tiles128 = 0;
+  int64_t tiles = 0;
   bool all_one = num_req > 0, prep_ok = true;
   for (int32_t r = 0; r < num_req; ++r) {
     const int64_t q0 = qo_indptr[r], q1 = qo_indptr[r + 1];
@@ -204,7 +204,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     start[r] = (int32_t)sp;
     kvs[r] = (int32_t)seg0;
     if (kv_len - seg0 > max_seen) max_seen = (int32_t)(kv_len - seg0);
-    tiles128 += (kv_len - seg0 + 127) / 128;
+    tiles += (kv_len - seg0 + 127) / 128;
     if (lpl > max_last) max_last = lpl;
     if (qo_len > max_qo) max_qo = (int32_t)qo_len;
     if (kv_len > max_kv) max_kv = (int32_t)kv_len;
@@ -337,7 +337,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.dev = d; q.dev_elems = host.size();
   q.dev_cap = fresh ? bytes : p->dev_cap;
   q.max_seen = max_seen;
-  q.tiles128 = tiles128;
+  q.tiles = tiles;
   q.host_ids = std::move(pids);
 
   // Commit: only now does the caller's plan change.
@@ -488,7 +488,7 @@ struct Bounded {
 // Workspace of the bounded-cache form: the tensor-core kernel's records, or the chunked kernel's
 // partials where that one runs.
 int32_t plan_max_tiles(const pg_plan* p) {
-  return (int32_t)std::min<int64_t>(p->tiles128 * p->num_kv_heads, INT32_MAX);
+  return (int32_t)std::min<int64_t>(p->tiles * p->num_kv_heads, INT32_MAX);
 }
 size_t bounded_ws_bytes(const pg_plan* p) {
   if (!p || !p->decode || p->num_req == 0) return 0;
@@ -951,11 +951,11 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
     if (!workspace || ws_bytes < need) return PG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PG_ERR_ALIGN;
   }
-  // every grid fits: at most a block per 64 keys of a head, and (decode) one per 512 output columns
+  // every grid fits: at most a block per 64 keys of a head, and (decode) one per 128 output columns
   int64_t blocks = 0, joins = 0;
   if (!mul_i64((plan->max_seen + 63) / 64, plan->num_req, &blocks) ||
       !mul_i64(blocks, plan->num_kv_heads, &blocks) ||
-      !mul_i64((int64_t)plan->num_req * plan->num_qo_heads, plan->head_dim / 256, &joins) ||
+      !mul_i64((int64_t)plan->num_req * plan->num_qo_heads, plan->head_dim / 64, &joins) ||
       !fits_i32(blocks + joins))
     return PG_ERR_I32_OVERFLOW;
   Bounded b;
