@@ -67,19 +67,22 @@ __device__ __forceinline__ uint32_t order_of(const EvictArgs& a, int64_t recent,
 
 // ------------------------------------------------------------------ select
 // One CTA (or a cluster of up to 8) per segment, its keys in registers: thread t of the segment
-// holds slots [KPT t, KPT (t + 1)), so slot order is thread order and every rank below is a bit
-// count over the thread's 32-bit masks and one scan over the threads. Statistics are read four
-// slots at a time where the pages and the arrays allow it (V4).
+// holds slots [k t, k (t + 1)), k <= KPT the segment's share of them in groups of four, so slot
+// order is thread order and every rank below is a bit count over the thread's 32-bit masks and one
+// scan over the threads. Statistics are read four slots at a time where the pages and the arrays
+// allow it (V4).
 //
 // The keep-th largest order value is built bit by bit from the top: a candidate stays when at
 // least keep keys reach it, one count over the segment per bit (compares in registers, a warp
 // reduction and one barrier: no histogram, so equal exponents cost nothing). The descent ends when
 // exactly keep keys reach the candidate (then nothing ties), about 20 bits in for masses that
-// differ. Bound: a segment is read once (8 bytes a key), and the counts are two instructions per
-// key and bit; with them one CTA on an SM covers the other's loads.
+// differ; once 1024 keys or fewer share the bits so far, they are gathered and only they are
+// counted (two a thread). Bound: a segment is read once (8 bytes a key), and the counts are two
+// instructions per key and bit; with them one CTA on an SM covers the other's loads.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kGather = 2 * kSelThreads;  // keys gathered out of the segment: two a thread
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
   const int32_t step = CL ? kSelThreads * ranks : kSelThreads, first = rank * kSelThreads + tid;
   const bool fits = q.n <= kSelThreads * KPT * (CL ? ranks : 1);
   // every slot keeps its key until a hole below says otherwise
-  if (!CL || q.keep == q.n || !fits)
+  if (!CL || q.keep == q.n || !fits)  // (a cluster that goes on does it below)
     for (int32_t s = first; s < a.budget; s += step) src[s] = s < q.keep ? s : -1;
   if (q.keep == q.n) return;  // (the whole cluster)
   if (!fits) {  // a plan that grew past its captured launch
@@ -177,14 +180,17 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
     return;
   }
   if constexpr (CL) {
-    // the CTA's own slots, so that its barrier orders them before its holes
-    const int32_t s1 = min(a.budget, (rank + 1) * kSelThreads * KPT);
-    for (int32_t s = rank * kSelThreads * KPT + tid; s < s1; s += kSelThreads) src[s] = s < q.keep ? s : -1;
-    for (int32_t s = kSelThreads * KPT * ranks + first; s < a.budget; s += step) src[s] = -1;
-    cluster_barrier();  // every peer runs before its shared memory is written
+    // (the cluster's barriers order every slot before the holes); and every peer runs before its
+    // shared memory is written
+    for (int32_t s = first; s < a.budget; s += step) src[s] = s < q.keep ? s : -1;
+    cluster_barrier();
   }
   const int64_t recent = recent_from(a, q);
-  const int32_t s0 = (rank * kSelThreads + tid) * KPT;
+  // the segment's slots in equal shares: groups of four (whole groups keep V4's vectors in a page)
+  const int32_t threads = kSelThreads * (CL ? ranks : 1);
+  const int32_t share = ((q.n + threads - 1) / threads + 3) & ~3;
+  const int32_t s0 = (rank * kSelThreads + tid) * share;
+  const int32_t s_end = min(q.n, s0 + share);
   uint32_t key[KPT];
   if constexpr (V4) {
     // four slots of one page at a time, all loads in flight before the first use
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
 #pragma unroll
       for (int i = 0; i < B; ++i) {
         const int32_t s = s0 + 4 * (i0 + i);
-        page[i] = s < q.n ? page_of(a, q, s) : -2;
+        page[i] = s < s_end ? page_of(a, q, s) : -2;
       }
 #pragma unroll
       for (int i = 0; i < B; ++i) {
@@ -216,14 +222,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
         const float m4[4] = {m[i].x, m[i].y, m[i].z, m[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          key[4 * (i0 + i) + e] = s + e >= q.n ? 0u : page[i] < 0 ? 1u : order_of(a, recent, p4[e], m4[e]);
+          key[4 * (i0 + i) + e] = s + e >= s_end ? 0u : page[i] < 0 ? 1u : order_of(a, recent, p4[e], m4[e]);
         if (page[i] == -1) atomicOr(a.status, kStatusBounds);
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-      const int32_t s = s0 + i, page = s < q.n ? page_of(a, q, s) : -2;
+      const int32_t s = s0 + i, page = s < s_end ? page_of(a, q, s) : -2;
       key[i] = page == -2 ? 0u : 1u;
       if (page >= 0) {
         const int64_t at = stat_at(a, q, page, s);
@@ -236,14 +242,59 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
   Counter<CL> count{warp_sum, cta_sum, rank, ranks, 0};
   // ---- the keep-th largest order value
   uint32_t cut = 0u;
-  for (int bit = 31; bit >= 0; --bit) {
+  int32_t reach = q.n, above = 0;  // keys from cut up, and from the end of its range (cut + 2^(bit + 1)) up
+  int bit = 31;
+  for (; bit >= 0; --bit) {
+    if (!CL && reach - above <= kGather && bit >= 3) break;
     const uint32_t cand = cut | (1u << bit);
     int32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) c += key[i] >= cand ? 1 : 0;
+    for (int i = 0; i < KPT; i += 4) {
+      if (i < share)  // (uniform)
+        c += (key[i] >= cand ? 1 : 0) + (key[i + 1] >= cand ? 1 : 0) + (key[i + 2] >= cand ? 1 : 0) +
+             (key[i + 3] >= cand ? 1 : 0);
+    }
     c = count.total(c);
-    if (c >= q.keep) cut = cand;
-    if (c == q.keep) break;  // exactly the keys from cand up: no lower bit can matter
+    if (c >= q.keep) {
+      cut = cand;
+      reach = c;
+    } else {
+      above = c;
+    }
+    if (c == q.keep) {  // exactly the keys from cand up: no lower bit can matter
+      bit = -1;
+      break;
+    }
+  }
+  if constexpr (!CL) {
+    if (bit >= 0) {
+      // the few keys of the range, two a thread
+      const uint32_t top = bit == 31 ? 0xFFFFFFFFu : cut + ((1u << (bit + 1)) - 1u);  // the range's last
+      int32_t mine = 0;
+#pragma unroll
+      for (int i = 0; i < KPT; ++i) mine += key[i] >= cut && key[i] <= top && key[i] != 0u ? 1 : 0;
+      int2 all;
+      int32_t at = count.before(mine, 0, &all).x;
+#pragma unroll
+      for (int i = 0; i < KPT; ++i)
+        if (key[i] >= cut && key[i] <= top && key[i] != 0u) list[at++] = (int32_t)key[i];
+      __syncthreads();
+      uint32_t few[kGather / kSelThreads];
+#pragma unroll
+      for (int i = 0; i < kGather / kSelThreads; ++i) {
+        const int32_t x = tid + i * kSelThreads;
+        few[i] = x < all.x ? (uint32_t)list[x] : 0u;
+      }
+      for (; bit >= 0; --bit) {
+        const uint32_t cand = cut | (1u << bit);
+        int32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < kGather / kSelThreads; ++i) c += few[i] >= cand ? 1 : 0;
+        c = above + count.total(c);
+        if (c >= q.keep) cut = cand;
+        if (c == q.keep) break;
+      }
+    }
   }
   // ---- kept slots: above the cut, and the lowest of those at it
   uint32_t kept = 0u, tie = 0u;
@@ -259,7 +310,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
     tie &= tie - 1u;
   }
   // ---- movers (kept, at or past the new length) and holes (not kept, below it)
-  const int32_t low = min(max(q.keep - s0, 0), KPT);  // this thread's slots below the new length
+  const int32_t low = min(max(q.keep - s0, 0), max(s_end - s0, 0));  // this thread's slots below the new length
   const uint32_t mask = low >= 32 ? 0xFFFFFFFFu : (1u << low) - 1u;
   uint32_t mover = kept & ~mask, hole = ~kept & mask;
   const int2 at = count.before(__popc(mover), __popc(hole), &all);
