@@ -50,8 +50,9 @@ enum {
   PG_KV_ERR_FRONTIER = -106,  /* a request's families disagree on the frontier, or a family
                                  holds other than the pages its frontier accounts for        */
   PG_KV_ERR_CAPACITY = -107,  /* a caller buffer is too small                                */
-  PG_KV_ERR_PENDING = -108    /* admit with a step already pending, or commit / abort / plan
-                                 inputs with no step pending                                 */
+  PG_KV_ERR_PENDING = -108,   /* admit with a step already pending, commit / abort / plan
+                                 inputs with no step pending, or an eviction with one pending */
+  PG_KV_ERR_EVICTED = -109    /* linear plan inputs asked for a request with evicted keys     */
 };
 
 enum { PG_KV_LOCAL = 0, PG_KV_GLOBAL = 1 };  /* the two families: hd256 local, hd512 global */
@@ -139,6 +140,25 @@ int pg_kv_batch_plan_inputs(pg_kv_server_t srv, int32_t family, int32_t n,
                             const int64_t* request_ids, const int32_t* step_tokens,
                             int64_t* kv_page_indptr, int32_t* page_ids, int32_t cap,
                             int32_t* last_page_len, int64_t* start_pos, int32_t* n_page_ids);
+
+/* Shorten a request's global family to `keep` keys (0 <= keep <= the keys it holds:
+ * PG_KV_ERR_ARG otherwise), after pg_kv_evict_select and pg_kv_evict_apply have put the kept keys
+ * into slots [0, keep) in every layer: the pages past ceil(keep / page_size) return to the pool.
+ * Positions go on counting: the frontier does not move, and the request's next global plan is a
+ * segment plan whose kv_start is the number of keys evicted so far (pg_kv_batch_segment_inputs).
+ * The pages may be issued again at once, so the call is made when the launches that read them are
+ * on the stream that later writes use. No step may be pending (PG_KV_ERR_PENDING). The local family
+ * is bounded by its window, not by eviction. */
+int pg_kv_request_evict(pg_kv_server_t srv, int64_t request_id, int32_t keep);
+
+/* pg_kv_batch_plan_inputs for pg_plan_paged_segment, global family: also kv_start [n], the keys of
+ * each request evicted so far (0: none), with which page_ids and last_page_len hold positions
+ * [kv_start, frontier + step). Arguments and errors otherwise as pg_kv_batch_plan_inputs, which
+ * fails with PG_KV_ERR_EVICTED for a request whose global keys were evicted. */
+int pg_kv_batch_segment_inputs(pg_kv_server_t srv, int32_t n, const int64_t* request_ids,
+                               const int32_t* step_tokens, int64_t* kv_page_indptr,
+                               int32_t* page_ids, int32_t cap, int32_t* last_page_len,
+                               int64_t* kv_start, int64_t* start_pos, int32_t* n_page_ids);
 
 #ifdef __cplusplus
 }

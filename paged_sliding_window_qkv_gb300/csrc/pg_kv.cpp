@@ -21,6 +21,7 @@ struct KvRequest {
   std::vector<int32_t> pages[2];    // page ids in position order, per family (pending included)
   int32_t pending = 0;              // tokens of the admitted, not yet committed step (0: none)
   int32_t pending_new[2] = {0, 0};  // pages that step took, per family (the tail of pages[f])
+  int32_t evicted = 0;              // keys of the global family given up (its slots start there)
 };
 
 int32_t pages_for(int64_t len, int32_t ps) { return (int32_t)((len + ps - 1) / ps); }
@@ -55,10 +56,10 @@ struct pg_kv_server {
   void give_back(int family, const std::vector<int32_t>& pages) {
     free_pages[family].insert(pages.begin(), pages.end());
   }
-  // Pages a family holds at a frontier: ceil(frontier / page_size), capped at the ring for
-  // the local family in ring mode.
-  int32_t held_for(int family, int64_t frontier) const {
-    const int32_t n = pages_for(frontier, page_size);
+  // Pages a family of request r holds at a frontier: ceil(frontier / page_size), capped at the ring
+  // for the local family in ring mode, without the evicted keys for the global family.
+  int32_t held_for(const KvRequest& r, int family, int64_t frontier) const {
+    const int32_t n = pages_for(frontier - (family == PG_KV_GLOBAL ? r.evicted : 0), page_size);
     return (family == PG_KV_LOCAL && ring_pages > 0 && n > ring_pages) ? ring_pages : n;
   }
   // The frontier account: both families at one frontier, each holding exactly the pages of
@@ -66,7 +67,7 @@ struct pg_kv_server {
   bool consistent(const KvRequest& r) const {
     if (r.frontier[0] != r.frontier[1] || r.pending < 0) return false;
     for (int f = 0; f < 2; ++f) {
-      if ((int64_t)r.pages[f].size() != held_for(f, (int64_t)r.frontier[f] + r.pending)) return false;
+      if ((int64_t)r.pages[f].size() != held_for(r, f, (int64_t)r.frontier[f] + r.pending)) return false;
       if (r.pending_new[f] < 0 || r.pending_new[f] > (int32_t)r.pages[f].size()) return false;
     }
     return true;
@@ -141,7 +142,7 @@ int pg_kv_admit_step(pg_kv_server_t srv, int64_t request_id, int32_t n_tokens) {
   if (srv->ring_pages > 0 && n_tokens > srv->ring_max_step) return PG_KV_ERR_WINDOW;
   if (len > srv->rope_rows) return PG_KV_ERR_ROPE;
   int32_t need[2];
-  for (int f = 0; f < 2; ++f) need[f] = srv->held_for(f, len) - (int32_t)r.pages[f].size();
+  for (int f = 0; f < 2; ++f) need[f] = srv->held_for(r, f, len) - (int32_t)r.pages[f].size();
   // reserve both before recording either; a refused side drops the other
   std::vector<int32_t> got[2];
   if (!srv->reserve(PG_KV_LOCAL, need[PG_KV_LOCAL], &got[PG_KV_LOCAL])) return PG_KV_ERR_NO_PAGES;
@@ -237,10 +238,14 @@ int pg_kv_inject_refusal(pg_kv_server_t srv, int32_t family, int32_t count) {
   return PG_KV_OK;
 }
 
-int pg_kv_batch_plan_inputs(pg_kv_server_t srv, int32_t family, int32_t n,
-                            const int64_t* request_ids, const int32_t* step_tokens,
-                            int64_t* kv_page_indptr, int32_t* page_ids, int32_t cap,
-                            int32_t* last_page_len, int64_t* start_pos, int32_t* n_page_ids) {
+}  // extern "C"
+
+namespace {
+
+// Plan inputs of a batch; kv_start null: linear plans, which evicted keys rule out.
+int batch_inputs(pg_kv_server_t srv, int32_t family, int32_t n, const int64_t* request_ids,
+                 const int32_t* step_tokens, int64_t* kv_page_indptr, int32_t* page_ids, int32_t cap,
+                 int32_t* last_page_len, int64_t* kv_start, int64_t* start_pos, int32_t* n_page_ids) {
   if (!srv || (family != PG_KV_LOCAL && family != PG_KV_GLOBAL) || n < 0 || cap < 0 ||
       !n_page_ids || !kv_page_indptr)
     return PG_KV_ERR_ARG;
@@ -256,6 +261,7 @@ int pg_kv_batch_plan_inputs(pg_kv_server_t srv, int32_t family, int32_t n,
     // the plan covers the request's admitted step, which must still be pending
     if (r.pending == 0) return PG_KV_ERR_PENDING;
     if (step_tokens[i] != r.pending) return PG_KV_ERR_ARG;
+    if (!kv_start && family == PG_KV_GLOBAL && r.evicted > 0) return PG_KV_ERR_EVICTED;
     total += (int64_t)r.pages[family].size();
   }
   if (total > cap) return PG_KV_ERR_CAPACITY;
@@ -268,12 +274,53 @@ int pg_kv_batch_plan_inputs(pg_kv_server_t srv, int32_t family, int32_t n,
     for (size_t k = 0; k < p.size(); ++k) page_ids[off + (int64_t)k] = p[k];
     off += (int64_t)p.size();
     kv_page_indptr[i + 1] = off;
+    const int32_t first = kv_start ? r.evicted : 0;
     // the step's last position's slot count in its page (a ring plan does not read it)
-    const int32_t end = r.frontier[family] + r.pending;
+    const int32_t end = r.frontier[family] + r.pending - first;
     last_page_len[i] = end - ((end - 1) / srv->page_size) * srv->page_size;
     start_pos[i] = (int64_t)r.frontier[family];
+    if (kv_start) kv_start[i] = first;
   }
   *n_page_ids = (int32_t)total;
+  return PG_KV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pg_kv_batch_plan_inputs(pg_kv_server_t srv, int32_t family, int32_t n,
+                            const int64_t* request_ids, const int32_t* step_tokens,
+                            int64_t* kv_page_indptr, int32_t* page_ids, int32_t cap,
+                            int32_t* last_page_len, int64_t* start_pos, int32_t* n_page_ids) {
+  return batch_inputs(srv, family, n, request_ids, step_tokens, kv_page_indptr, page_ids, cap,
+                      last_page_len, nullptr, start_pos, n_page_ids);
+}
+
+int pg_kv_batch_segment_inputs(pg_kv_server_t srv, int32_t n, const int64_t* request_ids,
+                               const int32_t* step_tokens, int64_t* kv_page_indptr,
+                               int32_t* page_ids, int32_t cap, int32_t* last_page_len,
+                               int64_t* kv_start, int64_t* start_pos, int32_t* n_page_ids) {
+  if (n > 0 && !kv_start) return PG_KV_ERR_ARG;
+  int64_t none = 0;  // a place for an empty batch
+  return batch_inputs(srv, PG_KV_GLOBAL, n, request_ids, step_tokens, kv_page_indptr, page_ids, cap,
+                      last_page_len, kv_start ? kv_start : &none, start_pos, n_page_ids);
+}
+
+int pg_kv_request_evict(pg_kv_server_t srv, int64_t request_id, int32_t keep) {
+  if (!srv || keep < 0) return PG_KV_ERR_ARG;
+  auto it = srv->requests.find(request_id);
+  if (it == srv->requests.end()) return PG_KV_ERR_FOREIGN;
+  KvRequest& r = it->second;
+  if (r.pending != 0) return PG_KV_ERR_PENDING;
+  if (!srv->consistent(r)) return PG_KV_ERR_FRONTIER;
+  const int32_t held = r.frontier[PG_KV_GLOBAL] - r.evicted;
+  if (keep > held) return PG_KV_ERR_ARG;
+  std::vector<int32_t>& p = r.pages[PG_KV_GLOBAL];
+  const size_t pages = (size_t)pages_for(keep, srv->page_size);
+  srv->free_pages[PG_KV_GLOBAL].insert(p.begin() + (std::ptrdiff_t)pages, p.end());
+  p.resize(pages);
+  r.evicted += held - keep;
   return PG_KV_OK;
 }
 

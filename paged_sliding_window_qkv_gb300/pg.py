@@ -413,6 +413,7 @@ PG_KV_ERR_FOREIGN = -105
 PG_KV_ERR_FRONTIER = -106
 PG_KV_ERR_CAPACITY = -107
 PG_KV_ERR_PENDING = -108
+PG_KV_ERR_EVICTED = -109
 PG_KV_LOCAL = 0
 PG_KV_GLOBAL = 1
 
@@ -540,7 +541,39 @@ def pg_kv_batch_plan_inputs(srv, family, request_ids, step_tokens, cap=1 << 20):
     return rc, indptr, pages[:cnt.value].copy(), last[:n].copy(), start[:n].copy()
 
 
-EXPORTED += ["pg_kv_server_create", "pg_kv_server_create_ring", "pg_kv_server_destroy", "pg_kv_request_open",
+_lib.pg_kv_request_evict.argtypes = [C.c_void_p, C.c_int64, C.c_int32]
+_lib.pg_kv_batch_segment_inputs.argtypes = [C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                            C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p,
+                                            C.c_void_p, C.c_void_p, _I32P]
+
+
+def pg_kv_request_evict(srv, request_id, keep) -> int:
+    """Shorten a request's global family to keep keys; its surplus pages return to the pool."""
+    return _lib.pg_kv_request_evict(srv, int(request_id), int(keep))
+
+
+def pg_kv_batch_segment_inputs(srv, request_ids, step_tokens, cap=1 << 20):
+    """Returns (status, kv_page_indptr, page_ids, last_page_len, kv_start, start_pos) as numpy
+    arrays in pg_plan_paged_segment's layout (global family)."""
+    rids = np.ascontiguousarray(request_ids, np.int64)
+    steps = np.ascontiguousarray(step_tokens, np.int32)
+    n = len(rids)
+    indptr = np.zeros(n + 1, np.int64)
+    pages = np.empty(max(cap, 1), np.int32)
+    last = np.zeros(max(n, 1), np.int32)
+    first = np.zeros(max(n, 1), np.int64)
+    start = np.zeros(max(n, 1), np.int64)
+    cnt = C.c_int32()
+    rc = _lib.pg_kv_batch_segment_inputs(srv, n, rids.ctypes.data, steps.ctypes.data,
+                                         indptr.ctypes.data, pages.ctypes.data, int(cap),
+                                         last.ctypes.data, first.ctypes.data, start.ctypes.data,
+                                         C.byref(cnt))
+    if rc != PG_KV_OK:
+        return rc, None, None, None, None, None
+    return rc, indptr, pages[:cnt.value].copy(), last[:n].copy(), first[:n].copy(), start[:n].copy()
+
+
+EXPORTED += ["pg_kv_request_evict", "pg_kv_batch_segment_inputs", "pg_kv_server_create", "pg_kv_server_create_ring", "pg_kv_server_destroy", "pg_kv_request_open",
              "pg_kv_request_close", "pg_kv_admit_step", "pg_kv_commit_step", "pg_kv_abort_step",
              "pg_kv_request_pending", "pg_kv_request_info", "pg_kv_request_pages",
              "pg_kv_free_pages", "pg_kv_inject_refusal", "pg_kv_batch_plan_inputs"]
