@@ -333,7 +333,8 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  *
  * They take plans of pg_plan_paged_prefill and pg_plan_paged_segment (PG_ERR_PLAN_MISMATCH for a
  * ring plan: its slots forget the positions these keep), and the plan's own device must be
- * current (PG_ERR_STREAM otherwise).
+ * current (PG_ERR_STREAM otherwise). A captured call follows a plan that is updated in place with
+ * as many requests, tokens and pages as it was captured with.
  *
  * After an eviction the cache's slots no longer count positions. The request's next plan is a
  * segment plan with kv_start = the number of its keys evicted so far: position p of a new token

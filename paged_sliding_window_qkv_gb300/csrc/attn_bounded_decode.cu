@@ -632,8 +632,9 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           if (m > ref[x] + kRescale) {
             const float r2 = m + kHeadroom;
             if (ref[x] != -INFINITY) {
-              al[x] = ex2(ref[x] - r2);
-              l[x] *= al[x];
+              // the root of the factor, applied twice: the step may pass 2^-126 (attn_tc.cu)
+              al[x] = ex2(0.5f * (ref[x] - r2));
+              l[x] = (l[x] * al[x]) * al[x];
               scaled = true;
             }
             ref[x] = r2;
@@ -651,7 +652,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
               tmem_ld16(at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < NQ; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * al[x]);
+              for (int x = 0; x < NQ; ++x) o[x] = __float_as_uint((__uint_as_float(o[x]) * al[x]) * al[x]);
               tmem_st16(at, o);
             }
             tmem_wait_st();
@@ -675,6 +676,13 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // V rows of keys that are not visible: zero once the copies have landed. The tile's V slots
         // follow K(i + 1) in the ring (K(0), K(1), V(0), ...; the last tile's follow V(i - 1))
         const int32_t before = PARTS * ((h.flags & kEnd) ? 2 * i + 1 : 2 * i + 2);
+        // A parity wait tells a slot's phases apart only once the use before has been consumed: the
+        // slots hold K(i + 1) and V(i - 1) before V(i), the last tile's V(i - 1) alone. Scores of tile
+        // i + 1 are complete after both (the MMAs run in order), PV of tile i - 1 after the latter.
+        if (!(h.flags & kEnd))
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(SFULL + 8 * (b ^ 1), ((i + 1) >> 1) & 1, wc));
+        else if (i > 0)
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(PVDONE + 8 * (b ^ 1), ((i - 1) >> 1) & 1, wc));
 #pragma unroll 1
         for (int p = 0; p < PARTS; ++p) {
           const int32_t at = before + p, sl = at % NS;

@@ -191,6 +191,15 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
   u.ntiles = hi > u.kb0 ? (hi - u.kb0 + kBN - 1) / kBN : 0;
   return u;
 }
+// The factor 2^e that moves sums from one reference to another, to be applied with moved(). A
+// reference may be left by up to 2^48 and set 2^64 above the next maximum, so a step can pass
+// 2^-126 while the sums it moves still count (a third tile 2^63 above the first's reference and
+// 2^17 above the second's): BC applies the root of the factor twice, which loses nothing.
+template <bool BC>
+__device__ __forceinline__ float move_factor(float e) { return ex2(BC ? 0.5f * e : e); }
+template <bool BC>
+__device__ __forceinline__ float moved(float x, float f) { return BC ? (x * f) * f : x * f; }
+
 // BC: the keys of a tile that a row sees: below hi, and from lo on or below sink (all relative to
 // the tile's first key).
 __device__ __forceinline__ uint64_t tile_bits(int32_t hi, int32_t lo, int32_t sink) {
@@ -800,7 +809,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           __syncwarp();
           if (lane == 0) mbar_arrive(PAIRX + 8 * ((JJ & 1) * 4 + quarter));
           if (m_mine != m_new) {
-            if (m_mine != -INFINITY) l *= ex2(m_mine - m_new);
+            if (m_mine != -INFINITY) l = moved<BC>(l, move_factor<BC>(m_mine - m_new));
             m_mine = m_new;
           }
           const float mu = m_new == -INFINITY ? 0.f : m_new;
@@ -837,7 +846,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const bool resc = m_prev != -INFINITY && m_new != m_prev;
           if (__any_sync(0xffffffffu, resc)) {
             // O holds PV(0 .. JJ - 1) at the old reference: rescale all its columns before PV(JJ)
-            const float alpha = resc ? ex2(m_prev - m_new) : 1.f;
+            const float alpha = resc ? move_factor<BC>(m_prev - m_new) : 1.f;
             const int32_t jp = JJ - 1;
             if (!__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jp % NSB), (jp / NSB) & 1, wc))) { ok = false; break; }
             tc_fence_after();
@@ -847,7 +856,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               tmem_ld32(tl + col, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(moved<BC>(__uint_as_float(o[e]), alpha));
               tmem_st32(tl + col, o);
             }
             tmem_wait_st();
@@ -868,7 +877,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               m_fin = hm[(jl & 1) * kM + row];
           }
           if (ok && m_fin != m_mine) {
-            if (m_mine != -INFINITY) l *= ex2(m_mine - m_fin);
+            if (m_mine != -INFINITY) l = moved<BC>(l, move_factor<BC>(m_mine - m_fin));
             m_mine = m_fin;
           }
         }
@@ -935,9 +944,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (mx > m_ref + kRescaleLog2) {
           // new reference with headroom above this maximum, so later growth rarely rescales
           const float m_new = mx + kHeadroomLog2;
-          alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
+          alpha = m_ref == -INFINITY ? 0.f : move_factor<BC>(m_ref - m_new);
           resc = m_ref != -INFINITY;
-          l *= alpha;
+          l = moved<BC>(l, alpha);
           m_ref = m_new;
         }
         if (j > 0 && __any_sync(0xffffffffu, resc)) {
@@ -950,7 +959,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tmem_ld32(tl + col, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(moved<BC>(__uint_as_float(o[e]), alpha));
             tmem_st32(tl + col, o);
           }
           tmem_wait_st();

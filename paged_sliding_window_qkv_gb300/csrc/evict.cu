@@ -51,10 +51,10 @@ __device__ __forceinline__ int64_t stat_at(const EvictArgs& a, const Seg& q, int
   return (int64_t)q.layer * a.stats.stride_layer +
          ((int64_t)page * a.pool.num_kv_heads + q.g) * a.pool.page_size + page_offset(a, slot);
 }
-// First protected position of the segment's last ones (past every position when none is).
+// First protected position of the segment's last ones.
 __device__ __forceinline__ int64_t recent_from(const EvictArgs& a, const Seg& q) {
   const int32_t end = a.plan.start_pos[q.r] + (a.plan.qo_indptr[q.r + 1] - a.plan.qo_indptr[q.r]);
-  return a.num_recent > 0 ? (int64_t)end - a.num_recent : INT64_MAX;
+  return (int64_t)end - a.num_recent;
 }
 // Order of a key as an unsigned number, larger kept first: protected positions above every mass,
 // NaN as -inf, -0 as +0. 0 is no key, 1 a key on a page that is out of range.

@@ -342,7 +342,7 @@ _evict_apply = _sig("pg_kv_evict_apply", C.c_int, _P, C.POINTER(pg_pool_t),
                     C.POINTER(pg_kv_stats_t), _I32, _I32, _I32, _P, _P)
 
 
-def stats_descriptor(mass, pos, **override) -> pg_kv_stats_t:
+def stats_descriptor(mass, pos, /, **override) -> pg_kv_stats_t:
     """pg_kv_stats_t for a torch float32 (mass) and int32 (pos) tensor, each dense
     [L, P, Hkv, ps]."""
     if mass.shape != pos.shape or not (mass.is_contiguous() and pos.is_contiguous()):
