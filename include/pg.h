@@ -349,8 +349,9 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  *   window_left < 0  or  p - j <= window_left  or  j < num_sink.
  * Positions are absolute: on a segment plan the sinks are the segment's keys below num_sink, so
  * disjoint segments still merge with pg_merge_attn_states. num_sink 0 is the windowed attention;
- * window_left -1 sees everything. Pages none of whose keys a query of its tile sees are not read
- * (head_dim 256 decode: 16 keys a tile; other decode 32; prefill 64).
+ * window_left -1 sees everything. A page none of whose keys any query of the call sees is not
+ * read: its place in the plan's page list may hold any page id of the pool, so a server can give
+ * the pages between the sinks and the window away.
  *   lse  [T][Hq] float32 or NULL: natural-log normaliser of the row's fp32 scores (-inf, with
  *        out 0, for a row that sees no key)
  * The row sum adds the fp32 weights (the entries above sum the bf16-rounded ones), so out and

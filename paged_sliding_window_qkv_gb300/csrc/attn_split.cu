@@ -20,7 +20,7 @@
 // (the key walk of bounded.cuh, tiles aligned from the first key held), the row sum adds the
 // unrounded fp32 weights, so lse is that of the fp32 scores, and a decode step's scores are kept
 // for the caller when it accumulates attention weights. The bf16 rounding of the weights that
-// multiply V (half a step, 2^-9 of each) then reaches the output instead of cancelling against
+// multiply V (half a step, 2^-8 of each) then reaches the output instead of cancelling against
 // a rounded sum; it is as large as the rounding of the output itself.
 #include "bounded.cuh"
 #include "pg_internal.h"

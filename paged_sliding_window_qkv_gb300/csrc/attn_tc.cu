@@ -148,9 +148,18 @@ struct TcUnit {
   // keys held: positions [kv_start, kv_len); key tiles start kb0 + 64 t, 64-aligned from kv_start
   int32_t kvp0, kvp1, kv_len, kv_start, sp, kb0, ntiles, g, dh;
   int32_t ns;  // BC: the first ns tiles are sink tiles, aligned from kv_start
+  int32_t lo, sink;  // BC: some row of the pair sees keys [lo, ...) and those below sink
   template <bool BC>
   __device__ __forceinline__ int32_t key(int32_t t) const {  // first key of the t-th tile
     return BC && t < ns ? kv_start + t * kBN : kb0 + (BC ? t - ns : t) * kBN;
+  }
+  // First key of the page box that stands at key ks of the t-th tile. BC: a box between the sinks
+  // and the window, which no row sees, is not read (its page may be someone else's by now): the
+  // nearest box with a visible key stands in for it, as finite as what the rows see anyway.
+  template <bool BC>
+  __device__ __forceinline__ int32_t box_key(int32_t t, int32_t ks, int32_t rows) const {
+    if (!BC || ks + rows > lo || ks < sink) return ks;
+    return kv_start + (((t < ns ? sink - 1 : lo) - kv_start) & ~(rows - 1));
   }
 };
 template <bool BC>
@@ -180,6 +189,8 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
   if constexpr (BC) {
     const KeyWalk k = key_walk(W, a.num_sink, u.kv_start, u.kv_len, p_first, p_last, kBN);
     u.ns = k.ns;
+    u.lo = k.lo;
+    u.sink = W >= 0 ? min(a.num_sink, k.hi) : u.kv_start;
     u.kb0 = u.kv_start + k.ft * kBN;
     u.ntiles = k.total;
     return u;
@@ -394,14 +405,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       auto lookup = [&](int32_t t0) -> int32_t {  // page id of this lane's box in the batch at t0
         const int32_t tt = t0 + my_t;
         if (tt >= u.ntiles) return -1;
-        const int32_t ks = u.key<BC>(tt) + key_off + my_b * BR;
+        const int32_t ks = u.template box_key<BC>(tt, u.template key<BC>(tt) + key_off + my_b * BR, BR);
         if (ks >= u.kv_len) return -1;
         const int32_t lp = (ks - u.kv_start) / ps;  // logical page; a ring wraps it over its pages
         const int32_t pidx = u.kvp0 + (pl.ring ? lp % max(u.kvp1 - u.kvp0, 1) : lp);
         return (pidx < u.kvp1 && pidx < pl.num_page_ids) ? pl.page_ids[pidx] : a.num_pages;
       };
       int32_t pg_next = lookup(0);
-      int32_t my_page = -1, my_row = 0;
+      int32_t my_page = -1, my_row = 0, my_ks = 0;
       uint32_t bm_load = 0u, bm_fix = 0u;
       const uint32_t box_mask = nbox >= 32 ? 0xffffffffu : ((1u << nbox) - 1u);
       const uint32_t box_bytes = (uint32_t)BR * row_bytes;
@@ -416,7 +427,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           my_page = pg_next;
           pg_next = lookup(t + TB);  // used TB tiles from now
           const int32_t tt = t + my_t;
-          const int32_t ks = u.key<BC>(tt) + key_off + my_b * BR;
+          const int32_t ks = u.template box_key<BC>(tt, u.template key<BC>(tt) + key_off + my_b * BR, BR);
+          my_ks = ks;
           const bool live = tt < u.ntiles;
           const bool past = !live || ks >= u.kv_len;
           const bool bad = !past && (my_page < 0 || my_page >= a.num_pages);
@@ -494,11 +506,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               fix_phase ^= 1u;
             }
             // zero this warp's rows that must not be read: keys past kv_len, keys on bad pages
-            const int32_t kb = u.key<BC>(t) + key_off;  // first key of this CTA's half
+            const int32_t kb = u.template key<BC>(t) + key_off;  // first key of this CTA's half
             for (int b = 0; b < nbox; ++b) {
               const int32_t pb = __shfl_sync(0xffffffffu, my_page, sh + b);
+              const int32_t k0 = BC ? __shfl_sync(0xffffffffu, my_ks, sh + b) : kb + b * BR;
               for (int rr = 0; rr < BR; ++rr) {
-                const int32_t key = kb + b * BR + rr;
+                const int32_t key = k0 + rr;
                 if (key < u.kv_len && pb >= 0 && pb < a.num_pages) continue;
                 const int c = lane >> 3, w16 = lane & 7;  // chunk c, 16-byte piece w16 of a 128-B row
                 const int kt = b * BR + rr;  // key within this CTA's half

@@ -517,3 +517,29 @@ def test_a_serving_loop_that_evicts():
             assert set(range(front[rid] - 16, front[rid])) <= seen
     plan.close()
     pg.pg_kv_server_destroy(srv)
+
+
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("ps", [8, 16, 32, 64, 3])
+@pytest.mark.parametrize("window,sinks", [(100, 4), (65, 70), (3, 1), (40, 0)])
+def test_pages_behind_the_window_may_be_given_away(D, ps, window, sinks):
+    """Places of pages that no query sees all name one page that holds NaN and that another request
+    owns; the outputs are those of the full page list."""
+    for qo, start in (([40, 3, 200], [700, 300, 450]), ([1, 1, 1], [700, 301, 64])):
+        c = Case(D, *HQ[D], qo, start, ps=ps, seed=window + ps)
+        foreign = int(np.setdiff1d(np.arange(c.P), c.ids)[0])
+        c.pool_cpu[0, foreign] = float("nan")
+        full = c.ids.copy()
+        for r in range(len(qo)):
+            for i in range(c.pg_indptr[r + 1] - c.pg_indptr[r]):
+                last = (i + 1) * ps - 1  # the page's last key
+                if last < start[r] - window and i * ps >= sinks:
+                    c.ids[c.pg_indptr[r] + i] = foreign
+        assert (c.ids == foreign).sum() > 1
+        c.build()
+        c.sink(window, sinks)
+        ok()
+        c.ids = full
+        c.reference(window, sinks)
+        c.check_attention(f"{qo}")
+        c.close()
