@@ -235,11 +235,13 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       *reinterpret_cast<uint4*>(gb + C::OFF_Q + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
   }
-  // everything below reads or writes memory that earlier work of the stream may still use
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (the producer finds its tiles while the others set up)
+  // The producers find their tiles while the others set up, and (launched programmatically) while
+  // the stream's previous kernel ends: a plan's metadata is written by copies alone, which no
+  // programmatic launch overtakes. Everything else waits for that kernel.
   int32_t n = 0, r = 0;
   int64_t in_req = 0;
+  constexpr int kHeld = 4;
+  int64_t held[kHeld] = {0, 0, 0, 0};  // inclusive sums of the first requests' tiles
   if (warp == 0 || warp == 6) {
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_kv) : "memory");
@@ -247,10 +249,8 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
     const int32_t R = a.plan.num_req;
     const int64_t S = gridDim.x, s = blockIdx.x;
-    // Tiles of every request (all heads) in scans of 32 requests: the total, (CTA 0) the prefix for
-    // the join, and the request that holds the CTA's first tile. The first scans' counts are
-    // loaded together and kept.
-    constexpr int kHeld = 4;
+    // Tiles of every request (all heads) in scans of 32 requests: the total, and the request that
+    // holds the CTA's first tile. The first scans' counts are loaded together and kept.
     auto tiles_of = [&](int32_t r) -> int64_t { return r < R ? (int64_t)req_tiles(args, r).total * Hkv : 0; };
     auto scan = [&](int64_t v) {
 #pragma unroll
@@ -260,34 +260,38 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
       return v;
     };
-    int64_t held[kHeld];
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) held[j] = tiles_of(32 * j + lane);
     int64_t U = 0;
     for (int32_t c = 0; c < R; c += 32) {
       const int j = c / 32;
       const int64_t v = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : j == 3 ? held[3] : tiles_of(c + lane);
-      const int64_t incl = scan(v);
-      if (s == 0 && warp == 0 && c + lane < R) args.prefix[c + lane] = U + incl - v;
-      U += __shfl_sync(0xffffffffu, incl, 31);
+      const int64_t incl = U + scan(v);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (k == j) held[k] = incl;
+      U = __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (s == 0 && threadIdx.x == 0) args.prefix[R] = U;
     const int64_t u0 = s * U / S, u1 = (s + 1) * U / S;
     n = (int32_t)(u1 - u0);
     if (n > 0) {
-      int64_t run = 0;
+      int64_t run = 0;  // tiles before request c
       for (int32_t c = 0; c < R; c += 32) {
         const int j = c / 32;
-        const int64_t v = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : j == 3 ? held[3] : tiles_of(c + lane);
-        const int64_t incl = scan(v);
-        const uint32_t past = __ballot_sync(0xffffffffu, run + incl > u0);
+        const int64_t incl = j == 0   ? held[0]
+                             : j == 1 ? held[1]
+                             : j == 2 ? held[2]
+                             : j == 3 ? held[3]
+                                      : run + scan(tiles_of(c + lane));
+        const uint32_t past = __ballot_sync(0xffffffffu, incl > u0);
         if (past) {
           const int f = __ffs(past) - 1;
           r = c + f;
-          in_req = u0 - run - __shfl_sync(0xffffffffu, incl - v, f);
+          const int64_t before = __shfl_up_sync(0xffffffffu, incl, 1);
+          in_req = u0 - __shfl_sync(0xffffffffu, lane == 0 ? run : before, f);
           break;
         }
-        run += __shfl_sync(0xffffffffu, incl, 31);
+        run = __shfl_sync(0xffffffffu, incl, 31);
       }
     }
   }
@@ -307,8 +311,35 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     // Both walk the tiles; warp 0 issues K, the queries and the headers, warp 6 issues V. (One warp
     // for both took some 5 us a tile at head_dim 512 without any copy in it: the copies' issue.)
     const bool is_v = warp == 6;
+    // the prefix for the join (CTA 0), once the stream's previous kernel, which may read the last one
+    // in the same workspace, has ended
+    auto write_prefix = [&]() {
+      if (blockIdx.x != 0 || is_v) return;
+      const int32_t R = a.plan.num_req;
+      int64_t run = 0;
+      for (int32_t c = 0; c < R; c += 32) {
+        const int j = c / 32;
+        int64_t incl;
+        if (j < kHeld) {
+          incl = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : held[3];
+        } else {
+          incl = c + lane < R ? (int64_t)req_tiles(args, c + lane).total * Hkv : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+          }
+          incl += run;
+        }
+        if (c + lane < R) args.prefix[c + lane + 1] = incl;
+        run = __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (lane == 0) args.prefix[0] = 0;
+    };
     bool ok = true;
     if (n == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      write_prefix();
       if (lane == 0 && !is_v) {
         hdrs[0].flags = kEmpty | kEnd;
         mbar_arrive(HFULL);
@@ -376,6 +407,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         return true;
       };
       Tile cur = next(0);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       int32_t segs = 0;
       for (int32_t i = 0; ok && i < n; ++i) {
         const bool good = cur.live && cur.page >= 0 && cur.page < a.pool.num_pages;
@@ -426,6 +458,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const Tile t = cur;
         if (i + 1 < n) cur = next(i + 1);
         ok = load(t, good, i == 0 ? 0 : PARTS * (2 * i - 1));
+        if (i == 0) write_prefix();  // (behind the first copies)
       }
     }
     if (!ok) {
@@ -511,6 +544,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     commit1(DRAIN);
   } else {
     // ------------------------------------------------------------ softmax
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;  // the thread's key of each tile, and output column of 128
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -731,6 +765,9 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (pending && ok) epilogue();
   }
 
+  // the join's launch overlaps the last CTAs' ends (released earlier, its blocks would sit on the SMs
+  // while the copies stream: 236 against 222 us on 64 requests of 8001 keys with weights)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -783,9 +820,6 @@ __device__ __forceinline__ bool holds_tiles(const SegRecs& s, int32_t c, int64_t
 // Blocks from there on (weights): 256 keys of one request, two a thread, all heads. The scores and
 // page ids load while the normalisers are taken from the records (eight lanes per head), or from
 // lse where the segment was written directly.
-// (Launched without programmatic serialisation: blocks that wait on the SMs while the decode
-// kernel streams cost it more than their earlier start saves, 236 against 222 us on 64 requests
-// of 8001 keys at head_dim 512.)
 constexpr int kJoinThreads = 128;
 constexpr int kPer = 2;                         // keys of a thread
 constexpr int kJoinKeys = kPer * kJoinThreads;  // keys of a weight block
@@ -800,6 +834,7 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
   const AttnArgs& a = args.a;
   // (a following kernel launched programmatically may set up; it waits for this one)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t Hkv = a.pool.num_kv_heads, G = a.group, Hq = a.num_qo_heads, R = a.plan.num_req;
   const int64_t U = args.prefix[R];
   const int tid = threadIdx.x;
@@ -1052,10 +1087,13 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   auto join = [&](auto kernel, int32_t RG) {
     const unsigned grid =
         (unsigned)((int64_t)segs * join_parts(G, D, RG) + (int64_t)a.plan.num_req * key_blocks);
-    kernel<<<grid, kJoinThreads, weigh ? a.num_qo_heads * sizeof(float) : 0, stream>>>(b, S, std::max(key_blocks, 1));
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.dynamicSmemBytes = weigh ? a.num_qo_heads * sizeof(float) : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, b, S, std::max(key_blocks, 1));
   };
-  if (segs * 4 < S) join(bounded_join_kernel<D, 4>, 4);
-  else join(bounded_join_kernel<D, 1>, 1);
+  e = segs * 4 < S ? join(bounded_join_kernel<D, 4>, 4) : join(bounded_join_kernel<D, 1>, 1);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }
