@@ -151,6 +151,18 @@ int pg_kv_batch_plan_inputs(pg_kv_server_t srv, int32_t family, int32_t n,
  * is bounded by its window, not by eviction. */
 int pg_kv_request_evict(pg_kv_server_t srv, int64_t request_id, int32_t keep);
 
+/* Give away the pages of a request's local family that no later query sees: those whose positions
+ * are all at or past num_sink (>= 0) and before frontier - window_left. They return to the pool; the
+ * request's page list keeps its length, with -1 in their places (pg_kv_request_pages), and
+ * pg_kv_batch_plan_inputs fills those with the page of the step's last position, which
+ * pg_attn_paged_sink, with this window and at most these sinks, does not read there; the other
+ * attention calls may, and are not for a trimmed request. A request under a window and sinks so holds at most
+ * ceil(num_sink / page_size) + ceil((window_left + step) / page_size) + 1 pages at any length. *freed (may
+ * be NULL) receives the pages given away by this call. Not for ring servers (PG_KV_ERR_WINDOW),
+ * whose slots are reused in place; no step may be pending (PG_KV_ERR_PENDING). As with
+ * pg_kv_request_evict, the pages may be issued again at once. */
+int pg_kv_request_trim(pg_kv_server_t srv, int64_t request_id, int32_t num_sink, int32_t* freed);
+
 /* pg_kv_batch_plan_inputs for pg_plan_paged_segment, global family: also kv_start [n], the keys of
  * each request evicted so far (0: none), with which page_ids and last_page_len hold positions
  * [kv_start, frontier + step). Arguments and errors otherwise as pg_kv_batch_plan_inputs, which

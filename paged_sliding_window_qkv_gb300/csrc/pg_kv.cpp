@@ -54,7 +54,8 @@ struct pg_kv_server {
     return true;
   }
   void give_back(int family, const std::vector<int32_t>& pages) {
-    free_pages[family].insert(pages.begin(), pages.end());
+    for (const int32_t p : pages)
+      if (p >= 0) free_pages[family].insert(p);  // (-1: given away before)
   }
   // Pages a family of request r holds at a frontier: ceil(frontier / page_size), capped at the ring
   // for the local family in ring mode, without the evicted keys for the global family.
@@ -271,7 +272,8 @@ int batch_inputs(pg_kv_server_t srv, int32_t family, int32_t n, const int64_t* r
   for (int32_t i = 0; i < n; ++i) {
     const KvRequest& r = srv->requests.find(request_ids[i])->second;
     const std::vector<int32_t>& p = r.pages[family];
-    for (size_t k = 0; k < p.size(); ++k) page_ids[off + (int64_t)k] = p[k];
+    // (the last page holds the pending step's tail: it is never given away)
+    for (size_t k = 0; k < p.size(); ++k) page_ids[off + (int64_t)k] = p[k] >= 0 ? p[k] : p.back();
     off += (int64_t)p.size();
     kv_page_indptr[i + 1] = off;
     const int32_t first = kv_start ? r.evicted : 0;
@@ -305,6 +307,28 @@ int pg_kv_batch_segment_inputs(pg_kv_server_t srv, int32_t n, const int64_t* req
   int64_t none = 0;  // a place for an empty batch
   return batch_inputs(srv, PG_KV_GLOBAL, n, request_ids, step_tokens, kv_page_indptr, page_ids, cap,
                       last_page_len, kv_start ? kv_start : &none, start_pos, n_page_ids);
+}
+
+int pg_kv_request_trim(pg_kv_server_t srv, int64_t request_id, int32_t num_sink, int32_t* freed) {
+  if (!srv || num_sink < 0) return PG_KV_ERR_ARG;
+  auto it = srv->requests.find(request_id);
+  if (it == srv->requests.end()) return PG_KV_ERR_FOREIGN;
+  KvRequest& r = it->second;
+  if (srv->ring_pages > 0) return PG_KV_ERR_WINDOW;
+  if (r.pending != 0) return PG_KV_ERR_PENDING;
+  if (!srv->consistent(r)) return PG_KV_ERR_FRONTIER;
+  std::vector<int32_t>& p = r.pages[PG_KV_LOCAL];
+  const int64_t ps = srv->page_size;
+  const int64_t lo = (int64_t)r.frontier[PG_KV_LOCAL] - srv->window_left;  // the next query's window
+  int32_t n = 0;
+  for (int64_t k = (num_sink + ps - 1) / ps; (k + 1) * ps <= lo; ++k) {
+    if (p[(size_t)k] < 0) continue;
+    srv->free_pages[PG_KV_LOCAL].insert(p[(size_t)k]);
+    p[(size_t)k] = -1;
+    ++n;
+  }
+  if (freed) *freed = n;
+  return PG_KV_OK;
 }
 
 int pg_kv_request_evict(pg_kv_server_t srv, int64_t request_id, int32_t keep) {

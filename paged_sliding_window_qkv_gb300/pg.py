@@ -552,6 +552,16 @@ def pg_kv_request_evict(srv, request_id, keep) -> int:
     return _lib.pg_kv_request_evict(srv, int(request_id), int(keep))
 
 
+_lib.pg_kv_request_trim.argtypes = [C.c_void_p, C.c_int64, C.c_int32, _I32P]
+
+
+def pg_kv_request_trim(srv, request_id, num_sink):
+    """Give away the local pages that no later query sees. Returns (status, pages freed)."""
+    n = C.c_int32()
+    rc = _lib.pg_kv_request_trim(srv, int(request_id), int(num_sink), C.byref(n))
+    return rc, n.value
+
+
 def pg_kv_batch_segment_inputs(srv, request_ids, step_tokens, cap=1 << 20):
     """Returns (status, kv_page_indptr, page_ids, last_page_len, kv_start, start_pos) as numpy
     arrays in pg_plan_paged_segment's layout (global family)."""
@@ -573,7 +583,7 @@ def pg_kv_batch_segment_inputs(srv, request_ids, step_tokens, cap=1 << 20):
     return rc, indptr, pages[:cnt.value].copy(), last[:n].copy(), first[:n].copy(), start[:n].copy()
 
 
-EXPORTED += ["pg_kv_request_evict", "pg_kv_batch_segment_inputs", "pg_kv_server_create", "pg_kv_server_create_ring", "pg_kv_server_destroy", "pg_kv_request_open",
+EXPORTED += ["pg_kv_request_evict", "pg_kv_request_trim", "pg_kv_batch_segment_inputs", "pg_kv_server_create", "pg_kv_server_create_ring", "pg_kv_server_destroy", "pg_kv_request_open",
              "pg_kv_request_close", "pg_kv_admit_step", "pg_kv_commit_step", "pg_kv_abort_step",
              "pg_kv_request_pending", "pg_kv_request_info", "pg_kv_request_pages",
              "pg_kv_free_pages", "pg_kv_inject_refusal", "pg_kv_batch_plan_inputs"]

@@ -543,3 +543,78 @@ def test_pages_behind_the_window_may_be_given_away(D, ps, window, sinks):
         c.reference(window, sinks)
         c.check_attention(f"{qo}")
         c.close()
+
+
+def test_a_local_layer_served_from_a_few_pages():
+    """Window and sinks through the page allocator: two requests run to ten times the window from a
+    pool that holds a fifth of their keys, prefill chunks and single tokens; each step against the
+    full history. A request under this window and a step of 30 holds up to 1 + 9 + 1 pages, so two
+    do not always fit in 20: the second is then refused and served in the batch after."""
+    D, hq, hkv, ps, window, sinks = 256, 16, 8, 8, 40, 5
+    P = 20  # pages; 2 requests of 400 tokens are 100
+    rc, srv = pg.pg_kv_server_create(P, 1000, ps, window, 0, 1 << 16)
+    pg.check(rc)
+    ids = [pg.pg_kv_request_open(srv)[1] for _ in range(2)]
+    g = torch.Generator(device="cuda").manual_seed(9)
+    cos, sin = (torch.empty((1024, D // 2), device="cuda") for _ in range(2))
+    pg.check(pg.pg_rope_table(cos, sin, 1024, D, 1.0e4))
+    wq = torch.full((D,), 2.0 / np.sqrt(D), dtype=torch.bfloat16, device="cuda")
+    wk = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    pool = torch.full((1, P, 2, hkv, ps, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    desc = pg.pool_descriptor(pool)
+    hist = [torch.zeros((0, 2, hkv, D), dtype=torch.bfloat16) for _ in ids]
+    plan = None
+    steps = [[30, 17]] + [[1, 1]] * 12 + [[25, 1], [3, 30]] + [[1, 1]] * 20 + [[30, 30]] * 8 + [[1, 1]] * 9
+    refused = 0
+    for step, lens in enumerate(steps):
+        todo = [0, 1]
+        while todo:
+            now = []
+            for i in todo:
+                free = pg.pg_kv_free_pages(srv, pg.PG_KV_LOCAL)[1]
+                rc = pg.pg_kv_admit_step(srv, ids[i], lens[i])
+                if rc == pg.PG_KV_OK:
+                    now.append(i)
+                    continue
+                end = len(hist[i]) + lens[i]
+                assert rc == pg.PG_KV_ERR_NO_PAGES and -(-end // ps) - -(-len(hist[i]) // ps) > free
+                assert pg.pg_kv_free_pages(srv, pg.PG_KV_LOCAL)[1] == free
+                refused += 1
+            assert now
+            todo = [i for i in todo if i not in now]
+            rids, n_new = [ids[i] for i in now], [lens[i] for i in now]
+            rc, ptr, pages, last, start = pg.pg_kv_batch_plan_inputs(srv, pg.PG_KV_LOCAL, rids, n_new)
+            pg.check(rc)
+            qo = np.concatenate([[0], np.cumsum(n_new)])
+            rc, plan = pg.pg_plan_paged_prefill(plan, len(now), qo, ptr, pages, last, start, hq, hkv, D, ps)
+            pg.check(rc)
+            T = int(qo[-1])
+            q, k, v = (torch.randn((T, h, D), device="cuda", generator=g).to(torch.bfloat16)
+                       for h in (hq, hkv, hkv))
+            qr, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty((T, hq), device="cuda")
+            n = pg.pg_workspace_bytes(plan)
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+            pg.check(pg.pg_prep_paged_hd256(plan, desc, 0, q, hq * D, k, hkv * D, v, hkv * D, wq, wk, 1e-6,
+                                            cos, sin, 1024, qr))
+            pg.check(pg.pg_attn_paged_sink(plan, desc, 0, qr, out, lse, window, sinks, 1.0, ws, n))
+            ok()
+            for j, i in enumerate(now):
+                s = np.arange(start[j], start[j] + n_new[j])
+                page = torch.from_numpy(pages[ptr[j] + s // ps].astype(np.int64)).cuda()
+                new = pool[0].permute(0, 3, 1, 2, 4)[page, torch.from_numpy(s % ps).cuda()].cpu()
+                hist[i] = torch.cat([hist[i], new])
+            # the same rows over a full page list of the whole history
+            c = Case(D, hq, hkv, n_new, start, ps=ps, seed=step)
+            for j, i in enumerate(now):
+                page, off = c.rows_of(j)
+                c.pool_cpu[0].permute(0, 3, 1, 2, 4)[torch.as_tensor(page), torch.as_tensor(off)] = hist[i]
+            c.q_cpu, c.out, c.lse = qr.cpu(), out, lse
+            c.reference(window, sinks)
+            c.check_attention(f"step {step}")
+            for rid in rids:
+                pg.check(pg.pg_kv_commit_step(srv, rid))
+                pg.check(pg.pg_kv_request_trim(srv, rid, sinks)[0])
+    assert refused
+    assert min(len(h) for h in hist) > 300 and pg.pg_kv_free_pages(srv, pg.PG_KV_LOCAL)[1] > 0
+    plan.close()
+    pg.pg_kv_server_destroy(srv)

@@ -96,6 +96,50 @@ def test_evict_refusals_change_nothing():
     pg.pg_kv_server_destroy(s)
 
 
+@pytest.mark.parametrize("ps", [1, 4, 16])
+@pytest.mark.parametrize("sinks", [0, 3, 20])
+def test_trim_keeps_what_a_later_query_sees(ps, sinks):
+    rng = np.random.Generator(np.random.PCG64(ps + sinks))
+    window, total = 30, 400
+    rc, s = pg.pg_kv_server_create(total, total, ps, window, 0, 1 << 20)
+    assert rc == pg.PG_KV_OK
+    ids = [pg.pg_kv_request_open(s)[1] for _ in range(2)]
+    front = dict.fromkeys(ids, 0)
+    for _ in range(60):
+        rid = ids[rng.integers(2)]
+        n = int(rng.integers(1, 6))
+        assert pg.pg_kv_admit_step(s, rid, n) == pg.PG_KV_OK
+        rc, ptr, pages, last, start = pg.pg_kv_batch_plan_inputs(s, L, [rid], [n])
+        assert rc == pg.PG_KV_OK and (pages >= 0).all()
+        held = pg.pg_kv_request_pages(s, rid, L)[1]
+        assert len(held) == len(pages) == -(-(front[rid] + n) // ps)
+        lo = front[rid] - window  # the step's first query's window
+        for k, (h, p) in enumerate(zip(held, pages)):
+            need = (k + 1) * ps > lo or k * ps < sinks
+            assert (h >= 0 or not need) and p == (h if h >= 0 else held[-1])
+        assert pg.pg_kv_request_trim(s, rid, sinks)[0] == pg.PG_KV_ERR_PENDING
+        assert pg.pg_kv_commit_step(s, rid) == pg.PG_KV_OK
+        front[rid] += n
+        before = pg.pg_kv_free_pages(s, L)[1]
+        rc, freed = pg.pg_kv_request_trim(s, rid, sinks)
+        assert rc == pg.PG_KV_OK and pg.pg_kv_free_pages(s, L)[1] == before + freed
+        assert pg.pg_kv_request_trim(s, rid, sinks) == (pg.PG_KV_OK, 0)
+        assert (pg.pg_kv_request_pages(s, rid, L)[1] >= 0).sum() <= -(-sinks // ps) + -(-(window + 5) // ps) + 1
+        assert (pg.pg_kv_request_pages(s, rid, G)[1] >= 0).all()
+    mine = [p for x in ids for p in pg.pg_kv_request_pages(s, x, L)[1] if p >= 0]
+    assert len(set(mine)) == len(mine) == total - pg.pg_kv_free_pages(s, L)[1]
+    for x in ids:
+        assert pg.pg_kv_request_close(s, x) == pg.PG_KV_OK
+    assert pg.pg_kv_free_pages(s, L)[1] == total
+    assert pg.pg_kv_request_trim(s, ids[0], sinks)[0] == pg.PG_KV_ERR_FOREIGN
+    pg.pg_kv_server_destroy(s)
+    s = server(ring=True)
+    rid = pg.pg_kv_request_open(s)[1]
+    assert pg.pg_kv_request_trim(s, rid, 0)[0] == pg.PG_KV_ERR_WINDOW
+    assert pg.pg_kv_request_trim(s, rid, -1)[0] == pg.PG_KV_ERR_ARG
+    pg.pg_kv_server_destroy(s)
+
+
 def test_a_null_plan_is_refused():
     pool, stats = pg.pg_pool_t(), pg.pg_kv_stats_t()
     before = pg.pg_launch_count()
