@@ -360,7 +360,8 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  * A key that some rows of its tile see and others do not takes part with weight 0 in the latter:
  * a non-finite V row among the keys held makes every row of a prefill tile that spans it
  * non-finite. K rows have no such effect, and in decode only visible keys take part.
- * Errors: those of pg_attn_paged_prefill, and PG_ERR_WINDOW for num_sink < 0.
+ * Errors: those of pg_attn_paged_prefill, PG_ERR_WINDOW for num_sink < 0, and
+ * PG_ERR_I32_OVERFLOW for a step that ends within 1024 positions of 2^31.
  */
 int pg_attn_paged_sink(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
                        const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,

@@ -544,7 +544,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         if (!ok) break;
         commit1(PVDONE + 8 * pb);
-            }
+      }
       if (end) break;
       end = flags & kEnd;
     }

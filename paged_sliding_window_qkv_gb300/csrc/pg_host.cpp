@@ -501,7 +501,8 @@ size_t bounded_ws_bytes(const pg_plan* p) {
 
 size_t plan_ws_bytes(const pg_plan* p) { return std::max(workspace_bytes(p), bounded_ws_bytes(p)); }
 
-// `args` (the accumulating entry, whose workspace holds more) receives the launched call's arguments, with num_tokens 0 when nothing ran.
+// `args` (the accumulating entry, whose workspace holds more) receives the launched call's
+// arguments, with num_tokens 0 when nothing ran.
 int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32_t D,
                 const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
                 float sm_scale, void* ws, size_t ws_bytes, cudaStream_t stream,
@@ -642,6 +643,15 @@ int check_bounded_plan(const pg_plan* plan, cudaStream_t stream) {
   if (dev != plan->device) return PG_ERR_STREAM;
   if (plan->ring) return PG_ERR_PLAN_MISMATCH;  // a ring overwrites the positions these keep
   return PG_OK;
+}
+
+// The attention kernels count keys in tiles, so a position past the step's last one by less than a
+// pair of query tiles (256 rows) and a key tile (128) must still be an int32.
+constexpr int32_t kLastEnd = INT32_MAX - 1024;
+int check_bounded_attn(const pg_plan* plan, int32_t num_sink) {
+  if (num_sink < 0) return PG_ERR_WINDOW;
+  if (plan->head_dim != 256 && plan->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
+  return plan->max_pos_end > kLastEnd ? PG_ERR_I32_OVERFLOW : PG_OK;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -917,10 +927,8 @@ int pg_attn_paged_sink(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
                        int32_t num_sink, float sm_scale, void* workspace, size_t ws_bytes,
                        pg_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int rc = check_bounded_plan(plan, s);
-  if (rc) return rc;
-  if (num_sink < 0) return PG_ERR_WINDOW;
-  if (plan->head_dim != 256 && plan->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
+  int rc = check_bounded_plan(plan, s);
+  if (rc || (rc = check_bounded_attn(plan, num_sink))) return rc;
   Bounded b;
   b.num_sink = num_sink;
   return attn_common(plan, pool, layer, plan->head_dim, q, out, lse, window_left, sm_scale, workspace,
@@ -935,9 +943,7 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
                        size_t ws_bytes, pg_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = check_bounded_plan(plan, s);
-  if (rc) return rc;
-  if (num_sink < 0) return PG_ERR_WINDOW;
-  if (plan->head_dim != 256 && plan->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
+  if (rc || (rc = check_bounded_attn(plan, num_sink))) return rc;
   if ((rc = check_plan_pool(plan, pool, layer, plan->head_dim))) return rc;
   if ((rc = check_stats(plan, stats, layer, 1))) return rc;
   if (stats->num_layers != pool->num_layers || stats->num_pages != pool->num_pages)

@@ -618,3 +618,25 @@ def test_a_local_layer_served_from_a_few_pages():
     assert min(len(h) for h in hist) > 300 and pg.pg_kv_free_pages(srv, pg.PG_KV_LOCAL)[1] > 0
     plan.close()
     pg.pg_kv_server_destroy(srv)
+
+
+@pytest.mark.parametrize("D,hq,hkv,ps,qo", [(256, 16, 8, 16, 1), (256, 16, 8, 16, 70), (512, 16, 1, 8, 1),
+                                            (512, 16, 1, 8, 130), (256, 4, 2, 4, 1), (256, 4, 2, 4, 9)])
+def test_the_last_positions(D, hq, hkv, ps, qo):
+    """A request whose earlier keys were evicted may sit anywhere in int32, up to the stated end."""
+    end = 2 ** 31 - 1 - 1024
+    for e, rc in [(end, pg.PG_OK), (end + 1, pg.PG_ERR_I32_OVERFLOW), (2 ** 31 - 1, pg.PG_ERR_I32_OVERFLOW)]:
+        start = e - qo
+        c = Case(D, hq, hkv, [qo], [start], ps=ps, evicted=start - 150, seed=D + qo).build()
+        n = max(pg.pg_workspace_bytes(c.plan), pg.pg_mass_workspace_bytes(c.plan), 16)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        for window, sinks in [(60, start - 140), (2 ** 31 - 1, 2 ** 31 - 1), (-1, 0)]:
+            args = (c.plan, c.desc, 0, c.q, c.out, c.lse)
+            assert pg.pg_attn_paged_sink(*args, window, sinks, 1.0, ws, n) == rc
+            if rc == pg.PG_OK:
+                ok()
+                c.reference(window, sinks)
+                c.check_attention(f"window {window}")
+            assert pg.pg_attn_paged_mass(*args, c.stats, window, sinks, 1.0, ws, n) == rc
+        ok()
+        c.close()
