@@ -6,8 +6,8 @@
 // page list. It keeps n' = min(n, budget): the keys whose position is below num_sink or among
 // the last num_recent first, then the largest masses, equal masses by lower slot.
 //
-//   select  finds the n'-th largest key by a radix descent over the masses' order-preserving bit
-//           patterns (8 bits a pass) and writes, for each slot below n', the slot whose key will
+//   select  finds the n'-th largest key by counts over the masses' order-preserving bit
+//           patterns and writes, for each slot below n', the slot whose key will
 //           sit there: kept keys already below n' stay, and the kept keys at or past n' fill the
 //           holes below it, both in slot order. At most min(n', n - n') rows move (one per head
 //           when a step evicts one key), and sources and destinations are disjoint, so
@@ -69,20 +69,27 @@ __device__ __forceinline__ uint32_t order_of(const EvictArgs& a, int64_t recent,
 // One CTA (or a cluster of up to 8) per segment, its keys in registers: thread t of the segment
 // holds slots [k t, k (t + 1)), k <= KPT the segment's share of them in groups of four, so slot
 // order is thread order and every rank below is a bit count over the thread's 32-bit masks and one
-// scan over the threads. Statistics are read four slots at a time where the pages and the arrays
-// allow it (V4).
+// scan over the threads. Statistics are read in slot order, four slots a load where the pages and
+// the arrays allow it (V4), and reach the threads' shares through shared memory (read by their own
+// threads, a warp's loads fell into 32 lines: 66 against 48 us on 512 segments of 16,384 keys, with
+// the next paragraph's sample).
 //
-// The keep-th largest order value is built bit by bit from the top: a candidate stays when at
-// least keep keys reach it, one count over the segment per bit (compares in registers, a warp
-// reduction and one barrier: no histogram, so equal exponents cost nothing). The descent ends when
-// exactly keep keys reach the candidate (then nothing ties), about 20 bits in for masses that
-// differ; once 1024 keys or fewer share the bits so far, they are gathered and only they are
-// counted (two a thread). Bound: a segment is read once (8 bytes a key), and the counts are two
-// instructions per key and bit; with them one CTA on an SM covers the other's loads.
+// The keep-th largest order value is searched for in a shrinking range [lo, last], one count over
+// the segment per step (compares in registers, a warp reduction and one barrier: no histogram, so
+// equal exponents cost nothing). One CTA starts from a range that 128 of its keys suggest, two
+// standard deviations of a rank to either side, verified by one double count; it usually holds
+// about a sixth of the keys. Then the range is cut in proportion to the counts, every fourth time
+// in half. Once 1024 keys or fewer are in it, they are gathered and only they are counted. The
+// search ends when exactly keep keys reach lo (then nothing ties) or the range is one value.
+//
+// Bound: latency, some 6.5 us of a 16,384-key segment's 14 before the keys are in registers on
+// an idle GPU; a segment is read once (8 bytes a key). 512 segments of 8000 keys take 28 us (1.4 TB/s),
+// of 16,384 48 us.
 constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelWarps = kSelThreads / 32;  // at most
 constexpr int kMaxCluster = 8;
-constexpr int kGather = 2 * kSelThreads;  // keys gathered out of the segment: two a thread
+constexpr int kGather = 1024;  // keys gathered out of the segment
+constexpr int kSampleRanks = 11;  // two standard deviations of a rank in 128 samples
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -97,7 +104,7 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // Counts over the segment's threads. Buffers are used alternately, so one barrier a call is enough.
-template <bool CL>
+template <int NW, bool CL>
 struct Counter {
   int32_t (*warp_sum)[kSelWarps];  // [2][warps]
   int2 (*cta_sum)[kMaxCluster];    // [2][ranks], in every CTA of the cluster
@@ -120,7 +127,7 @@ struct Counter {
     v = __reduce_add_sync(0xffffffffu, v);
     if (lane == 0) warp_sum[phase][warp] = v;
     __syncthreads();
-    int32_t t = __reduce_add_sync(0xffffffffu, lane < kSelWarps ? warp_sum[phase][lane] : 0);
+    int32_t t = __reduce_add_sync(0xffffffffu, lane < NW ? warp_sum[phase][lane] : 0);
     if constexpr (CL) {
       int2 unused;
       t = cluster(make_int2(t, 0), &unused).x;
@@ -141,7 +148,7 @@ struct Counter {
     }
     if (lane == 31) warp_sum[phase][warp] = (int32_t)incl;
     __syncthreads();
-    const uint32_t w = lane < kSelWarps ? (uint32_t)warp_sum[phase][lane] : 0u;
+    const uint32_t w = lane < NW ? (uint32_t)warp_sum[phase][lane] : 0u;
     const uint32_t t = __reduce_add_sync(0xffffffffu, w);
     const uint32_t p = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u) + incl - v;
     int2 b = make_int2((int32_t)(p & 0xFFFFu), (int32_t)(p >> 16));
@@ -157,20 +164,21 @@ struct Counter {
   }
 };
 
-template <int KPT, bool CL, bool V4>
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs a, int32_t ranks) {
+template <int NT, int KPT, bool CL, bool V4>
+__global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a, int32_t ranks) {
   // kept keys past the new length, by rank: at most half of the cluster's slots, spread over it
-  constexpr int kList = kSelThreads * KPT / 2;
+  constexpr int kList = NT * KPT / 2;
   __shared__ int32_t warp_sum[2][kSelWarps];
   __shared__ int2 cta_sum[2][kMaxCluster];
-  extern __shared__ int32_t list[];
+  extern __shared__ uint4 stage[];
+  int32_t* const list = reinterpret_cast<int32_t*>(stage);  // (once the keys are in registers)
   const int32_t rank = CL ? (int32_t)(blockIdx.x % ranks) : 0;
   const int32_t seg = CL ? (int32_t)(blockIdx.x / ranks) : (int32_t)blockIdx.x;
   const Seg q = load_seg(a, seg);
   int32_t* src = a.src + (int64_t)seg * a.budget;
   const int tid = threadIdx.x;
-  const int32_t step = CL ? kSelThreads * ranks : kSelThreads, first = rank * kSelThreads + tid;
-  const bool fits = q.n <= kSelThreads * KPT * (CL ? ranks : 1);
+  const int32_t step = CL ? NT * ranks : NT, first = rank * NT + tid;
+  const bool fits = q.n <= NT * KPT * (CL ? ranks : 1);
   // every slot keeps its key until a hole below says otherwise
   if (!CL || q.keep == q.n || !fits)  // (a cluster that goes on does it below)
     for (int32_t s = first; s < a.budget; s += step) src[s] = s < q.keep ? s : -1;
@@ -187,115 +195,203 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictArgs 
   }
   const int64_t recent = recent_from(a, q);
   // the segment's slots in equal shares: groups of four (whole groups keep V4's vectors in a page)
-  const int32_t threads = kSelThreads * (CL ? ranks : 1);
+  const int32_t threads = NT * (CL ? ranks : 1);
   const int32_t share = ((q.n + threads - 1) / threads + 3) & ~3;
-  const int32_t s0 = (rank * kSelThreads + tid) * share;
+  const int32_t s0 = (rank * NT + tid) * share;
   const int32_t s_end = min(q.n, s0 + share);
-  uint32_t key[KPT];
-  if constexpr (V4) {
-    // four slots of one page at a time, all loads in flight before the first use
-    constexpr int B = KPT < 16 ? KPT / 4 : 4;  // groups per batch
+  // read in the order of the slots, through shared memory to the threads' shares (rows of share / 4
+  // groups at an odd pitch, so rows read side by side fall on different banks)
+  const int32_t groups = share / 4, pitch = groups | 1;
+  {
+    const uint32_t mul = (65536u + (uint32_t)groups - 1u) / (uint32_t)groups;  // exact below 8192 groups
+    const int32_t c0 = rank * NT * share;
+    constexpr int B = KPT < 16 ? KPT / 4 : 4;  // groups of a thread whose loads are in flight
+    int32_t page[KPT / 4];                     // (V4) of each group; -2: none
+    if constexpr (V4) {
+#pragma unroll
+      for (int i = 0; i < KPT / 4; ++i) {
+        const int32_t s = c0 + 4 * (tid + i * NT);
+        page[i] = i < groups && s < q.n ? page_of(a, q, s) : -2;
+      }
+    }
 #pragma unroll
     for (int i0 = 0; i0 < KPT / 4; i0 += B) {
-      int32_t page[B];
-      int4 pos[B];
-      float4 m[B];
+      uint4 k[B];
+      if constexpr (V4) {
+        int4 pos[B];
+        float4 m[B];
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int32_t s = s0 + 4 * (i0 + i);
-        page[i] = s < s_end ? page_of(a, q, s) : -2;
-      }
+        for (int i = 0; i < B; ++i) {
+          pos[i] = make_int4(0, 0, 0, 0);
+          m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (page[i0 + i] >= 0) {
+            const int64_t at = stat_at(a, q, page[i0 + i], c0 + 4 * (tid + (i0 + i) * NT));
+            pos[i] = *reinterpret_cast<const int4*>(a.stats.pos + at);
+            m[i] = *reinterpret_cast<const float4*>(a.stats.mass + at);
+          }
+        }
 #pragma unroll
-      for (int i = 0; i < B; ++i) {
-        pos[i] = make_int4(0, 0, 0, 0);
-        m[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (page[i] >= 0) {
-          const int64_t at = stat_at(a, q, page[i], s0 + 4 * (i0 + i));
-          pos[i] = *reinterpret_cast<const int4*>(a.stats.pos + at);
-          m[i] = *reinterpret_cast<const float4*>(a.stats.mass + at);
+        for (int i = 0; i < B; ++i) {
+          const int32_t left = q.n - (c0 + 4 * (tid + (i0 + i) * NT));
+          const bool bad = page[i0 + i] < 0;
+          k[i].x = left <= 0 ? 0u : bad ? 1u : order_of(a, recent, pos[i].x, m[i].x);
+          k[i].y = left <= 1 ? 0u : bad ? 1u : order_of(a, recent, pos[i].y, m[i].y);
+          k[i].z = left <= 2 ? 0u : bad ? 1u : order_of(a, recent, pos[i].z, m[i].z);
+          k[i].w = left <= 3 ? 0u : bad ? 1u : order_of(a, recent, pos[i].w, m[i].w);
+          if (page[i0 + i] == -1) atomicOr(a.status, kStatusBounds);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          uint32_t e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t s = c0 + 4 * (tid + (i0 + i) * NT) + e;
+            const int32_t page = i0 + i < groups && s < q.n ? page_of(a, q, s) : -2;
+            e4[e] = page == -2 ? 0u : 1u;
+            if (page >= 0) {
+              const int64_t at = stat_at(a, q, page, s);
+              e4[e] = order_of(a, recent, a.stats.pos[at], a.stats.mass[at]);
+            } else if (page == -1) {
+              atomicOr(a.status, kStatusBounds);
+            }
+          }
+          k[i] = make_uint4(e4[0], e4[1], e4[2], e4[3]);
         }
       }
 #pragma unroll
       for (int i = 0; i < B; ++i) {
-        const int32_t s = s0 + 4 * (i0 + i);
-        const int32_t p4[4] = {pos[i].x, pos[i].y, pos[i].z, pos[i].w};
-        const float m4[4] = {m[i].x, m[i].y, m[i].z, m[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          key[4 * (i0 + i) + e] = s + e >= s_end ? 0u : page[i] < 0 ? 1u : order_of(a, recent, p4[e], m4[e]);
-        if (page[i] == -1) atomicOr(a.status, kStatusBounds);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < KPT; ++i) {
-      const int32_t s = s0 + i, page = s < s_end ? page_of(a, q, s) : -2;
-      key[i] = page == -2 ? 0u : 1u;
-      if (page >= 0) {
-        const int64_t at = stat_at(a, q, page, s);
-        key[i] = order_of(a, recent, a.stats.pos[at], a.stats.mass[at]);
-      } else if (page == -1) {
-        atomicOr(a.status, kStatusBounds);
+        const int32_t j = tid + (i0 + i) * NT, t = (int32_t)((uint32_t)j * mul >> 16);
+        if (i0 + i < groups) stage[t * pitch + j - t * groups] = k[i];
       }
     }
   }
-  Counter<CL> count{warp_sum, cta_sum, rank, ranks, 0};
-  // ---- the keep-th largest order value
-  uint32_t cut = 0u;
-  int32_t reach = q.n, above = 0;  // keys from cut up, and from the end of its range (cut + 2^(bit + 1)) up
-  int bit = 31;
-  for (; bit >= 0; --bit) {
-    if (!CL && reach - above <= kGather && bit >= 3) break;
-    const uint32_t cand = cut | (1u << bit);
+  __syncthreads();
+  uint32_t key[KPT];
+#pragma unroll
+  for (int i = 0; i < KPT / 4; ++i) {
+    const uint4 k = i < groups ? stage[tid * pitch + i] : make_uint4(0u, 0u, 0u, 0u);
+    key[4 * i] = k.x;
+    key[4 * i + 1] = k.y;
+    key[4 * i + 2] = k.z;
+    key[4 * i + 3] = k.w;
+  }
+  Counter<NT / 32, CL> count{warp_sum, cta_sum, rank, ranks, 0};
+  // ---- the keep-th largest order value: it lies in [lo, last], reach keys are lo or more and above
+  // (fewer than keep) are more than last
+  uint32_t lo = 1u, last = 0xFFFFFFFFu;
+  int32_t reach = q.n, above = 0;
+  auto at_least = [&](uint32_t v) {
     int32_t c = 0;
 #pragma unroll
     for (int i = 0; i < KPT; i += 4) {
       if (i < share)  // (uniform)
-        c += (key[i] >= cand ? 1 : 0) + (key[i + 1] >= cand ? 1 : 0) + (key[i + 2] >= cand ? 1 : 0) +
-             (key[i + 3] >= cand ? 1 : 0);
+        c += (key[i] >= v ? 1 : 0) + (key[i + 1] >= v ? 1 : 0) + (key[i + 2] >= v ? 1 : 0) +
+             (key[i + 3] >= v ? 1 : 0);
     }
-    c = count.total(c);
-    if (c >= q.keep) {
-      cut = cand;
-      reach = c;
+    return c;
+  };
+  if constexpr (!CL) {
+    // two values around it, by the ranks of a sample: 128 threads' first keys
+    constexpr int kEach = NT / 128, kPart = 128 / kEach;  // threads to a sample, keys that each looks at
+    __shared__ uint4 sample[kEach][kPart / 4 + 1];        // (the parts a group apart)
+    __shared__ uint32_t pick[2];
+    const int i = tid / kEach, part = tid % kEach;
+    uint32_t* const slot = reinterpret_cast<uint32_t*>(sample[i / kPart]) + i % kPart;
+    if (part == 0) *slot = key[0];
+    if (tid < 2) pick[tid] = 1u;
+    __syncthreads();
+    const uint32_t own = *slot;
+    int32_t c1 = 0;  // of the sample, keys not below this one
+#pragma unroll
+    for (int g = 0; g < kPart / 4; ++g) {
+      const uint4 k = sample[part][g];
+      c1 += (k.x >= own ? 1 : 0) + (k.y >= own ? 1 : 0) + (k.z >= own ? 1 : 0) + (k.w >= own ? 1 : 0);
+    }
+#pragma unroll
+    for (int o = 1; o < kEach; o <<= 1) c1 += __shfl_xor_sync(0xffffffffu, c1, o);
+    const int32_t held = ((q.n + share - 1) / share + kEach - 1) / kEach;  // sampled threads that hold keys
+    const int32_t r = q.keep * held / q.n;
+    const uint32_t mx = __reduce_max_sync(0xffffffffu, c1 >= r + kSampleRanks ? own : 0u);
+    const uint32_t my = __reduce_max_sync(0xffffffffu, c1 >= r - kSampleRanks ? own : 0u);
+    if ((tid & 31) == 0) {
+      atomicMax(&pick[0], mx);
+      atomicMax(&pick[1], my);
+    }
+    __syncthreads();
+    const uint32_t x = pick[0];
+    const bool top = pick[1] == 0xFFFFFFFFu || r - kSampleRanks <= 0;  // nothing is known past it
+    const uint32_t y = top ? 0u : pick[1] + 1u;
+    // (at most 16,384 keys: two counts of 16 bits)
+    const uint32_t c = (uint32_t)count.total(at_least(x) + (top ? 0 : at_least(y) << 16));
+    const int32_t cx = (int32_t)(c & 0xFFFFu), cy = (int32_t)(c >> 16);
+    if (cx >= q.keep) {
+      lo = x;
+      reach = cx;
     } else {
-      above = c;
+      last = x - 1u;
+      above = cx;
     }
-    if (c == q.keep) {  // exactly the keys from cand up: no lower bit can matter
-      bit = -1;
-      break;
+    if (!top && cx >= q.keep) {
+      if (cy >= q.keep) {
+        lo = y;
+        reach = cy;
+      } else {
+        last = y - 1u;
+        above = cy;
+      }
     }
   }
+  int32_t tries = 0;
+  auto middle = [&]() {  // in (lo, last]
+    const uint32_t span = last - lo;
+    ++tries;
+    if (span > (1u << 25) || (tries & 3) == 0) return lo + (span >> 1) + 1u;
+    const float f = (float)(reach - q.keep) / (float)(reach - above);
+    return lo + max(1u, min(span, (uint32_t)((float)span * f)));
+  };
+  auto narrow = [&](uint32_t v, int32_t c) {
+    if (c >= q.keep) {
+      lo = v;
+      reach = c;
+    } else {
+      last = v - 1u;
+      above = c;
+    }
+  };
+  while (lo < last && reach != q.keep && (CL || reach - above > kGather)) {
+    const uint32_t v = middle();
+    narrow(v, count.total(at_least(v)));
+  }
   if constexpr (!CL) {
-    if (bit >= 0) {
-      // the few keys of the range, two a thread
-      const uint32_t top = bit == 31 ? 0xFFFFFFFFu : cut + ((1u << (bit + 1)) - 1u);  // the range's last
+    if (lo < last && reach != q.keep) {
+      // the few keys of the range
       int32_t mine = 0;
 #pragma unroll
-      for (int i = 0; i < KPT; ++i) mine += key[i] >= cut && key[i] <= top && key[i] != 0u ? 1 : 0;
+      for (int i = 0; i < KPT; ++i) mine += key[i] >= lo && key[i] <= last ? 1 : 0;
       int2 all;
       int32_t at = count.before(mine, 0, &all).x;
 #pragma unroll
       for (int i = 0; i < KPT; ++i)
-        if (key[i] >= cut && key[i] <= top && key[i] != 0u) list[at++] = (int32_t)key[i];
+        if (key[i] >= lo && key[i] <= last) list[at++] = (int32_t)key[i];
       __syncthreads();
-      uint32_t few[kGather / kSelThreads];
+      const int32_t past = above;  // keys past the range
+      uint32_t few[kGather / NT];
 #pragma unroll
-      for (int i = 0; i < kGather / kSelThreads; ++i) {
-        const int32_t x = tid + i * kSelThreads;
+      for (int i = 0; i < kGather / NT; ++i) {
+        const int32_t x = tid + i * NT;
         few[i] = x < all.x ? (uint32_t)list[x] : 0u;
       }
-      for (; bit >= 0; --bit) {
-        const uint32_t cand = cut | (1u << bit);
-        int32_t c = 0;
+      while (lo < last && reach != q.keep) {
+        const uint32_t v = middle();
+        int32_t c = past;
 #pragma unroll
-        for (int i = 0; i < kGather / kSelThreads; ++i) c += few[i] >= cand ? 1 : 0;
-        c = above + count.total(c);
-        if (c >= q.keep) cut = cand;
-        if (c == q.keep) break;
+        for (int i = 0; i < kGather / NT; ++i) c += __syncthreads_count(few[i] >= v);
+        narrow(v, c);
       }
     }
   }
+  const uint32_t cut = lo;
   // ---- kept slots: above the cut, and the lowest of those at it
   uint32_t kept = 0u, tie = 0u;
 #pragma unroll
@@ -524,12 +620,21 @@ __global__ void __launch_bounds__(kApplyThreads) evict_apply_kernel(EvictArgs a,
   }
 }
 
-template <int KPT, bool CL, bool V4>
+template <int NT, int KPT, bool CL, bool V4>
 cudaError_t launch_select4(const EvictArgs& a, int32_t segs, int32_t ranks, cudaStream_t stream) {
-  constexpr int smem = kSelThreads * KPT / 2 * 4;
+  constexpr int smem = NT * (KPT / 4 | 1) * 16;  // (the list: NT KPT / 2 numbers)
+  static PerDeviceOnce setup;
+  int dev = 0, unused = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = setup.get(dev, [](int*) {
+    return cudaFuncSetAttribute(evict_select_kernel<NT, KPT, CL, V4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem);
+  }, &unused);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * ranks), 1, 1);
-  cfg.blockDim = dim3(kSelThreads, 1, 1);
+  cfg.blockDim = dim3(NT, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -539,19 +644,19 @@ cudaError_t launch_select4(const EvictArgs& a, int32_t segs, int32_t ranks, cuda
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CL ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel<KPT, CL, V4>, a, ranks);
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel<NT, KPT, CL, V4>, a, ranks);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }
 
-template <int KPT, bool CL>
+template <int NT, int KPT, bool CL>
 cudaError_t launch_select(const EvictArgs& a, int32_t segs, int32_t ranks, cudaStream_t stream) {
   // four slots a load: pages of whole groups, arrays on 16-byte boundaries (every layer's too)
   const bool v4 = a.pool.page_size % 4 == 0 && ((uintptr_t)a.stats.mass & 15u) == 0 &&
                   ((uintptr_t)a.stats.pos & 15u) == 0;
-  return v4 ? launch_select4<KPT, CL, true>(a, segs, ranks, stream)
-            : launch_select4<KPT, CL, false>(a, segs, ranks, stream);
+  return v4 ? launch_select4<NT, KPT, CL, true>(a, segs, ranks, stream)
+            : launch_select4<NT, KPT, CL, false>(a, segs, ranks, stream);
 }
 
 }  // namespace
@@ -568,12 +673,26 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t stream) {
   const int32_t segs = a.num_layers * a.plan.num_req * a.pool.num_kv_heads;
   if (segs == 0) return cudaSuccess;
   const int32_t n = a.max_keys, ranks = evict_select_ranks(n);
-  // the fewest registers that hold the longest segment: more CTAs share an SM
-  if (n <= kSelThreads * 4) return launch_select<4, false>(a, segs, 1, stream);
-  if (n <= kSelThreads * 8) return launch_select<8, false>(a, segs, 1, stream);
-  if (n <= kSelThreads * 16) return launch_select<16, false>(a, segs, 1, stream);
-  if (n <= kSelThreads * 32) return launch_select<32, false>(a, segs, 1, stream);
-  if (n <= kSelThreads * 32 * kMaxCluster) return launch_select<32, true>(a, segs, ranks, stream);
+  // the fewest registers that hold the longest segment
+  static PerDeviceOnce device;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = device.get(dev, [dev](int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); }, &sms);
+  if (e != cudaSuccess) return e;
+  // Two CTAs of 512 threads fill an SM's registers. Where there are more segments than that, 256
+  // threads each: four of their chains of loads and counts then overlap on an SM (512 segments of
+  // 2048, 4096, 8000 keys: 13.8, 17.1, 28.4 against 16.4, 20.9, 31.6 us).
+  if (segs > 2 * sms) {
+    if (n <= 256 * 8) return launch_select<256, 8, false>(a, segs, 1, stream);
+    if (n <= 256 * 16) return launch_select<256, 16, false>(a, segs, 1, stream);
+    if (n <= 256 * 32) return launch_select<256, 32, false>(a, segs, 1, stream);
+  }
+  if (n <= kSelThreads * 4) return launch_select<kSelThreads, 4, false>(a, segs, 1, stream);
+  if (n <= kSelThreads * 8) return launch_select<kSelThreads, 8, false>(a, segs, 1, stream);
+  if (n <= kSelThreads * 16) return launch_select<kSelThreads, 16, false>(a, segs, 1, stream);
+  if (n <= kSelThreads * 32) return launch_select<kSelThreads, 32, false>(a, segs, 1, stream);
+  if (n <= kSelThreads * 32 * kMaxCluster) return launch_select<kSelThreads, 32, true>(a, segs, ranks, stream);
   evict_select_long_kernel<<<(unsigned)segs, kLongThreads, 0, stream>>>(a);
   count_launch();
   return cudaGetLastError();

@@ -285,6 +285,57 @@ def test_evict_long(n, budget):
     c.close()
 
 
+@pytest.mark.parametrize("n,keep", [(2048, 1000), (5000, 1), (8192, 4096), (8193, 8192), (16384, 5000), (16384, 9),
+                                    (30000, 20000)])
+@pytest.mark.parametrize("masses", ["distinct", "rising", "falling", "two", "zeros", "wide", "first of four low",
+                                    "first of four high", "recent"])
+def test_evict_orders(n, keep, masses):
+    """Masses whose order follows the slots, ties at the cut, and some whose fourth slots tell nothing of
+    the others."""
+    R = 2
+    c = Case(256, 1, 1, [1] * R, [n - 1, n - 10], seed=n + keep)
+    g = np.random.Generator(np.random.PCG64(keep))
+    mass, pos = c.mass_cpu.numpy(), c.pos_cpu.numpy()
+    for r in range(R):
+        page, off = c.rows_of(r)
+        k, s = int(c.n[r]), np.arange(int(c.n[r]))
+        m = g.exponential(1.0, k)
+        if masses in ("rising", "falling"):
+            m = np.sort(m) if masses == "rising" else np.sort(m)[::-1]
+        elif masses == "two":
+            m = np.where(g.random(k) < 0.5, 1.0, np.nextafter(np.float32(1), np.float32(2)))
+        elif masses == "zeros":
+            m = np.where(g.random(k) < 0.1, m, 0.0)
+        elif masses == "wide":
+            m = np.exp2(g.uniform(-120, 120, k))
+        elif masses.startswith("first"):
+            m = np.where(s % 4 == 0, m * (1e-3 if masses.endswith("low") else 1e3), m)
+        mass[0, page, 0, off] = m.astype(np.float32)
+        pos[0, page, 0, off] = g.permutation(k)
+    c.build()
+    recent = keep if masses == "recent" else 0
+    src = torch.full((1, R, 1, keep), -99, dtype=torch.int32, device="cuda")
+    pg.check(pg.pg_kv_evict_select(c.plan, c.stats, 0, 1, keep, 0, recent, src))
+    ok()
+    want = select_reference(c, keep, 0, recent, mass, pos, [0])
+    assert (src.cpu().numpy() == want).all()
+    c.close()
+
+
+@pytest.mark.parametrize("n,budget", [(2048, 700), (2049, 2000), (4100, 4096), (8192, 33), (9000, 4000)])
+def test_evict_many_segments(n, budget):
+    R, hkv = 20, 2
+    c = Case(256, hkv, hkv, [1] * R, [max(1, n - 97 * r) - 1 for r in range(R)], layers=9, ps=64, seed=n)
+    _scramble(c, n)
+    c.build()
+    src = torch.full((9, R, hkv, budget), -99, dtype=torch.int32, device="cuda")
+    pg.check(pg.pg_kv_evict_select(c.plan, c.stats, 0, 9, budget, 3, 20, src))
+    ok()
+    want = select_reference(c, budget, 3, 20, c.mass_cpu.numpy(), c.pos_cpu.numpy(), list(range(9)))
+    assert (src.cpu().numpy() == want).all()
+    c.close()
+
+
 def test_evict_all_equal_masses():
     """Every key ties: the lower slots stay."""
     c = Case(512, 1, 1, [1], [999], seed=1)
