@@ -141,8 +141,8 @@ struct TcArgs {
 
 // ------------------------------------------------------------------ kernel
 // One work unit = (pair of adjacent query tiles of one request, KV head, 256-column part of the
-// output). Units are numbered longest first (the plan lists each request's tile pairs in token
-// order, so the last pairs come first); cluster i takes one unit per round of clusters.
+// output). Units are numbered longest first (the plan lists the batch's tile pairs by the keys they
+// see, and the last come first); cluster i takes one unit per round of clusters.
 struct TcUnit {
   int32_t q0, tok0, ntok;  // this CTA's query tile: request's first token, tile start, tokens (0: none)
   // keys held: positions [kv_start, kv_len); key tiles start kb0 + 64 t, 64-aligned from kv_start

@@ -246,6 +246,23 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       }
     }
     nwork = (int64_t)wreq.size();
+    // The kernel takes the pairs from the last to the first, so those that see the most keys come
+    // last (a window keeps that order): on 8 prompts of 384..2026 tokens the busiest cluster then has
+    // 4% more than the mean, against 22% request by request. (Decode looks requests up in the table.)
+    if (num_req > 1 && !all_one) {
+      const size_t n = ptab.size() / 8;
+      std::vector<int32_t> order(n), sorted(ptab.size());
+      for (size_t i = 0; i < n; ++i) order[i] = (int32_t)i;
+      auto seen = [&](int32_t i) {
+        const int32_t* e = ptab.data() + 8 * (size_t)i;
+        const int64_t end = (int64_t)e[3] + std::min<int64_t>((int64_t)e[0] + 2 * (int64_t)cta, e[2]);
+        return std::min<int64_t>(end, e[6]) - e[7];
+      };
+      std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return seen(x) < seen(y); });
+      for (size_t i = 0; i < n; ++i)
+        std::copy_n(ptab.data() + 8 * (size_t)order[i], 8, sorted.data() + 8 * i);
+      ptab.swap(sorted);
+    }
   }
   if (!fits_i32(nwork)) return PG_ERR_I32_OVERFLOW;
 

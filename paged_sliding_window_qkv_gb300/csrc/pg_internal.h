@@ -40,7 +40,8 @@ struct PlanDev {
   // [num_pairs][8]: two consecutive query tiles of one request, with the request's geometry so
   // a kernel reads it in one step: {first request-local token of the pair, qo_indptr[r],
   // qo_len, start_pos, kv_page_indptr[r], kv_page_indptr[r + 1], kv_end, kv_start}; the keys
-  // held are positions [kv_start, kv_end)
+  // held are positions [kv_start, kv_end). Decode plans: request r's entry is the r-th; others: by
+  // the keys that the pair sees, the fewest first
   const int32_t* pair_tab;
   int32_t num_req, num_tokens, num_page_ids, num_work, num_pairs;
   // ring addressing: logical page pos / page_size of request r is its page
