@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, 
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     const int k = warp * 16 + gid + 8 * e;
-    if (tig == 0 && k < nk) {
+    if (tig == 0 && k < nk && mass_seen(a, q, rel0 + k)) {
       const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
       if (page < a.pool.num_pages) mass_store(a, q, page, g, rel0 + k, s);
       else atomicOr(a.status, kStatusBounds);

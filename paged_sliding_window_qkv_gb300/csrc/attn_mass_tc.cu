@@ -460,7 +460,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const float both = xs[row] + xs[kMK + row];
         if (w.cut) {
           recs[((int64_t)s * 2 + (w.first ? 0 : 1)) * (2 * kMK) + rank * kMK + row] = both;
-        } else if (kvalid) {
+        } else if (kvalid && mass_seen(a, w.q, rel)) {
           const int32_t page = mass_page(pl, w.q, rel, ps, a.pool.num_pages);
           if (page < a.pool.num_pages) mass_store(a, w.q, page, w.g, rel, both);  // (else: reported)
         }
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(2 * kMK) mass_join_kernel(MassArgs m) {
   if (c.last <= s) return;
   const MassReq q = mass_req(a.plan, c.r, a.pool.page_size);
   const int32_t rel = c.kt * (2 * kMK) + (int32_t)threadIdx.x;
-  if (rel >= q.n) return;
+  if (rel >= q.n || !mass_seen(a, q, rel)) return;
   const int32_t page = mass_page(a.plan, q, rel, a.pool.page_size, a.pool.num_pages);
   if (page == a.pool.num_pages) return;  // reported by the producer
   float sum = recs[((int64_t)s * 2 + c.slot) * (2 * kMK) + threadIdx.x];

@@ -50,6 +50,14 @@ __device__ __forceinline__ MassTiles mass_tiles(const AttnArgs& a, const MassReq
   return t;
 }
 
+// Whether some row of the step sees key index rel: the first position at or past the key's is the
+// one that sees most of what lies before it. (The statistics of a key that no row sees are not
+// touched: its page may be someone else's by now.)
+__device__ __forceinline__ bool mass_seen(const AttnArgs& a, const MassReq& q, int32_t rel) {
+  const int32_t j = q.ks0 + rel;
+  return j < q.sp + q.len && (a.window_left < 0 || j < a.num_sink || max(j, q.sp) - j <= a.window_left);
+}
+
 // mass and position of one key: keys that the step wrote are set, older ones add
 __device__ __forceinline__ void mass_store(const AttnArgs& a, const MassReq& q, int32_t page,
                                            int32_t g, int32_t rel, float sum) {

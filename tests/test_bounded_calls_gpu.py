@@ -640,3 +640,30 @@ def test_the_last_positions(D, hq, hkv, ps, qo):
             assert pg.pg_attn_paged_mass(*args, c.stats, window, sinks, 1.0, ws, n) == rc
         ok()
         c.close()
+
+
+@pytest.mark.parametrize("D,hq,hkv,ps", [(512, 16, 1, 16), (256, 16, 8, 8), (256, 4, 2, 5), (512, 16, 1, 1)])
+@pytest.mark.parametrize("qo", [1, 40, 300])
+@pytest.mark.parametrize("window,sinks", [(60, 7), (0, 0), (600, 130), (-1, 0)])
+def test_statistics_of_unseen_keys_are_not_touched(D, hq, hkv, ps, qo, window, sinks):
+    """Their masses are -0 here, which adding nothing would turn into +0."""
+    c = Case(D, hq, hkv, [qo, qo], [700, 333], ps=ps, seed=qo + ps)
+    c.mass_cpu.fill_(-0.0)
+    c.build()
+    n = max(pg.pg_mass_workspace_bytes(c.plan), 16)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    pg.check(pg.pg_attn_paged_mass(c.plan, c.desc, 0, c.q, c.out, c.lse, c.stats, window, sinks, 1.0, ws, n))
+    ok()
+    mass, pos = c.mass.cpu().view(torch.int32).numpy(), c.pos.cpu().numpy()
+    held = np.zeros(mass.shape[1::2], bool)  # [page][slot]
+    for r in range(2):
+        p = c.start[r] + np.arange(qo)
+        j = np.arange(c.n[r])
+        see = (j[None] <= p[:, None]) & ((window < 0) | (p[:, None] - j[None] <= window) | (j[None] < sinks))
+        page, off = c.rows_of(r)
+        held[page[see.any(0)], off[see.any(0)]] = True
+        new = j >= c.start[r]
+        assert (pos[0, page[new], :, off[new]] == j[new][:, None]).all()
+        assert (pos[0, page[~new], :, off[~new]] == -7).all()
+    assert (mass[0].transpose(0, 2, 1)[~held] == -2 ** 31).all()
+    assert (mass[0].transpose(0, 2, 1)[held] >= 0).all()
