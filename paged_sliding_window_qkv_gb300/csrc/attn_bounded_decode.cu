@@ -101,11 +101,19 @@ struct BdArgs {
 };
 
 // ------------------------------------------------------------------ PTX (one CTA)
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* tm, int c2, int c3, uint32_t bar) {
+// K and V are read once a step: their lines leave L2 first, so that scores and records stay for the join
+// (64 requests of 8001 keys at head_dim 512: 176 -> 170 us, with weights 202 -> 197; 16: 63 -> 57).
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* tm, int c2, int c3, uint32_t bar,
+                                       uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(tm), "r"(0), "r"(c2), "r"(c3), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(tm), "r"(0), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
@@ -349,6 +357,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       }
     } else {
       const int br = args.box_rows, nbox = kT / br;
+      const uint64_t policy = evict_first();
       // the tile that the iterator stands on
       ReqTiles q = req_tiles(args, r);
       int32_t g = (int32_t)(in_req / q.total), j = (int32_t)(in_req % q.total);
@@ -404,7 +413,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           if (!__all_sync(0xffffffffu, mbar_wait_inline(EMPTY(slot), (round & 1) ^ 1, wc))) return false;
           if (lane == 0) mbar_expect_tx(FULL(slot), (uint32_t)__popc(boxes) * br * (C::SD * 2u));
           __syncwarp();
-          if (good) tma_4d(base + slot * C::SLOT + lane * br * (C::SD * 2), &tm_kv, C::NC * p, row / 8, FULL(slot));
+          if (good) tma_4d(base + slot * C::SLOT + lane * br * (C::SD * 2), &tm_kv, C::NC * p, row / 8, FULL(slot), policy);
           if (++slot == NS) { slot = 0; ++round; }
         }
         return true;
