@@ -553,23 +553,25 @@ __global__ void __launch_bounds__(kLongThreads) evict_select_long_kernel(EvictAr
 }
 
 // ------------------------------------------------------------------ apply
-// A block takes 256 N kept slots of one segment, a warp 32 N of them, N a lane: it lists the
-// slots whose key comes from elsewhere, then moves them four at a time, each row's 16-byte pieces
+// A warp takes S kept slots of one segment (up to 32, or a multiple of 32: S / 32 a lane): it lists
+// the slots whose key comes from elsewhere, then moves them four at a time, each row's 16-byte pieces
 // spread over the lanes (at head_dim 512 a lane has 16 loads in flight), so the moves of a warp
 // wait for memory once per four. Bound: 4 D bytes read and written per move, and the map read.
-constexpr int kApplyThreads = 256, kApplySlots = 1024, kMoves = 4;
-template <int D, int N>
+constexpr int kApplyThreads = 256, kApplyWarps = kApplyThreads / 32, kMoves = 4;
+constexpr int kApplyDense = 16, kApplySparse = 256;  // slots of a warp (see launch_evict_apply)
+template <int D, int S>
 __global__ void __launch_bounds__(kApplyThreads) evict_apply_kernel(EvictArgs a, int32_t blocks_per_seg) {
-  __shared__ int2 s_move[kApplyThreads / 32][32 * N];
+  constexpr int N = S < 32 ? 1 : S / 32;
+  __shared__ int2 s_move[kApplyWarps][S];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t seg = (int32_t)blockIdx.x / blocks_per_seg;
-  const int32_t t0 = ((int32_t)blockIdx.x % blocks_per_seg) * (kApplyThreads * N) + warp * (32 * N) + lane;
+  const int32_t t0 = ((int32_t)blockIdx.x % blocks_per_seg) * (kApplyWarps * S) + warp * S + lane;
   const int32_t* src = a.src + (int64_t)seg * a.budget;
   const Seg q = load_seg(a, seg);
   wait_previous();
   int32_t from[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) from[i] = t0 + 32 * i < a.budget ? src[t0 + 32 * i] : -1;
+  for (int i = 0; i < N; ++i) from[i] = (S >= 32 || lane < S) && t0 + 32 * i < a.budget ? src[t0 + 32 * i] : -1;
   bool any = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) any |= from[i] >= 0 && from[i] != t0 + 32 * i;
@@ -726,7 +728,8 @@ void set_page_divisor(EvictArgs* a) {
   a->page_shift = l - 1;
 }
 
-int32_t evict_apply_blocks(int32_t keep) { return (keep + kApplySlots - 1) / kApplySlots; }
+// At most as many blocks of the apply kernel per segment of `keep` kept slots.
+int32_t evict_apply_blocks(int32_t keep) { return (keep + kApplyWarps * kApplyDense - 1) / (kApplyWarps * kApplyDense); }
 
 cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream) {
   const int32_t segs = a.num_layers * a.plan.num_req * a.pool.num_kv_heads;
@@ -739,11 +742,14 @@ cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   err = device.get(dev, [dev](int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); }, &sms);
   if (err != cudaSuccess) return err;
-  // Blocks of twice the slots where the usual ones (eight fit an SM) are more than the GPU holds at
-  // once: one moved key in each of 512 segments of 4096 took 5.7 against 7.8 us.
+  // Few slots a warp keep its chain of moves short: half of 64 segments of 16,384 keys moved in 170 us
+  // against 182 with 128 slots, two thirds of 192 segments of 321 in 18 against 42. Where next to none
+  // move (a request gives up at most max_keys - budget keys) and there are more such blocks than fit
+  // the GPU at once, reading the map is all there is to do, and that wants many slots: one moved key
+  // in each of 512 segments of 4096 took 33 us with 16 slots, 7.8 with 128 and 5.7 with 256.
   int32_t blocks = evict_apply_blocks(slots);
-  const bool big = segs * blocks > 8 * sms && slots > kApplySlots;
-  if (big) blocks = (slots + 2 * kApplySlots - 1) / (2 * kApplySlots);
+  const bool sparse = (int64_t)(a.max_keys - slots) * 32 <= slots && segs * blocks > 8 * sms;
+  if (sparse) blocks = (slots + kApplyWarps * kApplySparse - 1) / (kApplyWarps * kApplySparse);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * blocks), 1, 1);
   cfg.blockDim = dim3(kApplyThreads, 1, 1);
@@ -754,8 +760,10 @@ cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto run = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, blocks); };
-  const cudaError_t e = a.pool.head_dim == 256 ? (big ? run(evict_apply_kernel<256, 8>) : run(evict_apply_kernel<256, 4>))
-                                               : (big ? run(evict_apply_kernel<512, 8>) : run(evict_apply_kernel<512, 4>));
+  const cudaError_t e =
+      a.pool.head_dim == 256
+          ? (sparse ? run(evict_apply_kernel<256, kApplySparse>) : run(evict_apply_kernel<256, kApplyDense>))
+          : (sparse ? run(evict_apply_kernel<512, kApplySparse>) : run(evict_apply_kernel<512, kApplyDense>));
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();

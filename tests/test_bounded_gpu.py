@@ -355,6 +355,27 @@ def test_evict_apply_many_segments():
     c.close()
 
 
+@pytest.mark.parametrize("D,n,budget", [(256, 1055, 1030), (512, 2304, 2299), (512, 2600, 2520)])
+def test_evict_apply_few_moves(D, n, budget):
+    """Next to none of the kept keys move, in more segments than a wave of small blocks."""
+    R, layers = 41, 4
+    c = Case(D, 1, 1, [1] * R, [n - 1 - r for r in range(R)], layers=layers, ps=32, seed=n)
+    _scramble(c, n)
+    c.build()
+    src = torch.full((layers, R, 1, budget), -99, dtype=torch.int32, device="cuda")
+    pg.check(pg.pg_kv_evict_select(c.plan, c.stats, 0, layers, budget, 4, 20, src))
+    pg.check(pg.pg_kv_evict_apply(c.plan, c.desc, c.stats, 0, layers, budget, src))
+    ok()
+    every = list(range(layers))
+    want = select_reference(c, budget, 4, 20, c.mass_cpu.numpy(), c.pos_cpu.numpy(), every)
+    assert (src.cpu().numpy() == want).all()
+    pool, mass, pos = apply_reference(c, want, every, c.pool_cpu, c.mass_cpu, c.pos_cpu)
+    assert torch.equal(c.pool.view(torch.int16).cpu(), pool.view(torch.int16))
+    assert torch.equal(c.mass.view(torch.int32).cpu(), mass.view(torch.int32))
+    assert torch.equal(c.pos.cpu(), pos)
+    c.close()
+
+
 def test_evict_all_equal_masses():
     """Every key ties: the lower slots stay."""
     c = Case(512, 1, 1, [1], [999], seed=1)
