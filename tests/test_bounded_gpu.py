@@ -376,6 +376,23 @@ def test_evict_apply_few_moves(D, n, budget):
     c.close()
 
 
+@pytest.mark.parametrize("n", [4, 129, 512, 513, 1024])
+@pytest.mark.parametrize("part", [0.02, 0.5, 0.98])
+@pytest.mark.parametrize("ps", [3, 16])
+def test_evict_short(n, part, ps):
+    lens = sorted({1, 2, n // 3 + 1, n - 1, n})
+    keep = max(1, int(n * part))
+    c = Case(256, 2, 2, [1] * len(lens), [x - 1 for x in lens], ps=ps, layers=2, seed=n)
+    _scramble(c, n + keep)
+    c.build()
+    src = torch.full((2, len(lens), 2, keep), -99, dtype=torch.int32, device="cuda")
+    pg.check(pg.pg_kv_evict_select(c.plan, c.stats, 0, 2, keep, 0, keep // 3, src))
+    ok()
+    want = select_reference(c, keep, 0, keep // 3, c.mass_cpu.numpy(), c.pos_cpu.numpy(), [0, 1])
+    assert (src.cpu().numpy() == want).all()
+    c.close()
+
+
 def test_evict_all_equal_masses():
     """Every key ties: the lower slots stay."""
     c = Case(512, 1, 1, [1], [999], seed=1)
