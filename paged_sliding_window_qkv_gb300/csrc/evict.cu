@@ -87,7 +87,9 @@ __device__ __forceinline__ void wait_previous() {
 // equal exponents cost nothing). One CTA starts from a range that 128 of its keys suggest, two
 // standard deviations of a rank to either side, verified by one double count; it usually holds
 // about a sixth of the keys. Then the range is cut in proportion to the counts, every fourth time
-// in half. Once 1024 keys or fewer are in it, they are gathered and only they are counted. The
+// in half; a count that told no keys of it apart shrinks it to the least and the largest key in it,
+// so equal keys at the cut end the search (216 segments of up to 667 keys with zeros and equal masses
+// 14.0 -> 9.0 us). Once 1024 keys or fewer are in it, they are gathered and only they are counted. The
 // search ends when exactly keep keys reach lo (then nothing ties) or the range is one value.
 //
 // (Keys left in shared memory, with 40 registers a thread and three CTAs of 512 on an SM, were slower: 512
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
   constexpr int kGather = NT * KPT < 1024 ? NT * KPT : 1024;  // keys gathered out of the segment
   __shared__ int32_t warp_sum[2][kSelWarps];
   __shared__ int2 cta_sum[2][kMaxCluster];
+  __shared__ uint32_t pick[2];
   extern __shared__ uint4 stage[];
   int32_t* const list = reinterpret_cast<int32_t*>(stage);  // (once the keys are in registers)
   const int32_t rank = CL ? (int32_t)(blockIdx.x % ranks) : 0;
@@ -307,7 +310,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
     // two values around it, by the ranks of a sample: 128 threads' first keys
     constexpr int kEach = NT / 128, kPart = 128 / kEach;  // threads to a sample, keys that each looks at
     __shared__ uint4 sample[kEach][kPart / 4 + 1];        // (the parts a group apart)
-    __shared__ uint32_t pick[2];
     const int i = tid / kEach, part = tid % kEach;
     uint32_t* const slot = reinterpret_cast<uint32_t*>(sample[i / kPart]) + i % kPart;
     if (part == 0) *slot = key[0];
@@ -355,14 +357,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
     }
   }
   int32_t tries = 0;
+  bool moved = true;  // the last count told keys of the range apart
   auto middle = [&]() {  // in (lo, last]
     const uint32_t span = last - lo;
     ++tries;
-    if (span > (1u << 25) || (tries & 3) == 0) return lo + (span >> 1) + 1u;
+    if (span > (1u << 25) || !moved || (tries & 3) == 0) return lo + (span >> 1) + 1u;
     const float f = (float)(reach - q.keep) / (float)(reach - above);
     return lo + max(1u, min(span, (uint32_t)((float)span * f)));
   };
   auto narrow = [&](uint32_t v, int32_t c) {
+    moved = c != reach && c != above;
     if (c >= q.keep) {
       lo = v;
       reach = c;
@@ -371,7 +375,34 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
       above = c;
     }
   };
+  // equal keys at the cut: the range shrinks to the least and largest key in it (one CTA; a cluster
+  // goes on by halves)
+  auto tighten = [&](uint32_t least, uint32_t most) {
+    if (tid < 2) pick[tid] = tid == 0 ? 0xFFFFFFFFu : 0u;
+    __syncthreads();
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((tid & 31) == 0) {
+      atomicMin(&pick[0], least);
+      atomicMax(&pick[1], most);
+    }
+    __syncthreads();
+    lo = pick[0];
+    last = pick[1];
+    moved = true;
+  };
   while (lo < last && reach != q.keep && (CL || reach - above > kGather)) {
+    if (!CL && !moved) {
+      uint32_t least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll
+      for (int i = 0; i < KPT; ++i) {
+        const bool in = key[i] >= lo && key[i] <= last;
+        least = in ? min(least, key[i]) : least;
+        most = in ? max(most, key[i]) : most;
+      }
+      tighten(least, most);
+      continue;
+    }
     const uint32_t v = middle();
     narrow(v, count.total(at_least(v)));
   }
@@ -395,6 +426,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
         few[i] = x < all.x ? (uint32_t)list[x] : 0u;
       }
       while (lo < last && reach != q.keep) {
+        if (!moved) {
+          uint32_t least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll
+          for (int i = 0; i < kGather / NT; ++i) {
+            const bool in = few[i] >= lo && few[i] <= last;
+            least = in ? min(least, few[i]) : least;
+            most = in ? max(most, few[i]) : most;
+          }
+          tighten(least, most);
+          continue;
+        }
         const uint32_t v = middle();
         int32_t c = past;
 #pragma unroll
