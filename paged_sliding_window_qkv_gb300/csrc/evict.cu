@@ -779,8 +779,7 @@ int32_t evict_apply_blocks(int32_t keep) { return (keep + kApplyWarps * kApplyDe
 
 cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream) {
   const int32_t segs = a.num_layers * a.plan.num_req * a.pool.num_kv_heads;
-  // slots of the budget that no request fills hold -1: they need no block
-  const int32_t slots = a.max_keys < a.budget ? a.max_keys : a.budget;
+  const int32_t slots = a.slots;
   if (segs == 0 || slots == 0) return cudaSuccess;
   static PerDeviceOnce device;
   int dev = 0, sms = 0;
@@ -790,7 +789,7 @@ cudaError_t launch_evict_apply(const EvictArgs& a, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   // Few slots a warp keep its chain of moves short: half of 64 segments of 16,384 keys moved in 170 us
   // against 182 with 128 slots, two thirds of 192 segments of 321 in 18 against 42. Where next to none
-  // move (a request gives up at most max_keys - budget keys) and there are more such blocks than fit
+  // move (a request gives up at most max_keys - budget keys as the plan stands) and there are more such blocks than fit
   // the GPU at once, reading the map is all there is to do, and that wants many slots: one moved key
   // in each of 512 segments of 4096 took 33 us with 16 slots, 7.8 with 128 and 5.7 with 256.
   int32_t blocks = evict_apply_blocks(slots);

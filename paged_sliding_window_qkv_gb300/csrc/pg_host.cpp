@@ -104,6 +104,7 @@ struct pg_plan {
          o_wreq = 0, o_wtok = 0, o_pair = 0;
   PlanStage stage;  // carried over from build to build of the same plan
   int32_t max_seen = 0;           // the most keys a request holds
+  int32_t page_keys = 0;          // the most keys one could hold in as many pages, the others keeping one each
   int64_t tiles = 0;              // tiles of 128 keys over all requests (one KV head)
   std::vector<int32_t> host_ids;  // the page list, for the check below
   mutable int8_t shared = -1;     // a page is listed twice (-1: not looked at yet)
@@ -354,6 +355,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.dev = d; q.dev_elems = host.size();
   q.dev_cap = fresh ? bytes : p->dev_cap;
   q.max_seen = max_seen;
+  q.page_keys = num_req > 0 ? (int32_t)std::min<int64_t>((int64_t)(NP - num_req + 1) * ps, INT32_MAX) : 0;
   q.tiles = tiles;
   q.host_ids = std::move(pids);
 
@@ -384,6 +386,17 @@ PlanDev plan_dev(const pg_plan* p) {
   v.num_pairs = p->num_pairs;
   v.ring = p->ring;
   return v;
+}
+
+// A captured launch is replayed under plans that are updated in place: what it bakes in has to hold
+// for any plan of as many requests, tokens and pages.
+bool capturing(cudaStream_t stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream beside another stream's capture: the launch reports it)
+    return false;
+  }
+  return st == cudaStreamCaptureStatusActive;
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -703,8 +716,9 @@ int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer,
   if ((uintptr_t)src & 3u) return PG_ERR_ALIGN;
   // every grid of the call fits
   int64_t segs = 0, blocks = 0;
-  const int32_t per_seg = std::max(evict_select_ranks(plan->max_seen),
-                                   evict_apply_blocks(std::min(plan->max_seen, budget)));
+  // (slots of the budget that no request fills hold -1: they need no block of apply)
+  a->slots = std::min(capturing(stream) ? plan->page_keys : plan->max_seen, budget);
+  const int32_t per_seg = std::max(evict_select_ranks(plan->max_seen), evict_apply_blocks(a->slots));
   if (!mul_i64(num_layers, plan->num_req, &segs) || !mul_i64(segs, plan->num_kv_heads, &segs) ||
       !mul_i64(segs, per_seg, &blocks) || !fits_i32(segs) || !fits_i32(blocks))
     return PG_ERR_I32_OVERFLOW;

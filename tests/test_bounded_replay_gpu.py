@@ -1,0 +1,89 @@
+"""Captured bounded-cache calls replayed under plans that are updated in place (GPU): as many
+requests, tokens and pages as the capture had, held by other requests than before. References and
+tolerances: bounded_ref.py."""
+import numpy as np
+import pytest
+import torch
+
+from bounded_ref import Case, apply_reference, select_reference
+from paged_sliding_window_qkv_gb300 import pg
+
+pytestmark = pytest.mark.gpu
+
+
+def replan(c, qo, start, seed):
+    """The case's plan, updated in place to other lengths and another order of as many pages."""
+    tokens, pages, storage = int(c.qo.sum()), len(c.ids), c.plan.info().d_page_ids
+    c.qo, c.start = np.asarray(qo, np.int64), np.asarray(start, np.int64)
+    c.n = c.start + c.qo - c.ks
+    npg = (c.n + c.ps - 1) // c.ps
+    assert int(c.qo.sum()) == tokens and int(npg.sum()) == pages
+    c.pg_indptr = np.concatenate([[0], np.cumsum(npg)])
+    c.qo_indptr = np.concatenate([[0], np.cumsum(c.qo)])
+    c.ids = np.random.Generator(np.random.PCG64(seed)).permutation(c.P)[:pages].astype(np.int32)
+    c.last = (c.n - (npg - 1) * c.ps).astype(np.int32)
+    rc, _ = pg.pg_plan_paged_segment(c.plan, len(c.qo), c.qo_indptr, c.pg_indptr, c.ids, c.last, c.ks,
+                                     c.start, c.hq, c.hkv, c.D, c.ps, c.stream)
+    pg.check(rc)
+    assert c.plan.info().d_page_ids == storage  # in place
+
+
+def capture(call, stream):
+    call()  # eager: configures every kernel once
+    stream.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        call()
+    return g
+
+
+def refill(c, seed, evicted=0):
+    """Distinct positions in any order, and masses with ties, into the case's own statistics."""
+    g = np.random.Generator(np.random.PCG64(seed))
+    pos, mass = c.pos_cpu.numpy(), c.mass_cpu.numpy()
+    for layer in range(c.layers):
+        for r in range(len(c.qo)):
+            page, off = c.rows_of(r)
+            for h in range(c.hkv):
+                pos[layer, page, h, off] = g.permutation(int(c.n[r]))
+                m = g.exponential(1.0, int(c.n[r])).astype(np.float32)
+                m[g.random(len(m)) < 0.2] = 0.5
+                mass[layer, page, h, off] = m
+    c.mass.copy_(c.mass_cpu)
+    c.pos.copy_(c.pos_cpu)
+
+
+# (head_dim, KV heads, page size, layers, keys captured, keys replayed, budget)
+GROWN = [
+    (512, 1, 256, 1, [300], [500], 450),             # inside the last page
+    (512, 1, 16, 2, [256, 256], [496, 16], 300),     # pages move to one request
+    (256, 2, 16, 1, [100, 100], [40, 170], 150),
+    (256, 2, 5, 1, [200, 200], [395, 5], 350),       # no power of two
+    (512, 1, 3, 1, [9, 9, 9], [21, 3, 3], 20),
+    (256, 8, 16, 4, [300] * 20, [2400] + [192] * 18 + [224], 2200),  # next to none move
+]
+
+
+@pytest.mark.parametrize("D,hkv,ps,layers,before,after,budget", GROWN)
+def test_captured_apply_moves_every_kept_key(D, hkv, ps, layers, before, after, budget):
+    s = torch.cuda.Stream()
+    every = list(range(layers))
+    with torch.cuda.stream(s):
+        c = Case(D, hkv, hkv, [1] * len(before), np.array(before) - 1, ps=ps, layers=layers, seed=budget,
+                 stream=s)
+        c.build()
+        src = torch.full((layers, len(before), hkv, budget), -1, dtype=torch.int32, device="cuda")
+        g = capture(lambda: pg.check(pg.pg_kv_evict_apply(c.plan, c.desc, c.stats, 0, layers, budget, src, s)), s)
+        for turn, n in enumerate((after, before, after)):
+            replan(c, [1] * len(n), np.array(n) - 1, turn)
+            refill(c, turn)
+            c.pool.copy_(c.pool_cpu)
+            want = select_reference(c, budget, 1, 2, c.mass_cpu.numpy(), c.pos_cpu.numpy(), every)
+            src.copy_(torch.from_numpy(want))
+            g.replay()
+            s.synchronize()
+            assert pg.pg_device_status(s) == pg.PG_OK
+            pool, mass, pos = apply_reference(c, want, every, c.pool_cpu, c.mass_cpu, c.pos_cpu)
+            assert torch.equal(c.pool.view(torch.int16).cpu(), pool.view(torch.int16))
+            assert torch.equal(c.mass.cpu(), mass) and torch.equal(c.pos.cpu(), pos)
+    c.close()
