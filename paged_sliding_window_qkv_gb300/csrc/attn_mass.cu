@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(kDecThreads) mass_decode_kernel(MassArgs m, in
 }
 
 // Prefill, any page size: one CTA per (request, KV head, 64 keys), four warps of 16 keys each;
-// the keys stay in shared memory while the query rows that see them pass by 32 at a time.
+// the keys stay in shared memory while the query rows that see them pass by 32 at a time. (A graph's
+// plan may have grown since the capture: a request's CTAs stride over its keys.)
 constexpr int kKeys = 64, kRows = 32, kMassThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, int32_t tiles_per_req) {
@@ -98,84 +99,86 @@ __global__ void __launch_bounds__(kMassThreads) mass_prefill_kernel(MassArgs m, 
   const int32_t kt = ((int32_t)blockIdx.x / Hkv) % tiles_per_req;
   const int32_t r = (int32_t)blockIdx.x / Hkv / tiles_per_req;
   const MassReq q = mass_req(a.plan, r, ps);
-  const int32_t rel0 = kt * kKeys;
-  if (rel0 >= q.n) return;
-  const int32_t k0 = q.ks0 + rel0, nk = min(kKeys, q.n - rel0);
-  // K rows; rows of no key, or on a page that is out of range, are zero
-  for (int idx = tid; idx < kKeys * CH; idx += kMassThreads) {
-    const int k = idx / CH, c = idx % CH;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (k < nk) {
-      const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
-      if (page < a.pool.num_pages)
-        v = *reinterpret_cast<const uint4*>(a.pool.layer_base + (int64_t)page * a.pool.stride_page +
-                                            (int64_t)g * a.pool.stride_head +
-                                            (int64_t)((rel0 + k) % ps) * D + c * 8);
-    }
-    *reinterpret_cast<uint4*>(sK + swz<D>(k, c)) = v;
-  }
-  // the tokens that may see a key of the tile
   const int32_t W = a.window_left;
-  const int32_t t0 = max(0, k0 - q.sp);
-  int64_t t1 = q.len;
-  if (W >= 0 && k0 >= a.num_sink) t1 = min(t1, (int64_t)k0 + nk - 1 + W - q.sp + 1);
-  const int64_t row_end = t1 * G;
   const int gid = lane >> 2, tig = lane & 3;
-  float sum[2] = {0.f, 0.f};
-  for (int64_t row0 = (int64_t)t0 * G; row0 < row_end; row0 += kRows) {
-    __syncthreads();  // the previous rows have been read
-    for (int idx = tid; idx < kRows * CH; idx += kMassThreads) {
-      const int n = idx / CH, c = idx % CH;
-      const int64_t row = row0 + n;
+  for (int64_t first = (int64_t)kt * kKeys; first < q.n; first += (int64_t)tiles_per_req * kKeys) {
+    const int32_t rel0 = (int32_t)first;
+    __syncthreads();  // the previous keys have been read
+    const int32_t k0 = q.ks0 + rel0, nk = min(kKeys, q.n - rel0);
+    // K rows; rows of no key, or on a page that is out of range, are zero
+    for (int idx = tid; idx < kKeys * CH; idx += kMassThreads) {
+      const int k = idx / CH, c = idx % CH;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (row < row_end)
-        v = *reinterpret_cast<const uint4*>(
-            a.q + ((q.q0 + row / G) * Hq + g * G + row % G) * (int64_t)D + c * 8);
-      *reinterpret_cast<uint4*>(sQ + swz<D>(n, c)) = v;
-    }
-    if (tid < kRows) {
-      const int64_t row = row0 + tid;
-      sL[tid] = row < row_end ? a.lse[(q.q0 + row / G) * Hq + g * G + row % G] * kLog2e : 0.f;
-    }
-    __syncthreads();
-    float acc[kRows / 8][4] = {};
-    for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t af[4];
-      ldsm_x4(smem_u32(sK) + swz<D>(warp * 16 + (lane & 7) + 8 * ((lane >> 3) & 1), kk * 2 + (lane >> 4)), af);
-#pragma unroll
-      for (int nt = 0; nt < kRows / 8; nt += 2) {
-        uint32_t bf[4];
-        ldsm_x4(smem_u32(sQ) + swz<D>(nt * 8 + (lane & 7) + 8 * (lane >> 4), kk * 2 + ((lane >> 3) & 1)), bf);
-        mma_bf16(acc[nt], af, bf[0], bf[1]);
-        mma_bf16(acc[nt + 1], af, bf[2], bf[3]);
+      if (k < nk) {
+        const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
+        if (page < a.pool.num_pages)
+          v = *reinterpret_cast<const uint4*>(a.pool.layer_base + (int64_t)page * a.pool.stride_page +
+                                              (int64_t)g * a.pool.stride_head +
+                                              (int64_t)((rel0 + k) % ps) * D + c * 8);
       }
+      *reinterpret_cast<uint4*>(sK + swz<D>(k, c)) = v;
     }
-    float part[2] = {0.f, 0.f};
-#pragma unroll
-    for (int nt = 0; nt < kRows / 8; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = nt * 8 + 2 * tig + (e & 1);
-        const int64_t row = row0 + col;
-        const int32_t p = q.sp + (int32_t)(row / G);
-        const int32_t j = k0 + warp * 16 + gid + 8 * (e >> 1);
-        const bool vis = row < row_end && j <= p && (W < 0 || p - j <= W || j < a.num_sink);
-        if (vis) part[e >> 1] += ex2(acc[nt][e] * a.sm_scale_log2 - sL[col]);
+    // the tokens that may see a key of the tile
+    const int32_t t0 = max(0, k0 - q.sp);
+    int64_t t1 = q.len;
+    if (W >= 0 && k0 >= a.num_sink) t1 = min(t1, (int64_t)k0 + nk - 1 + W - q.sp + 1);
+    const int64_t row_end = t1 * G;
+    float sum[2] = {0.f, 0.f};
+    for (int64_t row0 = (int64_t)t0 * G; row0 < row_end; row0 += kRows) {
+      __syncthreads();  // the previous rows have been read
+      for (int idx = tid; idx < kRows * CH; idx += kMassThreads) {
+        const int n = idx / CH, c = idx % CH;
+        const int64_t row = row0 + n;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row < row_end)
+          v = *reinterpret_cast<const uint4*>(
+              a.q + ((q.q0 + row / G) * Hq + g * G + row % G) * (int64_t)D + c * 8);
+        *reinterpret_cast<uint4*>(sQ + swz<D>(n, c)) = v;
       }
-    }
-    sum[0] += part[0];
-    sum[1] += part[1];
-  }
+      if (tid < kRows) {
+        const int64_t row = row0 + tid;
+        sL[tid] = row < row_end ? a.lse[(q.q0 + row / G) * Hq + g * G + row % G] * kLog2e : 0.f;
+      }
+      __syncthreads();
+      float acc[kRows / 8][4] = {};
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t af[4];
+        ldsm_x4(smem_u32(sK) + swz<D>(warp * 16 + (lane & 7) + 8 * ((lane >> 3) & 1), kk * 2 + (lane >> 4)), af);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float s = sum[e];
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    const int k = warp * 16 + gid + 8 * e;
-    if (tig == 0 && k < nk && mass_seen(a, q, rel0 + k)) {
-      const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
-      if (page < a.pool.num_pages) mass_store(a, q, page, g, rel0 + k, s);
-      else atomicOr(a.status, kStatusBounds);
+        for (int nt = 0; nt < kRows / 8; nt += 2) {
+          uint32_t bf[4];
+          ldsm_x4(smem_u32(sQ) + swz<D>(nt * 8 + (lane & 7) + 8 * (lane >> 4), kk * 2 + ((lane >> 3) & 1)), bf);
+          mma_bf16(acc[nt], af, bf[0], bf[1]);
+          mma_bf16(acc[nt + 1], af, bf[2], bf[3]);
+        }
+      }
+      float part[2] = {0.f, 0.f};
+#pragma unroll
+      for (int nt = 0; nt < kRows / 8; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = nt * 8 + 2 * tig + (e & 1);
+          const int64_t row = row0 + col;
+          const int32_t p = q.sp + (int32_t)(row / G);
+          const int32_t j = k0 + warp * 16 + gid + 8 * (e >> 1);
+          const bool vis = row < row_end && j <= p && (W < 0 || p - j <= W || j < a.num_sink);
+          if (vis) part[e >> 1] += ex2(acc[nt][e] * a.sm_scale_log2 - sL[col]);
+        }
+      }
+      sum[0] += part[0];
+      sum[1] += part[1];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = sum[e];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      const int k = warp * 16 + gid + 8 * e;
+      if (tig == 0 && k < nk && mass_seen(a, q, rel0 + k)) {
+        const int32_t page = mass_page(a.plan, q, rel0 + k, ps, a.pool.num_pages);
+        if (page < a.pool.num_pages) mass_store(a, q, page, g, rel0 + k, s);
+        else atomicOr(a.status, kStatusBounds);
+      }
     }
   }
 }

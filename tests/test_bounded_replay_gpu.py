@@ -87,3 +87,40 @@ def test_captured_apply_moves_every_kept_key(D, hkv, ps, layers, before, after, 
             assert torch.equal(c.pool.view(torch.int16).cpu(), pool.view(torch.int16))
             assert torch.equal(c.mass.cpu(), mass) and torch.equal(c.pos.cpu(), pos)
     c.close()
+
+
+def replayed_weights(D, hq, hkv, ps, shapes, window, sinks):
+    """Weights captured at the first of shapes [(tokens, keys) of each request, ...] and replayed at
+    all of them in turn, each against 64 bits."""
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        (qo, n), rest = shapes[0], shapes[1:]
+        c = Case(D, hq, hkv, qo, np.array(n) - qo, ps=ps, seed=ps, stream=s).build()
+        g = capture(lambda: c.weigh(window, sinks), s)
+        for turn, (qo, n) in enumerate([*rest, shapes[0], *rest]):
+            replan(c, qo, np.array(n) - qo, turn)
+            c.mass.copy_(c.mass_cpu)
+            c.pos.copy_(c.pos_cpu)
+            c.out.fill_(float("nan"))
+            c.lse.fill_(float("nan"))
+            c.ws.fill_(0xFF)
+            g.replay()
+            s.synchronize()
+            assert pg.pg_device_status(s) == pg.PG_OK
+            c.reference(window, sinks)
+            c.check_attention(f"{n}")
+            c.check_mass(f"{n}")
+    c.close()
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(256, 4, 2), (512, 4, 1)])
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (90, 5)])
+@pytest.mark.parametrize("ps,qo,before,after", [
+    (5, [20], [62], [65]),                     # inside the last page, past a block of 64 keys
+    (3, [10, 10], [150, 150], [288, 10]),      # pages move to one request
+    (1, [7, 30, 5], [100, 40, 60], [8, 187, 5]),
+    (16, [10, 33], [150, 160], [16, 300]),
+    (64, [40, 200], [250, 260], [40, 440]),
+])
+def test_captured_prompt_weights_follow_the_plan(D, hq, hkv, window, sinks, ps, qo, before, after):
+    replayed_weights(D, hq, hkv, ps, [(qo, before), (qo, after)], window, sinks)
