@@ -120,7 +120,7 @@ def replayed_weights(D, hq, hkv, ps, shapes, window, sinks):
     (3, [10, 10], [150, 150], [288, 10]),      # pages move to one request
     (1, [7, 30, 5], [100, 40, 60], [8, 187, 5]),
     (16, [10, 33], [150, 160], [16, 300]),
-    (64, [40, 200], [250, 260], [40, 440]),
+    (64, [40, 200], [250, 260], [40, 500]),
 ])
 def test_captured_prompt_weights_follow_the_plan(D, hq, hkv, window, sinks, ps, qo, before, after):
     replayed_weights(D, hq, hkv, ps, [(qo, before), (qo, after)], window, sinks)
