@@ -176,6 +176,115 @@ struct Counter {
   }
 };
 
+// A segment of any length in one CTA, whose keys are read again for each of four 8-bit histogram passes
+// and the two ranking passes.
+constexpr int kLongThreads = 1024;
+struct LongShared {
+  uint32_t hist[256];
+  int32_t warp_sum[kLongThreads / 32];
+  uint32_t prefix;
+  int32_t need;
+};
+__device__ __forceinline__ uint32_t order_at(const EvictArgs& a, const Seg& q, int64_t recent, int32_t slot) {
+  const int32_t page = page_of(a, q, slot);
+  if (page < 0) {
+    atomicOr(a.status, kStatusBounds);
+    return 1u;
+  }
+  const int64_t at = stat_at(a, q, page, slot);
+  return order_of(a, recent, a.stats.pos[at], a.stats.mass[at]);
+}
+// Inclusive counts over the block of a predicate, in thread order; *total the block's sum.
+template <int NT>
+__device__ __forceinline__ int32_t block_rank(bool v, int32_t* warp_sum, int32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t b = __ballot_sync(0xffffffffu, v);
+  if (lane == 0) warp_sum[warp] = __popc(b);
+  __syncthreads();
+  int32_t before = 0, all = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    const int32_t c = warp_sum[w];
+    before += w < warp ? c : 0;
+    all += c;
+  }
+  __syncthreads();
+  *total = all;
+  return before + __popc(b & ((2u << lane) - 1u));
+}
+
+// (Not inlined: the select kernel takes it for a plan that grew past its captured launch, and should
+// keep its registers for the others.)
+template <int NT>
+__device__ __noinline__ void select_long(const EvictArgs& a, const Seg& q, int64_t recent, int32_t* src,
+                                         LongShared& sh) {
+  const int tid = threadIdx.x;
+  for (int32_t s = q.keep + tid; s < a.budget; s += NT) src[s] = -1;
+  if (q.keep == q.n) {
+    for (int32_t s = tid; s < q.keep; s += NT) src[s] = s;
+    return;
+  }
+  // ---- the order value of the keep-th key, and how many of its equals are kept
+  uint32_t prefix = 0u;
+  int32_t need = q.keep;  // keys still to take among those matching the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += NT) sh.hist[i] = 0u;
+    __syncthreads();
+    for (int32_t s = tid; s < q.n; s += NT) {
+      const uint32_t o = order_at(a, q, recent, s);
+      if (shift == 24 || (o >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&sh.hist[(o >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int32_t left = need;
+      int b = 255;
+      while (b > 0 && (int32_t)sh.hist[b] < left) left -= (int32_t)sh.hist[b--];
+      sh.prefix = prefix | ((uint32_t)b << shift);
+      sh.need = left;
+    }
+    __syncthreads();
+    prefix = sh.prefix;
+    need = sh.need;
+    __syncthreads();
+  }
+  // ---- kept keys at or past the new length, in slot order, listed in src[0, movers)
+  int32_t ties = 0, ties_low = 0, movers = 0;
+  for (int32_t s0 = 0; s0 < q.n; s0 += NT) {
+    const int32_t s = s0 + tid;
+    const uint32_t o = s < q.n ? order_at(a, q, recent, s) : 0u;
+    const bool tie = s < q.n && o == prefix;
+    int32_t total;
+    const int32_t t = block_rank<NT>(tie, sh.warp_sum, &total);
+    const bool kept = s < q.n && (o > prefix || (tie && ties + t <= need));
+    ties += total;
+    ties_low += __syncthreads_count(tie && s < q.keep);
+    const bool mover = kept && s >= q.keep;
+    const int32_t k = block_rank<NT>(mover, sh.warp_sum, &total);
+    if (mover) src[movers + k - 1] = s;
+    movers += total;
+  }
+  __syncthreads();
+  // ---- holes below the new length, from the last block of slots to the first: a block reads
+  // the list entries of its holes (a hole's rank is at most its slot) before it writes its slots
+  int32_t holes_left = movers, ties_left = ties_low;
+  for (int32_t s0 = (q.keep - 1) / NT * NT; s0 >= 0; s0 -= NT) {
+    const int32_t s = s0 + tid;
+    const bool in = s < q.keep;
+    const uint32_t o = in ? order_at(a, q, recent, s) : 0u;
+    const bool tie = in && o == prefix;
+    int32_t total;
+    const int32_t t = block_rank<NT>(tie, sh.warp_sum, &total);
+    ties_left -= total;
+    const bool hole = in && !(o > prefix || (tie && ties_left + t <= need));
+    const int32_t k = block_rank<NT>(hole, sh.warp_sum, &total);
+    holes_left -= total;
+    const int32_t from = hole ? src[holes_left + k - 1] : s;
+    __syncthreads();
+    if (in) src[s] = from;
+    __syncthreads();
+  }
+}
+
 template <int NT, int KPT, bool CL, bool V4>
 __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a, int32_t ranks) {
   // kept keys past the new length, by rank: at most half of the cluster's slots, spread over it
@@ -194,15 +303,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
   int32_t* src = a.src + (int64_t)seg * a.budget;
   const int tid = threadIdx.x;
   const int32_t step = CL ? NT * ranks : NT, first = rank * NT + tid;
-  const bool fits = q.n <= NT * KPT * (CL ? ranks : 1);
-  // every slot keeps its key until a hole below says otherwise
-  if (!CL || q.keep == q.n || !fits)  // (a cluster that goes on does it below)
-    for (int32_t s = first; s < a.budget; s += step) src[s] = s < q.keep ? s : -1;
-  if (q.keep == q.n) return;  // (the whole cluster)
-  if (!fits) {  // a plan that grew past its captured launch
-    if (tid == 0) atomicOr(a.status, kStatusBounds);
+  if (q.keep != q.n && q.n > NT * KPT * (CL ? ranks : 1)) {  // a plan that grew past its captured launch
+    static_assert(NT * (KPT / 4 | 1) * 16 >= (int)sizeof(LongShared), "shared memory");
+    if (rank == 0) select_long<NT>(a, q, recent, src, *reinterpret_cast<LongShared*>(stage));
     return;
   }
+  // every slot keeps its key until a hole below says otherwise
+  if (!CL || q.keep == q.n)  // (a cluster that goes on does it below)
+    for (int32_t s = first; s < a.budget; s += step) src[s] = s < q.keep ? s : -1;
+  if (q.keep == q.n) return;  // (the whole cluster)
   if constexpr (CL) {
     // (the cluster's barriers order every slot before the holes); and every peer runs before its
     // shared memory is written
@@ -488,110 +597,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
   if constexpr (CL) cluster_barrier();  // the peers have read this CTA's list
 }
 
-// Segments longer than a cluster's registers (131,072 keys): one CTA, the keys read again for
-// each of four 8-bit histogram passes and the two ranking passes.
-constexpr int kLongThreads = 1024;
-constexpr int kLongWarps = kLongThreads / 32;
-__device__ __forceinline__ uint32_t order_at(const EvictArgs& a, const Seg& q, int64_t recent, int32_t slot) {
-  const int32_t page = page_of(a, q, slot);
-  if (page < 0) {
-    atomicOr(a.status, kStatusBounds);
-    return 1u;
-  }
-  const int64_t at = stat_at(a, q, page, slot);
-  return order_of(a, recent, a.stats.pos[at], a.stats.mass[at]);
-}
-// Inclusive counts over the block of a predicate, in thread order; *total the block's sum.
-__device__ __forceinline__ int32_t block_rank(bool v, int32_t* warp_sum, int32_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t b = __ballot_sync(0xffffffffu, v);
-  if (lane == 0) warp_sum[warp] = __popc(b);
-  __syncthreads();
-  int32_t before = 0, all = 0;
-  for (int w = 0; w < kLongWarps; ++w) {
-    const int32_t c = warp_sum[w];
-    before += w < warp ? c : 0;
-    all += c;
-  }
-  __syncthreads();
-  *total = all;
-  return before + __popc(b & ((2u << lane) - 1u));
-}
-
+// Segments longer than a cluster's registers (131,072 keys).
 __global__ void __launch_bounds__(kLongThreads) evict_select_long_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ int32_t warp_sum[kLongWarps];
-  __shared__ uint32_t s_prefix;
-  __shared__ int32_t s_need;
+  __shared__ LongShared sh;
   const Seg q = load_seg(a, (int32_t)blockIdx.x);
-  const int64_t recent = recent_from(a, q);
-  int32_t* src = a.src + (int64_t)blockIdx.x * a.budget;
-  const int tid = threadIdx.x;
-  for (int32_t s = q.keep + tid; s < a.budget; s += kLongThreads) src[s] = -1;
-  if (q.keep == q.n) {
-    for (int32_t s = tid; s < q.keep; s += kLongThreads) src[s] = s;
-    return;
-  }
-  // ---- the order value of the keep-th key, and how many of its equals are kept
-  uint32_t prefix = 0u;
-  int32_t need = q.keep;  // keys still to take among those matching the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kLongThreads) hist[i] = 0u;
-    __syncthreads();
-    for (int32_t s = tid; s < q.n; s += kLongThreads) {
-      const uint32_t o = order_at(a, q, recent, s);
-      if (shift == 24 || (o >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&hist[(o >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int32_t left = need;
-      int b = 255;
-      while (b > 0 && (int32_t)hist[b] < left) left -= (int32_t)hist[b--];
-      s_prefix = prefix | ((uint32_t)b << shift);
-      s_need = left;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    __syncthreads();
-  }
-  // ---- kept keys at or past the new length, in slot order, listed in src[0, movers)
-  int32_t ties = 0, ties_low = 0, movers = 0;
-  for (int32_t s0 = 0; s0 < q.n; s0 += kLongThreads) {
-    const int32_t s = s0 + tid;
-    const uint32_t o = s < q.n ? order_at(a, q, recent, s) : 0u;
-    const bool tie = s < q.n && o == prefix;
-    int32_t total;
-    const int32_t t = block_rank(tie, warp_sum, &total);
-    const bool kept = s < q.n && (o > prefix || (tie && ties + t <= need));
-    ties += total;
-    ties_low += __syncthreads_count(tie && s < q.keep);
-    const bool mover = kept && s >= q.keep;
-    const int32_t k = block_rank(mover, warp_sum, &total);
-    if (mover) src[movers + k - 1] = s;
-    movers += total;
-  }
-  __syncthreads();
-  // ---- holes below the new length, from the last block of slots to the first: a block reads
-  // the list entries of its holes (a hole's rank is at most its slot) before it writes its slots
-  int32_t holes_left = movers, ties_left = ties_low;
-  for (int32_t s0 = (q.keep - 1) / kLongThreads * kLongThreads; s0 >= 0; s0 -= kLongThreads) {
-    const int32_t s = s0 + tid;
-    const bool in = s < q.keep;
-    const uint32_t o = in ? order_at(a, q, recent, s) : 0u;
-    const bool tie = in && o == prefix;
-    int32_t total;
-    const int32_t t = block_rank(tie, warp_sum, &total);
-    ties_left -= total;
-    const bool hole = in && !(o > prefix || (tie && ties_left + t <= need));
-    const int32_t k = block_rank(hole, warp_sum, &total);
-    holes_left -= total;
-    const int32_t from = hole ? src[holes_left + k - 1] : s;
-    __syncthreads();
-    if (in) src[s] = from;
-    __syncthreads();
-  }
+  select_long<kLongThreads>(a, q, recent_from(a, q), a.src + (int64_t)blockIdx.x * a.budget, sh);
 }
 
 // ------------------------------------------------------------------ apply

@@ -128,9 +128,9 @@ struct EvictArgs {
   int32_t* src;           // [num_layers][num_req][num_kv_heads][budget]
   int32_t num_layers, budget, num_sink, num_recent;
   int32_t max_keys;       // the plan's longest request
-  int32_t slots;          // apply: the launch covers slots [0, slots) of every segment
   uint32_t page_mul, page_shift;  // division by the page size (page_mul 0: page size 1)
   int* status;
+  int32_t slots;          // apply: the launch covers slots [0, slots) of every segment
 };
 
 // Bounded-wait settings for the next launches: the default limit, or the test hook's.

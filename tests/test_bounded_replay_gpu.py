@@ -124,3 +124,43 @@ def replayed_weights(D, hq, hkv, ps, shapes, window, sinks):
 ])
 def test_captured_prompt_weights_follow_the_plan(D, hq, hkv, window, sinks, ps, qo, before, after):
     replayed_weights(D, hq, hkv, ps, [(qo, before), (qo, after)], window, sinks)
+
+
+# (head_dim, KV heads, page size, layers, keys captured, keys replayed, budget): the replayed segments
+# are longer than the registers that the captured choice holds its keys in
+@pytest.mark.parametrize("D,hkv,ps,layers,before,after,budget", [
+    (256, 2, 16, 1, [400, 400], [784, 16], 300),
+    (256, 2, 5, 2, [400, 400], [795, 5], 500),
+    (512, 1, 16, 1, [1000, 1000], [2000, 16], 1500),
+    (512, 1, 3, 1, [2000, 2000], [3999, 3], 100),
+    (256, 1, 16, 1, [20000, 17000], [36992, 16], 20000),                 # a cluster's
+    (256, 8, 16, 2, [1100] * 20, [16] * 19 + [21776], 5000),
+])
+def test_captured_choice_of_grown_requests(D, hkv, ps, layers, before, after, budget):
+    s = torch.cuda.Stream()
+    every = list(range(layers))
+    with torch.cuda.stream(s):
+        c = Case(D, hkv, hkv, [1] * len(before), np.array(before) - 1, ps=ps, layers=layers, seed=budget,
+                 stream=s)
+        c.build()
+        src = torch.full((layers, len(before), hkv, budget), -1, dtype=torch.int32, device="cuda")
+
+        def call():
+            pg.check(pg.pg_kv_evict_select(c.plan, c.stats, 0, layers, budget, 3, 40, src, s))
+            pg.check(pg.pg_kv_evict_apply(c.plan, c.desc, c.stats, 0, layers, budget, src, s))
+
+        g = capture(call, s)
+        for turn, n in enumerate((after, before)):
+            replan(c, [1] * len(n), np.array(n) - 1, turn)
+            refill(c, turn)
+            c.pool.copy_(c.pool_cpu)
+            src.fill_(-99)
+            g.replay()
+            s.synchronize()
+            assert pg.pg_device_status(s) == pg.PG_OK
+            want = select_reference(c, budget, 3, 40, c.mass_cpu.numpy(), c.pos_cpu.numpy(), every)
+            assert (src.cpu().numpy() == want).all()
+            pool, mass, pos = apply_reference(c, want, every, c.pool_cpu, c.mass_cpu, c.pos_cpu)
+            assert torch.equal(c.pool.view(torch.int16).cpu(), pool.view(torch.int16))
+            assert torch.equal(c.mass.cpu(), mass) and torch.equal(c.pos.cpu(), pos)
+    c.close()
