@@ -37,6 +37,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
 constexpr int kDecTile = 32;  // keys per tile of the decode form
+// Key tiles per decode chunk. The launch and the workspace have max_chunks chunks a request; where a
+// graph's plan has outgrown them since the capture, its chunks are longer instead.
+__device__ __forceinline__ int32_t chunk_tiles(const AttnArgs& a, int32_t tiles) {
+  const int32_t ct = a.kv_chunk / kDecTile;
+  return tiles <= (int64_t)ct * a.max_chunks ? ct : (tiles + a.max_chunks - 1) / a.max_chunks;
+}
 constexpr float kLn2 = 0.69314718055994531f;  // log2 units to natural log
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -162,18 +168,19 @@ attn_split_kernel(AttnArgs a) {
     lo = walk.lo;
     ntiles = walk.total;
     if (C::DECODE) {
-      const int32_t ct = a.kv_chunk / BN;
+      const int32_t ct = chunk_tiles(a, walk.total);
       nchunks = (walk.total + ct - 1) / ct;
       if (chunk >= max(nchunks, 1)) return;
       vt0 = chunk * ct;
       ntiles = min(ct, walk.total - vt0);
     }
   } else if (C::DECODE) {
-    nchunks = (hi - lo + a.kv_chunk - 1) / a.kv_chunk;
+    const int32_t keys = chunk_tiles(a, (hi - lo + BN - 1) / BN) * BN;
+    nchunks = (hi - lo + keys - 1) / keys;
     // a row that sees no key (possible in a key segment) is still written, by chunk 0
     if (chunk >= max(nchunks, 1)) return;
-    lo = lo + chunk * a.kv_chunk;
-    hi = min(hi, lo + a.kv_chunk);
+    lo = lo + chunk * keys;
+    hi = min(hi, lo + keys);
   }
   if constexpr (!BC) ntiles = (hi - lo + BN - 1) / BN;
   // first key of the CTA's it-th tile
@@ -500,16 +507,10 @@ attn_merge_kernel(AttnArgs a) {
   const int32_t W = a.window_left;
   const int32_t lo = W >= 0 ? max(ks0, p - W) : ks0;
   const int32_t hi = min(p + 1, kv_len);
-  int32_t nch = (hi - lo + a.kv_chunk - 1) / a.kv_chunk;
-  if constexpr (BC) {
-    // the key walk is counted in the partition kernel's tiles; a chunk is a whole number of them
-    const KeyWalk walk = key_walk(W, a.num_sink, ks0, kv_len, p, p, kDecTile);
-    nch = (walk.total + a.kv_chunk / kDecTile - 1) / (a.kv_chunk / kDecTile);
-    if (nch > a.max_chunks) {  // a plan that grew past the launch it was captured with
-      if (threadIdx.x == 0) atomicOr(a.status, kStatusBounds);
-      nch = a.max_chunks;
-    }
-  }
+  // the keys are counted in the partition kernel's tiles; a chunk is a whole number of them
+  int32_t tiles = (hi - lo + kDecTile - 1) / kDecTile;
+  if constexpr (BC) tiles = key_walk(W, a.num_sink, ks0, kv_len, p, p, kDecTile).total;
+  const int32_t ct = chunk_tiles(a, tiles), nch = (tiles + ct - 1) / ct;
   if (nch <= 1) return;  // written directly by the partition kernel
   const int64_t row = ((int64_t)r * a.num_qo_heads + h) * a.max_chunks;
   const int tid = threadIdx.x, lane = tid & 31;

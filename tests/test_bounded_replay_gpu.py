@@ -164,3 +164,51 @@ def test_captured_choice_of_grown_requests(D, hkv, ps, layers, before, after, bu
             assert torch.equal(c.pool.view(torch.int16).cpu(), pool.view(torch.int16))
             assert torch.equal(c.mass.cpu(), mass) and torch.equal(c.pos.cpu(), pos)
     c.close()
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(256, 4, 2), (256, 16, 8), (512, 4, 1), (512, 16, 1)])
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (900, 70)])
+@pytest.mark.parametrize("ps,before,after", [
+    (5, [600, 600], [1195, 5]),                # more chunks than the launch has
+    (1, [40, 300, 20], [2, 355, 3]),
+    (3, [30, 30, 30], [33, 27, 30]),
+    (16, [600, 600], [1200, 16]),
+    (256, [200, 300], [256, 500]),
+])
+def test_captured_token_weights_follow_the_plan(D, hq, hkv, window, sinks, ps, before, after):
+    one = [1] * len(before)
+    replayed_weights(D, hq, hkv, ps, [(one, before), (one, after)], window, sinks)
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(256, 4, 2), (512, 4, 1)])
+@pytest.mark.parametrize("window", [-1, 900])
+@pytest.mark.parametrize("ps,before,after", [(5, [600, 600], [1195, 5]), (1, [40, 300, 20], [2, 355, 3]),
+                                             (16, [600, 600], [1200, 16])])
+def test_captured_windowed_decode_follows_the_plan(D, hq, hkv, window, ps, before, after):
+    """The entries without sinks, whose decode form of other page sizes has the same chunks."""
+    fn = pg.pg_attn_paged_prefill_lse if D == 256 else pg.pg_attn_paged_prefill_hd512_lse
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        one = [1] * len(before)
+        c = Case(D, hq, hkv, one, np.array(before) - 1, ps=ps, seed=ps, stream=s).build()
+        n = pg.pg_workspace_bytes(c.plan)
+
+        def call():
+            pg.check(fn(c.plan, c.desc, 0, c.q, c.out, c.lse, window, 1.0, c.ws, n, s))
+
+        g = capture(call, s)
+        for turn, keys in enumerate((after, before, after)):
+            replan(c, one, np.array(keys) - 1, turn)
+            c.out.fill_(float("nan"))
+            c.ws.fill_(0xFF)
+            g.replay()
+            s.synchronize()
+            assert pg.pg_device_status(s) == pg.PG_OK
+            out, lse, _, _, wabs = c.reference(window, 0)
+            # (these entries sum the rounded weights: each within half a step of its own, so the sum
+            # is, and with it lse, which is off by at most 2^-8 more than bounded_ref.py says)
+            got = c.out.double().cpu().numpy()
+            assert (np.abs(got - out) <= 2.0 ** -8 * (2 * wabs + np.abs(out)) + c.e * wabs + 1e-30).all()
+            got = c.lse.double().cpu().numpy()
+            assert (np.abs(got - lse) <= 2.0 ** -8 + c.e + 2.0 ** -22 * np.abs(lse)).all()
+    c.close()
