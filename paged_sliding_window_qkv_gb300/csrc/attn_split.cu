@@ -142,6 +142,7 @@ attn_split_kernel(AttnArgs a) {
     ntok = 1;
     chunk = blockIdx.z;
   } else {
+    if (pl.live && (int32_t)blockIdx.x >= pl.live[0]) return;
     r = pl.work_req[blockIdx.x];
     tok0 = pl.work_tok0[blockIdx.x];
     ntok = 0;

@@ -142,7 +142,7 @@ struct TcArgs {
 // ------------------------------------------------------------------ kernel
 // One work unit = (pair of adjacent query tiles of one request, KV head, 256-column part of the
 // output). Units are numbered longest first (the plan lists the batch's tile pairs by the keys they
-// see, and the last come first); cluster i takes one unit per round of clusters.
+// see, the most first); cluster i takes one unit per round of clusters.
 struct TcUnit {
   int32_t q0, tok0, ntok;  // this CTA's query tile: request's first token, tile start, tokens (0: none)
   // keys held: positions [kv_start, kv_len); key tiles start kb0 + 64 t, 64-aligned from kv_start
@@ -166,7 +166,7 @@ template <bool BC>
 __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t ndh, int32_t rank) {
   const PlanDev& pl = a.plan;
   TcUnit u;
-  const int32_t pr = pl.num_pairs - 1 - w / (a.num_kv_heads * ndh);
+  const int32_t pr = w / (a.num_kv_heads * ndh);
   u.g = (w / ndh) % a.num_kv_heads;
   u.dh = w % ndh;
   // the pair's entry of the plan's pair table: two 16-byte loads, no dependent lookups
@@ -218,7 +218,7 @@ __device__ __forceinline__ uint64_t tile_bits(int32_t hi, int32_t lo, int32_t si
 }
 // L2 prefetch of unit w's pair-table entry, so tc_unit finds it there later
 __device__ __forceinline__ void tc_unit_prefetch(const TcArgs& a, int32_t w, int32_t ndh) {
-  const int32_t pr = a.plan.num_pairs - 1 - w / (a.num_kv_heads * ndh);
+  const int32_t pr = w / (a.num_kv_heads * ndh);
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a.plan.pair_tab + 8 * pr));
 }
 
@@ -272,7 +272,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const int32_t G = a.group, Hq = a.num_qo_heads;
   const int32_t ps = a.page_size;
   const int32_t W = a.window_left;
-  const int32_t nunits = pl.num_pairs * a.num_kv_heads * NDH;
+  const int32_t npairs = pl.live ? min(pl.num_pairs, __ldg(pl.live + 1)) : pl.num_pairs;
+  const int32_t nunits = npairs * a.num_kv_heads * NDH;
   // the cluster's k-th unit: rounds of (number of clusters) units, walked forwards in even
   // rounds and backwards in odd ones, so the long and the short units of the longest-first
   // order even out

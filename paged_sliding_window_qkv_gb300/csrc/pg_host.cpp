@@ -101,7 +101,8 @@ struct pg_plan {
   size_t dev_cap = 0;      // bytes allocated at dev
   // offsets (elements) of each array inside `dev`
   size_t o_qo = 0, o_kvp = 0, o_pages = 0, o_last = 0, o_start = 0, o_kvs = 0, o_tokreq = 0,
-         o_wreq = 0, o_wtok = 0, o_pair = 0;
+         o_wreq = 0, o_wtok = 0, o_pair = 0, o_live = 0;
+  int32_t room_work = 0, room_pairs = 0;  // entries that the work and the pair table have room for
   PlanStage stage;  // carried over from build to build of the same plan
   int32_t max_seen = 0;           // the most keys a request holds
   int32_t page_keys = 0;          // the most keys one could hold in as many pages, the others keeping one each
@@ -247,10 +248,10 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       }
     }
     nwork = (int64_t)wreq.size();
-    // The kernel takes the pairs from the last to the first, so those that see the most keys come
-    // last (a window keeps that order): on 8 prompts of 384..2026 tokens the busiest cluster then has
-    // 4% more than the mean, against 22% request by request. (Decode looks requests up in the table.)
-    if (num_req > 1 && !all_one) {
+    // The pairs that see the most keys come first (a window keeps that order): on 8 prompts of
+    // 384..2026 tokens the busiest cluster then has 4% more than the mean, against 22% request by
+    // request. (Decode looks requests up in the table.)
+    if (!all_one) {
       const size_t n = ptab.size() / 8;
       std::vector<int32_t> order(n), sorted(ptab.size());
       for (size_t i = 0; i < n; ++i) order[i] = (int32_t)i;
@@ -259,13 +260,25 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
         const int64_t end = (int64_t)e[3] + std::min<int64_t>((int64_t)e[0] + 2 * (int64_t)cta, e[2]);
         return std::min<int64_t>(end, e[6]) - e[7];
       };
-      std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return seen(x) < seen(y); });
+      if (num_req > 1)
+        std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return seen(x) < seen(y); });
+      std::reverse(order.begin(), order.end());
       for (size_t i = 0; i < n; ++i)
         std::copy_n(ptab.data() + 8 * (size_t)order[i], 8, sorted.data() + 8 * i);
       ptab.swap(sorted);
     }
   }
   if (!fits_i32(nwork)) return PG_ERR_I32_OVERFLOW;
+  // A graph that captured the plan's calls holds the addresses of these arrays, so an update to as many
+  // requests, tokens and pages has to find each at its place however the tokens are spread: the tables
+  // have room for the most tiles that any such plan has (a last one a request, and whole ones).
+  const int32_t npairs = (int32_t)(ptab.size() / 8);
+  const int32_t room_work = cta > 0 && num_req > 0 ? num_req + (T - num_req) / cta : 0;
+  const int32_t room_pairs = cta > 0 && num_req > 0 ? num_req + (T - num_req) / (2 * cta) : 0;
+  wreq.resize((size_t)room_work, 0);
+  wtok.resize((size_t)room_work, 0);
+  ptab.resize((size_t)room_pairs * 8, 0);
+  const int32_t live[2] = {(int32_t)nwork, npairs};
 
   // Pack everything into one int32 array and upload it on the plan's stream.
   std::vector<int32_t> host;
@@ -281,6 +294,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   std::vector<int32_t> pids(page_ids, page_ids + NP);
 
   pg_plan q;
+  q.o_live = put(live, 2);
   q.o_qo = put(qo.data(), qo.size());
   q.o_kvp = put(kvp.data(), kvp.size());
   q.o_pages = put(pids.data(), pids.size());
@@ -350,7 +364,8 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.ring_window = ring ? ring_window : -1;
   q.segment = segment ? 1 : 0;
   q.prep_ok = prep_ok ? 1 : 0;
-  q.num_work = (int32_t)nwork; q.num_pairs = (int32_t)(ptab.size() / 8); q.num_page_ids = NP;
+  q.num_work = (int32_t)nwork; q.num_pairs = npairs; q.num_page_ids = NP;
+  q.room_work = room_work; q.room_pairs = room_pairs;
   q.stream = stream; q.device = dev;
   q.dev = d; q.dev_elems = host.size();
   q.dev_cap = fresh ? bytes : p->dev_cap;
@@ -385,6 +400,7 @@ PlanDev plan_dev(const pg_plan* p) {
   v.num_work = p->num_work;
   v.num_pairs = p->num_pairs;
   v.ring = p->ring;
+  v.live = nullptr;
   return v;
 }
 
@@ -574,6 +590,11 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   if (!st) return err;
   AttnArgs a;
   a.plan = plan_dev(plan);
+  if (!plan->decode && capturing(stream)) {
+    a.plan.live = plan->dev + plan->o_live;
+    a.plan.num_work = plan->room_work;
+    a.plan.num_pairs = plan->room_pairs;
+  }
   a.pool = pool_dev(pool, layer);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);

@@ -41,8 +41,11 @@ struct PlanDev {
   // a kernel reads it in one step: {first request-local token of the pair, qo_indptr[r],
   // qo_len, start_pos, kv_page_indptr[r], kv_page_indptr[r + 1], kv_end, kv_start}; the keys
   // held are positions [kv_start, kv_end). Decode plans: request r's entry is the r-th; others: by
-  // the keys that the pair sees, the fewest first
+  // the keys that the pair sees, the most first
   const int32_t* pair_tab;
+  // Captured launches: {num_work, num_pairs} of the plan as it stands when they run, and num_work and
+  // num_pairs below are the most that any plan of as many requests and tokens has. Null otherwise.
+  const int32_t* live;
   int32_t num_req, num_tokens, num_page_ids, num_work, num_pairs;
   // ring addressing: logical page pos / page_size of request r is its page
   // (pos / page_size) mod (pages of r), and kv_len = start_pos + qo_len

@@ -180,26 +180,23 @@ def test_captured_token_weights_follow_the_plan(D, hq, hkv, window, sinks, ps, b
     replayed_weights(D, hq, hkv, ps, [(one, before), (one, after)], window, sinks)
 
 
-@pytest.mark.parametrize("D,hq,hkv", [(256, 4, 2), (512, 4, 1)])
-@pytest.mark.parametrize("window", [-1, 900])
-@pytest.mark.parametrize("ps,before,after", [(5, [600, 600], [1195, 5]), (1, [40, 300, 20], [2, 355, 3]),
-                                             (16, [600, 600], [1200, 16])])
-def test_captured_windowed_decode_follows_the_plan(D, hq, hkv, window, ps, before, after):
-    """The entries without sinks, whose decode form of other page sizes has the same chunks."""
+def replayed_windowed(D, hq, hkv, ps, shapes, window):
+    """replayed_weights, with the entries that have neither sinks nor weights."""
     fn = pg.pg_attn_paged_prefill_lse if D == 256 else pg.pg_attn_paged_prefill_hd512_lse
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
-        one = [1] * len(before)
-        c = Case(D, hq, hkv, one, np.array(before) - 1, ps=ps, seed=ps, stream=s).build()
-        n = pg.pg_workspace_bytes(c.plan)
+        qo, n = shapes[0]
+        c = Case(D, hq, hkv, qo, np.array(n) - qo, ps=ps, seed=ps, stream=s).build()
+        nb = pg.pg_workspace_bytes(c.plan)
 
         def call():
-            pg.check(fn(c.plan, c.desc, 0, c.q, c.out, c.lse, window, 1.0, c.ws, n, s))
+            pg.check(fn(c.plan, c.desc, 0, c.q, c.out, c.lse, window, 1.0, c.ws, nb, s))
 
         g = capture(call, s)
-        for turn, keys in enumerate((after, before, after)):
-            replan(c, one, np.array(keys) - 1, turn)
+        for turn, (qo, n) in enumerate([*shapes[1:], *shapes]):
+            replan(c, qo, np.array(n) - qo, turn)
             c.out.fill_(float("nan"))
+            c.lse.fill_(float("nan"))
             c.ws.fill_(0xFF)
             g.replay()
             s.synchronize()
@@ -212,3 +209,69 @@ def test_captured_windowed_decode_follows_the_plan(D, hq, hkv, window, ps, befor
             got = c.lse.double().cpu().numpy()
             assert (np.abs(got - lse) <= 2.0 ** -8 + c.e + 2.0 ** -22 * np.abs(lse)).all()
     c.close()
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(256, 4, 2), (512, 4, 1)])
+@pytest.mark.parametrize("window", [-1, 900])
+@pytest.mark.parametrize("ps,before,after", [(5, [600, 600], [1195, 5]), (1, [40, 300, 20], [2, 355, 3]),
+                                             (16, [600, 600], [1200, 16])])
+def test_captured_windowed_decode_follows_the_plan(D, hq, hkv, window, ps, before, after):
+    """The decode form of other page sizes than the tensor cores' has the same chunks."""
+    one = [1] * len(before)
+    replayed_windowed(D, hq, hkv, ps, [(one, before), (one, after)], window)
+
+
+# ([tokens], [keys]) captured and replayed: other requests hold the prompt's tokens, so it has more or
+# fewer query tiles
+SPREAD = [
+    (16, ([256, 256], [300, 300]), ([511, 1], [520, 70])),
+    (16, ([1, 1, 200], [16, 16, 208]), ([66, 68, 68], [80, 70, 75])),
+    (16, ([130, 2], [140, 300]), ([2, 130], [300, 130])),
+    (64, ([300] + [1] * 9, [700] + [60] * 9), ([30] * 9 + [39], [64] * 9 + [690])),
+    (5, ([33, 33, 33], [40, 40, 40]), ([97, 1, 1], [110, 5, 3])),
+    (1, ([120, 1], [200, 1]), ([60, 61], [100, 101])),
+]
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(256, 16, 8), (256, 4, 1), (512, 16, 1), (512, 2, 2)])
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (90, 5)])
+@pytest.mark.parametrize("ps,before,after", SPREAD)
+def test_captured_prompt_weights_of_other_lengths(D, hq, hkv, window, sinks, ps, before, after):
+    replayed_weights(D, hq, hkv, ps, [before, after], window, sinks)
+    replayed_weights(D, hq, hkv, ps, [after, before], window, sinks)
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(256, 16, 8), (512, 16, 1)])
+@pytest.mark.parametrize("ps,before,after", SPREAD)
+def test_captured_windowed_prompts_of_other_lengths(D, hq, hkv, ps, before, after):
+    replayed_windowed(D, hq, hkv, ps, [before, after], 90)
+    replayed_windowed(D, hq, hkv, ps, [after, before], -1)
+
+
+def test_a_plan_of_as_many_tokens_keeps_its_layout():
+    """Whatever the spread of 600 tokens over 7 requests, page sizes of both kernel families."""
+    g = np.random.Generator(np.random.PCG64(1))
+    for D, hq, hkv, ps in ((256, 16, 8, 16), (512, 16, 1, 8), (256, 4, 2, 5), (512, 2, 1, 1)):
+        sizes = set()
+        plan = None
+        for turn in range(40):
+            cut = np.sort(g.choice(np.arange(1, 600), 6, replace=False))
+            qo = np.concatenate([[0], cut, [600]])
+            n = np.diff(qo)
+            npg = -(-n // ps)
+            spare = 640 - int(npg.sum())
+            # (as many pages too: the first request's earlier keys fill them)
+            npg[0] += spare
+            start = np.zeros(7, np.int64)
+            start[0] = spare * ps
+            last = (n + start - (npg - 1) * ps).astype(np.int32)
+            indptr = np.concatenate([[0], np.cumsum(npg)])
+            rc, plan = pg.pg_plan_paged_prefill(plan, 7, qo, indptr, np.arange(640, dtype=np.int32), last, start,
+                                                hq, hkv, D, ps)
+            pg.check(rc)
+            info = plan.info()
+            sizes.add((info.metadata_bytes, info.d_page_ids))
+            tile = info.cta_tile_q
+            assert info.num_work == sum(-(-int(x) // tile) for x in n)
+        assert len(sizes) == 1
+        plan.close()
