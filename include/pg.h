@@ -356,7 +356,9 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  *        out 0, for a row that sees no key)
  * The row sum adds the fp32 weights (the entries above sum the bf16-rounded ones), so out and
  * lse agree with those entries to bf16 rounding, not bit for bit.
- *   q, out, workspace, ws_bytes: as for pg_attn_paged_prefill (pg_workspace_bytes).
+ *   q, out, workspace, ws_bytes: as for pg_attn_paged_prefill (pg_workspace_bytes). A decode step
+ *        of head_dim 512 runs on the tensor memory where the workspace also holds
+ *        pg_mass_workspace_bytes (it may need less), else in key chunks.
  * A key that some rows of its tile see and others do not takes part with weight 0 in the latter:
  * a non-finite V row among the keys held makes every row of a prefill tile that spans it
  * non-finite. K rows have no such effect, and in decode only visible keys take part.

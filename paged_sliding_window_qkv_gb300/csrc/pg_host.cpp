@@ -531,21 +531,31 @@ struct Bounded {
   StatsDev stats = {};
 };
 
-// Workspace of the bounded-cache form: the tensor-core kernel's records, or the chunked kernel's
-// partials where that one runs.
 int32_t plan_max_tiles(const pg_plan* p) {
   return (int32_t)std::min<int64_t>(p->tiles * p->num_kv_heads, INT32_MAX);
 }
+// Bytes of one chunk's partials over all rows of a decode step.
+size_t chunk_bytes(const pg_plan* p) {
+  return (size_t)p->num_req * p->num_qo_heads * ((size_t)p->head_dim + 2) * sizeof(float);
+}
+// Chunks per request of the bounded-cache form's chunked kernel: the plan's, as far as they fit the
+// workspace of the entries that take no sinks (where those run the streaming kernel, whose records
+// do not grow with the keys; longer chunks make up for it, and a single one leaves no partials).
+int32_t bounded_chunks(const pg_plan* p) {
+  return (int32_t)std::min<size_t>(p->max_chunks, std::max<size_t>(1, workspace_bytes(p) / chunk_bytes(p)));
+}
+bool bounded_tc(const pg_plan* p) {
+  return bounded_decode_supported(p->head_dim, p->num_qo_heads / p->num_kv_heads, p->page_size);
+}
+// Workspace of the bounded-cache form at its fastest: the tensor-core kernel's records, or the chunked
+// kernel's partials where that one runs.
 size_t bounded_ws_bytes(const pg_plan* p) {
   if (!p || !p->decode || p->num_req == 0) return 0;
-  const int32_t group = p->num_qo_heads / p->num_kv_heads;
-  if (bounded_decode_supported(p->head_dim, group, p->page_size))
-    return bounded_decode_ws_bytes(p->num_req, group, p->head_dim, plan_max_tiles(p));
-  const size_t rows = (size_t)p->num_req * p->num_qo_heads * p->max_chunks;
-  return rows * (size_t)p->head_dim * sizeof(float) + rows * 2 * sizeof(float);
+  if (bounded_tc(p))
+    return bounded_decode_ws_bytes(p->num_req, p->num_qo_heads / p->num_kv_heads, p->head_dim, plan_max_tiles(p));
+  const int32_t chunks = bounded_chunks(p);
+  return chunks > 1 ? chunks * chunk_bytes(p) : 0;
 }
-
-size_t plan_ws_bytes(const pg_plan* p) { return std::max(workspace_bytes(p), bounded_ws_bytes(p)); }
 
 // `args` (the accumulating entry, whose workspace holds more) receives the launched call's
 // arguments, with num_tokens 0 when nothing ran.
@@ -579,8 +589,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   // the tensor-core prefill kernel reads Q rows and writes output rows in 32-byte accesses
   if ((((uintptr_t)q | (uintptr_t)out) & 31u) != 0) return PG_ERR_ALIGN;
   if (lse && ((uintptr_t)lse & 3u) != 0) return PG_ERR_ALIGN;
-  // one size serves every entry that takes pg_workspace_bytes
-  const size_t need = args ? bounded_ws_bytes(plan) : plan_ws_bytes(plan);
+  const size_t need = args ? bounded_ws_bytes(plan) : workspace_bytes(plan);
   if (need > 0) {
     if (!ws || ws_bytes < need) return PG_ERR_WORKSPACE;
     if (!aligned16(ws)) return PG_ERR_ALIGN;
@@ -608,6 +617,9 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   a.max_chunks = plan->max_chunks;
   a.status = st;
   a.bounded = bounded ? 1 : 0;
+  // (at head_dim 512 the records may need more than pg_workspace_bytes: the chunked kernel does with it)
+  a.bounded_tc = bounded && bounded_tc(plan) && ws_bytes >= bounded_ws_bytes(plan) ? 1 : 0;
+  if (bounded && plan->decode && !a.bounded_tc) a.max_chunks = bounded_chunks(plan);
   a.num_sink = bounded ? bounded->num_sink : 0;
   a.logits = bounded ? bounded->logits : nullptr;
   a.logit_slots = bounded ? bounded->logit_slots : 0;
@@ -920,7 +932,7 @@ int pg_prep_paged_hd512(const pg_plan_t plan, const pg_pool_t* pool, int32_t lay
 }
 
 size_t pg_workspace_bytes(const pg_plan_t plan) {
-  return plan_ws_bytes(plan);
+  return workspace_bytes(plan);
 }
 
 int pg_attn_paged_prefill(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
@@ -1031,7 +1043,7 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
   m.ws = workspace;  // (prefill attention itself needs none)
   // (the tensor-core decode adds the weights itself)
-  const bool done = plan->decode && bounded_decode_supported(plan->head_dim, m.attn.group, plan->page_size);
+  const bool done = plan->decode && m.attn.bounded_tc;
   const cudaError_t e = done           ? cudaSuccess
                         : plan->decode ? launch_mass_decode(m, s)
                                        : launch_mass_prefill(m, plan->head_dim, s);

@@ -105,6 +105,7 @@ struct AttnArgs {
   // row sums add unrounded weights; decode scores go to logits[slot][Hq] (log2 units; slot counts
   // through the batch's page list, below logit_slots) when logits is not null
   int32_t bounded;
+  int32_t bounded_tc;   // decode: the tensor-core kernel runs (its records fit the workspace)
   int32_t num_sink;
   float* logits;
   int64_t logit_slots;
