@@ -43,6 +43,9 @@ __device__ __forceinline__ int32_t chunk_tiles(const AttnArgs& a, int32_t tiles)
   const int32_t ct = a.kv_chunk / kDecTile;
   return tiles <= (int64_t)ct * a.max_chunks ? ct : (tiles + a.max_chunks - 1) / a.max_chunks;
 }
+// a row sum with something in it (BC: a NaN sum, of a row that has seen a key, stays)
+template <bool BC>
+__device__ __forceinline__ bool some(float l) { return BC ? l != 0.f : l > 0.f; }
 constexpr float kLn2 = 0.69314718055994531f;  // log2 units to natural log
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -452,7 +455,7 @@ attn_split_kernel(AttnArgs a) {
   if (a.lse && !(C::DECODE && nchunks > 1) && sm_sub == 0 && sm_valid) {
     // natural-log normaliser of the row: row_m and row_l are in log2 units of the scores
     a.lse[(int64_t)(q0 + tok0 + sm_tl) * Hq + g * G + (sm_row % G)] =
-        row_l > 0.f ? (row_m + log2f(row_l)) * kLn2 : -INFINITY;
+        some<BC>(row_l) ? (row_m + log2f(row_l)) * kLn2 : -INFINITY;
   }
   if (C::DECODE && nchunks > 1 && sm_sub == 0 && sm_valid) {
     const int h = g * G + (sm_row % G);
@@ -467,7 +470,7 @@ attn_split_kernel(AttnArgs a) {
     const int m = o_mt * 16 + (lane >> 2) + h2 * 8;
     if (m >= ntok * G) continue;
     const float l = sL[m];
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = some<BC>(l) ? 1.f / l : 0.f;
     const int tl = m / G, h = g * G + (m % G);
     if (C::DECODE && nchunks > 1) {
       float* dst = a.ws_o + (((int64_t)r * Hq + h) * a.max_chunks + chunk) * D + o_cg * C::DCOLS;
@@ -546,7 +549,7 @@ attn_merge_kernel(AttnArgs a) {
       }
       __syncthreads();
     }
-    for (int c = tid; c < n; c += NT) s_l[c] = s_l[c] > 0.f ? s_l[c] * exp2f(s_m[c] - Mr) : 0.f;
+    for (int c = tid; c < n; c += NT) s_l[c] = some<BC>(s_l[c]) ? s_l[c] * exp2f(s_m[c] - Mr) : 0.f;
     __syncthreads();
     for (int c0 = 0; c0 < n; c0 += 8) {
       float4 v[8];
@@ -562,10 +565,10 @@ attn_merge_kernel(AttnArgs a) {
       }
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = some<BC>(den) ? 1.f / den : 0.f;
   if (a.lse && tid == 0)
     a.lse[(int64_t)pl.qo_indptr[r] * a.num_qo_heads + h] =
-        den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+        some<BC>(den) ? (M + log2f(den)) * kLn2 : -INFINITY;
   __nv_bfloat16* dst = a.out + ((int64_t)pl.qo_indptr[r] * a.num_qo_heads + h) * D + d;
   *reinterpret_cast<__nv_bfloat162*>(dst) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   *reinterpret_cast<__nv_bfloat162*>(dst + 2) = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);

@@ -1075,10 +1075,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (ok) {
         // epilogue: normalise this thread's 128 output columns [128h, 128h + 128) of the row
         tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // (a NaN sum of BC stays: the row has seen a key)
+        const bool some = BC ? l != 0.f : l > 0.f;
+        const float inv = some ? 1.f / l : 0.f;
         if (a.lse && rvalid && h == 0 && u.dh == 0)  // both output halves of hd512 agree
           a.lse[(int64_t)(u.q0 + u.tok0 + (row >> gsh)) * Hq + u.g * G + (row & gmask)] =
-              l > 0.f ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+              some ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
         if (DQK == 256) {
           // each 64-column half of this warp's 128 columns goes through the transposition
           // buffer (free: every PV of the unit has completed) and out in coalesced 16-byte
