@@ -10,6 +10,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <new>
 #include <algorithm>
@@ -154,7 +155,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     return PG_ERR_ARG;
   const int32_t group = Hq / Hkv;
 
-  std::vector<int32_t> qo(num_req + 1, 0), kvp(num_req + 1, 0), last(num_req), start(num_req),
+  std::vector<int32_t> qo((size_t)num_req + 1, 0), kvp((size_t)num_req + 1, 0), last(num_req), start(num_req),
       kvs(num_req, 0);
   if (num_req > 0) {
     if (qo_indptr[0] != 0 || kv_page_indptr[0] != 0) return PG_ERR_ARG;
@@ -775,6 +776,28 @@ int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer,
   return PG_OK;
 }
 
+// Builds *plan (null) or updates it. No exception leaves a C entry: memory that the host cannot give is
+// an argument that cannot be served, and nothing has changed by then.
+template <class... Args>
+int make_plan(pg_plan_t* plan, cudaStream_t stream, const Args&... args) {
+  if (!plan) return PG_ERR_ARG;
+  if (*plan && (*plan)->stream != stream) return PG_ERR_STREAM;
+  pg_plan* p = *plan ? *plan : new (std::nothrow) pg_plan();
+  if (!p) return PG_ERR_ARG;
+  int rc = PG_ERR_ARG;
+  try {
+    rc = build_plan(p, args...);
+  } catch (const std::exception&) {  // std::bad_alloc, std::length_error: before any CUDA call
+  }
+  if (rc != PG_OK && !*plan) {
+    free_stage(&p->stage);
+    delete p;
+    return rc;
+  }
+  *plan = p;
+  return rc;
+}
+
 // The device's status word if it already exists; never allocates.
 int* status_word_existing(int* err) {
   int dev = 0;
@@ -796,24 +819,9 @@ int pg_plan_paged_prefill(pg_plan_t* plan, int32_t num_req, const int64_t* qo_in
                           const int32_t* last_page_len, const int64_t* start_pos,
                           int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
                           int32_t page_size, pg_stream_t stream) {
-  if (!plan) return PG_ERR_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (*plan) {
-    if ((*plan)->stream != s) return PG_ERR_STREAM;
-    return build_plan(*plan, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len,
-                      start_pos, num_qo_heads, num_kv_heads, head_dim, page_size, s);
-  }
-  pg_plan* p = new (std::nothrow) pg_plan();
-  if (!p) return PG_ERR_ARG;
-  int rc = build_plan(p, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
-                      num_qo_heads, num_kv_heads, head_dim, page_size, s);
-  if (rc != PG_OK) {
-    free_stage(&p->stage);
-    delete p;
-    return rc;
-  }
-  *plan = p;
-  return PG_OK;
+  return make_plan(plan, s, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
+                   num_qo_heads, num_kv_heads, head_dim, page_size, s);
 }
 
 int pg_plan_paged_prefill_ring(pg_plan_t* plan, int32_t num_req, const int64_t* qo_indptr,
@@ -824,22 +832,8 @@ int pg_plan_paged_prefill_ring(pg_plan_t* plan, int32_t num_req, const int64_t* 
   if (!plan) return PG_ERR_ARG;
   if (window_left < 0) return PG_ERR_WINDOW;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (*plan) {
-    if ((*plan)->stream != s) return PG_ERR_STREAM;
-    return build_plan(*plan, num_req, qo_indptr, kv_page_indptr, page_ids, nullptr, start_pos,
-                      num_qo_heads, num_kv_heads, head_dim, page_size, s, window_left);
-  }
-  pg_plan* p = new (std::nothrow) pg_plan();
-  if (!p) return PG_ERR_ARG;
-  int rc = build_plan(p, num_req, qo_indptr, kv_page_indptr, page_ids, nullptr, start_pos,
-                      num_qo_heads, num_kv_heads, head_dim, page_size, s, window_left);
-  if (rc != PG_OK) {
-    free_stage(&p->stage);
-    delete p;
-    return rc;
-  }
-  *plan = p;
-  return PG_OK;
+  return make_plan(plan, s, num_req, qo_indptr, kv_page_indptr, page_ids, nullptr, start_pos,
+                   num_qo_heads, num_kv_heads, head_dim, page_size, s, window_left);
 }
 
 int pg_plan_paged_segment(pg_plan_t* plan, int32_t num_req, const int64_t* qo_indptr,
@@ -852,22 +846,8 @@ int pg_plan_paged_segment(pg_plan_t* plan, int32_t num_req, const int64_t* qo_in
   static const int64_t kNoSegments = 0;  // a non-null pointer for an empty batch
   const int64_t* ks = kv_start ? kv_start : &kNoSegments;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (*plan) {
-    if ((*plan)->stream != s) return PG_ERR_STREAM;
-    return build_plan(*plan, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len,
-                      start_pos, num_qo_heads, num_kv_heads, head_dim, page_size, s, -1, ks);
-  }
-  pg_plan* p = new (std::nothrow) pg_plan();
-  if (!p) return PG_ERR_ARG;
-  int rc = build_plan(p, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
-                      num_qo_heads, num_kv_heads, head_dim, page_size, s, -1, ks);
-  if (rc != PG_OK) {
-    free_stage(&p->stage);
-    delete p;
-    return rc;
-  }
-  *plan = p;
-  return PG_OK;
+  return make_plan(plan, s, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
+                   num_qo_heads, num_kv_heads, head_dim, page_size, s, -1, ks);
 }
 
 void pg_plan_destroy(pg_plan_t plan) {
