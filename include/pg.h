@@ -342,6 +342,9 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  * attention (window_left -1) sees every kept key, whatever slot it sits in.
  */
 
+/* Bytes of device workspace with which pg_attn_paged_sink runs at its fastest (0 when none). */
+size_t pg_sink_workspace_bytes(const pg_plan_t plan);
+
 /*
  * pg_attn_paged_sink -- the attention of pg_attn_paged_prefill (plan head_dim 256) or
  * pg_attn_paged_prefill_hd512 (512), prefill and decode, in which the first num_sink positions
@@ -356,9 +359,9 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  *        out 0, for a row that sees no key)
  * The row sum adds the fp32 weights (the entries above sum the bf16-rounded ones), so out and
  * lse agree with those entries to bf16 rounding, not bit for bit.
- *   q, out, workspace, ws_bytes: as for pg_attn_paged_prefill (pg_workspace_bytes). A decode step
- *        of head_dim 512 runs on the tensor memory where the workspace also holds
- *        pg_mass_workspace_bytes (it may need less), else in key chunks.
+ *   q, out: as for pg_attn_paged_prefill
+ *   workspace: pg_sink_workspace_bytes(plan), 16-byte aligned. ws_bytes >= pg_workspace_bytes(plan)
+ *        is enough; a decode step of head_dim 512 may then run on fewer SMs.
  * A key that some rows of its tile see and others do not takes part with weight 0 in the latter:
  * a non-finite V row among the keys held makes every row of a prefill tile that spans it
  * non-finite. K rows have no such effect, and in decode only visible keys take part.

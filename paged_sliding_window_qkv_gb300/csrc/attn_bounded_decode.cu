@@ -1033,6 +1033,13 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
 
 size_t al16(size_t n) { return (n + 15) & ~(size_t)15; }
 
+// CTAs whose records the workspace holds (one that runs alone cuts no segment and leaves none).
+int32_t record_room(const AttnArgs& a, int32_t D) {
+  const size_t prefix = al16((size_t)(a.plan.num_req + 1) * 8), cta = (size_t)2 * a.group * (D + 2) * sizeof(float);
+  const size_t room = a.ws_bytes > prefix ? (a.ws_bytes - prefix) / cta : 0;
+  return (int32_t)std::min<size_t>(std::max<size_t>(room, 1), kMaxCtas);
+}
+
 template <int D, int NQ>
 cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   using C = BdCfg<D>;
@@ -1073,7 +1080,8 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
     return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
   }, &sms);
   if (e != cudaSuccess) return e;
-  const int32_t S = std::max(1, std::min(std::min(sms, kMaxCtas), a.max_tiles));
+  // as many CTAs as have tiles and room for their records
+  const int32_t S = std::max(1, std::min(std::min(sms, record_room(a, D)), a.max_tiles));
   BdArgs b;
   b.a = a;
   b.box_rows = br;
@@ -1124,6 +1132,26 @@ bool bounded_decode_supported(int32_t head_dim, int32_t group, int32_t page_size
 size_t bounded_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles) {
   const size_t S = (size_t)std::max(1, std::min(kMaxCtas, max_tiles));
   return al16((size_t)(num_req + 1) * 8) + S * 2 * group * 2 * 4 + S * 2 * group * head_dim * 4;
+}
+
+// pg_workspace_bytes of head_dim 512 may hold the records of fewer CTAs than have tiles. With room for
+// less than half of them the chunked kernel is faster: 4 requests of 500 keys 35 against 65 us (17 with
+// room for all), 64 of them 37 against 50 (33). With more it is not: one request of 8000 keys under a window
+// of 1023, 10 tiles and room for 7 CTAs, 35 against 21 us.
+bool bounded_decode_fits(const AttnArgs& a, int32_t head_dim) {
+  if (a.logits) return true;  // (its workspace has them all)
+  static PerDeviceOnce device;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return true;
+  if (device.get(dev, [dev](int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); }, &sms) !=
+      cudaSuccess)
+    return true;
+  int64_t tiles = a.max_tiles;
+  if (a.window_left >= 0) {
+    const int64_t seen = ((int64_t)a.window_left + a.num_sink + kT) / kT + 1;
+    tiles = std::min(tiles, seen * a.plan.num_req * a.pool.num_kv_heads);
+  }
+  return 2 * (int64_t)record_room(a, head_dim) >= std::min<int64_t>(tiles, sms);
 }
 
 cudaError_t launch_bounded_decode(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {

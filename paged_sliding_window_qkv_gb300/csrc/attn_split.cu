@@ -627,12 +627,14 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t head_dim, cudaStream_
 cudaError_t launch_attn_decode(const AttnArgs& args, int32_t head_dim, cudaStream_t stream) {
   if (args.plan.num_req == 0) return cudaSuccess;
   if (args.bounded) {
-    if (args.bounded_tc) return launch_bounded_decode(args, head_dim, stream);
+    if (bounded_decode_supported(head_dim, args.group, args.pool.page_size) && bounded_decode_fits(args, head_dim))
+      return launch_bounded_decode(args, head_dim, stream);
   } else if (attn_decode_stream_supported(head_dim, args.group, args.pool.page_size)) {
     return launch_attn_decode_stream(args, head_dim, stream);
   }
-  // other page sizes (and a bounded call whose workspace holds no more): fixed key chunks per (request, KV head), partials in the workspace
+  // other page sizes (and a bounded call with room for few records): fixed key chunks per (request, KV head), partials in the workspace
   AttnArgs a = args;
+  if (a.bounded) a.max_chunks = a.bounded_chunks;
   const size_t rows = (size_t)a.plan.num_req * a.num_qo_heads * a.max_chunks;
   a.ws_o = reinterpret_cast<float*>(a.ws_raw);
   a.ws_ml = a.ws_o + rows * (size_t)head_dim;

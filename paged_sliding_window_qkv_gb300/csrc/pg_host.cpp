@@ -548,8 +548,8 @@ int32_t bounded_chunks(const pg_plan* p) {
 bool bounded_tc(const pg_plan* p) {
   return bounded_decode_supported(p->head_dim, p->num_qo_heads / p->num_kv_heads, p->page_size);
 }
-// Workspace of the bounded-cache form at its fastest: the tensor-core kernel's records, or the chunked
-// kernel's partials where that one runs.
+// Workspace of the bounded-cache form: the tensor-core kernel's records for every CTA (it does with
+// fewer), or the chunked kernel's partials where that one runs.
 size_t bounded_ws_bytes(const pg_plan* p) {
   if (!p || !p->decode || p->num_req == 0) return 0;
   if (bounded_tc(p))
@@ -618,9 +618,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   a.max_chunks = plan->max_chunks;
   a.status = st;
   a.bounded = bounded ? 1 : 0;
-  // (at head_dim 512 the records may need more than pg_workspace_bytes: the chunked kernel does with it)
-  a.bounded_tc = bounded && bounded_tc(plan) && ws_bytes >= bounded_ws_bytes(plan) ? 1 : 0;
-  if (bounded && plan->decode && !a.bounded_tc) a.max_chunks = bounded_chunks(plan);
+  a.bounded_chunks = bounded && plan->decode ? bounded_chunks(plan) : 0;
   a.num_sink = bounded ? bounded->num_sink : 0;
   a.logits = bounded ? bounded->logits : nullptr;
   a.logit_slots = bounded ? bounded->logit_slots : 0;
@@ -630,6 +628,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   wait_settings(&a.wait_ns, &a.test_withhold);
   cudaError_t e;
   a.ws_raw = ws;
+  a.ws_bytes = ws_bytes;
   a.ws_o = nullptr;
   a.ws_ml = nullptr;
   if (args) *args = a;
@@ -979,6 +978,10 @@ int pg_attn_paged_sink(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
                      ws_bytes, s, &b);
 }
 
+size_t pg_sink_workspace_bytes(const pg_plan_t plan) {
+  return std::max(workspace_bytes(plan), bounded_ws_bytes(plan));
+}
+
 size_t pg_mass_workspace_bytes(const pg_plan_t plan) { return mass_workspace_bytes(plan); }
 
 int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
@@ -1023,7 +1026,7 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
   m.ws = workspace;  // (prefill attention itself needs none)
   // (the tensor-core decode adds the weights itself)
-  const bool done = plan->decode && m.attn.bounded_tc;
+  const bool done = plan->decode && bounded_tc(plan);
   const cudaError_t e = done           ? cudaSuccess
                         : plan->decode ? launch_mass_decode(m, s)
                                        : launch_mass_prefill(m, plan->head_dim, s);

@@ -92,6 +92,7 @@ struct AttnArgs {
   __nv_bfloat16* out;
   float* lse;     // optional [T][Hq] natural-log normaliser of each row (null: not written)
   void* ws_raw;   // decode form: the caller's workspace (pg_workspace_bytes), 16-byte aligned
+  size_t ws_bytes;
   float* ws_o;    // chunked decode form: partial outputs [R][Hq][max_chunks][D]
   float* ws_ml;   // chunked decode form: [R][Hq][max_chunks][2] (running max in log2 units, sum)
   float sm_scale_log2;  // sm_scale * log2(e)
@@ -105,7 +106,7 @@ struct AttnArgs {
   // row sums add unrounded weights; decode scores go to logits[slot][Hq] (log2 units; slot counts
   // through the batch's page list, below logit_slots) when logits is not null
   int32_t bounded;
-  int32_t bounded_tc;   // decode: the tensor-core kernel runs (its records fit the workspace)
+  int32_t bounded_chunks;  // its chunks per request, where the chunked kernel runs
   int32_t num_sink;
   float* logits;
   int64_t logit_slots;
@@ -176,6 +177,8 @@ cudaError_t launch_attn_decode_stream(const AttnArgs& a, int32_t head_dim, cudaS
 // geometry it handles, its workspace for a plan of max_tiles tiles, and its launch.
 bool bounded_decode_supported(int32_t head_dim, int32_t group, int32_t page_size);
 size_t bounded_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles);
+// Whether the workspace of a call holds the records of enough CTAs (see attn_bounded_decode.cu).
+bool bounded_decode_fits(const AttnArgs& a, int32_t head_dim);
 cudaError_t launch_bounded_decode(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
 
 // Decode attention with its partials in the library's static scratch (no allocation).

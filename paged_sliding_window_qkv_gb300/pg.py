@@ -333,6 +333,7 @@ def pg_attn_paged_decode_noalloc(plan, pool: pg_pool_t, layer, q, out, window_le
 # ---------------------------------------------------------------- bounded caches
 _attn_sink = _sig("pg_attn_paged_sink", C.c_int, _P, C.POINTER(pg_pool_t), _I32, _P, _P, _P, _I32,
                   _I32, _F32, _P, _SZ, _P)
+_sink_wsb = _sig("pg_sink_workspace_bytes", _SZ, _P)
 _mass_wsb = _sig("pg_mass_workspace_bytes", _SZ, _P)
 _attn_mass = _sig("pg_attn_paged_mass", C.c_int, _P, C.POINTER(pg_pool_t), _I32, _P, _P, _P,
                   C.POINTER(pg_kv_stats_t), _I32, _I32, _F32, _P, _SZ, _P)
@@ -362,6 +363,10 @@ def pg_attn_paged_sink(plan, pool: pg_pool_t, layer, q, out, lse, window_left, n
     return _attn_sink(plan.handle if plan is not None else None, C.byref(pool), int(layer), _ptr(q),
                       _ptr(out), _ptr(lse), int(window_left), int(num_sink), float(sm_scale),
                       _ptr(workspace), int(ws_bytes), _stream(stream))
+
+
+def pg_sink_workspace_bytes(plan) -> int:
+    return int(_sink_wsb(plan.handle if plan is not None else None))
 
 
 def pg_mass_workspace_bytes(plan) -> int:
@@ -394,7 +399,7 @@ def pg_kv_evict_apply(plan, pool: pg_pool_t, stats: pg_kv_stats_t, layer, num_la
                         int(budget), _ptr(src), _stream(stream))
 
 
-EXPORTED = ["pg_attn_paged_sink", "pg_mass_workspace_bytes", "pg_attn_paged_mass",
+EXPORTED = ["pg_attn_paged_sink", "pg_sink_workspace_bytes", "pg_mass_workspace_bytes", "pg_attn_paged_mass",
             "pg_kv_evict_select", "pg_kv_evict_apply", "pg_plan_paged_prefill", "pg_plan_paged_prefill_ring", "pg_plan_paged_segment",
             "pg_attn_paged_prefill_lse", "pg_attn_paged_prefill_hd512_lse", "pg_merge_attn_states",
             "pg_plan_destroy", "pg_plan_info", "pg_rope_table",

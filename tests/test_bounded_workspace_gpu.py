@@ -71,16 +71,20 @@ def test_a_decode_loop_keeps_its_buffer(D, hq, hkv, ps):
     assert (ws[size:] == 0xFF).all()
 
 
-@pytest.mark.parametrize("D,hq,hkv,ps,R,top", [(512, 16, 1, 16, 3, 3001), (512, 2, 2, 64, 1, 700),
+@pytest.mark.parametrize("D,hq,hkv,ps,R,top", [(512, 16, 1, 16, 3, 3001), (512, 2, 2, 64, 1, 700), (512, 8, 1, 8, 30, 500),
                                                (256, 4, 4, 2, 160, 900), (256, 8, 8, 4, 80, 900)])
 def test_sink_decode_within_either_size(D, hq, hkv, ps, R, top):
-    """pg_workspace_bytes, and the larger of it and pg_mass_workspace_bytes (head_dim 512: another kernel)."""
+    """pg_workspace_bytes and the entry's own, larger size (head_dim 512: another kernel may run), and what
+    is between them."""
     g = np.random.Generator(np.random.PCG64(R))
     n = g.integers(1, top, R)
     n[-1] = top
     c = Case(D, hq, hkv, [1] * R, n - 1, ps=ps, seed=R).build()
     least = pg.pg_workspace_bytes(c.plan)
-    for size in (least, max(least, pg.pg_mass_workspace_bytes(c.plan))):
+    full = pg.pg_sink_workspace_bytes(c.plan)
+    assert least <= full <= max(least, pg.pg_mass_workspace_bytes(c.plan))
+    assert full == least if D == 256 else full > least
+    for size in sorted({least, (least + full) // 2, (least + 7 * full) // 8, full}):
         for window, sinks in ((600, 5), (-1, 0)):
             ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device="cuda")
             c.out.fill_(float("nan"))
