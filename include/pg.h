@@ -334,7 +334,8 @@ int pg_merge_attn_states(const pg_bf16_t* out_a, const float* lse_a, const pg_bf
  * They take plans of pg_plan_paged_prefill and pg_plan_paged_segment (PG_ERR_PLAN_MISMATCH for a
  * ring plan: its slots forget the positions these keep), and the plan's own device must be
  * current (PG_ERR_STREAM otherwise). A captured call follows a plan that is updated in place with
- * as many requests, tokens and pages as it was captured with.
+ * as many requests, tokens and pages as it was captured with, however they are spread (a request that
+ * holds many more keys than the longest one at capture costs pg_kv_evict_select more time).
  *
  * After an eviction the cache's slots no longer count positions. The request's next plan is a
  * segment plan with kv_start = the number of its keys evicted so far: position p of a new token
@@ -399,7 +400,9 @@ size_t pg_mass_workspace_bytes(const pg_plan_t plan);
  * Sums are fp32 in a fixed order: equal calls give equal bits.
  *   workspace: ws_bytes >= pg_mass_workspace_bytes(plan), 16-byte aligned
  * A page may be listed only once in the plan (PG_ERR_SHARED_PAGE): a shared page's slots belong
- * to several requests. A plan updated under a captured graph must keep to that.
+ * to several requests. So a cache is weighed or trimmed, not both: the list of a request whose pages
+ * were given away (pg_kv_request_trim) names one page in their places. A plan updated under a captured
+ * graph must keep to that.
  * Errors: those of pg_attn_paged_sink; PG_ERR_ARG (lse or stats NULL), PG_ERR_LAYOUT (statistics
  * geometry or capacity), PG_ERR_ALIGN.
  */

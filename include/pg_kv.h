@@ -156,7 +156,8 @@ int pg_kv_request_evict(pg_kv_server_t srv, int64_t request_id, int32_t keep);
  * request's page list keeps its length, with -1 in their places (pg_kv_request_pages), and
  * pg_kv_batch_plan_inputs fills those with the page of the step's last position, which
  * pg_attn_paged_sink, with this window and at most these sinks, does not read there; the other
- * attention calls may, and are not for a trimmed request. A request under a window and sinks so holds at most
+ * attention calls may, and are not for a trimmed request (pg_attn_paged_mass and the eviction refuse
+ * it). A request under a window and sinks so holds at most
  * ceil(num_sink / page_size) + ceil((window_left + step) / page_size) + 1 pages at any length. *freed (may
  * be NULL) receives the pages given away by this call. Not for ring servers (PG_KV_ERR_WINDOW),
  * whose slots are reused in place; no step may be pending (PG_KV_ERR_PENDING). As with

@@ -932,7 +932,10 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
   const float* src[kPer];
   int32_t page[kPer];
   float4 x[kPer][4];
-  const bool vec = Hq == 16;  // a key's scores are four vectors
+  // 16 heads: a key's scores are four vectors, on their way while the normalisers form; other head counts
+  // load them one at a time behind that (64 requests of 8001 keys at head_dim 512: 196 us with 16 heads, 187
+  // with 8, 419 with 32 over two KV heads; the bytes take 155, 155 and 310)
+  const bool vec = Hq == 16;
   auto load = [&](int64_t k0) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {

@@ -632,7 +632,8 @@ cudaError_t launch_attn_decode(const AttnArgs& args, int32_t head_dim, cudaStrea
   } else if (attn_decode_stream_supported(head_dim, args.group, args.pool.page_size)) {
     return launch_attn_decode_stream(args, head_dim, stream);
   }
-  // other page sizes (and a bounded call with room for few records): fixed key chunks per (request, KV head), partials in the workspace
+  // other page sizes, and a bounded call with room for few records: fixed key chunks per (request,
+  // KV head), partials in the workspace
   AttnArgs a = args;
   if (a.bounded) a.max_chunks = a.bounded_chunks;
   const size_t rows = (size_t)a.plan.num_req * a.num_qo_heads * a.max_chunks;

@@ -79,7 +79,7 @@ __device__ __forceinline__ void wait_previous() {
 // order is thread order and every rank below is a bit count over the thread's 32-bit masks and one
 // scan over the threads. Statistics are read in slot order, four slots a load where the pages and
 // the arrays allow it (V4), and reach the threads' shares through shared memory (read by their own
-// threads, a warp's loads fell into 32 lines: 66 against 48 us on 512 segments of 16,384 keys, with
+// threads, a warp's loads fell into 32 lines: 66 against 47 us on 512 segments of 16,384 keys, with
 // the next paragraph's sample).
 //
 // The keep-th largest order value is searched for in a shrinking range [lo, last], one count over
@@ -89,15 +89,15 @@ __device__ __forceinline__ void wait_previous() {
 // about a sixth of the keys. Then the range is cut in proportion to the counts, every fourth time
 // in half; a count that told no keys of it apart shrinks it to the least and the largest key in it,
 // so equal keys at the cut end the search (216 segments of up to 667 keys with zeros and equal masses
-// 14.0 -> 9.0 us). Once 1024 keys or fewer are in it, they are gathered and only they are counted. The
+// 14.0 -> 8.7 us). Once 1024 keys or fewer are in it, they are gathered and only they are counted. The
 // search ends when exactly keep keys reach lo (then nothing ties) or the range is one value.
 //
 // (Keys left in shared memory, with 40 registers a thread and three CTAs of 512 on an SM, were slower: 512
-// segments of 8000 keys 36.5 against 25.1 us, of 16,384 49 against 46.)
+// segments of 8000 keys 36 against 25 us, of 16,384 49 against 47.)
 //
 // Bound: latency, some 6.5 us of a 16,384-key segment's 14 before the keys are in registers on
 // an idle GPU; a segment is read once (8 bytes a key). 512 segments of 8000 keys take 25 us (1.6 TB/s),
-// of 16,384 46 us.
+// of 16,384 47 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;  // at most
 constexpr int kMaxCluster = 8;
@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_select_kernel(EvictArgs a
   if constexpr (CL) cluster_barrier();  // the peers have read this CTA's list
 }
 
-// Segments longer than a cluster's registers (131,072 keys).
+// Segments longer than a cluster's registers (131,072 keys): one of 140,000 keys takes 1.06 ms, 16 of
+// 200,000 1.58 ms (the longest of the form above, 131,072 keys, 37 us).
 __global__ void __launch_bounds__(kLongThreads) evict_select_long_kernel(EvictArgs a) {
   __shared__ LongShared sh;
   const Seg q = load_seg(a, (int32_t)blockIdx.x);
@@ -751,9 +752,9 @@ cudaError_t launch_evict_select(const EvictArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // Two CTAs of 512 threads fill an SM's registers. Where there are more segments than that, 256
   // threads each: four of their chains of loads and counts then overlap on an SM (512 segments of
-  // 2048, 4096, 8000 keys: 13.8, 17.1, 28.4 against 16.4, 20.9, 31.6 us).
+  // 2048, 4096, 8000 keys: 12.8, 15.4, 25 against 15.3, 19.7, 30 us).
   // Short segments need fewer threads, and the barriers among fewer are shorter: 240 segments of 300
-  // keys took 6.6 us in 128 threads against 10.7 in 512, 1000 of 1000 keys 13.5 in 256 against 14.7.
+  // keys take 6.8 us in 128 threads against 9.5 in 512, 1000 of 1000 keys 14.2 in 256 against 24.8.
   if (n <= 128 * 4) return launch_select<128, 4, false>(a, segs, 1, stream);
   if (n <= 256 * 4) return launch_select<256, 4, false>(a, segs, 1, stream);
   if (segs > 2 * sms) {

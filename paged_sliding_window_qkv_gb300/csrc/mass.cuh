@@ -51,8 +51,8 @@ __device__ __forceinline__ MassTiles mass_tiles(const AttnArgs& a, const MassReq
 }
 
 // Whether some row of the step sees key index rel: the first position at or past the key's is the
-// one that sees most of what lies before it. (The statistics of a key that no row sees are not
-// touched: its page may be someone else's by now.)
+// one that sees most of what lies before it. (The statistics of a key that no row sees stay
+// as they are, bit for bit: +0 would make +0 of -0.)
 __device__ __forceinline__ bool mass_seen(const AttnArgs& a, const MassReq& q, int32_t rel) {
   const int32_t j = q.ks0 + rel;
   return j < q.sp + q.len && (a.window_left < 0 || j < a.num_sink || max(j, q.sp) - j <= a.window_left);
