@@ -37,11 +37,16 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = 8;
 constexpr int kDecTile = 32;  // keys per tile of the decode form
-// Key tiles per decode chunk. The launch and the workspace have max_chunks chunks a request; where a
-// graph's plan has outgrown them since the capture, its chunks are longer instead.
-__device__ __forceinline__ int32_t chunk_tiles(const AttnArgs& a, int32_t tiles) {
-  const int32_t ct = a.kv_chunk / kDecTile;
-  return tiles <= (int64_t)ct * a.max_chunks ? ct : (tiles + a.max_chunks - 1) / a.max_chunks;
+// The decode chunks of a request whose visible keys are `keys` (BC: a whole number of tiles), chunk keys
+// each. The launch and the workspace have max_chunks a request; where a graph's plan has outgrown them
+// since the capture, its chunks are longer instead (a whole number of tiles).
+__device__ __forceinline__ int32_t count_chunks(const AttnArgs& a, int32_t keys, int32_t* chunk) {
+  *chunk = a.kv_chunk;
+  const int32_t n = (keys + a.kv_chunk - 1) / a.kv_chunk;
+  if (n <= a.max_chunks) return n;
+  const int32_t tiles = (keys + kDecTile - 1) / kDecTile;
+  *chunk = (tiles + a.max_chunks - 1) / a.max_chunks * kDecTile;
+  return (keys + *chunk - 1) / *chunk;
 }
 // a row sum with something in it (BC: a NaN sum, of a row that has seen a key, stays)
 template <bool BC>
@@ -172,15 +177,16 @@ attn_split_kernel(AttnArgs a) {
     lo = walk.lo;
     ntiles = walk.total;
     if (C::DECODE) {
-      const int32_t ct = chunk_tiles(a, walk.total);
-      nchunks = (walk.total + ct - 1) / ct;
+      int32_t keys;
+      nchunks = count_chunks(a, walk.total * BN, &keys);
       if (chunk >= max(nchunks, 1)) return;
+      const int32_t ct = keys / BN;
       vt0 = chunk * ct;
       ntiles = min(ct, walk.total - vt0);
     }
   } else if (C::DECODE) {
-    const int32_t keys = chunk_tiles(a, (hi - lo + BN - 1) / BN) * BN;
-    nchunks = (hi - lo + keys - 1) / keys;
+    int32_t keys;
+    nchunks = count_chunks(a, hi - lo, &keys);
     // a row that sees no key (possible in a key segment) is still written, by chunk 0
     if (chunk >= max(nchunks, 1)) return;
     lo = lo + chunk * keys;
@@ -511,10 +517,10 @@ attn_merge_kernel(AttnArgs a) {
   const int32_t W = a.window_left;
   const int32_t lo = W >= 0 ? max(ks0, p - W) : ks0;
   const int32_t hi = min(p + 1, kv_len);
-  // the keys are counted in the partition kernel's tiles; a chunk is a whole number of them
-  int32_t tiles = (hi - lo + kDecTile - 1) / kDecTile;
-  if constexpr (BC) tiles = key_walk(W, a.num_sink, ks0, kv_len, p, p, kDecTile).total;
-  const int32_t ct = chunk_tiles(a, tiles), nch = (tiles + ct - 1) / ct;
+  int32_t keys = hi - lo, chunk;
+  // (counted in the partition kernel's tiles)
+  if constexpr (BC) keys = key_walk(W, a.num_sink, ks0, kv_len, p, p, kDecTile).total * kDecTile;
+  const int32_t nch = count_chunks(a, keys, &chunk);
   if (nch <= 1) return;  // written directly by the partition kernel
   const int64_t row = ((int64_t)r * a.num_qo_heads + h) * a.max_chunks;
   const int tid = threadIdx.x, lane = tid & 31;
