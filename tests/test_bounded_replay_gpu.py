@@ -275,3 +275,41 @@ def test_a_plan_of_as_many_tokens_keeps_its_layout():
             assert info.num_work == sum(-(-int(x) // tile) for x in n)
         assert len(sizes) == 1
         plan.close()
+
+
+@pytest.mark.parametrize("D,hq,hkv,ps", [(256, 16, 8, 16), (256, 4, 2, 5), (512, 16, 1, 16), (512, 4, 1, 3)])
+@pytest.mark.parametrize("shapes", [([200, 3, 60], [2, 250, 11]), ([1, 1, 261], [88, 88, 87])])
+def test_captured_ring_prompts_of_other_lengths(D, hq, hkv, ps, shapes):
+    """A ring plan's tables have the same room: the replay equals the eager call under the updated plan."""
+    window, s = 100, torch.cuda.Stream()
+    g = np.random.Generator(np.random.PCG64(D + ps))
+    held = -(-(window + 261) // ps)  # pages a ring
+    with torch.cuda.stream(s):
+        pool = torch.randn((1, 3 * held, 2, hkv, ps, D), device="cuda", dtype=torch.bfloat16)
+        q = torch.randn((sum(shapes[0]), hq, D), device="cuda", dtype=torch.bfloat16) / D ** 0.5
+        outs = [torch.empty_like(q) for _ in range(2)]
+        desc, plan, graph = pg.pool_descriptor(pool), None, None
+        fn = pg.pg_attn_paged_prefill if D == 256 else pg.pg_attn_paged_prefill_hd512
+        for turn, qo in enumerate([*shapes, *shapes]):
+            rc, plan = pg.pg_plan_paged_prefill_ring(
+                plan, 3, np.concatenate([[0], np.cumsum(qo)]), np.arange(4) * held,
+                g.permutation(3 * held).astype(np.int32), g.integers(0, 5000, 3), hq, hkv, D, ps, window, s)
+            pg.check(rc)
+
+            def call(out):
+                pg.check(fn(plan, desc, 0, q, out, window, 1.0, None, 0, s))
+
+            outs[0].fill_(float("nan"))
+            call(outs[0])
+            if graph is None:
+                s.synchronize()
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=s):
+                    call(outs[1])
+            outs[1].fill_(float("nan"))
+            graph.replay()
+            s.synchronize()
+            assert pg.pg_device_status(s) == pg.PG_OK
+            assert torch.isfinite(outs[0].float()).all()
+            assert torch.equal(outs[0], outs[1])
+        plan.close()
