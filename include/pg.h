@@ -444,6 +444,82 @@ int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_s
                       int32_t layer, int32_t num_layers, int32_t budget, const int32_t* src,
                       pg_stream_t stream);
 
+/* ---------------------------------------------------------------- 8-bit caches */
+/*
+ * The same cache in half the bytes: prep that rounds K and V to 8 bits as it writes them, attention
+ * that reads them, and the way back to a bf16 pool. (The pages' pools are bf16; decode is bound by
+ * the bytes of the cache that it reads.)
+ *
+ * A row (one head of one slot, K or V) is head_dim e4m3 codes and one scale byte b, the power of
+ * two 2^(b - 127) (e8m0): an element stands for code * 2^(b - 127). Written rows take the least
+ * exponent e = b - 127 with max |y| <= 448 * 2^e, held to [-110, 120] (rows below 448 * 2^-110 lose
+ * their small elements), and round y * 2^-e to the nearest code, ties to even; an element that is
+ * not finite becomes a NaN code and has no part in the scale. The scale is a power of two so that
+ * every element is exactly a bf16 number: attention over a row is attention over its read-back.
+ *
+ * Layouts, dense: codes [layer][page][kv][kv_head][slot][d], kv = 0 for K, 1 for V, 16-byte
+ * aligned; scales [layer][page][kv][kv_head][slot]. capacity = the element count of scales =
+ * num_layers * num_pages * 2 * num_kv_heads * page_size; codes holds capacity * head_dim.
+ *
+ * The entries take plans of pg_plan_paged_prefill and pg_plan_paged_segment (PG_ERR_PLAN_MISMATCH
+ * for a ring plan), and the plan's own device must be current (PG_ERR_STREAM otherwise). Captured
+ * calls follow their plan as the bounded-cache entries do.
+ */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  int32_t num_layers, num_pages, page_size, num_kv_heads, head_dim;
+  int64_t capacity;
+} pg_q8_pool_t;
+
+/*
+ * pg_prep_paged_q8 -- pg_prep_paged_hd256 (plan head_dim 256) or pg_prep_paged_hd512 (512; v_raw
+ * NULL, v_tok_stride not read) into an 8-bit pool: q_out as there, K and V rounded once, from fp32
+ * to their codes. Only the rows of the plan's positions in `layer` are written, codes and scales.
+ * Errors: as those entries, PG_ERR_ARG for a v_raw at head_dim 512.
+ */
+int pg_prep_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer,
+                     const pg_bf16_t* q_raw, int64_t q_tok_stride,
+                     const pg_bf16_t* k_raw, int64_t k_tok_stride,
+                     const pg_bf16_t* v_raw, int64_t v_tok_stride,
+                     const pg_bf16_t* w_q, const pg_bf16_t* w_k, float eps,
+                     const float* rope_cos, const float* rope_sin, int32_t rope_rows,
+                     pg_bf16_t* q_out, pg_stream_t stream);
+
+/*
+ * pg_kv_dequantize -- the keys that the plan's requests hold, from an 8-bit pool into the same
+ * pages and slots of a bf16 pool, layers [layer, layer + num_layers) of both; exact. Slots behind a
+ * request's last key and all other pages stay as they are. The pools share page_size, num_kv_heads
+ * and head_dim and may differ in num_pages and num_layers (both must hold the plan's pages and the
+ * layers). Errors: those of the pool checks, PG_ERR_LAYER, PG_ERR_STREAM, PG_ERR_PLAN_MISMATCH,
+ * PG_ERR_I32_OVERFLOW, PG_ERR_CUDA.
+ */
+int pg_kv_dequantize(const pg_plan_t plan, const pg_q8_pool_t* src, const pg_pool_t* dst,
+                     int32_t layer, int32_t num_layers, pg_stream_t stream);
+
+/* Bytes of device workspace pg_attn_paged_q8 needs for this plan (0 when none). Decode plans with
+ * power-of-two pages of 16 slots and more need records alone; other plans are read back into the
+ * workspace first: 4 * num_kv_heads * page_size * head_dim bytes a page of the plan's list. */
+size_t pg_q8_workspace_bytes(const pg_plan_t plan);
+
+/*
+ * pg_attn_paged_q8 -- pg_attn_paged_sink over an 8-bit pool: prefill and decode, both head dims,
+ * window and sinks (num_sink 0: the windowed attention; window_left -1: full causal attention).
+ * Pages that no query of the call sees are not read.
+ *   lse  [T][Hq] float32 or NULL
+ *   workspace: ws_bytes >= pg_q8_workspace_bytes(plan), 16-byte aligned
+ * Decode multiplies 8-bit numbers: a query row is taken as the sum of two e4m3 terms, exact for
+ * elements down to 2^-15 of the row's largest and within 2^-23 of it below, and a weight as the sum
+ * of three, within 2^-13 of itself down to 2^-18 of the row's largest weight and within 2^-31 of
+ * that below. Sums are fp32; row sums add the unrounded weights. A query row with an element that
+ * is not finite gives a NaN row.
+ * Errors: those of pg_attn_paged_sink.
+ */
+int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer,
+                     const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
+                     int32_t num_sink, float sm_scale, void* workspace, size_t ws_bytes,
+                     pg_stream_t stream);
+
 /* ---------------------------------------------------------------- decode without allocation */
 /*
  * Bytes of library-owned device scratch behind pg_attn_paged_decode_noalloc. The buffer is a

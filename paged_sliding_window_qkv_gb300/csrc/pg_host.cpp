@@ -464,6 +464,48 @@ PoolDev pool_dev(const pg_pool_t* pool, int32_t layer) {
   return v;
 }
 
+// ---- 8-bit pools
+int check_q8(const pg_q8_pool_t* pool, int32_t D) {
+  if (!pool || !pool->codes || !pool->scales) return PG_ERR_ARG;
+  if (pool->head_dim != D) return PG_ERR_LAYOUT;
+  if (pool->num_layers <= 0 || pool->num_pages <= 0 || pool->page_size <= 0 || pool->num_kv_heads <= 0)
+    return PG_ERR_LAYOUT;
+  if (!aligned16(pool->codes)) return PG_ERR_ALIGN;
+  int64_t rows = 0, codes = 0;
+  if (!mul_i64((int64_t)pool->num_layers * 2, pool->num_pages, &rows) ||
+      !mul_i64(rows, pool->num_kv_heads, &rows) || !mul_i64(rows, pool->page_size, &rows) ||
+      !mul_i64(rows, D, &codes) || !mul_i64(codes, 2, &codes))
+    return PG_ERR_I32_OVERFLOW;
+  return pool->capacity == rows ? PG_OK : PG_ERR_LAYOUT;
+}
+int check_plan_q8(const pg_plan* p, const pg_q8_pool_t* pool, int32_t layer, int32_t num_layers) {
+  if (p->head_dim != 256 && p->head_dim != 512) return PG_ERR_PLAN_MISMATCH;
+  int rc = check_q8(pool, p->head_dim);
+  if (rc) return rc;
+  if (p->num_kv_heads != pool->num_kv_heads || p->page_size != pool->page_size) return PG_ERR_PLAN_MISMATCH;
+  if (layer < 0 || num_layers < 1 || layer > pool->num_layers - num_layers) return PG_ERR_LAYER;
+  return p->max_page_id >= pool->num_pages ? PG_ERR_PAGE_OOB : PG_OK;
+}
+Q8Dev q8_dev(const pg_q8_pool_t* pool, int32_t layer) {
+  Q8Dev v;
+  v.rows_layer = (int64_t)pool->num_pages * 2 * pool->num_kv_heads * pool->page_size;
+  v.codes = pool->codes + layer * v.rows_layer * pool->head_dim;
+  v.scales = pool->scales + layer * v.rows_layer;
+  return v;
+}
+// The geometry as kernels read it; strides in elements (codes), no storage.
+PoolDev q8_geometry(const pg_q8_pool_t* pool) {
+  PoolDev v{};
+  v.num_pages = pool->num_pages;
+  v.page_size = pool->page_size;
+  v.num_kv_heads = pool->num_kv_heads;
+  v.head_dim = pool->head_dim;
+  v.stride_head = (int64_t)pool->page_size * pool->head_dim;
+  v.stride_kv = pool->num_kv_heads * v.stride_head;
+  v.stride_page = 2 * v.stride_kv;
+  return v;
+}
+
 int check_tok_input(const pg_bf16_t* p, int64_t stride, int32_t heads, int32_t D) {
   if (!p) return PG_ERR_ARG;
   if (stride < (int64_t)heads * D) return PG_ERR_ARG;
@@ -471,7 +513,16 @@ int check_tok_input(const pg_bf16_t* p, int64_t stride, int32_t heads, int32_t D
   return PG_OK;
 }
 
-int prep_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32_t D,
+// The geometry checks of a prep call's pool, and its device view.
+struct PrepPool {
+  const pg_pool_t* bf16;
+  const pg_q8_pool_t* q8;
+};
+int check_prep_pool(const pg_plan* plan, const PrepPool& p, int32_t layer, int32_t D) {
+  return p.q8 ? check_plan_q8(plan, p.q8, layer, 1) : check_plan_pool(plan, p.bf16, layer, D);
+}
+
+int prep_common(const pg_plan* plan, const PrepPool& pool, int32_t layer, int32_t D,
                 const pg_bf16_t* q_raw, int64_t qs, const pg_bf16_t* k_raw, int64_t ks,
                 const pg_bf16_t* v_raw, int64_t vs, const pg_bf16_t* w_q, const pg_bf16_t* w_k,
                 float eps, const float* rc, const float* rsn, int32_t rope_rows,
@@ -480,7 +531,7 @@ int prep_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   if (stream != plan->stream) return PG_ERR_STREAM;
   // a key-segment plan takes prep only when every step's tokens are its segment's tail
   if (plan->segment && !plan->prep_ok) return PG_ERR_COVERAGE;
-  int rc_ = check_plan_pool(plan, pool, layer, D);
+  int rc_ = check_prep_pool(plan, pool, layer, D);
   if (rc_) return rc_;
   if (!std::isfinite(eps) || !(eps > 0.0f)) return PG_ERR_NONFINITE;
   if (plan->num_tokens == 0) return PG_OK;
@@ -499,7 +550,13 @@ int prep_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   int* st = status_word(&err);
   if (!st) return err;
   a->plan = plan_dev(plan);
-  a->pool = pool_dev(pool, layer);
+  if (pool.q8) {
+    a->pool = q8_geometry(pool.q8);
+    a->q8 = q8_dev(pool.q8, layer);
+  } else {
+    a->pool = pool_dev(pool.bf16, layer);
+    a->q8 = Q8Dev{};
+  }
   a->q_raw = reinterpret_cast<const __nv_bfloat16*>(q_raw);
   a->k_raw = reinterpret_cast<const __nv_bfloat16*>(k_raw);
   a->v_raw = reinterpret_cast<const __nv_bfloat16*>(v_raw);
@@ -530,6 +587,7 @@ struct Bounded {
   float* logits = nullptr;
   int64_t logit_slots = 0;
   StatsDev stats = {};
+  const int32_t* page_ids = nullptr;  // device: the pool's pages in the order of the plan's list
 };
 
 int32_t plan_max_tiles(const pg_plan* p) {
@@ -558,6 +616,30 @@ size_t bounded_ws_bytes(const pg_plan* p) {
   return chunks > 1 ? chunks * chunk_bytes(p) : 0;
 }
 
+// Geometry, window and scale of an attention call.
+int check_attn_args(const pg_plan* plan, int32_t D, int32_t window_left, float sm_scale) {
+  const int32_t group = plan->num_qo_heads / plan->num_kv_heads;
+  const int32_t kernel_cta = attn_kernel_cta_tile_q(D, group, plan->page_size);
+  if (kernel_cta == 0 || kernel_cta != plan->cta_tile_q) return PG_ERR_PLAN_MISMATCH;
+  if (attn_kernel_kv_chunk(D) != plan->kv_chunk) return PG_ERR_PLAN_MISMATCH;
+  if (window_left < -1) return PG_ERR_WINDOW;
+  // ring addressing holds only the window the plan was built for
+  if (plan->ring && (window_left < 0 || window_left > plan->ring_window)) return PG_ERR_WINDOW;
+  if (!std::isfinite(sm_scale)) return PG_ERR_NONFINITE;
+  // the chunked decode kernel's grid holds the key chunks of a request in its z dimension
+  if (plan->decode && !attn_decode_stream_supported(D, group, plan->page_size) &&
+      plan->max_chunks > 65535)
+    return PG_ERR_I32_OVERFLOW;
+  return PG_OK;
+}
+// The rows that an attention call reads and writes.
+int check_attn_rows(const pg_bf16_t* q, const pg_bf16_t* out, const float* lse) {
+  if (!q || !out) return PG_ERR_ARG;
+  // the tensor-core prefill kernel reads Q rows and writes output rows in 32-byte accesses
+  if ((((uintptr_t)q | (uintptr_t)out) & 31u) != 0) return PG_ERR_ALIGN;
+  return lse && ((uintptr_t)lse & 3u) != 0 ? PG_ERR_ALIGN : PG_OK;
+}
+
 // `args` (the accumulating entry, whose workspace holds more) receives the launched call's
 // arguments, with num_tokens 0 when nothing ran.
 int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32_t D,
@@ -567,29 +649,17 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   if (args) args->plan.num_tokens = 0;
   if (!plan) return PG_ERR_ARG;
   if (stream != plan->stream) return PG_ERR_STREAM;
-  int rc = check_plan_pool(plan, pool, layer, D);
+  const bool listed = bounded && bounded->page_ids;
+  int rc = listed ? check_pool(pool, D) : check_plan_pool(plan, pool, layer, D);
   if (rc) return rc;
+  if ((rc = check_attn_args(plan, D, window_left, sm_scale))) return rc;
   const int32_t group = plan->num_qo_heads / plan->num_kv_heads;
-  const int32_t kernel_cta = attn_kernel_cta_tile_q(D, group, plan->page_size);
-  if (kernel_cta == 0 || kernel_cta != plan->cta_tile_q) return PG_ERR_PLAN_MISMATCH;
-  if (attn_kernel_kv_chunk(D) != plan->kv_chunk) return PG_ERR_PLAN_MISMATCH;
-  if (window_left < -1) return PG_ERR_WINDOW;
-  // ring addressing holds only the window the plan was built for
-  if (plan->ring && (window_left < 0 || window_left > plan->ring_window)) return PG_ERR_WINDOW;
-  if (!std::isfinite(sm_scale)) return PG_ERR_NONFINITE;
   const bool tma_rows = plan->decode ? attn_decode_stream_supported(D, group, plan->page_size)
                                      : attn_tc_supported(D, group, plan->page_size);
-  // the chunked decode kernel's grid holds the key chunks of a request in its z dimension
-  if (plan->decode && !attn_decode_stream_supported(D, group, plan->page_size) &&
-      plan->max_chunks > 65535)
-    return PG_ERR_I32_OVERFLOW;
   if (tma_rows && (int64_t)pool->num_pages * 2 * pool->num_kv_heads * pool->page_size > INT32_MAX)
     return PG_ERR_I32_OVERFLOW;  // tensor-map row coordinates are int32
   if (plan->num_tokens == 0) return PG_OK;
-  if (!q || !out) return PG_ERR_ARG;
-  // the tensor-core prefill kernel reads Q rows and writes output rows in 32-byte accesses
-  if ((((uintptr_t)q | (uintptr_t)out) & 31u) != 0) return PG_ERR_ALIGN;
-  if (lse && ((uintptr_t)lse & 3u) != 0) return PG_ERR_ALIGN;
+  if ((rc = check_attn_rows(q, out, lse))) return rc;
   const size_t need = args ? bounded_ws_bytes(plan) : workspace_bytes(plan);
   if (need > 0) {
     if (!ws || ws_bytes < need) return PG_ERR_WORKSPACE;
@@ -605,6 +675,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
     a.plan.num_work = plan->room_work;
     a.plan.num_pairs = plan->room_pairs;
   }
+  if (listed) a.plan.page_ids = bounded->page_ids;
   a.pool = pool_dev(pool, layer);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
@@ -775,6 +846,75 @@ int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer,
   return PG_OK;
 }
 
+// ---- attention over an 8-bit cache
+size_t align1k(size_t n) { return (n + 1023) & ~(size_t)1023; }
+
+// Plans that the 8-bit kernels do not take are read back first: the workspace holds the page list
+// 0, 1, ..., the pages in the order of the plan's list, and what the bf16 kernel needs.
+struct ReadBack {
+  size_t pages, rest, bytes;  // offsets of the pages and of the kernel's workspace, total
+};
+bool read_back(const pg_plan* p, ReadBack* w) {
+  const __int128 page = (__int128)4 * p->num_kv_heads * p->page_size * p->head_dim;
+  const __int128 pages = page * p->num_page_ids;
+  if (pages > ((__int128)1 << 60)) return false;
+  w->pages = align1k((size_t)p->num_page_ids * sizeof(int32_t));
+  w->rest = w->pages + align1k((size_t)pages);
+  w->bytes = w->rest + std::max(workspace_bytes(p), bounded_ws_bytes(p));
+  return true;
+}
+size_t q8_workspace_bytes(const pg_plan* p) {
+  if (!p || p->num_req == 0 || (p->head_dim != 256 && p->head_dim != 512)) return 0;
+  ReadBack w;
+  return read_back(p, &w) ? w.bytes : SIZE_MAX;
+}
+
+int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
+            float* lse, int32_t window_left, int32_t num_sink, float sm_scale, void* ws, size_t ws_bytes,
+            cudaStream_t stream) {
+  int rc = check_bounded_plan(plan, stream);
+  if (rc || (rc = check_bounded_attn(plan, num_sink))) return rc;
+  if ((rc = check_plan_q8(plan, pool, layer, 1))) return rc;
+  const int32_t D = plan->head_dim;
+  // what the bf16 call would refuse is refused before the read-back is launched
+  if ((rc = check_attn_args(plan, D, window_left, sm_scale))) return rc;
+  if ((int64_t)plan->num_page_ids * 2 * plan->num_kv_heads * plan->page_size > INT32_MAX)
+    return PG_ERR_I32_OVERFLOW;  // tensor-map row coordinates are int32
+  if (plan->num_tokens == 0) return PG_OK;
+  if ((rc = check_attn_rows(q, out, lse))) return rc;
+  ReadBack w;
+  if (!read_back(plan, &w) || !ws || ws_bytes < w.bytes) return PG_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PG_ERR_ALIGN;
+  int err = PG_OK;
+  int* st = status_word(&err);
+  if (!st) return err;
+  unsigned char* const base = static_cast<unsigned char*>(ws);
+  DequantArgs d{};
+  d.plan = plan_dev(plan);
+  d.src = q8_dev(pool, layer);
+  d.dst = reinterpret_cast<__nv_bfloat16*>(base + w.pages);
+  d.num_pages = pool->num_pages;
+  d.page_size = plan->page_size;
+  d.num_kv_heads = plan->num_kv_heads;
+  d.head_dim = D;
+  d.num_layers = 1;
+  d.list = 1;
+  d.window_left = window_left;
+  d.num_sink = num_sink;
+  d.ids = reinterpret_cast<int32_t*>(base);
+  d.status = st;
+  if (launch_dequant(d, stream) != cudaSuccess) return PG_ERR_CUDA;
+  const int32_t ps = plan->page_size, H = plan->num_kv_heads;
+  const pg_pool_t copy = {reinterpret_cast<pg_bf16_t*>(base + w.pages), 1, plan->num_page_ids, ps, H, D,
+                          (int64_t)plan->num_page_ids * 2 * H * ps * D, (int64_t)2 * H * ps * D,
+                          (int64_t)H * ps * D, (int64_t)ps * D, D, (int64_t)plan->num_page_ids * 2 * H * ps * D};
+  Bounded b;
+  b.num_sink = num_sink;
+  b.page_ids = d.ids;
+  return attn_common(plan, &copy, 0, D, q, out, lse, window_left, sm_scale, base + w.rest, ws_bytes - w.rest, stream,
+                     &b);
+}
+
 // Builds *plan (null) or updates it. No exception leaves a C entry: memory that the host cannot give is
 // an argument that cannot be served, and nothing has changed by then.
 template <class... Args>
@@ -891,7 +1031,7 @@ int pg_prep_paged_hd256(const pg_plan_t plan, const pg_pool_t* pool, int32_t lay
                         pg_bf16_t* q_out, pg_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   PrepArgs a;
-  int rc = prep_common(plan, pool, layer, 256, q_raw, q_tok_stride, k_raw, k_tok_stride, v_raw,
+  int rc = prep_common(plan, PrepPool{pool, nullptr}, layer, 256, q_raw, q_tok_stride, k_raw, k_tok_stride, v_raw,
                        v_tok_stride, w_q, w_k, eps, rope_cos, rope_sin, rope_rows, q_out, s, &a);
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
   return launch_prep_hd256(a, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
@@ -904,7 +1044,7 @@ int pg_prep_paged_hd512(const pg_plan_t plan, const pg_pool_t* pool, int32_t lay
                         int32_t rope_rows, pg_bf16_t* q_out, pg_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   PrepArgs a;
-  int rc = prep_common(plan, pool, layer, 512, q_raw, q_tok_stride, k_raw, k_tok_stride, nullptr,
+  int rc = prep_common(plan, PrepPool{pool, nullptr}, layer, 512, q_raw, q_tok_stride, k_raw, k_tok_stride, nullptr,
                        0, w_q, w_k, eps, rope_cos, rope_sin, rope_rows, q_out, s, &a);
   if (rc != PG_OK || plan->num_tokens == 0) return rc;
   return launch_prep_hd512(a, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
@@ -1031,6 +1171,62 @@ int pg_attn_paged_mass(const pg_plan_t plan, const pg_pool_t* pool, int32_t laye
                         : plan->decode ? launch_mass_decode(m, s)
                                        : launch_mass_prefill(m, plan->head_dim, s);
   return e == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+int pg_prep_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q_raw,
+                     int64_t q_tok_stride, const pg_bf16_t* k_raw, int64_t k_tok_stride, const pg_bf16_t* v_raw,
+                     int64_t v_tok_stride, const pg_bf16_t* w_q, const pg_bf16_t* w_k, float eps,
+                     const float* rope_cos, const float* rope_sin, int32_t rope_rows, pg_bf16_t* q_out,
+                     pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = check_bounded_plan(plan, s);
+  if (rc) return rc;
+  if (!pool) return PG_ERR_ARG;
+  if (plan->head_dim == 512 && v_raw) return PG_ERR_ARG;  // V is the norm of the raw K
+  PrepArgs a;
+  rc = prep_common(plan, PrepPool{nullptr, pool}, layer, plan->head_dim, q_raw, q_tok_stride, k_raw, k_tok_stride,
+                   v_raw, plan->head_dim == 512 ? 0 : v_tok_stride, w_q, w_k, eps, rope_cos, rope_sin, rope_rows,
+                   q_out, s, &a);
+  if (rc != PG_OK || plan->num_tokens == 0) return rc;
+  return launch_prep_q8(a, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+int pg_kv_dequantize(const pg_plan_t plan, const pg_q8_pool_t* src, const pg_pool_t* dst, int32_t layer,
+                     int32_t num_layers, pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int rc = check_bounded_plan(plan, s);
+  if (rc || (rc = check_plan_q8(plan, src, layer, num_layers))) return rc;
+  if ((rc = check_plan_pool(plan, dst, layer, plan->head_dim))) return rc;
+  if (layer > dst->num_layers - num_layers) return PG_ERR_LAYER;
+  int64_t tasks = 0;
+  if (!mul_i64((int64_t)num_layers * plan->num_page_ids, (int64_t)2 * plan->num_kv_heads, &tasks) || !fits_i32(tasks))
+    return PG_ERR_I32_OVERFLOW;
+  if (plan->num_req == 0) return PG_OK;
+  int err = PG_OK;
+  int* st = status_word(&err);
+  if (!st) return err;
+  DequantArgs d{};
+  d.plan = plan_dev(plan);
+  d.src = q8_dev(src, layer);
+  d.dst = pool_dev(dst, layer).layer_base;
+  d.dst_stride_layer = dst->stride_layer;
+  d.num_pages = std::min(src->num_pages, dst->num_pages);
+  d.page_size = plan->page_size;
+  d.num_kv_heads = plan->num_kv_heads;
+  d.head_dim = plan->head_dim;
+  d.num_layers = num_layers;
+  d.window_left = -1;
+  d.status = st;
+  return launch_dequant(d, s) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+size_t pg_q8_workspace_bytes(const pg_plan_t plan) { return q8_workspace_bytes(plan); }
+
+int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
+                     float* lse, int32_t window_left, int32_t num_sink, float sm_scale, void* workspace,
+                     size_t ws_bytes, pg_stream_t stream) {
+  return q8_attn(plan, pool, layer, q, out, lse, window_left, num_sink, sm_scale, workspace, ws_bytes,
+                 reinterpret_cast<cudaStream_t>(stream));
 }
 
 int pg_kv_evict_select(const pg_plan_t plan, const pg_kv_stats_t* stats, int32_t layer,

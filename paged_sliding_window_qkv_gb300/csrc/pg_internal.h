@@ -59,9 +59,18 @@ struct PoolDev {
   int32_t num_pages, page_size, num_kv_heads, head_dim;
 };
 
+// Device view of an 8-bit pool, narrowed to the called layer: row i is codes [i D, (i + 1) D) and
+// scales[i] (value = code * 2^(scale - 127)); rows are [page][kv][kv_head][slot].
+struct Q8Dev {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows_layer;  // rows of one layer
+};
+
 struct PrepArgs {
   PlanDev plan;
-  PoolDev pool;
+  PoolDev pool;  // 8-bit form: the geometry alone
+  Q8Dev q8;      // 8-bit form (codes null: bf16)
   const __nv_bfloat16* q_raw;
   const __nv_bfloat16* k_raw;
   const __nv_bfloat16* v_raw;  // null for the head_dim-512 form
@@ -138,6 +147,21 @@ struct EvictArgs {
   int32_t slots;          // apply: the launch covers slots [0, slots) of every segment
 };
 
+// Read-back of an 8-bit pool (see dequant.cu): to the same pages of a bf16 pool, or (list) page i of
+// the plan's list to page i of the destination, for the pages that an attention call reads, with
+// ids[i] = i.
+struct DequantArgs {
+  PlanDev plan;
+  Q8Dev src;
+  __nv_bfloat16* dst;        // first layer of the range
+  int64_t dst_stride_layer;  // elements
+  int32_t num_pages;         // pages of the 8-bit pool
+  int32_t page_size, num_kv_heads, head_dim, num_layers;
+  int32_t list, window_left, num_sink;
+  int32_t* ids;
+  int* status;
+};
+
 // Bounded-wait settings for the next launches: the default limit, or the test hook's.
 void wait_settings(uint64_t* wait_ns, int32_t* test_withhold);
 
@@ -154,6 +178,9 @@ cudaError_t launch_rope_table(float* cos_t, float* sin_t, int32_t rows, int32_t 
                               double theta, cudaStream_t stream);
 cudaError_t launch_prep_hd256(const PrepArgs& a, cudaStream_t stream);
 cudaError_t launch_prep_hd512(const PrepArgs& a, cudaStream_t stream);
+// (a.q8.codes not null: into an 8-bit pool, either head dim)
+cudaError_t launch_prep_q8(const PrepArgs& a, cudaStream_t stream);
+cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t stream);
 
 // Query tokens per CTA of the prefill attention kernel for this geometry, or 0 when the
 // kernel does not support it. Defined next to the kernels (the kernel's own derivation).

@@ -18,10 +18,15 @@
 // key-segment plan). The producer also resolves each token's request, position and page
 // (32 tokens at a time, one per lane) and passes them to the consumers in the stage header.
 //
+// Q8: K and V rows are rounded to e4m3 codes under one power-of-two scale a row (q8.cuh): the
+// largest element is a shuffle over the row's lanes, which hold the whole row in registers, so the
+// quantised write costs no second pass; a lane stores its codes as two 8-byte pieces.
+//
 // Waits are bounded (two seconds of %globaltimer); a wait that runs out sets the device
 // status word and the CTA leaves the loop. Tokens whose metadata is out of range set the
 // status word and are skipped (no copy, no store).
 #include "pg_internal.h"
+#include "q8.cuh"
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -183,10 +188,44 @@ __device__ __forceinline__ void store_rotated(const RowIn& x, float inv, const f
       make_uint4(yb[0], yb[1], yb[2], yb[3]);
 }
 
+// The lane's 16 elements of a result row, quantised with the other LPR - 1 lanes of the row (every
+// lane of the warp takes part; `live` rows are stored).
+template <int LPR>
+__device__ __forceinline__ void store_q8(float2* y, bool live, const Q8Dev& q8, int64_t row, int j, int D) {
+  const int32_t e = q8_exponent<LPR, 8>(y);
+  const float inv = q8_pow2(-e);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = q8_codes(y[2 * k], y[2 * k + 1], inv);
+  if (!live) return;
+  uint8_t* const dst = q8.codes + row * D + 8 * j;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(w[2], w[3]);
+  if (j == 0) q8.scales[row] = (uint8_t)(e + 127);
+}
+__device__ __forceinline__ void plain_row(const RowIn& x, float inv, float2* y) {
+  const float2 iv = make_float2(inv, inv);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    y[k] = __fmul2_rn(x.a[k], iv);
+    y[4 + k] = __fmul2_rn(x.b[k], iv);
+  }
+}
+__device__ __forceinline__ void rotated_row(const RowIn& x, float inv, const float2* wa, const float2* wb,
+                                            const float2* c, const float2* s, const float2* ns, float2* y) {
+  const float2 iv = make_float2(inv, inv);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 ua = __fmul2_rn(x.a[k], wa[k]), ub = __fmul2_rn(x.b[k], wb[k]);
+    y[k] = __fmul2_rn(__ffma2_rn(ua, c[k], __fmul2_rn(ub, ns[k])), iv);
+    y[4 + k] = __fmul2_rn(__ffma2_rn(ub, c[k], __fmul2_rn(ua, s[k])), iv);
+  }
+}
+
 // Stage layout: raw rows [Hq Q rows][Hkv K rows][Hkv V rows (D = 256 only)] of D bf16, then the
 // token's rotary row (D/2 fp32 cos, D/2 fp32 sin), then its TokMeta header; stage_bytes is a
 // multiple of 128. Shared memory: 2 * nst mbarriers and the abort flag, then the stages.
-template <int D>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(kPrepThreads)
 prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
   extern __shared__ __align__(128) unsigned char psm[];
@@ -337,7 +376,16 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
           RowIn x;
           const float inv =
               load_row<LPR>(sg + (size_t)(Hq + (live ? r : r0)) * (D * 2), j, D2, inv_d, a.eps, &x);
-          if (live) {
+          if constexpr (Q8) {
+            const int64_t row = (m.slot + r * a.pool.stride_head) / D;
+            float2 y[8];
+            rotated_row(x, inv, wka, wkb, c, sn, ns, y);
+            store_q8<LPR>(y, live, a.q8, row, j, D);
+            if (D == 512) {
+              plain_row(x, inv, y);
+              store_q8<LPR>(y, live, a.q8, row + a.pool.stride_kv / D, j, D);
+            }
+          } else if (live) {
             __nv_bfloat16* dst = kbase + (int64_t)r * a.pool.stride_head;
             store_rotated(x, inv, wka, wkb, c, sn, ns, dst, j, D2);
             if (D == 512) store_plain(x, inv, dst + a.pool.stride_kv, j, D2);
@@ -351,7 +399,11 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
             RowIn x;
             const float inv = load_row<LPR>(sg + (size_t)(Hq + Hkv + (live ? r : r0)) * (D * 2), j,
                                             D2, inv_d, a.eps, &x);
-            if (live) store_plain(x, inv, kbase + a.pool.stride_kv + (int64_t)r * a.pool.stride_head, j, D2);
+            if constexpr (Q8) {
+              float2 y[8];
+              plain_row(x, inv, y);
+              store_q8<LPR>(y, live, a.q8, (m.slot + a.pool.stride_kv + r * a.pool.stride_head) / D, j, D);
+            } else if (live) store_plain(x, inv, kbase + a.pool.stride_kv + (int64_t)r * a.pool.stride_head, j, D2);
           }
         }
       }
@@ -381,7 +433,7 @@ __global__ void rope_table_kernel(float* cos_t, float* sin_t, int32_t rows, int3
 // The stages of all CTAs on an SM share about 210 KB of shared memory: the CTAs an SM holds
 // (limited by registers) split it, at least two stages each, so every SM keeps ~200 KB of
 // copies in flight.
-template <int D>
+template <int D, bool Q8>
 cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream) {
   const int32_t T = a.plan.num_tokens;
   if (T <= 0) return cudaSuccess;
@@ -395,7 +447,7 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = setup.get(dev, [dev](int* n) {
-    cudaError_t r = cudaFuncSetAttribute(prep_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t r = cudaFuncSetAttribute(prep_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          227 * 1024);
     if (r != cudaSuccess) return r;
     return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
@@ -407,7 +459,7 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream) {
   static thread_local size_t smem = 0;
   if (dev != cached_dev || stage != cached_stage) {
     int by_regs = 0;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_regs, prep_kernel<D>, kPrepThreads,
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_regs, prep_kernel<D, Q8>, kPrepThreads,
                                                            0)) != cudaSuccess)
       return e;
     if (by_regs < 1) by_regs = 1;
@@ -419,7 +471,7 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream) {
     const size_t sm_bytes = (size_t)((16 * n + 4 + 127) & ~127) + (size_t)n * stage;
     if (sm_bytes > 227 * 1024) return cudaErrorInvalidValue;
     int occ = 0;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, prep_kernel<D>, kPrepThreads,
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, prep_kernel<D, Q8>, kPrepThreads,
                                                            sm_bytes)) != cudaSuccess)
       return e;
     per_sm = occ < 1 ? 1 : occ;
@@ -429,7 +481,7 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream) {
     cached_stage = stage;
   }
   const int64_t ctas = std::min<int64_t>((int64_t)sms * per_sm, T);
-  prep_kernel<D><<<(unsigned)ctas, kPrepThreads, smem, stream>>>(a, nst, stage);
+  prep_kernel<D, Q8><<<(unsigned)ctas, kPrepThreads, smem, stream>>>(a, nst, stage);
   count_launch();
   return cudaGetLastError();
 }
@@ -448,11 +500,15 @@ cudaError_t launch_rope_table(float* cos_t, float* sin_t, int32_t rows, int32_t 
 }
 
 cudaError_t launch_prep_hd256(const PrepArgs& a, cudaStream_t stream) {
-  return launch_prep<256>(a, stream);
+  return launch_prep<256, false>(a, stream);
 }
 
 cudaError_t launch_prep_hd512(const PrepArgs& a, cudaStream_t stream) {
-  return launch_prep<512>(a, stream);
+  return launch_prep<512, false>(a, stream);
+}
+
+cudaError_t launch_prep_q8(const PrepArgs& a, cudaStream_t stream) {
+  return a.pool.head_dim == 256 ? launch_prep<256, true>(a, stream) : launch_prep<512, true>(a, stream);
 }
 
 }  // namespace pg

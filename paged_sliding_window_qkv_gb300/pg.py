@@ -69,6 +69,12 @@ class pg_kv_stats_t(C.Structure):
                 ("num_kv_heads", C.c_int32), ("capacity", C.c_int64)]
 
 
+class pg_q8_pool_t(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p),
+                ("num_layers", C.c_int32), ("num_pages", C.c_int32), ("page_size", C.c_int32),
+                ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("capacity", C.c_int64)]
+
+
 class pg_plan_info_t(C.Structure):
     _fields_ = [(n, C.c_int32) for n in (
         "num_req", "num_tokens", "num_qo_heads", "num_kv_heads", "head_dim", "page_size",
@@ -399,7 +405,65 @@ def pg_kv_evict_apply(plan, pool: pg_pool_t, stats: pg_kv_stats_t, layer, num_la
                         int(budget), _ptr(src), _stream(stream))
 
 
-EXPORTED = ["pg_attn_paged_sink", "pg_sink_workspace_bytes", "pg_mass_workspace_bytes", "pg_attn_paged_mass",
+# ------------------------------------------------------------------------------ 8-bit caches
+_prep_q8 = _sig("pg_prep_paged_q8", C.c_int, _P, C.POINTER(pg_q8_pool_t), _I32, _P, _I64, _P, _I64, _P,
+                _I64, _P, _P, _F32, _P, _P, _I32, _P, _P)
+_dequant = _sig("pg_kv_dequantize", C.c_int, _P, C.POINTER(pg_q8_pool_t), C.POINTER(pg_pool_t), _I32,
+                _I32, _P)
+_q8_wsb = _sig("pg_q8_workspace_bytes", _SZ, _P)
+_attn_q8 = _sig("pg_attn_paged_q8", C.c_int, _P, C.POINTER(pg_q8_pool_t), _I32, _P, _P, _P, _I32, _I32,
+                _F32, _P, _SZ, _P)
+
+
+def q8_descriptor(codes, scales, /, **override) -> pg_q8_pool_t:
+    """pg_q8_pool_t for dense one-byte torch tensors: codes [L, P, 2, Hkv, ps, D] (e4m3) and
+    scales [L, P, 2, Hkv, ps] (e8m0)."""
+    if codes.shape[:-1] != scales.shape or not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous and of one geometry")
+    if codes.element_size() != 1 or scales.element_size() != 1:
+        raise ValueError("codes and scales are one byte an element")
+    L, P, _, Hkv, ps, D = codes.shape
+    d = pg_q8_pool_t(codes.data_ptr(), scales.data_ptr(), L, P, ps, Hkv, D, scales.numel())
+    for k, v in override.items():
+        setattr(d, k, v)
+    return d
+
+
+def _q8(pool):
+    return C.byref(pool) if pool is not None else None
+
+
+def pg_prep_paged_q8(plan, pool: pg_q8_pool_t, layer, q_raw, q_tok_stride, k_raw, k_tok_stride, v_raw,
+                     v_tok_stride, w_q, w_k, eps, rope_cos, rope_sin, rope_rows, q_out,
+                     stream=None) -> int:
+    """Prep into an 8-bit pool, either head dim (512: v_raw None)."""
+    return _prep_q8(plan.handle if plan is not None else None, _q8(pool), int(layer), _ptr(q_raw),
+                    int(q_tok_stride), _ptr(k_raw), int(k_tok_stride), _ptr(v_raw), int(v_tok_stride),
+                    _ptr(w_q), _ptr(w_k), float(eps), _ptr(rope_cos), _ptr(rope_sin), int(rope_rows),
+                    _ptr(q_out), _stream(stream))
+
+
+def pg_kv_dequantize(plan, src: pg_q8_pool_t, dst: pg_pool_t, layer, num_layers, stream=None) -> int:
+    """The plan's keys from an 8-bit pool into the same pages of a bf16 pool."""
+    return _dequant(plan.handle if plan is not None else None, _q8(src),
+                    C.byref(dst) if dst is not None else None, int(layer), int(num_layers),
+                    _stream(stream))
+
+
+def pg_q8_workspace_bytes(plan) -> int:
+    return int(_q8_wsb(plan.handle if plan is not None else None))
+
+
+def pg_attn_paged_q8(plan, pool: pg_q8_pool_t, layer, q, out, lse, window_left, num_sink, sm_scale,
+                     workspace=None, ws_bytes=0, stream=None) -> int:
+    """Attention (window, sinks) over an 8-bit pool."""
+    return _attn_q8(plan.handle if plan is not None else None, _q8(pool), int(layer), _ptr(q), _ptr(out),
+                    _ptr(lse), int(window_left), int(num_sink), float(sm_scale), _ptr(workspace),
+                    int(ws_bytes), _stream(stream))
+
+
+EXPORTED = ["pg_prep_paged_q8", "pg_kv_dequantize", "pg_q8_workspace_bytes", "pg_attn_paged_q8",
+            "pg_attn_paged_sink", "pg_sink_workspace_bytes", "pg_mass_workspace_bytes", "pg_attn_paged_mass",
             "pg_kv_evict_select", "pg_kv_evict_apply", "pg_plan_paged_prefill", "pg_plan_paged_prefill_ring", "pg_plan_paged_segment",
             "pg_attn_paged_prefill_lse", "pg_attn_paged_prefill_hd512_lse", "pg_merge_attn_states",
             "pg_plan_destroy", "pg_plan_info", "pg_rope_table",
