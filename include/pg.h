@@ -461,8 +461,8 @@ int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_s
  * aligned; scales [layer][page][kv][kv_head][slot]. capacity = the element count of scales =
  * num_layers * num_pages * 2 * num_kv_heads * page_size; codes holds capacity * head_dim.
  *
- * The entries take plans of pg_plan_paged_prefill and pg_plan_paged_segment (PG_ERR_PLAN_MISMATCH
- * for a ring plan), and the plan's own device must be current (PG_ERR_STREAM otherwise). Captured
+ * The entries take plans of pg_plan_paged_prefill, pg_plan_paged_segment and
+ * pg_plan_paged_shared (PG_ERR_PLAN_MISMATCH for a ring plan), and the plan's own device must be current (PG_ERR_STREAM otherwise). Captured
  * calls follow their plan as the bounded-cache entries do.
  */
 typedef struct {
@@ -519,6 +519,60 @@ int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t lay
                      const pg_bf16_t* q, pg_bf16_t* out, float* lse, int32_t window_left,
                      int32_t num_sink, float sm_scale, void* workspace, size_t ws_bytes,
                      pg_stream_t stream);
+
+/* ---------------------------------------------------------------- shared prefixes */
+/*
+ * pg_plan_paged_shared -- the plan of pg_plan_paged_prefill for a batch whose requests share
+ * prefixes: groups of consecutive requests whose first keys are the same pages. It is that plan for
+ * every other entry (prep, pg_attn_paged_prefill, ...); pg_attn_paged_shared reads a group's prefix
+ * once for all its requests, where a cascade of segment plans reads it once a request.
+ *
+ * Inputs as for pg_plan_paged_prefill (every request lists all its pages), plus
+ *   group_indptr[num_groups+1]  int64, group_indptr[0] == 0, strictly increasing, last num_req:
+ *                               group i is requests group_indptr[i] .. group_indptr[i+1]-1
+ *   prefix_len[num_groups]      int64 >= 0, a multiple of page_size: the requests of the group list
+ *                               the same first prefix_len / page_size pages, and every request
+ *                               starts at or past it (start_pos >= prefix_len); PG_ERR_COVERAGE
+ *                               otherwise. 0: the group shares nothing.
+ * head_dim 256 or 512, page_size a power of two from 8 on, num_qo_heads / num_kv_heads 1, 2, 4, 8
+ * or 16 (PG_ERR_PLAN_MISMATCH otherwise). Updates in place, errors and stream binding as for
+ * pg_plan_paged_prefill; a plan that was built by another plan entry may become a shared one and
+ * back. A captured pg_attn_paged_shared follows updates to as many groups, requests, tokens and pages.
+ */
+int pg_plan_paged_shared(pg_plan_t* plan, int32_t num_req, const int64_t* qo_indptr,
+                         const int64_t* kv_page_indptr, const int32_t* page_ids,
+                         const int32_t* last_page_len, const int64_t* start_pos,
+                         int32_t num_groups, const int64_t* group_indptr,
+                         const int64_t* prefix_len, int32_t num_qo_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t page_size, pg_stream_t stream);
+
+/* Bytes of device workspace pg_attn_paged_shared / pg_attn_paged_shared_q8 need for this plan
+ * (0 when none, or when the plan is not one of pg_plan_paged_shared). */
+size_t pg_shared_workspace_bytes(const pg_plan_t plan);
+size_t pg_shared_q8_workspace_bytes(const pg_plan_t plan);
+
+/*
+ * pg_attn_paged_shared -- full causal attention (window_left -1) over a plan of
+ * pg_plan_paged_shared, prefill and decode, both head dims: the query rows of a group meet its
+ * prefix as one block of rows, cut along the keys where the batch has few rows, each request meets
+ * its own keys as in pg_attn_paged_sink, and the parts are joined in fp32 by their normalisers.
+ * (What a request's own keys give is rounded to bf16 before the join, a prefix's part is not.)
+ *   q, out  [T][Hq][head_dim] bf16, 32-byte aligned;  lse [T][Hq] float32 or NULL
+ *   workspace: ws_bytes >= pg_shared_workspace_bytes(plan), 16-byte aligned
+ * Errors: those of pg_attn_paged_sink; PG_ERR_PLAN_MISMATCH for another kind of plan.
+ */
+int pg_attn_paged_shared(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer,
+                         const pg_bf16_t* q, pg_bf16_t* out, float* lse, float sm_scale,
+                         void* workspace, size_t ws_bytes, pg_stream_t stream);
+
+/* The same over an 8-bit pool (workspace: pg_shared_q8_workspace_bytes(plan)); each prefix is read
+ * back into the workspace once a call, its requests' own keys are read as in pg_attn_paged_q8. Under
+ * a captured call an update's prefixes may hold as many pages as the workspace at capture has room
+ * for beyond that size (4 * num_kv_heads * page_size * head_dim bytes a page; pages past it set the
+ * device status word). */
+int pg_attn_paged_shared_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer,
+                            const pg_bf16_t* q, pg_bf16_t* out, float* lse, float sm_scale,
+                            void* workspace, size_t ws_bytes, pg_stream_t stream);
 
 /* ---------------------------------------------------------------- decode without allocation */
 /*

@@ -48,6 +48,10 @@
 // a unit walks its sink tiles and then its window tiles (bounded.cuh; one run where they meet),
 // and the row sum adds the unrounded weights (see attn_split.cu).
 //
+// PART (with BC) is one part of a row's keys: units are (pair of tiles, run of keys), and a row leaves
+// its mean in fp32 with its reference and sum, at the part's rows of a record array, for a later join
+// (shared.cu). A pair-table entry names its rows' query tokens and its run of keys; part_row its records.
+//
 // Every wait is bounded (two seconds of %globaltimer unless the launch passes a shorter limit);
 // a wait that runs out sets the device status word, makes the CTA drain and free its tensor
 // memory, and return.
@@ -134,6 +138,11 @@ struct TcArgs {
   int32_t page_size, num_pages, num_kv_heads, box_rows_k, box_rows_v;
   float scale_log2;
   float* lse;  // optional [T][Hq] natural-log normaliser of each row (null: not written)
+  // PART: records of a pair-table entry's token t at row part_row[entry] + t: mean [row][Hq][D] and
+  // (reference, sum) [row][Hq][2]
+  float* part_o;
+  float* part_ml;
+  const int32_t* part_row;
   int* status;
   uint64_t wait_ns;       // limit of every bounded wait
   int32_t test_withhold;  // test hook: the leader's K producer withholds its first arrival
@@ -148,6 +157,7 @@ struct TcUnit {
   // keys held: positions [kv_start, kv_len); key tiles start kb0 + 64 t, 64-aligned from kv_start
   int32_t kvp0, kvp1, kv_len, kv_start, sp, kb0, ntiles, g, dh;
   int32_t ns;  // BC: the first ns tiles are sink tiles, aligned from kv_start
+  int32_t prow;      // PART: the entry's first record row
   int32_t lo, sink;  // BC: some row of the pair sees keys [lo, ...) and those below sink
   template <bool BC>
   __device__ __forceinline__ int32_t key(int32_t t) const {  // first key of the t-th tile
@@ -162,11 +172,12 @@ struct TcUnit {
     return kv_start + (((t < ns ? sink - 1 : lo) - kv_start) & ~(rows - 1));
   }
 };
-template <bool BC>
+template <bool BC, bool PART = false>
 __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t ndh, int32_t rank) {
   const PlanDev& pl = a.plan;
   TcUnit u;
   const int32_t pr = w / (a.num_kv_heads * ndh);
+  if constexpr (PART) u.prow = __ldg(a.part_row + pr);
   u.g = (w / ndh) % a.num_kv_heads;
   u.dh = w % ndh;
   // the pair's entry of the plan's pair table: two 16-byte loads, no dependent lookups
@@ -222,7 +233,7 @@ __device__ __forceinline__ void tc_unit_prefetch(const TcArgs& a, int32_t w, int
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a.plan.pair_tab + 8 * pr));
 }
 
-template <int DQK, bool BC>
+template <int DQK, bool BC, bool PART>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                const __grid_constant__ CUtensorMap tm_v, TcArgs a) {
@@ -734,7 +745,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     TcUnit u;
     int32_t ui = 0;
     if (unit_at(0) < nunits) {
-      u = tc_unit<BC>(a, unit_at(0), NDH, (int32_t)rank);
+      u = tc_unit<BC, PART>(a, unit_at(0), NDH, (int32_t)rank);
       if (DQK != 256 || h == 0) ok = store_q(u, 0);
     }
     for (int32_t w = unit_at(0); ok && w < nunits; w = unit_at(++ui)) {
@@ -1023,7 +1034,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (!ok) break;
       const int32_t wn = unit_at(ui + 1);
       TcUnit un;
-      if (wn < nunits) un = tc_unit<BC>(a, wn, NDH, (int32_t)rank);
+      if (wn < nunits) un = tc_unit<BC, PART>(a, wn, NDH, (int32_t)rank);
       if constexpr (DQK == 256) {
         // The row sum is the sum of the two warps' partial sums, swapped through shared memory.
         // The warp that wrote the last tile's P waits for that tile's PV before publishing (its
@@ -1078,6 +1089,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // (a NaN sum of BC stays: the row has seen a key)
         const bool some = BC ? l != 0.f : l > 0.f;
         const float inv = some ? 1.f / l : 0.f;
+        if constexpr (PART) {
+          // the row's mean and (reference, sum): 512 contiguous bytes of the row per thread
+          const int64_t rec = (int64_t)(u.prow + u.q0 + u.tok0 + (row >> gsh)) * Hq + u.g * G + (row & gmask);
+          if (rvalid && h == 0 && u.dh == 0)  // (both output halves of hd512 agree)
+            *reinterpret_cast<float2*>(a.part_ml + 2 * rec) = make_float2(m_ref, l);
+          float* const dst = a.part_o + rec * DQK + u.dh * kDV + h * (kDV / 2);
+#pragma unroll 1
+          for (int c = 0; c < kDV / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tl + kTmO + h * (kDV / 2) + c * 32, o);
+            tmem_wait_ld();
+            if (rvalid) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = ntiles == 0 ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // (a workspace is 16-byte aligned)
+                *reinterpret_cast<uint4*>(dst + c * 32 + 4 * k) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+        } else {
         if (a.lse && rvalid && h == 0 && u.dh == 0)  // both output halves of hd512 agree
           a.lse[(int64_t)(u.q0 + u.tok0 + (row >> gsh)) * Hq + u.g * G + (row & gmask)] =
               some ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
@@ -1150,6 +1182,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
           }
         }
+        }  // !PART
         // the next unit's first PV overwrites O only after these reads
         tc_fence_before();
         if (DQK == 256 && ntiles > 0) {
@@ -1185,7 +1218,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // ------------------------------------------------------------------ host side
-template <int DQK, bool BC>
+template <int DQK, bool BC, bool PART = false>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
@@ -1251,6 +1284,9 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   t.stride_head = a.pool.stride_head;
   t.scale_log2 = a.sm_scale_log2;
   t.lse = a.lse;
+  t.part_o = a.part_o;
+  t.part_ml = a.part_ml;
+  t.part_row = a.part_row;
   t.status = a.status;
   t.wait_ns = a.wait_ns;
   t.test_withhold = a.test_withhold;
@@ -1261,7 +1297,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = setup.get(dev, [dev](int* n) {
-    cudaError_t r = cudaFuncSetAttribute(attn_tc_kernel<DQK, BC>,
+    cudaError_t r = cudaFuncSetAttribute(attn_tc_kernel<DQK, BC, PART>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<DQK>::SMEM);
     if (r != cudaSuccess) return r;
     r = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
@@ -1287,7 +1323,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, BC>, tq, tkv, tv, t);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, BC, PART>, tq, tkv, tv, t);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -1307,6 +1343,10 @@ cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int32_t head_dim, cudaStre
   if (a.bounded)
     return head_dim == 256 ? launch_tc<256, true>(a, stream) : launch_tc<512, true>(a, stream);
   return head_dim == 256 ? launch_tc<256, false>(a, stream) : launch_tc<512, false>(a, stream);
+}
+
+cudaError_t launch_attn_parts(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
+  return head_dim == 256 ? launch_tc<256, true, true>(a, stream) : launch_tc<512, true, true>(a, stream);
 }
 
 int32_t attn_tc_rows() { return kM; }

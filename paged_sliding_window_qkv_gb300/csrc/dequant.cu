@@ -45,18 +45,19 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(DequantArgs a) {
   const int32_t kvh = (int32_t)(task % heads);
   const int32_t i = (int32_t)(task / heads % NP), layer = (int32_t)(task / heads / NP);
   const PlanDev& pl = a.plan;
+  if (i >= (a.whole ? *a.whole : pl.kv_page_indptr[pl.num_req])) return;  // room behind the list
   if (a.list && kvh == 0 && lane == 0) a.ids[i] = i;
   const int32_t page = pl.page_ids[i];
-  const int32_t r = request_of(pl, i, lane);
-  // the keys that the page holds: key indices [k0, k0 + rows) from the request's first key
-  const int32_t k0 = (i - pl.kv_page_indptr[r]) * ps;
-  const bool last = i + 1 == pl.kv_page_indptr[r + 1];
-  int32_t rows = last ? min(ps, pl.last_page_len[r]) : ps;
-  if (a.list && a.window_left >= 0) {
-    // a page that lies between the sinks and the first query's window is not read
-    const int64_t first = (int64_t)pl.kv_start[r] + k0;
-    const int64_t lo = (int64_t)pl.start_pos[r] - a.window_left;
-    if (first + ps <= lo && first >= a.num_sink) return;
+  int32_t rows = ps;  // slots of the page that hold keys
+  if (!a.whole) {
+    const int32_t r = request_of(pl, i, lane);
+    if (i + 1 == pl.kv_page_indptr[r + 1]) rows = min(ps, pl.last_page_len[r]);
+    if (a.list && a.window_left >= 0) {
+      // a page that lies between the sinks and the first query's window is not read
+      const int64_t first = (int64_t)pl.kv_start[r] + (int64_t)(i - pl.kv_page_indptr[r]) * ps;
+      const int64_t lo = (int64_t)pl.start_pos[r] - a.window_left;
+      if (first + ps <= lo && first >= a.num_sink) return;
+    }
   }
   const bool good = page >= 0 && page < a.num_pages;
   if (!good) {

@@ -10,6 +10,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <memory>
 #include <exception>
 #include <mutex>
 #include <new>
@@ -110,6 +111,11 @@ struct pg_plan {
   int64_t tiles = 0;              // tiles of 128 keys over all requests (one KV head)
   std::vector<int32_t> host_ids;  // the page list, for the check below
   mutable int8_t shared = -1;     // a page is listed twice (-1: not looked at yet)
+  // shared prefixes (pg_plan_paged_shared; null otherwise): the requests' own keys as a segment plan
+  // over arrays in `dev` (it owns nothing there), and the prefixes' parts
+  std::unique_ptr<pg_plan> own;
+  int32_t num_groups = 0, num_parts = 0, room_parts = 0, parts_most = 0, prefix_pages = 0;
+  size_t o_part = 0, o_part_row = 0, o_part_live = 0, o_tok_parts = 0, o_pre_pages = 0;
 };
 
 namespace {
@@ -128,6 +134,61 @@ void free_stage(PlanStage* st) {
   }
 }
 
+// Groups of consecutive requests that share their first keys.
+struct Groups {
+  int32_t num = 0;
+  const int64_t* indptr = nullptr;
+  const int64_t* prefix = nullptr;
+};
+
+// SMs of the current device.
+int sm_count() {
+  static PerDeviceOnce once;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (once.get(dev, [dev](int* v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); }, &n) !=
+      cudaSuccess)
+    return 0;
+  return n;
+}
+
+// One entry of the pair table for every two query tiles of a run of rows (a request, or a group's
+// rows before its prefix): see PlanDev.
+void put_pairs(std::vector<int32_t>* tab, int32_t tile, int32_t q0, int32_t len, int32_t start, int32_t kvp0,
+               int32_t kvp1, int32_t kv_end, int32_t kv_start) {
+  for (int64_t t = 0; t < len; t += 2 * (int64_t)tile) {
+    const int32_t e[8] = {(int32_t)t, q0, len, start, kvp0, kvp1, kv_end, kv_start};
+    tab->insert(tab->end(), e, e + 8);
+  }
+}
+// The pairs that see the most keys come first (a window keeps that order): on 8 prompts of
+// 384..2026 tokens the busiest cluster then has 4% more than the mean, against 22% request by
+// request.
+void sort_pairs(std::vector<int32_t>* tab, int32_t tile, bool sort) {
+  const size_t n = tab->size() / 8;
+  std::vector<int32_t> order(n), sorted(tab->size());
+  for (size_t i = 0; i < n; ++i) order[i] = (int32_t)i;
+  auto seen = [&](int32_t i) {
+    const int32_t* e = tab->data() + 8 * (size_t)i;
+    const int64_t end = (int64_t)e[3] + std::min<int64_t>((int64_t)e[0] + 2 * (int64_t)tile, e[2]);
+    return std::min<int64_t>(end, e[6]) - e[7];
+  };
+  if (sort) std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return seen(x) < seen(y); });
+  std::reverse(order.begin(), order.end());
+  for (size_t i = 0; i < n; ++i) std::copy_n(tab->data() + 8 * (size_t)order[i], 8, sorted.data() + 8 * i);
+  tab->swap(sorted);
+}
+
+// The most parts that a prefix is cut into, for as many tokens and groups whatever their lengths (the
+// records' room, which captured calls keep): enough for one unit a cluster, and four where there are
+// fewer than two rounds of units anyway.
+int32_t most_parts(int32_t tokens, int32_t groups, int32_t tile, int32_t units_per_pair, int32_t sms) {
+  const int64_t pairs = std::max<int64_t>(groups, ((int64_t)tokens + 2 * tile - 1) / (2 * tile));
+  const int64_t units = std::max<int64_t>(1, pairs * units_per_pair), clusters = std::max(1, sms / 2);
+  if (2 * units <= clusters) return (int32_t)std::min<int64_t>(clusters / units, 64);
+  return units <= 2 * clusters ? 4 : 1;
+}
+
 // ring_window < 0: linear addressing (slot = position, pages cover [0, kv_len) exactly, with
 // last_page_len). ring_window >= 0: ring addressing for window-crossing requests: logical page
 // pos / ps lives in the request's page (pos / ps) mod (pages held), kv_len = start_pos + qo_len,
@@ -141,7 +202,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
                const int64_t* kv_page_indptr, const int32_t* page_ids,
                const int32_t* last_page_len, const int64_t* start_pos, int32_t Hq,
                int32_t Hkv, int32_t D, int32_t ps, cudaStream_t stream,
-               int32_t ring_window = -1, const int64_t* kv_start = nullptr) {
+               int32_t ring_window = -1, const int64_t* kv_start = nullptr, const Groups* groups = nullptr) {
   const bool ring = ring_window >= 0;
   const bool segment = kv_start != nullptr;
   if (ring && segment) return PG_ERR_ARG;
@@ -241,33 +302,12 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       }
       // the tcgen05 prefill runs query tiles in pairs (one per CTA of a cluster) that share
       // their key tiles; a request with an odd number of tiles ends with a single-tile pair
-      for (int64_t t = 0; t < len; t += 2 * (int64_t)cta) {
-        const int32_t kv_len =
-            ring ? start[r] + len : kvs[r] + (kvp[r + 1] - kvp[r] - 1) * ps + last[r];
-        const int32_t e[8] = {(int32_t)t, qo[r], len, start[r], kvp[r], kvp[r + 1], kv_len, kvs[r]};
-        ptab.insert(ptab.end(), e, e + 8);
-      }
+      const int32_t kv_len =
+          ring ? start[r] + len : kvs[r] + (kvp[r + 1] - kvp[r] - 1) * ps + last[r];
+      put_pairs(&ptab, cta, qo[r], len, start[r], kvp[r], kvp[r + 1], kv_len, kvs[r]);
     }
     nwork = (int64_t)wreq.size();
-    // The pairs that see the most keys come first (a window keeps that order): on 8 prompts of
-    // 384..2026 tokens the busiest cluster then has 4% more than the mean, against 22% request by
-    // request. (Decode looks requests up in the table.)
-    if (!all_one) {
-      const size_t n = ptab.size() / 8;
-      std::vector<int32_t> order(n), sorted(ptab.size());
-      for (size_t i = 0; i < n; ++i) order[i] = (int32_t)i;
-      auto seen = [&](int32_t i) {
-        const int32_t* e = ptab.data() + 8 * (size_t)i;
-        const int64_t end = (int64_t)e[3] + std::min<int64_t>((int64_t)e[0] + 2 * (int64_t)cta, e[2]);
-        return std::min<int64_t>(end, e[6]) - e[7];
-      };
-      if (num_req > 1)
-        std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return seen(x) < seen(y); });
-      std::reverse(order.begin(), order.end());
-      for (size_t i = 0; i < n; ++i)
-        std::copy_n(ptab.data() + 8 * (size_t)order[i], 8, sorted.data() + 8 * i);
-      ptab.swap(sorted);
-    }
+    if (!all_one) sort_pairs(&ptab, cta, num_req > 1);  // (decode looks requests up in the table)
   }
   if (!fits_i32(nwork)) return PG_ERR_I32_OVERFLOW;
   // A graph that captured the plan's calls holds the addresses of these arrays, so an update to as many
@@ -280,6 +320,86 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   wtok.resize((size_t)room_work, 0);
   ptab.resize((size_t)room_pairs * 8, 0);
   const int32_t live[2] = {(int32_t)nwork, npairs};
+
+  // Shared prefixes: the requests' own keys as segments, and the parts of each group's prefix.
+  std::vector<int32_t> kvp2, kvs2, pages2, ptab2, part, part_row, tok_parts, pre_pages;
+  int32_t seen2 = 0, num_parts = 0, room_parts = 0, parts_most = 0, pre_total = 0;
+  int64_t tiles2 = 0;
+  if (groups) {
+    if (!attn_tc_supported(D, group, ps) || cta <= 0) return PG_ERR_PLAN_MISMATCH;
+    if (groups->num < 0 || (groups->num > 0 && (!groups->indptr || !groups->prefix))) return PG_ERR_ARG;
+    if ((groups->num == 0) != (num_req == 0)) return PG_ERR_ARG;
+    if (groups->num > 0 && (groups->indptr[0] != 0 || groups->indptr[groups->num] != num_req)) return PG_ERR_ARG;
+    kvp2.push_back(0);
+    std::vector<int32_t> pre(groups->num);
+    for (int32_t g = 0; g < groups->num; ++g) {
+      const int64_t r0 = groups->indptr[g], r1 = groups->indptr[g + 1], len = groups->prefix[g];
+      if (r1 <= r0 || r1 > num_req) return PG_ERR_ARG;
+      if (len < 0) return PG_ERR_ARG;
+      if (len % ps != 0) return PG_ERR_COVERAGE;
+      for (int64_t r = r0; r < r1; ++r) {
+        if (len > start[r]) return PG_ERR_COVERAGE;
+        const int32_t n = (int32_t)(len / ps);
+        if (!std::equal(page_ids + kvp[r], page_ids + kvp[r] + n, page_ids + kvp[r0])) return PG_ERR_COVERAGE;
+        pages2.insert(pages2.end(), page_ids + kvp[r] + n, page_ids + kvp[r + 1]);
+        kvp2.push_back((int32_t)pages2.size());
+        kvs2.push_back((int32_t)len);
+        const int32_t held = (kvp[r + 1] - kvp[r] - 1) * ps + last[r] - (int32_t)len;
+        seen2 = std::max(seen2, held);
+        tiles2 += (held + 127) / 128;
+        put_pairs(&ptab2, cta, qo[r], qo[r + 1] - qo[r], start[r], kvp2[r], kvp2[r + 1], held + (int32_t)len,
+                  (int32_t)len);
+      }
+      pre[g] = (int32_t)len;
+    }
+    if (!all_one) sort_pairs(&ptab2, cta, num_req > 1);
+    // How long a part is: every candidate length costs rounds of units over the clusters, each as
+    // long as its key tiles and a start and an epilogue worth about five.
+    const int32_t heads = Hkv * (D / 256), clusters = std::max(1, sm_count() / 2);
+    parts_most = num_req > 0 ? most_parts(T, groups->num, cta, heads, sm_count()) : 0;
+    const int32_t most_len = pre.empty() ? 0 : *std::max_element(pre.begin(), pre.end());
+    const int32_t step = std::max(64, ps);
+    auto group_tokens = [&](int32_t g) { return qo[groups->indptr[g + 1]] - qo[groups->indptr[g]]; };
+    int64_t best = 0;
+    int32_t run = step;
+    for (int32_t k = 1; k <= parts_most && most_len > 0; ++k) {
+      const int64_t len = ((int64_t)most_len + (int64_t)k * step - 1) / ((int64_t)k * step) * step;
+      int64_t units = 0;
+      for (int32_t g = 0; g < groups->num; ++g)
+        units += (((int64_t)group_tokens(g) + 2 * cta - 1) / (2 * cta)) * ((pre[g] + len - 1) / len) * heads;
+      const int64_t cost = (units + clusters - 1) / clusters * (len / 64 + 5);
+      if (k == 1 || cost < best) {
+        best = cost;
+        run = (int32_t)std::min<int64_t>(len, INT32_MAX - 1024);
+      }
+    }
+    tok_parts.assign((size_t)T, 0);
+    for (int32_t g = 0; g < groups->num; ++g) {
+      const int32_t q0 = qo[groups->indptr[g]], len = group_tokens(g), at = kvp[groups->indptr[g]];
+      const int32_t parts = (int32_t)(((int64_t)pre[g] + run - 1) / run);
+      pre_pages.insert(pre_pages.end(), page_ids + at, page_ids + at + pre[g] / ps);
+      for (int32_t i = 0; i < parts; ++i) {
+        const int32_t k0 = i * run, k1 = (int32_t)std::min<int64_t>((int64_t)k0 + run, pre[g]);
+        const size_t before = part.size();
+        // (a row stands behind the whole prefix, so it sees every key of the run)
+        put_pairs(&part, cta, q0, len, k1, pre_total + k0 / ps, pre_total + (k1 + ps - 1) / ps, k1, k0);
+        if (!fits_i32((int64_t)i * T)) return PG_ERR_I32_OVERFLOW;
+        part_row.resize(part_row.size() + (part.size() - before) / 8, i * T);
+      }
+      std::fill(tok_parts.begin() + q0, tok_parts.begin() + q0 + len, parts);
+      pre_total += pre[g] / ps;
+    }
+    if (!fits_i32((int64_t)(part.size() / 8) * heads)) return PG_ERR_I32_OVERFLOW;
+    num_parts = (int32_t)(part.size() / 8);
+    // room for what any batch of as many groups, requests, tokens and pages needs
+    room_parts = num_req > 0 ? (groups->num + (T - groups->num) / (2 * cta)) * parts_most : 0;
+    part.resize((size_t)room_parts * 8, 0);
+    part_row.resize((size_t)room_parts, 0);
+    pages2.resize((size_t)NP, 0);
+    pre_pages.resize((size_t)NP, 0);
+    ptab2.resize((size_t)room_pairs * 8, 0);
+  }
+  const int32_t part_live[3] = {0, num_parts, pre_total};
 
   // Pack everything into one int32 array and upload it on the plan's stream.
   std::vector<int32_t> host;
@@ -306,6 +426,26 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.o_wreq = put(wreq.data(), wreq.size());
   q.o_wtok = put(wtok.data(), wtok.size());
   q.o_pair = put(ptab.data(), ptab.size());
+  std::unique_ptr<pg_plan> own;
+  if (groups) {
+    own.reset(new pg_plan);
+    own->o_live = q.o_live;
+    own->o_qo = q.o_qo;
+    own->o_last = q.o_last;
+    own->o_start = q.o_start;
+    own->o_tokreq = q.o_tokreq;
+    own->o_wreq = q.o_wreq;
+    own->o_wtok = q.o_wtok;
+    own->o_kvp = put(kvp2.data(), kvp2.size());
+    own->o_pages = put(pages2.data(), pages2.size());
+    own->o_kvs = put(kvs2.data(), kvs2.size());
+    own->o_pair = put(ptab2.data(), ptab2.size());
+    q.o_part = put(part.data(), part.size());
+    q.o_part_row = put(part_row.data(), part_row.size());
+    q.o_part_live = put(part_live, 3);
+    q.o_tok_parts = put(tok_parts.data(), tok_parts.size());
+    q.o_pre_pages = put(pre_pages.data(), pre_pages.size());
+  }
   if (host.empty()) host.assign(4, 0);
 
   int err = PG_OK;
@@ -374,6 +514,30 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   q.page_keys = num_req > 0 ? (int32_t)std::min<int64_t>((int64_t)(NP - num_req + 1) * ps, INT32_MAX) : 0;
   q.tiles = tiles;
   q.host_ids = std::move(pids);
+  if (groups) {
+    auto fields = [](pg_plan* o, const pg_plan& f) {
+      o->num_req = f.num_req; o->num_tokens = f.num_tokens; o->num_qo_heads = f.num_qo_heads;
+      o->num_kv_heads = f.num_kv_heads; o->head_dim = f.head_dim; o->page_size = f.page_size;
+      o->max_page_id = f.max_page_id; o->max_last_page_len = f.max_last_page_len; o->max_qo_len = f.max_qo_len;
+      o->max_kv_len = f.max_kv_len; o->max_pos_end = f.max_pos_end; o->cta_tile_q = f.cta_tile_q;
+      o->decode = f.decode; o->kv_chunk = f.kv_chunk; o->num_work = f.num_work; o->num_pairs = f.num_pairs;
+      o->room_work = f.room_work; o->room_pairs = f.room_pairs; o->stream = f.stream; o->device = f.device;
+      o->dev = f.dev; o->dev_elems = f.dev_elems; o->dev_cap = f.dev_cap;
+    };
+    fields(own.get(), q);
+    own->segment = 1;
+    own->max_chunks = (seen2 + chunk - 1) / chunk;
+    own->num_page_ids = NP;  // (the list's room: a captured call covers whatever an update leaves in it)
+    own->max_seen = seen2;
+    own->page_keys = num_req > 0 ? (int32_t)std::min<int64_t>((int64_t)(NP - num_req + 1) * ps, INT32_MAX) : 0;
+    own->tiles = tiles2;
+    q.own = std::move(own);
+    q.num_groups = groups->num;
+    q.num_parts = num_parts;
+    q.room_parts = room_parts;
+    q.parts_most = parts_most;
+    q.prefix_pages = pre_total;
+  }
 
   // Commit: only now does the caller's plan change.
   int32_t* old = p->dev;
@@ -915,6 +1079,186 @@ int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const 
                      &b);
 }
 
+// ---- attention over shared prefixes
+// The workspace: the parts' records, the rows' lse, and what the call on the own keys needs.
+struct SharedWs {
+  size_t ml, o, lse, own, bytes;
+};
+bool shared_ws(const pg_plan* p, size_t own_bytes, SharedWs* w) {
+  const __int128 rows = (__int128)p->num_tokens * p->num_qo_heads, recs = rows * p->parts_most;
+  if (recs * p->head_dim * 4 > ((__int128)1 << 60)) return false;
+  w->ml = 0;
+  w->o = align256((size_t)recs * 2 * sizeof(float));
+  w->lse = w->o + align256((size_t)recs * p->head_dim * sizeof(float));
+  w->own = w->lse + align256((size_t)rows * sizeof(float));
+  w->bytes = w->own + own_bytes;
+  return true;
+}
+size_t shared_workspace_bytes(const pg_plan* p) {
+  if (!p || !p->own || p->num_req == 0) return 0;
+  SharedWs w;
+  return shared_ws(p, std::max(workspace_bytes(p->own.get()), bounded_ws_bytes(p->own.get())), &w) ? w.bytes : SIZE_MAX;
+}
+
+// The prefixes' parts: pool pages `page_ids` (device, prefix by prefix) of `pool`.
+AttnArgs part_args(const pg_plan* p, const PoolDev& pool, const int32_t* page_ids, int32_t num_page_ids,
+                   const pg_bf16_t* q, float sm_scale, unsigned char* base, const SharedWs& w, int* status) {
+  AttnArgs a{};
+  a.plan = plan_dev(p);
+  a.plan.pair_tab = p->dev + p->o_part;
+  a.plan.page_ids = page_ids;
+  a.plan.num_page_ids = num_page_ids;
+  a.plan.num_pairs = p->num_parts;
+  if (capturing(p->stream)) {
+    a.plan.live = p->dev + p->o_part_live;
+    a.plan.num_pairs = p->room_parts;
+  }
+  a.pool = pool;
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  a.window_left = -1;
+  a.num_qo_heads = p->num_qo_heads;
+  a.group = p->num_qo_heads / p->num_kv_heads;
+  a.cta_tile_q = p->cta_tile_q;
+  a.bounded = 1;
+  a.part_o = reinterpret_cast<float*>(base + w.o);
+  a.part_ml = reinterpret_cast<float*>(base + w.ml);
+  a.part_row = p->dev + p->o_part_row;
+  a.status = status;
+  wait_settings(&a.wait_ns, &a.test_withhold);
+  return a;
+}
+cudaError_t shared_join(const pg_plan* p, pg_bf16_t* out, float* lse, unsigned char* base, const SharedWs& w,
+                        cudaStream_t stream) {
+  SharedJoinArgs j{};
+  j.part_o = reinterpret_cast<const float*>(base + w.o);
+  j.part_ml = reinterpret_cast<const float*>(base + w.ml);
+  j.tok_parts = p->dev + p->o_tok_parts;
+  j.out = reinterpret_cast<__nv_bfloat16*>(out);
+  j.lse = lse;
+  j.num_tokens = p->num_tokens;
+  j.num_qo_heads = p->num_qo_heads;
+  return launch_shared_join(j, p->head_dim, stream);
+}
+// checks that both shared entries make before anything is launched
+int check_shared(const pg_plan* plan, const pg_bf16_t* q, const pg_bf16_t* out, const float* lse, float sm_scale,
+                 cudaStream_t stream) {
+  int rc = check_bounded_plan(plan, stream);
+  if (rc) return rc;
+  if (!plan->own) return PG_ERR_PLAN_MISMATCH;
+  if ((rc = check_bounded_attn(plan, 0))) return rc;
+  // the rows of a group are counted on from the prefix's end
+  if ((int64_t)plan->max_pos_end + plan->num_tokens > kLastEnd) return PG_ERR_I32_OVERFLOW;
+  if (!fits_i32((int64_t)plan->num_tokens * plan->num_qo_heads)) return PG_ERR_I32_OVERFLOW;  // the join's grid
+  if ((rc = check_attn_args(plan, plan->head_dim, -1, sm_scale))) return rc;
+  if (plan->num_tokens == 0) return PG_OK;
+  return check_attn_rows(q, out, lse);
+}
+
+int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
+                float* lse, float sm_scale, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = check_shared(plan, q, out, lse, sm_scale, stream);
+  if (rc) return rc;
+  const int32_t D = plan->head_dim;
+  if ((rc = check_plan_pool(plan, pool, layer, D))) return rc;
+  if ((int64_t)pool->num_pages * 2 * pool->num_kv_heads * pool->page_size > INT32_MAX)
+    return PG_ERR_I32_OVERFLOW;  // tensor-map row coordinates are int32
+  if (plan->num_tokens == 0) return PG_OK;
+  const pg_plan* own = plan->own.get();
+  SharedWs w;
+  if (!shared_ws(plan, std::max(workspace_bytes(own), bounded_ws_bytes(own)), &w) || !ws || ws_bytes < w.bytes)
+    return PG_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PG_ERR_ALIGN;
+  int err = PG_OK;
+  int* st = status_word(&err);
+  if (!st) return err;
+  unsigned char* const base = static_cast<unsigned char*>(ws);
+  const bool join = plan->num_parts > 0 || capturing(stream);
+  float* const row_lse = lse ? lse : reinterpret_cast<float*>(base + w.lse);
+  if (join) {
+    const AttnArgs a = part_args(plan, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q,
+                                 sm_scale, base, w, st);
+    if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
+  }
+  Bounded b;
+  rc = attn_common(own, pool, layer, D, q, out, row_lse, -1, sm_scale, base + w.own, ws_bytes - w.own, stream, &b);
+  if (rc != PG_OK || !join) return rc;
+  return shared_join(plan, out, row_lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
+// The 8-bit form: each prefix's pages are read back to the end of the workspace, behind a list of
+// their places.
+struct SharedQ8Ws {
+  SharedWs w;
+  size_t ids, pages, page_bytes;
+};
+bool shared_q8_ws(const pg_plan* p, SharedQ8Ws* x) {
+  const size_t own = q8_workspace_bytes(p->own.get());
+  if (own > ((size_t)1 << 60) || !shared_ws(p, align256(own), &x->w)) return false;
+  x->page_bytes = (size_t)4 * p->num_kv_heads * p->page_size * p->head_dim;
+  x->ids = x->w.bytes;
+  x->pages = align1k(x->ids + (size_t)p->num_page_ids * sizeof(int32_t));
+  const __int128 end = (__int128)x->page_bytes * std::max(p->prefix_pages, 1) + x->pages;
+  if (end > ((__int128)1 << 61)) return false;
+  x->w.bytes = (size_t)end;
+  return true;
+}
+size_t shared_q8_workspace_bytes(const pg_plan* p) {
+  if (!p || !p->own || p->num_req == 0) return 0;
+  SharedQ8Ws x;
+  return shared_q8_ws(p, &x) ? x.w.bytes : SIZE_MAX;
+}
+
+int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
+                   float* lse, float sm_scale, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  int rc = check_shared(plan, q, out, lse, sm_scale, stream);
+  if (rc) return rc;
+  if ((rc = check_plan_q8(plan, pool, layer, 1))) return rc;
+  const int32_t D = plan->head_dim, ps = plan->page_size, H = plan->num_kv_heads;
+  if (plan->num_tokens == 0) return PG_OK;
+  SharedQ8Ws x;
+  if (!shared_q8_ws(plan, &x) || !ws || ws_bytes < x.w.bytes) return PG_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PG_ERR_ALIGN;
+  unsigned char* const base = static_cast<unsigned char*>(ws);
+  // a captured call's prefixes may come to hold as many pages as the workspace has room for
+  const bool captured = capturing(stream);
+  const int64_t room = captured ? (int64_t)((ws_bytes - x.pages) / x.page_bytes) : std::max(plan->prefix_pages, 1);
+  const int32_t pages = (int32_t)std::min<int64_t>(room, plan->num_page_ids);
+  if ((int64_t)std::max(pages, plan->num_page_ids) * 2 * H * ps > INT32_MAX) return PG_ERR_I32_OVERFLOW;
+  int err = PG_OK;
+  int* st = status_word(&err);
+  if (!st) return err;
+  const bool join = plan->num_parts > 0 || captured;
+  float* const row_lse = lse ? lse : reinterpret_cast<float*>(base + x.w.lse);
+  if (join) {
+    DequantArgs d{};
+    d.plan = plan_dev(plan);
+    d.plan.page_ids = plan->dev + plan->o_pre_pages;
+    d.plan.num_page_ids = pages;
+    d.src = q8_dev(pool, layer);
+    d.dst = reinterpret_cast<__nv_bfloat16*>(base + x.pages);
+    d.num_pages = pool->num_pages;
+    d.page_size = ps;
+    d.num_kv_heads = H;
+    d.head_dim = D;
+    d.num_layers = 1;
+    d.list = 1;
+    d.whole = plan->dev + plan->o_part_live + 2;
+    d.window_left = -1;
+    d.ids = reinterpret_cast<int32_t*>(base + x.ids);
+    d.status = st;
+    if (launch_dequant(d, stream) != cudaSuccess) return PG_ERR_CUDA;
+    PoolDev copy = q8_geometry(pool);
+    copy.layer_base = d.dst;
+    copy.num_pages = pages;
+    const AttnArgs a = part_args(plan, copy, d.ids, pages, q, sm_scale, base, x.w, st);
+    if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
+  }
+  rc = q8_attn(plan->own.get(), pool, layer, q, out, row_lse, -1, 0, sm_scale, base + x.w.own, x.ids - x.w.own, stream);
+  if (rc != PG_OK || !join) return rc;
+  return shared_join(plan, out, row_lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+}
+
 // Builds *plan (null) or updates it. No exception leaves a C entry: memory that the host cannot give is
 // an argument that cannot be served, and nothing has changed by then.
 template <class... Args>
@@ -987,6 +1331,20 @@ int pg_plan_paged_segment(pg_plan_t* plan, int32_t num_req, const int64_t* qo_in
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return make_plan(plan, s, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
                    num_qo_heads, num_kv_heads, head_dim, page_size, s, -1, ks);
+}
+
+int pg_plan_paged_shared(pg_plan_t* plan, int32_t num_req, const int64_t* qo_indptr,
+                         const int64_t* kv_page_indptr, const int32_t* page_ids,
+                         const int32_t* last_page_len, const int64_t* start_pos, int32_t num_groups,
+                         const int64_t* group_indptr, const int64_t* prefix_len, int32_t num_qo_heads,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t page_size, pg_stream_t stream) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  Groups g;
+  g.num = num_groups;
+  g.indptr = group_indptr;
+  g.prefix = prefix_len;
+  return make_plan(plan, s, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
+                   num_qo_heads, num_kv_heads, head_dim, page_size, s, -1, nullptr, &g);
 }
 
 void pg_plan_destroy(pg_plan_t plan) {
@@ -1227,6 +1585,23 @@ int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t lay
                      size_t ws_bytes, pg_stream_t stream) {
   return q8_attn(plan, pool, layer, q, out, lse, window_left, num_sink, sm_scale, workspace, ws_bytes,
                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pg_shared_workspace_bytes(const pg_plan_t plan) { return shared_workspace_bytes(plan); }
+
+int pg_attn_paged_shared(const pg_plan_t plan, const pg_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
+                         float* lse, float sm_scale, void* workspace, size_t ws_bytes, pg_stream_t stream) {
+  return shared_attn(plan, pool, layer, q, out, lse, sm_scale, workspace, ws_bytes,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pg_shared_q8_workspace_bytes(const pg_plan_t plan) { return shared_q8_workspace_bytes(plan); }
+
+int pg_attn_paged_shared_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q,
+                            pg_bf16_t* out, float* lse, float sm_scale, void* workspace, size_t ws_bytes,
+                            pg_stream_t stream) {
+  return shared_q8_attn(plan, pool, layer, q, out, lse, sm_scale, workspace, ws_bytes,
+                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 int pg_kv_evict_select(const pg_plan_t plan, const pg_kv_stats_t* stats, int32_t layer,

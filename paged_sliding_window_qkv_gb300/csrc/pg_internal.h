@@ -122,6 +122,10 @@ struct AttnArgs {
   StatsDev stats;       // decode: accumulate the weights here (mass null: do not)
   int32_t max_keys;     // the most keys a request holds
   int32_t max_tiles;    // decode: tiles of 128 keys over all requests and KV heads
+  // parts of a shared prefix (see attn_tc.cu): records, and each pair-table entry's first record row
+  float* part_o = nullptr;
+  float* part_ml = nullptr;
+  const int32_t* part_row = nullptr;
   int* status;
   uint64_t wait_ns;       // limit of the kernels' bounded waits (nanoseconds)
   int32_t test_withhold;  // test hook of pg_test_bounded_wait (0: off)
@@ -158,8 +162,19 @@ struct DequantArgs {
   int32_t num_pages;         // pages of the 8-bit pool
   int32_t page_size, num_kv_heads, head_dim, num_layers;
   int32_t list, window_left, num_sink;
+  const int32_t* whole;      // list: not null: its first *whole pages, all their slots
   int32_t* ids;
   int* status;
+};
+
+// Join of a shared prefix's parts with the rows' own keys (see shared.cu).
+struct SharedJoinArgs {
+  const float* part_o;        // [part][num_tokens][Hq][D]
+  const float* part_ml;       // [part][num_tokens][Hq][2]
+  const int32_t* tok_parts;   // [num_tokens] parts of the token's prefix
+  __nv_bfloat16* out;         // [num_tokens][Hq][D]: of the own keys, then of all
+  float* lse;                 // [num_tokens][Hq]: the same
+  int32_t num_tokens, num_qo_heads;
 };
 
 // Bounded-wait settings for the next launches: the default limit, or the test hook's.
@@ -189,6 +204,9 @@ int32_t attn_kernel_cta_tile_q(int32_t head_dim, int32_t group, int32_t page_siz
 bool attn_tc_supported(int32_t head_dim, int32_t group, int32_t page_size);
 int32_t attn_tc_rows();
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
+// Parts of a shared prefix: the pair table's entries are (pair of query tiles, run of keys).
+cudaError_t launch_attn_parts(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
+cudaError_t launch_shared_join(const SharedJoinArgs& a, int32_t head_dim, cudaStream_t stream);
 // Keys per split-KV chunk of the decode kernel.
 int32_t attn_kernel_kv_chunk(int32_t head_dim);
 cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);

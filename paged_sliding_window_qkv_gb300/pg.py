@@ -462,7 +462,61 @@ def pg_attn_paged_q8(plan, pool: pg_q8_pool_t, layer, q, out, lse, window_left, 
                     int(ws_bytes), _stream(stream))
 
 
-EXPORTED = ["pg_prep_paged_q8", "pg_kv_dequantize", "pg_q8_workspace_bytes", "pg_attn_paged_q8",
+# ------------------------------------------------------------------------------ shared prefixes
+_plan_shared = _sig("pg_plan_paged_shared", C.c_int, C.POINTER(_P), _I32, _P, _P, _P, _P, _P, _I32, _P, _P,
+                    _I32, _I32, _I32, _I32, _P)
+_shared_wsb = _sig("pg_shared_workspace_bytes", _SZ, _P)
+_shared_q8_wsb = _sig("pg_shared_q8_workspace_bytes", _SZ, _P)
+_attn_shared = _sig("pg_attn_paged_shared", C.c_int, _P, C.POINTER(pg_pool_t), _I32, _P, _P, _P, _F32, _P,
+                    _SZ, _P)
+_attn_shared_q8 = _sig("pg_attn_paged_shared_q8", C.c_int, _P, C.POINTER(pg_q8_pool_t), _I32, _P, _P, _P,
+                       _F32, _P, _SZ, _P)
+
+
+def pg_plan_paged_shared(plan, num_req, qo_indptr, kv_page_indptr, page_ids, last_page_len, start_pos,
+                         num_groups, group_indptr, prefix_len, num_qo_heads, num_kv_heads, head_dim,
+                         page_size, stream=None):
+    """Build (plan=None) or update (plan=Plan) a plan whose groups of requests share prefixes.
+    Returns (status, Plan or None)."""
+    h = _P(plan.handle if plan is not None else None)
+    keep = [_host(qo_indptr, np.int64), _host(kv_page_indptr, np.int64),
+            _host(page_ids, np.int32), _host(last_page_len, np.int32), _host(start_pos, np.int64)]
+    more = [_host(group_indptr, np.int64), _host(prefix_len, np.int64)]
+    rc = _plan_shared(C.byref(h), int(num_req), *[k[1] for k in keep], int(num_groups),
+                      *[k[1] for k in more], int(num_qo_heads), int(num_kv_heads), int(head_dim),
+                      int(page_size), _stream(stream))
+    del keep, more
+    if plan is not None:
+        return rc, plan
+    return rc, (Plan(h.value) if rc == PG_OK else None)
+
+
+def pg_shared_workspace_bytes(plan) -> int:
+    return int(_shared_wsb(plan.handle if plan is not None else None))
+
+
+def pg_shared_q8_workspace_bytes(plan) -> int:
+    return int(_shared_q8_wsb(plan.handle if plan is not None else None))
+
+
+def pg_attn_paged_shared(plan, pool: pg_pool_t, layer, q, out, lse, sm_scale, workspace=None, ws_bytes=0,
+                         stream=None) -> int:
+    """Full causal attention that reads each group's prefix once."""
+    return _attn_shared(plan.handle if plan is not None else None,
+                        C.byref(pool) if pool is not None else None, int(layer), _ptr(q), _ptr(out),
+                        _ptr(lse), float(sm_scale), _ptr(workspace), int(ws_bytes), _stream(stream))
+
+
+def pg_attn_paged_shared_q8(plan, pool: pg_q8_pool_t, layer, q, out, lse, sm_scale, workspace=None,
+                            ws_bytes=0, stream=None) -> int:
+    """pg_attn_paged_shared over an 8-bit pool."""
+    return _attn_shared_q8(plan.handle if plan is not None else None, _q8(pool), int(layer), _ptr(q),
+                           _ptr(out), _ptr(lse), float(sm_scale), _ptr(workspace), int(ws_bytes),
+                           _stream(stream))
+
+
+EXPORTED = ["pg_plan_paged_shared", "pg_shared_workspace_bytes", "pg_shared_q8_workspace_bytes",
+            "pg_attn_paged_shared", "pg_attn_paged_shared_q8", "pg_prep_paged_q8", "pg_kv_dequantize", "pg_q8_workspace_bytes", "pg_attn_paged_q8",
             "pg_attn_paged_sink", "pg_sink_workspace_bytes", "pg_mass_workspace_bytes", "pg_attn_paged_mass",
             "pg_kv_evict_select", "pg_kv_evict_apply", "pg_plan_paged_prefill", "pg_plan_paged_prefill_ring", "pg_plan_paged_segment",
             "pg_attn_paged_prefill_lse", "pg_attn_paged_prefill_hd512_lse", "pg_merge_attn_states",

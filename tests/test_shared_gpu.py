@@ -1,0 +1,285 @@
+"""Attention for batches that share prefixes, on bf16 and 8-bit pools (GPU), against the plain 64-bit
+reference of bounded_ref.py, request by request over all its keys.
+
+Tolerance: bounded_ref's, with one more rounding: the part of a row's own keys is rounded to bf16
+before the join, by at most half a step, 2^-8 of it, so 2^-8 * A more (A = sum_j w_j |v_j|)."""
+import numpy as np
+import pytest
+import torch
+
+from bounded_ref import Case
+from paged_sliding_window_qkv_gb300 import pg
+from q8_ref import Q8Case
+
+pytestmark = pytest.mark.gpu
+
+HEADS = {256: [(16, 8), (8, 8), (16, 1), (8, 2)], 512: [(16, 1), (8, 1), (4, 2), (2, 2)]}
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert pg.pg_device_status() == pg.PG_OK
+
+
+def shared(base):
+    class Shared(base):
+        """groups: (requests, prefix pages) in order; own: keys of each request before the step."""
+
+        def __init__(self, D, hq, hkv, qo, own, groups, ps=16, seed=0, **kw):
+            self.group_indptr = np.concatenate([[0], np.cumsum([g for g, _ in groups])])
+            self.prefix = np.asarray([p * ps for _, p in groups], np.int64)
+            of = np.repeat(np.arange(len(groups)), [g for g, _ in groups])
+            super().__init__(D, hq, hkv, qo, np.asarray(own) + self.prefix[of], ps=ps, seed=seed, **kw)
+            for r in range(len(self.qo)):
+                k, first = int(self.prefix[of[r]]) // ps, int(self.group_indptr[of[r]])
+                a, b = int(self.pg_indptr[r]), int(self.pg_indptr[first])
+                self.ids[a:a + k] = self.ids[b:b + k]
+
+        def replan(self, plan=None, **kw):
+            a = dict(num_req=len(self.qo), qo_indptr=self.qo_indptr, kv_page_indptr=self.pg_indptr,
+                     page_ids=self.ids, last_page_len=self.last, start_pos=self.start,
+                     num_groups=len(self.prefix), group_indptr=self.group_indptr, prefix_len=self.prefix,
+                     num_qo_heads=self.hq, num_kv_heads=self.hkv, head_dim=self.D, page_size=self.ps) | kw
+            return pg.pg_plan_paged_shared(plan, stream=self.stream, **a)
+
+        def build(self):
+            rc, self.plan = self.replan()
+            pg.check(rc, "shared plan")
+            self.upload()
+            return self
+
+        def upload(self):
+            super().upload()
+            q8 = isinstance(self, Q8Case)
+            self.ws_bytes = (pg.pg_shared_q8_workspace_bytes if q8 else pg.pg_shared_workspace_bytes)(self.plan)
+            self.ws = torch.full((self.ws_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+
+        def attend(self, scale=1.0, lse=True):
+            f, pool = (pg.pg_attn_paged_shared_q8, self.q8) if isinstance(self, Q8Case) else \
+                (pg.pg_attn_paged_shared, self.desc)
+            pg.check(f(self.plan, pool, self.layer, self.q, self.out, self.lse if lse else None, scale,
+                       self.ws, self.ws_bytes, self.stream), "shared")
+
+        def check(self, what="", scale=1.0):
+            out, lse, m, p, wabs = self.reference(-1, 0, scale)
+            self.ref = (out, lse, m, p, 2 * wabs)
+            self.check_attention(what)
+
+    return Shared
+
+
+Bf16, Q8 = shared(Case), shared(Q8Case)
+KINDS = [Bf16, Q8]
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("qo,own,groups", [
+    ([1] * 6, [0, 3, 15, 16, 100, 333], [(6, 40)]),
+    ([1] * 7, [5, 0, 0, 64, 1, 300, 17], [(1, 9), (3, 1), (2, 33), (1, 0)]),
+    ([1], [0], [(1, 1)]),
+    ([1] * 40, list(range(40)), [(20, 13), (20, 70)]),
+    ([5, 130, 1, 64], [0, 7, 200, 0], [(3, 25), (1, 4)]),
+    ([300, 2, 17], [0, 0, 40], [(3, 64)]),
+    ([3, 1], [9, 0], [(1, 0), (1, 0)]),
+])
+def test_shared_prefixes(kind, D, qo, own, groups):
+    hq, hkv = HEADS[D][0]
+    c = kind(D, hq, hkv, qo, own, groups, seed=len(qo)).build()
+    c.attend()
+    ok()
+    c.check()
+    c.close()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("D,hq,hkv", [(d, *h) for d in (256, 512) for h in HEADS[d]])
+def test_head_groups_and_layers(kind, D, hq, hkv):
+    for qo in ([1, 1, 1], [20, 3, 70]):
+        c = kind(D, hq, hkv, qo, [10, 0, 99], [(2, 21), (1, 3)], seed=hq + hkv, layers=2, layer=1).build()
+        c.attend()
+        ok()
+        c.check(f"{qo}")
+        c.close()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("ps", [8, 32, 128])
+def test_page_sizes(kind, D, ps):
+    hq, hkv = HEADS[D][0]
+    for qo in ([1, 1, 1], [33, 1, 80]):
+        c = kind(D, hq, hkv, qo, [10, 0, 77], [(3, 5)], ps=ps, seed=ps).build()
+        c.attend()
+        ok()
+        c.check(f"{qo}")
+        c.close()
+
+
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("scale", [0.0, -1.0, 0.25])
+def test_scales_and_no_lse(D, scale):
+    hq, hkv = HEADS[D][0]
+    for qo in ([1, 1], [90, 4]):
+        c = Bf16(D, hq, hkv, qo, [30, 2], [(2, 30)], seed=3).build()
+        c.attend(scale)
+        ok()
+        c.check(scale=scale)
+        first = c.out.clone()
+        c.out.fill_(float("nan"))
+        c.attend(scale, lse=False)
+        ok()
+        assert torch.equal(c.out, first)  # the parts and their order are fixed
+        c.close()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+def test_a_long_prefix_is_cut_into_many_parts(kind):
+    for D in (256, 512):
+        hq, hkv = HEADS[D][0]
+        c = kind(D, hq, hkv, [1, 1], [3, 40], [(2, 500)], seed=6).build()
+        c.attend()
+        ok()
+        c.check()
+        c.close()
+
+
+@pytest.mark.parametrize("D", [256, 512])
+def test_a_prefix_that_outweighs_the_own_keys_and_the_other_way(D):
+    """Scores of the two parts far apart: one part's weights underflow beside the other's."""
+    hq, hkv = HEADS[D][0]
+    for sign in (1.0, -1.0):
+        c = Bf16(D, hq, hkv, [1, 1, 30], [60, 20, 50], [(3, 12)], seed=9)
+        pre = c.ids[:12].astype(int)
+        c.q_cpu[:] = torch.abs(c.q_cpu)
+        c.pool_cpu[0, pre, 0] = torch.abs(c.pool_cpu[0, pre, 0]) * sign * 4
+        c.build()
+        c.attend()
+        ok()
+        c.check(f"{sign}")
+        c.close()
+
+
+@pytest.mark.parametrize("D", [256, 512])
+def test_the_plan_serves_the_other_entries(D):
+    """A shared plan is its plain plan everywhere else: attention of both entries agrees, and prep
+    writes the rows that the plain plan's writes."""
+    hq, hkv = HEADS[D][0]
+    c = Bf16(D, hq, hkv, [1, 1, 1], [10, 0, 99], [(2, 21), (1, 3)], seed=5).build()
+    ws = torch.empty(max(16, pg.pg_sink_workspace_bytes(c.plan)), dtype=torch.uint8, device="cuda")
+    pg.check(pg.pg_attn_paged_sink(c.plan, c.desc, 0, c.q, c.out, c.lse, -1, 0, 1.0, ws, ws.numel()))
+    ok()
+    c.check("sink entry")
+    c.close()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("D", [256, 512])
+def test_captured_call_follows_its_plan(kind, decode, D):
+    """Replayed after an update to as many groups, requests, tokens and pages, spread otherwise."""
+    hq, hkv = HEADS[D][0]
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        qo = [1, 1, 1, 1] if decode else [40, 1, 9, 2]
+        a = kind(D, hq, hkv, qo, [0, 15, 40, 8], [(2, 30), (2, 2)], seed=1, stream=stream).build()
+        extra = 64 * 4 * hkv * 16 * D  # room for more pages in prefixes
+        a.ws_bytes += extra
+        a.ws = torch.full((a.ws_bytes,), 0xFF, dtype=torch.uint8, device="cuda")
+        a.attend()
+        stream.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            a.attend()
+        total = len(a.ids)
+        for groups, seed in (([(1, 3), (3, 14)], 2), ([(3, 0), (1, 40)], 3), ([(2, 0), (2, 0)], 4)):
+            own = [0, 15, 40, 8]
+            need = sum(r * p for r, p in groups)
+            qb = qo if decode else [2, 9, 1, 40]
+            left = total - need - sum(-(-(o + q) // 16) for o, q in zip(own, qb))
+            own[0] += 16 * left
+            b = kind(D, hq, hkv, qb, own, groups, seed=seed, stream=stream)
+            assert left >= 0 and len(b.ids) == total and b.P == a.P, (left, len(b.ids), total)
+            rc, _ = b.replan(a.plan)
+            pg.check(rc)
+            a.q.copy_(b.q_cpu)
+            if kind is Q8:
+                a.codes.copy_(b.codes_cpu)
+                a.scales.copy_(b.scales_cpu)
+            else:
+                a.pool.copy_(b.pool_cpu)
+            a.out.fill_(float("nan"))
+            a.ws.fill_(0xFF)
+            g.replay()
+            stream.synchronize()
+            assert pg.pg_device_status(stream) == pg.PG_OK
+            b.out, b.lse = a.out, a.lse
+            b.check(f"{groups}")
+    a.close()
+
+
+def test_plans_change_kind_in_place():
+    c = Bf16(512, 16, 1, [1, 1], [10, 20], [(2, 4)], seed=2).build()
+    rc, _ = pg.pg_plan_paged_prefill(c.plan, 2, c.qo_indptr, c.pg_indptr, c.ids, c.last, c.start, 16, 1, 512, 16)
+    pg.check(rc)
+    assert pg.pg_shared_workspace_bytes(c.plan) == 0
+    assert pg.pg_attn_paged_shared(c.plan, c.desc, 0, c.q, c.out, None, 1.0, c.ws, c.ws_bytes) == \
+        pg.PG_ERR_PLAN_MISMATCH
+    rc, _ = c.replan(c.plan)
+    pg.check(rc)
+    c.attend()
+    ok()
+    c.check()
+    c.close()
+
+
+def test_a_refused_update_leaves_the_plan_as_it_was():
+    c = Bf16(256, 16, 8, [1, 1, 1], [10, 20, 0], [(2, 4), (1, 2)], seed=2).build()
+    rc, _ = c.replan(c.plan, prefix_len=[64, 40])
+    assert rc == pg.PG_ERR_COVERAGE
+    c.attend()
+    ok()
+    c.check()
+    c.close()
+
+
+def test_refusals_launch_nothing():
+    for c in (Bf16(512, 16, 1, [1, 1], [10, 20], [(2, 4)], seed=2).build(),
+              Q8(512, 16, 1, [1, 1], [10, 20], [(2, 4)], seed=2).build()):
+        torch.cuda.synchronize()
+        before = pg.pg_launch_count()
+        q8 = isinstance(c, Q8Case)
+        f, pool = (pg.pg_attn_paged_shared_q8, c.q8) if q8 else (pg.pg_attn_paged_shared, c.desc)
+
+        def call(want, plan=c.plan, pool=pool, layer=0, q=c.q, out=c.out, lse=c.lse, scale=1.0, ws=c.ws,
+                 n=c.ws_bytes, stream=None):
+            assert f(plan, pool, layer, q, out, lse, scale, ws, n, stream) == want
+
+        call(pg.PG_ERR_ARG, plan=None)
+        call(pg.PG_ERR_ARG, pool=None)
+        call(pg.PG_ERR_ARG, q=None)
+        call(pg.PG_ERR_ARG, out=None)
+        call(pg.PG_ERR_LAYER, layer=3)
+        call(pg.PG_ERR_NONFINITE, scale=float("inf"))
+        call(pg.PG_ERR_WORKSPACE, ws=None)
+        call(pg.PG_ERR_WORKSPACE, n=c.ws_bytes - 1)
+        call(pg.PG_ERR_ALIGN, ws=c.ws.data_ptr() + 8)
+        call(pg.PG_ERR_ALIGN, out=c.out.data_ptr() + 16)
+        call(pg.PG_ERR_ALIGN, lse=c.lse.data_ptr() + 1)
+        call(pg.PG_ERR_STREAM, stream=torch.cuda.Stream())
+        assert pg.pg_launch_count() == before
+        assert torch.isnan(c.out).all()
+        ok()
+        c.close()
+
+
+def test_empty_batch():
+    rc, plan = pg.pg_plan_paged_shared(None, 0, [0], [0], [], [], [], 0, [0], [], 16, 1, 512, 16)
+    pg.check(rc)
+    c = Bf16(512, 16, 1, [1], [0], [(1, 0)]).build()
+    before = pg.pg_launch_count()
+    assert pg.pg_shared_workspace_bytes(plan) == 0
+    pg.check(pg.pg_attn_paged_shared(plan, c.desc, 0, None, None, None, 1.0))
+    assert pg.pg_launch_count() == before
+    plan.close()
+    c.close()
