@@ -18,7 +18,7 @@ OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpg.so")
 SOURCES = ["pg_host.cpp", "pg_kv.cpp", "prep.cu", "attn_split.cu", "attn_decode.cu", "attn_tc.cu",
            "attn_bounded_decode.cu", "attn_mass.cu", "attn_mass_tc.cu", "evict.cu", "cascade.cu",
-           "dequant.cu", "shared.cu"]
+           "attn_q8_decode.cu", "dequant.cu", "shared.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

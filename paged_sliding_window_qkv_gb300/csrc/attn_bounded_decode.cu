@@ -37,10 +37,8 @@
 //
 // Every wait is bounded (a wait that runs out sets the device status word and the CTA leaves); the
 // softmax warps agree on giving up before any barrier among themselves.
-#include "bounded.cuh"
+#include "bounded_decode.cuh"
 #include "mass.cuh"
-#include "pg_internal.h"
-#include "tc_ptx.cuh"
 
 #include <math.h>
 
@@ -49,16 +47,8 @@
 namespace pg {
 namespace {
 
-constexpr int kT = 128;               // keys per tile
 constexpr int kN = 16;                // MMA columns: query rows of the group, padded
 constexpr int kThreadsDec = 224;
-constexpr int kMaxCtas = 256;         // records are sized for at most this many CTAs
-constexpr int kHdrs = 4;
-constexpr float kRescale = 48.f, kHeadroom = 64.f;  // see attn_tc.cu
-constexpr float kLn2f = 0.69314718055994531f, kLog2ef = 1.4426950408889634f;
-
-constexpr int kFirst = 1, kLast = 2, kSplit = 4, kEnd = 8, kEmpty = 16, kRec1 = 32;
-
 struct alignas(16) TileHdr {
   uint32_t vis[4];  // visible keys
   int32_t rel[16];  // key index (from the request's first key) of each box's first row
@@ -91,31 +81,6 @@ struct BdCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-struct BdArgs {
-  AttnArgs a;
-  float* rec_o;     // [S][2][G][D]
-  float* rec_ml;    // [S][2][G][2]
-  int64_t* prefix;  // [R + 1] tiles before request r (all heads)
-  int32_t box_rows;
-  int32_t box_lg, page_lg;  // log2 of box_rows and of the page size (both powers of two)
-};
-
-// ------------------------------------------------------------------ PTX (one CTA)
-// K and V are read once a step: their lines leave L2 first, so that scores and records stay for the join
-// (64 requests of 8001 keys at head_dim 512: 176 -> 170 us, with weights 202 -> 197; 16: 63 -> 57).
-__device__ __forceinline__ uint64_t evict_first() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* tm, int c2, int c3, uint32_t bar,
-                                       uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(tm), "r"(0), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
-      : "memory");
-}
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -131,69 +96,6 @@ __device__ __forceinline__ void mma1(uint32_t d, uint64_t a, uint64_t b, uint32_
       "l"(a), "l"(b), "r"(acc), "n"(IDESC)
       : "memory");
 }
-__device__ __forceinline__ void commit1(uint32_t bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n .reg .u32 ln;\n mov.u32 ln, %%laneid;\n setp.eq.u32 e, ln, 0;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : PG_R8(0), PG_R8(8)
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      PG_W8(0), PG_W8(8)
-      : "memory");
-}
-// barriers among the 128 softmax threads
-__device__ __forceinline__ bool any4(bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void sync4() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-// maximum over the warp
-__device__ __forceinline__ float warp_max(float x) {
-  const int32_t b = __float_as_int(x);
-  const int32_t m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7FFFFFFF));
-  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
-}
-
-// The boxes of request r that its query sees, and the tiles they fill (one KV head).
-struct ReqTiles {
-  KeyWalk w;      // in boxes
-  int32_t total;  // tiles
-  int32_t tok, kvp0, kvp1, kv_len, ks0, sink;
-  __device__ __forceinline__ bool sees(int32_t key) const {
-    return key < w.hi && (key >= w.lo || key < sink);
-  }
-};
-__device__ __forceinline__ ReqTiles req_tiles(const BdArgs& args, int32_t r) {
-  const AttnArgs& a = args.a;
-  const int4 e0 = __ldg(reinterpret_cast<const int4*>(a.plan.pair_tab) + 2 * r);
-  const int4 e1 = __ldg(reinterpret_cast<const int4*>(a.plan.pair_tab) + 2 * r + 1);
-  ReqTiles t;
-  t.tok = e0.y;
-  t.kvp0 = e1.x;
-  t.kvp1 = e1.y;
-  t.kv_len = e1.z;
-  t.ks0 = e1.w;
-  t.sink = a.window_left >= 0 ? a.num_sink : 0;
-  t.w = key_walk(a.window_left, a.num_sink, t.ks0, t.kv_len, e0.w, e0.w, args.box_rows);
-  const int32_t nbox = kT >> args.box_lg;
-  t.total = (t.w.total + nbox - 1) / nbox;
-  return t;
-}
-
 template <int D, int NQ>
 __global__ void __launch_bounds__(kThreadsDec, 1)
 bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -251,60 +153,13 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   // programmatic launch overtakes. Everything else waits for that kernel.
   int32_t n = 0, r = 0;
   int64_t in_req = 0;
-  constexpr int kHeld = 4;
   int64_t held[kHeld] = {0, 0, 0, 0};  // inclusive sums of the first requests' tiles
   if (warp == 0 || warp == 6) {
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_kv) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_q) : "memory");
     }
-    const int32_t R = a.plan.num_req;
-    const int64_t S = gridDim.x, s = blockIdx.x;
-    // Tiles of every request (all heads) in scans of 32 requests: the total, and the request that
-    // holds the CTA's first tile. The first scans' counts are loaded together and kept.
-    auto tiles_of = [&](int32_t r) -> int64_t { return r < R ? (int64_t)req_tiles(args, r).total * Hkv : 0; };
-    auto scan = [&](int64_t v) {
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-      }
-      return v;
-    };
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) held[j] = tiles_of(32 * j + lane);
-    int64_t U = 0;
-    for (int32_t c = 0; c < R; c += 32) {
-      const int j = c / 32;
-      const int64_t v = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : j == 3 ? held[3] : tiles_of(c + lane);
-      const int64_t incl = U + scan(v);
-#pragma unroll
-      for (int k = 0; k < kHeld; ++k)
-        if (k == j) held[k] = incl;
-      U = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    const int64_t u0 = s * U / S, u1 = (s + 1) * U / S;
-    n = (int32_t)(u1 - u0);
-    if (n > 0) {
-      int64_t run = 0;  // tiles before request c
-      for (int32_t c = 0; c < R; c += 32) {
-        const int j = c / 32;
-        const int64_t incl = j == 0   ? held[0]
-                             : j == 1 ? held[1]
-                             : j == 2 ? held[2]
-                             : j == 3 ? held[3]
-                                      : run + scan(tiles_of(c + lane));
-        const uint32_t past = __ballot_sync(0xffffffffu, incl > u0);
-        if (past) {
-          const int f = __ffs(past) - 1;
-          r = c + f;
-          const int64_t before = __shfl_up_sync(0xffffffffu, incl, 1);
-          in_req = u0 - __shfl_sync(0xffffffffu, lane == 0 ? run : before, f);
-          break;
-        }
-        run = __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
+    n = find_tiles(args, lane, held, &r, &in_req);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
@@ -325,27 +180,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     // the prefix for the join (CTA 0), once the stream's previous kernel, which may read the last one
     // in the same workspace, has ended
     auto write_prefix = [&]() {
-      if (blockIdx.x != 0 || is_v) return;
-      const int32_t R = a.plan.num_req;
-      int64_t run = 0;
-      for (int32_t c = 0; c < R; c += 32) {
-        const int j = c / 32;
-        int64_t incl;
-        if (j < kHeld) {
-          incl = j == 0 ? held[0] : j == 1 ? held[1] : j == 2 ? held[2] : held[3];
-        } else {
-          incl = c + lane < R ? (int64_t)req_tiles(args, c + lane).total * Hkv : 0;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-          }
-          incl += run;
-        }
-        if (c + lane < R) args.prefix[c + lane + 1] = incl;
-        run = __shfl_sync(0xffffffffu, incl, 31);
-      }
-      if (lane == 0) args.prefix[0] = 0;
+      if (blockIdx.x == 0 && !is_v) write_tile_prefix(args, lane, held);
     };
     bool ok = true;
     if (n == 0) {
@@ -358,52 +193,8 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     } else {
       const int br = args.box_rows, nbox = kT / br;
       const uint64_t policy = evict_first();
-      // the tile that the iterator stands on
-      ReqTiles q = req_tiles(args, r);
-      int32_t g = (int32_t)(in_req / q.total), j = (int32_t)(in_req % q.total);
-      int32_t nseg = 0;
-      struct Tile {
-        int32_t flags, r, g;
-        int32_t rel, page, off;  // this lane's box: key index of its first row, page, row in the page
-        bool live;               // the lane has a box
-        ReqTiles q;
-      };
-      // describes tile i and steps on; the lane's page id is loaded here and used a tile later
-      int32_t seg_split = 0;
-      auto next = [&](int32_t i) {
-        Tile t;
-        if (i == 0 || j == 0) {
-          const int32_t rest = q.total - j;
-          seg_split = (j != 0 || rest > n - i) ? kSplit : 0;
-          seg_split |= nseg > 0 ? kRec1 : 0;
-          ++nseg;
-          t.flags = kFirst;
-        } else {
-          t.flags = 0;
-        }
-        t.flags |= seg_split | (j == q.total - 1 || i == n - 1 ? kLast : 0) | (i == n - 1 ? kEnd : 0);
-        t.r = r;
-        t.g = g;
-        t.q = q;
-        const int32_t v = j * nbox + lane;
-        t.live = lane < nbox && v < q.w.total;
-        t.rel = t.live ? q.w.tile(v) << args.box_lg : 0;
-        t.page = -1;
-        t.off = t.rel & (ps - 1);
-        if (t.live) {
-          const int32_t pidx = q.kvp0 + (t.rel >> args.page_lg);
-          t.page = (pidx < q.kvp1 && pidx < a.plan.num_page_ids) ? a.plan.page_ids[pidx] : -1;
-        }
-        if (++j == q.total && i + 1 < n) {
-          j = 0;
-          if (++g == Hkv) {
-            g = 0;
-            do q = req_tiles(args, ++r);
-            while (q.total == 0);
-          }
-        }
-        return t;
-      };
+      TileWalk walk(args, lane, n, r, in_req);
+      auto next = [&](int32_t i) { return walk.next(i); };
       // PARTS slots of K or V, from the at-th of the CTA's stream of slots (K0 K1 V0 K2 V1 ...)
       auto load = [&](const Tile& t, bool good, int32_t at) {
         const uint32_t boxes = __ballot_sync(0xffffffffu, good);
@@ -1043,6 +834,34 @@ int32_t record_room(const AttnArgs& a, int32_t D) {
   return (int32_t)std::min<size_t>(std::max<size_t>(room, 1), kMaxCtas);
 }
 
+template <int D>
+cudaError_t launch_join(const BdArgs& b, int32_t S, cudaStream_t stream) {
+  const AttnArgs& a = b.a;
+  const int32_t Hkv = a.pool.num_kv_heads, G = a.group;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool weigh = a.stats.mass != nullptr;
+  const int32_t key_blocks = weigh ? (a.max_keys + kJoinKeys - 1) / kJoinKeys : 0;
+  const int32_t segs = a.plan.num_req * Hkv;
+  auto join = [&](auto kernel, int32_t RG) {
+    const unsigned grid =
+        (unsigned)((int64_t)segs * join_parts(G, D, RG) + (int64_t)a.plan.num_req * key_blocks);
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.dynamicSmemBytes = weigh ? a.num_qo_heads * sizeof(float) : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, b, S, std::max(key_blocks, 1));
+  };
+  const cudaError_t e = segs * 4 < S ? join(bounded_join_kernel<D, 4>, 4) : join(bounded_join_kernel<D, 1>, 1);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
 template <int D, int NQ>
 cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   using C = BdCfg<D>;
@@ -1090,10 +909,7 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   b.box_rows = br;
   b.box_lg = 31 - __builtin_clz((unsigned)br);
   b.page_lg = 31 - __builtin_clz((unsigned)ps);
-  unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws_raw);
-  b.prefix = reinterpret_cast<int64_t*>(ws);
-  b.rec_ml = reinterpret_cast<float*>(ws + al16((size_t)(a.plan.num_req + 1) * 8));
-  b.rec_o = b.rec_ml + (size_t)S * 2 * G * 2;
+  bounded_records(a, S, &b);
   // programmatic serialisation: the CTAs' set-up overlaps the end of the stream's previous kernel
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, 1, 1);
@@ -1108,24 +924,21 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   e = cudaLaunchKernelEx(&cfg, bounded_decode_kernel<D, NQ>, tq, tkv, b);
   if (e != cudaSuccess) return e;
   count_launch();
-  const bool weigh = a.stats.mass != nullptr;
-  const int32_t key_blocks = weigh ? (a.max_keys + kJoinKeys - 1) / kJoinKeys : 0;
-  const int32_t segs = a.plan.num_req * Hkv;
-  auto join = [&](auto kernel, int32_t RG) {
-    const unsigned grid =
-        (unsigned)((int64_t)segs * join_parts(G, D, RG) + (int64_t)a.plan.num_req * key_blocks);
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
-    cfg.dynamicSmemBytes = weigh ? a.num_qo_heads * sizeof(float) : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, b, S, std::max(key_blocks, 1));
-  };
-  e = segs * 4 < S ? join(bounded_join_kernel<D, 4>, 4) : join(bounded_join_kernel<D, 1>, 1);
-  if (e != cudaSuccess) return e;
-  count_launch();
-  return cudaGetLastError();
+  return launch_join<D>(b, S, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_bounded_join(const BdArgs& b, int32_t S, int32_t head_dim, cudaStream_t stream) {
+  return head_dim == 256 ? launch_join<256>(b, S, stream) : launch_join<512>(b, S, stream);
+}
+int32_t bounded_record_room(const AttnArgs& a, int32_t head_dim) { return record_room(a, head_dim); }
+void bounded_records(const AttnArgs& a, int32_t S, BdArgs* b) {
+  unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws_raw);
+  b->prefix = reinterpret_cast<int64_t*>(ws);
+  b->rec_ml = reinterpret_cast<float*>(ws + al16((size_t)(a.plan.num_req + 1) * 8));
+  b->rec_o = b->rec_ml + (size_t)S * 2 * a.group * 2;
+}
 
 bool bounded_decode_supported(int32_t head_dim, int32_t group, int32_t page_size) {
   return (head_dim == 256 || head_dim == 512) && group >= 1 && group <= kN && page_size >= 8 &&

@@ -1027,8 +1027,13 @@ bool read_back(const pg_plan* p, ReadBack* w) {
   w->bytes = w->rest + std::max(workspace_bytes(p), bounded_ws_bytes(p));
   return true;
 }
+bool q8_direct(const pg_plan* p) {
+  return p->decode && q8_decode_supported(p->head_dim, p->num_qo_heads / p->num_kv_heads, p->page_size);
+}
 size_t q8_workspace_bytes(const pg_plan* p) {
   if (!p || p->num_req == 0 || (p->head_dim != 256 && p->head_dim != 512)) return 0;
+  if (q8_direct(p))
+    return bounded_decode_ws_bytes(p->num_req, p->num_qo_heads / p->num_kv_heads, p->head_dim, plan_max_tiles(p));
   ReadBack w;
   return read_back(p, &w) ? w.bytes : SIZE_MAX;
 }
@@ -1042,10 +1047,35 @@ int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const 
   const int32_t D = plan->head_dim;
   // what the bf16 call would refuse is refused before the read-back is launched
   if ((rc = check_attn_args(plan, D, window_left, sm_scale))) return rc;
-  if ((int64_t)plan->num_page_ids * 2 * plan->num_kv_heads * plan->page_size > INT32_MAX)
+  const bool direct = q8_direct(plan);
+  if ((int64_t)(direct ? pool->num_pages : plan->num_page_ids) * 2 * plan->num_kv_heads * plan->page_size > INT32_MAX)
     return PG_ERR_I32_OVERFLOW;  // tensor-map row coordinates are int32
   if (plan->num_tokens == 0) return PG_OK;
   if ((rc = check_attn_rows(q, out, lse))) return rc;
+  if (direct) {
+    if (!ws || ws_bytes < q8_workspace_bytes(plan)) return PG_ERR_WORKSPACE;
+    if (!aligned16(ws)) return PG_ERR_ALIGN;
+    int err = PG_OK;
+    AttnArgs a{};
+    if (!(a.status = status_word(&err))) return err;
+    a.plan = plan_dev(plan);
+    a.pool = q8_geometry(pool);
+    a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+    a.out = reinterpret_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.ws_raw = ws;
+    a.ws_bytes = ws_bytes;
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.window_left = window_left;
+    a.num_sink = num_sink;
+    a.num_qo_heads = plan->num_qo_heads;
+    a.group = plan->num_qo_heads / plan->num_kv_heads;
+    a.bounded = 1;
+    a.max_keys = plan->max_seen;
+    a.max_tiles = plan_max_tiles(plan);
+    wait_settings(&a.wait_ns, &a.test_withhold);
+    return launch_q8_decode(a, q8_dev(pool, layer), D, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+  }
   ReadBack w;
   if (!read_back(plan, &w) || !ws || ws_bytes < w.bytes) return PG_ERR_WORKSPACE;
   if (!aligned16(ws)) return PG_ERR_ALIGN;
