@@ -595,7 +595,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
 // ------------------------------------------------------------------ join
 // Where the records of a segment are: CTAs sa .. sb, the record slot of sa. (64-bit divisions only
-// where the products need them: S is at most 256.)
+// where the products need them: S is at most 320.)
 struct SegRecs {
   int32_t sa, sb, slot_a;
   bool sparse;  // fewer tiles than CTAs: some of the CTAs hold none
@@ -828,10 +828,10 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
 size_t al16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // CTAs whose records the workspace holds (one that runs alone cuts no segment and leaves none).
-int32_t record_room(const AttnArgs& a, int32_t D) {
+int32_t record_room(const AttnArgs& a, int32_t D, int32_t most = kMaxCtas) {
   const size_t prefix = al16((size_t)(a.plan.num_req + 1) * 8), cta = (size_t)2 * a.group * (D + 2) * sizeof(float);
   const size_t room = a.ws_bytes > prefix ? (a.ws_bytes - prefix) / cta : 0;
-  return (int32_t)std::min<size_t>(std::max<size_t>(room, 1), kMaxCtas);
+  return (int32_t)std::min<size_t>(std::max<size_t>(room, 1), most);
 }
 
 template <int D>
@@ -932,7 +932,11 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
 cudaError_t launch_bounded_join(const BdArgs& b, int32_t S, int32_t head_dim, cudaStream_t stream) {
   return head_dim == 256 ? launch_join<256>(b, S, stream) : launch_join<512>(b, S, stream);
 }
-int32_t bounded_record_room(const AttnArgs& a, int32_t head_dim) { return record_room(a, head_dim); }
+int32_t bounded_record_room(const AttnArgs& a, int32_t head_dim, int32_t most) { return record_room(a, head_dim, most); }
+size_t bounded_records_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t ctas) {
+  const size_t S = (size_t)std::max(1, ctas);
+  return al16((size_t)(num_req + 1) * 8) + S * 2 * group * 2 * 4 + S * 2 * group * head_dim * 4;
+}
 void bounded_records(const AttnArgs& a, int32_t S, BdArgs* b) {
   unsigned char* ws = reinterpret_cast<unsigned char*>(a.ws_raw);
   b->prefix = reinterpret_cast<int64_t*>(ws);
@@ -946,8 +950,7 @@ bool bounded_decode_supported(int32_t head_dim, int32_t group, int32_t page_size
 }
 
 size_t bounded_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles) {
-  const size_t S = (size_t)std::max(1, std::min(kMaxCtas, max_tiles));
-  return al16((size_t)(num_req + 1) * 8) + S * 2 * group * 2 * 4 + S * 2 * group * head_dim * 4;
+  return bounded_records_bytes(num_req, group, head_dim, std::min(kMaxCtas, max_tiles));
 }
 
 // pg_workspace_bytes of head_dim 512 may hold the records of fewer CTAs than have tiles. With room for

@@ -22,9 +22,14 @@
 // Work, walk, records and join are those of attn_bounded_decode.cu; a ring slot is a tile of K or V
 // (128 keys x head_dim codes: three slots of 64 KB, or six of 32 KB), in the order K0 K1 V0 K2 V1 ...
 //   warps 0, 6  producers of K (with a header a tile) and of V: one 4-D box per 16 keys
-//   warp 7      the group's query rows into their terms, a segment ahead as far as its buffer allows
+//   warp 7      the group's query rows into their terms, a segment ahead as far as their buffer allows
+//   (the last)  (groups above 4: every other row each); and V rows of keys that are not visible to zero,
+//               whatever they held, once a tile's weights and V have arrived
 //   warp 1      MMA issuer: QK of tile i + 1 before PV of tile i
-//   warps 2-5   softmax: a thread is a key; its row scales load a tile ahead
+//   warps 2-5   softmax: a thread is a key and up to 8 query rows; its row scales load a tile ahead.
+//   (8-11)      Groups above 8 take two such sets, which share nothing but the tiles. (One set over
+//               16 rows took some 5,000 cycles a tile, as long as the tile's bytes; and references
+//               found by a reduction a row 9,000 where they moved: 146 us on the 64 requests below.)
 // Every wait is bounded, as there.
 #include "bounded_decode.cuh"
 #include "q8.cuh"
@@ -36,7 +41,8 @@
 namespace pg {
 namespace {
 
-constexpr int kThreadsQ8 = 256;
+constexpr int kQ8Ctas = 320;  // records are sized for at most this many CTAs (two an SM)
+constexpr int kReady = 8;  // tiles whose V may be said to be ready ahead of their products
 constexpr int kQs = 4;  // segments whose query scales are kept
 constexpr int kBox = 16, kBoxes = kT / kBox;  // key rows of a box, boxes of a tile
 // P is at most 448 where a weight stands kRoom octaves above its reference; a reference is set kLead
@@ -49,31 +55,38 @@ struct alignas(16) Q8Hdr {
   int32_t flags, g, tok;
 };
 
-// NR: rows of a term (8 or 16, the group padded)
-template <int D, int NR>
+// NQ: query rows of the softmax; NR: rows of a term (8 or 16, the group padded)
+template <int D, int NQ, int NR>
 struct Q8Cfg {
+  static constexpr int SETS = NQ > 8 ? 2 : 1;   // sets of four softmax warps
+  static constexpr int CQ = NQ / SETS;          // query rows of a set
+  static constexpr int QW = NQ > 4 ? 2 : 1;     // query warps
+  static constexpr int THREADS = 224 + 32 * QW + 128 * (SETS - 1);
+  // Small groups at head_dim 256: two CTAs an SM, each with half the ring, so that one streams while the
+  // other starts or ends a segment (of some 9 tiles under a window of 1023).
+  static constexpr int PER_SM = D == 256 && NQ <= 4 ? 2 : 1;
   static constexpr int NC = D / 128;            // 128-d chunks of a row
   static constexpr int SLOT = kT * D;
-  static constexpr int NSLOT = D == 256 ? 6 : 3;
+  static constexpr int NSLOT = D == 256 ? 6 / PER_SM : 3;
   static constexpr int QN = 2 * NR;             // columns of S: two terms
   static constexpr int PN = NR == 8 ? 32 : 48;  // of O: three terms (N is a multiple of 16)
-  static constexpr int NQB = D == 256 ? 2 : 1;  // query buffers (segments)
+  static constexpr int NQB = D == 256 && PER_SM == 1 ? 2 : 1;  // query buffers (segments)
   static constexpr int Q_BYTES = NC * QN * 128; // [128-d chunk][QN rows][128 B]
   static constexpr int P_BYTES = PN * 128;      // [PN rows][128 keys]
   static constexpr int OFF_Q = NSLOT * SLOT;
   static constexpr int OFF_P = OFF_Q + NQB * Q_BYTES;
   static constexpr int OFF_QS = OFF_P + 2 * P_BYTES;                 // [kQs][16] query scales
   static constexpr int OFF_HDR = OFF_QS + kQs * 16 * 4;
-  static constexpr int OFF_RED = OFF_HDR + kHdrs * (int)sizeof(Q8Hdr);  // [2][4 warps][16]
-  static constexpr int OFF_FIN = OFF_RED + 2 * 4 * 16 * 4;           // [16] (l, its reference, P's)
+  static constexpr int OFF_RED = OFF_HDR + kHdrs * (int)sizeof(Q8Hdr);  // [sets][4 warps][8] pairs
+  static constexpr int OFF_FIN = OFF_RED + SETS * 4 * 8 * 8;         // [16] (l, its reference, P's)
   static constexpr int OFF_BAR = OFF_FIN + 16 * 16;
   // FULL, EMPTY; QFULL[2], QEMPTY[2], HFULL[4], HEMPTY[4], SFULL[2], SFREE[2], PFULL[2], PVDONE[2],
-  // OFREE[2], DRAIN, QS[4]
-  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs;
+  // OFREE[2], DRAIN, QSCALE[4], VREADY[8]
+  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs + kReady;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static constexpr uint32_t TM_O = 0, O_COLS = NC * PN, TM_S = 2 * O_COLS;
   static constexpr uint32_t TM_COLS = TM_S + 2 * QN <= 256 ? 256 : 512;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory");
   static_assert(TM_S + 2 * QN <= 512, "tensor memory");
 };
 
@@ -94,33 +107,74 @@ __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_
       "l"(a), "l"(b), "r"(acc), "n"(IDESC)
       : "memory");
 }
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
-  if constexpr (N >= 32) {
-    tmem_ld32(taddr, r);
-    if constexpr (N > 32) tmem_ld<N - 32>(taddr + 32, r + 32);
-  } else {
-    tmem_ld16(taddr, r);
-  }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : PG_R8(0) : "r"(taddr));
 }
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
-  if constexpr (N >= 32) {
-    tmem_st32(taddr, r);
-    if constexpr (N > 32) tmem_st<N - 32>(taddr + 32, r + 32);
-  } else {
-    tmem_st16(taddr, r);
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), PG_W8(0)
+               : "memory");
+}
+// barriers among the 128 threads of a softmax set
+__device__ __forceinline__ bool any_of(int bar, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u), "r"(bar)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_set(int bar) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(bar) : "memory"); }
+// The warp's maxima (SUM: sums) of CQ values a lane: lane i returns that of value set_col<CQ>(i). Halves
+// the values at each exchange, so CQ of them cost about CQ + log2(32 / CQ) shuffles.
+template <int CQ>
+__device__ __forceinline__ int set_col(int lane) { return lane / (32 / CQ); }
+template <int CQ, bool SUM>
+__device__ __forceinline__ float warp_reduce(const float* x, int lane) {
+  float v[CQ];
+#pragma unroll
+  for (int k = 0; k < CQ; ++k) v[k] = x[k];
+  auto two = [](float p, float q) { return SUM ? p + q : fmaxf(p, q); };
+  int mask = 16;
+#pragma unroll
+  for (int w = CQ; w > 1; w /= 2, mask /= 2) {
+    const bool upper = lane & mask;
+#pragma unroll
+    for (int k = 0; k < w / 2; ++k) {
+      const float got = __shfl_xor_sync(0xffffffffu, upper ? v[k] : v[k + w / 2], mask);
+      v[k] = two(upper ? v[k + w / 2] : v[k], got);
+    }
   }
+#pragma unroll
+  for (int m = 16 / CQ; m > 0; m /= 2) v[0] = two(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
+  return v[0];
+}
+// Whether the phase of the given parity is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 // two e4m3 numbers, the first in the low byte, and what they stand for
 __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 
+__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
+  const __half2_raw r = *reinterpret_cast<const __half2_raw*>(&v);
+  return __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);  // (without saturation it takes a subroutine)
+}
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
 template <int D, int NQ, int NR>
-__global__ void __launch_bounds__(kThreadsQ8, 1)
+__global__ void __launch_bounds__(Q8Cfg<D, NQ, NR>::THREADS, Q8Cfg<D, NQ, NR>::PER_SM)
 q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
-  using C = Q8Cfg<D, NR>;
+  using C = Q8Cfg<D, NQ, NR>;
   constexpr int NS = C::NSLOT, NC = C::NC;
   const BdArgs& args = qa.b;
   const AttnArgs& a = args.a;
@@ -133,7 +187,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
   auto EMPTY = [&](int s) { return bars + 8u * (NS + s); };
   const uint32_t QFULL = bars + 8u * (2 * NS), QEMPTY = QFULL + 16, HFULL = QFULL + 32, HEMPTY = HFULL + 32,
                  SFULL = HEMPTY + 32, SFREE = SFULL + 16, PFULL = SFULL + 32, PVDONE = SFULL + 48,
-                 OFREE = SFULL + 64, DRAIN = SFULL + 80, QSCALE = SFULL + 88;
+                 OFREE = SFULL + 64, DRAIN = SFULL + 80, QSCALE = SFULL + 88, VREADY = QSCALE + 8 * kQs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::OFF_BAR + C::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const WaitCtx wc{abort_flag, a.status, a.wait_ns};
@@ -147,19 +201,20 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       mbar_init(EMPTY(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(QFULL + 8 * b, 1);
+      mbar_init(QFULL + 8 * b, C::QW);
       mbar_init(QEMPTY + 8 * b, 1);
       mbar_init(SFULL + 8 * b, 1);
-      mbar_init(SFREE + 8 * b, 4);
-      mbar_init(PFULL + 8 * b, 4);
+      mbar_init(SFREE + 8 * b, 4 * C::SETS);
+      mbar_init(PFULL + 8 * b, 4 * C::SETS);
       mbar_init(PVDONE + 8 * b, 1);
-      mbar_init(OFREE + 8 * b, 4);
+      mbar_init(OFREE + 8 * b, 4 * C::SETS);
     }
     for (int h = 0; h < kHdrs; ++h) {
       mbar_init(HFULL + 8 * h, 1);
-      mbar_init(HEMPTY + 8 * h, 6);  // the softmax warps, the query warp and the MMA issuer
+      mbar_init(HEMPTY + 8 * h, 4 * C::SETS + 1 + C::QW);  // the softmax warps, the query warps and the MMA issuer
     }
-    for (int q = 0; q < kQs; ++q) mbar_init(QSCALE + 8 * q, 1);
+    for (int q = 0; q < kQs; ++q) mbar_init(QSCALE + 8 * q, C::QW);
+    for (int q = 0; q < kReady; ++q) mbar_init(VREADY + 8 * q, 1);
     mbar_init(DRAIN, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -257,95 +312,167 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       while (globaltimer() - t0 < 100000ull) {
       }
     }
-  } else if (warp >= 7) {
+  } else if (warp == 7 || (C::QW == 2 && warp == C::THREADS / 32 - 1)) {
     // ------------------------------------------------------------ queries
     // A row's elements are all in the warp, 8 consecutive ones a lane and piece of 256.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int PC = D / 256;
-    constexpr int HALF = NQ < 8 ? NQ : 8;  // rows in registers at a time
-    bool ok = true;
-    int32_t segs = 0;
-    for (int32_t i = 0;; ++i) {
-      const int hb = i % kHdrs;
-      ok = __all_sync(0xffffffffu, mbar_wait_inline(HFULL + 8 * hb, (i / kHdrs) & 1, wc));
-      if (!ok) break;
-      const int32_t flags = hdrs[hb].flags, g = hdrs[hb].g, tok = hdrs[hb].tok;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(HEMPTY + 8 * hb);
-      if (flags & kEmpty) break;
-      if (flags & kFirst) {
-        const int qb = segs % C::NQB;
-        unsigned char* const dst = gb + C::OFF_Q + qb * C::Q_BYTES;
-        float* const qs = reinterpret_cast<float*>(gb + C::OFF_QS) + (segs % kQs) * 16;
-        const __nv_bfloat16* const src = a.q + ((int64_t)tok * Hq + (int64_t)g * G) * D + 8 * lane;
-        bool waited = false;
-#pragma unroll 1
-        for (int r0 = 0; ok && r0 < NQ; r0 += HALF) {
-          uint4 x[HALF][PC];
-#pragma unroll
-          for (int k = 0; k < HALF; ++k) {
-            const int row = r0 + k;
-#pragma unroll
-            for (int c = 0; c < PC; ++c)
-              x[k][c] = row < G ? *reinterpret_cast<const uint4*>(src + (int64_t)row * D + 256 * c)
-                                : make_uint4(0u, 0u, 0u, 0u);
-          }
-          if (!waited) {
-            ok = __all_sync(0xffffffffu, mbar_wait(QEMPTY + 8 * qb, ((segs / C::NQB) & 1) ^ 1, wc));
-            waited = true;
-            if (!ok) break;
-          }
-#pragma unroll
-          for (int k = 0; k < HALF; ++k) {
-            const int row = r0 + k;
-            if (row >= G) break;  // (uniform)
-            float2 y[4 * PC];
-#pragma unroll
-            for (int c = 0; c < PC; ++c) {
-              const uint32_t w[4] = {x[k][c].x, x[k][c].y, x[k][c].z, x[k][c].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                y[4 * c + e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-            }
-            const int32_t e = q8_exponent<32, 4 * PC>(y);
-            const float inv = q8_pow2(-e);
-#pragma unroll
-            for (int c = 0; c < PC; ++c) {
-              uint32_t hi[2], lo[2];
-#pragma unroll
-              for (int p = 0; p < 2; ++p) {
-                uint32_t h2[2], l2[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  const float2 v = y[4 * c + 2 * p + z];
-                  const float2 s = make_float2(v.x * inv, v.y * inv);
-                  h2[z] = e4m3x2(s);
-                  const float2 got = q8_values(h2[z]);
-                  l2[z] = e4m3x2(make_float2(16.f * (s.x - got.x), 16.f * (s.y - got.y)));
-                }
-                hi[p] = h2[0] | (h2[1] << 16);
-                lo[p] = l2[0] | (l2[1] << 16);
-              }
-              // d = 256 c + 8 lane: its 128-d chunk, and 8 bytes of a swizzled row there
-              const int d = 256 * c + 8 * lane;
-              unsigned char* const at = dst + (d >> 7) * (C::QN * 128);
-              const int pos = (((d & 127) >> 4) ^ (row & 7)) * 16 + (d & 8);
-              *reinterpret_cast<uint2*>(at + row * 128 + pos) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(at + (NR + row) * 128 + pos) = make_uint2(lo[0], lo[1]);
-            }
-            if (lane == 0) qs[row] = q8_pow2(e) * a.sm_scale_log2;
-          }
-        }
-        if (!ok) break;
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(QFULL + 8 * qb);
-          mbar_arrive(QSCALE + 8 * (segs % kQs));
-        }
-        ++segs;
+    constexpr int PC = D / 256, ROWS = NQ / C::QW;  // (NQ is 2, 4, 8 or 16)
+    const int first = warp == 7 ? 0 : 1;
+    int32_t segs = 0, i = 0, j = 0;  // headers read, and given back
+    int32_t g = 0, tok = 0;
+    bool end = false, fresh = false;  // fresh: the last header read began a segment whose queries are to come
+    uint64_t since = 0;               // when nothing was left to do
+    // Headers are read as they come, for the queries of new segments; warp 7 gives each back once V rows of
+    // its tile need nothing more. Nothing here waits for one thing alone: the query buffer may come free
+    // only behind a tile whose V rows are still to be cleared.
+    while (!end || fresh || j < i) {
+      bool idle = true;
+      if (!end && !fresh && i - j < kHdrs &&
+          __all_sync(0xffffffffu, mbar_test(HFULL + 8 * (i % kHdrs), (i / kHdrs) & 1))) {
+        idle = false;
+        const Q8Hdr& h = hdrs[i % kHdrs];
+        ++i;
+        if (h.flags & kEmpty) break;
+        end = h.flags & kEnd;
+        fresh = h.flags & kFirst;
+        g = h.g;
+        tok = h.tok;
       }
-      if (flags & kEnd) break;
+      if (fresh) {
+        const int qb = segs % C::NQB;
+        if (__all_sync(0xffffffffu, mbar_test(QEMPTY + 8 * qb, ((segs / C::NQB) & 1) ^ 1))) {
+          idle = fresh = false;
+          unsigned char* const dst = gb + C::OFF_Q + qb * C::Q_BYTES;
+          float* const qs = reinterpret_cast<float*>(gb + C::OFF_QS) + (segs % kQs) * 16;
+          const __nv_bfloat16* const src = a.q + ((int64_t)tok * Hq + (int64_t)g * G) * D + 8 * lane;
+          // A loop of few instructions over the rows, two at a time (unrolled over all of them it took
+          // 10,000 cycles at a CTA's start, most of it to fetch the code)
+          constexpr int STEP = ROWS < 2 ? 1 : 2;
+          uint4 x[STEP][PC];
+          auto load = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < STEP; ++k)
+#pragma unroll
+              for (int c = 0; c < PC; ++c) {
+                const int row = first + C::QW * (k0 + k);
+                x[k][c] = row < G ? *reinterpret_cast<const uint4*>(src + (int64_t)row * D + 256 * c)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+              }
+          };
+          load(0);
+#pragma unroll 1
+          for (int k0 = 0; k0 < ROWS; k0 += STEP) {
+            uint4 y[STEP][PC];
+#pragma unroll
+            for (int k = 0; k < STEP; ++k)
+#pragma unroll
+              for (int c = 0; c < PC; ++c) y[k][c] = x[k][c];
+            if (k0 + STEP < ROWS) load(k0 + STEP);
+            float f[STEP];
+#pragma unroll
+            for (int k = 0; k < STEP; ++k) {
+              __nv_bfloat162 m = __habs2(as_bf2(y[k][0].x));
+#pragma unroll
+              for (int c = 0; c < PC; ++c) {
+                if (c > 0) m = __hmax2(m, __habs2(as_bf2(y[k][c].x)));
+                m = __hmax2(m, __habs2(as_bf2(y[k][c].y)));
+                m = __hmax2(m, __habs2(as_bf2(y[k][c].z)));
+                m = __hmax2(m, __habs2(as_bf2(y[k][c].w)));
+              }
+              f[k] = fmaxf(__low2float(m), __high2float(m));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+              for (int k = 0; k < STEP; ++k) f[k] = fmaxf(f[k], __shfl_xor_sync(0xffffffffu, f[k], o));
+#pragma unroll
+            for (int k = 0; k < STEP; ++k) {
+              const int row = first + C::QW * (k0 + k);
+              const int32_t e = q8_exponent_of(f[k] > 0.f ? f[k] : 0.f);
+              const float inv = q8_pow2(-e);
+#pragma unroll
+              for (int c = 0; c < PC; ++c) {
+                const uint32_t w[4] = {y[k][c].x, y[k][c].y, y[k][c].z, y[k][c].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  // (16 bits hold 8 of significand down to 2^-17, and 2^-25 below: finer than a1 / 16)
+                  const __half2 s = __floats2half2_rn(__uint_as_float(w[p] << 16) * inv,
+                                                      __uint_as_float(w[p] & 0xFFFF0000u) * inv);
+                  hi[p] = e4m3x2(s);
+                  lo[p] = e4m3x2(__hmul2(__hsub2(s, q8_halves(hi[p])), __float2half2_rn(16.f)));
+                }
+                // d = 256 c + 8 lane: its 128-d chunk, and 8 bytes of a swizzled row there
+                const int d = 256 * c + 8 * lane;
+                unsigned char* const at = dst + (d >> 7) * (C::QN * 128);
+                const int pos = (((d & 127) >> 4) ^ (row & 7)) * 16 + (d & 8);
+                *reinterpret_cast<uint2*>(at + row * 128 + pos) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                *reinterpret_cast<uint2*>(at + (NR + row) * 128 + pos) =
+                    make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+              }
+              // (NaN is passed over by the maxima and stays NaN in the terms; the conversion turns an
+              // infinity into 448, so its row's scores become NaN here)
+              if (lane == 0) qs[row] = row >= G ? 0.f : f[k] == INFINITY ? NAN : q8_pow2(e) * a.sm_scale_log2;
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(QFULL + 8 * qb);
+            mbar_arrive(QSCALE + 8 * (segs % kQs));
+          }
+          ++segs;
+        }
+      }
+      if (j < i) {
+        const int hb = j % kHdrs;
+        const Q8Hdr& h = hdrs[hb];
+        bool done = warp != 7 || (h.vis[0] & h.vis[1] & h.vis[2] & h.vis[3]) == 0xFFFFFFFFu;
+        // The tile's weights have been written: its scores have been read, and PV of the tile two before is
+        // done, so the V slot's use before (K(j), V(j - 2) or an earlier one; V(j) follows K(j + 1) in the
+        // ring, the last one K(j)) has been consumed and a parity test tells the phases apart.
+        if (!done && __all_sync(0xffffffffu, mbar_test(PFULL + 8 * (j & 1), (j >> 1) & 1))) {
+          const int32_t at = (h.flags & kEnd) ? 2 * j + 1 : 2 * j + 2, sl = at % NS;
+          if (__all_sync(0xffffffffu, mbar_test(FULL(sl), (at / NS) & 1))) {
+            done = true;
+            // eight lanes a row
+#pragma unroll 1
+            for (int k = lane >> 3; k < kT; k += 4) {
+              if ((h.vis[k >> 5] >> (k & 31)) & 1u) continue;
+              unsigned char* const v = gb + sl * C::SLOT + (k >> 3) * (NC * 1024) + (k & 7) * 128 + (lane & 7) * 16;
+#pragma unroll
+              for (int c = 0; c < NC; ++c) *reinterpret_cast<uint4*>(v + c * 1024) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+          }
+        }
+        if (done) {
+          idle = false;
+          __syncwarp();
+          if (lane == 0) {
+            // (header j + 8 is behind the MMA issuer's reading of header j + 4, and that behind PV(j))
+            if (warp == 7) mbar_arrive(VREADY + 8 * (j % kReady));
+            mbar_arrive(HEMPTY + 8 * hb);
+          }
+          ++j;
+        }
+      }
+      if (!idle) {
+        since = 0;
+        continue;
+      }
+      const uint64_t now = globaltimer();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, *abort_flag != 0 || now - since > wc.limit_ns)) {
+        if (lane == 0 && *abort_flag == 0) {
+          atomicOr(a.status, kStatusTimeout);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      // (the softmax warps want the issue slots: a spinning warp here cost 3% of a step)
+      if (j == i && !fresh) mbar_try_wait(HFULL + 8 * (i % kHdrs), (i / kHdrs) & 1);
+      else __nanosleep(100);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -396,7 +523,8 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         const int pb = jt & 1, ob = pseg & 1;
         ok = wait1(PFULL + 8 * pb, (jt >> 1) & 1);
         if (ok && (pflags & kFirst)) ok = wait1(OFREE + 8 * ob, ((pseg >> 1) & 1) ^ 1);
-        ok = ok && wait1(FULL(slot), round & 1);
+        ok = ok && wait1(FULL(slot), round & 1) && 
+             wait1(VREADY + 8 * (jt % kReady), (jt / kReady) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint64_t pd = sdesc(base + C::OFF_P + pb * C::P_BYTES, 16, 1024);
@@ -420,19 +548,24 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
   } else {
     // ------------------------------------------------------------ softmax
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int CQ = C::CQ;
+    const int set = warp >= 8 ? 1 : 0, bar = 1 + set;
+    const int x0 = set * CQ;  // the set's first query row
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;  // the thread's key of each tile, and output column of 128
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    float* const red = reinterpret_cast<float*>(gb + C::OFF_RED);
-    float4* const fin = reinterpret_cast<float4*>(gb + C::OFF_FIN);
-    const float* const qs0 = reinterpret_cast<const float*>(gb + C::OFF_QS);
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + x0;
+    float2* const red = reinterpret_cast<float2*>(gb + C::OFF_RED) + set * 32;
+    float4* const fin = reinterpret_cast<float4*>(gb + C::OFF_FIN) + x0;
+    const float* const qs0 = reinterpret_cast<const float*>(gb + C::OFF_QS) + x0;
+    const int32_t Gs = min(max(G - x0, 0), CQ);  // rows of the group in the set
     // l and its reference (of s), and P's reference (of s + v, less kTop)
-    float l[NQ], ref[NQ], top[NQ];
+    float l[CQ], ref[CQ], top[CQ];
+    float my_ref = -INFINITY, my_top = -INFINITY;  // those of row set_col(lane)
     bool ok = true;
     int32_t segs = 0;
     struct Head {
       int32_t flags, g, tok;
-      uint32_t mine, all, k, v;  // visible keys of the warp, of every warp; the key's scale bytes
+      uint32_t mine, k, v;  // visible keys of the warp; the key's scale bytes
     };
     // header of tile i, and the loads of this key's scales
     auto fetch = [&](int32_t i) {
@@ -446,7 +579,6 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       h.g = x.g;
       h.tok = x.tok;
       h.mine = x.vis[quarter];
-      h.all = x.vis[0] & x.vis[1] & x.vis[2] & x.vis[3];
       if ((h.mine >> lane) & 1u) {
         const uint8_t* const at = qa.scales + x.row[row / kBox] + (row & (kBox - 1));
         h.k = *at;
@@ -465,33 +597,35 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         return;
       }
       tc_fence_after();
-      const int64_t row0 = (int64_t)p_tok * Hq + (int64_t)p_g * G;
-      const int64_t rec = ((int64_t)blockIdx.x * 2 + ((p_flags & kRec1) ? 1 : 0)) * G;
+      const int64_t row0 = (int64_t)p_tok * Hq + (int64_t)p_g * G + x0;
+      const int64_t rec = ((int64_t)blockIdx.x * 2 + ((p_flags & kRec1) ? 1 : 0)) * G + x0;
       // O stands at P's reference, l at its own: the root of the factor between them, applied twice
-      float inv[NQ], root[NQ];
+      float inv[CQ], root[CQ];
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) {
+      for (int x = 0; x < CQ; ++x) {
         const float4 f = fin[x];
         inv[x] = f.x == 0.f ? 0.f : 1.f / f.x;
         root[x] = f.x == 0.f ? 0.f : ex2(0.5f * (f.z - f.y));
       }
 #pragma unroll 1
       for (int p = 0; p < NC; ++p) {
-        uint32_t o[C::PN];
-        tmem_ld<C::PN>(tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * C::PN, o);
+        uint32_t o[3][8];
+        const uint32_t at = tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * C::PN;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) tmem_ld8(at + k * NR, o[k]);
         tmem_wait_ld();
         const int d = p * 128 + row;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          if (x >= G) break;
-          const float sum = fmaf(__uint_as_float(o[2 * NR + x]), 1.f / 256,
-                                 fmaf(__uint_as_float(o[NR + x]), 1.f / 16, __uint_as_float(o[x])));
+        for (int x = 0; x < CQ; ++x) {
+          if (x >= Gs) break;
+          const float sum = fmaf(__uint_as_float(o[2][x]), 1.f / 256,
+                                 fmaf(__uint_as_float(o[1][x]), 1.f / 16, __uint_as_float(o[0][x])));
           const float v = inv[x] == 0.f ? 0.f : sum * root[x] * inv[x] * root[x];
           if (p_flags & kSplit) args.rec_o[(rec + x) * D + d] = v;
           else a.out[(row0 + x) * D + d] = __float2bfloat16_rn(v);
         }
       }
-      if (row < G) {
+      if (row < Gs) {
         const float4 f = fin[row];
         if (p_flags & kSplit) *reinterpret_cast<float2*>(args.rec_ml + (rec + row) * 2) = make_float2(f.y, f.x);
         else if (a.lse) a.lse[row0 + row] = f.x != 0.f ? (f.y + log2f(f.x)) * kLn2f : -INFINITY;
@@ -501,10 +635,9 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       if (lane == 0) mbar_arrive(OFREE + 8 * (p_seg & 1));
     };
     Head h = fetch(0);
-    for (int32_t i = 0;; ++i) {
+    const bool none = any_of(bar, !ok) || (h.flags & kEmpty);  // (all of the set's warps leave together)
+    for (int32_t i = 0; !none; ++i) {
       const int b = i & 1;
-      if (any4(!ok)) break;  // all four warps leave together
-      if (h.flags & kEmpty) break;
       Head next{};
       if (!(h.flags & kEnd)) next = fetch(i + 1);
       ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(SFULL + 8 * b, (i >> 1) & 1, wc));
@@ -514,104 +647,101 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         ok = ok && __all_sync(0xffffffffu, mbar_wait(QSCALE + 8 * (segs % kQs), (segs / kQs) & 1, wc));
         ++segs;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
+        for (int x = 0; x < CQ; ++x) {
           l[x] = 0.f;
           ref[x] = top[x] = -INFINITY;
         }
+        my_ref = my_top = -INFINITY;
       }
       const bool vis = (h.mine >> lane) & 1u;
-      uint32_t sv[C::QN];
+      uint32_t s0[8], s1[8];
       tc_fence_after();
-      tmem_ld<C::QN>(tl + C::TM_S + b * C::QN, sv);
+      tmem_ld8(tl + C::TM_S + b * C::QN, s0);
+      tmem_ld8(tl + C::TM_S + b * C::QN + NR, s1);
       tmem_wait_ld();
       tc_fence_before();
       const float* const qs = qs0 + ((segs - 1) % kQs) * 16;
-      float t[NQ];
+      float t[CQ];
       const float ks = q8_scale(h.k);
       const float ve = (float)((int32_t)h.v - 127);
       bool over = false;
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) {
-        const float s = fmaf(__uint_as_float(sv[NR + x]), 1.f / 16, __uint_as_float(sv[x]));
+      for (int x = 0; x < CQ; ++x) {
+        const float s = fmaf(__uint_as_float(s1[x]), 1.f / 16, __uint_as_float(s0[x]));
         t[x] = vis ? s * ks * qs[x] : -INFINITY;
         over |= t[x] > ref[x] + kRescale || t[x] + ve > top[x] + (kTop + kRoom);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(SFREE + 8 * b);
-      if (any4(over)) {
-        // the rows' maxima over the tile, of s and of s + v, then references where they were outgrown
-        float mine = -INFINITY, mine2 = -INFINITY;
+      if (any_of(bar, over || !ok)) {
+        if (any_of(bar, !ok)) break;
+        // The rows' maxima over the tile, of s and of s + v, then references where they were outgrown:
+        // lane i looks after row set_col(i), and every lane takes what it finds.
+        float u[CQ];
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          const float m = warp_max(t[x]), m2 = warp_max(t[x] + ve);
-          if (lane == x) {
-            mine = m;
-            mine2 = m2;
-          }
-        }
-        if (lane < NQ) {
-          red[quarter * 16 + lane] = mine;
-          red[64 + quarter * 16 + lane] = mine2;
-        }
-        sync4();
-        float al[NQ];
-        bool scaled = false;
+        for (int x = 0; x < CQ; ++x) u[x] = t[x] + ve;
+        const int col = set_col<CQ>(lane);
+        const float2 mine = make_float2(warp_reduce<CQ, false>(t, lane), warp_reduce<CQ, false>(u, lane));
+        if (lane % (32 / CQ) == 0) red[quarter * 8 + col] = mine;
+        sync_set(bar);
+        float2 m = red[col];
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          const float m = fmaxf(fmaxf(red[x], red[16 + x]), fmaxf(red[32 + x], red[48 + x]));
-          const float m2 = fmaxf(fmaxf(red[64 + x], red[80 + x]), fmaxf(red[96 + x], red[112 + x]));
-          if (m > ref[x] + kRescale) {
-            const float to = m + kHeadroom;
-            if (ref[x] != -INFINITY) {
-              const float f = ex2(0.5f * (ref[x] - to));  // (its root, twice: attn_tc.cu)
-              l[x] = (l[x] * f) * f;
-            }
-            ref[x] = to;
-          }
-          al[x] = 1.f;
-          if (m2 > top[x] + (kTop + kRoom)) {
-            const float to = m2 + kLead - kTop;
-            if (top[x] != -INFINITY) {
-              al[x] = ex2(0.5f * (top[x] - to));
-              scaled = true;
-            }
-            top[x] = to;
-          }
+        for (int k = 1; k < 4; ++k) {
+          const float2 y = red[8 * k + col];
+          m = make_float2(fmaxf(m.x, y.x), fmaxf(m.y, y.y));
         }
-        // O holds the segment's earlier tiles at the old references (uniform over the threads)
+        const bool move_l = m.x > my_ref + kRescale, move_o = m.y > my_top + (kTop + kRoom);
+        const float to_l = move_l ? m.x + kHeadroom : my_ref, to_o = move_o ? m.y + kLead - kTop : my_top;
+        // roots of the factors, to be applied twice (attn_tc.cu)
+        const float fl = move_l && my_ref != -INFINITY ? ex2(0.5f * (my_ref - to_l)) : 1.f;
+        const float fo = move_o && my_top != -INFINITY ? ex2(0.5f * (my_top - to_o)) : 1.f;
+        const bool scaled = __any_sync(0xffffffffu, move_o && my_top != -INFINITY);
+        my_ref = to_l;
+        my_top = to_o;
+        float al[CQ];
+#pragma unroll
+        for (int x = 0; x < CQ; ++x) {
+          const int from = x * (32 / CQ);
+          ref[x] = __shfl_sync(0xffffffffu, my_ref, from);
+          top[x] = __shfl_sync(0xffffffffu, my_top, from);
+          al[x] = __shfl_sync(0xffffffffu, fo, from);
+          const float f = __shfl_sync(0xffffffffu, fl, from);
+          l[x] = (l[x] * f) * f;
+        }
+        // O holds the segment's earlier tiles at the old references (uniform over the set)
         if (scaled && !(h.flags & kFirst)) {
           const int32_t jt = i - 1;
           if (__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jt & 1), (jt >> 1) & 1, wc))) {
             tc_fence_after();
 #pragma unroll 1
             for (int p = 0; p < NC; ++p) {
-              uint32_t o[C::PN];
+              uint32_t o[3][8];
               const uint32_t at = tl + C::TM_O + ((segs - 1) & 1) * C::O_COLS + p * C::PN;
-              tmem_ld<C::PN>(at, o);
+#pragma unroll
+              for (int k = 0; k < 3; ++k) tmem_ld8(at + k * NR, o[k]);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 3; ++k)
+              for (int k = 0; k < 3; ++k) {
 #pragma unroll
-                for (int x = 0; x < NQ; ++x)
-                  o[k * NR + x] = __float_as_uint((__uint_as_float(o[k * NR + x]) * al[x]) * al[x]);
-              tmem_st<C::PN>(at, o);
+                for (int x = 0; x < CQ; ++x) o[k][x] = __float_as_uint((__uint_as_float(o[k][x]) * al[x]) * al[x]);
+                tmem_st8(at + k * NR, o[k]);
+              }
             }
             tmem_wait_st();
           } else {
             ok = false;
           }
         }
-        sync4();  // red has been read
+        sync_set(bar);  // red has been read
       }
       // the P buffer is free once PV(i - 2) has read it
       ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(PVDONE + 8 * b, ((i >> 1) & 1) ^ 1, wc));
       unsigned char* const pp = gb + C::OFF_P + b * C::P_BYTES + (row & 15);
 #pragma unroll
-      for (int x = 0; x < NQ; x += 2) {
+      for (int x = 0; x < CQ; x += 2) {
         float2 w;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          if (x + z >= NQ) break;
           l[x + z] += ex2(t[x + z] - (ref[x + z] == -INFINITY ? 0.f : ref[x + z]));
           (z ? w.y : w.x) = ex2(t[x + z] + (ve - (top[x + z] == -INFINITY ? 0.f : top[x + z])));
         }
@@ -623,28 +753,14 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         const uint32_t p2 = e4m3x2(make_float2(16.f * (r1.x - v1.x), 16.f * (r1.y - v1.y)));
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          if (x + z >= NQ) break;
           // row x of each term; the 16 keys of a piece are contiguous, pieces swizzled by the row
-          unsigned char* const at = pp + (x + z) * 128 + (((row >> 4) ^ ((x + z) & 7)) << 4);
+          unsigned char* const at = pp + (x0 + x + z) * 128 + (((row >> 4) ^ ((x + z) & 7)) << 4);
           at[0] = (unsigned char)(p0 >> (8 * z));
           at[NR * 128] = (unsigned char)(p1 >> (8 * z));
           at[2 * NR * 128] = (unsigned char)(p2 >> (8 * z));
         }
       }
-      if (h.all != 0xFFFFFFFFu) {
-        // V rows of keys that are not visible: zero once the copy has landed. The tile's V slot follows
-        // K(i + 1) in the ring (the last tile's follows K(i)); the slot's use before was V(i - 2) or
-        // earlier, which has been consumed (above), so a parity wait tells the phases apart.
-        const int32_t at = (h.flags & kEnd) ? 2 * i + 1 : 2 * i + 2, sl = at % NS;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(FULL(sl), (at / NS) & 1, wc));
-        if (ok && !vis) {
-          unsigned char* const v = gb + sl * C::SLOT + (row >> 3) * (NC * 1024) + (row & 7) * 128;
-#pragma unroll
-          for (int c = 0; c < 8 * NC; ++c)
-            *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      fence_proxy_async();  // the MMA reads P (and cleared V rows) through the async proxy
+      fence_proxy_async();  // the MMA reads P through the async proxy
       tc_fence_before();    // and O after any rescaling above
       __syncwarp();
       if (lane == 0) mbar_arrive(PFULL + 8 * b);
@@ -652,21 +768,14 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       pending = false;
       if (h.flags & kLast) {
         // the row sums over the 128 keys of every tile, and the references, for the epilogue
-        float mine = 0.f;
+        const int col = set_col<CQ>(lane);
+        const float mine = warp_reduce<CQ, true>(l, lane);
+        if (lane % (32 / CQ) == 0) red[quarter * 8 + col].x = mine;
+        sync_set(bar);
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          float s = l[x];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == x) mine = s;
-        }
-        if (lane < NQ) red[quarter * 16 + lane] = mine;
-        sync4();
-#pragma unroll
-        for (int x = 0; x < NQ; ++x)
-          if (row == x)
-            fin[x] = make_float4((red[x] + red[16 + x]) + (red[32 + x] + red[48 + x]), ref[x], top[x], 0.f);
-        sync4();
+        for (int x = 0; x < CQ; ++x)
+          if (row == x) fin[x] = make_float4((red[x].x + red[8 + x].x) + (red[16 + x].x + red[24 + x].x), ref[x], top[x], 0.f);
+        sync_set(bar);
         pending = true;
         p_tile = i;
         p_flags = h.flags;
@@ -701,7 +810,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
 
 template <int D, int NQ, int NR>
 cudaError_t launch_q8(const AttnArgs& a, const Q8Dev& q8, cudaStream_t stream) {
-  using C = Q8Cfg<D, NR>;
+  using C = Q8Cfg<D, NQ, NR>;
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
   const int32_t ps = a.pool.page_size, Hkv = a.pool.num_kv_heads;
@@ -728,7 +837,7 @@ cudaError_t launch_q8(const AttnArgs& a, const Q8Dev& q8, cudaStream_t stream) {
     return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
   }, &sms);
   if (e != cudaSuccess) return e;
-  const int32_t S = std::max(1, std::min(std::min(sms, bounded_record_room(a, D)), a.max_tiles));
+  const int32_t S = std::max(1, std::min(std::min(sms * C::PER_SM, bounded_record_room(a, D, kQ8Ctas)), a.max_tiles));
   Q8Args x;
   x.b.a = a;
   x.b.box_rows = kBox;
@@ -738,7 +847,7 @@ cudaError_t launch_q8(const AttnArgs& a, const Q8Dev& q8, cudaStream_t stream) {
   x.scales = q8.scales;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, 1, 1);
-  cfg.blockDim = dim3(kThreadsQ8, 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -753,6 +862,10 @@ cudaError_t launch_q8(const AttnArgs& a, const Q8Dev& q8, cudaStream_t stream) {
 }
 
 }  // namespace
+
+size_t q8_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles) {
+  return bounded_records_bytes(num_req, group, head_dim, std::min(kQ8Ctas, max_tiles));
+}
 
 bool q8_decode_supported(int32_t head_dim, int32_t group, int32_t page_size) {
   return (head_dim == 256 || head_dim == 512) && group >= 1 && group <= 16 && page_size >= kBox &&

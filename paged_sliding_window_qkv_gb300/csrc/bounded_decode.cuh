@@ -21,7 +21,8 @@ struct BdArgs {
 // The join of a decode kernel's records (attn_bounded_decode.cu); S: the CTAs that the kernel ran on.
 cudaError_t launch_bounded_join(const BdArgs& b, int32_t S, int32_t head_dim, cudaStream_t stream);
 // CTAs whose records the workspace holds, and where the records lie in it.
-int32_t bounded_record_room(const AttnArgs& a, int32_t head_dim);
+int32_t bounded_record_room(const AttnArgs& a, int32_t head_dim, int32_t most);
+size_t bounded_records_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t ctas);
 void bounded_records(const AttnArgs& a, int32_t S, BdArgs* b);
 
 namespace {

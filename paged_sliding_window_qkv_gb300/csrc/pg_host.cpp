@@ -1033,7 +1033,7 @@ bool q8_direct(const pg_plan* p) {
 size_t q8_workspace_bytes(const pg_plan* p) {
   if (!p || p->num_req == 0 || (p->head_dim != 256 && p->head_dim != 512)) return 0;
   if (q8_direct(p))
-    return bounded_decode_ws_bytes(p->num_req, p->num_qo_heads / p->num_kv_heads, p->head_dim, plan_max_tiles(p));
+    return q8_decode_ws_bytes(p->num_req, p->num_qo_heads / p->num_kv_heads, p->head_dim, plan_max_tiles(p));
   ReadBack w;
   return read_back(p, &w) ? w.bytes : SIZE_MAX;
 }

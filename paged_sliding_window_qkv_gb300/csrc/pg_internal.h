@@ -226,8 +226,8 @@ size_t bounded_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim,
 bool bounded_decode_fits(const AttnArgs& a, int32_t head_dim);
 cudaError_t launch_bounded_decode(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
 
-// Decode over an 8-bit pool on the tensor cores (a.pool: its geometry); workspace as
-// bounded_decode_ws_bytes.
+// Decode over an 8-bit pool on the tensor cores (a.pool: its geometry).
+size_t q8_decode_ws_bytes(int32_t num_req, int32_t group, int32_t head_dim, int32_t max_tiles);
 bool q8_decode_supported(int32_t head_dim, int32_t group, int32_t page_size);
 cudaError_t launch_q8_decode(const AttnArgs& a, const Q8Dev& q8, int32_t head_dim, cudaStream_t stream);
 

@@ -58,11 +58,12 @@ __device__ __forceinline__ uint32_t q8_codes(float2 a, float2 b, float inv) {
   return lo | (hi << 16);
 }
 
-// Values of two codes (the low 16 bits), unscaled.
-__device__ __forceinline__ float2 q8_values(uint32_t two) {
+// Values of two codes (the low 16 bits), unscaled; exact in 16 bits.
+__device__ __forceinline__ __half2 q8_halves(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return *reinterpret_cast<const __half2*>(&h);
 }
+__device__ __forceinline__ float2 q8_values(uint32_t two) { return __half22float2(q8_halves(two)); }
 
 }  // namespace
 }  // namespace pg
