@@ -184,7 +184,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     };
     bool ok = true;
     if (n == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      wait_previous(a);
       write_prefix();
       if (lane == 0 && !is_v) {
         hdrs[0].flags = kEmpty | kEnd;
@@ -210,7 +210,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         return true;
       };
       Tile cur = next(0);
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      wait_previous(a);
       int32_t segs = 0;
       for (int32_t i = 0; ok && i < n; ++i) {
         const bool good = cur.live && cur.page >= 0 && cur.page < a.pool.num_pages;
@@ -351,7 +351,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     commit1(DRAIN);
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous(a);
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;  // the thread's key of each tile, and output column of 128
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -575,6 +575,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   // the join's launch overlaps the last CTAs' ends (released earlier, its blocks would sit on the SMs
   // while the copies stream: 236 against 222 us on 64 requests of 8001 keys with weights)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_beside(a);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -633,10 +634,12 @@ constexpr int kJoinKeys = kPer * kJoinThreads;  // keys of a weight block
 constexpr int kJoinRecs = 8;
 // RG: threads that share the records of four columns (4 where segments are cut into many, so that
 // 32 records are in flight, else 1)
+// PARTS: the rows also have records of a shared prefix's parts (attn_tc.cu), and a segment that was
+// written directly takes part with its bf16 output.
 __host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D, int32_t RG) {
   return (group * D * RG + 511) / 512;
 }
-template <int D, int RG>
+template <int D, int RG, bool PARTS>
 __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
   const AttnArgs& a = args.a;
   // (a following kernel launched programmatically may set up; it waits for this one)
@@ -660,15 +663,23 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
     if (RG == 1 && row >= G) return;
     const bool mine = row < G && rg == 0;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (row0 + row) * D + 4 * c4);
-    if (q.total == 0) {
+    const int64_t part_rows = (int64_t)a.plan.num_tokens * Hq;
+    const int32_t num_parts = PARTS ? a.tok_parts[q.tok] : 0;
+    if (q.total == 0 && num_parts == 0) {
       if (mine) {
         dst[0] = dst[1] = 0u;
-        if (a.lse && c4 == 0) a.lse[row0 + row] = -INFINITY;
+        float* const lse = PARTS ? a.join_lse : a.lse;
+        if (lse && c4 == 0) lse[row0 + row] = -INFINITY;
       }
       return;
     }
-    const SegRecs s = seg_recs(pre + (int64_t)g * q.total, q.total, U, S);
-    if (s.sa == s.sb) return;
+    SegRecs s{0, 0, 0, false};
+    if (q.total > 0) s = seg_recs(pre + (int64_t)g * q.total, q.total, U, S);
+    const bool direct = s.sa == s.sb;
+    if (direct && num_parts == 0) {
+      if (PARTS && mine && c4 == 0 && a.join_lse) a.join_lse[row0 + row] = a.lse[row0 + row];
+      return;
+    }
     float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float m2, float w2, float4 x, bool mean) {
@@ -680,7 +691,7 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
       den = den * so + w2 * e;
       M = mn;
     };
-    for (int32_t c0 = s.sa + rg; row < G && c0 <= s.sb; c0 += RG * kJoinRecs) {
+    for (int32_t c0 = s.sa + rg; !direct && row < G && c0 <= s.sb; c0 += RG * kJoinRecs) {
       float2 ml[kJoinRecs];
       float4 v[kJoinRecs];
 #pragma unroll
@@ -693,6 +704,30 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
       }
 #pragma unroll
       for (int k = 0; k < kJoinRecs; ++k) add(ml[k].x, ml[k].y, v[k], true);
+    }
+    if constexpr (PARTS) {
+      for (int32_t c0 = rg; row < G && c0 < num_parts; c0 += RG * kJoinRecs) {
+        float2 ml[kJoinRecs];
+        float4 v[kJoinRecs];
+#pragma unroll
+        for (int k = 0; k < kJoinRecs; ++k) {
+          const int32_t c = c0 + RG * k;
+          const int64_t at = c * part_rows + row0 + row;
+          ml[k] = c < num_parts ? *reinterpret_cast<const float2*>(a.part_ml + 2 * at) : make_float2(-INFINITY, 0.f);
+          v[k] = c < num_parts ? __ldcs(reinterpret_cast<const float4*>(a.part_o + at * D) + c4)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinRecs; ++k) add(ml[k].x, ml[k].y, v[k], true);
+      }
+      if (mine && direct && q.total > 0) {
+        const float own = a.lse[row0 + row];
+        const uint32_t w0 = dst[0], w1 = dst[1];
+        add(own * kLog2ef, own == -INFINITY ? 0.f : 1.f,
+            make_float4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xFFFF0000u), __uint_as_float(w1 << 16),
+                        __uint_as_float(w1 & 0xFFFF0000u)),
+            true);
+      }
     }
     if constexpr (RG > 1) {
       s_acc[tid] = acc;
@@ -708,7 +743,8 @@ __global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs ar
     const float inv = den != 0.f ? 1.f / den : 0.f;
     dst[0] = pack_bf16(acc.x * inv, acc.y * inv);
     dst[1] = pack_bf16(acc.z * inv, acc.w * inv);
-    if (a.lse && c4 == 0) a.lse[row0 + row] = den != 0.f ? (M + log2f(den)) * kLn2f : -INFINITY;
+    float* const lse = PARTS ? a.join_lse : a.lse;
+    if (lse && c4 == 0) lse[row0 + row] = den != 0.f ? (M + log2f(den)) * kLn2f : -INFINITY;
     return;
   }
   // ---- weights
@@ -848,6 +884,7 @@ cudaError_t launch_join(const BdArgs& b, int32_t S, cudaStream_t stream) {
   const bool weigh = a.stats.mass != nullptr;
   const int32_t key_blocks = weigh ? (a.max_keys + kJoinKeys - 1) / kJoinKeys : 0;
   const int32_t segs = a.plan.num_req * Hkv;
+  const bool parts = a.tok_parts != nullptr;
   auto join = [&](auto kernel, int32_t RG) {
     const unsigned grid =
         (unsigned)((int64_t)segs * join_parts(G, D, RG) + (int64_t)a.plan.num_req * key_blocks);
@@ -856,7 +893,9 @@ cudaError_t launch_join(const BdArgs& b, int32_t S, cudaStream_t stream) {
     cfg.dynamicSmemBytes = weigh ? a.num_qo_heads * sizeof(float) : 0;
     return cudaLaunchKernelEx(&cfg, kernel, b, S, std::max(key_blocks, 1));
   };
-  const cudaError_t e = segs * 4 < S ? join(bounded_join_kernel<D, 4>, 4) : join(bounded_join_kernel<D, 1>, 1);
+  const bool many = segs * 4 < S;
+  const cudaError_t e = parts ? (many ? join(bounded_join_kernel<D, 4, true>, 4) : join(bounded_join_kernel<D, 1, true>, 1))
+                              : (many ? join(bounded_join_kernel<D, 4, false>, 4) : join(bounded_join_kernel<D, 1, false>, 1));
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -903,7 +942,8 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   }, &sms);
   if (e != cudaSuccess) return e;
   // as many CTAs as have tiles and room for their records
-  const int32_t S = std::max(1, std::min(std::min(sms, record_room(a, D)), a.max_tiles));
+  const int32_t on = a.beside > 0 ? std::min(a.beside, sms) : sms;
+  const int32_t S = std::max(1, std::min(std::min(on, record_room(a, D)), a.max_tiles));
   BdArgs b;
   b.a = a;
   b.box_rows = br;

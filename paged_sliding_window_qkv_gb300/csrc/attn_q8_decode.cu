@@ -42,7 +42,7 @@ namespace pg {
 namespace {
 
 constexpr int kQ8Ctas = 320;  // records are sized for at most this many CTAs (two an SM)
-constexpr int kReady = 8;  // tiles whose V may be said to be ready ahead of their products
+constexpr int kFix = 64;  // a tile flag: it has keys that are not visible, so V waits to be cleared
 constexpr int kQs = 4;  // segments whose query scales are kept
 constexpr int kBox = 16, kBoxes = kT / kBox;  // key rows of a box, boxes of a tile
 // P is at most 448 where a weight stands kRoom octaves above its reference; a reference is set kLead
@@ -81,8 +81,8 @@ struct Q8Cfg {
   static constexpr int OFF_FIN = OFF_RED + SETS * 4 * 8 * 8;         // [16] (l, its reference, P's)
   static constexpr int OFF_BAR = OFF_FIN + 16 * 16;
   // FULL, EMPTY; QFULL[2], QEMPTY[2], HFULL[4], HEMPTY[4], SFULL[2], SFREE[2], PFULL[2], PVDONE[2],
-  // OFREE[2], DRAIN, QSCALE[4], VREADY[8]
-  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs + kReady;
+  // OFREE[2], DRAIN, QSCALE[4], VREADY[2]
+  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs + 2;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static constexpr uint32_t TM_O = 0, O_COLS = NC * PN, TM_S = 2 * O_COLS;
   static constexpr uint32_t TM_COLS = TM_S + 2 * QN <= 256 ? 256 : 512;
@@ -214,7 +214,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       mbar_init(HEMPTY + 8 * h, 4 * C::SETS + 1 + C::QW);  // the softmax warps, the query warps and the MMA issuer
     }
     for (int q = 0; q < kQs; ++q) mbar_init(QSCALE + 8 * q, C::QW);
-    for (int q = 0; q < kReady; ++q) mbar_init(VREADY + 8 * q, 1);
+    for (int q = 0; q < 2; ++q) mbar_init(VREADY + 8 * q, 1);
     mbar_init(DRAIN, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -249,7 +249,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     const bool is_v = warp == 6;
     bool ok = true;
     if (n == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      wait_previous(a);
       if (blockIdx.x == 0 && !is_v) write_tile_prefix(args, lane, held);
       if (lane == 0 && !is_v) {
         hdrs[0].flags = kEmpty | kEnd;
@@ -269,7 +269,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         return true;
       };
       Tile cur = walk.next(0);
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      wait_previous(a);
       for (int32_t i = 0; ok && i < n; ++i) {
         const bool good = cur.live && cur.page >= 0 && cur.page < a.pool.num_pages;
         const int32_t row = (int32_t)((((int64_t)cur.page * 2 + (is_v ? 1 : 0)) * Hkv + cur.g) * ps + cur.off);
@@ -295,7 +295,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         if (lane == 0) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) h.vis[w] = vis[w];
-          h.flags = cur.flags;
+          h.flags = cur.flags | ((vis[0] & vis[1] & vis[2] & vis[3]) == 0xFFFFFFFFu ? 0 : kFix);
           h.g = cur.g;
           h.tok = cur.q.tok;
         }
@@ -315,15 +315,15 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
   } else if (warp == 7 || (C::QW == 2 && warp == C::THREADS / 32 - 1)) {
     // ------------------------------------------------------------ queries
     // A row's elements are all in the warp, 8 consecutive ones a lane and piece of 256.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous(a);
     constexpr int PC = D / 256, ROWS = NQ / C::QW;  // (NQ is 2, 4, 8 or 16)
     const int first = warp == 7 ? 0 : 1;
     int32_t segs = 0, i = 0, j = 0;  // headers read, and given back
-    int32_t g = 0, tok = 0;
+    int32_t g = 0, tok = 0, fixes = 0;
     bool end = false, fresh = false;  // fresh: the last header read began a segment whose queries are to come
     uint64_t since = 0;               // when nothing was left to do
-    // Headers are read as they come, for the queries of new segments; warp 7 gives each back once V rows of
-    // its tile need nothing more. Nothing here waits for one thing alone: the query buffer may come free
+    // Headers are read as they come, for the queries of new segments; warp 7 gives each back once its tile's
+    // V rows need nothing more. Nothing here waits for one thing alone: the query buffer may come free
     // only behind a tile whose V rows are still to be cleared.
     while (!end || fresh || j < i) {
       bool idle = true;
@@ -427,14 +427,16 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       if (j < i) {
         const int hb = j % kHdrs;
         const Q8Hdr& h = hdrs[hb];
-        bool done = warp != 7 || (h.vis[0] & h.vis[1] & h.vis[2] & h.vis[3]) == 0xFFFFFFFFu;
-        // The tile's weights have been written: its scores have been read, and PV of the tile two before is
-        // done, so the V slot's use before (K(j), V(j - 2) or an earlier one; V(j) follows K(j + 1) in the
-        // ring, the last one K(j)) has been consumed and a parity test tells the phases apart.
-        if (!done && __all_sync(0xffffffffu, mbar_test(PFULL + 8 * (j & 1), (j >> 1) & 1))) {
+        // Warp 7 goes on once the tile's weights have been written. (Every tile's in turn: a parity test
+        // tells two phases apart only when the one before is over.) The tile's scores have then been read
+        // and PV of the tile two before is done, so the V slot's use before (K(j), V(j - 2) or an earlier
+        // one; V(j) follows K(j + 1) in the ring, the last one K(j)) has been consumed too.
+        bool done = warp != 7 || __all_sync(0xffffffffu, mbar_test(PFULL + 8 * (j & 1), (j >> 1) & 1));
+        const bool fix = warp == 7 && (h.flags & kFix);
+        if (done && fix) {
           const int32_t at = (h.flags & kEnd) ? 2 * j + 1 : 2 * j + 2, sl = at % NS;
-          if (__all_sync(0xffffffffu, mbar_test(FULL(sl), (at / NS) & 1))) {
-            done = true;
+          done = __all_sync(0xffffffffu, mbar_test(FULL(sl), (at / NS) & 1));
+          if (done) {
             // eight lanes a row
 #pragma unroll 1
             for (int k = lane >> 3; k < kT; k += 4) {
@@ -450,10 +452,11 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
           idle = false;
           __syncwarp();
           if (lane == 0) {
-            // (header j + 8 is behind the MMA issuer's reading of header j + 4, and that behind PV(j))
-            if (warp == 7) mbar_arrive(VREADY + 8 * (j % kReady));
+            // (weights of a third such tile wait for the first one's PV, so two barriers do)
+            if (fix) mbar_arrive(VREADY + 8 * (fixes & 1));
             mbar_arrive(HEMPTY + 8 * hb);
           }
+          fixes += fix ? 1 : 0;
           ++j;
         }
       }
@@ -486,7 +489,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     auto step = [&]() {
       if (++slot == NS) { slot = 0; ++round; }
     };
-    int32_t segs = 0, flags = 0, pflags = 0, pseg = 0;
+    int32_t segs = 0, flags = 0, pflags = 0, pseg = 0, fixes = 0;
     bool end = false;
     for (int32_t i = 0;; ++i) {
       bool ok = true;
@@ -523,8 +526,11 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
         const int pb = jt & 1, ob = pseg & 1;
         ok = wait1(PFULL + 8 * pb, (jt >> 1) & 1);
         if (ok && (pflags & kFirst)) ok = wait1(OFREE + 8 * ob, ((pseg >> 1) & 1) ^ 1);
-        ok = ok && wait1(FULL(slot), round & 1) && 
-             wait1(VREADY + 8 * (jt % kReady), (jt / kReady) & 1);
+        ok = ok && wait1(FULL(slot), round & 1);
+        if (ok && (pflags & kFix)) {
+          ok = wait1(VREADY + 8 * (fixes & 1), (fixes >> 1) & 1);
+          ++fixes;
+        }
         if (!ok) break;
         tc_fence_after();
         const uint64_t pd = sdesc(base + C::OFF_P + pb * C::P_BYTES, 16, 1024);
@@ -547,7 +553,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     commit1(DRAIN);
   } else {
     // ------------------------------------------------------------ softmax
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_previous(a);
     constexpr int CQ = C::CQ;
     const int set = warp >= 8 ? 1 : 0, bar = 1 + set;
     const int x0 = set * CQ;  // the set's first query row
@@ -790,6 +796,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
   }
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_beside(a);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -837,7 +844,7 @@ cudaError_t launch_q8(const AttnArgs& a, const Q8Dev& q8, cudaStream_t stream) {
     return cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
   }, &sms);
   if (e != cudaSuccess) return e;
-  const int32_t S = std::max(1, std::min(std::min(sms * C::PER_SM, bounded_record_room(a, D, kQ8Ctas)), a.max_tiles));
+  const int32_t S = std::max(1, std::min(std::min((a.beside > 0 ? std::min(a.beside, sms) : sms) * C::PER_SM, bounded_record_room(a, D, kQ8Ctas)), a.max_tiles));
   Q8Args x;
   x.b.a = a;
   x.b.box_rows = kBox;

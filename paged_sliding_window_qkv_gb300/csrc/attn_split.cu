@@ -633,7 +633,9 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t head_dim, cudaStream_
 cudaError_t launch_attn_decode(const AttnArgs& args, int32_t head_dim, cudaStream_t stream) {
   if (args.plan.num_req == 0) return cudaSuccess;
   if (args.bounded) {
-    if (bounded_decode_supported(head_dim, args.group, args.pool.page_size) && bounded_decode_fits(args, head_dim))
+    // (beside a shared prefix's parts: its join takes them, and the workspace has every record)
+    if (bounded_decode_supported(head_dim, args.group, args.pool.page_size) &&
+        (args.tok_parts || bounded_decode_fits(args, head_dim)))
       return launch_bounded_decode(args, head_dim, stream);
   } else if (attn_decode_stream_supported(head_dim, args.group, args.pool.page_size)) {
     return launch_attn_decode_stream(args, head_dim, stream);

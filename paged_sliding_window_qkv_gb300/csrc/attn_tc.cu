@@ -1310,7 +1310,8 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   // rounds
   const int64_t units = (int64_t)a.plan.num_pairs * a.pool.num_kv_heads * (DQK / kDV);
   if (units == 0) return cudaSuccess;
-  const int64_t clusters = std::min<int64_t>(units, nsm / 2 > 0 ? nsm / 2 : 1);
+  int64_t clusters = std::min<int64_t>(units, nsm / 2 > 0 ? nsm / 2 : 1);
+  if (PART && a.part_clusters > 0) clusters = std::min<int64_t>(clusters, a.part_clusters);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
   cfg.blockDim = dim3(kThreadsTc, 1, 1);

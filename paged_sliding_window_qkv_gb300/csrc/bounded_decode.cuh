@@ -88,6 +88,15 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
 }
 
+// What the kernel reads may come from the stream's previous kernel, unless it runs beside that one: then
+// it only ends behind it, so that the stream's order holds for what follows.
+__device__ __forceinline__ void wait_previous(const AttnArgs& a) {
+  if (a.beside == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void wait_beside(const AttnArgs& a) {
+  if (a.beside != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // The boxes of request r that its query sees, and the tiles they fill (one KV head).
 struct ReqTiles {
   KeyWalk w;      // in boxes

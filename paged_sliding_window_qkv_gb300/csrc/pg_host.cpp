@@ -115,6 +115,7 @@ struct pg_plan {
   // over arrays in `dev` (it owns nothing there), and the prefixes' parts
   std::unique_ptr<pg_plan> own;
   int32_t num_groups = 0, num_parts = 0, room_parts = 0, parts_most = 0, prefix_pages = 0;
+  int32_t beside = 0;  // decode: SMs for the own keys while the others take the parts (0: one after the other)
   size_t o_part = 0, o_part_row = 0, o_part_live = 0, o_tok_parts = 0, o_pre_pages = 0;
 };
 
@@ -323,7 +324,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
 
   // Shared prefixes: the requests' own keys as segments, and the parts of each group's prefix.
   std::vector<int32_t> kvp2, kvs2, pages2, ptab2, part, part_row, tok_parts, pre_pages;
-  int32_t seen2 = 0, num_parts = 0, room_parts = 0, parts_most = 0, pre_total = 0;
+  int32_t seen2 = 0, num_parts = 0, room_parts = 0, parts_most = 0, pre_total = 0, beside = 0;
   int64_t tiles2 = 0;
   if (groups) {
     if (!attn_tc_supported(D, group, ps) || cta <= 0) return PG_ERR_PLAN_MISMATCH;
@@ -354,23 +355,34 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     }
     if (!all_one) sort_pairs(&ptab2, cta, num_req > 1);
     // How long a part is: every candidate length costs rounds of units over the clusters, each as
-    // long as its key tiles and a start and an epilogue worth about five.
-    const int32_t heads = Hkv * (D / 256), clusters = std::max(1, sm_count() / 2);
-    parts_most = num_req > 0 ? most_parts(T, groups->num, cta, heads, sm_count()) : 0;
+    // long as its key tiles (about a microsecond each) and a start and an epilogue worth about five.
+    // A decode step's own keys are a stream of bytes: they run beside the parts, on SMs of their own
+    // (some 80 GB/s each, 6 TB/s together, and some 6 us to begin and end), where that ends sooner.
+    const int32_t heads = Hkv * (D / 256), sms = std::max(2, sm_count());
+    int64_t own_keys = 0;
+    for (int32_t r = 0; r < num_req; ++r) own_keys += (kvp[r + 1] - kvp[r] - 1) * (int64_t)ps + last[r] - kvs2[r];
+    const double own_bytes = (double)own_keys * Hkv * D * 4;
+    auto own_us = [&](int32_t on) { return 6 + own_bytes / std::min(6e6, on * 8e4); };
+    parts_most = num_req > 0 ? most_parts(T, groups->num, cta, heads, sms) : 0;
     const int32_t most_len = pre.empty() ? 0 : *std::max_element(pre.begin(), pre.end());
     const int32_t step = std::max(64, ps);
     auto group_tokens = [&](int32_t g) { return qo[groups->indptr[g + 1]] - qo[groups->indptr[g]]; };
-    int64_t best = 0;
+    double best = 0;
     int32_t run = step;
     for (int32_t k = 1; k <= parts_most && most_len > 0; ++k) {
       const int64_t len = ((int64_t)most_len + (int64_t)k * step - 1) / ((int64_t)k * step) * step;
       int64_t units = 0;
       for (int32_t g = 0; g < groups->num; ++g)
         units += (((int64_t)group_tokens(g) + 2 * cta - 1) / (2 * cta)) * ((pre[g] + len - 1) / len) * heads;
-      const int64_t cost = (units + clusters - 1) / clusters * (len / 64 + 5);
-      if (k == 1 || cost < best) {
-        best = cost;
-        run = (int32_t)std::min<int64_t>(len, INT32_MAX - 1024);
+      for (int32_t on = 0; on <= (all_one ? sms / 2 : 0); on += 8) {  // SMs of the own keys
+        const int64_t clusters = std::max(1, (sms - on) / 2);
+        const double parts_us = (double)((units + clusters - 1) / clusters * (len / 64 + 5));
+        const double cost = on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on));
+        if ((k == 1 && on == 0) || cost < best) {
+          best = cost;
+          run = (int32_t)std::min<int64_t>(len, INT32_MAX - 1024);
+          beside = on;
+        }
       }
     }
     tok_parts.assign((size_t)T, 0);
@@ -536,6 +548,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     q.num_parts = num_parts;
     q.room_parts = room_parts;
     q.parts_most = parts_most;
+    q.beside = beside;
     q.prefix_pages = pre_total;
   }
 
@@ -752,7 +765,17 @@ struct Bounded {
   int64_t logit_slots = 0;
   StatsDev stats = {};
   const int32_t* page_ids = nullptr;  // device: the pool's pages in the order of the plan's list
+  const AttnArgs* parts = nullptr;    // decode: parts of the rows' prefixes, for the join
 };
+// The parts' records into the arguments of the call on the own keys.
+void take_parts(AttnArgs* a, const AttnArgs* parts) {
+  if (!parts) return;
+  a->part_o = parts->part_o;
+  a->part_ml = parts->part_ml;
+  a->tok_parts = parts->tok_parts;
+  a->join_lse = parts->join_lse;
+  a->beside = parts->beside;
+}
 
 int32_t plan_max_tiles(const pg_plan* p) {
   return (int32_t)std::min<int64_t>(p->tiles * p->num_kv_heads, INT32_MAX);
@@ -866,6 +889,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   a.ws_bytes = ws_bytes;
   a.ws_o = nullptr;
   a.ws_ml = nullptr;
+  if (bounded) take_parts(&a, bounded->parts);
   if (args) *args = a;
   if (plan->decode) {
     e = launch_attn_decode(a, D, stream);
@@ -1040,7 +1064,7 @@ size_t q8_workspace_bytes(const pg_plan* p) {
 
 int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
             float* lse, int32_t window_left, int32_t num_sink, float sm_scale, void* ws, size_t ws_bytes,
-            cudaStream_t stream) {
+            cudaStream_t stream, const AttnArgs* parts = nullptr) {
   int rc = check_bounded_plan(plan, stream);
   if (rc || (rc = check_bounded_attn(plan, num_sink))) return rc;
   if ((rc = check_plan_q8(plan, pool, layer, 1))) return rc;
@@ -1074,6 +1098,7 @@ int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const 
     a.max_keys = plan->max_seen;
     a.max_tiles = plan_max_tiles(plan);
     wait_settings(&a.wait_ns, &a.test_withhold);
+    take_parts(&a, parts);
     return launch_q8_decode(a, q8_dev(pool, layer), D, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
   }
   ReadBack w;
@@ -1154,6 +1179,9 @@ AttnArgs part_args(const pg_plan* p, const PoolDev& pool, const int32_t* page_id
   a.part_o = reinterpret_cast<float*>(base + w.o);
   a.part_ml = reinterpret_cast<float*>(base + w.ml);
   a.part_row = p->dev + p->o_part_row;
+  a.tok_parts = p->dev + p->o_tok_parts;
+  a.beside = p->beside;
+  if (p->beside > 0) a.part_clusters = std::max(1, (sm_count() - p->beside) / 2);
   a.status = status;
   wait_settings(&a.wait_ns, &a.test_withhold);
   return a;
@@ -1165,6 +1193,7 @@ cudaError_t shared_join(const pg_plan* p, pg_bf16_t* out, float* lse, unsigned c
   j.part_ml = reinterpret_cast<const float*>(base + w.ml);
   j.tok_parts = p->dev + p->o_tok_parts;
   j.out = reinterpret_cast<__nv_bfloat16*>(out);
+  j.own_lse = reinterpret_cast<const float*>(base + w.lse);
   j.lse = lse;
   j.num_tokens = p->num_tokens;
   j.num_qo_heads = p->num_qo_heads;
@@ -1204,16 +1233,19 @@ int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const
   if (!st) return err;
   unsigned char* const base = static_cast<unsigned char*>(ws);
   const bool join = plan->num_parts > 0 || capturing(stream);
-  float* const row_lse = lse ? lse : reinterpret_cast<float*>(base + w.lse);
-  if (join) {
-    const AttnArgs a = part_args(plan, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q,
-                                 sm_scale, base, w, st);
-    if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
-  }
+  float* const own_lse = join ? reinterpret_cast<float*>(base + w.lse) : lse;
   Bounded b;
-  rc = attn_common(own, pool, layer, D, q, out, row_lse, -1, sm_scale, base + w.own, ws_bytes - w.own, stream, &b);
-  if (rc != PG_OK || !join) return rc;
-  return shared_join(plan, out, row_lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+  AttnArgs a;
+  if (join) {
+    a = part_args(plan, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q, sm_scale, base, w,
+                  st);
+    if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
+    a.join_lse = lse;
+    if (plan->decode) b.parts = &a;  // (the decode's join takes the parts along)
+  }
+  rc = attn_common(own, pool, layer, D, q, out, own_lse, -1, sm_scale, base + w.own, ws_bytes - w.own, stream, &b);
+  if (rc != PG_OK || !join || b.parts) return rc;
+  return shared_join(plan, out, lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
 // The 8-bit form: each prefix's pages are read back to the end of the workspace, behind a list of
@@ -1259,7 +1291,9 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
   int* st = status_word(&err);
   if (!st) return err;
   const bool join = plan->num_parts > 0 || captured;
-  float* const row_lse = lse ? lse : reinterpret_cast<float*>(base + x.w.lse);
+  float* const own_lse = join ? reinterpret_cast<float*>(base + x.w.lse) : lse;
+  AttnArgs a;
+  const bool along = join && q8_direct(plan->own.get());  // the decode's join takes the parts along
   if (join) {
     DequantArgs d{};
     d.plan = plan_dev(plan);
@@ -1281,12 +1315,14 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
     PoolDev copy = q8_geometry(pool);
     copy.layer_base = d.dst;
     copy.num_pages = pages;
-    const AttnArgs a = part_args(plan, copy, d.ids, pages, q, sm_scale, base, x.w, st);
+    a = part_args(plan, copy, d.ids, pages, q, sm_scale, base, x.w, st);
     if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
+    a.join_lse = lse;
   }
-  rc = q8_attn(plan->own.get(), pool, layer, q, out, row_lse, -1, 0, sm_scale, base + x.w.own, x.ids - x.w.own, stream);
-  if (rc != PG_OK || !join) return rc;
-  return shared_join(plan, out, row_lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+  rc = q8_attn(plan->own.get(), pool, layer, q, out, own_lse, -1, 0, sm_scale, base + x.w.own, x.ids - x.w.own, stream,
+               along ? &a : nullptr);
+  if (rc != PG_OK || !join || along) return rc;
+  return shared_join(plan, out, lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
 // Builds *plan (null) or updates it. No exception leaves a C entry: memory that the host cannot give is

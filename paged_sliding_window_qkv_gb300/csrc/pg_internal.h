@@ -126,6 +126,13 @@ struct AttnArgs {
   float* part_o = nullptr;
   float* part_ml = nullptr;
   const int32_t* part_row = nullptr;
+  // decode of a request's own keys beside such parts: the parts of each token's prefix, added by the join
+  // (tok_parts null: none); with `beside` SMs the kernel runs there while the stream's previous kernel,
+  // whose results it does not read, runs on the others
+  const int32_t* tok_parts = nullptr;
+  float* join_lse = nullptr;  // the join's lse (null: not written); `lse` is the own keys' alone
+  int32_t beside = 0;
+  int32_t part_clusters = 0;  // parts: clusters to run on (0: all)
   int* status;
   uint64_t wait_ns;       // limit of the kernels' bounded waits (nanoseconds)
   int32_t test_withhold;  // test hook of pg_test_bounded_wait (0: off)
@@ -173,7 +180,8 @@ struct SharedJoinArgs {
   const float* part_ml;       // [part][num_tokens][Hq][2]
   const int32_t* tok_parts;   // [num_tokens] parts of the token's prefix
   __nv_bfloat16* out;         // [num_tokens][Hq][D]: of the own keys, then of all
-  float* lse;                 // [num_tokens][Hq]: the same
+  const float* own_lse;       // [num_tokens][Hq] of the own keys
+  float* lse;                 // of all (null: not written)
   int32_t num_tokens, num_qo_heads;
 };
 

@@ -393,6 +393,26 @@ def test_scores_that_grow_along_the_keys(D):
     c.close()
 
 
+@pytest.mark.parametrize("D,hq,hkv,n,keys", [(256, 16, 8, 38, 385), (256, 16, 8, 60, 401), (256, 16, 8, 20, 485),
+                                             (256, 16, 4, 40, 385), (256, 16, 1, 76, 385), (512, 16, 1, 152, 385),
+                                             (512, 16, 1, 76, 300), (512, 8, 1, 152, 900), (256, 16, 8, 76, 130)])
+def test_segments_that_end_with_their_ctas(D, hq, hkv, n, keys):
+    """Many equal requests, whose tiles fall to the SMs in whole segments (on 152 of them): a last tile of
+    few keys ends a CTA's work. Repeated, for what depends on timing."""
+    c = Q8Case(D, hq, hkv, [1] * n, [keys - 1] * n, seed=n).build()
+    c.attend()
+    ok()
+    first = c.out.clone()
+    c.reference()
+    c.check_attention()
+    for _ in range(20):
+        c.out.fill_(float("nan"))
+        c.attend()
+        ok()
+        assert torch.equal(c.out, first)
+    c.close()
+
+
 def test_long_cache():
     """Element offsets past 2^31: a pool of 2.4e9 codes, the request's pages at its end."""
     D, hq, hkv, ps = 512, 16, 1, 16
