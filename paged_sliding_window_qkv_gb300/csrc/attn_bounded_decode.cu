@@ -358,6 +358,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     float* const red = reinterpret_cast<float*>(gb + C::OFF_RED);
     float2* const fin = reinterpret_cast<float2*>(gb + C::OFF_FIN);
     float l[NQ], ref[NQ];
+    float my_ref = -INFINITY;  // that of row set_col(lane)
 #pragma unroll
     for (int x = 0; x < NQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
     bool ok = true;
@@ -419,6 +420,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         ++segs;
 #pragma unroll
         for (int x = 0; x < NQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
+        my_ref = -INFINITY;
       }
       const bool vis = (h.mine >> lane) & 1u;
       uint32_t sv[kN];
@@ -455,31 +457,27 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
       }
       if (any4(over)) {
-        // the rows' maximum over the tile, then references with headroom where it outgrew them
-        float mine = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          const float m = warp_max(t[x]);
-          if (lane == x) mine = m;
-        }
-        if (lane < NQ) red[quarter * kN + lane] = mine;
+        // The rows' maxima over the tile, then references with headroom where they were outgrown: lane i
+        // looks after row set_col(i), and every lane takes what it finds. (A reduction, eight loads and a
+        // branch a row took some 8,000 cycles.)
+        const int col = set_col<NQ>(lane);
+        const float mine = warp_reduce<NQ, false>(t, lane);
+        if (lane % (32 / NQ) == 0) red[quarter * kN + col] = mine;
         sync4();
+        const float m = fmaxf(fmaxf(red[col], red[kN + col]), fmaxf(red[2 * kN + col], red[3 * kN + col]));
+        const bool move = m > my_ref + kRescale;
+        const float to = move ? m + kHeadroom : my_ref;
+        // the root of the factor, applied twice: the step may pass 2^-126 (attn_tc.cu)
+        const float root = move && my_ref != -INFINITY ? ex2(0.5f * (my_ref - to)) : 1.f;
+        const bool scaled = __any_sync(0xffffffffu, move && my_ref != -INFINITY);
+        my_ref = to;
         float al[NQ];
-        bool scaled = false;
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
-          const float m = fmaxf(fmaxf(red[x], red[kN + x]), fmaxf(red[2 * kN + x], red[3 * kN + x]));
-          al[x] = 1.f;
-          if (m > ref[x] + kRescale) {
-            const float r2 = m + kHeadroom;
-            if (ref[x] != -INFINITY) {
-              // the root of the factor, applied twice: the step may pass 2^-126 (attn_tc.cu)
-              al[x] = ex2(0.5f * (ref[x] - r2));
-              l[x] = (l[x] * al[x]) * al[x];
-              scaled = true;
-            }
-            ref[x] = r2;
-          }
+          const int from = x * (32 / NQ);
+          ref[x] = __shfl_sync(0xffffffffu, my_ref, from);
+          al[x] = __shfl_sync(0xffffffffu, root, from);
+          l[x] = (l[x] * al[x]) * al[x];
         }
         // O holds the segment's earlier tiles at the old references (uniform over the threads)
         if (scaled && !(h.flags & kFirst)) {

@@ -125,30 +125,6 @@ __device__ __forceinline__ bool any_of(int bar, bool v) {
   return r != 0;
 }
 __device__ __forceinline__ void sync_set(int bar) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(bar) : "memory"); }
-// The warp's maxima (SUM: sums) of CQ values a lane: lane i returns that of value set_col<CQ>(i). Halves
-// the values at each exchange, so CQ of them cost about CQ + log2(32 / CQ) shuffles.
-template <int CQ>
-__device__ __forceinline__ int set_col(int lane) { return lane / (32 / CQ); }
-template <int CQ, bool SUM>
-__device__ __forceinline__ float warp_reduce(const float* x, int lane) {
-  float v[CQ];
-#pragma unroll
-  for (int k = 0; k < CQ; ++k) v[k] = x[k];
-  auto two = [](float p, float q) { return SUM ? p + q : fmaxf(p, q); };
-  int mask = 16;
-#pragma unroll
-  for (int w = CQ; w > 1; w /= 2, mask /= 2) {
-    const bool upper = lane & mask;
-#pragma unroll
-    for (int k = 0; k < w / 2; ++k) {
-      const float got = __shfl_xor_sync(0xffffffffu, upper ? v[k] : v[k + w / 2], mask);
-      v[k] = two(upper ? v[k + w / 2] : v[k], got);
-    }
-  }
-#pragma unroll
-  for (int m = 16 / CQ; m > 0; m /= 2) v[0] = two(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
-  return v[0];
-}
 // Whether the phase of the given parity is over, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;

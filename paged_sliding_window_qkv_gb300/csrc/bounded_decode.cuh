@@ -81,11 +81,30 @@ __device__ __forceinline__ bool any4(bool v) {
   return r != 0;
 }
 __device__ __forceinline__ void sync4() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-// maximum over the warp
-__device__ __forceinline__ float warp_max(float x) {
-  const int32_t b = __float_as_int(x);
-  const int32_t m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7FFFFFFF));
-  return __int_as_float(m ^ ((m >> 31) & 0x7FFFFFFF));
+
+// The warp's maxima (SUM: sums) of CQ values a lane: lane i returns that of value set_col<CQ>(i). Halves
+// the values at each exchange, so CQ of them cost about CQ + log2(32 / CQ) shuffles.
+template <int CQ>
+__device__ __forceinline__ int set_col(int lane) { return lane / (32 / CQ); }
+template <int CQ, bool SUM>
+__device__ __forceinline__ float warp_reduce(const float* x, int lane) {
+  float v[CQ];
+#pragma unroll
+  for (int k = 0; k < CQ; ++k) v[k] = x[k];
+  auto two = [](float p, float q) { return SUM ? p + q : fmaxf(p, q); };
+  int mask = 16;
+#pragma unroll
+  for (int w = CQ; w > 1; w /= 2, mask /= 2) {
+    const bool upper = lane & mask;
+#pragma unroll
+    for (int k = 0; k < w / 2; ++k) {
+      const float got = __shfl_xor_sync(0xffffffffu, upper ? v[k] : v[k + w / 2], mask);
+      v[k] = two(upper ? v[k + w / 2] : v[k], got);
+    }
+  }
+#pragma unroll
+  for (int m = 16 / CQ; m > 0; m /= 2) v[0] = two(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
+  return v[0];
 }
 
 // What the kernel reads may come from the stream's previous kernel, unless it runs beside that one: then

@@ -115,7 +115,7 @@ struct pg_plan {
   // over arrays in `dev` (it owns nothing there), and the prefixes' parts
   std::unique_ptr<pg_plan> own;
   int32_t num_groups = 0, num_parts = 0, room_parts = 0, parts_most = 0, prefix_pages = 0;
-  int32_t beside = 0;  // decode: SMs for the own keys while the others take the parts (0: one after the other)
+  int32_t beside = 0;  // decode: SMs that the parts leave to the own keys (0: one after the other)
   size_t o_part = 0, o_part_row = 0, o_part_live = 0, o_tok_parts = 0, o_pre_pages = 0;
 };
 
@@ -356,13 +356,10 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     if (!all_one) sort_pairs(&ptab2, cta, num_req > 1);
     // How long a part is: every candidate length costs rounds of units over the clusters, each as
     // long as its key tiles (about a microsecond each) and a start and an epilogue worth about five.
-    // A decode step's own keys are a stream of bytes: they run beside the parts, on SMs of their own
-    // (some 80 GB/s each, 6 TB/s together, and some 6 us to begin and end), where that ends sooner.
+    // A decode step's own keys run beside the parts, on SMs left free for them (a CTA takes about 8 us to
+    // begin and end and 6.5 for a tile of 256 KB), where that ends sooner.
     const int32_t heads = Hkv * (D / 256), sms = std::max(2, sm_count());
-    int64_t own_keys = 0;
-    for (int32_t r = 0; r < num_req; ++r) own_keys += (kvp[r + 1] - kvp[r] - 1) * (int64_t)ps + last[r] - kvs2[r];
-    const double own_bytes = (double)own_keys * Hkv * D * 4;
-    auto own_us = [&](int32_t on) { return 6 + own_bytes / std::min(6e6, on * 8e4); };
+    auto own_us = [&](int32_t on) { return 8 + 6.5 * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
     parts_most = num_req > 0 ? most_parts(T, groups->num, cta, heads, sms) : 0;
     const int32_t most_len = pre.empty() ? 0 : *std::max_element(pre.begin(), pre.end());
     const int32_t step = std::max(64, ps);
@@ -374,7 +371,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       int64_t units = 0;
       for (int32_t g = 0; g < groups->num; ++g)
         units += (((int64_t)group_tokens(g) + 2 * cta - 1) / (2 * cta)) * ((pre[g] + len - 1) / len) * heads;
-      for (int32_t on = 0; on <= (all_one ? sms / 2 : 0); on += 8) {  // SMs of the own keys
+      for (int32_t on = 0; on <= (all_one ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
         const int64_t clusters = std::max(1, (sms - on) / 2);
         const double parts_us = (double)((units + clusters - 1) / clusters * (len / 64 + 5));
         const double cost = on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on));

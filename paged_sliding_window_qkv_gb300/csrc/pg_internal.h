@@ -127,7 +127,7 @@ struct AttnArgs {
   float* part_ml = nullptr;
   const int32_t* part_row = nullptr;
   // decode of a request's own keys beside such parts: the parts of each token's prefix, added by the join
-  // (tok_parts null: none); with `beside` SMs the kernel runs there while the stream's previous kernel,
+  // (tok_parts null: none); on `beside` SMs (0: all) the kernel runs while the stream's previous kernel,
   // whose results it does not read, runs on the others
   const int32_t* tok_parts = nullptr;
   float* join_lse = nullptr;  // the join's lse (null: not written); `lse` is the own keys' alone
