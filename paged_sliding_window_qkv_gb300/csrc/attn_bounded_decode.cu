@@ -25,7 +25,8 @@
 //             bytes: 187 against 171 us on 64 requests of 8001 keys at head_dim 512.)
 //   warp 1    MMA issuer: QK of tile i + 1 before PV of tile i, so a tile's softmax has a tile's
 //             load time to finish
-//   warps 2-5 softmax: a thread is a key (TMEM lane); 16 scores, exponentials against a per-row
+//   warps 2-5 softmax: a thread is a key (TMEM lane) and up to 8 query rows (groups above 8 take a second
+//   (7-10)    set of warps: one over 16 rows took as long as a tile's bytes); exponentials against a per-row
 //             reference with 2^64 headroom that moves only when a score outgrows it by 2^48 (so no
 //             maximum is taken across keys in the common tile), P to shared memory; V rows of keys
 //             that are not visible are zeroed (whatever they held); a segment's output leaves one
@@ -48,12 +49,17 @@ namespace pg {
 namespace {
 
 constexpr int kN = 16;                // MMA columns: query rows of the group, padded
-constexpr int kThreadsDec = 224;
 struct alignas(16) TileHdr {
   uint32_t vis[4];  // visible keys
   int32_t rel[16];  // key index (from the request's first key) of each box's first row
   int32_t flags, r, g, tok;
   int64_t slot0;    // slot of the request's first key, counted through the batch's page list
+};
+
+// Softmax warps: sets of four, a set for up to 8 query rows (they share nothing but the tiles).
+template <int NQ>
+struct BdSets {
+  static constexpr int SETS = NQ > 8 ? 2 : 1, CQ = NQ / SETS, THREADS = 224 + 128 * (SETS - 1);
 };
 
 template <int D>
@@ -97,11 +103,11 @@ __device__ __forceinline__ void mma1(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 template <int D, int NQ>
-__global__ void __launch_bounds__(kThreadsDec, 1)
+__global__ void __launch_bounds__(BdSets<NQ>::THREADS, 1)
 bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                       BdArgs args) {
   using C = BdCfg<D>;
-  constexpr int NS = C::NSLOT, PARTS = C::PARTS;
+  constexpr int NS = C::NSLOT, PARTS = C::PARTS, SETS = BdSets<NQ>::SETS;
   const AttnArgs& a = args.a;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
@@ -129,14 +135,14 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       mbar_init(QFULL + 8 * b, 1);
       mbar_init(QEMPTY + 8 * b, 1);
       mbar_init(SFULL + 8 * b, 1);
-      mbar_init(SFREE + 8 * b, 4);
-      mbar_init(PFULL + 8 * b, 4);
+      mbar_init(SFREE + 8 * b, 4 * SETS);
+      mbar_init(PFULL + 8 * b, 4 * SETS);
       mbar_init(PVDONE + 8 * b, 1);
-      mbar_init(OFREE + 8 * b, 4);
+      mbar_init(OFREE + 8 * b, 4 * SETS);
     }
     for (int h = 0; h < kHdrs; ++h) {
       mbar_init(HFULL + 8 * h, 1);
-      mbar_init(HEMPTY + 8 * h, 5);  // the softmax warps and the MMA issuer
+      mbar_init(HEMPTY + 8 * h, 4 * SETS + 1);  // the softmax warps and the MMA issuer
     }
     mbar_init(DRAIN, 1);
     *abort_flag = 0;
@@ -352,15 +358,19 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   } else {
     // ------------------------------------------------------------ softmax
     wait_previous(a);
+    constexpr int CQ = BdSets<NQ>::CQ;
+    const int set = warp > 6 ? 1 : 0, bar = 1 + set;
+    const int x0 = set * CQ;  // the set's first query row
+    const int32_t Gs = min(max(G - x0, 0), CQ);  // rows of the group in the set
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;  // the thread's key of each tile, and output column of 128
-    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
-    float* const red = reinterpret_cast<float*>(gb + C::OFF_RED);
-    float2* const fin = reinterpret_cast<float2*>(gb + C::OFF_FIN);
-    float l[NQ], ref[NQ];
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16) + x0;
+    float* const red = reinterpret_cast<float*>(gb + C::OFF_RED) + x0;
+    float2* const fin = reinterpret_cast<float2*>(gb + C::OFF_FIN) + x0;
+    float l[CQ], ref[CQ];
     float my_ref = -INFINITY;  // that of row set_col(lane)
 #pragma unroll
-    for (int x = 0; x < NQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
+    for (int x = 0; x < CQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
     bool ok = true;
     int32_t segs = 0;
     // the segment whose output is still to leave
@@ -372,26 +382,26 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         return;
       }
       tc_fence_after();
-      const int64_t row0 = (int64_t)p_tok * Hq + (int64_t)p_g * G;
-      const int64_t rec = ((int64_t)blockIdx.x * 2 + ((p_flags & kRec1) ? 1 : 0)) * G;
-      float inv[NQ];
+      const int64_t row0 = (int64_t)p_tok * Hq + (int64_t)p_g * G + x0;
+      const int64_t rec = ((int64_t)blockIdx.x * 2 + ((p_flags & kRec1) ? 1 : 0)) * G + x0;
+      float inv[CQ];
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) inv[x] = fin[x].x == 0.f ? 0.f : 1.f / fin[x].x;
+      for (int x = 0; x < CQ; ++x) inv[x] = fin[x].x == 0.f ? 0.f : 1.f / fin[x].x;
 #pragma unroll 1
       for (int p = 0; p < D / 128; ++p) {
-        uint32_t o[kN];
-        tmem_ld16(tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * kN, o);
+        uint32_t o[8];
+        tmem_ld8(tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * kN, o);
         tmem_wait_ld();
         const int d = p * 128 + row;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          if (x >= G) break;
+        for (int x = 0; x < CQ; ++x) {
+          if (x >= Gs) break;
           const float v = inv[x] == 0.f ? 0.f : __uint_as_float(o[x]) * inv[x];
           if (p_flags & kSplit) args.rec_o[(rec + x) * D + d] = v;
           else a.out[(row0 + x) * D + d] = __float2bfloat16_rn(v);
         }
       }
-      if (row < G) {
+      if (row < Gs) {
         const float2 f = fin[row];
         if (p_flags & kSplit) *reinterpret_cast<float2*>(args.rec_ml + (rec + row) * 2) = make_float2(f.y, f.x);
         else if (a.lse) a.lse[row0 + row] = f.x != 0.f ? (f.y + log2f(f.x)) * kLn2f : -INFINITY;
@@ -413,19 +423,19 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         h.mine = x.vis[quarter];
         h.all = x.vis[0] & x.vis[1] & x.vis[2] & x.vis[3];
       }
-      if (any4(!ok)) break;  // all four warps leave together
+      if (any_of(bar, !ok)) break;  // all four warps leave together
       if (h.flags & kEmpty) break;
       ok = __all_sync(0xffffffffu, mbar_wait_inline(SFULL + 8 * b, (i >> 1) & 1, wc));
       if (h.flags & kFirst) {
         ++segs;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
+        for (int x = 0; x < CQ; ++x) { l[x] = 0.f; ref[x] = -INFINITY; }
         my_ref = -INFINITY;
       }
       const bool vis = (h.mine >> lane) & 1u;
-      uint32_t sv[kN];
+      uint32_t sv[8];
       tc_fence_after();
-      tmem_ld16(tl + C::TM_S + b * kN, sv);
+      tmem_ld8(tl + C::TM_S + b * kN, sv);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -433,37 +443,37 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         mbar_arrive(SFREE + 8 * b);
         mbar_arrive(HEMPTY + 8 * hb);
       }
-      float t[NQ];
+      float t[CQ];
       bool over = false;
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) {
+      for (int x = 0; x < CQ; ++x) {
         t[x] = vis ? __uint_as_float(sv[x]) * a.sm_scale_log2 : -INFINITY;
         over |= t[x] > ref[x] + kRescale;
       }
       if (a.logits && vis) {
         if (h.slot < a.logit_slots) {
-          float* dst = a.logits + h.slot * Hq + h.g * G;
-          if (NQ % 4 == 0 && G == NQ) {
+          float* dst = a.logits + h.slot * Hq + h.g * G + x0;
+          if (CQ % 4 == 0 && G == NQ) {
 #pragma unroll
-            for (int x = 0; x + 3 < NQ; x += 4)
+            for (int x = 0; x + 3 < CQ; x += 4)
               *reinterpret_cast<float4*>(dst + x) = make_float4(t[x], t[x + 1], t[x + 2], t[x + 3]);
           } else {
 #pragma unroll
-            for (int x = 0; x < NQ; ++x)
-              if (x < G) dst[x] = t[x];
+            for (int x = 0; x < CQ; ++x)
+              if (x < Gs) dst[x] = t[x];
           }
         } else {
           atomicOr(a.status, kStatusBounds);
         }
       }
-      if (any4(over)) {
+      if (any_of(bar, over)) {
         // The rows' maxima over the tile, then references with headroom where they were outgrown: lane i
         // looks after row set_col(i), and every lane takes what it finds. (A reduction, eight loads and a
         // branch a row took some 8,000 cycles.)
-        const int col = set_col<NQ>(lane);
-        const float mine = warp_reduce<NQ, false>(t, lane);
-        if (lane % (32 / NQ) == 0) red[quarter * kN + col] = mine;
-        sync4();
+        const int col = set_col<CQ>(lane);
+        const float mine = warp_reduce<CQ, false>(t, lane);
+        if (lane % (32 / CQ) == 0) red[quarter * kN + col] = mine;
+        sync_set(bar);
         const float m = fmaxf(fmaxf(red[col], red[kN + col]), fmaxf(red[2 * kN + col], red[3 * kN + col]));
         const bool move = m > my_ref + kRescale;
         const float to = move ? m + kHeadroom : my_ref;
@@ -471,10 +481,10 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const float root = move && my_ref != -INFINITY ? ex2(0.5f * (my_ref - to)) : 1.f;
         const bool scaled = __any_sync(0xffffffffu, move && my_ref != -INFINITY);
         my_ref = to;
-        float al[NQ];
+        float al[CQ];
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
-          const int from = x * (32 / NQ);
+        for (int x = 0; x < CQ; ++x) {
+          const int from = x * (32 / CQ);
           ref[x] = __shfl_sync(0xffffffffu, my_ref, from);
           al[x] = __shfl_sync(0xffffffffu, root, from);
           l[x] = (l[x] * al[x]) * al[x];
@@ -486,29 +496,29 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             tc_fence_after();
 #pragma unroll 1
             for (int p = 0; p < D / 128; ++p) {
-              uint32_t o[kN];
+              uint32_t o[8];
               const uint32_t at = tl + C::TM_O + ((segs - 1) & 1) * C::O_COLS + p * kN;
-              tmem_ld16(at, o);
+              tmem_ld8(at, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < NQ; ++x) o[x] = __float_as_uint((__uint_as_float(o[x]) * al[x]) * al[x]);
-              tmem_st16(at, o);
+              for (int x = 0; x < CQ; ++x) o[x] = __float_as_uint((__uint_as_float(o[x]) * al[x]) * al[x]);
+              tmem_st8(at, o);
             }
             tmem_wait_st();
           } else {
             ok = false;
           }
         }
-        sync4();  // red has been read
+        sync_set(bar);  // red has been read
       }
       // the P buffer is free once PV(i - 2) has read it
       ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(PVDONE + 8 * b, ((i >> 1) & 1) ^ 1, wc));
       unsigned char* const pp = gb + C::OFF_P + b * C::P_BYTES + (row >> 6) * (kN * 128) + (row & 7) * 2;
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) {
+      for (int x = 0; x < CQ; ++x) {
         const float e = ex2(t[x] - (ref[x] == -INFINITY ? 0.f : ref[x]));
         l[x] += e;
-        *reinterpret_cast<__nv_bfloat16*>(pp + x * 128 + ((((row >> 3) & 7) ^ (x & 7)) << 4)) =
+        *reinterpret_cast<__nv_bfloat16*>(pp + (x0 + x) * 128 + ((((row >> 3) & 7) ^ (x & 7)) << 4)) =
             __float2bfloat16_rn(e);
       }
       if (h.all != 0xFFFFFFFFu) {
@@ -530,9 +540,12 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           ok = ok && __all_sync(0xffffffffu, mbar_wait_inline(FULL(sl), (at / NS) & 1, wc));
           if (ok && !vis) {
             unsigned char* v = gb + sl * C::SLOT + (row >> 3) * (C::NC * 1024) + (row & 7) * 128;
+            constexpr int N16 = 8 * C::NC / SETS;  // (the sets share the row)
 #pragma unroll
-            for (int c = 0; c < 8 * C::NC; ++c)
+            for (int k = 0; k < N16; ++k) {
+              const int c = set * N16 + k;
               *reinterpret_cast<uint4*>(v + (c >> 3) * 1024 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
         }
       }
@@ -546,18 +559,18 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         // the row sums over the 128 keys of every tile, and the references, for the epilogue
         float mine = 0.f;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x) {
+        for (int x = 0; x < CQ; ++x) {
           float s = l[x];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
           if (lane == x) mine = s;
         }
-        if (lane < NQ) red[quarter * kN + lane] = mine;
-        sync4();
+        if (lane < CQ) red[quarter * kN + lane] = mine;
+        sync_set(bar);
 #pragma unroll
-        for (int x = 0; x < NQ; ++x)
+        for (int x = 0; x < CQ; ++x)
           if (row == x) fin[x] = make_float2((red[x] + red[kN + x]) + (red[2 * kN + x] + red[3 * kN + x]), ref[x]);
-        sync4();
+        sync_set(bar);
         pending = true;
         p_tile = i;
         p_flags = h.flags;
@@ -638,7 +651,7 @@ __host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D,
   return (group * D * RG + 511) / 512;
 }
 template <int D, int RG, bool PARTS>
-__global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
+__global__ void __launch_bounds__(kJoinThreads, PARTS ? 5 : 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
   const AttnArgs& a = args.a;
   // (a following kernel launched programmatically may set up; it waits for this one)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -951,7 +964,7 @@ cudaError_t launch_bd(const AttnArgs& a, cudaStream_t stream) {
   // programmatic serialisation: the CTAs' set-up overlaps the end of the stream's previous kernel
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)S, 1, 1);
-  cfg.blockDim = dim3(kThreadsDec, 1, 1);
+  cfg.blockDim = dim3(BdSets<NQ>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -107,24 +107,6 @@ __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_
       "l"(a), "l"(b), "r"(acc), "n"(IDESC)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : PG_R8(0) : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), PG_W8(0)
-               : "memory");
-}
-// barriers among the 128 threads of a softmax set
-__device__ __forceinline__ bool any_of(int bar, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u), "r"(bar)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void sync_set(int bar) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(bar) : "memory"); }
 // Whether the phase of the given parity is over, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;

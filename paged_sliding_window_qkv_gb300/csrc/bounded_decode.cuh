@@ -57,31 +57,24 @@ __device__ __forceinline__ void commit1(uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : PG_R8(0), PG_R8(8)
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : PG_R8(0) : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      PG_W8(0), PG_W8(8)
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), PG_W8(0)
+               : "memory");
 }
-// barriers among the 128 softmax threads
-__device__ __forceinline__ bool any4(bool v) {
+// barriers among the 128 threads of a softmax set
+__device__ __forceinline__ bool any_of(int bar, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(v ? 1u : 0u)
+      : "r"(v ? 1u : 0u), "r"(bar)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void sync4() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
+__device__ __forceinline__ void sync_set(int bar) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(bar) : "memory"); }
 // The warp's maxima (SUM: sums) of CQ values a lane: lane i returns that of value set_col<CQ>(i). Halves
 // the values at each exchange, so CQ of them cost about CQ + log2(32 / CQ) shuffles.
 template <int CQ>
