@@ -332,6 +332,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const uint32_t tmem = *tmem_slot;
   // BC: the pass that accumulates weights may start on SMs that this one has left (it waits for
   // this grid's completion before it reads lse)
+  // (PART: the set-up above overlaps the end of the stream's previous kernel; the own keys' decode, which
+  // does not wait for this grid, may start once that kernel has ended)
+  if constexpr (PART) asm volatile("griddepcontrol.wait;" ::: "memory");
   if constexpr (BC) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 || warp == 10) {
@@ -1317,13 +1320,15 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreadsTc, 1, 1);
   cfg.dynamicSmemBytes = TcCfg<DQK>::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = PART ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, BC, PART>, tq, tkv, tv, t);
   if (e != cudaSuccess) return e;
   count_launch();

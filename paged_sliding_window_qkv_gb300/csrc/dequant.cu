@@ -45,20 +45,26 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(DequantArgs a) {
   const int32_t kvh = (int32_t)(task % heads);
   const int32_t i = (int32_t)(task / heads % NP), layer = (int32_t)(task / heads / NP);
   const PlanDev& pl = a.plan;
-  if (i >= (a.whole ? *a.whole : pl.kv_page_indptr[pl.num_req])) return;  // room behind the list
-  if (a.list && kvh == 0 && lane == 0) a.ids[i] = i;
-  const int32_t page = pl.page_ids[i];
+  // (launched programmatically: the plan, which copies alone write, is looked at while the stream's
+  // previous kernel ends; every warp then waits for that kernel, whatever it has to do)
+  bool skip = i >= (a.whole ? *a.whole : pl.kv_page_indptr[pl.num_req]);  // room behind the list
+  const int32_t page = skip ? -1 : pl.page_ids[i];
   int32_t rows = ps;  // slots of the page that hold keys
-  if (!a.whole) {
+  bool seen = true;
+  if (!skip && !a.whole) {
     const int32_t r = request_of(pl, i, lane);
     if (i + 1 == pl.kv_page_indptr[r + 1]) rows = min(ps, pl.last_page_len[r]);
     if (a.list && a.window_left >= 0) {
       // a page that lies between the sinks and the first query's window is not read
       const int64_t first = (int64_t)pl.kv_start[r] + (int64_t)(i - pl.kv_page_indptr[r]) * ps;
       const int64_t lo = (int64_t)pl.start_pos[r] - a.window_left;
-      if (first + ps <= lo && first >= a.num_sink) return;
+      seen = first + ps > lo || first < a.num_sink;
     }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (skip) return;
+  if (a.list && kvh == 0 && lane == 0) a.ids[i] = i;
+  if (!seen) return;
   const bool good = page >= 0 && page < a.num_pages;
   if (!good) {
     if (lane == 0) atomicOr(a.status, kStatusBounds);
@@ -99,8 +105,18 @@ cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t stream) {
   const int64_t tasks = (int64_t)a.num_layers * a.plan.num_page_ids * 2 * a.num_kv_heads;
   if (tasks == 0) return cudaSuccess;
   const unsigned grid = (unsigned)((tasks + kWarps - 1) / kWarps);
-  if (a.head_dim == 256) dequant_kernel<256><<<grid, kWarps * 32, 0, stream>>>(a);
-  else dequant_kernel<512><<<grid, kWarps * 32, 0, stream>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = a.head_dim == 256 ? cudaLaunchKernelEx(&cfg, dequant_kernel<256>, a)
+                                          : cudaLaunchKernelEx(&cfg, dequant_kernel<512>, a);
+  if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }

@@ -241,6 +241,8 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
   auto FULL = [&](int s) { return bars + 8u * s; };
   auto EMPTY = [&](int s) { return bars + 8u * (nst + s); };
 
+  // (launched programmatically: the set-up and the producer's look at the plan, which copies alone
+  // write, overlap the end of the stream's previous kernel; all else waits for it)
   const int32_t T = a.plan.num_tokens, G = gridDim.x;
   const int32_t count = T > (int32_t)blockIdx.x ? (T - 1 - (int32_t)blockIdx.x) / G + 1 : 0;
   if (threadIdx.x == 0) {
@@ -271,6 +273,7 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
         m.ok = 0;
         atomicOr(a.status, kStatusBounds);
       }
+      if (kb == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int i = 0; i < n; ++i) {
         const int32_t k = kb + i;
         const int st = k % nst;
@@ -326,6 +329,7 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
     const float inv_d = 1.0f / (float)D;
     // this lane's weights (Q and K) as fp32 pairs, loaded once
     float2 wqa[4], wqb[4], wka[4], wkb[4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     {
       const uint4 qa = __ldg(reinterpret_cast<const uint4*>(a.w_q) + j);
       const uint4 qb = __ldg(reinterpret_cast<const uint4*>(a.w_q + D / 2) + j);
@@ -391,9 +395,11 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
             if (D == 512) store_plain(x, inv, dst + a.pool.stride_kv, j, D2);
           }
         }
-        // V rows of head_dim 256 (weightless, never rotated)
+        // V rows of head_dim 256 (weightless, never rotated), from the warp behind the last K row's on: with
+        // 8 KV heads the first four warps take the K rows, the others the V rows
         if (D == 256) {
-          for (int r0 = cw * RPW; r0 < Hkv; r0 += kPrepConsumerWarps * RPW) {
+          const int behind = (cw + kPrepConsumerWarps - (Hkv + RPW - 1) / RPW % kPrepConsumerWarps) % kPrepConsumerWarps;
+          for (int r0 = behind * RPW; r0 < Hkv; r0 += kPrepConsumerWarps * RPW) {
             const int r = r0 + sub;
             const bool live = r < Hkv;
             RowIn x;
@@ -412,6 +418,7 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
       if (lane == 0) bar_arrive(EMPTY(st));
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ----------------------------------------------------------------------------- rotary table
@@ -481,7 +488,17 @@ cudaError_t launch_prep(const PrepArgs& a, cudaStream_t stream) {
     cached_stage = stage;
   }
   const int64_t ctas = std::min<int64_t>((int64_t)sms * per_sm, T);
-  prep_kernel<D, Q8><<<(unsigned)ctas, kPrepThreads, smem, stream>>>(a, nst, stage);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kPrepThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, prep_kernel<D, Q8>, a, nst, stage)) != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
 }

@@ -37,17 +37,21 @@ __device__ __forceinline__ int32_t q8_exponent(float2* y) {
     for (int k = 0; k < N; ++k) m = fmaxf(m, fmaxf(fabsf(y[k].x), fabsf(y[k].y)));  // (a NaN is passed over)
     return m;
   };
-  float m = largest();
-  if (m == INFINITY) {
+  auto reduced = [&]() {
+    float m = largest();
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+  };
+  float m = reduced();
+  if (__any_sync(0xffffffffu, m == INFINITY)) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       if (fabsf(y[k].x) == INFINITY) y[k].x = NAN;
       if (fabsf(y[k].y) == INFINITY) y[k].y = NAN;
     }
-    m = largest();
+    m = reduced();
   }
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   return q8_exponent_of(m);
 }
 
