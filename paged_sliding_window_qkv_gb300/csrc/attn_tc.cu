@@ -139,7 +139,7 @@ struct TcArgs {
   float scale_log2;
   float* lse;  // optional [T][Hq] natural-log normaliser of each row (null: not written)
   // PART: records of a pair-table entry's token t at row part_row[entry] + t: mean [row][Hq][D] and
-  // (reference, sum) [row][Hq][2]
+  // (reference, sum) [row][Hq][2]; part_o is 32-byte aligned
   float* part_o;
   float* part_ml;
   const int32_t* part_row;
@@ -1107,9 +1107,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = ntiles == 0 ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
 #pragma unroll
-              for (int k = 0; k < 8; ++k)  // (a workspace is 16-byte aligned)
-                *reinterpret_cast<uint4*>(dst + c * 32 + 4 * k) =
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 4; ++k)  // whole 32-byte sectors
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + c * 32 + 8 * k),
+                             "r"(o[8 * k]), "r"(o[8 * k + 1]), "r"(o[8 * k + 2]), "r"(o[8 * k + 3]),
+                             "r"(o[8 * k + 4]), "r"(o[8 * k + 5]), "r"(o[8 * k + 6]), "r"(o[8 * k + 7])
+                             : "memory");
             }
           }
         } else {

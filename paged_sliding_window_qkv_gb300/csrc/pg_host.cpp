@@ -135,6 +135,8 @@ void free_stage(PlanStage* st) {
   }
 }
 
+constexpr int32_t kPartEnds = 8;
+
 // Groups of consecutive requests that share their first keys.
 struct Groups {
   int32_t num = 0;
@@ -355,7 +357,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     }
     if (!all_one) sort_pairs(&ptab2, cta, num_req > 1);
     // How long a part is: every candidate length costs rounds of units over the clusters, each as
-    // long as its key tiles (about a microsecond each) and a start and an epilogue worth about five.
+    // long as its key tiles (about a microsecond each) and a start and an epilogue worth kPartEnds.
     // A decode step's own keys run beside the parts, on SMs left free for them (a CTA takes about 8 us to
     // begin and end and 6.5 for a tile of 256 KB), where that ends sooner.
     const int32_t heads = Hkv * (D / 256), sms = std::max(2, sm_count());
@@ -364,20 +366,24 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     const int32_t most_len = pre.empty() ? 0 : *std::max_element(pre.begin(), pre.end());
     const int32_t step = std::max(64, ps);
     auto group_tokens = [&](int32_t g) { return qo[groups->indptr[g + 1]] - qo[groups->indptr[g]]; };
+    // Steps (of 64 keys, or a page) of the longest part; a group is cut into as few parts of one length.
+    int32_t longest = 1;
     double best = 0;
-    int32_t run = step;
-    for (int32_t k = 1; k <= parts_most && most_len > 0; ++k) {
-      const int64_t len = ((int64_t)most_len + (int64_t)k * step - 1) / ((int64_t)k * step) * step;
+    const int64_t most_steps = ((int64_t)most_len + step - 1) / step;
+    const int64_t least = parts_most > 0 ? (most_steps + parts_most - 1) / parts_most : 0;
+    auto group_steps = [&](int32_t g) { return ((int64_t)pre[g] + step - 1) / step; };
+    const int64_t stride = std::max<int64_t>(1, (most_steps - least) / 256);
+    for (int64_t len = std::max<int64_t>(least, 1); len <= most_steps; len += stride) {
       int64_t units = 0;
       for (int32_t g = 0; g < groups->num; ++g)
-        units += (((int64_t)group_tokens(g) + 2 * cta - 1) / (2 * cta)) * ((pre[g] + len - 1) / len) * heads;
+        units += (((int64_t)group_tokens(g) + 2 * cta - 1) / (2 * cta)) * ((group_steps(g) + len - 1) / len) * heads;
       for (int32_t on = 0; on <= (all_one ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
         const int64_t clusters = std::max(1, (sms - on) / 2);
-        const double parts_us = (double)((units + clusters - 1) / clusters * (len / 64 + 5));
+        const double parts_us = (double)((units + clusters - 1) / clusters * (len * step / 64 + kPartEnds));
         const double cost = on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on));
-        if ((k == 1 && on == 0) || cost < best) {
+        if (best == 0 || cost < best) {
           best = cost;
-          run = (int32_t)std::min<int64_t>(len, INT32_MAX - 1024);
+          longest = (int32_t)len;
           beside = on;
         }
       }
@@ -385,9 +391,11 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     tok_parts.assign((size_t)T, 0);
     for (int32_t g = 0; g < groups->num; ++g) {
       const int32_t q0 = qo[groups->indptr[g]], len = group_tokens(g), at = kvp[groups->indptr[g]];
-      const int32_t parts = (int32_t)(((int64_t)pre[g] + run - 1) / run);
+      const int32_t parts = (int32_t)((group_steps(g) + longest - 1) / longest);
+      const int32_t run = parts > 0 ? (int32_t)((group_steps(g) + parts - 1) / parts) * step : step;
       pre_pages.insert(pre_pages.end(), page_ids + at, page_ids + at + pre[g] / ps);
       for (int32_t i = 0; i < parts; ++i) {
+        if ((int64_t)i * run >= pre[g]) break;  // (rounded up, fewer parts may do)
         const int32_t k0 = i * run, k1 = (int32_t)std::min<int64_t>((int64_t)k0 + run, pre[g]);
         const size_t before = part.size();
         // (a row stands behind the whole prefix, so it sees every key of the run)
@@ -395,11 +403,25 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
         if (!fits_i32((int64_t)i * T)) return PG_ERR_I32_OVERFLOW;
         part_row.resize(part_row.size() + (part.size() - before) / 8, i * T);
       }
-      std::fill(tok_parts.begin() + q0, tok_parts.begin() + q0 + len, parts);
+      const int32_t cut = parts > 0 ? (int32_t)(((int64_t)pre[g] + run - 1) / run) : 0;
+      std::fill(tok_parts.begin() + q0, tok_parts.begin() + q0 + len, cut);
       pre_total += pre[g] / ps;
     }
     if (!fits_i32((int64_t)(part.size() / 8) * heads)) return PG_ERR_I32_OVERFLOW;
     num_parts = (int32_t)(part.size() / 8);
+    {
+      // the longest first, as in the pair table
+      std::vector<int32_t> order((size_t)num_parts), tab(part.size()), rows((size_t)num_parts);
+      for (int32_t i = 0; i < num_parts; ++i) order[i] = i;
+      auto keys = [&](int32_t i) { return part[8 * (size_t)i + 6] - part[8 * (size_t)i + 7]; };
+      std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return keys(x) > keys(y); });
+      for (int32_t i = 0; i < num_parts; ++i) {
+        std::copy_n(part.data() + 8 * (size_t)order[i], 8, tab.data() + 8 * (size_t)i);
+        rows[i] = part_row[order[i]];
+      }
+      part.swap(tab);
+      part_row.swap(rows);
+    }
     // room for what any batch of as many groups, requests, tokens and pages needs
     room_parts = num_req > 0 ? (groups->num + (T - groups->num) / (2 * cta)) * parts_most : 0;
     part.resize((size_t)room_parts * 8, 0);
@@ -1146,10 +1168,16 @@ bool shared_ws(const pg_plan* p, size_t own_bytes, SharedWs* w) {
   w->bytes = w->own + own_bytes;
   return true;
 }
+// A workspace is 16-byte aligned, the records 256: the offsets count from here.
+constexpr size_t kSharedPad = 256;
+unsigned char* shared_base(void* ws) {
+  return reinterpret_cast<unsigned char*>(((uintptr_t)ws + kSharedPad - 1) & ~(uintptr_t)(kSharedPad - 1));
+}
 size_t shared_workspace_bytes(const pg_plan* p) {
   if (!p || !p->own || p->num_req == 0) return 0;
   SharedWs w;
-  return shared_ws(p, std::max(workspace_bytes(p->own.get()), bounded_ws_bytes(p->own.get())), &w) ? w.bytes : SIZE_MAX;
+  return shared_ws(p, std::max(workspace_bytes(p->own.get()), bounded_ws_bytes(p->own.get())), &w) ? w.bytes + kSharedPad
+                                                                                                    : SIZE_MAX;
 }
 
 // The prefixes' parts: pool pages `page_ids` (device, prefix by prefix) of `pool`.
@@ -1222,13 +1250,14 @@ int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const
   if (plan->num_tokens == 0) return PG_OK;
   const pg_plan* own = plan->own.get();
   SharedWs w;
-  if (!shared_ws(plan, std::max(workspace_bytes(own), bounded_ws_bytes(own)), &w) || !ws || ws_bytes < w.bytes)
+  if (!shared_ws(plan, std::max(workspace_bytes(own), bounded_ws_bytes(own)), &w) || !ws || ws_bytes < w.bytes + kSharedPad)
     return PG_ERR_WORKSPACE;
   if (!aligned16(ws)) return PG_ERR_ALIGN;
+  ws_bytes -= kSharedPad;
   int err = PG_OK;
   int* st = status_word(&err);
   if (!st) return err;
-  unsigned char* const base = static_cast<unsigned char*>(ws);
+  unsigned char* const base = shared_base(ws);
   const bool join = plan->num_parts > 0 || capturing(stream);
   float* const own_lse = join ? reinterpret_cast<float*>(base + w.lse) : lse;
   Bounded b;
@@ -1265,7 +1294,7 @@ bool shared_q8_ws(const pg_plan* p, SharedQ8Ws* x) {
 size_t shared_q8_workspace_bytes(const pg_plan* p) {
   if (!p || !p->own || p->num_req == 0) return 0;
   SharedQ8Ws x;
-  return shared_q8_ws(p, &x) ? x.w.bytes : SIZE_MAX;
+  return shared_q8_ws(p, &x) ? x.w.bytes + kSharedPad : SIZE_MAX;
 }
 
 int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
@@ -1276,9 +1305,10 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
   const int32_t D = plan->head_dim, ps = plan->page_size, H = plan->num_kv_heads;
   if (plan->num_tokens == 0) return PG_OK;
   SharedQ8Ws x;
-  if (!shared_q8_ws(plan, &x) || !ws || ws_bytes < x.w.bytes) return PG_ERR_WORKSPACE;
+  if (!shared_q8_ws(plan, &x) || !ws || ws_bytes < x.w.bytes + kSharedPad) return PG_ERR_WORKSPACE;
   if (!aligned16(ws)) return PG_ERR_ALIGN;
-  unsigned char* const base = static_cast<unsigned char*>(ws);
+  ws_bytes -= kSharedPad;
+  unsigned char* const base = shared_base(ws);
   // a captured call's prefixes may come to hold as many pages as the workspace has room for
   const bool captured = capturing(stream);
   const int64_t room = captured ? (int64_t)((ws_bytes - x.pages) / x.page_bytes) : std::max(plan->prefix_pages, 1);
