@@ -651,7 +651,7 @@ __host__ __device__ __forceinline__ int32_t join_parts(int32_t group, int32_t D,
   return (group * D * RG + 511) / 512;
 }
 template <int D, int RG, bool PARTS>
-__global__ void __launch_bounds__(kJoinThreads, PARTS ? 5 : 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
+__global__ void __launch_bounds__(kJoinThreads, 7) bounded_join_kernel(BdArgs args, int32_t S, int32_t key_blocks) {
   const AttnArgs& a = args.a;
   // (a following kernel launched programmatically may set up; it waits for this one)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -717,11 +717,12 @@ __global__ void __launch_bounds__(kJoinThreads, PARTS ? 5 : 7) bounded_join_kern
       for (int k = 0; k < kJoinRecs; ++k) add(ml[k].x, ml[k].y, v[k], true);
     }
     if constexpr (PARTS) {
-      for (int32_t c0 = rg; row < G && c0 < num_parts; c0 += RG * kJoinRecs) {
-        float2 ml[kJoinRecs];
-        float4 v[kJoinRecs];
+      constexpr int kParts = kJoinRecs / 2;  // (as many registers as the blocks of 7 to an SM have)
+      for (int32_t c0 = rg; row < G && c0 < num_parts; c0 += RG * kParts) {
+        float2 ml[kParts];
+        float4 v[kParts];
 #pragma unroll
-        for (int k = 0; k < kJoinRecs; ++k) {
+        for (int k = 0; k < kParts; ++k) {
           const int32_t c = c0 + RG * k;
           const int64_t at = c * part_rows + row0 + row;
           ml[k] = c < num_parts ? *reinterpret_cast<const float2*>(a.part_ml + 2 * at) : make_float2(-INFINITY, 0.f);
@@ -729,7 +730,7 @@ __global__ void __launch_bounds__(kJoinThreads, PARTS ? 5 : 7) bounded_join_kern
                                : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int k = 0; k < kJoinRecs; ++k) add(ml[k].x, ml[k].y, v[k], true);
+        for (int k = 0; k < kParts; ++k) add(ml[k].x, ml[k].y, v[k], true);
       }
       if (mine && direct && q.total > 0) {
         const float own = a.lse[row0 + row];

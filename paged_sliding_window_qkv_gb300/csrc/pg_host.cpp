@@ -85,6 +85,13 @@ struct PlanStage {
   int next = 0;
 };
 
+// The parts that a plan's prefixes are cut into.
+struct PartSet {
+  int32_t num = 0;
+  int32_t beside = 0;  // decode: SMs that the parts leave to the own keys (0: one after the other)
+  size_t o_tab = 0, o_row = 0, o_live = 0, o_tok = 0;  // pair table, record rows, counts, parts of each token
+};
+
 struct pg_plan {
   int32_t num_req = 0, num_tokens = 0, num_qo_heads = 0, num_kv_heads = 0, head_dim = 0,
           page_size = 0;
@@ -114,9 +121,9 @@ struct pg_plan {
   // shared prefixes (pg_plan_paged_shared; null otherwise): the requests' own keys as a segment plan
   // over arrays in `dev` (it owns nothing there), and the prefixes' parts
   std::unique_ptr<pg_plan> own;
-  int32_t num_groups = 0, num_parts = 0, room_parts = 0, parts_most = 0, prefix_pages = 0;
-  int32_t beside = 0;  // decode: SMs that the parts leave to the own keys (0: one after the other)
-  size_t o_part = 0, o_part_row = 0, o_part_live = 0, o_tok_parts = 0, o_pre_pages = 0;
+  int32_t num_groups = 0, room_parts = 0, parts_most = 0, prefix_pages = 0;
+  size_t o_pre_pages = 0;
+  PartSet parts[2];  // over a bf16 pool, and over an 8-bit one
 };
 
 namespace {
@@ -325,8 +332,12 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   const int32_t live[2] = {(int32_t)nwork, npairs};
 
   // Shared prefixes: the requests' own keys as segments, and the parts of each group's prefix.
-  std::vector<int32_t> kvp2, kvs2, pages2, ptab2, part, part_row, tok_parts, pre_pages;
-  int32_t seen2 = 0, num_parts = 0, room_parts = 0, parts_most = 0, pre_total = 0, beside = 0;
+  struct Parts {
+    std::vector<int32_t> tab, row, tok;
+    int32_t num = 0, beside = 0;
+  } parts[2];
+  std::vector<int32_t> kvp2, kvs2, pages2, ptab2, pre_pages;
+  int32_t seen2 = 0, room_parts = 0, parts_most = 0;
   int64_t tiles2 = 0;
   if (groups) {
     if (!attn_tc_supported(D, group, ps) || cta <= 0) return PG_ERR_PLAN_MISMATCH;
@@ -354,83 +365,83 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
                   (int32_t)len);
       }
       pre[g] = (int32_t)len;
+      pre_pages.insert(pre_pages.end(), page_ids + kvp[r0], page_ids + kvp[r0] + len / ps);
     }
     if (!all_one) sort_pairs(&ptab2, cta, num_req > 1);
-    // How long a part is: every candidate length costs rounds of units over the clusters, each as
-    // long as its key tiles (about a microsecond each) and a start and an epilogue worth kPartEnds.
-    // A decode step's own keys run beside the parts, on SMs left free for them (a CTA takes about 8 us to
-    // begin and end and 6.5 for a tile of 256 KB), where that ends sooner.
-    const int32_t heads = Hkv * (D / 256), sms = std::max(2, sm_count());
-    auto own_us = [&](int32_t on) { return 8 + 6.5 * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
+    const int32_t heads = Hkv * (D / 256), sms = std::max(2, sm_count()), step = std::max(64, ps);
     parts_most = num_req > 0 ? most_parts(T, groups->num, cta, heads, sms) : 0;
-    const int32_t most_len = pre.empty() ? 0 : *std::max_element(pre.begin(), pre.end());
-    const int32_t step = std::max(64, ps);
-    auto group_tokens = [&](int32_t g) { return qo[groups->indptr[g + 1]] - qo[groups->indptr[g]]; };
-    // Steps (of 64 keys, or a page) of the longest part; a group is cut into as few parts of one length.
-    int32_t longest = 1;
-    double best = 0;
-    const int64_t most_steps = ((int64_t)most_len + step - 1) / step;
-    const int64_t least = parts_most > 0 ? (most_steps + parts_most - 1) / parts_most : 0;
-    auto group_steps = [&](int32_t g) { return ((int64_t)pre[g] + step - 1) / step; };
-    const int64_t stride = std::max<int64_t>(1, (most_steps - least) / 256);
-    for (int64_t len = std::max<int64_t>(least, 1); len <= most_steps; len += stride) {
-      int64_t units = 0;
-      for (int32_t g = 0; g < groups->num; ++g)
-        units += (((int64_t)group_tokens(g) + 2 * cta - 1) / (2 * cta)) * ((group_steps(g) + len - 1) / len) * heads;
-      for (int32_t on = 0; on <= (all_one ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
-        const int64_t clusters = std::max(1, (sms - on) / 2);
-        const double parts_us = (double)((units + clusters - 1) / clusters * (len * step / 64 + kPartEnds));
-        const double cost = on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on));
-        if (best == 0 || cost < best) {
-          best = cost;
-          longest = (int32_t)len;
-          beside = on;
-        }
-      }
-    }
-    tok_parts.assign((size_t)T, 0);
-    for (int32_t g = 0; g < groups->num; ++g) {
-      const int32_t q0 = qo[groups->indptr[g]], len = group_tokens(g), at = kvp[groups->indptr[g]];
-      const int32_t parts = (int32_t)((group_steps(g) + longest - 1) / longest);
-      const int32_t run = parts > 0 ? (int32_t)((group_steps(g) + parts - 1) / parts) * step : step;
-      pre_pages.insert(pre_pages.end(), page_ids + at, page_ids + at + pre[g] / ps);
-      for (int32_t i = 0; i < parts; ++i) {
-        if ((int64_t)i * run >= pre[g]) break;  // (rounded up, fewer parts may do)
-        const int32_t k0 = i * run, k1 = (int32_t)std::min<int64_t>((int64_t)k0 + run, pre[g]);
-        const size_t before = part.size();
-        // (a row stands behind the whole prefix, so it sees every key of the run)
-        put_pairs(&part, cta, q0, len, k1, pre_total + k0 / ps, pre_total + (k1 + ps - 1) / ps, k1, k0);
-        if (!fits_i32((int64_t)i * T)) return PG_ERR_I32_OVERFLOW;
-        part_row.resize(part_row.size() + (part.size() - before) / 8, i * T);
-      }
-      const int32_t cut = parts > 0 ? (int32_t)(((int64_t)pre[g] + run - 1) / run) : 0;
-      std::fill(tok_parts.begin() + q0, tok_parts.begin() + q0 + len, cut);
-      pre_total += pre[g] / ps;
-    }
-    if (!fits_i32((int64_t)(part.size() / 8) * heads)) return PG_ERR_I32_OVERFLOW;
-    num_parts = (int32_t)(part.size() / 8);
-    {
-      // the longest first, as in the pair table
-      std::vector<int32_t> order((size_t)num_parts), tab(part.size()), rows((size_t)num_parts);
-      for (int32_t i = 0; i < num_parts; ++i) order[i] = i;
-      auto keys = [&](int32_t i) { return part[8 * (size_t)i + 6] - part[8 * (size_t)i + 7]; };
-      std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return keys(x) > keys(y); });
-      for (int32_t i = 0; i < num_parts; ++i) {
-        std::copy_n(part.data() + 8 * (size_t)order[i], 8, tab.data() + 8 * (size_t)i);
-        rows[i] = part_row[order[i]];
-      }
-      part.swap(tab);
-      part_row.swap(rows);
-    }
     // room for what any batch of as many groups, requests, tokens and pages needs
     room_parts = num_req > 0 ? (groups->num + (T - groups->num) / (2 * cta)) * parts_most : 0;
-    part.resize((size_t)room_parts * 8, 0);
-    part_row.resize((size_t)room_parts, 0);
+    const int32_t most_len = pre.empty() ? 0 : *std::max_element(pre.begin(), pre.end());
+    auto tokens_of = [&](int32_t g) { return qo[groups->indptr[g + 1]] - qo[groups->indptr[g]]; };
+    auto pairs_of = [&](int32_t g) { return ((int64_t)tokens_of(g) + 2 * cta - 1) / (2 * cta); };
+    auto steps_of = [&](int32_t g) { return ((int64_t)pre[g] + step - 1) / step; };
+    for (int set = 0; set < 2; ++set) {
+      Parts& p = parts[set];
+      // How long a part is (in steps of 64 keys, or a page; a group is cut into as few of one length):
+      // every candidate costs rounds of units over the clusters, each as long as its key tiles (about a
+      // microsecond each) and a start and an epilogue worth kPartEnds. A decode step's own keys run beside
+      // the parts, on SMs left free for them, where that ends sooner: a CTA takes about 8 us to begin and
+      // end and 6.5 for a tile of 256 KB, half of that in 8 bits.
+      auto own_us = [&](int32_t on) { return 8 + (set == 0 ? 6.5 : 3.25) * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
+      int64_t longest = 1;
+      double best = 0;
+      const int64_t most_steps = ((int64_t)most_len + step - 1) / step;
+      const int64_t least = parts_most > 0 ? (most_steps + parts_most - 1) / parts_most : 0;
+      const int64_t stride = std::max<int64_t>(1, (most_steps - least) / 256);
+      for (int64_t len = std::max<int64_t>(least, 1); len <= most_steps; len += stride) {
+        int64_t units = 0;
+        for (int32_t g = 0; g < groups->num; ++g) units += pairs_of(g) * ((steps_of(g) + len - 1) / len) * heads;
+        for (int32_t on = 0; on <= (all_one ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
+          const int64_t clusters = std::max(1, (sms - on) / 2);
+          const double parts_us = (double)((units + clusters - 1) / clusters * (len * step / 64 + kPartEnds));
+          const double cost = on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on));
+          if (best == 0 || cost < best) {
+            best = cost;
+            longest = len;
+            p.beside = on;
+          }
+        }
+      }
+      p.tok.assign((size_t)T, 0);
+      std::vector<int32_t> tab, row;
+      int32_t pages = 0;  // of the prefixes before
+      for (int32_t g = 0; g < groups->num; ++g) {
+        const int32_t q0 = qo[groups->indptr[g]], len = tokens_of(g);
+        const int64_t few = (steps_of(g) + longest - 1) / longest;
+        const int64_t run = few > 0 ? (steps_of(g) + few - 1) / few * step : step;
+        const int32_t cut = (int32_t)((pre[g] + run - 1) / run);
+        if (!fits_i32((int64_t)cut * T)) return PG_ERR_I32_OVERFLOW;
+        for (int32_t i = 0; i < cut; ++i) {
+          const int32_t k0 = (int32_t)(i * run), k1 = (int32_t)std::min<int64_t>(k0 + run, pre[g]);
+          // (a row stands behind the whole prefix, so it sees every key of the part)
+          put_pairs(&tab, cta, q0, len, k1, pages + k0 / ps, pages + (k1 + ps - 1) / ps, k1, k0);
+          row.resize(tab.size() / 8, i * T);
+        }
+        std::fill(p.tok.begin() + q0, p.tok.begin() + q0 + len, cut);
+        pages += pre[g] / ps;
+      }
+      if (!fits_i32((int64_t)(tab.size() / 8) * heads)) return PG_ERR_I32_OVERFLOW;
+      p.num = (int32_t)(tab.size() / 8);
+      // the longest first, as in the pair table
+      std::vector<int32_t> order((size_t)p.num);
+      for (int32_t i = 0; i < p.num; ++i) order[i] = i;
+      auto keys = [&](int32_t i) { return tab[8 * (size_t)i + 6] - tab[8 * (size_t)i + 7]; };
+      std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return keys(x) > keys(y); });
+      p.tab.assign((size_t)room_parts * 8, 0);
+      p.row.assign((size_t)room_parts, 0);
+      for (int32_t i = 0; i < p.num; ++i) {
+        std::copy_n(tab.data() + 8 * (size_t)order[i], 8, p.tab.data() + 8 * (size_t)i);
+        p.row[i] = row[order[i]];
+      }
+    }
+  }
+  const int32_t pre_total = (int32_t)pre_pages.size();
+  if (groups) {
     pages2.resize((size_t)NP, 0);
     pre_pages.resize((size_t)NP, 0);
     ptab2.resize((size_t)room_pairs * 8, 0);
   }
-  const int32_t part_live[3] = {0, num_parts, pre_total};
 
   // Pack everything into one int32 array and upload it on the plan's stream.
   std::vector<int32_t> host;
@@ -471,10 +482,12 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     own->o_pages = put(pages2.data(), pages2.size());
     own->o_kvs = put(kvs2.data(), kvs2.size());
     own->o_pair = put(ptab2.data(), ptab2.size());
-    q.o_part = put(part.data(), part.size());
-    q.o_part_row = put(part_row.data(), part_row.size());
-    q.o_part_live = put(part_live, 3);
-    q.o_tok_parts = put(tok_parts.data(), tok_parts.size());
+    for (int set = 0; set < 2; ++set) {
+      const Parts& p = parts[set];
+      const int32_t count[3] = {0, p.num, pre_total};
+      q.parts[set] = PartSet{p.num, p.beside, put(p.tab.data(), p.tab.size()), put(p.row.data(), p.row.size()),
+                             put(count, 3), put(p.tok.data(), p.tok.size())};
+    }
     q.o_pre_pages = put(pre_pages.data(), pre_pages.size());
   }
   if (host.empty()) host.assign(4, 0);
@@ -564,10 +577,8 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     own->tiles = tiles2;
     q.own = std::move(own);
     q.num_groups = groups->num;
-    q.num_parts = num_parts;
     q.room_parts = room_parts;
     q.parts_most = parts_most;
-    q.beside = beside;
     q.prefix_pages = pre_total;
   }
 
@@ -1181,16 +1192,16 @@ size_t shared_workspace_bytes(const pg_plan* p) {
 }
 
 // The prefixes' parts: pool pages `page_ids` (device, prefix by prefix) of `pool`.
-AttnArgs part_args(const pg_plan* p, const PoolDev& pool, const int32_t* page_ids, int32_t num_page_ids,
-                   const pg_bf16_t* q, float sm_scale, unsigned char* base, const SharedWs& w, int* status) {
+AttnArgs part_args(const pg_plan* p, const PartSet& set, const PoolDev& pool, const int32_t* page_ids,
+                   int32_t num_page_ids, const pg_bf16_t* q, float sm_scale, unsigned char* base, const SharedWs& w, int* status) {
   AttnArgs a{};
   a.plan = plan_dev(p);
-  a.plan.pair_tab = p->dev + p->o_part;
+  a.plan.pair_tab = p->dev + set.o_tab;
   a.plan.page_ids = page_ids;
   a.plan.num_page_ids = num_page_ids;
-  a.plan.num_pairs = p->num_parts;
+  a.plan.num_pairs = set.num;
   if (capturing(p->stream)) {
-    a.plan.live = p->dev + p->o_part_live;
+    a.plan.live = p->dev + set.o_live;
     a.plan.num_pairs = p->room_parts;
   }
   a.pool = pool;
@@ -1203,20 +1214,20 @@ AttnArgs part_args(const pg_plan* p, const PoolDev& pool, const int32_t* page_id
   a.bounded = 1;
   a.part_o = reinterpret_cast<float*>(base + w.o);
   a.part_ml = reinterpret_cast<float*>(base + w.ml);
-  a.part_row = p->dev + p->o_part_row;
-  a.tok_parts = p->dev + p->o_tok_parts;
-  a.beside = p->beside;
-  if (p->beside > 0) a.part_clusters = std::max(1, (sm_count() - p->beside) / 2);
+  a.part_row = p->dev + set.o_row;
+  a.tok_parts = p->dev + set.o_tok;
+  a.beside = set.beside;
+  if (set.beside > 0) a.part_clusters = std::max(1, (sm_count() - set.beside) / 2);
   a.status = status;
   wait_settings(&a.wait_ns, &a.test_withhold);
   return a;
 }
-cudaError_t shared_join(const pg_plan* p, pg_bf16_t* out, float* lse, unsigned char* base, const SharedWs& w,
+cudaError_t shared_join(const pg_plan* p, const PartSet& set, pg_bf16_t* out, float* lse, unsigned char* base, const SharedWs& w,
                         cudaStream_t stream) {
   SharedJoinArgs j{};
   j.part_o = reinterpret_cast<const float*>(base + w.o);
   j.part_ml = reinterpret_cast<const float*>(base + w.ml);
-  j.tok_parts = p->dev + p->o_tok_parts;
+  j.tok_parts = p->dev + set.o_tok;
   j.out = reinterpret_cast<__nv_bfloat16*>(out);
   j.own_lse = reinterpret_cast<const float*>(base + w.lse);
   j.lse = lse;
@@ -1258,12 +1269,13 @@ int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const
   int* st = status_word(&err);
   if (!st) return err;
   unsigned char* const base = shared_base(ws);
-  const bool join = plan->num_parts > 0 || capturing(stream);
+  const PartSet& set = plan->parts[0];
+  const bool join = set.num > 0 || capturing(stream);
   float* const own_lse = join ? reinterpret_cast<float*>(base + w.lse) : lse;
   Bounded b;
   AttnArgs a;
   if (join) {
-    a = part_args(plan, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q, sm_scale, base, w,
+    a = part_args(plan, set, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q, sm_scale, base, w,
                   st);
     if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
     a.join_lse = lse;
@@ -1271,7 +1283,7 @@ int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const
   }
   rc = attn_common(own, pool, layer, D, q, out, own_lse, -1, sm_scale, base + w.own, ws_bytes - w.own, stream, &b);
   if (rc != PG_OK || !join || b.parts) return rc;
-  return shared_join(plan, out, lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+  return shared_join(plan, set, out, lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
 // The 8-bit form: each prefix's pages are read back to the end of the workspace, behind a list of
@@ -1317,7 +1329,8 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
   int err = PG_OK;
   int* st = status_word(&err);
   if (!st) return err;
-  const bool join = plan->num_parts > 0 || captured;
+  const PartSet& set = plan->parts[1];
+  const bool join = set.num > 0 || captured;
   float* const own_lse = join ? reinterpret_cast<float*>(base + x.w.lse) : lse;
   AttnArgs a;
   const bool along = join && q8_direct(plan->own.get());  // the decode's join takes the parts along
@@ -1334,7 +1347,7 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
     d.head_dim = D;
     d.num_layers = 1;
     d.list = 1;
-    d.whole = plan->dev + plan->o_part_live + 2;
+    d.whole = plan->dev + set.o_live + 2;
     d.window_left = -1;
     d.ids = reinterpret_cast<int32_t*>(base + x.ids);
     d.status = st;
@@ -1342,14 +1355,14 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
     PoolDev copy = q8_geometry(pool);
     copy.layer_base = d.dst;
     copy.num_pages = pages;
-    a = part_args(plan, copy, d.ids, pages, q, sm_scale, base, x.w, st);
+    a = part_args(plan, set, copy, d.ids, pages, q, sm_scale, base, x.w, st);
     if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
     a.join_lse = lse;
   }
   rc = q8_attn(plan->own.get(), pool, layer, q, out, own_lse, -1, 0, sm_scale, base + x.w.own, x.ids - x.w.own, stream,
                along ? &a : nullptr);
   if (rc != PG_OK || !join || along) return rc;
-  return shared_join(plan, out, lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
+  return shared_join(plan, set, out, lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
 // Builds *plan (null) or updates it. No exception leaves a C entry: memory that the host cannot give is
