@@ -23,8 +23,8 @@
 // (128 keys x head_dim codes: three slots of 64 KB, or six of 32 KB), in the order K0 K1 V0 K2 V1 ...
 //   warps 0, 6  producers of K (with a header a tile) and of V: one 4-D box per 16 keys
 //   warp 7      the group's query rows into their terms, a segment ahead as far as their buffer allows
-//   (the last)  (groups above 4: every other row each); and V rows of keys that are not visible to zero,
-//               whatever they held, once a tile's weights and V have arrived
+//   (the last)  (groups above 4: four warps, which share the rows); and V rows of keys that are not visible
+//               to zero, whatever they held, once a tile's weights and V have arrived
 //   warp 1      MMA issuer: QK of tile i + 1 before PV of tile i
 //   warps 2-5   softmax: a thread is a key and up to 8 query rows; its row scales load a tile ahead.
 //   (8-11)      Groups above 8 take two such sets, which share nothing but the tiles. (One set over
@@ -60,7 +60,7 @@ template <int D, int NQ, int NR>
 struct Q8Cfg {
   static constexpr int SETS = NQ > 8 ? 2 : 1;   // sets of four softmax warps
   static constexpr int CQ = NQ / SETS;          // query rows of a set
-  static constexpr int QW = NQ > 4 ? 2 : 1;     // query warps
+  static constexpr int QW = NQ > 4 ? 4 : 1;     // query warps
   static constexpr int THREADS = 224 + 32 * QW + 128 * (SETS - 1);
   // Small groups at head_dim 256: two CTAs an SM, each with half the ring, so that one streams while the
   // other starts or ends a segment (of some 9 tiles under a window of 1023).
@@ -270,12 +270,12 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       while (globaltimer() - t0 < 100000ull) {
       }
     }
-  } else if (warp == 7 || (C::QW == 2 && warp == C::THREADS / 32 - 1)) {
+  } else if (warp == 7 || (C::QW > 1 && warp > C::THREADS / 32 - C::QW)) {
     // ------------------------------------------------------------ queries
     // A row's elements are all in the warp, 8 consecutive ones a lane and piece of 256.
     wait_previous(a);
     constexpr int PC = D / 256, ROWS = NQ / C::QW;  // (NQ is 2, 4, 8 or 16)
-    const int first = warp == 7 ? 0 : 1;
+    const int first = warp == 7 ? 0 : C::THREADS / 32 - warp;
     int32_t segs = 0, i = 0, j = 0;  // headers read, and given back
     int32_t g = 0, tok = 0, fixes = 0;
     bool end = false, fresh = false;  // fresh: the last header read began a segment whose queries are to come
@@ -637,7 +637,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(SFREE + 8 * b);
-      if (any_of(bar, over || !ok)) {
+      if ((h.flags & kFirst) || any_of(bar, over || !ok)) {
         if (any_of(bar, !ok)) break;
         // The rows' maxima over the tile, of s and of s + v, then references where they were outgrown:
         // lane i looks after row set_col(i), and every lane takes what it finds.
