@@ -630,3 +630,94 @@ def test_empty_batch():
     assert pg.pg_launch_count() == before
     plan.close()
     c.close()
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_a_bad_device_page_is_reported_and_skipped(decode):
+    """A page id out of range on the device: nothing is read there, the other requests are right."""
+    import ctypes as C
+    rt = None
+    for name in ("libcudart.so.13", "libcudart.so"):
+        try:
+            rt = C.CDLL(name)
+            break
+        except OSError:
+            continue
+    if rt is None:
+        pytest.skip("libcudart not loadable by name")
+    qo, start = ([1] * 4, [100, 300, 40, 7]) if decode else ([30, 2, 60, 9], [100, 300, 40, 7])
+    c = Q8Case(512, 16, 1, qo, start, seed=60).build()
+    torch.cuda.synchronize()
+    bad = np.array([c.P + 1000], np.int32)
+    rt.cudaMemcpy.argtypes = [C.c_void_p, C.c_void_p, C.c_size_t, C.c_int]
+    at = c.plan.info().d_page_ids + 4 * int(c.pg_indptr[1] + 2)
+    assert rt.cudaMemcpy(at, bad.ctypes.data, 4, 1) == 0
+    c.attend()
+    torch.cuda.synchronize()
+    assert pg.pg_device_status() == pg.PG_ERR_DEVICE_BOUNDS
+    c.reference()
+    rows = np.concatenate([np.arange(c.qo_indptr[r], c.qo_indptr[r + 1]) for r in (0, 2, 3)])
+    c.check_attention(rows=rows)
+    dst = torch.full(c.pool.shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    pg.check(pg.pg_kv_dequantize(c.plan, c.q8, pg.pool_descriptor(dst), 0, 1))
+    torch.cuda.synchronize()
+    assert pg.pg_device_status() == pg.PG_ERR_DEVICE_BOUNDS
+    want = torch.full(dst.shape, 3.0, dtype=torch.bfloat16)
+    for r in range(4):
+        page, off = (torch.from_numpy(x) for x in c.rows_of(r))
+        keep = torch.ones(len(page), dtype=torch.bool)
+        if r == 1:
+            keep[32:48] = False
+        want[0, page[keep], :, :, off[keep]] = c.pool_cpu[0, page[keep], :, :, off[keep]]
+    assert torch.equal(dst.cpu(), want)
+    c.close()
+
+
+@pytest.mark.parametrize("D", [256, 512])
+def test_query_rows_of_any_size(D):
+    """Rows of zeros, of 2^-40 and of 2^20, one with an infinity, one with a NaN: the last two give NaN rows
+    and no other."""
+    hq, hkv = (4, 2)
+    c = Q8Case(D, hq, hkv, [1, 1], [300, 40], seed=61)
+    c.q_cpu[0, 0] = 0
+    c.q_cpu[0, 1] *= 2.0 ** -40
+    c.q_cpu[0, 2, :5] *= 2.0 ** 3
+    c.q_cpu[1, 0, 7] = float("inf")
+    c.q_cpu[1, 3, 9] = float("nan")
+    c.build()
+    c.attend()
+    ok()
+    bad = torch.zeros((2, hq), dtype=torch.bool)
+    bad[1, 0] = bad[1, 3] = True
+    assert torch.equal(torch.isnan(c.out.cpu()).all(-1), bad)
+    assert torch.equal(torch.isnan(c.out.cpu()).any(-1), bad)
+    assert torch.equal(torch.isnan(c.lse.cpu()), bad)
+    c.q_cpu[bad] = 0
+    keep = c.out, c.lse
+    c.reference()
+    c.out, c.lse = torch.where(bad[..., None].cuda(), 0, keep[0]), torch.where(bad.cuda(), 0, keep[1])
+    out, lse, m, p, wabs = c.ref
+    out[bad.numpy()] = 0
+    lse[bad.numpy()] = 0
+    c.check_attention()
+    c.close()
+
+
+def test_two_plans_on_two_streams():
+    """Calls of two plans at once, each with its own workspace."""
+    D, hq, hkv = 512, 16, 1
+    cs = []
+    for seed in (70, 71):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            cs.append(Q8Case(D, hq, hkv, [1] * 20, list(range(100, 2100, 100)), seed=seed, stream=s).build())
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c in cs:
+            with torch.cuda.stream(c.stream):
+                c.attend()
+    ok()
+    for c in cs:
+        c.reference()
+        c.check_attention()
+        c.close()

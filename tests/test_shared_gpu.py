@@ -283,3 +283,111 @@ def test_empty_batch():
     assert pg.pg_launch_count() == before
     plan.close()
     c.close()
+
+
+# ------------------------------------------------------------------ a run together
+@pytest.mark.parametrize("D", [256, 512])
+def test_requests_fork_from_a_prompt_on_an_8_bit_cache(D):
+    """A document is read once into an 8-bit pool; three requests go on from its pages: their own prompts,
+    then tokens, each step written (prep) and attended (shared) on one plan updated in place. At the end
+    the cache is read back and the last step's attention repeated on the bf16 pool."""
+    from q8_ref import values
+    hq, hkv = HEADS[D][0]
+    ps, doc, R = 16, 160, 3
+    g = np.random.Generator(np.random.PCG64(50 + D))
+    P = doc // ps + R * 4
+    codes = torch.full((1, P, 2, hkv, ps, D), 0x7F, dtype=torch.uint8, device="cuda")
+    scales = torch.full((1, P, 2, hkv, ps), 0xFF, dtype=torch.uint8, device="cuda")
+    q8 = pg.q8_descriptor(codes, scales)
+    order = g.permutation(P).astype(np.int32)
+    prefix, rest = order[:doc // ps], order[doc // ps:]
+    f = (1e4 if D == 256 else 1e6) ** (-2.0 * np.arange(D // 2) / D)
+    a = np.arange(256)[:, None] * f
+    cos, sin = (torch.from_numpy(x.astype(np.float32)).cuda() for x in (np.cos(a), np.sin(a)))
+    w = torch.from_numpy((0.2 * (1 + 0.1 * g.standard_normal((2, D)))).astype(np.float32)).to(torch.bfloat16).cuda()
+    plan = None
+
+    def step(groups, pre, qo, start, lists):
+        nonlocal plan
+        qo, start = np.asarray(qo), np.asarray(start)
+        n = start + qo
+        npg = -(-n // ps)
+        ids = np.concatenate([p[:k] for p, k in zip(lists, npg)])
+        kw = [len(qo), np.concatenate([[0], np.cumsum(qo)]), np.concatenate([[0], np.cumsum(npg)]), ids,
+              n - (npg - 1) * ps, start, len(groups), np.concatenate([[0], np.cumsum(groups)]), pre, hq, hkv, D, ps]
+        rc, plan = pg.pg_plan_paged_shared(plan, *kw)
+        pg.check(rc, "plan")
+        T = int(qo.sum())
+        cols = (hq + (2 if D == 256 else 1) * hkv) * D
+        raw = torch.from_numpy(g.standard_normal((T, cols)).astype(np.float32)).to(torch.bfloat16).cuda()
+        q = torch.full((T, hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        pg.check(pg.pg_prep_paged_q8(plan, q8, 0, raw, cols, raw[:, hq * D:], cols,
+                                     raw[:, (hq + hkv) * D:] if D == 256 else None, cols, w[0], w[1], 1e-6, cos, sin,
+                                     256, q), "prep")
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full((T, hq), float("nan"), device="cuda")
+        ws = torch.full((pg.pg_shared_q8_workspace_bytes(plan),), 0xFF, dtype=torch.uint8, device="cuda")
+        pg.check(pg.pg_attn_paged_shared_q8(plan, q8, 0, q, out, lse, 1.0, ws, ws.numel()), "attention")
+        ok()
+        rows = values(codes.cpu()[0], scales.cpu()[0]).numpy()  # [P, kv, head, slot, D]
+        check(q, out, lse, qo, start, lists, rows)
+        return q, out, lse, qo, start, rows
+
+    def check(q, out, lse, qo, start, lists, rows):
+        qd, got, gl = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+        t = 0
+        for r in range(len(qo)):
+            n = int(start[r] + qo[r])
+            kv = rows[np.asarray(lists[r])].transpose(0, 3, 1, 2, 4).reshape(-1, 2, hkv, D)[:n]
+            for i in range(int(qo[r])):
+                m = int(start[r]) + i + 1
+                for h in range(hq):
+                    k, v = kv[:m, 0, h * hkv // hq], kv[:m, 1, h * hkv // hq]
+                    z = k @ qd[t, h]
+                    top = z.max()
+                    p = np.exp(z - top)
+                    ref, mag = p @ v / p.sum(), p @ np.abs(v) / p.sum()
+                    # scores of up to D products of about unit size in all; bounded_ref's rule with the
+                    # own keys' rounding and q8_ref's floor of small weights
+                    e = 2 * (16 * 2.0 ** -23 * float(np.abs(qd[t, h]) @ np.abs(k).max(0)) + 2.0 ** -21 * 70) + 2.0 ** -20
+                    lim = 2.0 ** -8 * (2 * mag + np.abs(ref)) + e * mag + 2.0 ** -21 * m * np.abs(v).max()
+                    assert (np.abs(got[t, h] - ref) <= lim).all(), (r, i, h)
+                    assert abs(gl[t, h] - (top + np.log(p.sum()))) <= e + 2.0 ** -20, (r, i, h)
+                t += 1
+
+    step([1], [0], [doc], [0], [prefix])
+    lists = [np.concatenate([prefix, rest[r::R]]) for r in range(R)]
+    lens = np.array([doc, doc, doc])
+    before = codes[0, torch.from_numpy(prefix).long().cuda()].clone()
+    for qo in ([20, 3, 7], [1, 1, 1], [1, 1, 1], [2, 1, 1]):
+        last = step([R], [doc], qo, lens, lists)
+        lens = lens + np.asarray(qo)
+    assert torch.equal(codes[0, torch.from_numpy(prefix).long().cuda()], before)  # no step wrote the document
+    q, out, lse, qo, start, rows = last
+    bf = torch.zeros((1, P, 2, hkv, ps, D), dtype=torch.bfloat16, device="cuda")
+    pg.check(pg.pg_kv_dequantize(plan, q8, pg.pool_descriptor(bf), 0, 1))
+    ws = torch.empty(pg.pg_shared_workspace_bytes(plan), dtype=torch.uint8, device="cuda")
+    pg.check(pg.pg_attn_paged_shared(plan, pg.pool_descriptor(bf), 0, q, out, lse, 1.0, ws, ws.numel()))
+    ok()
+    check(q, out, lse, qo, start, lists, rows)
+    plan.close()
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    """The parts' kernel withholds an arrival: the call returns, the status word says so, and the context
+    stays usable."""
+    c = Bf16(512, 16, 1, [1, 1], [10, 20], [(2, 40)], seed=2).build()
+    c.attend()
+    ok()
+    try:
+        assert pg.pg_test_bounded_wait(1, 20_000_000) == pg.PG_OK
+        c.attend()
+        torch.cuda.synchronize()
+        assert pg.pg_device_status() == pg.PG_ERR_DEVICE_TIMEOUT
+    finally:
+        assert pg.pg_test_bounded_wait(0) == pg.PG_OK
+    c.out.fill_(float("nan"))
+    c.attend()
+    ok()
+    c.check()
+    c.close()
