@@ -234,7 +234,7 @@ attn_split_kernel(AttnArgs a) {
       const int32_t lp = rel / ps;  // logical page; ring addressing wraps it over the pages held
       const int32_t pidx = kvp0 + (pl.ring ? lp % max(kvp1 - kvp0, 1) : lp);
       r.off = rel - lp * ps;
-      r.page = pidx < kvp1 ? pl.page_ids[pidx] : -1;
+      r.page = pidx < kvp1 ? pl.page_at(pidx) : -1;
     }
     return r;
   };

@@ -424,7 +424,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (ks >= u.kv_len) return -1;
         const int32_t lp = (ks - u.kv_start) / ps;  // logical page; a ring wraps it over its pages
         const int32_t pidx = u.kvp0 + (pl.ring ? lp % max(u.kvp1 - u.kvp0, 1) : lp);
-        return (pidx < u.kvp1 && pidx < pl.num_page_ids) ? pl.page_ids[pidx] : a.num_pages;
+        return (pidx < u.kvp1 && pidx < pl.num_page_ids) ? pl.page_at(pidx) : a.num_pages;
       };
       int32_t pg_next = lookup(0);
       int32_t my_page = -1, my_row = 0, my_ks = 0;
@@ -1219,6 +1219,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  // (a decode kernel, whose CTAs allocate alone, may take over an SM that this one leaves while the stream
+  // still runs it: neither CTA leaves before both have freed)
+  if constexpr (PART) {
+    __syncthreads();
+    cluster_sync();
   }
 }
 

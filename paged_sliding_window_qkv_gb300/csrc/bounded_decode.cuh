@@ -257,7 +257,7 @@ struct TileWalk {
     t.off = t.rel & (a.pool.page_size - 1);
     if (t.live) {
       const int32_t pidx = q.kvp0 + (t.rel >> args.page_lg);
-      t.page = (pidx < q.kvp1 && pidx < a.plan.num_page_ids) ? a.plan.page_ids[pidx] : -1;
+      t.page = (pidx < q.kvp1 && pidx < a.plan.num_page_ids) ? a.plan.page_at(pidx) : -1;
     }
     if (++j == q.total && i + 1 < n) {
       j = 0;

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(DequantArgs a) {
   // (launched programmatically: the plan, which copies alone write, is looked at while the stream's
   // previous kernel ends; every warp then waits for that kernel, whatever it has to do)
   bool skip = i >= (a.whole ? *a.whole : pl.kv_page_indptr[pl.num_req]);  // room behind the list
-  const int32_t page = skip ? -1 : pl.page_ids[i];
+  const int32_t page = skip ? -1 : pl.page_at(i);
   int32_t rows = ps;  // slots of the page that hold keys
   bool seen = true;
   if (!skip && !a.whole) {
@@ -63,7 +63,6 @@ __global__ void __launch_bounds__(kWarps * 32) dequant_kernel(DequantArgs a) {
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (skip) return;
-  if (a.list && kvh == 0 && lane == 0) a.ids[i] = i;
   if (!seen) return;
   const bool good = page >= 0 && page < a.num_pages;
   if (!good) {

@@ -794,7 +794,7 @@ struct Bounded {
   float* logits = nullptr;
   int64_t logit_slots = 0;
   StatsDev stats = {};
-  const int32_t* page_ids = nullptr;  // device: the pool's pages in the order of the plan's list
+  bool in_order = false;              // the pool's pages lie in the order of the plan's list
   const AttnArgs* parts = nullptr;    // decode: parts of the rows' prefixes, for the join
 };
 // The parts' records into the arguments of the call on the own keys.
@@ -866,7 +866,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
   if (args) args->plan.num_tokens = 0;
   if (!plan) return PG_ERR_ARG;
   if (stream != plan->stream) return PG_ERR_STREAM;
-  const bool listed = bounded && bounded->page_ids;
+  const bool listed = bounded && bounded->in_order;
   int rc = listed ? check_pool(pool, D) : check_plan_pool(plan, pool, layer, D);
   if (rc) return rc;
   if ((rc = check_attn_args(plan, D, window_left, sm_scale))) return rc;
@@ -892,7 +892,7 @@ int attn_common(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, int32
     a.plan.num_work = plan->room_work;
     a.plan.num_pairs = plan->room_pairs;
   }
-  if (listed) a.plan.page_ids = bounded->page_ids;
+  if (listed) a.plan.page_ids = nullptr;
   a.pool = pool_dev(pool, layer);
   a.q = reinterpret_cast<const __nv_bfloat16*>(q);
   a.out = reinterpret_cast<__nv_bfloat16*>(out);
@@ -1067,17 +1067,17 @@ int evict_common(const pg_plan* plan, const pg_kv_stats_t* stats, int32_t layer,
 // ---- attention over an 8-bit cache
 size_t align1k(size_t n) { return (n + 1023) & ~(size_t)1023; }
 
-// Plans that the 8-bit kernels do not take are read back first: the workspace holds the page list
-// 0, 1, ..., the pages in the order of the plan's list, and what the bf16 kernel needs.
+// Plans that the 8-bit kernels do not take are read back first: the workspace holds the pages in the
+// order of the plan's list, and what the bf16 kernel needs. (No list of them: a decode kernel looks at
+// page ids while the stream's previous kernel, which would have written it, still runs.)
 struct ReadBack {
-  size_t pages, rest, bytes;  // offsets of the pages and of the kernel's workspace, total
+  size_t rest, bytes;  // offset of the kernel's workspace, total
 };
 bool read_back(const pg_plan* p, ReadBack* w) {
   const __int128 page = (__int128)4 * p->num_kv_heads * p->page_size * p->head_dim;
   const __int128 pages = page * p->num_page_ids;
   if (pages > ((__int128)1 << 60)) return false;
-  w->pages = align1k((size_t)p->num_page_ids * sizeof(int32_t));
-  w->rest = w->pages + align1k((size_t)pages);
+  w->rest = align1k((size_t)pages);
   w->bytes = w->rest + std::max(workspace_bytes(p), bounded_ws_bytes(p));
   return true;
 }
@@ -1141,7 +1141,7 @@ int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const 
   DequantArgs d{};
   d.plan = plan_dev(plan);
   d.src = q8_dev(pool, layer);
-  d.dst = reinterpret_cast<__nv_bfloat16*>(base + w.pages);
+  d.dst = reinterpret_cast<__nv_bfloat16*>(base);
   d.num_pages = pool->num_pages;
   d.page_size = plan->page_size;
   d.num_kv_heads = plan->num_kv_heads;
@@ -1150,16 +1150,15 @@ int q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const 
   d.list = 1;
   d.window_left = window_left;
   d.num_sink = num_sink;
-  d.ids = reinterpret_cast<int32_t*>(base);
   d.status = st;
   if (launch_dequant(d, stream) != cudaSuccess) return PG_ERR_CUDA;
   const int32_t ps = plan->page_size, H = plan->num_kv_heads;
-  const pg_pool_t copy = {reinterpret_cast<pg_bf16_t*>(base + w.pages), 1, plan->num_page_ids, ps, H, D,
+  const pg_pool_t copy = {reinterpret_cast<pg_bf16_t*>(base), 1, plan->num_page_ids, ps, H, D,
                           (int64_t)plan->num_page_ids * 2 * H * ps * D, (int64_t)2 * H * ps * D,
                           (int64_t)H * ps * D, (int64_t)ps * D, D, (int64_t)plan->num_page_ids * 2 * H * ps * D};
   Bounded b;
   b.num_sink = num_sink;
-  b.page_ids = d.ids;
+  b.in_order = true;
   return attn_common(plan, &copy, 0, D, q, out, lse, window_left, sm_scale, base + w.rest, ws_bytes - w.rest, stream,
                      &b);
 }
@@ -1191,7 +1190,7 @@ size_t shared_workspace_bytes(const pg_plan* p) {
                                                                                                     : SIZE_MAX;
 }
 
-// The prefixes' parts: pool pages `page_ids` (device, prefix by prefix) of `pool`.
+// The prefixes' parts: pool pages `page_ids` (device, prefix by prefix; null: in that order) of `pool`.
 AttnArgs part_args(const pg_plan* p, const PartSet& set, const PoolDev& pool, const int32_t* page_ids,
                    int32_t num_page_ids, const pg_bf16_t* q, float sm_scale, unsigned char* base, const SharedWs& w, int* status) {
   AttnArgs a{};
@@ -1286,18 +1285,16 @@ int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const
   return shared_join(plan, set, out, lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
-// The 8-bit form: each prefix's pages are read back to the end of the workspace, behind a list of
-// their places.
+// The 8-bit form: each prefix's pages are read back to the end of the workspace.
 struct SharedQ8Ws {
   SharedWs w;
-  size_t ids, pages, page_bytes;
+  size_t pages, page_bytes;
 };
 bool shared_q8_ws(const pg_plan* p, SharedQ8Ws* x) {
   const size_t own = q8_workspace_bytes(p->own.get());
   if (own > ((size_t)1 << 60) || !shared_ws(p, align256(own), &x->w)) return false;
   x->page_bytes = (size_t)4 * p->num_kv_heads * p->page_size * p->head_dim;
-  x->ids = x->w.bytes;
-  x->pages = align1k(x->ids + (size_t)p->num_page_ids * sizeof(int32_t));
+  x->pages = align1k(x->w.bytes);
   const __int128 end = (__int128)x->page_bytes * std::max(p->prefix_pages, 1) + x->pages;
   if (end > ((__int128)1 << 61)) return false;
   x->w.bytes = (size_t)end;
@@ -1349,17 +1346,16 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
     d.list = 1;
     d.whole = plan->dev + set.o_live + 2;
     d.window_left = -1;
-    d.ids = reinterpret_cast<int32_t*>(base + x.ids);
     d.status = st;
     if (launch_dequant(d, stream) != cudaSuccess) return PG_ERR_CUDA;
     PoolDev copy = q8_geometry(pool);
     copy.layer_base = d.dst;
     copy.num_pages = pages;
-    a = part_args(plan, set, copy, d.ids, pages, q, sm_scale, base, x.w, st);
+    a = part_args(plan, set, copy, nullptr, pages, q, sm_scale, base, x.w, st);
     if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
     a.join_lse = lse;
   }
-  rc = q8_attn(plan->own.get(), pool, layer, q, out, own_lse, -1, 0, sm_scale, base + x.w.own, x.ids - x.w.own, stream,
+  rc = q8_attn(plan->own.get(), pool, layer, q, out, own_lse, -1, 0, sm_scale, base + x.w.own, x.pages - x.w.own, stream,
                along ? &a : nullptr);
   if (rc != PG_OK || !join || along) return rc;
   return shared_join(plan, set, out, lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;

@@ -30,7 +30,7 @@ struct PerDeviceOnce {
 struct PlanDev {
   const int32_t* qo_indptr;       // [R+1]
   const int32_t* kv_page_indptr;  // [R+1]
-  const int32_t* page_ids;        // [num_page_ids]
+  const int32_t* page_ids;        // [num_page_ids] (null: the pool's pages lie in the order of the list)
   const int32_t* last_page_len;   // [R]
   const int32_t* start_pos;       // [R]
   const int32_t* kv_start;        // [R]   first key position held (0 unless a key segment)
@@ -50,6 +50,9 @@ struct PlanDev {
   // ring addressing: logical page pos / page_size of request r is its page
   // (pos / page_size) mod (pages of r), and kv_len = start_pos + qo_len
   int32_t ring;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int32_t page_at(int32_t i) const { return page_ids ? page_ids[i] : i; }
+#endif
 };
 
 // Device view of one family's pool, already narrowed to the called layer.
@@ -159,8 +162,7 @@ struct EvictArgs {
 };
 
 // Read-back of an 8-bit pool (see dequant.cu): to the same pages of a bf16 pool, or (list) page i of
-// the plan's list to page i of the destination, for the pages that an attention call reads, with
-// ids[i] = i.
+// the plan's list to page i of the destination, for the pages that an attention call reads.
 struct DequantArgs {
   PlanDev plan;
   Q8Dev src;
@@ -170,7 +172,6 @@ struct DequantArgs {
   int32_t page_size, num_kv_heads, head_dim, num_layers;
   int32_t list, window_left, num_sink;
   const int32_t* whole;      // list: not null: its first *whole pages, all their slots
-  int32_t* ids;
   int* status;
 };
 
