@@ -509,10 +509,10 @@ size_t pg_q8_workspace_bytes(const pg_plan_t plan);
  *   lse  [T][Hq] float32 or NULL
  *   workspace: ws_bytes >= pg_q8_workspace_bytes(plan), 16-byte aligned
  * Decode multiplies 8-bit numbers: a query row is taken as the sum of two e4m3 terms, exact for
- * elements down to 2^-15 of the row's largest and within 2^-23 of it below, and a weight as the sum
- * of three, within 2^-13 of itself down to 2^-18 of the row's largest weight and within 2^-31 of
- * that below. Sums are fp32; row sums add the unrounded weights. A query row with an element that
- * is not finite gives a NaN row.
+ * elements down to 2^-13 of the row's largest and within 2^-21 of it below, and a weight times its V
+ * row's scale as the sum of three, within 2^-12 of itself down to 2^-10 of the row's largest such
+ * product and within 2^-22 of that below. Sums are fp32; row sums add the unrounded weights. A query
+ * row with an element that is not finite gives a NaN row.
  * Errors: those of pg_attn_paged_sink.
  */
 int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer,
@@ -525,7 +525,8 @@ int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t lay
  * pg_plan_paged_shared -- the plan of pg_plan_paged_prefill for a batch whose requests share
  * prefixes: groups of consecutive requests whose first keys are the same pages. It is that plan for
  * every other entry (prep, pg_attn_paged_prefill, ...); pg_attn_paged_shared reads a group's prefix
- * once for all its requests, where a cascade of segment plans reads it once a request.
+ * once for all its requests, where a cascade of segment plans reads it once a request. Whether that
+ * is sooner than every request reading its own list is settled by the plan, from its sizes.
  *
  * Inputs as for pg_plan_paged_prefill (every request lists all its pages), plus
  *   group_indptr[num_groups+1]  int64, group_indptr[0] == 0, strictly increasing, last num_req:
@@ -557,6 +558,9 @@ size_t pg_shared_q8_workspace_bytes(const pg_plan_t plan);
  * prefix as one block of rows, cut along the keys where the batch has few rows, each request meets
  * its own keys as in pg_attn_paged_sink, and the parts are joined in fp32 by their normalisers.
  * (What a request's own keys give is rounded to bf16 before the join, a prefix's part is not.)
+ * With short prefixes, few requests or long chunks that takes longer than pg_attn_paged_sink over
+ * the same plan (window_left -1, num_sink 0), and the call is that one. The form is the plan's: the
+ * same plan gives the same bits each time, and a captured call keeps the form it was captured in.
  *   q, out  [T][Hq][head_dim] bf16, 32-byte aligned;  lse [T][Hq] float32 or NULL
  *   workspace: ws_bytes >= pg_shared_workspace_bytes(plan), 16-byte aligned
  * Errors: those of pg_attn_paged_sink; PG_ERR_PLAN_MISMATCH for another kind of plan.
@@ -569,7 +573,7 @@ int pg_attn_paged_shared(const pg_plan_t plan, const pg_pool_t* pool, int32_t la
  * back into the workspace once a call, its requests' own keys are read as in pg_attn_paged_q8. Under
  * a captured call an update's prefixes may hold as many pages as the workspace at capture has room
  * for beyond that size (4 * num_kv_heads * page_size * head_dim bytes a page; pages past it set the
- * device status word). */
+ * device status word). The other form is pg_attn_paged_q8's. */
 int pg_attn_paged_shared_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer,
                             const pg_bf16_t* q, pg_bf16_t* out, float* lse, float sm_scale,
                             void* workspace, size_t ws_bytes, pg_stream_t stream);
@@ -627,6 +631,13 @@ int64_t pg_launch_count(void);
  * not for use while other threads launch. Errors: PG_ERR_ARG.
  */
 int pg_test_bounded_wait(int32_t withhold, int64_t wait_limit_ns);
+
+/*
+ * Test hook for plans of pg_plan_paged_shared built from now on: 0 their calls take the form that
+ * the plan expects to be sooner, 1 the prefixes' parts and their join, 2 the plain walk (a batch
+ * without any prefix always does). Process-wide. Errors: PG_ERR_ARG.
+ */
+int pg_test_shared_form(int32_t form);
 
 /* Static text for a status code. */
 const char* pg_status_string(int status);

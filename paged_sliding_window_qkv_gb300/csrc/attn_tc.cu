@@ -1220,9 +1220,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // (a decode kernel, whose CTAs allocate alone, may take over an SM that this one leaves while the stream
-  // still runs it: neither CTA leaves before both have freed)
-  if constexpr (PART) {
+  // (launch_dependents above: a decode kernel, whose CTAs allocate alone, may take over an SM that this CTA
+  // leaves while its pair still frees; neither leaves before both have)
+  if constexpr (BC) {
     __syncthreads();
     cluster_sync();
   }

@@ -89,6 +89,7 @@ struct PlanStage {
 struct PartSet {
   int32_t num = 0;
   int32_t beside = 0;  // decode: SMs that the parts leave to the own keys (0: one after the other)
+  bool plain = true;   // every request reads its prefix itself: by the estimate that is sooner
   size_t o_tab = 0, o_row = 0, o_live = 0, o_tok = 0;  // pair table, record rows, counts, parts of each token
 };
 
@@ -142,7 +143,41 @@ void free_stage(PlanStage* st) {
   }
 }
 
-constexpr int32_t kPartEnds = 8;
+// What the kernels of a shared plan take, in us by head_dim (256, 512) and set (bf16, 8-bit pools), as
+// measured: batches of 1..64 requests, prefixes of 128..8192 keys, 16 and 8 query heads.
+struct SharedCost {
+  double start[2] = {9, 11};                          // of a first tensor-core prefill kernel; a later one kLater
+  double tile[2] = {0.7, 1.05}, ends[2] = {4.8, 3.5};  // of its units: 64 keys, start and epilogue
+  double dec_start[2][2] = {{9.5, 12.5}, {11, 13}};   // of a decode kernel with its join
+  double dec_l2[2][2] = {{1.65, 3.4}, {0.85, 2.8}};   // of its tiles of 128 keys: another request's too,
+  double dec_dram[2][2] = {{2.6, 5.5}, {1.25, 3.4}};  // or a request's alone
+};
+constexpr SharedCost kCost;
+constexpr double kLater = 6, kJoin = 4, kReadBack = 3.5, kBytesPerUs = 6.5e6;
+std::atomic<int32_t> g_test_shared{0};  // test hook: 1 parts, 2 plain, whatever the estimate says
+
+// The time of the longest-loaded cluster of a prefill kernel (attn_tc.cu's rounds): the table's first
+// pairs in their order, `heads` units each.
+double tc_load_us(const std::vector<int32_t>& tab, int64_t pairs, int32_t tile, int64_t heads, int64_t clusters,
+                  int32_t d) {
+  const int64_t units = pairs * heads;
+  std::vector<double> load((size_t)std::max<int64_t>(clusters, 1), 0.0);
+  const int64_t n = (int64_t)load.size();
+  double sum = 0, most = 0;
+  for (int64_t i = 0; i < pairs; ++i) {
+    const int32_t* e = tab.data() + 8 * (size_t)i;
+    const int64_t end = (int64_t)e[3] + std::min<int64_t>((int64_t)e[0] + 2 * (int64_t)tile, e[2]);
+    const double us = (double)((std::min<int64_t>(end, e[6]) - e[7] + 63) / 64) * kCost.tile[d] + kCost.ends[d];
+    sum += us * (double)heads;
+    for (int64_t w = i * heads; units <= 65536 && w < (i + 1) * heads; ++w) {
+      const int64_t at = w % n;
+      double& l = load[(size_t)((w / n) & 1 ? n - 1 - at : at)];
+      l += us;
+      most = std::max(most, l);
+    }
+  }
+  return units <= 65536 ? most : sum / (double)n;  // (that many units even out)
+}
 
 // Groups of consecutive requests that share their first keys.
 struct Groups {
@@ -335,10 +370,11 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
   struct Parts {
     std::vector<int32_t> tab, row, tok;
     int32_t num = 0, beside = 0;
+    bool plain = true;
   } parts[2];
   std::vector<int32_t> kvp2, kvs2, pages2, ptab2, pre_pages;
   int32_t seen2 = 0, room_parts = 0, parts_most = 0;
-  int64_t tiles2 = 0;
+  int64_t tiles2 = 0, tiles_l2 = 0;  // of 128 keys: own ones, and those that an earlier request has read
   if (groups) {
     if (!attn_tc_supported(D, group, ps) || cta <= 0) return PG_ERR_PLAN_MISMATCH;
     if (groups->num < 0 || (groups->num > 0 && (!groups->indptr || !groups->prefix))) return PG_ERR_ARG;
@@ -365,10 +401,12 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
                   (int32_t)len);
       }
       pre[g] = (int32_t)len;
+      tiles_l2 += (r1 - r0 - 1) * (len / 128);
       pre_pages.insert(pre_pages.end(), page_ids + kvp[r0], page_ids + kvp[r0] + len / ps);
     }
     if (!all_one) sort_pairs(&ptab2, cta, num_req > 1);
     const int32_t heads = Hkv * (D / 256), sms = std::max(2, sm_count()), step = std::max(64, ps);
+    const int32_t dx = D == 512 ? 1 : 0;
     parts_most = num_req > 0 ? most_parts(T, groups->num, cta, heads, sms) : 0;
     // room for what any batch of as many groups, requests, tokens and pages needs
     room_parts = num_req > 0 ? (groups->num + (T - groups->num) / (2 * cta)) * parts_most : 0;
@@ -379,11 +417,12 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     for (int set = 0; set < 2; ++set) {
       Parts& p = parts[set];
       // How long a part is (in steps of 64 keys, or a page; a group is cut into as few of one length):
-      // every candidate costs rounds of units over the clusters, each as long as its key tiles (about a
-      // microsecond each) and a start and an epilogue worth kPartEnds. A decode step's own keys run beside
-      // the parts, on SMs left free for them, where that ends sooner: a CTA takes about 8 us to begin and
-      // end and 6.5 for a tile of 256 KB, half of that in 8 bits.
+      // every candidate costs rounds of units over the clusters, each as long as its key tiles, a start and
+      // an epilogue. A decode step's own keys run beside the parts, on SMs left free for them, where that
+      // ends sooner: a CTA takes about 8 us to begin and end and 6.5 for a tile of 256 KB, half of that in
+      // 8 bits.
       auto own_us = [&](int32_t on) { return 8 + (set == 0 ? 6.5 : 3.25) * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
+      const double own_tc = all_one ? 0 : kLater + tc_load_us(ptab2, (int64_t)ptab2.size() / 8, cta, heads, sms / 2, dx);
       int64_t longest = 1;
       double best = 0;
       const int64_t most_steps = ((int64_t)most_len + step - 1) / step;
@@ -392,10 +431,13 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       for (int64_t len = std::max<int64_t>(least, 1); len <= most_steps; len += stride) {
         int64_t units = 0;
         for (int32_t g = 0; g < groups->num; ++g) units += pairs_of(g) * ((steps_of(g) + len - 1) / len) * heads;
+        const double join = (double)T * Hq * D * ((most_steps + len - 1) / len * 4 + (all_one ? 0 : 4)) / kBytesPerUs;
         for (int32_t on = 0; on <= (all_one ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
           const int64_t clusters = std::max(1, (sms - on) / 2);
-          const double parts_us = (double)((units + clusters - 1) / clusters * (len * step / 64 + kPartEnds));
-          const double cost = on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on));
+          const double parts_us = kCost.start[dx] + (double)((units + clusters - 1) / clusters) *
+                                                        ((double)(len * step / 64) * kCost.tile[dx] + kCost.ends[dx]);
+          const double cost =
+              join + (!all_one ? parts_us + own_tc : on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on)));
           if (best == 0 || cost < best) {
             best = cost;
             longest = len;
@@ -403,6 +445,25 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
           }
         }
       }
+      // Against every request reading its prefix itself, behind the first one's from L2: short prefixes,
+      // few requests, long chunks (whose products, not their reads, take the time).
+      const double page_us = 6.0 * Hkv * ps * D / kBytesPerUs;  // a page's codes read and its rows written
+      double plain = 0;
+      if (all_one) {
+        const double n = (double)(tiles * Hkv) / sms, l2 = (double)(tiles_l2 * Hkv) / sms;
+        plain = kCost.dec_start[set][dx] +
+                (l2 * kCost.dec_l2[set][dx] + (n - l2) * kCost.dec_dram[set][dx]) * std::ceil(n) / std::max(n, 1e-9);
+      } else {
+        plain = kCost.start[dx] + tc_load_us(ptab, npairs, cta, heads, sms / 2, dx);
+      }
+      const bool read_back = set == 1 && !all_one;
+      if (set == 1) best += kReadBack + (double)pre_pages.size() * page_us;
+      if (read_back) {
+        best += kReadBack + (double)pages2.size() * page_us;
+        plain += kReadBack + (double)NP * page_us;
+      }
+      const int32_t forced = g_test_shared.load(std::memory_order_relaxed);
+      p.plain = most_len == 0 || (forced == 0 ? plain <= best + kJoin : forced == 2);
       p.tok.assign((size_t)T, 0);
       std::vector<int32_t> tab, row;
       int32_t pages = 0;  // of the prefixes before
@@ -485,7 +546,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     for (int set = 0; set < 2; ++set) {
       const Parts& p = parts[set];
       const int32_t count[3] = {0, p.num, pre_total};
-      q.parts[set] = PartSet{p.num, p.beside, put(p.tab.data(), p.tab.size()), put(p.row.data(), p.row.size()),
+      q.parts[set] = PartSet{p.num, p.beside, p.plain, put(p.tab.data(), p.tab.size()), put(p.row.data(), p.row.size()),
                              put(count, 3), put(p.tok.data(), p.tok.size())};
     }
     q.o_pre_pages = put(pre_pages.data(), pre_pages.size());
@@ -1186,8 +1247,9 @@ unsigned char* shared_base(void* ws) {
 size_t shared_workspace_bytes(const pg_plan* p) {
   if (!p || !p->own || p->num_req == 0) return 0;
   SharedWs w;
-  return shared_ws(p, std::max(workspace_bytes(p->own.get()), bounded_ws_bytes(p->own.get())), &w) ? w.bytes + kSharedPad
-                                                                                                    : SIZE_MAX;
+  if (!shared_ws(p, std::max(workspace_bytes(p->own.get()), bounded_ws_bytes(p->own.get())), &w)) return SIZE_MAX;
+  // (enough for the plain walk: an update may take either)
+  return std::max(w.bytes + kSharedPad, std::max(workspace_bytes(p), bounded_ws_bytes(p)));
 }
 
 // The prefixes' parts: pool pages `page_ids` (device, prefix by prefix; null: in that order) of `pool`.
@@ -1260,28 +1322,27 @@ int shared_attn(const pg_plan* plan, const pg_pool_t* pool, int32_t layer, const
   if (plan->num_tokens == 0) return PG_OK;
   const pg_plan* own = plan->own.get();
   SharedWs w;
-  if (!shared_ws(plan, std::max(workspace_bytes(own), bounded_ws_bytes(own)), &w) || !ws || ws_bytes < w.bytes + kSharedPad)
+  if (!shared_ws(plan, std::max(workspace_bytes(own), bounded_ws_bytes(own)), &w) || !ws ||
+      ws_bytes < shared_workspace_bytes(plan))
     return PG_ERR_WORKSPACE;
   if (!aligned16(ws)) return PG_ERR_ALIGN;
+  Bounded b;
+  if (plan->parts[0].plain)
+    return attn_common(plan, pool, layer, D, q, out, lse, -1, sm_scale, ws, ws_bytes, stream, &b);
   ws_bytes -= kSharedPad;
   int err = PG_OK;
   int* st = status_word(&err);
   if (!st) return err;
   unsigned char* const base = shared_base(ws);
   const PartSet& set = plan->parts[0];
-  const bool join = set.num > 0 || capturing(stream);
-  float* const own_lse = join ? reinterpret_cast<float*>(base + w.lse) : lse;
-  Bounded b;
-  AttnArgs a;
-  if (join) {
-    a = part_args(plan, set, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q, sm_scale, base, w,
-                  st);
-    if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
-    a.join_lse = lse;
-    if (plan->decode) b.parts = &a;  // (the decode's join takes the parts along)
-  }
-  rc = attn_common(own, pool, layer, D, q, out, own_lse, -1, sm_scale, base + w.own, ws_bytes - w.own, stream, &b);
-  if (rc != PG_OK || !join || b.parts) return rc;
+  AttnArgs a = part_args(plan, set, pool_dev(pool, layer), plan->dev + plan->o_pre_pages, plan->num_page_ids, q, sm_scale,
+                         base, w, st);
+  if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
+  a.join_lse = lse;
+  if (plan->decode) b.parts = &a;  // (the decode's join takes the parts along)
+  rc = attn_common(own, pool, layer, D, q, out, reinterpret_cast<float*>(base + w.lse), -1, sm_scale, base + w.own,
+                   ws_bytes - w.own, stream, &b);
+  if (rc != PG_OK || b.parts) return rc;
   return shared_join(plan, set, out, lse, base, w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
@@ -1303,7 +1364,7 @@ bool shared_q8_ws(const pg_plan* p, SharedQ8Ws* x) {
 size_t shared_q8_workspace_bytes(const pg_plan* p) {
   if (!p || !p->own || p->num_req == 0) return 0;
   SharedQ8Ws x;
-  return shared_q8_ws(p, &x) ? x.w.bytes + kSharedPad : SIZE_MAX;
+  return shared_q8_ws(p, &x) ? std::max(x.w.bytes + kSharedPad, q8_workspace_bytes(p)) : SIZE_MAX;
 }
 
 int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer, const pg_bf16_t* q, pg_bf16_t* out,
@@ -1314,8 +1375,10 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
   const int32_t D = plan->head_dim, ps = plan->page_size, H = plan->num_kv_heads;
   if (plan->num_tokens == 0) return PG_OK;
   SharedQ8Ws x;
-  if (!shared_q8_ws(plan, &x) || !ws || ws_bytes < x.w.bytes + kSharedPad) return PG_ERR_WORKSPACE;
+  if (!shared_q8_ws(plan, &x) || !ws || ws_bytes < shared_q8_workspace_bytes(plan)) return PG_ERR_WORKSPACE;
   if (!aligned16(ws)) return PG_ERR_ALIGN;
+  if (plan->parts[1].plain)
+    return q8_attn(plan, pool, layer, q, out, lse, -1, 0, sm_scale, ws, ws_bytes, stream);
   ws_bytes -= kSharedPad;
   unsigned char* const base = shared_base(ws);
   // a captured call's prefixes may come to hold as many pages as the workspace has room for
@@ -1327,37 +1390,32 @@ int shared_q8_attn(const pg_plan* plan, const pg_q8_pool_t* pool, int32_t layer,
   int* st = status_word(&err);
   if (!st) return err;
   const PartSet& set = plan->parts[1];
-  const bool join = set.num > 0 || captured;
-  float* const own_lse = join ? reinterpret_cast<float*>(base + x.w.lse) : lse;
-  AttnArgs a;
-  const bool along = join && q8_direct(plan->own.get());  // the decode's join takes the parts along
-  if (join) {
-    DequantArgs d{};
-    d.plan = plan_dev(plan);
-    d.plan.page_ids = plan->dev + plan->o_pre_pages;
-    d.plan.num_page_ids = pages;
-    d.src = q8_dev(pool, layer);
-    d.dst = reinterpret_cast<__nv_bfloat16*>(base + x.pages);
-    d.num_pages = pool->num_pages;
-    d.page_size = ps;
-    d.num_kv_heads = H;
-    d.head_dim = D;
-    d.num_layers = 1;
-    d.list = 1;
-    d.whole = plan->dev + set.o_live + 2;
-    d.window_left = -1;
-    d.status = st;
-    if (launch_dequant(d, stream) != cudaSuccess) return PG_ERR_CUDA;
-    PoolDev copy = q8_geometry(pool);
-    copy.layer_base = d.dst;
-    copy.num_pages = pages;
-    a = part_args(plan, set, copy, nullptr, pages, q, sm_scale, base, x.w, st);
-    if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
-    a.join_lse = lse;
-  }
-  rc = q8_attn(plan->own.get(), pool, layer, q, out, own_lse, -1, 0, sm_scale, base + x.w.own, x.pages - x.w.own, stream,
-               along ? &a : nullptr);
-  if (rc != PG_OK || !join || along) return rc;
+  DequantArgs d{};
+  d.plan = plan_dev(plan);
+  d.plan.page_ids = plan->dev + plan->o_pre_pages;
+  d.plan.num_page_ids = pages;
+  d.src = q8_dev(pool, layer);
+  d.dst = reinterpret_cast<__nv_bfloat16*>(base + x.pages);
+  d.num_pages = pool->num_pages;
+  d.page_size = ps;
+  d.num_kv_heads = H;
+  d.head_dim = D;
+  d.num_layers = 1;
+  d.list = 1;
+  d.whole = plan->dev + set.o_live + 2;
+  d.window_left = -1;
+  d.status = st;
+  if (launch_dequant(d, stream) != cudaSuccess) return PG_ERR_CUDA;
+  PoolDev copy = q8_geometry(pool);
+  copy.layer_base = d.dst;
+  copy.num_pages = pages;
+  AttnArgs a = part_args(plan, set, copy, nullptr, pages, q, sm_scale, base, x.w, st);
+  if (launch_attn_parts(a, D, stream) != cudaSuccess) return PG_ERR_CUDA;
+  a.join_lse = lse;
+  const bool along = q8_direct(plan->own.get());  // the decode's join takes the parts along
+  rc = q8_attn(plan->own.get(), pool, layer, q, out, reinterpret_cast<float*>(base + x.w.lse), -1, 0, sm_scale,
+               base + x.w.own, x.pages - x.w.own, stream, along ? &a : nullptr);
+  if (rc != PG_OK || along) return rc;
   return shared_join(plan, set, out, lse, base, x.w, stream) == cudaSuccess ? PG_OK : PG_ERR_CUDA;
 }
 
@@ -1805,6 +1863,12 @@ int pg_device_status(pg_stream_t stream) {
 }
 
 int64_t pg_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
+
+int pg_test_shared_form(int32_t form) {
+  if (form < 0 || form > 2) return PG_ERR_ARG;
+  g_test_shared.store(form, std::memory_order_relaxed);
+  return PG_OK;
+}
 
 int pg_test_bounded_wait(int32_t withhold, int64_t wait_limit_ns) {
   if (withhold == 0) {

@@ -118,6 +118,7 @@ PG_NOALLOC_SCRATCH_BYTES = 32 << 20
 _devstat = _sig("pg_device_status", C.c_int, _P)
 _launches = _sig("pg_launch_count", _I64)
 _test_wait = _sig("pg_test_bounded_wait", C.c_int, _I32, _I64)
+_test_shared = _sig("pg_test_shared_form", C.c_int, _I32)
 _sstr = _sig("pg_status_string", C.c_char_p, C.c_int)
 
 
@@ -164,6 +165,11 @@ def pg_test_bounded_wait(withhold, wait_limit_ns=0) -> int:
     """Test hook: withhold=1 makes later tensor-core prefill launches skip one key-tile
     arrival and give up their bounded waits after wait_limit_ns; withhold=0 restores them."""
     return int(_test_wait(int(withhold), int(wait_limit_ns)))
+
+
+def pg_test_shared_form(form) -> int:
+    """Test hook: shared plans built from now on take the sooner form (0), parts (1) or the plain walk (2)."""
+    return int(_test_shared(int(form)))
 
 
 def pg_device_status(stream=None) -> int:
@@ -523,7 +529,7 @@ EXPORTED = ["pg_plan_paged_shared", "pg_shared_workspace_bytes", "pg_shared_q8_w
             "pg_plan_destroy", "pg_plan_info", "pg_rope_table",
             "pg_prep_paged_hd256", "pg_prep_paged_hd512", "pg_workspace_bytes",
             "pg_attn_paged_prefill", "pg_attn_paged_prefill_hd512", "pg_device_status",
-            "pg_launch_count", "pg_status_string", "pg_test_bounded_wait"]
+            "pg_launch_count", "pg_status_string", "pg_test_bounded_wait", "pg_test_shared_form"]
 
 
 # ---------------------------------------------------------------- page accounting (include/pg_kv.h)

@@ -13,6 +13,15 @@ from q8_ref import Q8Case
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def parts():
+    """The tests' batches are small: what is tested here is the prefixes' parts, unless a test says otherwise."""
+    assert pg.pg_test_shared_form(1) == pg.PG_OK
+    yield
+    assert pg.pg_test_shared_form(0) == pg.PG_OK
+
+
 HEADS = {256: [(16, 8), (8, 8), (16, 1), (8, 2)], 512: [(16, 1), (8, 1), (4, 2), (2, 2)]}
 
 
@@ -391,3 +400,98 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     ok()
     c.check()
     c.close()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("D", [256, 512])
+@pytest.mark.parametrize("qo,own,groups", [
+    ([1] * 7, [5, 0, 0, 64, 1, 300, 17], [(1, 9), (3, 1), (2, 33), (1, 0)]),
+    ([5, 130, 1, 64], [0, 7, 200, 0], [(3, 25), (1, 4)]),
+])
+def test_both_forms_and_the_choice(kind, D, qo, own, groups):
+    """The plain walk is the entry without prefixes, to the bit; the choice is one of the two forms."""
+    hq, hkv = HEADS[D][0]
+    got = {}
+    for form in (2, 1, 0):
+        pg.check(pg.pg_test_shared_form(form))
+        c = kind(D, hq, hkv, qo, own, groups, seed=21).build()
+        c.attend()
+        ok()
+        c.check(f"form {form}")
+        got[form] = c.out.clone(), c.lse.clone()
+        if form == 2:
+            q8 = isinstance(c, Q8Case)
+            nbytes, f, pool = (pg.pg_q8_workspace_bytes, pg.pg_attn_paged_q8, c.q8) if q8 else \
+                (pg.pg_sink_workspace_bytes, pg.pg_attn_paged_sink, c.desc)
+            ws = torch.empty(max(16, nbytes(c.plan)), dtype=torch.uint8, device="cuda")
+            pg.check(f(c.plan, pool, 0, c.q, c.out, c.lse, -1, 0, 1.0, ws, ws.numel()))
+            ok()
+            assert torch.equal(c.out, got[2][0]) and torch.equal(c.lse, got[2][1])
+        c.close()
+    assert any(torch.equal(got[0][0], got[f][0]) and torch.equal(got[0][1], got[f][1]) for f in (1, 2))
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("qo,own,groups,plain", [
+    ([1], [100], [(1, 8)], True),             # nothing to share
+    ([1] * 3, [10, 0, 99], [(3, 0)], True),   # no prefix
+    ([1] * 64, [20] * 64, [(64, 256)], False),
+    ([256] * 8, [0] * 8, [(8, 32)], True),    # long chunks behind a short prefix
+    ([2] * 32, [64] * 32, [(32, 256)], False),
+])
+def test_the_plan_chooses_by_size(kind, qo, own, groups, plain):
+    """Parts are a kernel of their own (and a read-back, and a join behind prompts): told by the launches."""
+    pg.check(pg.pg_test_shared_form(0))
+    c = kind(512, 16, 1, qo, own, groups, seed=5).build()
+
+    def launches():
+        torch.cuda.synchronize()
+        n = pg.pg_launch_count()
+        c.attend()
+        ok()
+        return pg.pg_launch_count() - n
+
+    chosen = launches()
+    c.check()
+    decode, q8 = max(qo) == 1, isinstance(c, Q8Case)
+    assert chosen == (2 if decode else 2 if q8 else 1) + (0 if plain else 1 + q8 + (not decode))
+    c.close()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=["bf16", "q8"])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("D", [256, 512])
+def test_a_captured_plain_walk_follows_its_plan(kind, decode, D):
+    """Captured in the plain form, replayed under a plan whose own calls would take parts."""
+    hq, hkv = HEADS[D][0]
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        pg.check(pg.pg_test_shared_form(2))
+        qo = [1, 1, 1, 1] if decode else [40, 1, 9, 2]
+        a = kind(D, hq, hkv, qo, [0, 15, 40, 8], [(2, 30), (2, 2)], seed=1, stream=stream).build()
+        a.attend()
+        stream.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            a.attend()
+        pg.check(pg.pg_test_shared_form(1))
+        total, own = len(a.ids), [0, 15, 40, 8]
+        qb = qo if decode else [2, 9, 1, 40]
+        own[0] += 16 * (total - 45 - sum(-(-(o + q) // 16) for o, q in zip(own, qb)))
+        b = kind(D, hq, hkv, qb, own, [(1, 3), (3, 14)], seed=2, stream=stream)
+        assert len(b.ids) == total and b.P == a.P
+        pg.check(b.replan(a.plan)[0])
+        a.q.copy_(b.q_cpu)
+        if kind is Q8:
+            a.codes.copy_(b.codes_cpu)
+            a.scales.copy_(b.scales_cpu)
+        else:
+            a.pool.copy_(b.pool_cpu)
+        a.out.fill_(float("nan"))
+        a.ws.fill_(0xFF)
+        g.replay()
+        stream.synchronize()
+        assert pg.pg_device_status(stream) == pg.PG_OK
+        b.out, b.lse = a.out, a.lse
+        b.check()
+    a.close()

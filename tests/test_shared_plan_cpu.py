@@ -56,6 +56,12 @@ def test_null_plan_pointer_and_sizes():
         assert f(None) == 0
 
 
+def test_form_hook_refuses_other_numbers():
+    for form in (-1, 3):
+        assert pg.pg_test_shared_form(form) == pg.PG_ERR_ARG
+    assert pg.pg_test_shared_form(0) == pg.PG_OK
+
+
 def test_null_plan_calls():
     z = pg.pg_q8_pool_t()
     p = pg.pg_pool_t()
