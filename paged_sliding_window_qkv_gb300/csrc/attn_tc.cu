@@ -1220,12 +1220,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  // (launch_dependents above: a decode kernel, whose CTAs allocate alone, may take over an SM that this CTA
-  // leaves while its pair still frees; neither leaves before both have)
-  if constexpr (BC) {
-    __syncthreads();
-    cluster_sync();
-  }
 }
 
 // ------------------------------------------------------------------ host side
