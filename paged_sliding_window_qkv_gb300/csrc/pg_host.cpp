@@ -419,9 +419,9 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       // How long a part is (in steps of 64 keys, or a page; a group is cut into as few of one length):
       // every candidate costs rounds of units over the clusters, each as long as its key tiles, a start and
       // an epilogue. A decode step's own keys run beside the parts, on SMs left free for them, where that
-      // ends sooner: a CTA takes about 8 us to begin and end and 6.5 for a tile of 256 KB, half of that in
-      // 8 bits.
-      auto own_us = [&](int32_t on) { return 8 + (set == 0 ? 6.5 : 3.25) * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
+      // ends sooner: a CTA takes about 8 us to begin and end and 6.5 for a tile of 128 keys at head_dim 512,
+      // 4 in 8 bits.
+      auto own_us = [&](int32_t on) { return 8 + (set == 0 ? 6.5 : 4.0) * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
       const double own_tc = all_one ? 0 : kLater + tc_load_us(ptab2, (int64_t)ptab2.size() / 8, cta, heads, sms / 2, dx);
       int64_t longest = 1;
       double best = 0;

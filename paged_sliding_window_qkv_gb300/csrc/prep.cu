@@ -188,20 +188,60 @@ __device__ __forceinline__ void store_rotated(const RowIn& x, float inv, const f
       make_uint4(yb[0], yb[1], yb[2], yb[3]);
 }
 
-// The lane's 16 elements of a result row, quantised with the other LPR - 1 lanes of the row (every
-// lane of the warp takes part; `live` rows are stored).
-template <int LPR>
-__device__ __forceinline__ void store_q8(float2* y, bool live, const Q8Dev& q8, int64_t row, int j, int D) {
-  const int32_t e = q8_exponent<LPR, 8>(y);
+// The exponent of a staged row in 64 bits from its raw elements: their largest result u against the norm, by
+// u^2 > (448 * 2^e)^2 (mean + eps). Every lane of the warp takes part.
+template <int LPR, bool ROTATED>
+__device__ __forceinline__ int32_t exponent64(const unsigned char* raw, int j, const __nv_bfloat16* w,
+                                              const float* rope, float eps) {
+  constexpr int D = 16 * LPR;
+  const __nv_bfloat16* const x = reinterpret_cast<const __nv_bfloat16*>(raw);
+  double ss = 0, top = 0;
+#pragma unroll 1
+  for (int k = 8 * j; k < 8 * j + 8; ++k) {
+    double p = __bfloat162float(x[k]), q = __bfloat162float(x[k + D / 2]);
+    ss += p * p + q * q;
+    if (ROTATED) {
+      const double c = rope[k], s = rope[k + D / 2];
+      p *= __bfloat162float(w[k]);
+      q *= __bfloat162float(w[k + D / 2]);
+      const double u = p * c - q * s;
+      q = q * c + p * s;
+      p = u;
+    }
+    top = fmax(top, fmax(fabs(p), fabs(q)));
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) {
+    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    top = fmax(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  const double norm = ss * (1.0 / D) + (double)eps;
+  const int32_t lo = q8_exponent_of((float)top * rsqrtf((float)norm) * (1.f - 0x1p-20f));
+  const double border = 448.0 * (double)q8_pow2(lo);
+  return top * top > border * border * norm ? min(lo + 1, kQ8Most) : lo;
+}
+
+// The lane's 16 elements of a row under exponent e.
+__device__ __forceinline__ void store_codes(const float2* y, int32_t e, const Q8Dev& q8, int64_t row, int j, int D) {
   const float inv = q8_pow2(-e);
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[k] = q8_codes(y[2 * k], y[2 * k + 1], inv);
-  if (!live) return;
   uint8_t* const dst = q8.codes + row * D + 8 * j;
   *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(w[2], w[3]);
   if (j == 0) q8.scales[row] = (uint8_t)(e + 127);
+}
+// The lane's 16 elements of a result row, quantised with the other LPR - 1 lanes of the row (every
+// lane of the warp takes part; `live` rows are stored). Where the largest stands so near 448 times a power of
+// two that 32 bits do not tell the side (one row in some 200,000) it returns true, for settle_row.
+template <int LPR>
+__device__ __forceinline__ bool store_q8(float2* y, bool live, const Q8Dev& q8, int64_t row, int j, int D) {
+  const float m = q8_largest<LPR, 8>(y);
+  if (live) store_codes(y, q8_exponent_of(m), q8, row, j, D);
+  // (448 * 2^e has the significand 1.75. m is off by at most 9 * 2^-23 of itself, 16 steps there: half of the 14
+  // roundings of the sum of squares, 2 of rsqrtf, a product's, and a rotation's three at twice the result.)
+  return live && ((__float_as_uint(m) - 0x600000u + 16u) & 0x7FFFFFu) <= 32u;
 }
 __device__ __forceinline__ void plain_row(const RowIn& x, float inv, float2* y) {
   const float2 iv = make_float2(inv, inv);
@@ -220,6 +260,23 @@ __device__ __forceinline__ void rotated_row(const RowIn& x, float inv, const flo
     y[k] = __fmul2_rn(__ffma2_rn(ua, c[k], __fmul2_rn(ub, ns[k])), iv);
     y[4 + k] = __fmul2_rn(__ffma2_rn(ub, c[k], __fmul2_rn(ua, s[k])), iv);
   }
+}
+
+// Stores such a row again under its exponent in 64 bits. Apart from the first form, so that its registers come
+// behind that one's: 16384 tokens at head_dim 256 take 92 us, 86 without it, 136 with a call in its place.
+template <int LPR, bool ROTATED>
+__device__ __forceinline__ void settle_row(bool near, const unsigned char* raw, const PrepArgs& a, const float* rope,
+                                           const float2* wa, const float2* wb, const float2* c, const float2* s,
+                                           const float2* ns, int64_t row, int j) {
+  constexpr int D = 16 * LPR;
+  if (!__any_sync(0xffffffffu, near)) return;
+  const int32_t e = exponent64<LPR, ROTATED>(raw, j, a.w_k, rope, a.eps);
+  RowIn x;
+  float2 y[8];
+  const float inv = load_row<LPR>(raw, j, D, 1.f / D, a.eps, &x);
+  if (ROTATED) rotated_row(x, inv, wa, wb, c, s, ns, y);
+  else plain_row(x, inv, y);
+  if (near) store_codes(y, e, a.q8, row, j, D);
 }
 
 // Stage layout: raw rows [Hq Q rows][Hkv K rows][Hkv V rows (D = 256 only)] of D bf16, then the
@@ -384,11 +441,16 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
             const int64_t row = (m.slot + r * a.pool.stride_head) / D;
             float2 y[8];
             rotated_row(x, inv, wka, wkb, c, sn, ns, y);
-            store_q8<LPR>(y, live, a.q8, row, j, D);
+            const bool k_near = store_q8<LPR>(y, live, a.q8, row, j, D);
+            bool v_near = false;
             if (D == 512) {
               plain_row(x, inv, y);
-              store_q8<LPR>(y, live, a.q8, row + a.pool.stride_kv / D, j, D);
+              v_near = store_q8<LPR>(y, live, a.q8, row + a.pool.stride_kv / D, j, D);
             }
+            const unsigned char* const raw = sg + (size_t)(Hq + (live ? r : r0)) * (D * 2);
+            settle_row<LPR, true>(k_near, raw, a, reinterpret_cast<const float*>(sg + rows_bytes), wka, wkb, c, sn, ns, row, j);
+            if (D == 512)
+              settle_row<LPR, false>(v_near, raw, a, nullptr, wka, wkb, c, sn, ns, row + a.pool.stride_kv / D, j);
           } else if (live) {
             __nv_bfloat16* dst = kbase + (int64_t)r * a.pool.stride_head;
             store_rotated(x, inv, wka, wkb, c, sn, ns, dst, j, D2);
@@ -408,7 +470,10 @@ prep_kernel(PrepArgs a, int32_t nst, uint32_t stage_bytes) {
             if constexpr (Q8) {
               float2 y[8];
               plain_row(x, inv, y);
-              store_q8<LPR>(y, live, a.q8, (m.slot + a.pool.stride_kv + r * a.pool.stride_head) / D, j, D);
+              const int64_t row = (m.slot + a.pool.stride_kv + r * a.pool.stride_head) / D;
+              const bool near = store_q8<LPR>(y, live, a.q8, row, j, D);
+              settle_row<LPR, false>(near, sg + (size_t)(Hq + Hkv + (live ? r : r0)) * (D * 2), a, nullptr, wka, wkb, c, sn,
+                                     ns, row, j);
             } else if (live) store_plain(x, inv, kbase + a.pool.stride_kv + (int64_t)r * a.pool.stride_head, j, D2);
           }
         }

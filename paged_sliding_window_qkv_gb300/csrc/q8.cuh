@@ -26,11 +26,11 @@ __device__ __forceinline__ int32_t q8_exponent_of(float m) {
   return min(max(e, kQ8Least), kQ8Most);
 }
 
-// The exponent of a row spread over LPR consecutive lanes, N pairs a lane. Elements that are not
+// The largest magnitude of a row spread over LPR consecutive lanes, N pairs a lane. Elements that are not
 // finite become NaN (the conversion would turn an infinity into 448) and have no part in it. Every
 // lane of the warp takes part.
 template <int LPR, int N>
-__device__ __forceinline__ int32_t q8_exponent(float2* y) {
+__device__ __forceinline__ float q8_largest(float2* y) {
   auto largest = [&]() {
     float m = 0.f;
 #pragma unroll
@@ -52,7 +52,7 @@ __device__ __forceinline__ int32_t q8_exponent(float2* y) {
     }
     m = reduced();
   }
-  return q8_exponent_of(m);
+  return m;
 }
 
 // Codes of four elements, the first in the low byte.

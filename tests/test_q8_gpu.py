@@ -721,3 +721,52 @@ def test_two_plans_on_two_streams():
         c.reference()
         c.check_attention()
         c.close()
+
+
+def rows_near_a_border(D, count):
+    """Raw rows whose largest element is 14 * (1 + d) in 64 bits with |d| below 2^-24 (14 = 448 / 32): one
+    element a, D - 1 others of two values. Closest first, both sides among them."""
+    mant = 1 + np.arange(128) / 128.0  # bf16 numbers of one octave
+    b1, b2 = mant[:, None], mant[None, :] / 2
+    eps = np.float64(np.float32(1e-6))
+    found = []
+    for a in np.concatenate([mant * 16, mant * 32]):
+        s = (a * a / 196 - eps) * D - a * a  # what the others' squares have to add up to
+        n = np.clip(np.rint((s - (D - 1) * b2 ** 2) / (b1 ** 2 - b2 ** 2 + (b1 == b2))), 0, D - 1)
+        d = a / np.sqrt((a * a + n * b1 ** 2 + (D - 1 - n) * b2 ** 2) / D + eps) / 14 - 1
+        for x, y in zip(*np.nonzero((np.abs(d) < 2.0 ** -24) & (np.abs(d) > 1e-12))):
+            found.append((abs(d[x, y]), d[x, y] > 0, a, mant[x], mant[y] / 2, int(n[x, y])))
+    found.sort()
+    rows = np.zeros((count, D))
+    for r, (_, _, a, p, q, n) in enumerate(found[:count]):
+        rows[r, 0], rows[r, 1:1 + n], rows[r, 1 + n:] = a, p, q
+    assert len(found) >= count and {f[1] for f in found[:count]} == {True, False}
+    return rows
+
+
+@pytest.mark.parametrize("D", [256, 512])
+def test_a_row_at_the_border_has_the_exponent_of_64_bits(D):
+    hq, hkv, T = 2, 2, 48
+    rows = rows_near_a_border(D, T * hkv)
+
+    def edit(raw):
+        for h in range(hkv):
+            at = (hq + h) * D
+            raw[:, at:at + D] = torch.from_numpy(rows[h::hkv]).to(raw.dtype)
+            if D == 256:
+                at = (hq + hkv + h) * D
+                raw[:, at:at + D] = torch.from_numpy(rows[::-1][h::hkv].copy()).to(raw.dtype)
+
+    p = Prep(D, hq, hkv, [T], [0], edit=edit)
+    p.w[1] = 1
+    p.cos.fill_(1.0)
+    p.sin.fill_(0.0)
+    p.run()
+    ok()
+    p.check()
+    page, off = p.c.rows_of(0)
+    _, (k, _), (v, _) = p.reference()
+    for i, y in enumerate((k, v)):
+        got = p.c.scales.cpu()[0][page, i, :, off].numpy().astype(np.int64) - 127
+        assert (got == exponents(y)).all(), (i, int((got != exponents(y)).sum()))
+    p.c.close()
