@@ -10,7 +10,7 @@
 //   s = 2^(e + k) (S0 + S1 / 16)            k: the exponent of the key's K row
 //   P = 2^(s + v - R) = p0 + p1 / 16 + p2 / 256   v: of its V row; s in log2 units
 //   O^T = V^T [p0 p1 p2]^T  (M = 128 output columns, N = the rows three times, K = 32 keys a step)
-// Two terms hold a bf16 query exactly (8 bits of significand) down to 2^-15 of the row's largest
+// Two terms hold a bf16 query exactly (8 bits of significand) down to 2^-13 of the row's largest
 // element; three hold a weight to 12 bits. The terms only widen N, which at these sizes costs nothing:
 // an instruction's time is that of reading A (the codes) from shared memory.
 //
@@ -30,6 +30,9 @@
 //   (8-11)      Groups above 8 take two such sets, which share nothing but the tiles. (One set over
 //               16 rows took some 5,000 cycles a tile, as long as the tile's bytes; and references
 //               found by a reduction a row 9,000 where they moved: 146 us on the 64 requests below.)
+// Measured: 64 requests of up to 16384 keys at head_dim 512, 16 heads, 104 us (5.6 TB/s over the call; the read-back and
+// the bf16 kernel take 450); 64 under a window of 1023 at head_dim 256, 16 / 8 heads, 53 us (317); one of 8001
+// keys at head_dim 512 17 us (latency of two launches). Bound by HBM, and by CTAs that end unevenly.
 // Every wait is bounded, as there.
 #include "bounded_decode.cuh"
 #include "q8.cuh"

@@ -9,7 +9,8 @@
 //   M = max(m_i, lse / ln 2),  w_i = l_i 2^(m_i - M),  w = 2^(lse / ln 2 - M)
 //   out = (sum w_i o_i + w o) / (sum w_i + w),  lse' = (M + log2(sum w_i + w)) ln 2
 // (Of a decode step it is the join of the own keys' records that takes the parts along, in
-// attn_bounded_decode.cu; this kernel is for steps of more tokens.)
+// attn_bounded_decode.cu; this kernel is for steps of more tokens.) Bound by the records' bytes: a row a warp, everything
+// on its way before it is added, 23 us of 8 prompts behind 4096 keys at head_dim 512 (76 with a block of columns).
 #include "pg_internal.h"
 
 #include <cuda_bf16.h>
