@@ -698,6 +698,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           for (int e = 0; e < 8; ++e) w[8 * q + e] = 0u;
         }
       }
+      __syncwarp();  // (a tensor-memory access is one instruction of a whole warp: it meets after lane branches)
       tmem_st32(tl + kTmQ + d0 / 2, w);
       tmem_st32(tl + kTmQ + d0 / 2 + 32, w + 32);
       tmem_wait_st();
@@ -1101,6 +1102,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll 1
           for (int c = 0; c < kDV / 64; ++c) {
             uint32_t o[32];
+            __syncwarp();
             tmem_ld32(tl + kTmO + h * (kDV / 2) + c * 32, o);
             tmem_wait_ld();
             if (rvalid) {
@@ -1118,6 +1120,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (a.lse && rvalid && h == 0 && u.dh == 0)  // both output halves of hd512 agree
           a.lse[(int64_t)(u.q0 + u.tok0 + (row >> gsh)) * Hq + u.g * G + (row & gmask)] =
               some ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        __syncwarp();
         if (DQK == 256) {
           // each 64-column half of this warp's 128 columns goes through the transposition
           // buffer (free: every PV of the unit has completed) and out in coalesced 16-byte
@@ -1163,6 +1166,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           for (int c2 = 0; c2 < kDV / 64; c2 += 2) {
             // two 32-column loads in flight per wait
             uint32_t o[64];
+            __syncwarp();
             tmem_ld32(tl + kTmO + h * (kDV / 2) + c2 * 32, o);
             tmem_ld32(tl + kTmO + h * (kDV / 2) + c2 * 32 + 32, o + 32);
             tmem_wait_ld();
