@@ -526,7 +526,7 @@ int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t lay
  * prefixes: groups of consecutive requests whose first keys are the same pages. It is that plan for
  * every other entry (prep, pg_attn_paged_prefill, ...); pg_attn_paged_shared reads a group's prefix
  * once for all its requests, where a cascade of segment plans reads it once a request. Whether that
- * is sooner than every request reading its own list is settled by the plan, from its sizes.
+ * is sooner for a decode step than every request reading its own list is settled by the plan, from its sizes.
  *
  * Inputs as for pg_plan_paged_prefill (every request lists all its pages), plus
  *   group_indptr[num_groups+1]  int64, group_indptr[0] == 0, strictly increasing, last num_req:
@@ -558,7 +558,7 @@ size_t pg_shared_q8_workspace_bytes(const pg_plan_t plan);
  * prefix as one block of rows, cut along the keys where the batch has few rows, each request meets
  * its own keys as in pg_attn_paged_sink, and the parts are joined in fp32 by their normalisers.
  * (What a request's own keys give is rounded to bf16 before the join, a prefix's part is not.)
- * With short prefixes, few requests or long chunks that takes longer than pg_attn_paged_sink over
+ * A decode step of few requests or short prefixes takes longer so than in pg_attn_paged_sink over
  * the same plan (window_left -1, num_sink 0), and the call is that one. The form is the plan's: the
  * same plan gives the same bits each time, and a captured call keeps the form it was captured in.
  *   q, out  [T][Hq][head_dim] bf16, 32-byte aligned;  lse [T][Hq] float32 or NULL

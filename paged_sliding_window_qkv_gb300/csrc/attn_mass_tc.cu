@@ -405,6 +405,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll 1
         for (int cb = 0; cb < kNQ / 2; cb += 64) {
           uint32_t sv[64];
+          __syncwarp();  // (one instruction of the whole warp, behind lane branches)
           tmem_ld32(tl + b * kNQ + cb, sv);
           tmem_ld32(tl + b * kNQ + cb + 32, sv + 32);
           tmem_wait_ld();

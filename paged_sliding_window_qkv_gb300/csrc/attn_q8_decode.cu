@@ -195,6 +195,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     n = find_tiles(args, lane, held, &r, &in_req);
   }
   if (warp == 1) {
+    __syncwarp();  // (lane 0 has set up the barriers)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                  "r"(C::TM_COLS)
                  : "memory");

@@ -143,6 +143,7 @@ struct TcArgs {
   float* part_o;
   float* part_ml;
   const int32_t* part_row;
+  int32_t weights;        // BC: a weight pass follows
   int* status;
   uint64_t wait_ns;       // limit of every bounded wait
   int32_t test_withhold;  // test hook: the leader's K producer withholds its first arrival
@@ -330,12 +331,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   cluster_sync();  // both CTAs' barriers exist before either CTA signals the other
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // BC: the pass that accumulates weights may start on SMs that this one has left (it waits for
+  // BC with weights: the pass that accumulates them may start on SMs that this one has left (it waits for
   // this grid's completion before it reads lse)
   // (PART: the set-up above overlaps the end of the stream's previous kernel; the own keys' decode, which
   // does not wait for this grid, may start once that kernel has ended)
   if constexpr (PART) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if constexpr (BC) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (PART || (BC && a.weights)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------ producers
@@ -1296,6 +1297,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   t.part_o = a.part_o;
   t.part_ml = a.part_ml;
   t.part_row = a.part_row;
+  t.weights = a.stats.mass != nullptr;
   t.status = a.status;
   t.wait_ns = a.wait_ns;
   t.test_withhold = a.test_withhold;

@@ -144,41 +144,19 @@ void free_stage(PlanStage* st) {
 }
 
 // What the kernels of a shared plan take, in us by head_dim (256, 512) and set (bf16, 8-bit pools), as
-// measured: batches of 1..64 requests, prefixes of 128..8192 keys, 16 and 8 query heads. (Over 160 of them
-// the parts alone took 1.29 times the better form's time in the mean, the form chosen by these 1.00.)
+// measured: decode steps of 1..64 requests, prefixes of 128..8192 keys, 16 and 8 query heads. (Over 112 of them,
+// on either kind of pool, the parts alone took 1.30 times the better form's time in the mean, the form chosen
+// by these 1.00.)
 struct SharedCost {
-  double start[2] = {9, 11};                          // of a first tensor-core prefill kernel; a later one kLater
+  double start[2] = {9, 11};                          // of the parts' kernel
   double tile[2] = {0.7, 1.05}, ends[2] = {4.8, 3.5};  // of its units: 64 keys, start and epilogue
   double dec_start[2][2] = {{9.5, 12.5}, {11, 13}};   // of a decode kernel with its join
   double dec_l2[2][2] = {{1.65, 3.4}, {0.85, 2.8}};   // of its tiles of 128 keys: another request's too,
   double dec_dram[2][2] = {{2.6, 5.5}, {1.25, 3.4}};  // or a request's alone
 };
 constexpr SharedCost kCost;
-constexpr double kLater = 6, kJoin = 4, kReadBack = 3.5, kBytesPerUs = 6.5e6;
+constexpr double kJoin = 4, kReadBack = 3.5, kBytesPerUs = 6.5e6;
 std::atomic<int32_t> g_test_shared{0};  // test hook: 1 parts, 2 plain, whatever the estimate says
-
-// The time of the longest-loaded cluster of a prefill kernel (attn_tc.cu's rounds): the table's first
-// pairs in their order, `heads` units each.
-double tc_load_us(const std::vector<int32_t>& tab, int64_t pairs, int32_t tile, int64_t heads, int64_t clusters,
-                  int32_t d) {
-  const int64_t units = pairs * heads;
-  std::vector<double> load((size_t)std::max<int64_t>(clusters, 1), 0.0);
-  const int64_t n = (int64_t)load.size();
-  double sum = 0, most = 0;
-  for (int64_t i = 0; i < pairs; ++i) {
-    const int32_t* e = tab.data() + 8 * (size_t)i;
-    const int64_t end = (int64_t)e[3] + std::min<int64_t>((int64_t)e[0] + 2 * (int64_t)tile, e[2]);
-    const double us = (double)((std::min<int64_t>(end, e[6]) - e[7] + 63) / 64) * kCost.tile[d] + kCost.ends[d];
-    sum += us * (double)heads;
-    for (int64_t w = i * heads; units <= 65536 && w < (i + 1) * heads; ++w) {
-      const int64_t at = w % n;
-      double& l = load[(size_t)((w / n) & 1 ? n - 1 - at : at)];
-      l += us;
-      most = std::max(most, l);
-    }
-  }
-  return units <= 65536 ? most : sum / (double)n;  // (that many units even out)
-}
 
 // Groups of consecutive requests that share their first keys.
 struct Groups {
@@ -423,7 +401,6 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       // ends sooner: a CTA takes about 8 us to begin and end and 6.5 for a tile of 128 keys at head_dim 512,
       // 4 in 8 bits.
       auto own_us = [&](int32_t on) { return 8 + (set == 0 ? 6.5 : 4.0) * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
-      const double own_tc = all_one ? 0 : kLater + tc_load_us(ptab2, (int64_t)ptab2.size() / 8, cta, heads, sms / 2, dx);
       int64_t longest = 1;
       double best = 0;
       const int64_t most_steps = ((int64_t)most_len + step - 1) / step;
@@ -438,7 +415,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
           const double parts_us = kCost.start[dx] + (double)((units + clusters - 1) / clusters) *
                                                         ((double)(len * step / 64) * kCost.tile[dx] + kCost.ends[dx]);
           const double cost =
-              join + (!all_one ? parts_us + own_tc : on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on)));
+              join + (!all_one ? parts_us : on == 0 ? parts_us + own_us(sms) : std::max(parts_us, own_us(on)));
           if (best == 0 || cost < best) {
             best = cost;
             longest = len;
@@ -446,25 +423,20 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
           }
         }
       }
-      // Against every request reading its prefix itself, behind the first one's from L2: short prefixes,
-      // few requests, long chunks (whose products, not their reads, take the time).
-      const double page_us = 6.0 * Hkv * ps * D / kBytesPerUs;  // a page's codes read and its rows written
-      double plain = 0;
+      // Against every request of a decode step reading its prefix itself, behind the first one's from L2: short
+      // prefixes, few requests.
+      p.plain = most_len == 0;
       if (all_one) {
         const double n = (double)(tiles * Hkv) / sms, l2 = (double)(tiles_l2 * Hkv) / sms;
-        plain = kCost.dec_start[set][dx] +
-                (l2 * kCost.dec_l2[set][dx] + (n - l2) * kCost.dec_dram[set][dx]) * std::ceil(n) / std::max(n, 1e-9);
-      } else {
-        plain = kCost.start[dx] + tc_load_us(ptab, npairs, cta, heads, sms / 2, dx);
-      }
-      const bool read_back = set == 1 && !all_one;
-      if (set == 1) best += kReadBack + (double)pre_pages.size() * page_us;
-      if (read_back) {
-        best += kReadBack + (double)pages2.size() * page_us;
-        plain += kReadBack + (double)NP * page_us;
+        const double plain =
+            kCost.dec_start[set][dx] +
+            (l2 * kCost.dec_l2[set][dx] + (n - l2) * kCost.dec_dram[set][dx]) * std::ceil(n) / std::max(n, 1e-9);
+        // (8-bit pools: a page's codes read and its rows written)
+        if (set == 1) best += kReadBack + (double)pre_pages.size() * 6 * Hkv * ps * D / kBytesPerUs;
+        p.plain = p.plain || plain <= best + kJoin;
       }
       const int32_t forced = g_test_shared.load(std::memory_order_relaxed);
-      p.plain = most_len == 0 || (forced == 0 ? plain <= best + kJoin : forced == 2);
+      if (forced != 0 && most_len > 0) p.plain = forced == 2;
       p.tok.assign((size_t)T, 0);
       std::vector<int32_t> tab, row;
       int32_t pages = 0;  // of the prefixes before

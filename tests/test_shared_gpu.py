@@ -436,7 +436,7 @@ def test_both_forms_and_the_choice(kind, D, qo, own, groups):
     ([1], [100], [(1, 8)], True),             # nothing to share
     ([1] * 3, [10, 0, 99], [(3, 0)], True),   # no prefix
     ([1] * 64, [20] * 64, [(64, 256)], False),
-    ([256] * 8, [0] * 8, [(8, 32)], True),    # long chunks behind a short prefix
+    ([256] * 8, [0] * 8, [(8, 32)], False),   # (steps of more tokens take the parts)
     ([2] * 32, [64] * 32, [(32, 256)], False),
 ])
 def test_the_plan_chooses_by_size(kind, qo, own, groups, plain):
