@@ -333,9 +333,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const uint32_t tmem = *tmem_slot;
   // BC with weights: the pass that accumulates them may start on SMs that this one has left (it waits for
   // this grid's completion before it reads lse)
-  // (BC: the set-up above overlaps the end of the stream's previous kernel. PART: the own keys' decode, which
+  // (PART: the set-up above overlaps the end of the stream's previous kernel; the own keys' decode, which
   // does not wait for this grid, may start once that kernel has ended)
-  if constexpr (BC) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (PART) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (PART || (BC && a.weights)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 || warp == 10) {
@@ -1336,7 +1336,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = BC ? 2 : 1;
+  cfg.numAttrs = PART ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, BC, PART>, tq, tkv, tv, t);
   if (e != cudaSuccess) return e;
   count_launch();
