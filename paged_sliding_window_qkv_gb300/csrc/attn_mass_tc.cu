@@ -228,13 +228,15 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     *abort_flag = 0;
     fence_barrier_init();
   }
+  // (both CTAs run before either takes part in the pair's allocation, see attn_tc.cu)
+  __syncwarp();
+  cluster_sync();
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int32_t TQ = kNQ / G;  // tokens per query tile
@@ -482,14 +484,17 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1 && lane == 0) {
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(DRAIN, 0)) {
-      if (globaltimer() - t0 > a.wait_ns) {
-        atomicOr(a.status, kStatusTimeout);
-        break;
+  if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(DRAIN, 0)) {
+        if (globaltimer() - t0 > a.wait_ns) {
+          atomicOr(a.status, kStatusTimeout);
+          break;
+        }
       }
     }
+    __syncwarp();
   }
   __syncthreads();
   cluster_sync();
@@ -497,6 +502,8 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  __syncwarp();
+  cluster_sync();  // neither leaves before both have freed their tensor memory
 }
 
 // Block s: the segment that starts in cluster s and goes on past it, a thread per key.

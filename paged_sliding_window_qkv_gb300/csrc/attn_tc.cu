@@ -322,13 +322,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     *abort_flag = 0;
     fence_barrier_init();
   }
+  // Both CTAs run, and their barriers exist, before either signals the other or takes part in the pair's
+  // allocation: an access to the other CTA is defined only once that CTA has begun.
+  __syncwarp();
+  cluster_sync();
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before either CTA signals the other
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // BC with weights: the pass that accumulates them may start on SMs that this one has left (it waits for
@@ -659,6 +662,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // sum. At the end of a unit the warps store the next unit's Q columns into TMEM (the QK
     // MMAs of this unit are complete), so its first QK products overlap this unit's epilogue.
     // Arrivals that the leader's MMA warps wait on go to the leader's barriers.
+    // A tensor-memory access is one instruction of a whole warp: behind waits and branches of single lanes
+    // the warp meets first.
     const int quarter = warp & 3;
     const int h = (warp - 2) >> 2;
     const int row = quarter * 32 + lane;
@@ -699,7 +704,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           for (int e = 0; e < 8; ++e) w[8 * q + e] = 0u;
         }
       }
-      __syncwarp();  // (a tensor-memory access is one instruction of a whole warp: it meets after lane branches)
+      __syncwarp();
       tmem_st32(tl + kTmQ + d0 / 2, w);
       tmem_st32(tl + kTmQ + d0 / 2 + 32, w + 32);
       tmem_wait_st();
@@ -710,6 +715,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     auto copy_q256 = [&](int32_t k) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(QSFULL, k & 1, wc))) return false;
       const unsigned char* src = gbase + (sQ - base) + row * 128;
+      __syncwarp();
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t w[32];
@@ -777,6 +783,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const int b = JJ & 1;  // this warp's S and P buffers
           if (!__all_sync(0xffffffffu, mbar_wait_inline(SFULL + 8 * b, (JJ >> 1) & 1, wc))) { ok = false; break; }
           tc_fence_after();
+          __syncwarp();
           uint32_t sv[kBN];
           tmem_ld32(tl + kTmS + b * kBN, sv);
           tmem_ld32(tl + kTmS + b * kBN + 32, sv + 32);
@@ -880,6 +887,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int32_t jp = JJ - 1;
             if (!__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jp % NSB), (jp / NSB) & 1, wc))) { ok = false; break; }
             tc_fence_after();
+            __syncwarp();
             for (int c = 0; c < kDV / 32; ++c) {
               uint32_t o[32];
               const uint32_t col = kTmO + c * 32;
@@ -918,6 +926,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int b = JJ % NSB;
         if (!__all_sync(0xffffffffu, mbar_wait_inline(SFULL + 8 * b, (JJ / NSB) & 1, wc))) { ok = false; break; }
         tc_fence_after();
+        __syncwarp();
         float mx;
         // this thread's 32 keys (masked keys: -inf); log2 units are t * tscale
         float t[HC];
@@ -983,6 +992,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const int32_t jp = JJ - 1;
           if (!__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jp % NSB), (jp / NSB) & 1, wc))) { ok = false; break; }
           tc_fence_after();
+          __syncwarp();
           for (int c = 0; c < kDV / 64; ++c) {
             uint32_t o[32];
             const uint32_t col = kTmO + h * (kDV / 2) + c * 32;
@@ -1207,24 +1217,30 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1 && lane == 0) {
-    // every MMA of the pair has completed once the leader's final commits have arrived (in
-    // both CTAs); a wait that runs out is reported like any other
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(DRAIN, 0)) {
-      if (globaltimer() - t0 > a.wait_ns) {
-        atomicOr(a.status, kStatusTimeout);
-        break;
+  if (warp == 1) {
+    if (lane == 0) {
+      // every MMA of the pair has completed once the leader's final commits have arrived (in
+      // both CTAs); a wait that runs out is reported like any other
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(DRAIN, 0)) {
+        if (globaltimer() - t0 > a.wait_ns) {
+          atomicOr(a.status, kStatusTimeout);
+          break;
+        }
       }
     }
+    __syncwarp();
   }
   __syncthreads();
-  // neither CTA frees its tensor memory or leaves while the other may still use the pair's
+  // neither CTA frees its tensor memory while the other may still use the pair's, or leaves before
+  // both have freed it (the release is the pair's, as the allocation is)
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  __syncwarp();
+  cluster_sync();
 }
 
 // ------------------------------------------------------------------ host side
