@@ -363,8 +363,6 @@ size_t pg_sink_workspace_bytes(const pg_plan_t plan);
  *   q, out: as for pg_attn_paged_prefill
  *   workspace: pg_sink_workspace_bytes(plan), 16-byte aligned. ws_bytes >= pg_workspace_bytes(plan)
  *        is enough; a decode step of head_dim 512 may then run on fewer SMs.
- * Steps of more than a token a request at head_dim 512 under a window with sinks do not run on the tensor
- * cores' newer form and take longer than with num_sink 0 (here, in pg_attn_paged_mass and pg_attn_paged_q8).
  * A key that some rows of its tile see and others do not takes part with weight 0 in the latter:
  * a non-finite V row among the keys held makes every row of a prefill tile that spans it
  * non-finite. K rows have no such effect, and in decode only visible keys take part.

@@ -150,18 +150,14 @@ attn_split_kernel(AttnArgs a) {
     ntok = 1;
     chunk = blockIdx.z;
   } else {
-    const int32_t w = (int32_t)blockIdx.x / a.work_parts;
-    if (pl.live && w >= pl.live[0]) return;
-    r = pl.work_req[w];
-    tok0 = pl.work_tok0[w] + (int32_t)blockIdx.x % a.work_parts * a.cta_tile_q;
+    if (pl.live && (int32_t)blockIdx.x >= pl.live[0]) return;
+    r = pl.work_req[blockIdx.x];
+    tok0 = pl.work_tok0[blockIdx.x];
     ntok = 0;
   }
   const int32_t q0 = pl.qo_indptr[r];
   const int32_t qo_len = pl.qo_indptr[r + 1] - q0;
-  if (!C::DECODE) {
-    ntok = min(a.cta_tile_q, qo_len - tok0);
-    if (ntok <= 0) return;
-  }
+  if (!C::DECODE) ntok = min(a.cta_tile_q, qo_len - tok0);
   const int32_t kvp0 = pl.kv_page_indptr[r], kvp1 = pl.kv_page_indptr[r + 1];
   const int32_t ps = a.pool.page_size;
   const int32_t sp = pl.start_pos[r];
@@ -622,19 +618,11 @@ int32_t attn_kernel_cta_tile_q(int32_t head_dim, int32_t group, int32_t page_siz
 
 int32_t attn_kernel_kv_chunk(int32_t head_dim) { return head_dim == 512 ? 512 : 256; }
 
-cudaError_t launch_attn_prefill(const AttnArgs& args, int32_t head_dim, cudaStream_t stream) {
-  if (args.plan.num_work == 0) return cudaSuccess;
-  if (attn_tc_takes(args, head_dim)) return launch_attn_prefill_tc(args, head_dim, stream);
-  AttnArgs a = args;
-  if (attn_tc_supported(head_dim, a.group, a.pool.page_size)) {
-    // the plan's work items are of that kernel's rows: each goes to as many CTAs as have them
-    const int32_t tile = (head_dim == 256 ? Pre256::BM : Pre512::BM) / a.group;
-    a.work_parts = a.cta_tile_q / tile;
-    a.cta_tile_q = tile;
-  }
-  const int64_t work = (int64_t)a.plan.num_work * a.work_parts;
-  if (work > INT32_MAX) return cudaErrorInvalidConfiguration;
-  dim3 grid((unsigned)work, a.pool.num_kv_heads, 1);
+cudaError_t launch_attn_prefill(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
+  if (a.plan.num_work == 0) return cudaSuccess;
+  if (attn_tc_supported(head_dim, a.group, a.pool.page_size))
+    return launch_attn_prefill_tc(a, head_dim, stream);
+  dim3 grid(a.plan.num_work, a.pool.num_kv_heads, 1);
   if (a.bounded)
     return head_dim == 256 ? launch_split<Pre256, true>(a, grid, stream)
                            : launch_split<Pre512, true>(a, grid, stream);

@@ -44,18 +44,13 @@
 // O holds 256 output columns: for head_dim 512 each query tile is two units, each computing
 // the full 512-wide S and half of O. The TMEM map is described at TcCfg.
 //
-// Forms of the bounded caches (Form):
-//   kSums   the row sum adds the unrounded weights (see attn_split.cu), and page boxes that no row sees
-//           are not read.
-//   kSinks  (head_dim 256) kSums, and the first num_sink positions stay visible behind the window: a unit
-//           walks its sink tiles and then its window tiles (bounded.cuh; one run where they meet).
-//   kPart   kSums for one part of a row's keys: units are (pair of tiles, run of keys), and a row leaves
-//           its mean in fp32 with its reference and sum, at the part's rows of a record array, for a later
-//           join (shared.cu). A pair-table entry names its rows' query tokens and its run of keys; part_row
-//           its records.
-// At head_dim 512 there is no kSinks: launches of its walk over long ragged units ended in SM exceptions
-// ("misaligned address", five in some 90,000) whose cause reading did not show, where the plain walk has
-// none on record. A window with sinks goes to attn_split.cu there.
+// BC is the bounded-cache form: the first num_sink positions stay visible behind the window, so
+// a unit walks its sink tiles and then its window tiles (bounded.cuh; one run where they meet),
+// and the row sum adds the unrounded weights (see attn_split.cu).
+//
+// PART (with BC) is one part of a row's keys: units are (pair of tiles, run of keys), and a row leaves
+// its mean in fp32 with its reference and sum, at the part's rows of a record array, for a later join
+// (shared.cu). A pair-table entry names its rows' query tokens and its run of keys; part_row its records.
 //
 // Every wait is bounded (two seconds of %globaltimer unless the launch passes a shorter limit);
 // a wait that runs out sets the device status word, makes the CTA drain and free its tensor
@@ -143,18 +138,16 @@ struct TcArgs {
   int32_t page_size, num_pages, num_kv_heads, box_rows_k, box_rows_v;
   float scale_log2;
   float* lse;  // optional [T][Hq] natural-log normaliser of each row (null: not written)
-  // kPart: records of a pair-table entry's token t at row part_row[entry] + t: mean [row][Hq][D] and
+  // PART: records of a pair-table entry's token t at row part_row[entry] + t: mean [row][Hq][D] and
   // (reference, sum) [row][Hq][2]; part_o is 32-byte aligned
   float* part_o;
   float* part_ml;
   const int32_t* part_row;
-  int32_t weights;        // bounded caches: a weight pass follows
+  int32_t weights;        // BC: a weight pass follows
   int* status;
   uint64_t wait_ns;       // limit of every bounded wait
   int32_t test_withhold;  // test hook: the leader's K producer withholds its first arrival
 };
-
-enum Form { kPlain, kSums, kSinks, kPart };
 
 // ------------------------------------------------------------------ kernel
 // One work unit = (pair of adjacent query tiles of one request, KV head, 256-column part of the
@@ -164,29 +157,28 @@ struct TcUnit {
   int32_t q0, tok0, ntok;  // this CTA's query tile: request's first token, tile start, tokens (0: none)
   // keys held: positions [kv_start, kv_len); key tiles start kb0 + 64 t, 64-aligned from kv_start
   int32_t kvp0, kvp1, kv_len, kv_start, sp, kb0, ntiles, g, dh;
-  int32_t ns;  // kSinks: the first ns tiles are sink tiles, aligned from kv_start
-  int32_t prow;      // kPart: the entry's first record row
-  int32_t lo, sink;  // some row of the pair sees keys [lo, ...) and (kSinks) those below sink
-  template <Form F>
+  int32_t ns;  // BC: the first ns tiles are sink tiles, aligned from kv_start
+  int32_t prow;      // PART: the entry's first record row
+  int32_t lo, sink;  // BC: some row of the pair sees keys [lo, ...) and those below sink
+  template <bool BC>
   __device__ __forceinline__ int32_t key(int32_t t) const {  // first key of the t-th tile
-    return F == kSinks && t < ns ? kv_start + t * kBN : kb0 + (F == kSinks ? t - ns : t) * kBN;
+    return BC && t < ns ? kv_start + t * kBN : kb0 + (BC ? t - ns : t) * kBN;
   }
-  // First key of the page box that stands at key ks of the t-th tile. Bounded caches: a box before the
-  // window (behind the sinks), which no row sees, is not read (its page may be someone else's by now): the
+  // First key of the page box that stands at key ks of the t-th tile. BC: a box between the sinks
+  // and the window, which no row sees, is not read (its page may be someone else's by now): the
   // nearest box with a visible key stands in for it, as finite as what the rows see anyway.
-  template <Form F>
+  template <bool BC>
   __device__ __forceinline__ int32_t box_key(int32_t t, int32_t ks, int32_t rows) const {
-    if (F == kPlain || ks + rows > lo) return ks;
-    if (F == kSinks && ks < sink) return ks;
-    return kv_start + (((F == kSinks && t < ns ? sink - 1 : lo) - kv_start) & ~(rows - 1));
+    if (!BC || ks + rows > lo || ks < sink) return ks;
+    return kv_start + (((t < ns ? sink - 1 : lo) - kv_start) & ~(rows - 1));
   }
 };
-template <Form F>
+template <bool BC, bool PART = false>
 __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t ndh, int32_t rank) {
   const PlanDev& pl = a.plan;
   TcUnit u;
   const int32_t pr = w / (a.num_kv_heads * ndh);
-  if constexpr (F == kPart) u.prow = __ldg(a.part_row + pr);
+  if constexpr (PART) u.prow = __ldg(a.part_row + pr);
   u.g = (w / ndh) % a.num_kv_heads;
   u.dh = w % ndh;
   // the pair's entry of the plan's pair table: two 16-byte loads, no dependent lookups
@@ -206,7 +198,7 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
   const int32_t W = a.window_left;
   const int32_t p_first = u.sp + t0, p_last = u.sp + min(t0 + 2 * TQ, len) - 1;
   u.ns = 0;
-  if constexpr (F == kSinks) {
+  if constexpr (BC) {
     const KeyWalk k = key_walk(W, a.num_sink, u.kv_start, u.kv_len, p_first, p_last, kBN);
     u.ns = k.ns;
     u.lo = k.lo;
@@ -217,7 +209,6 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
   }
   const int32_t lo = W >= 0 ? max(u.kv_start, p_first - W) : u.kv_start;
   const int32_t hi = min(p_last + 1, u.kv_len);
-  u.lo = lo;
   // tiles are aligned from the first key held, so a box of page rows never straddles a page
   u.kb0 = u.kv_start + ((lo - u.kv_start) & ~(kBN - 1));
   u.ntiles = hi > u.kb0 ? (hi - u.kb0 + kBN - 1) / kBN : 0;
@@ -226,13 +217,13 @@ __device__ __forceinline__ TcUnit tc_unit(const TcArgs& a, int32_t w, int32_t nd
 // The factor 2^e that moves sums from one reference to another, to be applied with moved(). A
 // reference may be left by up to 2^48 and set 2^64 above the next maximum, so a step can pass
 // 2^-126 while the sums it moves still count (a third tile 2^63 above the first's reference and
-// 2^17 above the second's): the bounded caches' forms apply the root of the factor twice, which loses nothing.
-template <Form F>
-__device__ __forceinline__ float move_factor(float e) { return ex2(F != kPlain ? 0.5f * e : e); }
-template <Form F>
-__device__ __forceinline__ float moved(float x, float f) { return F != kPlain ? (x * f) * f : x * f; }
+// 2^17 above the second's): BC applies the root of the factor twice, which loses nothing.
+template <bool BC>
+__device__ __forceinline__ float move_factor(float e) { return ex2(BC ? 0.5f * e : e); }
+template <bool BC>
+__device__ __forceinline__ float moved(float x, float f) { return BC ? (x * f) * f : x * f; }
 
-// kSinks: the keys of a tile that a row sees: below hi, and from lo on or below sink (all relative to
+// BC: the keys of a tile that a row sees: below hi, and from lo on or below sink (all relative to
 // the tile's first key).
 __device__ __forceinline__ uint64_t tile_bits(int32_t hi, int32_t lo, int32_t sink) {
   return bits_below(hi) & (~bits_below(lo) | bits_below(sink));
@@ -243,14 +234,13 @@ __device__ __forceinline__ void tc_unit_prefetch(const TcArgs& a, int32_t w, int
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a.plan.pair_tab + 8 * pr));
 }
 
-template <int DQK, Form F>
+template <int DQK, bool BC, bool PART>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                const __grid_constant__ CUtensorMap tm_v, TcArgs a) {
   using C = TcCfg<DQK>;
   constexpr int KP = C::KP, NKS = C::NKS, NVR = C::NVR, NS = C::NS;
   constexpr int NSB = C::NSB;
-  constexpr bool BOUNDED = F != kPlain, SINKS = F == kSinks, PART = F == kPart;
   constexpr int32_t NDH = DQK / kDV;
   constexpr uint32_t kTmO = C::TM_O, kTmQ = C::TM_Q, kTmS = C::TM_S;
   extern __shared__ unsigned char smem_raw[];
@@ -344,12 +334,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // Bounded caches with weights: the pass that accumulates them may start on SMs that this one has left (it waits for
+  // BC with weights: the pass that accumulates them may start on SMs that this one has left (it waits for
   // this grid's completion before it reads lse)
-  // (kPart: the set-up above overlaps the end of the stream's previous kernel; the own keys' decode, which
+  // (PART: the set-up above overlaps the end of the stream's previous kernel; the own keys' decode, which
   // does not wait for this grid, may start once that kernel has ended)
   if constexpr (PART) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (PART || (BOUNDED && a.weights)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (PART || (BC && a.weights)) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------ producers
@@ -379,7 +369,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     auto stage_q = [&](int32_t k) -> bool {
       if (lane != 0) return true;
       if (k > 0 && !mbar_wait(QSFREE, (k - 1) & 1, wc)) return false;
-      const TcUnit v = tc_unit<F>(a, unit_at(k), NDH, (int32_t)rank);
+      const TcUnit v = tc_unit<BC>(a, unit_at(k), NDH, (int32_t)rank);
       mbar_expect_tx(QSFULL, v.ntok > 0 ? (uint32_t)C::QS_BYTES : 0u);
       if (v.ntok > 0)
         for (int c = 0; c < 4; ++c)
@@ -390,7 +380,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     int32_t J = 0;  // tiles of this cluster's earlier units
     int32_t ui = 0;
     for (int32_t w = unit_at(0); ok && w < nunits; w = unit_at(++ui)) {
-      const TcUnit u = tc_unit<F>(a, w, NDH, (int32_t)rank);
+      const TcUnit u = tc_unit<BC>(a, w, NDH, (int32_t)rank);
       // head_dim 256: the next unit's Q is staged after this unit's fourth K tile has been issued:
       // that tile's slot wait shows this unit's first QK complete, so its Q has left the staging
       // buffer and the wait for it does not hold up the ring (in units of up to four tiles it
@@ -402,7 +392,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // L2, so the softmax warps' move to that unit waits on L2 rather than DRAM
         if (unit_at(ui + 2) < nunits) tc_unit_prefetch(a, unit_at(ui + 2), NDH);
         if (DQK != 256 && unit_at(ui + 1) < nunits) {
-          const TcUnit un = tc_unit<F>(a, unit_at(ui + 1), NDH, (int32_t)rank);
+          const TcUnit un = tc_unit<BC>(a, unit_at(ui + 1), NDH, (int32_t)rank);
           if (un.ntok > 0)
             for (int c = 0; c < DQK / 64; ++c) tma_prefetch_3d(&tm_q, c * 64, un.g * G, un.q0 + un.tok0);
         }
@@ -434,7 +424,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       auto lookup = [&](int32_t t0) -> int32_t {  // page id of this lane's box in the batch at t0
         const int32_t tt = t0 + my_t;
         if (tt >= u.ntiles) return -1;
-        const int32_t ks = u.template box_key<F>(tt, u.template key<F>(tt) + key_off + my_b * BR, BR);
+        const int32_t ks = u.template box_key<BC>(tt, u.template key<BC>(tt) + key_off + my_b * BR, BR);
         if (ks >= u.kv_len) return -1;
         const int32_t lp = (ks - u.kv_start) / ps;  // logical page; a ring wraps it over its pages
         const int32_t pidx = u.kvp0 + (pl.ring ? lp % max(u.kvp1 - u.kvp0, 1) : lp);
@@ -456,7 +446,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           my_page = pg_next;
           pg_next = lookup(t + TB);  // used TB tiles from now
           const int32_t tt = t + my_t;
-          const int32_t ks = u.template box_key<F>(tt, u.template key<F>(tt) + key_off + my_b * BR, BR);
+          const int32_t ks = u.template box_key<BC>(tt, u.template key<BC>(tt) + key_off + my_b * BR, BR);
           my_ks = ks;
           const bool live = tt < u.ntiles;
           const bool past = !live || ks >= u.kv_len;
@@ -535,10 +525,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               fix_phase ^= 1u;
             }
             // zero this warp's rows that must not be read: keys past kv_len, keys on bad pages
-            const int32_t kb = u.template key<F>(t) + key_off;  // first key of this CTA's half
+            const int32_t kb = u.template key<BC>(t) + key_off;  // first key of this CTA's half
             for (int b = 0; b < nbox; ++b) {
               const int32_t pb = __shfl_sync(0xffffffffu, my_page, sh + b);
-              const int32_t k0 = BOUNDED ? __shfl_sync(0xffffffffu, my_ks, sh + b) : kb + b * BR;
+              const int32_t k0 = BC ? __shfl_sync(0xffffffffu, my_ks, sh + b) : kb + b * BR;
               for (int rr = 0; rr < BR; ++rr) {
                 const int32_t key = k0 + rr;
                 if (key < u.kv_len && pb >= 0 && pb < a.num_pages) continue;
@@ -583,7 +573,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     int32_t ui = 0;
     int32_t nof = 0;  // head_dim 256: units with tiles whose PVs this warp has issued
     for (int32_t w = unit_at(0); leader && ok && w < nunits; w = unit_at(++ui)) {
-      const int32_t ntiles = tc_unit<F>(a, w, NDH, 0).ntiles;
+      const int32_t ntiles = tc_unit<BC>(a, w, NDH, 0).ntiles;
       if (warp == 1) {
         ok = wait1(QFULL, ui & 1);  // this unit's Q is in place in both CTAs
         for (int32_t j = 0; ok && j < ntiles; ++j) {
@@ -766,7 +756,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     TcUnit u;
     int32_t ui = 0;
     if (unit_at(0) < nunits) {
-      u = tc_unit<F>(a, unit_at(0), NDH, (int32_t)rank);
+      u = tc_unit<BC, PART>(a, unit_at(0), NDH, (int32_t)rank);
       if (DQK != 256 || h == 0) ok = store_q(u, 0);
     }
     for (int32_t w = unit_at(0); ok && w < nunits; w = unit_at(++ui)) {
@@ -775,7 +765,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const int32_t prow = u.sp + u.tok0 + (row >> gsh);
       const int32_t rlo = W >= 0 ? max(u.kv_start, prow - W) : u.kv_start;
       const int32_t rhi = min(prow + 1, u.kv_len);
-      const int32_t sink = a.num_sink;  // kSinks: keys below it are visible whatever the window
+      const int32_t sink = a.num_sink;  // BC: keys below it are visible whatever the window
       float m_ref = -INFINITY, l = 0.f;
       if constexpr (DQK == 256) {
         // Tile-parity softmax: the two warps of a lane quarter take alternate key tiles (warp h
@@ -802,11 +792,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           __syncwarp();
           // this warp has read S(JJ): the S buffer is free for QK(JJ + 2) once all have
           if (lane == 0) mbar_arrive_cl(LEAD(SFREE + 8 * b));
-          const int32_t kb = u.key<F>(j);
+          const int32_t kb = u.key<BC>(j);
           const bool interior =
-              __all_sync(0xffffffffu, rvalid && (kb >= rlo || (SINKS && kb + kBN <= sink)) && kb + kBN <= rhi);
+              __all_sync(0xffffffffu, rvalid && (kb >= rlo || (BC && kb + kBN <= sink)) && kb + kBN <= rhi);
           if (!interior) {
-            if constexpr (SINKS) {
+            if constexpr (BC) {
               // the row's visible keys as 64 bits: a test per key whatever the sinks
               const uint64_t vis = tile_bits(rvalid ? rhi - kb : 0, rlo - kb, sink - kb);
 #pragma unroll
@@ -856,14 +846,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           __syncwarp();
           if (lane == 0) mbar_arrive(PAIRX + 8 * ((JJ & 1) * 4 + quarter));
           if (m_mine != m_new) {
-            if (m_mine != -INFINITY) l = moved<F>(l, move_factor<F>(m_mine - m_new));
+            if (m_mine != -INFINITY) l = moved<BC>(l, move_factor<BC>(m_mine - m_new));
             m_mine = m_new;
           }
           const float mu = m_new == -INFINITY ? 0.f : m_new;
           uint32_t pk[kBN / 2];
           {
             // exponents and row sums on fp32 pairs; the row sum adds the bf16-rounded weights the
-            // PV product uses, so O / l is an exact weighted average of V rows (BOUNDED: the unrounded)
+            // PV product uses, so O / l is an exact weighted average of V rows (BC: the unrounded)
             const float2 ts2 = make_float2(tscale, tscale), nmu2 = make_float2(-mu, -mu);
             float2 sa = make_float2(0.f, 0.f), sb2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -872,7 +862,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               const float2 x = make_float2(ex2(e.x), ex2(e.y));
               pk[k] = pack_bf16(x.x, x.y);
               const float2 wv =
-                  BOUNDED ? x : make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
+                  BC ? x : make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
               if (k & 1) sb2 = __fadd2_rn(sb2, wv);
               else sa = __fadd2_rn(sa, wv);
             }
@@ -893,7 +883,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const bool resc = m_prev != -INFINITY && m_new != m_prev;
           if (__any_sync(0xffffffffu, resc)) {
             // O holds PV(0 .. JJ - 1) at the old reference: rescale all its columns before PV(JJ)
-            const float alpha = resc ? move_factor<F>(m_prev - m_new) : 1.f;
+            const float alpha = resc ? move_factor<BC>(m_prev - m_new) : 1.f;
             const int32_t jp = JJ - 1;
             if (!__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jp % NSB), (jp / NSB) & 1, wc))) { ok = false; break; }
             tc_fence_after();
@@ -904,7 +894,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               tmem_ld32(tl + col, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(moved<F>(__uint_as_float(o[e]), alpha));
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(moved<BC>(__uint_as_float(o[e]), alpha));
               tmem_st32(tl + col, o);
             }
             tmem_wait_st();
@@ -925,7 +915,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
               m_fin = hm[(jl & 1) * kM + row];
           }
           if (ok && m_fin != m_mine) {
-            if (m_mine != -INFINITY) l = moved<F>(l, move_factor<F>(m_mine - m_fin));
+            if (m_mine != -INFINITY) l = moved<BC>(l, move_factor<BC>(m_mine - m_fin));
             m_mine = m_fin;
           }
         }
@@ -941,7 +931,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // this thread's 32 keys (masked keys: -inf); log2 units are t * tscale
         float t[HC];
         const float tscale = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
-        const int32_t kb = u.key<F>(j);
+        const int32_t kb = u.key<BC>(j);
         {
         // both warps of the pair read the whole 64-key row: the row maximum needs no exchange
         uint32_t sv[kBN];
@@ -953,9 +943,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // this warp has read S(JJ): the S buffer is free for QK(JJ + 2) once all have
         if (lane == 0) mbar_arrive_cl(LEAD(SFREE + 8 * b));
         const bool interior =
-            __all_sync(0xffffffffu, rvalid && (kb >= rlo || (SINKS && kb + kBN <= sink)) && kb + kBN <= rhi);
+            __all_sync(0xffffffffu, rvalid && (kb >= rlo || (BC && kb + kBN <= sink)) && kb + kBN <= rhi);
         if (!interior) {
-          if constexpr (SINKS) {
+          if constexpr (BC) {
             const uint64_t vis = tile_bits(rvalid ? rhi - kb : 0, rlo - kb, sink - kb);
 #pragma unroll
             for (int k = 0; k < kBN; ++k) sv[k] = (vis >> k) & 1u ? sv[k] : 0xFF800000u;
@@ -993,9 +983,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (mx > m_ref + kRescaleLog2) {
           // new reference with headroom above this maximum, so later growth rarely rescales
           const float m_new = mx + kHeadroomLog2;
-          alpha = m_ref == -INFINITY ? 0.f : move_factor<F>(m_ref - m_new);
+          alpha = m_ref == -INFINITY ? 0.f : move_factor<BC>(m_ref - m_new);
           resc = m_ref != -INFINITY;
-          l = moved<F>(l, alpha);
+          l = moved<BC>(l, alpha);
           m_ref = m_new;
         }
         if (j > 0 && __any_sync(0xffffffffu, resc)) {
@@ -1009,7 +999,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tmem_ld32(tl + col, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(moved<F>(__uint_as_float(o[e]), alpha));
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(moved<BC>(__uint_as_float(o[e]), alpha));
             tmem_st32(tl + col, o);
           }
           tmem_wait_st();
@@ -1028,7 +1018,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const float2 x = make_float2(ex2(e.x), ex2(e.y));
             pk[k] = pack_bf16(x.x, x.y);
             const float2 w =
-                BOUNDED ? x : make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
+                BC ? x : make_float2(__uint_as_float(pk[k] << 16), __uint_as_float(pk[k] & 0xFFFF0000u));
             if (k & 1) sb2 = __fadd2_rn(sb2, w);
             else sa = __fadd2_rn(sa, w);
           }
@@ -1059,7 +1049,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (!ok) break;
       const int32_t wn = unit_at(ui + 1);
       TcUnit un;
-      if (wn < nunits) un = tc_unit<F>(a, wn, NDH, (int32_t)rank);
+      if (wn < nunits) un = tc_unit<BC, PART>(a, wn, NDH, (int32_t)rank);
       if constexpr (DQK == 256) {
         // The row sum is the sum of the two warps' partial sums, swapped through shared memory.
         // The warp that wrote the last tile's P waits for that tile's PV before publishing (its
@@ -1111,8 +1101,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (ok) {
         // epilogue: normalise this thread's 128 output columns [128h, 128h + 128) of the row
         tc_fence_after();
-        // (a NaN sum of the bounded caches' forms stays: the row has seen a key)
-        const bool some = BOUNDED ? l != 0.f : l > 0.f;
+        // (a NaN sum of BC stays: the row has seen a key)
+        const bool some = BC ? l != 0.f : l > 0.f;
         const float inv = some ? 1.f / l : 0.f;
         if constexpr (PART) {
           // the row's mean and (reference, sum): 512 contiguous bytes of the row per thread
@@ -1212,7 +1202,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
           }
         }
-        }  // !kPart
+        }  // !PART
         // the next unit's first PV overwrites O only after these reads
         tc_fence_before();
         if (DQK == 256 && ntiles > 0) {
@@ -1254,9 +1244,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // ------------------------------------------------------------------ host side
-template <int DQK, Form F>
+template <int DQK, bool BC, bool PART = false>
 cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
-  constexpr bool PART = F == kPart;
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
   const int32_t G = a.group, TQ = a.cta_tile_q;
@@ -1335,7 +1324,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = setup.get(dev, [dev](int* n) {
-    cudaError_t r = cudaFuncSetAttribute(attn_tc_kernel<DQK, F>,
+    cudaError_t r = cudaFuncSetAttribute(attn_tc_kernel<DQK, BC, PART>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<DQK>::SMEM);
     if (r != cudaSuccess) return r;
     r = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
@@ -1364,7 +1353,7 @@ cudaError_t launch_tc(const AttnArgs& a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PART ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, F>, tq, tkv, tv, t);
+  e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<DQK, BC, PART>, tq, tkv, tv, t);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -1379,21 +1368,15 @@ bool attn_tc_supported(int32_t head_dim, int32_t group, int32_t page_size) {
   return true;
 }
 
-bool attn_tc_takes(const AttnArgs& a, int32_t head_dim) {
-  // (the sinks of a call without a window are keys like any other)
-  return attn_tc_supported(head_dim, a.group, a.pool.page_size) &&
-         !(a.bounded && head_dim == 512 && a.window_left >= 0 && a.num_sink > 0);
-}
-
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
   if (a.plan.num_work == 0) return cudaSuccess;
   if (a.bounded)
-    return head_dim == 256 ? launch_tc<256, kSinks>(a, stream) : launch_tc<512, kSums>(a, stream);
-  return head_dim == 256 ? launch_tc<256, kPlain>(a, stream) : launch_tc<512, kPlain>(a, stream);
+    return head_dim == 256 ? launch_tc<256, true>(a, stream) : launch_tc<512, true>(a, stream);
+  return head_dim == 256 ? launch_tc<256, false>(a, stream) : launch_tc<512, false>(a, stream);
 }
 
 cudaError_t launch_attn_parts(const AttnArgs& a, int32_t head_dim, cudaStream_t stream) {
-  return head_dim == 256 ? launch_tc<256, kPart>(a, stream) : launch_tc<512, kPart>(a, stream);
+  return head_dim == 256 ? launch_tc<256, true, true>(a, stream) : launch_tc<512, true, true>(a, stream);
 }
 
 int32_t attn_tc_rows() { return kM; }

@@ -136,7 +136,6 @@ struct AttnArgs {
   float* join_lse = nullptr;  // the join's lse (null: not written); `lse` is the own keys' alone
   int32_t beside = 0;
   int32_t part_clusters = 0;  // parts: clusters to run on (0: all)
-  int32_t work_parts = 1;  // attn_split.cu, prefill: CTAs that share a work item's tokens (per KV head)
   int* status;
   uint64_t wait_ns;       // limit of the kernels' bounded waits (nanoseconds)
   int32_t test_withhold;  // test hook of pg_test_bounded_wait (0: off)
@@ -213,8 +212,6 @@ int32_t attn_kernel_cta_tile_q(int32_t head_dim, int32_t group, int32_t page_siz
 // tcgen05 prefill kernel: geometry it handles, rows per CTA, launch.
 bool attn_tc_supported(int32_t head_dim, int32_t group, int32_t page_size);
 int32_t attn_tc_rows();
-// Whether it takes a prefill call of such a geometry (see attn_tc.cu, kSinks).
-bool attn_tc_takes(const AttnArgs& a, int32_t head_dim);
 cudaError_t launch_attn_prefill_tc(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
 // Parts of a shared prefix: the pair table's entries are (pair of query tiles, run of keys).
 cudaError_t launch_attn_parts(const AttnArgs& a, int32_t head_dim, cudaStream_t stream);
