@@ -281,8 +281,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     constexpr uint32_t IDESC_QK = idesc_bf16(kT, kN, false);
     constexpr uint32_t IDESC_PV = idesc_bf16(kT, kN, false) | (1u << 15);  // A (V) is MN-major
     auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
-      const bool w = lane == 0 ? mbar_wait_inline(bar, parity, wc) : false;
-      return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, wc));
     };
     int slot = 0, round = 0;
     auto step = [&]() {
@@ -391,6 +390,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 #pragma unroll 1
       for (int p = 0; p < D / 128; ++p) {
         uint32_t o[8];
+        __syncwarp();
         tmem_ld8(tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * kN, o);
         tmem_wait_ld();
         const int d = p * 128 + row;
@@ -436,6 +436,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       const bool vis = (h.mine >> lane) & 1u;
       uint32_t sv[8];
       tc_fence_after();
+      __syncwarp();  // (a tensor-memory access is the whole warp's: it meets behind the lanes' waits)
       tmem_ld8(tl + C::TM_S + b * kN, sv);
       tmem_wait_ld();
       tc_fence_before();
@@ -495,6 +496,7 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           const int32_t jt = i - 1;
           if (__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jt & 1), (jt >> 1) & 1, wc))) {
             tc_fence_after();
+            __syncwarp();
 #pragma unroll 1
             for (int p = 0; p < D / 128; ++p) {
               uint32_t o[8];
@@ -591,13 +593,11 @@ bounded_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(DRAIN, 0)) {
-        if (globaltimer() - t0 > a.wait_ns) {
-          atomicOr(a.status, kStatusTimeout);
-          break;
-        }
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(DRAIN, 0)) {
+      if (globaltimer() - t0 > a.wait_ns) {
+        atomicOr(a.status, kStatusTimeout);
+        break;
       }
     }
     __syncwarp();

@@ -256,12 +256,8 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // part p of the segment's K, once the part that used its slot has been multiplied; lane
             // l takes page boxes l, l + 32, ...
             const int sl = kc & 1;
-            int go = 1;
-            if (lane == 0) go = mbar_wait_inline(KEMPTY + 8 * sl, ((kc >> 1) & 1) ^ 1, wc) ? 1 : 0;
-            if (!__shfl_sync(0xffffffffu, go, 0)) {
-              ok = false;
-              break;
-            }
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(KEMPTY + 8 * sl, ((kc >> 1) & 1) ^ 1, wc));
+            if (!ok) break;
             uint32_t bytes = 0u;
             bool bad = false;
             for (int b = lane; b < nbox; b += 32) {
@@ -287,22 +283,16 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             ++kc;
           }
           // four stages of the query tile
-          int go = 1;
-          if (lane == 0) {
-            int y = x, rd = round;
-            for (int ch = 4 * p; go && ch < 4 * p + 4; ++ch) {
-              if (!mbar_wait_inline(EMPTY(y), (rd & 1) ^ 1, wc)) {
-                go = 0;
-                break;
-              }
-              mbar_expect_tx_cl_relaxed(LEAD(FULL(y)), kStage);
-              tma_load_3d(base + C::OFF_Q + y * kStage, &tm_q, ch * 64, w.g * G, tok, LEAD(FULL(y)));
-              if (++y == NS) { y = 0; ++rd; }
+          for (int ch = 4 * p; ok && ch < 4 * p + 4; ++ch) {
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(EMPTY(x), (round & 1) ^ 1, wc));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_expect_tx_cl_relaxed(LEAD(FULL(x)), kStage);
+              tma_load_3d(base + C::OFF_Q + x * kStage, &tm_q, ch * 64, w.g * G, tok, LEAD(FULL(x)));
             }
+            __syncwarp();
+            if (++x == NS) { x = 0; ++round; }
           }
-          x += 4;
-          if (x >= NS) { x -= NS; ++round; }
-          if (!__shfl_sync(0xffffffffu, go, 0)) ok = false;
         }
       }
       more = ok && walk_next(a, w);
@@ -316,8 +306,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // ------------------------------------------------------------ MMA issuer (the leader's)
     constexpr uint32_t IDESC = idesc_bf16(2 * kMK, kNQ, false);
     auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
-      const bool y = lane == 0 ? mbar_wait_inline(bar, parity, wc) : false;
-      return __shfl_sync(0xffffffffu, y ? 1 : 0, 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, wc));
     };
     if (leader) {
       bool ok = true, more = true;
@@ -485,13 +474,11 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(DRAIN, 0)) {
-        if (globaltimer() - t0 > a.wait_ns) {
-          atomicOr(a.status, kStatusTimeout);
-          break;
-        }
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(DRAIN, 0)) {
+      if (globaltimer() - t0 > a.wait_ns) {
+        atomicOr(a.status, kStatusTimeout);
+        break;
       }
     }
     __syncwarp();

@@ -444,8 +444,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     constexpr uint32_t IDESC_QK = idesc_e4m3(C::QN, false);
     constexpr uint32_t IDESC_PV = idesc_e4m3(C::PN, true);  // A (V) is MN-major
     auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
-      const bool w = lane == 0 ? mbar_wait_inline(bar, parity, wc) : false;
-      return __shfl_sync(0xffffffffu, w ? 1 : 0, 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, wc));
     };
     int slot = 0, round = 0;
     auto step = [&]() {
@@ -578,6 +577,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
 #pragma unroll 1
       for (int p = 0; p < NC; ++p) {
         uint32_t o[3][8];
+        __syncwarp();
         const uint32_t at = tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * C::PN;
 #pragma unroll
         for (int k = 0; k < 3; ++k) tmem_ld8(at + k * NR, o[k]);
@@ -624,6 +624,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       const bool vis = (h.mine >> lane) & 1u;
       uint32_t s0[8], s1[8];
       tc_fence_after();
+      __syncwarp();  // (a tensor-memory access is the whole warp's: it meets behind the lanes' waits)
       tmem_ld8(tl + C::TM_S + b * C::QN, s0);
       tmem_ld8(tl + C::TM_S + b * C::QN + NR, s1);
       tmem_wait_ld();
@@ -681,6 +682,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
           const int32_t jt = i - 1;
           if (__all_sync(0xffffffffu, mbar_wait(PVDONE + 8 * (jt & 1), (jt >> 1) & 1, wc))) {
             tc_fence_after();
+            __syncwarp();
 #pragma unroll 1
             for (int p = 0; p < NC; ++p) {
               uint32_t o[3][8];
@@ -762,13 +764,11 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(DRAIN, 0)) {
-        if (globaltimer() - t0 > a.wait_ns) {
-          atomicOr(a.status, kStatusTimeout);
-          break;
-        }
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(DRAIN, 0)) {
+      if (globaltimer() - t0 > a.wait_ns) {
+        atomicOr(a.status, kStatusTimeout);
+        break;
       }
     }
     __syncwarp();

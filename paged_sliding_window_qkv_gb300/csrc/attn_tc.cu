@@ -367,16 +367,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // head_dim 256: Q of the cluster's k-th unit goes into the staging buffer once the softmax
     // warps have moved Q of unit k - 1 out of it (QSFREE phase k - 1); one lane issues it
     auto stage_q = [&](int32_t k) -> bool {
-      if (lane != 0) return true;
-      if (k > 0 && !mbar_wait(QSFREE, (k - 1) & 1, wc)) return false;
+      if (k > 0 && !__all_sync(0xffffffffu, mbar_wait(QSFREE, (k - 1) & 1, wc))) return false;
       const TcUnit v = tc_unit<BC>(a, unit_at(k), NDH, (int32_t)rank);
-      mbar_expect_tx(QSFULL, v.ntok > 0 ? (uint32_t)C::QS_BYTES : 0u);
-      if (v.ntok > 0)
-        for (int c = 0; c < 4; ++c)
-          tma_load_3d(sQ + c * (kM * 128), &tm_q, c * 64, v.g * G, v.q0 + v.tok0, mapa(QSFULL, rank));
+      if (lane == 0) {
+        mbar_expect_tx(QSFULL, v.ntok > 0 ? (uint32_t)C::QS_BYTES : 0u);
+        if (v.ntok > 0)
+          for (int c = 0; c < 4; ++c)
+            tma_load_3d(sQ + c * (kM * 128), &tm_q, c * 64, v.g * G, v.q0 + v.tok0, mapa(QSFULL, rank));
+      }
+      __syncwarp();
       return true;
     };
-    if (DQK == 256 && !is_v && unit_at(0) < nunits) ok = __shfl_sync(0xffffffffu, stage_q(0) ? 1 : 0, 0) != 0;
+    if (DQK == 256 && !is_v && unit_at(0) < nunits) ok = stage_q(0);
     int32_t J = 0;  // tiles of this cluster's earlier units
     int32_t ui = 0;
     for (int32_t w = unit_at(0); ok && w < nunits; w = unit_at(++ui)) {
@@ -399,22 +401,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       }
       if (DQK == 512 && !is_v) {
         // Q columns [256,512) of this CTA's tile, once the previous unit's QK MMAs have read them
-        int go = 1;
-        if (lane == 0) {
-          if (ui > 0 && !mbar_wait(QFREE, (ui - 1) & 1, wc)) {
-            go = 0;
-          } else {
-            mbar_expect_tx_cl_relaxed(LEAD(QFULL), u.ntok > 0 ? (uint32_t)C::QS_BYTES : 0u);
-            if (u.ntok > 0)
-              for (int c = 0; c < (DQK - 256) / 64; ++c)
-                tma_load_3d(sQ + c * (kM * 128), &tm_q, 256 + c * 64, u.g * G, u.q0 + u.tok0,
-                            LEAD(QFULL));
-          }
-        }
-        if (!__shfl_sync(0xffffffffu, go, 0)) {
+        if (ui > 0 && !__all_sync(0xffffffffu, mbar_wait(QFREE, (ui - 1) & 1, wc))) {
           ok = false;
           break;
         }
+        if (lane == 0) {
+          mbar_expect_tx_cl_relaxed(LEAD(QFULL), u.ntok > 0 ? (uint32_t)C::QS_BYTES : 0u);
+          if (u.ntok > 0)
+            for (int c = 0; c < (DQK - 256) / 64; ++c)
+              tma_load_3d(sQ + c * (kM * 128), &tm_q, 256 + c * 64, u.g * G, u.q0 + u.tok0, LEAD(QFULL));
+        }
+        __syncwarp();
       }
       // Box coordinates are worked out a batch of TB tiles at a time, one box per lane: lane i
       // holds box i mod nbox of tile (batch start + i / nbox). Page ids are read a batch ahead,
@@ -437,7 +434,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const uint32_t box_bytes = (uint32_t)BR * row_bytes;
       for (int32_t t = 0; ok && t < u.ntiles; ++t) {
         const int32_t JJ = J + t;
-        if (stage_next && t == stage_at && !__shfl_sync(0xffffffffu, stage_q(ui + 1) ? 1 : 0, 0)) {
+        if (stage_next && t == stage_at && !stage_q(ui + 1)) {
           ok = false;
           break;
         }
@@ -472,19 +469,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (!is_v && KP > 1 && !fix) {
           // every K part of the tile in one copy instruction (each warp-level copy instruction
           // costs the producer hundreds of cycles, whatever its box count): lane i copies box
-          // i mod nbox of part i / nbox, after lane 0 has seen every part's slot free and
-          // announced each part's bytes
-          int r = 1;
-          if (lane == 0) {
-            for (int pp = 0; r && pp < KP; ++pp)
-              r = mbar_wait_inline(EMPTY(KSLOT(JJ, pp)), (KROUND(JJ, pp) & 1) ^ 1, wc) ? 1 : 0;
-            if (r)
-              for (int pp = 0; pp < KP; ++pp) mbar_expect_tx_cl_relaxed(LEAD(FULL(KSLOT(JJ, pp))), bytes);
-          }
-          if (!__shfl_sync(0xffffffffu, r, 0)) {
-            ok = false;
-            break;
-          }
+          // i mod nbox of part i / nbox, once every part's slot is free and lane 0 has announced
+          // each part's bytes
+          for (int pp = 0; ok && pp < KP; ++pp)
+            ok = __all_sync(0xffffffffu, mbar_wait_inline(EMPTY(KSLOT(JJ, pp)), (KROUND(JJ, pp) & 1) ^ 1, wc));
+          if (!ok) break;
+          if (lane == 0)
+            for (int pp = 0; pp < KP; ++pp) mbar_expect_tx_cl_relaxed(LEAD(FULL(KSLOT(JJ, pp))), bytes);
+          __syncwarp();
           const int pp = lane / nbox, b = lane % nbox;
           const int32_t row = __shfl_sync(0xffffffffu, my_row, sh + b);
           const bool go = pp < KP && ((bm_load >> (sh + b)) & 1u);
@@ -493,18 +485,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tma_load_4d(sSlots + s * kSlotBytes + b * (BR * 512), &tm_kv, 0, 0, pp * 4, row / 8,
                         LEAD(FULL(s)));
           }
+          __syncwarp();
           continue;
         }
         for (int pp = 0; ok && pp < nparts; ++pp) {
           const int s = is_v ? VSLOT(JJ) : KSLOT(JJ, pp);
           const int round = is_v ? (int)(JJ / NVR) : KROUND(JJ, pp);
           const int c0 = is_v ? u.dh * 4 + (int)rank * 2 : pp * 4;
-          int r = 1;
-          if (lane == 0) r = mbar_wait_inline(EMPTY(s), (round & 1) ^ 1, wc) ? 1 : 0;
-          if (!__shfl_sync(0xffffffffu, r, 0)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait_inline(EMPTY(s), (round & 1) ^ 1, wc));
+          if (!ok) break;
           const uint32_t slot = sSlots + s * kSlotBytes;
           const uint32_t bar = fix ? FIX : LEAD(FULL(s));
           if (lane == 0) {
@@ -516,6 +505,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (is_v) tma_load_3d(slot + my_b * (BR * 256), &tm_v, 0, my_row, c0, bar);
             else tma_load_4d(slot + my_b * (BR * 512), &tm_kv, 0, 0, c0, my_row / 8, bar);
           }
+          __syncwarp();
           if (fix) {
             if (bytes > 0) {
               if (!__all_sync(0xffffffffu, mbar_wait(FIX, fix_phase, wc))) {
@@ -546,8 +536,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           }
         }
       }
-      if (ok && stage_next && stage_at == u.ntiles)
-        ok = __shfl_sync(0xffffffffu, stage_q(ui + 1) ? 1 : 0, 0) != 0;
+      if (ok && stage_next && stage_at == u.ntiles) ok = stage_q(ui + 1);
       J += u.ntiles;
     }
     if (!ok) {
@@ -561,12 +550,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // ------------------------------------------------------------ MMA issuers (the leader's)
     // QK (warp 1) and PV (warp 11) are issued by two warps of the leader CTA; they accumulate
     // into disjoint TMEM (S and O) of both CTAs and are ordered against each other only through
-    // the barriers. Lane 0 waits on the barriers and issues; the other lanes follow it.
+    // the barriers. The warp waits on the barriers together, and lane 0 issues.
     constexpr uint32_t IDESC_QK = idesc_bf16(2 * kM, kBN, false);
     constexpr uint32_t IDESC_PV = idesc_bf16(2 * kM, kDV, true);
     auto wait1 = [&](uint32_t bar, uint32_t parity) -> bool {
-      const bool r = lane == 0 ? mbar_wait_inline(bar, parity, wc) : false;
-      return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, wc));
     };
     bool ok = true;
     int32_t J = 0;  // tiles of this cluster's earlier units
@@ -1218,15 +1206,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) {
-      // every MMA of the pair has completed once the leader's final commits have arrived (in
-      // both CTAs); a wait that runs out is reported like any other
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(DRAIN, 0)) {
-        if (globaltimer() - t0 > a.wait_ns) {
-          atomicOr(a.status, kStatusTimeout);
-          break;
-        }
+    // every MMA of the pair has completed once the leader's final commits have arrived (in
+    // both CTAs); a wait that runs out is reported like any other
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(DRAIN, 0)) {
+      if (globaltimer() - t0 > a.wait_ns) {
+        atomicOr(a.status, kStatusTimeout);
+        break;
       }
     }
     __syncwarp();
