@@ -84,8 +84,8 @@ struct Q8Cfg {
   static constexpr int OFF_FIN = OFF_RED + SETS * 4 * 8 * 8;         // [16] (l, its reference, P's)
   static constexpr int OFF_BAR = OFF_FIN + 16 * 16;
   // FULL, EMPTY; QFULL[2], QEMPTY[2], HFULL[4], HEMPTY[4], SFULL[2], SFREE[2], PFULL[2], PVDONE[2],
-  // OFREE[2], DRAIN, QSCALE[4], VREADY[2]
-  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs + 2;
+  // OFREE[2], DRAIN, QSCALE[4], VREADY[2], VCLEAR[2]
+  static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs + 4;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static constexpr uint32_t TM_O = 0, O_COLS = NC * PN, TM_S = 2 * O_COLS;
   static constexpr uint32_t TM_COLS = TM_S + 2 * QN <= 256 ? 256 : 512;
@@ -148,7 +148,8 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
   auto EMPTY = [&](int s) { return bars + 8u * (NS + s); };
   const uint32_t QFULL = bars + 8u * (2 * NS), QEMPTY = QFULL + 16, HFULL = QFULL + 32, HEMPTY = HFULL + 32,
                  SFULL = HEMPTY + 32, SFREE = SFULL + 16, PFULL = SFULL + 32, PVDONE = SFULL + 48,
-                 OFREE = SFULL + 64, DRAIN = SFULL + 80, QSCALE = SFULL + 88, VREADY = QSCALE + 8 * kQs;
+                 OFREE = SFULL + 64, DRAIN = SFULL + 80, QSCALE = SFULL + 88, VREADY = QSCALE + 8 * kQs,
+                 VCLEAR = VREADY + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gb + C::OFF_BAR + C::NBAR * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const WaitCtx wc{abort_flag, a.status, a.wait_ns};
@@ -175,7 +176,10 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       mbar_init(HEMPTY + 8 * h, 4 * C::SETS + 1 + C::QW);  // the softmax warps, the query warps and the MMA issuer
     }
     for (int q = 0; q < kQs; ++q) mbar_init(QSCALE + 8 * q, C::QW);
-    for (int q = 0; q < 2; ++q) mbar_init(VREADY + 8 * q, 1);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(VREADY + 8 * q, 1);
+      mbar_init(VCLEAR + 8 * q, 4 * C::SETS);
+    }
     mbar_init(DRAIN, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -284,7 +288,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     int32_t g = 0, tok = 0, fixes = 0;
     bool end = false, fresh = false;  // fresh: the last header read began a segment whose queries are to come
     uint64_t since = 0;               // when nothing was left to do
-    // Headers are read as they come, for the queries of new segments; warp 7 gives each back once its tile's
+    // Headers are read as they come, for the queries of new segments, and given back; by warp 7 once its tile's
     // V rows need nothing more. Nothing here waits for one thing alone: the query buffer may come free
     // only behind a tile whose V rows are still to be cleared.
     while (!end || fresh || j < i) {
@@ -389,13 +393,15 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       if (j < i) {
         const int hb = j % kHdrs;
         const Q8Hdr& h = hdrs[hb];
-        // Warp 7 goes on once the tile's weights have been written. (Every tile's in turn: a parity test
-        // tells two phases apart only when the one before is over.) The tile's scores have then been read
-        // and PV of the tile two before is done, so the V slot's use before (K(j), V(j - 2) or an earlier
-        // one; V(j) follows K(j + 1) in the ring, the last one K(j)) has been consumed too.
-        bool done = warp != 7 || __all_sync(0xffffffffu, mbar_test(PFULL + 8 * (j & 1), (j >> 1) & 1));
+        // Warp 7 clears a tile's V rows once its weights have been written: its scores have then been read and
+        // PV of the tile two before is done, so the V slot's use before (K(j), V(j - 2) or an earlier one; V(j)
+        // follows K(j + 1) in the ring, the last one K(j)) has been consumed too. The weights of such tiles
+        // have barriers of their own (VCLEAR). A parity test takes two phases for none, and the weights of tiles
+        // without hidden keys wait for nothing of this warp: on PFULL two of them could pass while queries are
+        // converted here. Those of a third such tile wait for the first one's PV, which waits for VREADY.
         const bool fix = warp == 7 && (h.flags & kFix);
-        if (done && fix) {
+        bool done = !fix;
+        if (fix && __all_sync(0xffffffffu, mbar_test(VCLEAR + 8 * (fixes & 1), (fixes >> 1) & 1))) {
           const int32_t at = (h.flags & kEnd) ? 2 * j + 1 : 2 * j + 2, sl = at % NS;
           done = __all_sync(0xffffffffu, mbar_test(FULL(sl), (at / NS) & 1));
           if (done) {
@@ -414,7 +420,6 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
           idle = false;
           __syncwarp();
           if (lane == 0) {
-            // (weights of a third such tile wait for the first one's PV, so two barriers do)
             if (fix) mbar_arrive(VREADY + 8 * (fixes & 1));
             mbar_arrive(HEMPTY + 8 * hb);
           }
@@ -529,7 +534,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
     float l[CQ], ref[CQ], top[CQ];
     float my_ref = -INFINITY, my_top = -INFINITY;  // those of row set_col(lane)
     bool ok = true;
-    int32_t segs = 0;
+    int32_t segs = 0, fixes = 0;
     struct Head {
       int32_t flags, g, tok;
       uint32_t mine, k, v;  // visible keys of the warp; the key's scale bytes
@@ -733,7 +738,11 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       fence_proxy_async();  // the MMA reads P through the async proxy
       tc_fence_before();    // and O after any rescaling above
       __syncwarp();
-      if (lane == 0) mbar_arrive(PFULL + 8 * b);
+      if (lane == 0) {
+        mbar_arrive(PFULL + 8 * b);
+        if (h.flags & kFix) mbar_arrive(VCLEAR + 8 * (fixes & 1));
+      }
+      fixes += h.flags & kFix ? 1 : 0;
       if (pending && ok) epilogue();
       pending = false;
       if (h.flags & kLast) {
