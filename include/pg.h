@@ -455,7 +455,8 @@ int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_s
  * exponent e = b - 127 with max |y| <= 448 * 2^e, held to [-110, 120] (rows below 448 * 2^-110 lose
  * their small elements), and round y * 2^-e to the nearest code, ties to even; an element that is
  * not finite becomes a NaN code and has no part in the scale. The scale is a power of two so that
- * every element is exactly a bf16 number: attention over a row is attention over its read-back.
+ * every element is exactly a bf16 number: a row's read-back is exact, and prompts are attended over it.
+ * (Decode rounds weights otherwise than over the read-back: see pg_attn_paged_q8.)
  *
  * Layouts, dense: codes [layer][page][kv][kv_head][slot][d], kv = 0 for K, 1 for V, 16-byte
  * aligned; scales [layer][page][kv][kv_head][slot]. capacity = the element count of scales =
@@ -510,9 +511,11 @@ size_t pg_q8_workspace_bytes(const pg_plan_t plan);
  *   workspace: ws_bytes >= pg_q8_workspace_bytes(plan), 16-byte aligned
  * Decode multiplies 8-bit numbers: a query row is taken as the sum of two e4m3 terms, exact for
  * elements down to 2^-13 of the row's largest and within 2^-21 of it below, and a weight times its V
- * row's scale as the sum of three, within 2^-12 of itself down to 2^-10 of the row's largest such
- * product and within 2^-22 of that below. Sums are fp32; row sums add the unrounded weights. A query
- * row with an element that is not finite gives a NaN row.
+ * row's scale as the sum of four, within 2^-16 of itself down to 2^-10 of the row's largest such
+ * product and within 2^-26 of that below. So n keys whose products are that small may be off by n * 2^-26 of
+ * the largest together, a bf16 output's half step at n = 131072 (a read-back and pg_attn_paged_sink keep
+ * every weight to 2^-8 of itself). Sums are fp32; row sums add the unrounded weights. A query row with an
+ * element that is not finite gives a NaN row.
  * Errors: those of pg_attn_paged_sink.
  */
 int pg_attn_paged_q8(const pg_plan_t plan, const pg_q8_pool_t* pool, int32_t layer,

@@ -8,16 +8,17 @@
 //   q = 2^e (a0 + a1 / 16)                  a0 = e4m3(q 2^-e), a1 = e4m3(16 (q 2^-e - a0))
 //   S^T = K [a0 a1]^T  (M = 128 keys, N = the group's rows twice, K = 32 d a step)
 //   s = 2^(e + k) (S0 + S1 / 16)            k: the exponent of the key's K row
-//   P = 2^(s + v - R) = p0 + p1 / 16 + p2 / 256   v: of its V row; s in log2 units
-//   O^T = V^T [p0 p1 p2]^T  (M = 128 output columns, N = the rows three times, K = 32 keys a step)
+//   P = 2^(s + v - R) = p0 + p1 / 16 + p2 / 256 + p3 / 4096   v: of its V row; s in log2 units
+//   O^T = V^T [p0 p1 p2 p3]^T  (M = 128 output columns, N = the rows four times, K = 32 keys a step)
 // Two terms hold a bf16 query exactly (8 bits of significand) down to 2^-13 of the row's largest
-// element; three hold a weight to 12 bits. The terms only widen N, which at these sizes costs nothing:
+// element; four hold a weight to 16 bits. The terms only widen N, which at these sizes costs nothing:
 // an instruction's time is that of reading A (the codes) from shared memory.
 //
 // e4m3 reaches from 2^-9 to 448, so R must stand near the row's largest s + v, not 2^48 off as in the
-// bf16 kernels: it moves when an exponent outgrows it, to leave 4.8 octaves of room, and weights are
-// cut off 2^-22 below the largest. The row sum keeps its own reference (of s alone) and adds the
-// unrounded weights.
+// bf16 kernels: it moves when an exponent outgrows it, to leave kLead + kRoom octaves of room. A weight's
+// last term ends 2^-22 below 1, 2^-26 below the largest: n keys there are off by n times that together, a
+// bf16 output's half step for n = 131072. (With three terms, and 2^-22 below the largest, 16384 such keys lost
+// 0.4% of the output.) The row sum keeps its own reference (of s alone) and adds the unrounded weights.
 //
 // Work, walk, records and join are those of attn_bounded_decode.cu; a ring slot is a tile of K or V
 // (128 keys x head_dim codes: three slots of 64 KB, or six of 32 KB), in the order K0 K1 V0 K2 V1 ...
@@ -51,6 +52,7 @@ constexpr int kBox = 16, kBoxes = kT / kBox;  // key rows of a box, boxes of a t
 // P is at most 448 where a weight stands kRoom octaves above its reference; a reference is set kLead
 // above the largest weight (P = 2^(8 - kLead) there).
 constexpr float kTop = 8.f, kLead = 4.f, kRoom = 0.8f;
+constexpr int kTerms = 4;  // of a weight
 
 struct alignas(16) Q8Hdr {
   uint32_t vis[4];       // visible keys
@@ -72,7 +74,9 @@ struct Q8Cfg {
   static constexpr int SLOT = kT * D;
   static constexpr int NSLOT = D == 256 ? 6 / PER_SM : 3;
   static constexpr int QN = 2 * NR;             // columns of S: two terms
-  static constexpr int PN = NR == 8 ? 32 : 48;  // of O: three terms (N is a multiple of 16)
+  static constexpr int PN = kTerms * NR;        // of O
+  // O buffers (segments): two, but where tensor memory holds one beside the scores
+  static constexpr int NOB = D == 512 && NR == 16 ? 1 : 2;
   static constexpr int NQB = D == 256 && PER_SM == 1 ? 2 : 1;  // query buffers (segments)
   static constexpr int Q_BYTES = NC * QN * 128; // [128-d chunk][QN rows][128 B]
   static constexpr int P_BYTES = PN * 128;      // [PN rows][128 keys]
@@ -87,7 +91,7 @@ struct Q8Cfg {
   // OFREE[2], DRAIN, QSCALE[4], VREADY[2], VCLEAR[2]
   static constexpr int NBAR = 2 * NSLOT + 4 + 8 + 10 + 1 + kQs + 4;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-  static constexpr uint32_t TM_O = 0, O_COLS = NC * PN, TM_S = 2 * O_COLS;
+  static constexpr uint32_t TM_O = 0, O_COLS = NC * PN, TM_S = NOB * O_COLS;
   static constexpr uint32_t TM_COLS = TM_S + 2 * QN <= 256 ? 256 : 512;
   static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory");
   static_assert(TM_S + 2 * QN <= 512, "tensor memory");
@@ -489,9 +493,9 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       }
       if (i > 0) {
         const int32_t jt = i - 1;
-        const int pb = jt & 1, ob = pseg & 1;
+        const int pb = jt & 1, ob = pseg % C::NOB;
         ok = wait1(PFULL + 8 * pb, (jt >> 1) & 1);
-        if (ok && (pflags & kFirst)) ok = wait1(OFREE + 8 * ob, ((pseg >> 1) & 1) ^ 1);
+        if (ok && (pflags & kFirst)) ok = wait1(OFREE + 8 * ob, ((pseg / C::NOB) & 1) ^ 1);
         ok = ok && wait1(FULL(slot), round & 1);
         if (ok && (pflags & kFix)) {
           ok = wait1(VREADY + 8 * (fixes & 1), (fixes >> 1) & 1);
@@ -581,18 +585,19 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       }
 #pragma unroll 1
       for (int p = 0; p < NC; ++p) {
-        uint32_t o[3][8];
+        uint32_t o[kTerms][8];
         __syncwarp();
-        const uint32_t at = tl + C::TM_O + (p_seg & 1) * C::O_COLS + p * C::PN;
+        const uint32_t at = tl + C::TM_O + (p_seg % C::NOB) * C::O_COLS + p * C::PN;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) tmem_ld8(at + k * NR, o[k]);
+        for (int k = 0; k < kTerms; ++k) tmem_ld8(at + k * NR, o[k]);
         tmem_wait_ld();
         const int d = p * 128 + row;
 #pragma unroll
         for (int x = 0; x < CQ; ++x) {
           if (x >= Gs) break;
-          const float sum = fmaf(__uint_as_float(o[2][x]), 1.f / 256,
-                                 fmaf(__uint_as_float(o[1][x]), 1.f / 16, __uint_as_float(o[0][x])));
+          float sum = __uint_as_float(o[kTerms - 1][x]);
+#pragma unroll
+          for (int k = kTerms - 2; k >= 0; --k) sum = fmaf(sum, 1.f / 16, __uint_as_float(o[k][x]));
           const float v = inv[x] == 0.f ? 0.f : sum * root[x] * inv[x] * root[x];
           if (p_flags & kSplit) args.rec_o[(rec + x) * D + d] = v;
           else a.out[(row0 + x) * D + d] = __float2bfloat16_rn(v);
@@ -605,7 +610,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(OFREE + 8 * (p_seg & 1));
+      if (lane == 0) mbar_arrive(OFREE + 8 * (p_seg % C::NOB));
     };
     Head h = fetch(0);
     const bool none = any_of(bar, !ok) || (h.flags & kEmpty);  // (all of the set's warps leave together)
@@ -690,13 +695,13 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
             __syncwarp();
 #pragma unroll 1
             for (int p = 0; p < NC; ++p) {
-              uint32_t o[3][8];
-              const uint32_t at = tl + C::TM_O + ((segs - 1) & 1) * C::O_COLS + p * C::PN;
+              uint32_t o[kTerms][8];
+              const uint32_t at = tl + C::TM_O + ((segs - 1) % C::NOB) * C::O_COLS + p * C::PN;
 #pragma unroll
-              for (int k = 0; k < 3; ++k) tmem_ld8(at + k * NR, o[k]);
+              for (int k = 0; k < kTerms; ++k) tmem_ld8(at + k * NR, o[k]);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 3; ++k) {
+              for (int k = 0; k < kTerms; ++k) {
 #pragma unroll
                 for (int x = 0; x < CQ; ++x) o[k][x] = __float_as_uint((__uint_as_float(o[k][x]) * al[x]) * al[x]);
                 tmem_st8(at + k * NR, o[k]);
@@ -720,19 +725,19 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
           l[x + z] += ex2(t[x + z] - (ref[x + z] == -INFINITY ? 0.f : ref[x + z]));
           (z ? w.y : w.x) = ex2(t[x + z] + (ve - (top[x + z] == -INFINITY ? 0.f : top[x + z])));
         }
-        const uint32_t p0 = e4m3x2(w);
-        const float2 v0 = q8_values(p0);
-        const float2 r1 = make_float2(16.f * (w.x - v0.x), 16.f * (w.y - v0.y));
-        const uint32_t p1 = e4m3x2(r1);
-        const float2 v1 = q8_values(p1);
-        const uint32_t p2 = e4m3x2(make_float2(16.f * (r1.x - v1.x), 16.f * (r1.y - v1.y)));
+        uint32_t p[kTerms];
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) {
+          p[k] = e4m3x2(w);
+          const float2 v = q8_values(p[k]);
+          w = make_float2(16.f * (w.x - v.x), 16.f * (w.y - v.y));
+        }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           // row x of each term; the 16 keys of a piece are contiguous, pieces swizzled by the row
           unsigned char* const at = pp + (x0 + x + z) * 128 + (((row >> 4) ^ ((x + z) & 7)) << 4);
-          at[0] = (unsigned char)(p0 >> (8 * z));
-          at[NR * 128] = (unsigned char)(p1 >> (8 * z));
-          at[2 * NR * 128] = (unsigned char)(p2 >> (8 * z));
+#pragma unroll
+          for (int k = 0; k < kTerms; ++k) at[k * NR * 128] = (unsigned char)(p[k] >> (8 * z));
         }
       }
       fence_proxy_async();  // the MMA reads P through the async proxy
