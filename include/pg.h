@@ -456,6 +456,8 @@ int pg_kv_evict_apply(const pg_plan_t plan, const pg_pool_t* pool, const pg_kv_s
  * their small elements), and round y * 2^-e to the nearest code, ties to even; an element that is
  * not finite becomes a NaN code and has no part in the scale. The scale is a power of two so that
  * every element is exactly a bf16 number: a row's read-back is exact, and prompts are attended over it.
+ * A pool that was filled elsewhere may hold any byte: 255 makes every element of its row NaN, elements past
+ * bf16's range read back as infinities, and bytes below 3 as the nearest bf16 numbers.
  * (Decode rounds weights otherwise than over the read-back: see pg_attn_paged_q8.)
  *
  * Layouts, dense: codes [layer][page][kv][kv_head][slot][d], kv = 0 for K, 1 for V, 16-byte

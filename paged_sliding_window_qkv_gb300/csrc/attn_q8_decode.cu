@@ -642,7 +642,7 @@ q8_decode_kernel(const __grid_constant__ CUtensorMap tm_kv, Q8Args qa) {
       const float* const qs = qs0 + ((segs - 1) % kQs) * 16;
       float t[CQ];
       const float ks = q8_scale(h.k);
-      const float ve = (float)((int32_t)h.v - 127);
+      const float ve = h.v == 255u ? NAN : (float)((int32_t)h.v - 127);
       bool over = false;
 #pragma unroll
       for (int x = 0; x < CQ; ++x) {

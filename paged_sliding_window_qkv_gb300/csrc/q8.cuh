@@ -16,8 +16,10 @@ constexpr int32_t kQ8Least = -110, kQ8Most = 120;
 
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float q8_pow2(int32_t e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// What a scale byte stands for (bytes that no kernel writes: 0 gives 0, 255 infinity).
-__device__ __forceinline__ float q8_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+// What a scale byte stands for: 2^(byte - 127), for byte 0 a subnormal number; 255 is NaN.
+__device__ __forceinline__ float q8_scale(uint32_t byte) {
+  return __uint_as_float(byte << 23 | (byte - 1u >= 254u ? 0x00400000u : 0u));
+}
 
 // The exponent of a row whose largest magnitude (finite, or 0) is m.
 __device__ __forceinline__ int32_t q8_exponent_of(float m) {
