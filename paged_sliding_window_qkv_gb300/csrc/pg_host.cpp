@@ -144,18 +144,19 @@ void free_stage(PlanStage* st) {
 }
 
 // What the kernels of a shared plan take, in us by head_dim (256, 512) and set (bf16, 8-bit pools), as
-// measured: decode steps of 1..64 requests, prefixes of 128..8192 keys, 16 and 8 query heads. (Over 112 of them,
-// on either kind of pool, the parts alone took 1.30 times the better form's time in the mean, the form chosen
-// by these 1.00.)
+// measured: decode steps of 1..64 requests, prefixes of 128..8192 keys, 16 and 8 query heads, pages of 8..64
+// slots. (Over 192 of them on either kind of pool the form chosen by these took 1.006 times the better form's
+// time in the mean on bf16 pools, 1.18 at most, 1.001 and 1.09 on 8-bit ones; the parts alone 1.29 and 1.59.)
 struct SharedCost {
   double start[2] = {9, 11};                          // of the parts' kernel
   double tile[2] = {0.7, 1.05}, ends[2] = {4.8, 3.5};  // of its units: 64 keys, start and epilogue
-  double dec_start[2][2] = {{9.5, 12.5}, {11, 13}};   // of a decode kernel with its join
-  double dec_l2[2][2] = {{1.65, 3.4}, {0.85, 2.8}};   // of its tiles of 128 keys: another request's too,
-  double dec_dram[2][2] = {{2.6, 5.5}, {1.25, 3.4}};  // or a request's alone
+  double dec_start[2][2] = {{9, 11.5}, {10.5, 13.5}};  // of a decode kernel with its join
+  double dec_l2[2][2] = {{1.15, 2.8}, {0.6, 2.25}};    // of its tiles of 128 keys: another request's too,
+  double dec_dram[2][2] = {{2.5, 5.4}, {1.2, 3.2}};    // or a request's alone
 };
 constexpr SharedCost kCost;
-constexpr double kJoin = 4, kReadBack = 3.5, kBytesPerUs = 6.5e6;
+constexpr double kJoin = 4, kBytesPerUs = 6.5e6;
+constexpr double kReadBack = 2, kBackBatch = 1.5;  // a read-back's launch, and each batch of a warp's loads
 std::atomic<int32_t> g_test_shared{0};  // test hook: 1 parts, 2 plain, whatever the estimate says
 
 // Groups of consecutive requests that share their first keys.
@@ -395,12 +396,22 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
     auto steps_of = [&](int32_t g) { return ((int64_t)pre[g] + step - 1) / step; };
     for (int set = 0; set < 2; ++set) {
       Parts& p = parts[set];
+      // Over 8-bit pools whose pages the decode on codes does not take, own keys and the plain walk go over a
+      // read-back with the bf16 kernel, one after the other; the plain walk's repeats the prefixes.
+      const bool back = set == 1 && !q8_decode_supported(D, group, ps);
+      const int cs = back ? 0 : set;  // whose kernel
+      // (a warp takes a page of a head, in batches of 16 x 256 codes)
+      auto back_us = [&](size_t n) {
+        return kReadBack + kBackBatch * ((ps * (D / 256) + 15) / 16) + (double)n * 6 * Hkv * ps * D / kBytesPerUs;
+      };
       // How long a part is (in steps of 64 keys, or a page; a group is cut into as few of one length):
       // every candidate costs rounds of units over the clusters, each as long as its key tiles, a start and
       // an epilogue. A decode step's own keys run beside the parts, on SMs left free for them, where that
       // ends sooner: a CTA takes about 8 us to begin and end and 6.5 for a tile of 128 keys at head_dim 512,
       // 4 in 8 bits.
-      auto own_us = [&](int32_t on) { return 8 + (set == 0 ? 6.5 : 4.0) * D / 512 * ((tiles2 * Hkv + on - 1) / on); };
+      auto own_us = [&](int32_t on) {
+        return 8 + (cs == 0 ? 6.5 : 4.0) * D / 512 * ((tiles2 * Hkv + on - 1) / on) + (back ? back_us(pages2.size()) + kJoin : 0);
+      };
       int64_t longest = 1;
       double best = 0;
       const int64_t most_steps = ((int64_t)most_len + step - 1) / step;
@@ -410,7 +421,7 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
         int64_t units = 0;
         for (int32_t g = 0; g < groups->num; ++g) units += pairs_of(g) * ((steps_of(g) + len - 1) / len) * heads;
         const double join = (double)T * Hq * D * ((most_steps + len - 1) / len * 4 + (all_one ? 0 : 4)) / kBytesPerUs;
-        for (int32_t on = 0; on <= (all_one ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
+        for (int32_t on = 0; on <= (all_one && !back ? sms * 3 / 4 : 0); on += 8) {  // SMs left free
           const int64_t clusters = std::max(1, (sms - on) / 2);
           const double parts_us = kCost.start[dx] + (double)((units + clusters - 1) / clusters) *
                                                         ((double)(len * step / 64) * kCost.tile[dx] + kCost.ends[dx]);
@@ -427,12 +438,13 @@ int build_plan(pg_plan* p, int32_t num_req, const int64_t* qo_indptr,
       // prefixes, few requests.
       p.plain = most_len == 0;
       if (all_one) {
-        const double n = (double)(tiles * Hkv) / sms, l2 = (double)(tiles_l2 * Hkv) / sms;
+        const double n = (double)(tiles * Hkv) / sms, l2 = back ? 0 : (double)(tiles_l2 * Hkv) / sms;
         const double plain =
-            kCost.dec_start[set][dx] +
-            (l2 * kCost.dec_l2[set][dx] + (n - l2) * kCost.dec_dram[set][dx]) * std::ceil(n) / std::max(n, 1e-9);
+            kCost.dec_start[cs][dx] +
+            (l2 * kCost.dec_l2[cs][dx] + (n - l2) * kCost.dec_dram[cs][dx]) * std::ceil(n) / std::max(n, 1e-9) +
+            (back ? back_us((size_t)NP) : 0);
         // (8-bit pools: a page's codes read and its rows written)
-        if (set == 1) best += kReadBack + (double)pre_pages.size() * 6 * Hkv * ps * D / kBytesPerUs;
+        if (set == 1) best += back_us(pre_pages.size());
         p.plain = p.plain || plain <= best + kJoin;
       }
       const int32_t forced = g_test_shared.load(std::memory_order_relaxed);
