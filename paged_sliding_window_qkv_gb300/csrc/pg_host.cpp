@@ -145,13 +145,13 @@ void free_stage(PlanStage* st) {
 
 // What the kernels of a shared plan take, in us by head_dim (256, 512) and set (bf16, 8-bit pools), as
 // measured: decode steps of 1..64 requests, prefixes of 128..8192 keys, 16 and 8 query heads, pages of 8..64
-// slots. (Over 192 of them on either kind of pool the form chosen by these took 1.006 times the better form's
-// time in the mean on bf16 pools, 1.18 at most, 1.001 and 1.09 on 8-bit ones; the parts alone 1.29 and 1.59.)
+// slots. (Over 192 of them on either kind of pool the form chosen by these took 1.007 times the better form's
+// time in the mean on bf16 pools and 1.003 on 8-bit ones, 1.19 at most; the parts alone 1.28 and 1.58.)
 struct SharedCost {
   double start[2] = {9, 11};                          // of the parts' kernel
   double tile[2] = {0.7, 1.05}, ends[2] = {4.8, 3.5};  // of its units: 64 keys, start and epilogue
   double dec_start[2][2] = {{9, 11.5}, {10.5, 13.5}};  // of a decode kernel with its join
-  double dec_l2[2][2] = {{1.15, 2.8}, {0.6, 2.25}};    // of its tiles of 128 keys: another request's too,
+  double dec_l2[2][2] = {{1.15, 2.8}, {0.6, 2.45}};    // of its tiles of 128 keys: another request's too,
   double dec_dram[2][2] = {{2.5, 5.4}, {1.2, 3.2}};    // or a request's alone
 };
 constexpr SharedCost kCost;
