@@ -31,9 +31,9 @@
 //   (8-11)      Groups above 8 take two such sets, which share nothing but the tiles. (One set over
 //               16 rows took some 5,000 cycles a tile, as long as the tile's bytes; and references
 //               found by a reduction a row 9,000 where they moved: 146 us on the 64 requests below.)
-// Measured: 64 requests of up to 16384 keys at head_dim 512, 16 heads, 104 us (5.6 TB/s over the call; the read-back and
-// the bf16 kernel take 450); 64 under a window of 1023 at head_dim 256, 16 / 8 heads, 53 us (317); one of 8001
-// keys at head_dim 512 17 us (latency of two launches). Bound by HBM, and by CTAs that end unevenly.
+// Measured: 64 requests of up to 16384 keys at head_dim 512, 16 heads, 101 us (5.8 TB/s over the call; the read-back and
+// the bf16 kernel take 450); 64 under a window of 1023 at head_dim 256, 16 / 8 heads, 50 us (317); one of 8001
+// keys at head_dim 512 16.5 us (latency of two launches). Bound by HBM, and by CTAs that end unevenly.
 // Every wait is bounded, as there.
 #include "bounded_decode.cuh"
 #include "q8.cuh"

@@ -37,7 +37,8 @@ constexpr int kFirst = 1, kLast = 2, kSplit = 4, kEnd = 8, kEmpty = 16, kRec1 = 
 
 // ------------------------------------------------------------------ PTX (one CTA)
 // K and V are read once a step: their lines leave L2 first, so that scores and records stay for the join
-// (64 requests of 8001 keys at head_dim 512: 176 -> 170 us, with weights 202 -> 197; 16: 63 -> 57).
+// (64 requests of 8001 keys at head_dim 512: 176 -> 170 us, with weights 202 -> 197; 16: 63 -> 57; 64 of up to
+// 16384 keys in 8 bits 112 -> 104).
 __device__ __forceinline__ uint64_t evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));

@@ -5,7 +5,7 @@
 // HBM-bound: 1 byte in and 2 out an element, and nothing to compute but the conversion (exact). A
 // warp takes one (layer, page of the list, K or V, head) in pieces of 256 codes, 8 a lane, so that a
 // store instruction writes 512 contiguous bytes, with sixteen loads in flight. 32 requests of up to 16384 keys,
-// two layers, head_dim 512: 258 us, 6.7 TB/s; one of 4097 keys 4.4 us (7 before it started while the
+// two layers, head_dim 512: 259 us, 6.7 TB/s; one of 4097 keys 4.4 us (7 before it started while the
 // stream's previous kernel ends).
 #include "pg_internal.h"
 #include "q8.cuh"
